@@ -219,7 +219,7 @@ def _prepare_own(s, case):
         s["cache"] = nv.KVCache(s["kc"], s["vc"])
     if op in ("prompt", "paged"):
         s["ws"] = nv.workspace(nv.attn_workspace_bytes())
-        nv.nvfp4_attn_plan(s["step"], s["q_len"], s["ctx_len"])
+        nv.nvfp4_attn_plan(s["step"], s["q_len"], s["ctx_len"] if op == "paged" else None)
     elif op == "append":
         nv.nvfp4_attn_plan(s["step"], s["q_len"], s["ctx_len"], s["free"], s["cursor"])
 
