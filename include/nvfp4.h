@@ -391,6 +391,135 @@ int nvfp4_mlp_noalloc(const void* x, int64_t T, int64_t H, int64_t ldx,
  */
 int nvfp4_noalloc_scratch(void** device_ptr, size_t* bytes);
 
+/* ------------------------------------------- attention over a paged KV cache
+ *
+ * One step of a serving loop gives every request r some new tokens (q_len[r]:
+ * 1 when decoding, a chunk of its prompt when prefilling) on top of those
+ * already in the cache (ctx_len[r]).  The new tokens of all requests are
+ * packed, request after request, into the rows of one matrix.
+ *   nvfp4_attn_plan    once per step: packed offsets, positions, block tables,
+ *                      slots and the attention's work schedule, from the lengths
+ *   nvfp4_kv_append    per layer: the new tokens' K and V rows into the cache
+ *   nvfp4_attn_paged   per layer: attention of the new tokens over the cache
+ *   nvfp4_attn_prompt  per layer, without a cache: attention within packed prompts
+ * The lengths stay on the device: no call reads them on the host, and the
+ * calls of a step can be captured in a CUDA graph and replayed with new
+ * lengths.  The pages have no attention core (they measure the projections
+ * around it); these are additions of this library.
+ */
+
+/* The tables of one step (device pointers, int32 arrays unless stated). */
+typedef struct {
+    int64_t requests;          /* R, 1 .. 8192 */
+    int64_t tokens;            /* rows of the packed matrices; >= sum of q_len (rows past it are padding) */
+    const int32_t* q_len;      /* [R] new tokens of each request, >= 0 */
+    const int32_t* ctx_len;    /* [R] tokens already in the cache, >= 0; NULL: none */
+    int32_t* cu_q;             /* [R+1] out: first packed row of each request; cu_q[R] = all new tokens */
+    int32_t* kv_len;           /* [R] out: ctx_len + q_len */
+    int32_t* pos;              /* [tokens] out: position of each packed row (0 for padding rows), or NULL */
+    /* paged cache; page_size 0: none, and the rest of this group is ignored */
+    int64_t page_size;         /* tokens per page: 16, 32, 64 or 128 */
+    int32_t* block_table;      /* [R x table_cols], row pitch table_ld: page of tokens j*page_size .. of request r */
+    int64_t table_cols, table_ld;
+    int32_t* slot;             /* [tokens] out: page * page_size + row of each packed row; -1: none */
+    const int32_t* free_pages; /* [free_count] free page ids, taken in order; NULL: block_table is complete already */
+    int64_t free_count;
+    const int32_t* cursor;     /* [1] entries of free_pages already taken, or NULL: 0 */
+    int32_t* cursor_out;       /* [1] out: cursor + pages taken by this step (may alias cursor), or NULL */
+    /* attention; heads 0: no schedule */
+    int64_t heads, kv_heads;   /* heads % kv_heads == 0, heads / kv_heads <= 128 */
+    int64_t window;            /* keys a row sees, its own included; 0: all up to its own */
+    void* schedule;            /* nvfp4_attn_schedule_bytes() bytes, 256-B aligned, out */
+    size_t schedule_bytes;
+} nvfp4_step_t;
+
+/* A paged KV cache: page p, kv head h, row i, column d of K at
+ * k + p*page_stride + (h*page_size + i)*head_dim + d (elements); V likewise. */
+typedef struct {
+    void* k;                   /* bf16 */
+    void* v;                   /* bf16 */
+    int64_t pages, page_size, kv_heads, head_dim;
+    int64_t page_stride;       /* elements, >= kv_heads*page_size*head_dim, % 8 == 0 */
+} nvfp4_kv_cache_t;
+
+/* Query rows, outputs and scaling of one attention call: the row of token t,
+ * head h starts at q + t*ldq + h*hq (elements), its output at out + t*ldo + h*ho. */
+typedef struct {
+    const void* q;             /* bf16 [tokens][heads][head_dim] */
+    int64_t ldq, hq;
+    void* out;                 /* bf16 [tokens][heads][head_dim] */
+    int64_t ldo, ho;
+    float* lse;                /* NULL, or fp32 [tokens x heads]: log of the row's sum of exp(score) */
+    int64_t head_dim;          /* 16 .. 128, % 8 == 0 */
+    float scale;               /* score = scale * q.k */
+} nvfp4_attn_io_t;
+
+/* Bytes of a step's schedule for any lengths of R requests and tokens rows. */
+size_t nvfp4_attn_schedule_bytes(int64_t requests, int64_t tokens, int64_t heads, int64_t kv_heads);
+/* Workspace of the attention calls on the current device, any sizes. */
+size_t nvfp4_attn_workspace_bytes(void);
+
+/*
+ * nvfp4_attn_plan -- the tables of a step from its requests' lengths, in one
+ * launch.  With need(x) = ceil(x / page_size) pages for x tokens:
+ *   cu_q[r+1] = cu_q[r] + q_len[r],  kv_len[r] = ctx_len[r] + q_len[r];
+ *   packed row cu_q[r] + t: pos = ctx_len[r] + t,
+ *                           slot = block_table[r][pos / page_size] * page_size + pos % page_size;
+ *   request r takes need(kv_len[r]) - need(ctx_len[r]) pages from free_pages,
+ *   request after request from *cursor on, into block_table[r][need(ctx_len[r])] ...
+ *   (earlier entries are read, never written).
+ * Rows past the last token get pos 0 and slot -1.  A negative length counts as
+ * 0; tokens past `tokens` are dropped; a row whose page does not exist (the
+ * free list ran out, the table has no such column) gets slot -1, its table
+ * entry -1.  Each of these records NVFP4_ERR_INVALID_ARG * 100 + 31 in the
+ * device status word.  *cursor_out counts the pages asked for, so that a value
+ * above free_count tells how many were missing.
+ */
+int nvfp4_attn_plan(const nvfp4_step_t* step, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_kv_append -- writes packed row t of K and V, all kv heads, into slot
+ * slot[t] of the cache (bf16 copied bit for bit):
+ *   k_cache[slot / page_size][h][slot % page_size][:] = k[t][h][:];  v likewise.
+ *   k, v     bf16, row of token t, head h at k + t*ldk + h*hk (elements);
+ *            16-byte aligned, pitches % 8 == 0.
+ *   slot     int32 [tokens]; -1 is skipped; any other value outside the cache
+ *            is skipped and records NVFP4_ERR_INVALID_ARG * 100 + 32.  No slot
+ *            appears twice.
+ */
+int nvfp4_kv_append(const void* k, int64_t ldk, int64_t hk, const void* v, int64_t ldv, int64_t hv,
+                    const int32_t* slot, int64_t tokens, const nvfp4_kv_cache_t* cache, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_attn_prompt -- causal attention within packed prompts (the rows of
+ * request r are cu_q[r] .. cu_q[r+1] - 1 of q, k and v alike), grouped heads:
+ *   head h reads kv head h / (heads / kv_heads);
+ *   row t of a request sees keys max(0, t - window + 1) .. t of that request;
+ *   out = bf16( sum_j softmax_j(scale * q.k_j) v_j ),  lse = log sum_j exp(scale * q.k_j).
+ * Scores, softmax statistics and sums are binary32; the probabilities are
+ * rounded to bf16 for the product with V.  Rows past cu_q[R] are not written.
+ *   step     after nvfp4_attn_plan on the same stream order, with a schedule
+ *            and ctx_len NULL.
+ *   k, v     as nvfp4_kv_append.
+ *   workspace nvfp4_attn_workspace_bytes() bytes, 256-B aligned, zero-filled
+ *            once after allocation; calls sharing it must be stream-ordered.
+ */
+int nvfp4_attn_prompt(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const void* k, int64_t ldk, int64_t hk,
+                      const void* v, int64_t ldv, int64_t hv, void* workspace, size_t workspace_bytes,
+                      nvfp4_stream_t stream);
+
+/*
+ * nvfp4_attn_paged -- attention of a step's new tokens over the paged cache,
+ * which holds their own K and V already (nvfp4_kv_append): row t of request r
+ * is at position p = kv_len[r] - q_len[r] + t and sees cache positions
+ * max(0, p - window + 1) .. p of its request, found through block_table.  The
+ * rest as nvfp4_attn_prompt.  Cache rows that no row sees may hold anything,
+ * NaN included.  A row that sees no key (its window lies past the table's last
+ * column) gives out 0 and lse -inf.  A page id outside the cache counts as a page of zeros.
+ */
+int nvfp4_attn_paged(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const nvfp4_kv_cache_t* cache,
+                     void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -43,6 +43,28 @@ class _RopeC(ctypes.Structure):
                 ("inverse", ctypes.c_int)]
 
 
+class _StepC(ctypes.Structure):
+    _fields_ = [("requests", ctypes.c_int64), ("tokens", ctypes.c_int64), ("q_len", ctypes.c_void_p),
+                ("ctx_len", ctypes.c_void_p), ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p), ("page_size", ctypes.c_int64), ("block_table", ctypes.c_void_p),
+                ("table_cols", ctypes.c_int64), ("table_ld", ctypes.c_int64), ("slot", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_int64), ("cursor", ctypes.c_void_p),
+                ("cursor_out", ctypes.c_void_p), ("heads", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("window", ctypes.c_int64), ("schedule", ctypes.c_void_p), ("schedule_bytes", ctypes.c_size_t)]
+
+
+class _CacheC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64)]
+
+
+class _AttnIOC(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("hq", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("ldo", ctypes.c_int64), ("ho", ctypes.c_int64), ("lse", ctypes.c_void_p),
+                ("head_dim", ctypes.c_int64), ("scale", ctypes.c_float)]
+
+
 _SIGS = {
     "nvfp4_codes_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
     "nvfp4_sf_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
@@ -89,6 +111,17 @@ _SIGS = {
                                          ctypes.POINTER(_TensorC), ctypes.POINTER(_TensorC), ctypes.c_int,
                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
                                          ctypes.c_void_p]),
+    "nvfp4_attn_schedule_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
+    "nvfp4_attn_workspace_bytes": (ctypes.c_size_t, []),
+    "nvfp4_attn_plan": (ctypes.c_int, [ctypes.POINTER(_StepC), ctypes.c_void_p]),
+    "nvfp4_kv_append": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                       ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                       ctypes.POINTER(_CacheC), ctypes.c_void_p]),
+    "nvfp4_attn_prompt": (ctypes.c_int, [ctypes.POINTER(_StepC), ctypes.POINTER(_AttnIOC), ctypes.c_void_p,
+                                         ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                         ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "nvfp4_attn_paged": (ctypes.c_int, [ctypes.POINTER(_StepC), ctypes.POINTER(_AttnIOC), ctypes.POINTER(_CacheC),
+                                        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
 }
 
 EXPORTED_FUNCTIONS = tuple(_SIGS)
@@ -327,3 +360,154 @@ def nvfp4_gemm_experts(A: NVFP4Tensor, W: NVFP4Tensor, num_experts: int, ids: to
     a, w = A.c(), W.c()
     _check(lib().nvfp4_gemm_experts(ctypes.byref(a), ctypes.byref(w), num_experts, _ptr(ids), topk, _ptr(out), ldo,
                                     _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "nvfp4_gemm_experts")
+
+
+# ------------------------------------------------ attention over a KV cache
+def _i32(t, n, name):
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of at least {n} elements")
+    return t.data_ptr()
+
+
+def _heads_3d(x: torch.Tensor, name: str, tokens: int, heads: int, head_dim: int | None = None):
+    """(address, row pitch, head pitch) of bf16 [tokens, heads, head_dim] with unit column stride."""
+    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.stride(2) != 1 or not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA bf16 [tokens, heads, head_dim] tensor with unit column stride")
+    if x.shape[0] != tokens or x.shape[1] != heads or (head_dim is not None and x.shape[2] != head_dim):
+        raise ValueError(f"{name} is {tuple(x.shape)}, not ({tokens}, {heads}, {head_dim})")
+    return x.data_ptr(), x.stride(0), x.stride(1)
+
+
+def attn_schedule_bytes(requests: int, tokens: int, heads: int, kv_heads: int) -> int:
+    return int(lib().nvfp4_attn_schedule_bytes(requests, tokens, heads, kv_heads))
+
+
+def attn_workspace_bytes() -> int:
+    return int(lib().nvfp4_attn_workspace_bytes())
+
+
+class KVCache:
+    """A paged KV cache: bf16 ``k`` and ``v`` of shape [pages, kv_heads,
+    page_size, head_dim].  Pages may be apart (stride(0), e.g. the two halves
+    of one [pages, 2, ...] tensor); within a page they are contiguous."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        for name, t in (("k", k), ("v", v)):
+            if t.dtype != torch.bfloat16 or t.dim() != 4 or not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA bf16 [pages, kv_heads, page_size, head_dim] tensor")
+            if t.stride()[1:] != (t.shape[2] * t.shape[3], t.shape[3], 1):
+                raise ValueError(f"{name}'s pages must be contiguous")
+        if k.shape != v.shape or (k.stride(0) != v.stride(0) and k.shape[0] > 1):
+            raise ValueError("k and v must have one shape and one page stride")
+        self.k, self.v = k, v
+        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        page = self.kv_heads * self.page_size * self.head_dim
+        self._c = _CacheC(k.data_ptr(), v.data_ptr(), self.pages, self.page_size, self.kv_heads, self.head_dim,
+                          k.stride(0) if self.pages > 1 else page)
+
+    @staticmethod
+    def empty(pages: int, kv_heads: int, page_size: int, head_dim: int, device=None) -> "KVCache":
+        k, v = (torch.empty((pages, kv_heads, page_size, head_dim), dtype=torch.bfloat16, device=device or "cuda")
+                for _ in range(2))
+        return KVCache(k, v)
+
+
+class AttnPlan:
+    """The tables of one serving step (see nvfp4_step_t), in buffers that
+    stay: cu_q int32 [requests + 1], kv_len int32 [requests], pos and slot
+    int32 [tokens], block_table int32 [requests, pages per request], cursor
+    int32 [1] (the free list's cursor after the step), and the attention's
+    schedule.  Filled by :func:`nvfp4_attn_plan`, once per step; read by every
+    layer's :func:`nvfp4_kv_append`, :func:`nvfp4_attn_paged` and
+    :func:`nvfp4_attn_prompt`, and ``pos`` by :func:`nvfp4_gemm_rope`.
+
+    requests, tokens: the most a step has (tokens: the rows of its matrices).
+    page_size and block_table: for a paged cache; block_table (or the
+    columns of a new one, all -1) holds the pages of the cached tokens.
+    window: keys a row sees, its own included (0: all up to its own)."""
+
+    def __init__(self, requests: int, tokens: int, heads: int, kv_heads: int, page_size: int = 0, block_table=None,
+                 window: int = 0, device=None):
+        self.requests, self.tokens, self.heads, self.kv_heads = requests, tokens, heads, kv_heads
+        self.page_size, self.window = page_size, window
+        if isinstance(block_table, torch.Tensor):
+            if block_table.dtype != torch.int32 or not block_table.is_cuda or block_table.dim() != 2 or \
+                    block_table.shape[0] < requests or block_table.stride(1) != 1:
+                raise ValueError("block_table must be a CUDA int32 [requests, pages] tensor with unit column stride")
+            device = block_table.device
+        device = device or "cuda"
+        empty = lambda n: torch.empty((n,), dtype=torch.int32, device=device)
+        self.cu_q, self.kv_len, self.pos = empty(requests + 1), empty(requests), empty(tokens)
+        self.slot = self.block_table = self.cursor = None
+        if page_size:
+            if not isinstance(block_table, torch.Tensor):
+                block_table = torch.full((requests, int(block_table)), -1, dtype=torch.int32, device=device)
+            self.block_table = block_table
+            self.slot, self.cursor = empty(tokens), torch.zeros((1,), dtype=torch.int32, device=device)
+        nbytes = attn_schedule_bytes(requests, tokens, heads, kv_heads)
+        self.schedule = torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=device)
+        t = self.block_table
+        self._c = _StepC(requests, tokens, None, None, self.cu_q.data_ptr(), self.kv_len.data_ptr(),
+                         self.pos.data_ptr(), page_size, None if t is None else t.data_ptr(),
+                         0 if t is None else t.shape[1], 0 if t is None else max(t.stride(0), t.shape[1]),
+                         None if t is None else self.slot.data_ptr(), None, 0, None,
+                         None if t is None else self.cursor.data_ptr(), heads, kv_heads, window,
+                         self.schedule.data_ptr(), nbytes)
+
+
+def nvfp4_attn_plan(plan: AttnPlan, q_len: torch.Tensor, ctx_len=None, free_pages=None, cursor=None, stream=None):
+    """The step's tables from its lengths: q_len, ctx_len int32 [requests]
+    on the device; free_pages int32 and cursor int32 [1] (the entries of
+    free_pages already taken; None: 0) for the pages the new tokens open, or
+    None where block_table holds them already."""
+    c = plan._c
+    c.q_len = _i32(q_len, plan.requests, "q_len")
+    c.ctx_len = None if ctx_len is None else _i32(ctx_len, plan.requests, "ctx_len")
+    if free_pages is not None:
+        c.free_pages, c.free_count = _i32(free_pages, 0, "free_pages"), free_pages.numel()
+    else:
+        c.free_pages, c.free_count = None, 0
+    c.cursor = None if cursor is None else _i32(cursor, 1, "cursor")
+    _check(lib().nvfp4_attn_plan(ctypes.byref(c), _stream(stream)), "nvfp4_attn_plan")
+
+
+def nvfp4_kv_append(k: torch.Tensor, v: torch.Tensor, plan: AttnPlan, cache: KVCache, stream=None):
+    """k, v: bf16 [tokens, kv_heads, head_dim] (any row and head pitch, e.g.
+    column slices of a QKV projection's output) into the cache's slots plan.slot."""
+    if plan.slot is None:
+        raise ValueError("the plan has no paged cache (page_size 0)")
+    kp = _heads_3d(k, "k", plan.tokens, cache.kv_heads, cache.head_dim)
+    vp = _heads_3d(v, "v", plan.tokens, cache.kv_heads, cache.head_dim)
+    _check(lib().nvfp4_kv_append(*kp, *vp, plan.slot.data_ptr(), plan.tokens, ctypes.byref(cache._c),
+                                 _stream(stream)), "nvfp4_kv_append")
+
+
+def _attn_io(plan: AttnPlan, q: torch.Tensor, out: torch.Tensor, scale, lse) -> _AttnIOC:
+    d = q.shape[-1]
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or not lse.is_cuda or
+                            lse.numel() != plan.tokens * plan.heads):
+        raise ValueError("lse must be a contiguous CUDA float32 [tokens, heads] tensor")
+    return _AttnIOC(*_heads_3d(q, "q", plan.tokens, plan.heads, d), *_heads_3d(out, "out", plan.tokens, plan.heads, d),
+                    None if lse is None else lse.data_ptr(), d, d ** -0.5 if scale is None else scale)
+
+
+def nvfp4_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: AttnPlan, out: torch.Tensor,
+                      ws: torch.Tensor, scale=None, lse=None, stream=None):
+    """Causal attention within packed prompts.  q, out: bf16 [tokens, heads,
+    head_dim]; k, v: bf16 [tokens, kv_heads, head_dim] (any row and head
+    pitch); scale: head_dim ** -0.5 if None; lse: None or float32 [tokens,
+    heads]; ws: a zero-filled workspace of attn_workspace_bytes()."""
+    io = _attn_io(plan, q, out, scale, lse)
+    kp = _heads_3d(k, "k", plan.tokens, plan.kv_heads, q.shape[2])
+    vp = _heads_3d(v, "v", plan.tokens, plan.kv_heads, q.shape[2])
+    _check(lib().nvfp4_attn_prompt(ctypes.byref(plan._c), ctypes.byref(io), *kp, *vp, ws.data_ptr(),
+                                   ws.numel() * ws.element_size(), _stream(stream)), "nvfp4_attn_prompt")
+
+
+def nvfp4_attn_paged(q: torch.Tensor, cache: KVCache, plan: AttnPlan, out: torch.Tensor, ws: torch.Tensor, scale=None,
+                     lse=None, stream=None):
+    """Attention of a step's new tokens over the paged cache, which holds
+    their K and V already.  The rest as :func:`nvfp4_attn_prompt`."""
+    io = _attn_io(plan, q, out, scale, lse)
+    _check(lib().nvfp4_attn_paged(ctypes.byref(plan._c), ctypes.byref(io), ctypes.byref(cache._c), ws.data_ptr(),
+                                  ws.numel() * ws.element_size(), _stream(stream)), "nvfp4_attn_paged")

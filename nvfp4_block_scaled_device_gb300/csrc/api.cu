@@ -6,6 +6,7 @@
 
 #include <mutex>
 
+#include "attn.h"
 #include "gemv.h"
 #include "internal.h"
 #include "nvfp4.h"
@@ -665,5 +666,162 @@ int nvfp4_mlp(const void* x, int64_t T, int64_t H, int64_t ldx, const void* norm
 // Debug builds only: copy the GEMM timeline of CTA 0 to the host.
 int nvfp4_debug_trace(unsigned long long* out, int n);
 #endif
+
+}  // extern "C"
+
+// ------------------------------------------------- attention over the cache
+namespace {
+
+// The fields of a step that every call reads; `what`: 1 the paged tables,
+// 2 the schedule.
+int check_step(const nvfp4_step_t* s, int what)
+{
+    if (!s || s->requests < 1 || s->requests > kStepMaxRequests || s->tokens < 1 || s->tokens > INT32_MAX)
+        return NVFP4_ERR_INVALID_ARG;
+    if (!s->cu_q || !s->kv_len) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned(s->cu_q, 4) || !aligned(s->kv_len, 4) || !aligned(s->pos, 4)) return NVFP4_ERR_MISALIGNED;
+    if (what & 1) {
+        const int64_t P = s->page_size;
+        if (P != 16 && P != 32 && P != 64 && P != 128) return NVFP4_ERR_INVALID_ARG;
+        if (!s->block_table || s->table_cols < 1 || s->table_ld < s->table_cols || s->table_cols * P > INT32_MAX)
+            return NVFP4_ERR_INVALID_ARG;
+        if (!aligned(s->block_table, 4)) return NVFP4_ERR_MISALIGNED;
+    }
+    if (what & 2) {
+        if (s->kv_heads < 1 || s->heads < s->kv_heads || s->heads % s->kv_heads != 0 ||
+            s->heads / s->kv_heads > 128 || s->heads > 65535 || s->window < 0 || s->window > INT32_MAX)
+            return NVFP4_ERR_INVALID_ARG;
+        const size_t need = nvfp4_attn_schedule_bytes(s->requests, s->tokens, s->heads, s->kv_heads);
+        if (!s->schedule || s->schedule_bytes < need) return NVFP4_ERR_WORKSPACE;
+        if (!aligned(s->schedule, 256)) return NVFP4_ERR_MISALIGNED;
+    }
+    return NVFP4_OK;
+}
+
+// Rows [tokens][heads][head_dim] with pitches ld and h (elements).
+int check_rows(const void* p, int64_t tokens, int64_t heads, int64_t head_dim, int64_t ld, int64_t h)
+{
+    if (!p || (tokens > 1 && ld < head_dim) || (heads > 1 && h < head_dim)) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned(p, 16) || (tokens > 1 && ld % 8 != 0) || (heads > 1 && h % 8 != 0)) return NVFP4_ERR_MISALIGNED;
+    return NVFP4_OK;
+}
+
+int check_head_dim(int64_t d) { return d >= 16 && d <= 128 && d % 8 == 0 ? NVFP4_OK : NVFP4_ERR_INVALID_ARG; }
+
+int check_cache(const nvfp4_kv_cache_t* c)
+{
+    if (!c || !c->k || !c->v || c->pages < 1 || c->kv_heads < 1) return NVFP4_ERR_INVALID_ARG;
+    const int64_t P = c->page_size;
+    if (P != 16 && P != 32 && P != 64 && P != 128) return NVFP4_ERR_INVALID_ARG;
+    NVFP4_TRY(check_head_dim(c->head_dim));
+    if (c->pages > INT32_MAX / P || c->kv_heads > 65535 || c->page_stride < c->kv_heads * P * c->head_dim)
+        return NVFP4_ERR_INVALID_ARG;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % 8 != 0) return NVFP4_ERR_MISALIGNED;
+    return NVFP4_OK;
+}
+
+int run_attn(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const AttnKV& kv, void* workspace,
+             size_t workspace_bytes, nvfp4_stream_t stream)
+{
+    if (io->lse && !aligned(io->lse, 4)) return NVFP4_ERR_MISALIGNED;
+    if (!workspace || workspace_bytes < nvfp4_attn_workspace_bytes()) return NVFP4_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return NVFP4_ERR_MISALIGNED;
+    DeviceInfo* d = nullptr;
+    NVFP4_TRY(device_info(&d));
+    NVFP4_CUDA(launch_attn(*step, *io, kv, d->num_sms, (cudaStream_t)stream));
+    return NVFP4_OK;
+}
+
+int check_io(const nvfp4_step_t* step, const nvfp4_attn_io_t* io)
+{
+    if (!io) return NVFP4_ERR_INVALID_ARG;
+    NVFP4_TRY(check_head_dim(io->head_dim));
+    NVFP4_TRY(check_rows(io->q, step->tokens, step->heads, io->head_dim, io->ldq, io->hq));
+    return check_rows(io->out, step->tokens, step->heads, io->head_dim, io->ldo, io->ho);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t nvfp4_attn_schedule_bytes(int64_t requests, int64_t tokens, int64_t heads, int64_t kv_heads)
+{
+    if (requests < 1 || tokens < 1 || heads < 1 || kv_heads < 1) return 0;
+    return 256;
+}
+
+size_t nvfp4_attn_workspace_bytes(void) { return 256; }
+
+int nvfp4_attn_plan(const nvfp4_step_t* step, nvfp4_stream_t stream)
+{
+    if (!step) return NVFP4_ERR_INVALID_ARG;
+    NVFP4_TRY(check_step(step, (step->page_size ? 1 : 0) | (step->heads ? 2 : 0)));
+    if (!step->q_len || (step->page_size && !step->slot)) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned(step->q_len, 4) || !aligned(step->ctx_len, 4)) return NVFP4_ERR_MISALIGNED;
+    if (step->page_size) {
+        if (step->free_pages && step->free_count < 0) return NVFP4_ERR_INVALID_ARG;
+        if (!aligned(step->slot, 4) || !aligned(step->free_pages, 4) || !aligned(step->cursor, 4) ||
+            !aligned(step->cursor_out, 4))
+            return NVFP4_ERR_MISALIGNED;
+    }
+    DeviceInfo* d = nullptr;
+    NVFP4_TRY(device_info(&d));
+    NVFP4_CUDA(launch_attn_plan(*step, d->status, d->num_sms, (cudaStream_t)stream));
+    return NVFP4_OK;
+}
+
+int nvfp4_kv_append(const void* k, int64_t ldk, int64_t hk, const void* v, int64_t ldv, int64_t hv,
+                    const int32_t* slot, int64_t tokens, const nvfp4_kv_cache_t* cache, nvfp4_stream_t stream)
+{
+    NVFP4_TRY(check_cache(cache));
+    if (tokens < 1 || tokens > INT32_MAX || !slot) return NVFP4_ERR_INVALID_ARG;
+    NVFP4_TRY(check_rows(k, tokens, cache->kv_heads, cache->head_dim, ldk, hk));
+    NVFP4_TRY(check_rows(v, tokens, cache->kv_heads, cache->head_dim, ldv, hv));
+    if (!aligned(slot, 4)) return NVFP4_ERR_MISALIGNED;
+    DeviceInfo* d = nullptr;
+    NVFP4_TRY(device_info(&d));
+    NVFP4_CUDA(launch_kv_append(static_cast<const __nv_bfloat16*>(k), ldk, hk, static_cast<const __nv_bfloat16*>(v),
+                                ldv, hv, slot, tokens, *cache, d->status, d->num_sms, (cudaStream_t)stream));
+    return NVFP4_OK;
+}
+
+int nvfp4_attn_prompt(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const void* k, int64_t ldk, int64_t hk,
+                      const void* v, int64_t ldv, int64_t hv, void* workspace, size_t workspace_bytes,
+                      nvfp4_stream_t stream)
+{
+    NVFP4_TRY(check_step(step, 2));
+    if (step->ctx_len) return NVFP4_ERR_INVALID_ARG;      // the keys are the packed rows alone
+    NVFP4_TRY(check_io(step, io));
+    NVFP4_TRY(check_rows(k, step->tokens, step->kv_heads, io->head_dim, ldk, hk));
+    NVFP4_TRY(check_rows(v, step->tokens, step->kv_heads, io->head_dim, ldv, hv));
+    AttnKV kv = {};
+    kv.k = static_cast<const __nv_bfloat16*>(k);
+    kv.v = static_cast<const __nv_bfloat16*>(v);
+    kv.ldk = ldk;
+    kv.hk = hk;
+    kv.ldv = ldv;
+    kv.hv = hv;
+    return run_attn(step, io, kv, workspace, workspace_bytes, stream);
+}
+
+int nvfp4_attn_paged(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const nvfp4_kv_cache_t* cache,
+                     void* workspace, size_t workspace_bytes, nvfp4_stream_t stream)
+{
+    NVFP4_TRY(check_step(step, 3));
+    NVFP4_TRY(check_io(step, io));
+    NVFP4_TRY(check_cache(cache));
+    if (cache->page_size != step->page_size || cache->kv_heads != step->kv_heads || cache->head_dim != io->head_dim)
+        return NVFP4_ERR_INVALID_ARG;
+    AttnKV kv = {};
+    kv.k = static_cast<const __nv_bfloat16*>(cache->k);
+    kv.v = static_cast<const __nv_bfloat16*>(cache->v);
+    kv.block_table = step->block_table;
+    kv.table_cols = step->table_cols;
+    kv.table_ld = step->table_ld;
+    kv.page_size = cache->page_size;
+    kv.pages = cache->pages;
+    kv.page_stride = cache->page_stride;
+    return run_attn(step, io, kv, workspace, workspace_bytes, stream);
+}
 
 }  // extern "C"

@@ -1,0 +1,275 @@
+// The tables of one serving step (nvfp4_attn_plan) and the write of its new
+// K and V rows into the paged cache (nvfp4_kv_append).
+//
+// Plan.  Everything follows from two prefix sums over the requests, of the
+// new tokens and of the pages they open.  Every block computes both sums for
+// all requests in shared memory (a few KB of lengths out of L2) instead of
+// waiting for a first kernel to do it, then fills its own slice of the
+// tables; so the whole plan is one launch without a grid-wide wait.  The
+// tables are small (a few hundred KB at most): the launch and the dependent
+// reads set the time, not bandwidth.
+#include "attn.h"
+#include "common.cuh"
+#include "internal.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+
+struct PlanParams {
+    nvfp4_step_t s;
+    int* status;
+    int page_shift;
+};
+
+__device__ __forceinline__ void report(int* status, int code)
+{
+    if (status) atomicCAS(status, 0, code);
+}
+
+__device__ __forceinline__ int64_t warp_incl_sum(int64_t v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    return v;
+}
+
+// A request's lengths, with negative ones taken as zero.
+struct Lens {
+    int64_t ctx, q;
+    bool bad;
+};
+
+__device__ __forceinline__ Lens lens_of(const nvfp4_step_t& s, int r)
+{
+    const int q = __ldg(s.q_len + r), c = s.ctx_len ? __ldg(s.ctx_len + r) : 0;
+    return {c < 0 ? 0 : c, q < 0 ? 0 : q, q < 0 || c < 0};
+}
+
+// shared memory: cu [R+1] int32 (new tokens before each request, at most
+// `tokens`), first [R+1] int32 (pages taken before each request)
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
+{
+    extern __shared__ int32_t sh[];
+    __shared__ int64_t s_q[kPlanWarps], s_n[kPlanWarps];
+    griddep_launch_dependents();
+    griddep_wait();                 // the lengths may come from the previous kernel
+    const nvfp4_step_t& s = p.s;
+    const int R = (int)s.requests;
+    const bool paged = s.page_size != 0;
+    int32_t* cu = sh;
+    int32_t* first = sh + R + 1;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int64_t P = paged ? s.page_size : 1, round = P - 1;
+    const int sft = p.page_shift;
+
+    // prefix sums over the requests: thread t takes the requests
+    // per*t .. per*t + per - 1
+    const int per = (R + kPlanThreads - 1) / kPlanThreads;
+    int64_t sq = 0, sn = 0;
+    bool bad = false;
+    for (int j = 0; j < per; j++) {
+        const int r = t * per + j;
+        if (r >= R) break;
+        const Lens l = lens_of(s, r);
+        bad |= l.bad;
+        sq += l.q;
+        if (paged) sn += ((l.ctx + l.q + round) >> sft) - ((l.ctx + round) >> sft);
+    }
+    const int64_t iq = warp_incl_sum(sq, lane), in = warp_incl_sum(sn, lane);
+    if (lane == 31) {
+        s_q[warp] = iq;
+        s_n[warp] = in;
+    }
+    __syncthreads();
+    int64_t bq = iq - sq, bn = in - sn, total_q = 0, total_n = 0;
+    for (int w = 0; w < kPlanWarps; w++) {
+        if (w < warp) {
+            bq += s_q[w];
+            bn += s_n[w];
+        }
+        total_q += s_q[w];
+        total_n += s_n[w];
+    }
+    const int64_t cap = s.tokens;
+    const int64_t cursor = paged && s.cursor ? __ldg(s.cursor) : 0;
+    const int64_t kIntMax = 0x7fffffff;
+    for (int j = 0; j < per; j++) {
+        const int r = t * per + j;
+        if (r >= R) break;
+        const Lens l = lens_of(s, r);
+        cu[r] = (int32_t)min(bq, cap);
+        first[r] = (int32_t)min(bn, kIntMax);
+        bq += l.q;
+        if (paged) bn += ((l.ctx + l.q + round) >> sft) - ((l.ctx + round) >> sft);
+    }
+    if (t == 0) {
+        cu[R] = (int32_t)min(total_q, cap);
+        if (total_q > cap) bad = true;
+    }
+    if (bad && blockIdx.x == 0) report(p.status, kStatusPlan);
+    __syncthreads();
+    const int32_t T = cu[R];
+
+    // per-request tables: block b takes every gridDim-th request, a warp each
+    for (int r = blockIdx.x * kPlanWarps + warp; r < R; r += gridDim.x * kPlanWarps) {
+        const Lens l = lens_of(s, r);
+        const int q = cu[r + 1] - cu[r];
+        if (lane == 0) {
+            s.cu_q[r] = cu[r];
+            if (r == R - 1) s.cu_q[R] = T;
+            s.kv_len[r] = (int32_t)min(l.ctx + q, kIntMax);
+        }
+        if (paged && s.free_pages) {
+            const int64_t have = (l.ctx + round) >> sft, need = (l.ctx + l.q + round) >> sft;
+            for (int64_t j = have + lane; j < need; j += 32) {
+                const int64_t at = cursor + first[r] + (j - have);
+                const bool ok = at >= 0 && at < s.free_count && j < s.table_cols;
+                if (j < s.table_cols) s.block_table[r * s.table_ld + j] = ok ? __ldg(s.free_pages + at) : -1;
+                if (!ok) report(p.status, kStatusPlan);
+            }
+        }
+    }
+    if (paged && blockIdx.x == 0 && t == 0 && s.cursor_out && s.free_pages)
+        *s.cursor_out = (int32_t)min(cursor + total_n, kIntMax);
+
+    // per-token tables
+    for (int64_t i = (int64_t)blockIdx.x * kPlanThreads + t; i < cap; i += (int64_t)gridDim.x * kPlanThreads) {
+        int pos = 0, slot = -1;
+        if (i < T) {
+            // the last request that starts at or before row i and has rows
+            int lo = 0, hi = R - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (cu[mid] <= i) lo = mid; else hi = mid - 1;
+            }
+            const int64_t ctx = lens_of(s, lo).ctx;
+            const int64_t at = ctx + (i - cu[lo]);
+            pos = (int)min(at, kIntMax);
+            if (paged) {
+                const int64_t j = at >> sft, have = (ctx + round) >> sft;
+                int64_t page = -1;
+                if (j < s.table_cols) {
+                    if (!s.free_pages || j < have) {
+                        page = s.block_table[lo * s.table_ld + j];
+                    } else {
+                        const int64_t f = cursor + first[lo] + (j - have);
+                        if (f >= 0 && f < s.free_count) page = __ldg(s.free_pages + f);
+                    }
+                }
+                const int64_t sl = page * P + (at & round);
+                if (page >= 0 && sl <= kIntMax)
+                    slot = (int)sl;
+                else
+                    report(p.status, kStatusPlan);
+            }
+        }
+        if (s.pos) s.pos[i] = pos;
+        if (paged) s.slot[i] = slot;
+    }
+}
+
+// ---------------------------------------------------------------- append
+// One 16-byte vector of a head's row per thread: a block copies whole packed
+// rows (both K and V, every kv head), kAppendRows of them at a time, all
+// their loads in flight before the first store.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendRows = 4;
+
+struct AppendParams {
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    int64_t ldk, hk, ldv, hv;
+    const int32_t* slot;
+    int64_t tokens;
+    nvfp4_kv_cache_t c;
+    int page_shift;
+    int* status;
+};
+
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int dv = (int)(p.c.head_dim / 8);             // vectors of a head's row
+    const int per = (int)p.c.kv_heads * dv;             // vectors of a packed row of K (or V)
+    const int64_t slots = p.c.pages << p.page_shift;
+    const int64_t mask = p.c.page_size - 1;
+    const int64_t hstride = p.c.page_size * p.c.head_dim;
+    for (int64_t t0 = (int64_t)blockIdx.x * kAppendRows; t0 < p.tokens; t0 += (int64_t)gridDim.x * kAppendRows) {
+        int64_t dst[kAppendRows];
+        bool ok[kAppendRows];
+#pragma unroll
+        for (int u = 0; u < kAppendRows; u++) {
+            const int64_t sl = t0 + u < p.tokens ? __ldg(p.slot + t0 + u) : -1;
+            ok[u] = sl >= 0 && sl < slots;
+            if (!ok[u] && sl != -1 && threadIdx.x == 0) report(p.status, kStatusSlot);
+            dst[u] = (sl >> p.page_shift) * p.c.page_stride + (sl & mask) * p.c.head_dim;
+        }
+        for (int x = threadIdx.x; x < 2 * per; x += kAppendThreads) {
+            const bool is_v = x >= per;
+            const int y = is_v ? x - per : x;
+            const int h = y / dv, d = 8 * (y - h * dv);
+            const __nv_bfloat16* src = is_v ? p.v + h * p.hv + d : p.k + h * p.hk + d;
+            const int64_t ld = is_v ? p.ldv : p.ldk;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(is_v ? p.c.v : p.c.k) + h * hstride + d;
+            uint4 val[kAppendRows];
+#pragma unroll
+            for (int u = 0; u < kAppendRows; u++)
+                if (ok[u]) val[u] = __ldg(reinterpret_cast<const uint4*>(src + (t0 + u) * ld));
+#pragma unroll
+            for (int u = 0; u < kAppendRows; u++)
+                if (ok[u]) *reinterpret_cast<uint4*>(out + dst[u]) = val[u];
+        }
+    }
+}
+
+int log2_of(int64_t v)
+{
+    int s = 0;
+    while (((int64_t)1 << s) < v) s++;
+    return s;
+}
+
+}  // namespace
+
+cudaError_t launch_attn_plan(const nvfp4_step_t& step, int* status, int num_sms, cudaStream_t stream)
+{
+    const size_t smem = (size_t)(step.requests + 1) * 8;
+    static int attr_set_for_device[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && !attr_set_for_device[dev]) {
+        e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)((kStepMaxRequests + 1) * 8));
+        if (e != cudaSuccess) return e;
+        attr_set_for_device[dev] = 1;
+    }
+    PlanParams p;
+    p.s = step;
+    p.status = status;
+    p.page_shift = step.page_size ? log2_of(step.page_size) : 0;
+    const int64_t by_tokens = (step.tokens + kPlanThreads - 1) / kPlanThreads;
+    const int64_t by_requests = (step.requests + kPlanWarps - 1) / kPlanWarps;
+    int64_t grid = by_tokens > by_requests ? by_tokens : by_requests;
+    if (grid > num_sms) grid = num_sms;
+    return launch_programmatic(plan_kernel, dim3((unsigned)grid), dim3(kPlanThreads), smem, stream, p);
+}
+
+cudaError_t launch_kv_append(const __nv_bfloat16* k, int64_t ldk, int64_t hk, const __nv_bfloat16* v, int64_t ldv,
+                             int64_t hv, const int32_t* slot, int64_t tokens, const nvfp4_kv_cache_t& cache,
+                             int* status, int num_sms, cudaStream_t stream)
+{
+    AppendParams p = {k, v, ldk, hk, ldv, hv, slot, tokens, cache, log2_of(cache.page_size), status};
+    int64_t grid = (tokens + kAppendRows - 1) / kAppendRows;
+    if (grid > (int64_t)num_sms * 8) grid = (int64_t)num_sms * 8;
+    return launch_programmatic(append_kernel, dim3((unsigned)grid), dim3(kAppendThreads), 0, stream, p);
+}
+
+}  // namespace nvfp4
