@@ -445,7 +445,7 @@ class AttnPlan:
             self.block_table = block_table
             self.slot, self.cursor = empty(tokens), torch.zeros((1,), dtype=torch.int32, device=device)
         nbytes = attn_schedule_bytes(requests, tokens, heads, kv_heads)
-        self.schedule = torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=device)
+        self.schedule = torch.zeros((max(nbytes, 1),), dtype=torch.uint8, device=device)
         t = self.block_table
         self._c = _StepC(requests, tokens, None, None, self.cu_q.data_ptr(), self.kv_len.data_ptr(),
                          self.pos.data_ptr(), page_size, None if t is None else t.data_ptr(),

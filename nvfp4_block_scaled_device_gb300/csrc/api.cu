@@ -720,6 +720,34 @@ int check_cache(const nvfp4_kv_cache_t* c)
     return NVFP4_OK;
 }
 
+// Keys and values of an attention call: packed rows (cache NULL), or the
+// paged cache.
+struct AttnKV {
+    const void* k;
+    const void* v;
+    int64_t ldk, hk, ldv, hv;
+    const nvfp4_kv_cache_t* cache;
+};
+
+// bf16 tensor map of `rank` dimensions (innermost first, strides in elements
+// from dimension 1 on), 64-column boxes with 128-byte swizzle.  The stride of
+// a dimension of size 1 is never used: any valid value stands for it.
+int make_rows_map(CUtensorMap* m, const void* base, int rank, const int64_t* dims, const int64_t* strides,
+                  const int* box)
+{
+    cuuint64_t d[4], st[3];
+    cuuint32_t b[4], es[4] = {1, 1, 1, 1};
+    for (int i = 0; i < rank; i++) {
+        d[i] = (cuuint64_t)dims[i];
+        b[i] = (cuuint32_t)box[i];
+        if (i > 0) st[i - 1] = dims[i] > 1 ? (cuuint64_t)strides[i - 1] * 2 : 256;
+    }
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
 int run_attn(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const AttnKV& kv, void* workspace,
              size_t workspace_bytes, nvfp4_stream_t stream)
 {
@@ -728,7 +756,50 @@ int run_attn(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const AttnKV& 
     if (!aligned(workspace, 256)) return NVFP4_ERR_MISALIGNED;
     DeviceInfo* d = nullptr;
     NVFP4_TRY(device_info(&d));
-    NVFP4_CUDA(launch_attn(*step, *io, kv, d->num_sms, (cudaStream_t)stream));
+    NVFP4_TRY(encoder());
+    const int group = (int)(step->heads / step->kv_heads);
+    const int64_t D = io->head_dim;
+    CUtensorMap mq, mk, mv;
+    {
+        const int64_t dims[3] = {D, step->heads, step->tokens}, st[2] = {io->hq, io->ldq};
+        const int box[3] = {64, group, row_tile_tokens(group)};
+        NVFP4_TRY(make_rows_map(&mq, io->q, 3, dims, st, box));
+    }
+    if (kv.cache) {
+        const nvfp4_kv_cache_t& c = *kv.cache;
+        const int64_t dims[4] = {D, c.page_size, c.kv_heads, c.pages};
+        const int64_t st[3] = {D, c.page_size * D, c.page_stride};
+        const int box[4] = {64, (int)c.page_size, 1, 1};
+        NVFP4_TRY(make_rows_map(&mk, kv.k, 4, dims, st, box));
+        NVFP4_TRY(make_rows_map(&mv, kv.v, 4, dims, st, box));
+    } else {
+        const int64_t dims[3] = {D, step->kv_heads, step->tokens};
+        const int64_t sk[2] = {kv.hk, kv.ldk}, sv[2] = {kv.hv, kv.ldv};
+        const int box[3] = {64, 1, kAttnKeys};
+        NVFP4_TRY(make_rows_map(&mk, kv.k, 3, dims, sk, box));
+        NVFP4_TRY(make_rows_map(&mv, kv.v, 3, dims, sv, box));
+    }
+    AttnArgs a = {};
+    a.sched = static_cast<const ScheduleHead*>(step->schedule);
+    a.out = static_cast<__nv_bfloat16*>(io->out);
+    a.ldo = io->ldo;
+    a.ho = io->ho;
+    a.lse = io->lse;
+    a.heads = (int)step->heads;
+    a.kv_heads = (int)step->kv_heads;
+    a.group = group;
+    a.head_dim = (int)D;
+    a.window = (int)step->window;
+    a.scale = io->scale;
+    if (kv.cache) {
+        a.block_table = step->block_table;
+        a.table_ld = step->table_ld;
+        a.page_size = (int)kv.cache->page_size;
+    }
+    a.tickets = static_cast<int*>(workspace);
+    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttnTicketBytes);
+    a.status = d->status;
+    NVFP4_CUDA(launch_attn(mq, mk, mv, a, d->num_sms, (cudaStream_t)stream));
     return NVFP4_OK;
 }
 
@@ -746,11 +817,11 @@ extern "C" {
 
 size_t nvfp4_attn_schedule_bytes(int64_t requests, int64_t tokens, int64_t heads, int64_t kv_heads)
 {
-    if (requests < 1 || tokens < 1 || heads < 1 || kv_heads < 1) return 0;
-    return 256;
+    if (requests < 1 || tokens < 1 || kv_heads < 1 || heads < kv_heads || heads / kv_heads > kAttnRows) return 0;
+    return sizeof(ScheduleHead) + (size_t)max_qtiles(requests, tokens, heads / kv_heads) * sizeof(QTile);
 }
 
-size_t nvfp4_attn_workspace_bytes(void) { return 256; }
+size_t nvfp4_attn_workspace_bytes(void) { return attn_workspace_bytes(current_device_sms()); }
 
 int nvfp4_attn_plan(const nvfp4_step_t* step, nvfp4_stream_t stream)
 {
@@ -815,12 +886,7 @@ int nvfp4_attn_paged(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const 
     AttnKV kv = {};
     kv.k = static_cast<const __nv_bfloat16*>(cache->k);
     kv.v = static_cast<const __nv_bfloat16*>(cache->v);
-    kv.block_table = step->block_table;
-    kv.table_cols = step->table_cols;
-    kv.table_ld = step->table_ld;
-    kv.page_size = cache->page_size;
-    kv.pages = cache->pages;
-    kv.page_stride = cache->page_stride;
+    kv.cache = cache;
     return run_attn(step, io, kv, workspace, workspace_bytes, stream);
 }
 

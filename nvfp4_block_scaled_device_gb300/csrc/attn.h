@@ -18,23 +18,89 @@ constexpr int64_t kStepMaxRequests = 8192;
 constexpr int kStatusPlan = NVFP4_ERR_INVALID_ARG * 100 + 31;
 constexpr int kStatusSlot = NVFP4_ERR_INVALID_ARG * 100 + 32;
 
+// ---- attention schedule (built by the plan kernel, walked by the attention)
+//
+// A row tile is 128 rows of the attention's MMAs: the `group` query heads of
+// one kv head for kAttnRows / group consecutive tokens (row = token * group +
+// head).  A work item is a QTile for one kv head: up to two row tiles of one
+// request, over the 128-key tiles that any of its rows sees.  The items'
+// key tiles, all kv heads of a QTile one after the other, form one axis of
+// `units`; CTA c takes units [c * per_cta, (c + 1) * per_cta), so that every
+// CTA has the same number of key tiles whatever the lengths.
+constexpr int kAttnRows = 128;
+constexpr int kAttnKeys = 128;
+constexpr int kAttnMaxCtas = 256;
+
+struct QTile {
+    int32_t tok0, n_tok;     // packed rows (tokens) tok0 .. tok0 + n_tok - 1
+    int32_t req, pos0;       // the request, the position of token tok0
+    int32_t kv_end, kv_row;  // no row sees keys from kv_end on; packed row of the request's key 0
+    int32_t tile0, tiles;    // key tiles tile0 .. tile0 + tiles - 1
+    int64_t unit0;           // units before this QTile; it has tiles * kv_heads
+    int64_t pad;
+};
+static_assert(sizeof(QTile) == 48, "QTile");
+
+struct ScheduleHead {
+    int64_t units, per_cta;
+    int32_t qtiles, pad[11];
+    int32_t first[kAttnMaxCtas];   // QTile of the first unit of CTA c
+};
+static_assert(sizeof(ScheduleHead) % 16 == 0, "QTiles follow the head, 16-byte aligned");
+
+inline __host__ __device__ const QTile* schedule_tiles(const ScheduleHead* h)
+{
+    return reinterpret_cast<const QTile*>(h + 1);
+}
+
+// Tokens of a row tile.
+inline __host__ __device__ int row_tile_tokens(int group) { return kAttnRows / group; }
+
+// QTiles of any step of that many requests and tokens, at most.
+inline int64_t max_qtiles(int64_t requests, int64_t tokens, int64_t group)
+{
+    const int64_t per = 2 * row_tile_tokens((int)group);
+    const int64_t n = tokens / per + requests;
+    return n < tokens ? n : tokens;
+}
+
 cudaError_t launch_attn_plan(const nvfp4_step_t& step, int* status, int num_sms, cudaStream_t stream);
 
 cudaError_t launch_kv_append(const __nv_bfloat16* k, int64_t ldk, int64_t hk, const __nv_bfloat16* v, int64_t ldv,
                              int64_t hv, const int32_t* slot, int64_t tokens, const nvfp4_kv_cache_t& cache,
                              int* status, int num_sms, cudaStream_t stream);
 
-// Keys and values of an attention call: packed rows (block_table NULL), or
-// the paged cache.
-struct AttnKV {
-    const __nv_bfloat16* k;
-    const __nv_bfloat16* v;
-    int64_t ldk, hk, ldv, hv;          // packed: row and head pitches (elements)
-    const int32_t* block_table;        // paged
-    int64_t table_cols, table_ld, page_size, pages, page_stride;
+// Workspace of the attention kernel: tickets (zero between calls), then two
+// partial slots per CTA: the unnormalised outputs [head_dim / 4][256 rows][4]
+// of an item that other CTAs share, its rows' maxima and sums.
+constexpr size_t kAttnTicketBytes = (size_t)kAttnMaxCtas * 8 * 4;
+constexpr int64_t kAttnSlotRows = 2 * kAttnRows;
+constexpr int64_t kAttnSlotFloats = kAttnSlotRows * (128 + 2);
+inline size_t attn_workspace_bytes(int ctas) { return kAttnTicketBytes + (size_t)ctas * 2 * kAttnSlotFloats * 4; }
+
+// Arguments of the attention kernel (tensor maps apart).
+struct AttnArgs {
+    const ScheduleHead* sched;
+    __nv_bfloat16* out;
+    int64_t ldo, ho;
+    float* lse;
+    int heads, kv_heads, group, head_dim;
+    int window;
+    float scale;
+    // paged cache (block_table NULL: packed keys)
+    const int32_t* block_table;
+    int64_t table_ld;
+    int page_size;
+    int* tickets;
+    float* partials;
+    int* status;
 };
 
-cudaError_t launch_attn(const nvfp4_step_t& step, const nvfp4_attn_io_t& io, const AttnKV& kv, int num_sms,
-                        cudaStream_t stream);
+// map_q: [head_dim, heads, tokens], boxes {64, group, tokens of a row tile};
+// map_k, map_v: packed [head_dim, kv_heads, tokens], boxes {64, 1, 128}, or
+// the cache [head_dim, page_size, kv_heads, pages], boxes {64, page_size, 1, 1};
+// all with 128-byte swizzle.
+cudaError_t launch_attn(const CUtensorMap& map_q, const CUtensorMap& map_k, const CUtensorMap& map_v,
+                        const AttnArgs& args, int num_sms, cudaStream_t stream);
 
 }  // namespace nvfp4

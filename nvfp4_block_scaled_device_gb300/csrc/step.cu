@@ -17,11 +17,13 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kMinUnits = 4;   // key tiles a CTA takes at least: fewer cost more to join than they save
 
 struct PlanParams {
     nvfp4_step_t s;
     int* status;
     int page_shift;
+    int ctas, min_units;     // of the attention kernel: its grid, and the units worth a CTA
 };
 
 __device__ __forceinline__ void report(int* status, int code)
@@ -51,12 +53,103 @@ __device__ __forceinline__ Lens lens_of(const nvfp4_step_t& s, int r)
     return {c < 0 ? 0 : c, q < 0 ? 0 : q, q < 0 || c < 0};
 }
 
+// Block-wide inclusive prefix sum over the threads (kPlanThreads of them);
+// total: the sum of all.  Every thread of the block calls it.
+__device__ __forceinline__ int64_t block_incl_sum(int64_t v, int64_t* warp_sums, int64_t* total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    v = warp_incl_sum(v, lane);
+    __syncthreads();                // the sums of an earlier call have been read
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanWarps; w++) {
+        if (w < warp) before += warp_sums[w];
+        all += warp_sums[w];
+    }
+    *total = all;
+    return v + before;
+}
+
+// The attention's schedule, by one block: the QTiles of all requests in
+// order, the prefix sum of their units, and the QTile of each CTA's first
+// unit.  cu: new tokens before each request (shared memory); tile0: room for
+// R + 1 int32 in shared memory.
+__device__ void build_schedule(const PlanParams& p, const int32_t* cu, int32_t* tile0, int64_t* warp_sums)
+{
+    const nvfp4_step_t& s = p.s;
+    const int R = (int)s.requests, t = threadIdx.x;
+    const int per_tile = 2 * row_tile_tokens((int)(s.heads / s.kv_heads));
+    ScheduleHead* head = static_cast<ScheduleHead*>(s.schedule);
+    QTile* tiles = const_cast<QTile*>(schedule_tiles(head));
+    // QTiles before each request
+    const int per = (R + kPlanThreads - 1) / kPlanThreads;
+    int64_t mine = 0, total = 0;
+    for (int r = t * per; r < min(R, (t + 1) * per); r++) mine += (cu[r + 1] - cu[r] + per_tile - 1) / per_tile;
+    int64_t before = block_incl_sum(mine, warp_sums, &total) - mine;
+    for (int r = t * per; r < min(R, (t + 1) * per); r++) {
+        tile0[r] = (int32_t)before;
+        before += (cu[r + 1] - cu[r] + per_tile - 1) / per_tile;
+    }
+    if (t == 0) tile0[R] = (int32_t)total;
+    __syncthreads();
+    const int n = (int)total;
+    const int64_t cap = s.page_size ? s.table_cols * s.page_size : 0x7fffffff;
+    int64_t units = 0;
+    for (int base = 0; base < n; base += kPlanThreads) {
+        const int i = base + t;
+        QTile q = {};
+        int64_t u = 0;
+        if (i < n) {
+            int lo = 0, hi = R - 1;      // the last request whose first QTile is at or before i
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (tile0[mid] <= i) lo = mid; else hi = mid - 1;
+            }
+            const int off = (i - tile0[lo]) * per_tile, q_len = cu[lo + 1] - cu[lo];
+            const int64_t ctx = lens_of(s, lo).ctx;
+            q.tok0 = cu[lo] + off;
+            q.n_tok = min(per_tile, q_len - off);
+            q.req = lo;
+            q.kv_row = cu[lo];
+            const int64_t pos0 = min(ctx + off, (int64_t)0x7fffffff - q.n_tok);
+            q.pos0 = (int32_t)pos0;
+            const int64_t end = min(min(pos0 + q.n_tok, ctx + q_len), cap);
+            const int64_t begin = s.window ? max(pos0 + 1 - s.window, (int64_t)0) : 0;
+            q.kv_end = (int32_t)end;
+            q.tile0 = (int32_t)(begin / kAttnKeys);
+            // at least one tile, so that rows that see no key are written too
+            q.tiles = (int32_t)max((end + kAttnKeys - 1) / kAttnKeys - q.tile0, (int64_t)1);
+            u = (int64_t)q.tiles * s.kv_heads;
+        }
+        int64_t sum = 0;
+        const int64_t incl = block_incl_sum(u, warp_sums, &sum);
+        if (i < n) {
+            q.unit0 = units + incl - u;
+            tiles[i] = q;
+        }
+        units += sum;
+    }
+    const int64_t share = (units + p.ctas - 1) / p.ctas;
+    const int64_t per_cta = share > p.min_units ? share : p.min_units;
+    if (t == 0) {
+        head->units = units;
+        head->per_cta = per_cta;
+        head->qtiles = n;
+    }
+    for (int i = t; i < n; i += kPlanThreads) {     // each thread reads the entries it wrote
+        const int64_t u0 = tiles[i].unit0, u1 = u0 + (int64_t)tiles[i].tiles * s.kv_heads;
+        for (int64_t c = (u0 + per_cta - 1) / per_cta; c * per_cta < u1; c++) head->first[c] = i;
+    }
+}
+
 // shared memory: cu [R+1] int32 (new tokens before each request, at most
 // `tokens`), first [R+1] int32 (pages taken before each request)
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
 {
     extern __shared__ int32_t sh[];
-    __shared__ int64_t s_q[kPlanWarps], s_n[kPlanWarps];
+    __shared__ int64_t s_sums[kPlanWarps];
     griddep_launch_dependents();
     griddep_wait();                 // the lengths may come from the previous kernel
     const nvfp4_step_t& s = p.s;
@@ -81,21 +174,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         sq += l.q;
         if (paged) sn += ((l.ctx + l.q + round) >> sft) - ((l.ctx + round) >> sft);
     }
-    const int64_t iq = warp_incl_sum(sq, lane), in = warp_incl_sum(sn, lane);
-    if (lane == 31) {
-        s_q[warp] = iq;
-        s_n[warp] = in;
-    }
-    __syncthreads();
-    int64_t bq = iq - sq, bn = in - sn, total_q = 0, total_n = 0;
-    for (int w = 0; w < kPlanWarps; w++) {
-        if (w < warp) {
-            bq += s_q[w];
-            bn += s_n[w];
-        }
-        total_q += s_q[w];
-        total_n += s_n[w];
-    }
+    int64_t total_q = 0, total_n = 0;
+    int64_t bq = block_incl_sum(sq, s_sums, &total_q) - sq;
+    int64_t bn = paged ? block_incl_sum(sn, s_sums, &total_n) - sn : 0;
     const int64_t cap = s.tokens;
     const int64_t cursor = paged && s.cursor ? __ldg(s.cursor) : 0;
     const int64_t kIntMax = 0x7fffffff;
@@ -112,12 +193,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         cu[R] = (int32_t)min(total_q, cap);
         if (total_q > cap) bad = true;
     }
+    const bool scheduler = s.heads != 0 && blockIdx.x == gridDim.x - 1;   // the last block builds the schedule
     if (bad && blockIdx.x == 0) report(p.status, kStatusPlan);
     __syncthreads();
+    if (scheduler) {
+        build_schedule(p, cu, first, s_sums);
+        return;
+    }
+    const int blocks = s.heads ? gridDim.x - 1 : gridDim.x;
     const int32_t T = cu[R];
 
-    // per-request tables: block b takes every gridDim-th request, a warp each
-    for (int r = blockIdx.x * kPlanWarps + warp; r < R; r += gridDim.x * kPlanWarps) {
+    // per-request tables: a warp per request
+    for (int r = blockIdx.x * kPlanWarps + warp; r < R; r += blocks * kPlanWarps) {
         const Lens l = lens_of(s, r);
         const int q = cu[r + 1] - cu[r];
         if (lane == 0) {
@@ -139,7 +226,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         *s.cursor_out = (int32_t)min(cursor + total_n, kIntMax);
 
     // per-token tables
-    for (int64_t i = (int64_t)blockIdx.x * kPlanThreads + t; i < cap; i += (int64_t)gridDim.x * kPlanThreads) {
+    for (int64_t i = (int64_t)blockIdx.x * kPlanThreads + t; i < cap; i += (int64_t)blocks * kPlanThreads) {
         int pos = 0, slot = -1;
         if (i < T) {
             // the last request that starts at or before row i and has rows
@@ -259,6 +346,9 @@ cudaError_t launch_attn_plan(const nvfp4_step_t& step, int* status, int num_sms,
     const int64_t by_requests = (step.requests + kPlanWarps - 1) / kPlanWarps;
     int64_t grid = by_tokens > by_requests ? by_tokens : by_requests;
     if (grid > num_sms) grid = num_sms;
+    if (step.heads) grid++;
+    p.ctas = num_sms < kAttnMaxCtas ? num_sms : kAttnMaxCtas;
+    p.min_units = kMinUnits;
     return launch_programmatic(plan_kernel, dim3((unsigned)grid), dim3(kPlanThreads), smem, stream, p);
 }
 
