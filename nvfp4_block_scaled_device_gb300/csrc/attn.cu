@@ -28,8 +28,10 @@
 // takes a part's last ticket adds the parts up in CTA order (the same result
 // whatever the order of arrival).  No CTA waits for another.
 //
-// Warps: 0-3 and 4-7 softmax and epilogue, 8 MMA, 9 K/V copies, 10 Q copies,
-// 11 the keys' end (below).
+// Warps: 0-3 and 4-7 softmax and epilogue; 8 and 9 the MMAs of the first and
+// the second warpgroup (one warp's instruction stream for both would take
+// longer than the MMAs themselves); 10 K/V copies; 11 Q copies and the keys'
+// end (below).
 //
 // Rows past the last key of an item's last tile hold other requests' rows,
 // pages' unused rows or nothing at all.  Their scores are masked, and warp 11
@@ -45,9 +47,10 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kWarpMma = 8, kWarpKV = 9, kWarpQ = 10, kWarpEnd = 11;
+constexpr int kWarpMma = 8, kWarpKV = 10, kWarpQ = 11;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256;      // + 128 * warpgroup
+constexpr uint32_t kColP = 64;                  // P within S's columns: over the scores of the last 64 keys
 constexpr float kLazy = 8.0f;                   // log2 of the growth that P may carry
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "the block's registers at launch");
@@ -57,11 +60,13 @@ constexpr int kMaxStages = 10;
 struct Ctrl {
     uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], v_end[kMaxStages];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+    uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];
     uint64_t ml_full[4];
+    uint64_t turn[2][4];
     uint64_t teardown;
     uint32_t tmem_base;
     int abort_flag;
+    uint32_t issued;                            // ring stages whose copies have begun
     float m[kAttnRows], l[kAttnRows];           // second warpgroup's statistics (merge)
 };
 
@@ -91,27 +96,90 @@ __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_n_major)
            ((128u >> 4) << 24);
 }
 
-// The warp-wide form of the other kernels: the converged warp executes, one
-// elected lane issues.  kSteps MMAs of K = 16.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// The tensor-core products of one step, each issued by one elected lane of the
+// converged warp from a single asm block (see stage_issue_1sm).
+// S = Q K^T: operands as 128-byte swizzled rows, K-major; K = 16 columns an
+// MMA, 64-column halves 16 KB apart.
+template <int kDP>
+__device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q_lo, uint32_t k_lo, uint32_t hi, uint32_t idesc)
 {
-    asm volatile(
-        "{\n .reg .pred p, e;\n .reg .b32 r;\n"
-        " setp.ne.b32 p, %4, 0;\n"
-        " elect.sync r|e, 0xffffffff;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
-        "}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+    if (kDP == 128)
+        asm volatile(
+        "{\n .reg .pred e, pf, pt;\n .reg .b32 r, x, y;\n .reg .b64 da, db;\n"
+        " elect.sync r|e, 0xffffffff;\n setp.eq.b32 pt, 0, 0;\n setp.ne.b32 pf, 0, 0;\n"
+        " add.u32 x, %1, 0; add.u32 y, %2, 0; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pf;\n"
+        " add.u32 x, %1, 2; add.u32 y, %2, 2; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
+        " add.u32 x, %1, 4; add.u32 y, %2, 4; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
+        " add.u32 x, %1, 6; add.u32 y, %2, 6; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
+        " add.u32 x, %1, 1024; add.u32 y, %2, 1024; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
+        " add.u32 x, %1, 1026; add.u32 y, %2, 1026; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
+        " add.u32 x, %1, 1028; add.u32 y, %2, 1028; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
+        " add.u32 x, %1, 1030; add.u32 y, %2, 1030; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
+        "}\n" ::"r"(s), "r"(q_lo), "r"(k_lo), "r"(hi), "r"(idesc)
+        : "memory");
+    else
+        asm volatile(
+        "{\n .reg .pred e, pf, pt;\n .reg .b32 r, x, y;\n .reg .b64 da, db;\n"
+        " elect.sync r|e, 0xffffffff;\n setp.eq.b32 pt, 0, 0;\n setp.ne.b32 pf, 0, 0;\n"
+        " add.u32 x, %1, 0; add.u32 y, %2, 0; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pf;\n"
+        " add.u32 x, %1, 2; add.u32 y, %2, 2; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
+        " add.u32 x, %1, 4; add.u32 y, %2, 4; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
+        " add.u32 x, %1, 6; add.u32 y, %2, 6; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
+        "}\n" ::"r"(s), "r"(q_lo), "r"(k_lo), "r"(hi), "r"(idesc)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc)
+// O += P V for half of a key tile's keys: P in tensor memory (8 columns for
+// 16 keys), V as stored (N-major; 16 keys are 2 KB).
+template <int kHalf>
+__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint32_t v_lo, uint32_t hi, uint32_t idesc,
+                                         uint32_t acc)
 {
-    asm volatile(
-        "{\n .reg .pred p, e;\n .reg .b32 r;\n"
-        " setp.ne.b32 p, %4, 0;\n"
-        " elect.sync r|e, 0xffffffff;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
-        "}\n" ::"r"(d), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+    if (kHalf == 0)
+        asm volatile(
+        "{\n .reg .pred e, p, pt;\n .reg .b32 r, x, y;\n .reg .b64 db;\n"
+        " elect.sync r|e, 0xffffffff;\n setp.eq.b32 pt, 0, 0;\n setp.ne.b32 p, %5, 0;\n"
+        " add.u32 x, %2, 0; mov.b64 db, {x, %3}; add.u32 y, %1, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, p;\n"
+        " add.u32 x, %2, 128; mov.b64 db, {x, %3}; add.u32 y, %1, 8;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
+        " add.u32 x, %2, 256; mov.b64 db, {x, %3}; add.u32 y, %1, 16;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
+        " add.u32 x, %2, 384; mov.b64 db, {x, %3}; add.u32 y, %1, 24;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
+        "}\n" ::"r"(o), "r"(p), "r"(v_lo), "r"(hi), "r"(idesc), "r"(acc)
         : "memory");
+    else
+        asm volatile(
+        "{\n .reg .pred e, p, pt;\n .reg .b32 r, x, y;\n .reg .b64 db;\n"
+        " elect.sync r|e, 0xffffffff;\n setp.eq.b32 pt, 0, 0;\n setp.ne.b32 p, %5, 0;\n"
+        " add.u32 x, %2, 512; mov.b64 db, {x, %3}; add.u32 y, %1, 32;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, p;\n"
+        " add.u32 x, %2, 640; mov.b64 db, {x, %3}; add.u32 y, %1, 40;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
+        " add.u32 x, %2, 768; mov.b64 db, {x, %3}; add.u32 y, %1, 48;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
+        " add.u32 x, %2, 896; mov.b64 db, {x, %3}; add.u32 y, %1, 56;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
+        "}\n" ::"r"(o), "r"(p), "r"(v_lo), "r"(hi), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// One poll, without waiting (warp-uniform).
+__device__ __forceinline__ bool mbar_test_warp(uint32_t bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z)
@@ -132,15 +200,24 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r)
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v)
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r)
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -185,10 +262,102 @@ __device__ __forceinline__ int atom_add_acq_rel(int* p, int v)
     return old;
 }
 
+// The MMA warp's waits: mbar_wait_warp with less code around the poll.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status, int site)
+{
+    if (mbar_test_warp(bar, parity)) return true;
+    const uint32_t t0 = (uint32_t)clock64();
+    while (!mbar_poll_warp<false>(bar, parity)) {
+        const bool late = (uint32_t)clock64() - t0 > 0xE0000000u;      // about 2 s
+        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+            if (late && *abort_flag == 0) atomicCAS(status, 0, kErrTimeout * 100 + site);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// Waits for the ring's stage use `use` to be full.  A warp that leaves uses to
+// the other MMA warp has not seen their phases end, and a parity wait is only
+// right from the phase before on: so first the copies of this use have begun,
+// which they do once the stage's use before has been consumed.
+__device__ __forceinline__ bool wait_use(const volatile uint32_t* issued, uint32_t use, uint32_t bar, uint32_t parity,
+                                         volatile int* abort_flag, int* status, int site)
+{
+    if (__any_sync(0xffffffffu, (int32_t)(*issued - use) <= 0)) {
+        const uint32_t t0 = (uint32_t)clock64();
+        while (__any_sync(0xffffffffu, (int32_t)(*issued - use) <= 0)) {
+            const bool late = (uint32_t)clock64() - t0 > 0xE0000000u;
+            if (__any_sync(0xffffffffu, late || *abort_flag)) {
+                if (late && *abort_flag == 0) atomicCAS(status, 0, kErrTimeout * 100 + site);
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+    return wait_on(bar, parity, abort_flag, status, site);
+}
+
+// Scores of 64 keys from tensor memory, and what is done to them: the sign of
+// a negative scale, -inf at keys outside lw .. h - 1.
+__device__ __forceinline__ void load_half(float* s, uint32_t taddr)
+{
+    tmem_ld32(taddr, s);
+    tmem_ld32(taddr + 32, s + 32);
+    tmem_ld_wait();
+}
+__device__ __forceinline__ void finish_half(float* s, bool negate, bool masked, int h, int lw)
+{
+    if (negate) {
+#pragma unroll
+        for (int k = 0; k < 64; k++) s[k] = -s[k];
+    }
+    if (masked) {
+#pragma unroll
+        for (int k = 0; k < 64; k++) s[k] = k < h && k >= lw ? s[k] : -INFINITY;
+    }
+}
+
+// P of 64 keys into tensor memory: e = 2^(c s + mc) as bf16 pairs; returns
+// the two partial sums of e.
+__device__ __forceinline__ float2 exp_half(const float* s, float c, float mc, uint32_t taddr)
+{
+    float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        uint32_t r[16];
+#pragma unroll
+        for (int y = 0; y < 16; y++) {
+            const int x = 32 * k + 2 * y;
+            float2 e = fma2(make_float2(s[x], s[x + 1]), make_float2(c, c), make_float2(mc, mc));
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            sum[y & 1] = add2(sum[y & 1], e);
+            r[y] = cvt_bf16x2(e.x, e.y);
+        }
+        tmem_st16(taddr + 16 * k, r);
+    }
+    return add2(sum[0], sum[1]);
+}
+
+__device__ __forceinline__ float max128(const float* s)
+{
+    float x[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+    for (int k = 4; k < 124; k += 8) {
+#pragma unroll
+        for (int y = 0; y < 4; y++) x[y] = max3(x[y], s[k + 2 * y], s[k + 2 * y + 1]);
+    }
+#pragma unroll
+    for (int y = 0; y < 4; y++) x[y] = fmaxf(x[y], s[124 + y]);
+    return fmaxf(max3(x[0], x[1], x[2]), x[3]);
+}
+
 // ------------------------------------------------------------------ pieces
 // A CTA's share of one item.
 struct Piece {
-    QTile q;
+    int tok0, n_tok, req, pos0, kv_end, kv_row;   // of its QTile
     int hk;              // kv head
     int tile0, n;        // key tiles tile0 .. tile0 + n - 1
     bool two;            // two row tiles
@@ -196,49 +365,66 @@ struct Piece {
 };
 
 // The pieces of CTA `cta` in order; every warp of the CTA walks them alike.
+// kAhead: the next QTile is fetched while the current one is worked on.
+template <bool kAhead>
 struct Pieces {
-    const ScheduleHead* s;
-    int64_t u, end, per_cta;
-    int qt;
-    int kv_heads, row_tokens;
+    const int4* table;
+    int u, end, per_cta, qt, kv_heads, row_tokens;
+    int4 f0, f1, f2;     // QTile qt, or (kAhead) the one that comes next
 
     __device__ __forceinline__ Pieces(const AttnArgs& a, int cta)
     {
-        s = a.sched;
+        const ScheduleHead* s = a.sched;
+        table = reinterpret_cast<const int4*>(schedule_tiles(s));
         kv_heads = a.kv_heads;
         row_tokens = row_tile_tokens(a.group);
-        const int64_t units = s->units;
+        const int4* start = reinterpret_cast<const int4*>(&s->start[cta]);
+        f0 = start[0];
+        f1 = start[1];
+        f2 = start[2];
+        qt = s->first[cta];
+        const int units = s->units;
         per_cta = s->per_cta;
-        u = cta * per_cta;
-        end = u + per_cta < units ? u + per_cta : units;
-        qt = u < end ? s->first[cta] : 0;
+        u = cta * per_cta < units ? cta * per_cta : units;
+        end = units - u < per_cta ? units : u + per_cta;
     }
     __device__ __forceinline__ bool next(Piece& p)
     {
         if (u >= end) return false;
-        const int4* e = reinterpret_cast<const int4*>(schedule_tiles(s) + qt);
-        const int4 e0 = e[0], e1 = e[1], e2 = e[2];
-        p.q.tok0 = e0.x;
-        p.q.n_tok = e0.y;
-        p.q.req = e0.z;
-        p.q.pos0 = e0.w;
-        p.q.kv_end = e1.x;
-        p.q.kv_row = e1.y;
-        p.q.tiles = e1.w;
-        const int64_t unit0 = (int64_t)(uint32_t)e2.x | ((int64_t)e2.y << 32);
-        const int rel = (int)(u - unit0), tiles = e1.w;
+        int rel = u - f2.x;
+        if (!kAhead && rel == f1.w * kv_heads) {
+            qt++;
+            f0 = table[3 * qt];
+            f1 = table[3 * qt + 1];
+            f2 = table[3 * qt + 2];
+            rel = 0;
+        }
+        const int tiles = f1.w;
+        p.tok0 = f0.x;
+        p.n_tok = f0.y;
+        p.req = f0.z;
+        p.pos0 = f0.w;
+        p.kv_end = f1.x;
+        p.kv_row = f1.y;
         p.hk = rel / tiles;
         const int k0 = rel - p.hk * tiles;
-        const int64_t left = end - u;
-        p.n = left < tiles - k0 ? (int)left : tiles - k0;
-        p.tile0 = e1.z + k0;
-        p.two = e0.y > row_tokens;
-        const int64_t i0 = u - k0;                   // the item's first unit
-        const int64_t c0 = i0 / per_cta, c1 = (i0 + tiles - 1) / per_cta;
-        p.cta0 = (int)c0;
-        p.parts = (int)(c1 - c0) + 1;
+        p.n = min(end - u, tiles - k0);
+        p.tile0 = f1.z + k0;
+        p.two = f0.y > row_tokens;
+        p.cta0 = 0;
+        p.parts = 1;
+        if (p.n < tiles) {                           // shared with other CTAs
+            const int i0 = u - k0;
+            p.cta0 = i0 / per_cta;
+            p.parts = (i0 + tiles - 1) / per_cta - p.cta0 + 1;
+        }
         u += p.n;
-        if (rel + p.n == tiles * kv_heads) qt++;
+        if (kAhead && rel + p.n == tiles * kv_heads && u < end) {
+            qt++;
+            f0 = table[3 * qt];
+            f1 = table[3 * qt + 1];
+            f2 = table[3 * qt + 2];
+        }
         return true;
     }
 };
@@ -272,20 +458,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; s++) {
             mbar_init(smem_u32(&ctrl->kv_full[s]), 1);
-            mbar_init(smem_u32(&ctrl->kv_empty[s]), 1);
+            mbar_init(smem_u32(&ctrl->kv_empty[s]), 2);      // both MMA warps
             mbar_init(smem_u32(&ctrl->v_end[s]), 1);
         }
         mbar_init(smem_u32(&ctrl->q_full), 1);
-        mbar_init(smem_u32(&ctrl->q_empty), 1);
+        mbar_init(smem_u32(&ctrl->q_empty), 2);
         for (int j = 0; j < 2; j++) {
             mbar_init(smem_u32(&ctrl->s_full[j]), 1);
+            mbar_init(smem_u32(&ctrl->p_half[j]), 4);
             mbar_init(smem_u32(&ctrl->p_full[j]), 4);
             mbar_init(smem_u32(&ctrl->o_full[j]), 1);
             mbar_init(smem_u32(&ctrl->o_free[j]), 4);
         }
-        for (int w = 0; w < 4; w++) mbar_init(smem_u32(&ctrl->ml_full[w]), 1);
-        mbar_init(smem_u32(&ctrl->teardown), 1);
+        for (int w = 0; w < 4; w++) {
+            mbar_init(smem_u32(&ctrl->ml_full[w]), 1);
+            mbar_init(smem_u32(&ctrl->turn[0][w]), 1);
+            mbar_init(smem_u32(&ctrl->turn[1][w]), 1);
+        }
+        mbar_init(smem_u32(&ctrl->teardown), 2);
         ctrl->abort_flag = 0;
+        ctrl->issued = 0;
         fence_barrier_init();
     }
     if (warp == kWarpKV && lane == 0) {
@@ -303,10 +495,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const uint32_t tmem = ctrl->tmem_base;
     griddep_launch_dependents();
     griddep_wait();                  // schedule, Q, K, V, outputs, workspace: after the previous kernel
-    Pieces pieces(a, cta);
     Piece p;
 
     if (warp >= 8) {
+        Pieces<true> pieces(a, cta);
         setmaxnreg_dec<kRegsOther>();
         if (warp == kWarpKV) {
             // ------------------------------------------------ K/V copies
@@ -316,10 +508,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             uint32_t issued = 0, issued_ph = 0;   // stages with copies under way, and whose phase
             bool ok = true;
             while (ok && pieces.next(p)) {
-                const int* table = paged ? a.block_table + (int64_t)p.q.req * a.table_ld : nullptr;
+                const int* table = paged ? a.block_table + (int64_t)p.req * a.table_ld : nullptr;
                 for (int i = 0; i < p.n && ok; i++) {
                     const int key0 = (p.tile0 + i) * kAttnKeys;
-                    const int valid = min(kAttnKeys, max(p.q.kv_end - key0, 0));
+                    const int valid = min(kAttnKeys, max(p.kv_end - key0, 0));
                     const int pages = paged ? (valid + a.page_size - 1) / a.page_size : 0;
                     int page = 0;
                     if (lane < pages) page = __ldg(table + (key0 / a.page_size) + lane);
@@ -330,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                             ok = false;
                             break;
                         }
+                        if (lane == 0) *(volatile uint32_t*)&ctrl->issued = use + 1;
                         const CUtensorMap* map = kv ? &prm.map_v : &prm.map_k;
                         const uint32_t dst = base + C::kOffRing + s * C::kTileBytes;
                         // an item's last values go through warp 11
@@ -347,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                                 tma_load_4d(dst + half * 16384 + pg * a.page_size * 128, map, bar, half * 64, 0, p.hk,
                                             id);
                         } else if (lane < C::kHalves) {
-                            tma_load_3d(dst + lane * 16384, map, bar, lane * 64, p.hk, p.q.kv_row + key0);
+                            tma_load_3d(dst + lane * 16384, map, bar, lane * 64, p.hk, p.kv_row + key0);
                         }
                         __syncwarp();
                         issued |= 1u << s;
@@ -369,40 +562,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             }
             __syncwarp();
         } else if (warp == kWarpQ) {
-            // --------------------------------------------------- Q copies
-            uint32_t n = 0;
+            // ------------------- Q copies, and values past the last key
+            uint32_t n = 0, tile = 0, ends = 0;    // items, key tiles; ends: bit s = phase of v_end[s]
             bool ok = true;
-            const int rows = a.group * row_tile_tokens(a.group);
+            const int row_tokens = row_tile_tokens(a.group), rows = a.group * row_tokens;
+            const uint32_t bar = smem_u32(&ctrl->q_full);
             while (pieces.next(p)) {
                 if (!mbar_wait_warp(smem_u32(&ctrl->q_empty), (n & 1u) ^ 1u, abort_flag, status, 42)) {
                     ok = false;
                     break;
                 }
                 const int boxes = (p.two ? 2 : 1) * C::kHalves;
-                const uint32_t bar = smem_u32(&ctrl->q_full);
                 if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * rows * 128));
                 __syncwarp();
                 if (lane < boxes) {
                     const int j = lane / C::kHalves, half = lane - j * C::kHalves;
                     tma_load_3d(base + j * C::kTileBytes + half * 16384, &prm.map_q, bar, half * 64, p.hk * a.group,
-                                p.q.tok0 + j * row_tile_tokens(a.group));
+                                p.tok0 + j * row_tokens);
                 }
                 __syncwarp();
                 n++;
-            }
-            if (!ok && n > 0 && lane == 0) mbar_wait_teardown(smem_u32(&ctrl->q_full), (n - 1) & 1u);
-            __syncwarp();
-        } else if (warp == kWarpEnd) {
-            // ----------------------------------- values past the last key
-            uint32_t tile = 0, ends = 0;       // ends: bit s = phase of v_end[s]
-            while (pieces.next(p)) {
                 tile += p.n;
-                const int key0 = (p.tile0 + p.n - 1) * kAttnKeys;
-                const int valid = min(kAttnKeys, max(p.q.kv_end - key0, 0));
+                const int valid = min(kAttnKeys, max(p.kv_end - (p.tile0 + p.n - 1) * kAttnKeys, 0));
                 if (valid == kAttnKeys) continue;
                 uint32_t ph;
                 const uint32_t s = stage_of<kStages>(2 * (tile - 1) + 1, &ph);
-                if (!mbar_wait_warp<true>(smem_u32(&ctrl->v_end[s]), (ends >> s) & 1u, abort_flag, status, 43)) break;
+                if (!mbar_wait_warp<true>(smem_u32(&ctrl->v_end[s]), (ends >> s) & 1u, abort_flag, status, 43)) {
+                    ok = false;
+                    break;
+                }
                 ends ^= 1u << s;
                 uint8_t* v = smem + C::kOffRing + s * C::kTileBytes;
                 const int vec = (kAttnKeys - valid) * 8;          // 16-byte vectors of a half's rows
@@ -414,65 +602,86 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ctrl->kv_full[s]));
             }
+            if (!ok && n > 0 && lane == 0) mbar_wait_teardown(bar, (n - 1) & 1u);
+            __syncwarp();
         } else {
             // ------------------------------------------------------- MMA
-            const uint64_t kdesc0 = make_smem_desc(base, 16, 1024, 2);              // K-major: 8-row groups 1 KB apart
-            const uint64_t vdesc0 = make_smem_desc(base, 16384, 1024, 2);           // N-major: 64-column halves 16 KB
-                                                                                    // apart, 8-key groups 1 KB apart
+            // Warp 8 + j issues warpgroup j's products: S of a key tile, then
+            // its O once P is there, then the next S into the same columns,
+            // across items too.  Two row tiles: both warps use every key
+            // tile; one row tile: warp j the tiles j, j + 2, ...  Either way
+            // a stage is free after two commits on it.
+            const int j = warp - kWarpMma;
+            const uint64_t kdesc0 = make_smem_desc(base, 16, 1024, 2);       // K-major: 8-row groups 1 KB apart
+            const uint64_t vdesc0 = make_smem_desc(base, 16384, 1024, 2);    // N-major: 64-column halves 16 KB
+                                                                             // apart, 8-key groups 1 KB apart
             constexpr uint32_t kIdescS = idesc_of(128, false), kIdescO = idesc_of(kDP, true);
-            uint32_t tile = 0, np = 0;                  // key tiles and pieces done
-            uint32_t p_cnt[2] = {0, 0}, o_cnt[2] = {0, 0};
+            const uint32_t k_hi = (uint32_t)(kdesc0 >> 32), v_hi = (uint32_t)(vdesc0 >> 32);
+            const uint32_t q_lo = (uint32_t)kdesc0;
+            const uint32_t ring_k = q_lo + (C::kOffRing >> 4), ring_v = (uint32_t)vdesc0 + (C::kOffRing >> 4);
+            const uint32_t full0 = smem_u32(&ctrl->kv_full[0]), empty0 = smem_u32(&ctrl->kv_empty[0]);
+            const uint32_t ts = tmem + kColS + 128u * j, to = tmem + kColO + 128u * j;
+            const uint32_t s_full = smem_u32(&ctrl->s_full[j]), o_full = smem_u32(&ctrl->o_full[j]);
+            const uint32_t p_half = smem_u32(&ctrl->p_half[j]), p_full = smem_u32(&ctrl->p_full[j]);
+            const uint32_t q_empty = smem_u32(&ctrl->q_empty);
+            uint32_t use = 0;                      // stages used by the items before
+            uint32_t qph = 0, pph = 0, oph = 1;    // phases: Q, P, O free (nothing to wait for at first)
             bool ok = true;
             while (ok && pieces.next(p)) {
-                const int N = p.two ? 2 * p.n : p.n;
-                if (!mbar_wait_warp(smem_u32(&ctrl->q_full), np & 1u, abort_flag, status, 44)) break;
-                np++;
-                // step n: warpgroup n & 1, key tile n / 2 (two row tiles) or n
-                auto issue_s = [&](int n) {
-                    const int j = n & 1, i = p.two ? n >> 1 : n;
-                    uint32_t ph;
-                    const uint32_t s = stage_of<kStages>(2 * (tile + i), &ph);
-                    if (!mbar_wait_warp(smem_u32(&ctrl->kv_full[s]), ph, abort_flag, status, 45)) return false;
-                    tc_fence_after();
-                    const uint64_t qd = kdesc0 + ((p.two && j ? C::kTileBytes : 0) >> 4);
-                    const uint64_t kd = kdesc0 + ((C::kOffRing + s * C::kTileBytes) >> 4);
-#pragma unroll
-                    for (int k = 0; k < kDP / 16; k++) {
-                        const uint32_t off = (uint32_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                        mma_ss(tmem + kColS + 128 * j, qd + off, kd + off, kIdescS, k != 0);
+                const int first = p.two ? 0 : j, by = p.two ? 1 : 2;
+                uint32_t kph;                      // stage of the warp's next K, its phase; V is in the stage after
+                uint32_t ks = stage_of<kStages>(use + 2 * first, &kph);
+                const uint32_t qt = q_lo + (p.two && j ? C::kTileBytes >> 4 : 0);
+                if (!wait_on(smem_u32(&ctrl->q_full), qph, abort_flag, status, 44)) break;
+                qph ^= 1u;
+                if (first >= p.n && lane == 0) mbar_arrive(q_empty);     // no tile for this warp
+                for (int i = first; i < p.n; i += by) {
+                    const uint32_t ku = use + 2u * (uint32_t)i;
+                    if (!wait_use(&ctrl->issued, ku, full0 + 8u * ks, kph, abort_flag, status, 45)) {
+                        ok = false;
+                        break;
                     }
-                    if (!p.two || j) mma_commit_warp(smem_u32(&ctrl->kv_empty[s]));
-                    mma_commit_warp(smem_u32(&ctrl->s_full[j]));
-                    if (n == N - 1) mma_commit_warp(smem_u32(&ctrl->q_empty));
-                    return true;
-                };
-                auto issue_o = [&](int n) {
-                    const int j = n & 1, i = p.two ? n >> 1 : n;
-                    uint32_t ph;
-                    const uint32_t s = stage_of<kStages>(2 * (tile + i) + 1, &ph);
-                    if (!mbar_wait_warp(smem_u32(&ctrl->kv_full[s]), ph, abort_flag, status, 46)) return false;
-                    if (n < 2) {
-                        // the accumulator's previous item has been read
-                        if (o_cnt[j] > 0 && !mbar_wait_warp(smem_u32(&ctrl->o_free[j]), (o_cnt[j] - 1) & 1u, abort_flag,
-                                                            status, 47))
-                            return false;
-                        o_cnt[j]++;
-                    }
-                    if (!mbar_wait_warp(smem_u32(&ctrl->p_full[j]), p_cnt[j] & 1u, abort_flag, status, 48)) return false;
-                    p_cnt[j]++;
                     tc_fence_after();
-                    const uint64_t vd = vdesc0 + ((C::kOffRing + s * C::kTileBytes) >> 4);
-#pragma unroll
-                    for (int k = 0; k < kAttnKeys / 16; k++)
-                        mma_ts(tmem + kColO + 128 * j, tmem + kColS + 128 * j + 8 * k, vd + ((k * 2048) >> 4), kIdescO,
-                               n >= 2 || k != 0);
-                    if (!p.two || j) mma_commit_warp(smem_u32(&ctrl->kv_empty[s]));
-                    mma_commit_warp(smem_u32(&ctrl->o_full[j]));
-                    return true;
-                };
-                ok = issue_s(0) && (N < 2 || issue_s(1));
-                for (int n = 0; n < N && ok; n++) ok = issue_o(n) && (n + 2 >= N || issue_s(n + 2));
-                tile += p.n;
+                    issue_qk<kDP>(ts, qt, ring_k + ks * (C::kTileBytes >> 4), k_hi, kIdescS);
+                    mma_commit_warp(s_full);
+                    mma_commit_warp(empty0 + 8u * ks);
+                    if (!p.two) mma_commit_warp(empty0 + 8u * ks);
+                    if (i + by >= p.n) mma_commit_warp(q_empty);
+                    const bool wrap = ks + 1 == kStages;
+                    const uint32_t vs = wrap ? 0 : ks + 1, vph = wrap ? kph ^ 1u : kph;
+                    // the accumulator's previous item has been read
+                    if (i == first) {
+                        if (!wait_on(smem_u32(&ctrl->o_free[j]), oph, abort_flag, status, 47)) {
+                            ok = false;
+                            break;
+                        }
+                        oph ^= 1u;
+                    }
+                    const uint32_t v_lo = ring_v + vs * (C::kTileBytes >> 4);
+                    if (!wait_use(&ctrl->issued, ku + 1, full0 + 8u * vs, vph, abort_flag, status, 46) ||
+                        !wait_on(p_half, pph, abort_flag, status, 48)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    issue_pv<0>(to, ts + kColP, v_lo, v_hi, kIdescO, i != first);
+                    if (!wait_on(p_full, pph, abort_flag, status, 49)) {
+                        ok = false;
+                        break;
+                    }
+                    pph ^= 1u;
+                    tc_fence_after();
+                    issue_pv<1>(to, ts + kColP, v_lo, v_hi, kIdescO, 1u);
+                    mma_commit_warp(o_full);
+                    mma_commit_warp(empty0 + 8u * vs);
+                    if (!p.two) mma_commit_warp(empty0 + 8u * vs);
+                    ks += 2 * by;
+                    if (ks >= kStages) {
+                        ks -= kStages;
+                        kph ^= 1u;
+                    }
+                }
+                use += 2u * (uint32_t)p.n;
             }
             // every MMA issued has completed before teardown
             mma_commit_warp(smem_u32(&ctrl->teardown));
@@ -482,25 +691,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     } else {
         // ------------------------------------------- softmax and epilogue
         setmaxnreg_inc<kRegsSoftmax>();
+        Pieces<false> pieces(a, cta);
         const int j = warp >> 2, w = warp & 3;
         const int row = w * 32 + lane;
         const int row_tokens = row_tile_tokens(a.group);
         const int tk = row / a.group, g = row - tk * a.group;    // this thread's token and head in a row tile
         const uint32_t lane_addr = tmem + ((uint32_t)(w * 32) << 16);
-        const uint32_t ts = lane_addr + kColS + 128 * j, to = lane_addr + kColO + 128 * j;
+        const uint32_t ts = lane_addr + kColS + 128 * j, tp = ts + kColP, to = lane_addr + kColO + 128 * j;
         const bool negate = a.scale < 0.0f;
         // a zero scale: any tiny factor gives equal probabilities, without 0 * inf at masked keys
         const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
         const float lazy = kLazy / c;
-        uint32_t s_cnt = 0, ml_cnt = 0;
+        uint32_t s_cnt = 0, ml_cnt = 0, t_cnt = 0;
         bool ok = true;
         while (ok && pieces.next(p)) {
             const int N = p.two ? 2 * p.n : p.n;
             const int t = (p.two && j ? row_tokens : 0) + tk;    // token of the item
-            const bool mine = tk < row_tokens && t < p.q.n_tok;
+            const bool mine = tk < row_tokens && t < p.n_tok;
             const bool any = __any_sync(0xffffffffu, mine);
-            const int pos = p.q.pos0 + t;
-            const int hi = mine ? min(pos + 1, p.q.kv_end) : 0;      // keys lo .. hi - 1
+            const int pos = p.pos0 + t;
+            const int hi = mine ? min(pos + 1, p.kv_end) : 0;      // keys lo .. hi - 1
             const int lo = mine && a.window ? max(pos + 1 - a.window, 0) : 0;
             float m = -INFINITY, l = 0.0f;
             if (j >= N) continue;            // the second warpgroup of a single key tile
@@ -511,31 +721,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     break;
                 }
                 s_cnt++;
+                if (p.two) {
+                    // the two warpgroups' exponentials in turn (per pair of
+                    // warps): together they would wait for the tensor pipe
+                    // together, and leave it idle together
+                    if (!mbar_wait_warp(smem_u32(&ctrl->turn[j][w]), (t_cnt & 1u) ^ (j ? 0u : 1u), abort_flag, status,
+                                        54)) {
+                        ok = false;
+                        break;
+                    }
+                    t_cnt++;
+                }
                 if (any) {
                     tc_fence_after();
                     float s[128];
-#pragma unroll
-                    for (int k = 0; k < 4; k++) tmem_ld32(ts + 32 * k, s + 32 * k);
-                    tmem_ld_wait();
-                    if (negate) {
-#pragma unroll
-                        for (int k = 0; k < 128; k++) s[k] = -s[k];
-                    }
+                    load_half(s, ts);
+                    load_half(s + 64, ts + 64);
                     const int key0 = (p.tile0 + i) * kAttnKeys;
                     const int h = hi - key0, lw = lo - key0;
-                    if (__any_sync(0xffffffffu, mine && (h < kAttnKeys || lw > 0))) {
-#pragma unroll
-                        for (int k = 0; k < 128; k++) s[k] = k < h && k >= lw ? s[k] : -INFINITY;
-                    }
-                    float x[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                    for (int k = 4; k < 124; k += 8) {
-#pragma unroll
-                        for (int y = 0; y < 4; y++) x[y] = max3(x[y], s[k + 2 * y], s[k + 2 * y + 1]);
-                    }
-#pragma unroll
-                    for (int y = 0; y < 4; y++) x[y] = fmaxf(x[y], s[124 + y]);
-                    const float mx = fmaxf(max3(x[0], x[1], x[2]), x[3]);
+                    const bool masked = __any_sync(0xffffffffu, mine && (h < kAttnKeys || lw > 0));
+                    finish_half(s, negate, masked, h, lw);
+                    finish_half(s + 64, negate, masked, h - 64, lw - 64);
+                    // P of the first 64 keys with the m in use, the tile's
+                    // maximum beside it; where the maximum has outgrown m
+                    // (and at an item's first tile) that is done again
+                    float mc = m == -INFINITY ? 0.0f : -m * c;
+                    const float mx = max128(s);
+                    float2 sum = exp_half(s, c, mc, tp);
                     const bool up = mine && (mx > m + lazy || (m == -INFINITY && mx > m));
                     if (__any_sync(0xffffffffu, up)) {
                         const float m1 = up ? mx : m;
@@ -549,38 +761,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                             }
                             tc_fence_after();
 #pragma unroll 1
-                            for (int k = 0; k < kDP / 32; k++) {
-                                float o[32];
-                                tmem_ld32(to + 32 * k, o);
+                            for (int k = 0; k < kDP / 16; k++) {
+                                float o[16];
+                                tmem_ld16(to + 16 * k, o);
                                 tmem_ld_wait();
-                                uint32_t r[32];
+                                uint32_t q[16];
 #pragma unroll
-                                for (int y = 0; y < 32; y++) r[y] = __float_as_uint(f == 0.0f ? 0.0f : o[y] * f);
-                                tmem_st32(to + 32 * k, r);
+                                for (int y = 0; y < 16; y++) q[y] = __float_as_uint(f == 0.0f ? 0.0f : o[y] * f);
+                                tmem_st16(to + 16 * k, q);
                             }
                         }
                         m = m1;
+                        mc = m == -INFINITY ? 0.0f : -m * c;
+                        load_half(s, ts);        // P has not touched their columns
+                        finish_half(s, negate, masked, h, lw);
+                        sum = exp_half(s, c, mc, tp);
                     }
-                    const float mc = m == -INFINITY ? 0.0f : -m * c;
-                    float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-#pragma unroll
-                    for (int k = 0; k < 2; k++) {
-                        uint32_t r[32];
-#pragma unroll
-                        for (int y = 0; y < 32; y++) {
-                            float2 e = fma2(make_float2(s[64 * k + 2 * y], s[64 * k + 2 * y + 1]), make_float2(c, c),
-                                            make_float2(mc, mc));
-                            e.x = ex2(e.x);
-                            e.y = ex2(e.y);
-                            sum[y & 1] = add2(sum[y & 1], e);
-                            r[y] = cvt_bf16x2(e.x, e.y);
-                        }
-                        tmem_st32(ts + 32 * k, r);
-                    }
-                    sum[0] = add2(sum[0], sum[1]);
-                    l += sum[0].x + sum[0].y;
                     tmem_st_wait();
                     tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&ctrl->p_half[j]));
+                        if (p.two) mbar_arrive(smem_u32(&ctrl->turn[1 - j][w]));
+                    }
+                    sum = add2(sum, exp_half(s + 64, c, mc, tp + 32));
+                    l += sum.x + sum.y;
+                    tmem_st_wait();
+                    tc_fence_before();
+                } else if (lane == 0) {
+                    mbar_arrive(smem_u32(&ctrl->p_half[j]));
+                    if (p.two) mbar_arrive(smem_u32(&ctrl->turn[1 - j][w]));
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ctrl->p_full[j]));
@@ -614,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             const bool whole = p.parts == 1;
             const bool none = l == 0.0f;                         // the row sees no key
             const int head = p.hk * a.group + g;
-            const int64_t tok = p.q.tok0 + t;
+            const int64_t tok = p.tok0 + t;
             if (any) {
                 const float inv = whole ? (none ? 0.0f : 1.0f / l) : 1.0f;
                 const int slot = 2 * cta + (p.cta0 == cta ? 1 : 0);

@@ -36,15 +36,14 @@ struct QTile {
     int32_t req, pos0;       // the request, the position of token tok0
     int32_t kv_end, kv_row;  // no row sees keys from kv_end on; packed row of the request's key 0
     int32_t tile0, tiles;    // key tiles tile0 .. tile0 + tiles - 1
-    int64_t unit0;           // units before this QTile; it has tiles * kv_heads
-    int64_t pad;
+    int32_t unit0, pad[3];   // units before this QTile; it has tiles * kv_heads
 };
 static_assert(sizeof(QTile) == 48, "QTile");
 
 struct ScheduleHead {
-    int64_t units, per_cta;
-    int32_t qtiles, pad[11];
-    int32_t first[kAttnMaxCtas];   // QTile of the first unit of CTA c
+    int32_t units, per_cta, qtiles, pad[13];
+    int32_t first[kAttnMaxCtas];   // QTile of the first unit of CTA c ...
+    QTile start[kAttnMaxCtas];     // ... and a copy of it, next to what a CTA reads first
 };
 static_assert(sizeof(ScheduleHead) % 16 == 0, "QTiles follow the head, 16-byte aligned");
 

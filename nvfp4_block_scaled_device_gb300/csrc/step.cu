@@ -17,13 +17,14 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kMinUnits = 4;   // key tiles a CTA takes at least: fewer cost more to join than they save
+constexpr int64_t kMaxUnits = (int64_t)1 << 30;   // of a schedule (a call of seconds): the rest is not worked on
+constexpr int kMinUnits = 4;   // key tiles of a shared item's parts, at least: smaller ones cost more to join than they save
 
 struct PlanParams {
     nvfp4_step_t s;
     int* status;
     int page_shift;
-    int ctas, min_units;     // of the attention kernel: its grid, and the units worth a CTA
+    int ctas;                // the attention kernel's grid
 };
 
 __device__ __forceinline__ void report(int* status, int code)
@@ -92,7 +93,10 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, int32_t* 
         tile0[r] = (int32_t)before;
         before += (cu[r + 1] - cu[r] + per_tile - 1) / per_tile;
     }
-    if (t == 0) tile0[R] = (int32_t)total;
+    if (t == 0) {
+        tile0[R] = (int32_t)total;
+        warp_sums[kPlanWarps] = 1;                  // tiles of the longest QTile
+    }
     __syncthreads();
     const int n = (int)total;
     const int64_t cap = s.page_size ? s.table_cols * s.page_size : 0x7fffffff;
@@ -122,25 +126,36 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, int32_t* 
             // at least one tile, so that rows that see no key are written too
             q.tiles = (int32_t)max((end + kAttnKeys - 1) / kAttnKeys - q.tile0, (int64_t)1);
             u = (int64_t)q.tiles * s.kv_heads;
+            atomicMax(reinterpret_cast<unsigned long long*>(warp_sums + kPlanWarps), (unsigned long long)q.tiles);
         }
         int64_t sum = 0;
         const int64_t incl = block_incl_sum(u, warp_sums, &sum);
         if (i < n) {
-            q.unit0 = units + incl - u;
+            q.unit0 = (int32_t)min(units + incl - u, kMaxUnits);
             tiles[i] = q;
         }
         units += sum;
     }
+    if (units > kMaxUnits) {
+        units = kMaxUnits;
+        if (t == 0) report(p.status, kStatusPlan);
+    }
+    __syncthreads();
     const int64_t share = (units + p.ctas - 1) / p.ctas;
-    const int64_t per_cta = share > p.min_units ? share : p.min_units;
+    const int64_t least = min((int64_t)kMinUnits, warp_sums[kPlanWarps]);
+    const int64_t per_cta = share > least ? share : least;
     if (t == 0) {
-        head->units = units;
-        head->per_cta = per_cta;
+        head->units = (int32_t)units;
+        head->per_cta = (int32_t)per_cta;
         head->qtiles = n;
     }
     for (int i = t; i < n; i += kPlanThreads) {     // each thread reads the entries it wrote
-        const int64_t u0 = tiles[i].unit0, u1 = u0 + (int64_t)tiles[i].tiles * s.kv_heads;
-        for (int64_t c = (u0 + per_cta - 1) / per_cta; c * per_cta < u1; c++) head->first[c] = i;
+        const QTile q = tiles[i];
+        const int64_t u1 = min(q.unit0 + (int64_t)q.tiles * s.kv_heads, units);
+        for (int64_t c = (q.unit0 + per_cta - 1) / per_cta; c * per_cta < u1; c++) {
+            head->first[c] = i;
+            head->start[c] = q;
+        }
     }
 }
 
@@ -149,7 +164,7 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, int32_t* 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
 {
     extern __shared__ int32_t sh[];
-    __shared__ int64_t s_sums[kPlanWarps];
+    __shared__ int64_t s_sums[kPlanWarps + 1];
     griddep_launch_dependents();
     griddep_wait();                 // the lengths may come from the previous kernel
     const nvfp4_step_t& s = p.s;
@@ -348,7 +363,6 @@ cudaError_t launch_attn_plan(const nvfp4_step_t& step, int* status, int num_sms,
     if (grid > num_sms) grid = num_sms;
     if (step.heads) grid++;
     p.ctas = num_sms < kAttnMaxCtas ? num_sms : kAttnMaxCtas;
-    p.min_units = kMinUnits;
     return launch_programmatic(plan_kernel, dim3((unsigned)grid), dim3(kPlanThreads), smem, stream, p);
 }
 
