@@ -56,6 +56,7 @@ constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "the block's registers at launch");
 
 constexpr int kMaxStages = 10;
+constexpr int kJoin = 8;                        // vectors of a shared item's parts under way per lane
 
 struct Ctrl {
     uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], v_end[kMaxStages];
@@ -388,44 +389,49 @@ struct Pieces {
         u = cta * per_cta < units ? cta * per_cta : units;
         end = units - u < per_cta ? units : u + per_cta;
     }
+    __device__ __forceinline__ void fetch()
+    {
+        qt++;
+        f0 = table[3 * qt];
+        f1 = table[3 * qt + 1];
+        f2 = table[3 * qt + 2];
+    }
     __device__ __forceinline__ bool next(Piece& p)
     {
-        if (u >= end) return false;
-        int rel = u - f2.x;
-        if (!kAhead && rel == f1.w * kv_heads) {
-            qt++;
-            f0 = table[3 * qt];
-            f1 = table[3 * qt + 1];
-            f2 = table[3 * qt + 2];
-            rel = 0;
+        while (u < end) {
+            int rel = u - f2.x;
+            if (!kAhead && rel == (kItemUnits + f1.w) * kv_heads) {
+                fetch();
+                rel = 0;
+            }
+            const int tiles = f1.w, item = kItemUnits + tiles;
+            p.hk = rel / item;
+            const int r0 = rel - p.hk * item, r1 = min(end - u, item - r0) + r0;   // the CTA's units of the item
+            const int k0 = max(snap_unit(r0, item) - kItemUnits, 0);
+            p.n = max(snap_unit(r1, item) - kItemUnits, 0) - k0;
+            p.tok0 = f0.x;
+            p.n_tok = f0.y;
+            p.req = f0.z;
+            p.pos0 = f0.w;
+            p.kv_end = f1.x;
+            p.kv_row = f1.y;
+            p.tile0 = f1.z + k0;
+            p.two = f0.y > row_tokens;
+            p.cta0 = 0;
+            p.parts = 1;
+            if (p.n < tiles) {                           // shared with other CTAs
+                const int i0 = u - r0;                   // the item's first unit
+                int c0 = i0 / per_cta, c1 = (i0 + item - 1) / per_cta;
+                if (snap_unit((c0 + 1) * per_cta - i0, item) == 0) c0++;
+                if (c1 > c0 && snap_unit(c1 * per_cta - i0, item) == item) c1--;
+                p.cta0 = c0;
+                p.parts = c1 - c0 + 1;
+            }
+            u += r1 - r0;
+            if (kAhead && rel + (r1 - r0) == item * kv_heads && u < end) fetch();
+            if (p.n > 0) return true;
         }
-        const int tiles = f1.w;
-        p.tok0 = f0.x;
-        p.n_tok = f0.y;
-        p.req = f0.z;
-        p.pos0 = f0.w;
-        p.kv_end = f1.x;
-        p.kv_row = f1.y;
-        p.hk = rel / tiles;
-        const int k0 = rel - p.hk * tiles;
-        p.n = min(end - u, tiles - k0);
-        p.tile0 = f1.z + k0;
-        p.two = f0.y > row_tokens;
-        p.cta0 = 0;
-        p.parts = 1;
-        if (p.n < tiles) {                           // shared with other CTAs
-            const int i0 = u - k0;
-            p.cta0 = i0 / per_cta;
-            p.parts = (i0 + tiles - 1) / per_cta - p.cta0 + 1;
-        }
-        u += p.n;
-        if (kAhead && rel + p.n == tiles * kv_heads && u < end) {
-            qt++;
-            f0 = table[3 * qt];
-            f1 = table[3 * qt + 1];
-            f2 = table[3 * qt + 2];
-        }
-        return true;
+        return false;
     }
 };
 
@@ -903,32 +909,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                             ex2(__ldcg(part_of(i) + kAttnSlotRows * kDP + row0 + lane) - ms);
                 if (a.lse) a.lse[tok * a.heads + head] = lall == 0.0f ? -INFINITY : (mall + log2f(lall)) * 0.6931471805599453f;
             }
-            // 4 columns of a row per lane
+            // 4 columns of a row per lane, kJoin of them at a time
             const int vecs = rows * (a.head_dim / 4);
-            for (int b = 0; b < vecs; b += 32) {
-                const int x = min(b + lane, vecs - 1);
-                const int v = x / rows, r = x - v * rows;
-                const float mr = __shfl_sync(0xffffffffu, mall, r), lr = __shfl_sync(0xffffffffu, lall, r);
-                const int64_t tr = __shfl_sync(0xffffffffu, tok, r);
-                const int hr = __shfl_sync(0xffffffffu, head, r);
-                const float ms = mr == -INFINITY ? 0.0f : mr;
-                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+            const float inv = lall == 0.0f ? 0.0f : 1.0f / lall;
+            for (int b = 0; b < vecs; b += 32 * kJoin) {
+                float4 acc[kJoin];
+                int at[kJoin];
+                float ms[kJoin];
+#pragma unroll
+                for (int y = 0; y < kJoin; y++) {
+                    const int x = min(b + 32 * y + lane, vecs - 1), v = x / rows, r = x - v * rows;
+                    const float mr = __shfl_sync(0xffffffffu, mall, r);
+                    ms[y] = mr == -INFINITY ? 0.0f : mr;
+                    at[y] = v * kAttnSlotRows + row0 + r;
+                    acc[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+#pragma unroll 2
                 for (int i = 0; i < p.parts; i++) {
                     const float* part = part_of(i);
-                    const float f = ex2(__ldcg(part + kAttnSlotRows * kDP + row0 + r) - ms);
-                    const float4 o = __ldcg(reinterpret_cast<const float4*>(part) + v * kAttnSlotRows + row0 + r);
-                    acc.x += f * o.x;
-                    acc.y += f * o.y;
-                    acc.z += f * o.z;
-                    acc.w += f * o.w;
+#pragma unroll
+                    for (int y = 0; y < kJoin; y++) {
+                        const float f =
+                            ex2(__ldcg(part + kAttnSlotRows * kDP + (at[y] & (kAttnSlotRows - 1))) - ms[y]);
+                        const float4 o = __ldcg(reinterpret_cast<const float4*>(part) + at[y]);
+                        acc[y].x += f * o.x;
+                        acc[y].y += f * o.y;
+                        acc[y].z += f * o.z;
+                        acc[y].w += f * o.w;
+                    }
                 }
-                const float inv = lr == 0.0f ? 0.0f : 1.0f / lr;
-                const bool zero = lr == 0.0f;
-                uint2 v2;
-                v2.x = cvt_bf16x2(zero ? 0.0f : acc.x * inv, zero ? 0.0f : acc.y * inv);
-                v2.y = cvt_bf16x2(zero ? 0.0f : acc.z * inv, zero ? 0.0f : acc.w * inv);
-                if (b + lane < vecs) *reinterpret_cast<uint2*>(a.out + tr * a.ldo + hr * a.ho + 4 * v) = v2;
+#pragma unroll
+                for (int y = 0; y < kJoin; y++) {
+                    const int r = (at[y] & (kAttnSlotRows - 1)) - row0, v = at[y] / kAttnSlotRows;
+                    const float f = __shfl_sync(0xffffffffu, inv, r);
+                    const int64_t tr = __shfl_sync(0xffffffffu, tok, r);
+                    const int hr = __shfl_sync(0xffffffffu, head, r);
+                    uint2 v2 = make_uint2(0u, 0u);
+                    if (f != 0.0f) {
+                        v2.x = cvt_bf16x2(acc[y].x * f, acc[y].y * f);
+                        v2.y = cvt_bf16x2(acc[y].z * f, acc[y].w * f);
+                    }
+                    if (b + 32 * y + lane < vecs) *reinterpret_cast<uint2*>(a.out + tr * a.ldo + hr * a.ho + 4 * v) = v2;
+                }
             }
         }
     }

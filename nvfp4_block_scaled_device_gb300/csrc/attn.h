@@ -23,20 +23,23 @@ constexpr int kStatusSlot = NVFP4_ERR_INVALID_ARG * 100 + 32;
 // A row tile is 128 rows of the attention's MMAs: the `group` query heads of
 // one kv head for kAttnRows / group consecutive tokens (row = token * group +
 // head).  A work item is a QTile for one kv head: up to two row tiles of one
-// request, over the 128-key tiles that any of its rows sees.  The items'
-// key tiles, all kv heads of a QTile one after the other, form one axis of
-// `units`; CTA c takes units [c * per_cta, (c + 1) * per_cta), so that every
-// CTA has the same number of key tiles whatever the lengths.
+// request, over the 128-key tiles that any of its rows sees.  The items, all
+// kv heads of a QTile one after the other, form one axis of `units`: for each
+// item kItemUnits for its start and end, then one per key tile.  CTA c takes
+// the key tiles among units [c * per_cta, (c + 1) * per_cta), so that every
+// CTA has about the same work whatever the lengths.  A boundary that would
+// leave a CTA one tile of an item moves to the item's edge (snap_unit).
 constexpr int kAttnRows = 128;
 constexpr int kAttnKeys = 128;
 constexpr int kAttnMaxCtas = 256;
+constexpr int kItemUnits = 2;
 
 struct QTile {
     int32_t tok0, n_tok;     // packed rows (tokens) tok0 .. tok0 + n_tok - 1
     int32_t req, pos0;       // the request, the position of token tok0
     int32_t kv_end, kv_row;  // no row sees keys from kv_end on; packed row of the request's key 0
     int32_t tile0, tiles;    // key tiles tile0 .. tile0 + tiles - 1
-    int32_t unit0, pad[3];   // units before this QTile; it has tiles * kv_heads
+    int32_t unit0, pad[3];   // units before this QTile; it has (kItemUnits + tiles) * kv_heads
 };
 static_assert(sizeof(QTile) == 48, "QTile");
 
@@ -50,6 +53,12 @@ static_assert(sizeof(ScheduleHead) % 16 == 0, "QTiles follow the head, 16-byte a
 inline __host__ __device__ const QTile* schedule_tiles(const ScheduleHead* h)
 {
     return reinterpret_cast<const QTile*>(h + 1);
+}
+
+// Boundary r (units from the item's start) of an item of `item` units.
+inline __host__ __device__ int snap_unit(int r, int item)
+{
+    return item - r <= 1 ? item : r <= kItemUnits + 1 ? 0 : r;
 }
 
 // Tokens of a row tile.

@@ -18,7 +18,7 @@ namespace {
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int64_t kMaxUnits = (int64_t)1 << 30;   // of a schedule (a call of seconds): the rest is not worked on
-constexpr int kMinUnits = 4;   // key tiles of a shared item's parts, at least: smaller ones cost more to join than they save
+constexpr int kMinTiles = 4;   // key tiles of a shared item's parts, at least: smaller ones cost more to join than they save
 
 struct PlanParams {
     nvfp4_step_t s;
@@ -95,7 +95,7 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, int32_t* 
     }
     if (t == 0) {
         tile0[R] = (int32_t)total;
-        warp_sums[kPlanWarps] = 1;                  // tiles of the longest QTile
+        warp_sums[kPlanWarps] = 1;                  // units of the longest item
     }
     __syncthreads();
     const int n = (int)total;
@@ -125,8 +125,8 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, int32_t* 
             q.tile0 = (int32_t)(begin / kAttnKeys);
             // at least one tile, so that rows that see no key are written too
             q.tiles = (int32_t)max((end + kAttnKeys - 1) / kAttnKeys - q.tile0, (int64_t)1);
-            u = (int64_t)q.tiles * s.kv_heads;
-            atomicMax(reinterpret_cast<unsigned long long*>(warp_sums + kPlanWarps), (unsigned long long)q.tiles);
+            u = (int64_t)(kItemUnits + q.tiles) * s.kv_heads;
+            atomicMax(reinterpret_cast<unsigned long long*>(warp_sums + kPlanWarps), (unsigned long long)(kItemUnits + q.tiles));
         }
         int64_t sum = 0;
         const int64_t incl = block_incl_sum(u, warp_sums, &sum);
@@ -142,7 +142,7 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, int32_t* 
     }
     __syncthreads();
     const int64_t share = (units + p.ctas - 1) / p.ctas;
-    const int64_t least = min((int64_t)kMinUnits, warp_sums[kPlanWarps]);
+    const int64_t least = min((int64_t)(kItemUnits + kMinTiles), warp_sums[kPlanWarps]);
     const int64_t per_cta = share > least ? share : least;
     if (t == 0) {
         head->units = (int32_t)units;
@@ -151,7 +151,7 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, int32_t* 
     }
     for (int i = t; i < n; i += kPlanThreads) {     // each thread reads the entries it wrote
         const QTile q = tiles[i];
-        const int64_t u1 = min(q.unit0 + (int64_t)q.tiles * s.kv_heads, units);
+        const int64_t u1 = min(q.unit0 + (int64_t)(kItemUnits + q.tiles) * s.kv_heads, units);
         for (int64_t c = (q.unit0 + per_cta - 1) / per_cta; c * per_cta < u1; c++) {
             head->first[c] = i;
             head->start[c] = q;
