@@ -212,6 +212,32 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v)
 #pragma unroll
     for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
 }
+// 32 columns of 16 rows in the layout of the warp-level MMAs' accumulators:
+// v[4i + 2b + x] is row lane / 4 + 8b, column 8i + 2 (lane % 4) + x.
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float* v)
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
+}
+// 4 x 4 transpose among four lanes: lane q's a[m] becomes lane m's a[q].
+__device__ __forceinline__ void quad_transpose(uint32_t* a, int q)
+{
+    const bool b0 = q & 1, b1 = q & 2;
+    uint32_t x = __shfl_xor_sync(0xffffffffu, b0 ? a[0] : a[1], 1);
+    uint32_t y = __shfl_xor_sync(0xffffffffu, b0 ? a[2] : a[3], 1);
+    (b0 ? a[0] : a[1]) = x;
+    (b0 ? a[2] : a[3]) = y;
+    x = __shfl_xor_sync(0xffffffffu, b1 ? a[0] : a[2], 2);
+    y = __shfl_xor_sync(0xffffffffu, b1 ? a[1] : a[3], 2);
+    (b1 ? a[0] : a[2]) = x;
+    (b1 ? a[1] : a[3]) = y;
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r)
 {
     asm volatile(
@@ -308,6 +334,7 @@ __device__ __forceinline__ void load_half(float* s, uint32_t taddr)
     tmem_ld32(taddr + 32, s + 32);
     tmem_ld_wait();
 }
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 __device__ __forceinline__ void finish_half(float* s, bool negate, bool masked, int h, int lw)
 {
     if (negate) {
@@ -316,7 +343,12 @@ __device__ __forceinline__ void finish_half(float* s, bool negate, bool masked, 
     }
     if (masked) {
 #pragma unroll
-        for (int k = 0; k < 64; k++) s[k] = k < h && k >= lw ? s[k] : -INFINITY;
+        for (int x = 0; x < 64; x += 32) {
+            const uint32_t seen = low_bits(h - x) & ~low_bits(lw - x);
+            if (__all_sync(0xffffffffu, seen == ~0u)) continue;
+#pragma unroll
+            for (int k = 0; k < 32; k++) s[x + k] = (seen >> k) & 1u ? s[x + k] : -INFINITY;
+        }
     }
 }
 
@@ -536,7 +568,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                             smem_u32(kv && valid < kAttnKeys ? &ctrl->v_end[s] : &ctrl->kv_full[s]);
                         const uint32_t bytes =
                             paged ? (uint32_t)(pages * a.page_size * kDP * 2) : (uint32_t)C::kTileBytes;
-                        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(bar, bytes);
+                            if (!p.two) mbar_arrive(smem_u32(&ctrl->kv_empty[s]));   // only one MMA warp will use it
+                        }
                         __syncwarp();
                         if (paged) {
                             // box b: half b / ppt of page b % ppt (at most 16)
@@ -651,7 +686,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     issue_qk<kDP>(ts, qt, ring_k + ks * (C::kTileBytes >> 4), k_hi, kIdescS);
                     mma_commit_warp(s_full);
                     mma_commit_warp(empty0 + 8u * ks);
-                    if (!p.two) mma_commit_warp(empty0 + 8u * ks);
                     if (i + by >= p.n) mma_commit_warp(q_empty);
                     const bool wrap = ks + 1 == kStages;
                     const uint32_t vs = wrap ? 0 : ks + 1, vph = wrap ? kph ^ 1u : kph;
@@ -680,7 +714,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     issue_pv<1>(to, ts + kColP, v_lo, v_hi, kIdescO, 1u);
                     mma_commit_warp(o_full);
                     mma_commit_warp(empty0 + 8u * vs);
-                    if (!p.two) mma_commit_warp(empty0 + 8u * vs);
                     ks += 2 * by;
                     if (ks >= kStages) {
                         ks -= kStages;
@@ -831,10 +864,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             const bool none = l == 0.0f;                         // the row sees no key
             const int head = p.hk * a.group + g;
             const int64_t tok = p.tok0 + t;
-            if (any) {
-                const float inv = whole ? (none ? 0.0f : 1.0f / l) : 1.0f;
-                const int slot = 2 * cta + (p.cta0 == cta ? 1 : 0);
-                float* part = a.partials + slot * kAttnSlotFloats;
+            if (any && whole) {
+                // rows in the accumulator layout, four lanes to a row: 64
+                // contiguous bytes of 8 rows a store (a row a lane would be
+                // 16 bytes of 32 rows, four times the accesses)
+                const float inv = none ? 0.0f : 1.0f / l;
+                const uint32_t valid = __ballot_sync(0xffffffffu, mine);
+                const int64_t at = tok * a.ldo + head * a.ho;
+#pragma unroll 1
+                for (int h = 0; h < 2; h++) {                    // rows 16h .. 16h + 15 of the warp
+                    float fa[2], fb[2];
+                    __nv_bfloat16* out[2];
+                    bool live[2];
+#pragma unroll
+                    for (int b = 0; b < 2; b++) {
+                        const int r = 16 * h + 8 * b + (lane >> 2);
+                        fa[b] = __shfl_sync(0xffffffffu, f0 * inv, r);
+                        fb[b] = __shfl_sync(0xffffffffu, f1 * inv, r);
+                        out[b] = a.out + __shfl_sync(0xffffffffu, at, r) + 8 * (lane & 3);
+                        live[b] = (valid >> r) & 1u;
+                    }
+                    if ((valid >> (16 * h)) == 0) break;         // (the rows of an item are its first)
+#pragma unroll 1
+                    for (int k = 0; k < kDP; k += 64) {          // 64 columns at a time
+                        float o[32];
+                        const uint32_t at_h = ((uint32_t)(16 * h) << 16) + k;
+                        tmem_ld_rows(to + at_h, o);
+                        tmem_ld_rows(to + at_h + 32, o + 16);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int x = 0; x < 32; x++) o[x] = fa[(x >> 1) & 1] == 0.0f ? 0.0f : o[x] * fa[(x >> 1) & 1];
+                        if (merge) {
+                            float o1[32];
+                            tmem_ld_rows(to + 128 + at_h, o1);
+                            tmem_ld_rows(to + 128 + at_h + 32, o1 + 16);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int x = 0; x < 32; x++)
+                                o[x] += fb[(x >> 1) & 1] == 0.0f ? 0.0f : o1[x] * fb[(x >> 1) & 1];
+                        }
+#pragma unroll
+                        for (int y = 0; y < 2; y++) {
+#pragma unroll
+                            for (int b = 0; b < 2; b++) {
+                                uint32_t x[4];
+#pragma unroll
+                                for (int i = 0; i < 4; i++)
+                                    x[i] = cvt_bf16x2(o[16 * y + 4 * i + 2 * b], o[16 * y + 4 * i + 2 * b + 1]);
+                                quad_transpose(x, lane & 3);
+                                const int col = k + 32 * y;
+                                if (live[b] && col + 8 * (lane & 3) < a.head_dim)
+                                    *reinterpret_cast<uint4*>(out[b] + col) = make_uint4(x[0], x[1], x[2], x[3]);
+                            }
+                        }
+                    }
+                }
+                if (mine && a.lse)
+                    a.lse[tok * a.heads + head] = none ? -INFINITY : (m2 + log2f(l)) * 0.6931471805599453f;
+            } else if (any) {
+                float* part = a.partials + (2 * cta + (p.cta0 == cta ? 1 : 0)) * kAttnSlotFloats;
                 const int srow = (p.two ? j * kAttnRows : 0) + row;
 #pragma unroll 1
                 for (int k = 0; k < kDP / 32; k++) {
@@ -843,33 +931,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     tmem_ld_wait();
                     if (merge) {
                         float o1[32];
-                        tmem_ld32(lane_addr + kColO + 128 + 32 * k, o1);
+                        tmem_ld32(to + 128 + 32 * k, o1);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int y = 0; y < 32; y++) o[y] = o[y] * f0 + o1[y] * f1;
+                        for (int y = 0; y < 32; y++) o[y] = (f0 == 0.0f ? 0.0f : o[y] * f0) + (f1 == 0.0f ? 0.0f : o1[y] * f1);
                     }
                     if (!mine) continue;
-                    if (whole) {
-                        __nv_bfloat16* out = a.out + tok * a.ldo + head * a.ho + 32 * k;
 #pragma unroll
-                        for (int y = 0; y < 4; y++) {
-                            uint4 v;
-                            v.x = cvt_bf16x2(none ? 0.0f : o[8 * y] * inv, none ? 0.0f : o[8 * y + 1] * inv);
-                            v.y = cvt_bf16x2(none ? 0.0f : o[8 * y + 2] * inv, none ? 0.0f : o[8 * y + 3] * inv);
-                            v.z = cvt_bf16x2(none ? 0.0f : o[8 * y + 4] * inv, none ? 0.0f : o[8 * y + 5] * inv);
-                            v.w = cvt_bf16x2(none ? 0.0f : o[8 * y + 6] * inv, none ? 0.0f : o[8 * y + 7] * inv);
-                            if (32 * k + 8 * y < a.head_dim) *reinterpret_cast<uint4*>(out + 8 * y) = v;
-                        }
-                    } else {
-#pragma unroll
-                        for (int y = 0; y < 8; y++)
-                            __stcg(reinterpret_cast<float4*>(part) + (8 * k + y) * kAttnSlotRows + srow,
-                                   make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]));
-                    }
+                    for (int y = 0; y < 8; y++)
+                        __stcg(reinterpret_cast<float4*>(part) + (8 * k + y) * kAttnSlotRows + srow,
+                               make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]));
                 }
-                if (mine && whole && a.lse)
-                    a.lse[tok * a.heads + head] = none ? -INFINITY : (m2 + log2f(l)) * 0.6931471805599453f;
-                if (mine && !whole) {
+                if (mine) {
                     __stcg(part + kAttnSlotRows * kDP + srow, m2);
                     __stcg(part + kAttnSlotRows * (kDP + 1) + srow, l);
                 }
@@ -884,72 +957,74 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             if (whole || !any) continue;
 
             // ---- a shared item: the last of its CTAs adds the parts up, per warp
-            __threadfence();
             __syncwarp();
             int* ticket = a.tickets + (p.cta0 * 2 + (p.two ? j : 0)) * 4 + w;
             int last = 0;
-            if (lane == 0) last = atom_add_acq_rel(ticket, 1) == p.parts - 1;
+            if (lane == 0) last = atom_add_acq_rel(ticket, 1) == p.parts - 1;   // (after the warp's stores: cumulative)
             last = __shfl_sync(0xffffffffu, last, 0);
             if (!last) continue;
-            __threadfence();
             if (lane == 0) *ticket = 0;
             const int row0 = (p.two ? j * kAttnRows : 0) + w * 32;   // the warp's first row in a slot
             const int rows = __popc(__ballot_sync(0xffffffffu, mine));
-            auto part_of = [&](int i) {
-                const int cc = p.cta0 + i;
-                return a.partials + (int64_t)(2 * cc + (i == 0 ? 1 : 0)) * kAttnSlotFloats;
-            };
+            // part i of the item is in slot 2 (cta0 + i), the first in 2 cta0 + 1
+            const float* const part0 = a.partials + (2 * p.cta0 + 1) * kAttnSlotFloats;
+            auto part_of = [&](int i) { return part0 + (i == 0 ? 0 : 2 * i - 1) * kAttnSlotFloats; };
+            const int my = row0 + min(lane, rows - 1);
             float mall = -INFINITY, lall = 0.0f;
-            if (mine) {
-                for (int i = 0; i < p.parts; i++)
-                    mall = fmaxf(mall, __ldcg(part_of(i) + kAttnSlotRows * kDP + row0 + lane));
-                const float ms = mall == -INFINITY ? 0.0f : mall;
-                for (int i = 0; i < p.parts; i++)
-                    lall += __ldcg(part_of(i) + kAttnSlotRows * (kDP + 1) + row0 + lane) *
-                            ex2(__ldcg(part_of(i) + kAttnSlotRows * kDP + row0 + lane) - ms);
-                if (a.lse) a.lse[tok * a.heads + head] = lall == 0.0f ? -INFINITY : (mall + log2f(lall)) * 0.6931471805599453f;
+#pragma unroll 4
+            for (int i = 0; i < p.parts; i++) mall = fmaxf(mall, __ldcg(part_of(i) + kAttnSlotRows * kDP + my));
+            const float ms = mall == -INFINITY ? 0.0f : mall;
+#pragma unroll 4
+            for (int i = 0; i < p.parts; i++) {
+                const float* part = part_of(i) + kAttnSlotRows * kDP + my;
+                lall += __ldcg(part + kAttnSlotRows) * ex2(__ldcg(part) - ms);
             }
-            // 4 columns of a row per lane, kJoin of them at a time
-            const int vecs = rows * (a.head_dim / 4);
+            if (mine && a.lse)
+                a.lse[tok * a.heads + head] = lall == 0.0f ? -INFINITY : (mall + log2f(lall)) * 0.6931471805599453f;
             const float inv = lall == 0.0f ? 0.0f : 1.0f / lall;
-            for (int b = 0; b < vecs; b += 32 * kJoin) {
+            const int64_t at = tok * a.ldo + head * a.ho;
+            // lane l takes the 4-column vectors l, l + 32, ... of the rows'
+            // vectors (row fastest), kJoin of them at a time
+            const int vecs = rows * (a.head_dim / 4);
+            const int dv = 32 / rows, dr = 32 - dv * rows;
+            int v = lane / rows, r = lane - v * rows;
+            for (int b = lane; b - lane < vecs; b += 32 * kJoin) {
                 float4 acc[kJoin];
-                int at[kJoin];
-                float ms[kJoin];
+                int vv[kJoin], rr[kJoin];
 #pragma unroll
                 for (int y = 0; y < kJoin; y++) {
-                    const int x = min(b + 32 * y + lane, vecs - 1), v = x / rows, r = x - v * rows;
-                    const float mr = __shfl_sync(0xffffffffu, mall, r);
-                    ms[y] = mr == -INFINITY ? 0.0f : mr;
-                    at[y] = v * kAttnSlotRows + row0 + r;
+                    const bool in = b + 32 * y < vecs;
+                    vv[y] = in ? v : 0;
+                    rr[y] = in ? r : 0;
+                    v += dv;
+                    r += dr;
+                    if (r >= rows) {
+                        r -= rows;
+                        v++;
+                    }
                     acc[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 }
 #pragma unroll 2
                 for (int i = 0; i < p.parts; i++) {
                     const float* part = part_of(i);
+                    const float f = ex2(__ldcg(part + kAttnSlotRows * kDP + my) - ms) * inv;
 #pragma unroll
                     for (int y = 0; y < kJoin; y++) {
-                        const float f =
-                            ex2(__ldcg(part + kAttnSlotRows * kDP + (at[y] & (kAttnSlotRows - 1))) - ms[y]);
-                        const float4 o = __ldcg(reinterpret_cast<const float4*>(part) + at[y]);
-                        acc[y].x += f * o.x;
-                        acc[y].y += f * o.y;
-                        acc[y].z += f * o.z;
-                        acc[y].w += f * o.w;
+                        const float4 o = __ldcg(reinterpret_cast<const float4*>(part) + vv[y] * kAttnSlotRows + row0 + rr[y]);
+                        const float fy = __shfl_sync(0xffffffffu, f, rr[y]);
+                        acc[y].x += fy * o.x;
+                        acc[y].y += fy * o.y;
+                        acc[y].z += fy * o.z;
+                        acc[y].w += fy * o.w;
                     }
                 }
 #pragma unroll
                 for (int y = 0; y < kJoin; y++) {
-                    const int r = (at[y] & (kAttnSlotRows - 1)) - row0, v = at[y] / kAttnSlotRows;
-                    const float f = __shfl_sync(0xffffffffu, inv, r);
-                    const int64_t tr = __shfl_sync(0xffffffffu, tok, r);
-                    const int hr = __shfl_sync(0xffffffffu, head, r);
-                    uint2 v2 = make_uint2(0u, 0u);
-                    if (f != 0.0f) {
-                        v2.x = cvt_bf16x2(acc[y].x * f, acc[y].y * f);
-                        v2.y = cvt_bf16x2(acc[y].z * f, acc[y].w * f);
-                    }
-                    if (b + 32 * y + lane < vecs) *reinterpret_cast<uint2*>(a.out + tr * a.ldo + hr * a.ho + 4 * v) = v2;
+                    const int64_t ar = __shfl_sync(0xffffffffu, at, rr[y]);
+                    const bool none_r = __shfl_sync(0xffffffffu, inv, rr[y]) == 0.0f;
+                    const uint2 w2 = make_uint2(cvt_bf16x2(acc[y].x, acc[y].y), cvt_bf16x2(acc[y].z, acc[y].w));
+                    if (b + 32 * y < vecs)
+                        *reinterpret_cast<uint2*>(a.out + ar + 4 * vv[y]) = none_r ? make_uint2(0u, 0u) : w2;
                 }
             }
         }
