@@ -395,6 +395,19 @@ struct Piece {
     int tile0, n;        // key tiles tile0 .. tile0 + n - 1
     bool two;            // two row tiles
     int cta0, parts;     // first CTA of the item and how many share it
+
+    // Tiles lo .. hi - 1 of the piece that rows of row tile j see (one at
+    // least, so that rows that see no key are written too).
+    __device__ __forceinline__ void range(int j, int row_tokens, int window, int& lo, int& hi) const
+    {
+        lo = 0;
+        hi = n;
+        if (!two) return;
+        const int first = pos0 + j * row_tokens, last = pos0 + min(n_tok, (j + 1) * row_tokens) - 1;
+        const int lo_key = window ? max(first + 1 - window, 0) : 0, hi_key = min(last + 1, kv_end);
+        lo = min(max(lo_key / kAttnKeys - tile0, 0), n - 1);
+        hi = min(max((hi_key - 1) / kAttnKeys + 1 - tile0, lo + 1), n);
+    }
 };
 
 // The pieces of CTA `cta` in order; every warp of the CTA walks them alike.
@@ -547,6 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             bool ok = true;
             while (ok && pieces.next(p)) {
                 const int* table = paged ? a.block_table + (int64_t)p.req * a.table_ld : nullptr;
+                int lo[2], hi[2];
+                for (int j = 0; j < 2; j++) p.range(j, row_tile_tokens(a.group), a.window, lo[j], hi[j]);
                 for (int i = 0; i < p.n && ok; i++) {
                     const int key0 = (p.tile0 + i) * kAttnKeys;
                     const int valid = min(kAttnKeys, max(p.kv_end - key0, 0));
@@ -570,7 +585,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                             paged ? (uint32_t)(pages * a.page_size * kDP * 2) : (uint32_t)C::kTileBytes;
                         if (lane == 0) {
                             mbar_arrive_expect_tx(bar, bytes);
-                            if (!p.two) mbar_arrive(smem_u32(&ctrl->kv_empty[s]));   // only one MMA warp will use it
+                            // only one MMA warp will use it
+                            if (!p.two || i < lo[0] || i >= hi[0] || i < lo[1] || i >= hi[1])
+                                mbar_arrive(smem_u32(&ctrl->kv_empty[s]));
                         }
                         __syncwarp();
                         if (paged) {
@@ -669,14 +686,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             uint32_t qph = 0, pph = 0, oph = 1;    // phases: Q, P, O free (nothing to wait for at first)
             bool ok = true;
             while (ok && pieces.next(p)) {
-                const int first = p.two ? 0 : j, by = p.two ? 1 : 2;
+                int first, end;
+                p.range(j, row_tile_tokens(a.group), a.window, first, end);
+                const int by = p.two ? 1 : 2;
+                if (!p.two) first = j;
                 uint32_t kph;                      // stage of the warp's next K, its phase; V is in the stage after
                 uint32_t ks = stage_of<kStages>(use + 2 * first, &kph);
                 const uint32_t qt = q_lo + (p.two && j ? C::kTileBytes >> 4 : 0);
                 if (!wait_on(smem_u32(&ctrl->q_full), qph, abort_flag, status, 44)) break;
                 qph ^= 1u;
-                if (first >= p.n && lane == 0) mbar_arrive(q_empty);     // no tile for this warp
-                for (int i = first; i < p.n; i += by) {
+                if (first >= end && lane == 0) mbar_arrive(q_empty);     // no tile for this warp
+                for (int i = first; i < end; i += by) {
                     const uint32_t ku = use + 2u * (uint32_t)i;
                     if (!wait_use(&ctrl->issued, ku, full0 + 8u * ks, kph, abort_flag, status, 45)) {
                         ok = false;
@@ -686,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     issue_qk<kDP>(ts, qt, ring_k + ks * (C::kTileBytes >> 4), k_hi, kIdescS);
                     mma_commit_warp(s_full);
                     mma_commit_warp(empty0 + 8u * ks);
-                    if (i + by >= p.n) mma_commit_warp(q_empty);
+                    if (i + by >= end) mma_commit_warp(q_empty);
                     const bool wrap = ks + 1 == kStages;
                     const uint32_t vs = wrap ? 0 : ks + 1, vph = wrap ? kph ^ 1u : kph;
                     // the accumulator's previous item has been read
@@ -744,7 +764,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         uint32_t s_cnt = 0, ml_cnt = 0, t_cnt = 0;
         bool ok = true;
         while (ok && pieces.next(p)) {
-            const int N = p.two ? 2 * p.n : p.n;
+            int first, end, first_o, end_o;                      // tiles of this warpgroup, of the other
+            p.range(j, row_tokens, a.window, first, end);
+            p.range(1 - j, row_tokens, a.window, first_o, end_o);
+            const int by = p.two ? 1 : 2;
+            if (!p.two) first = j;
             const int t = (p.two && j ? row_tokens : 0) + tk;    // token of the item
             const bool mine = tk < row_tokens && t < p.n_tok;
             const bool any = __any_sync(0xffffffffu, mine);
@@ -752,15 +776,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             const int hi = mine ? min(pos + 1, p.kv_end) : 0;      // keys lo .. hi - 1
             const int lo = mine && a.window ? max(pos + 1 - a.window, 0) : 0;
             float m = -INFINITY, l = 0.0f;
-            if (j >= N) continue;            // the second warpgroup of a single key tile
-            for (int n = j; n < N; n += 2) {
-                const int i = p.two ? n >> 1 : n;
+            if (first >= end) continue;      // the second warpgroup of a single key tile
+            for (int i = first; i < end; i += by) {
                 if (!mbar_wait_warp(smem_u32(&ctrl->s_full[j]), s_cnt & 1u, abort_flag, status, 50)) {
                     ok = false;
                     break;
                 }
                 s_cnt++;
-                if (p.two) {
+                const bool both = p.two && i >= first_o && i < end_o;
+                if (both) {
                     // the two warpgroups' exponentials in turn (per pair of
                     // warps): together they would wait for the tensor pipe
                     // together, and leave it idle together
@@ -790,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     const bool up = mine && (mx > m + lazy || (m == -INFINITY && mx > m));
                     if (__any_sync(0xffffffffu, up)) {
                         const float m1 = up ? mx : m;
-                        if (n >= 2) {
+                        if (i > first) {
                             // rescale what has been summed with the old maximum
                             const float f = up ? ex2((m - m1) * c) : 1.0f;
                             l *= f;
@@ -821,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(smem_u32(&ctrl->p_half[j]));
-                        if (p.two) mbar_arrive(smem_u32(&ctrl->turn[1 - j][w]));
+                        if (both) mbar_arrive(smem_u32(&ctrl->turn[1 - j][w]));
                     }
                     sum = add2(sum, exp_half(s + 64, c, mc, tp + 32));
                     l += sum.x + sum.y;
@@ -829,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     tc_fence_before();
                 } else if (lane == 0) {
                     mbar_arrive(smem_u32(&ctrl->p_half[j]));
-                    if (p.two) mbar_arrive(smem_u32(&ctrl->turn[1 - j][w]));
+                    if (both) mbar_arrive(smem_u32(&ctrl->turn[1 - j][w]));
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ctrl->p_full[j]));

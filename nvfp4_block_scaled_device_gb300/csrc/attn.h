@@ -28,7 +28,8 @@ constexpr int kStatusSlot = NVFP4_ERR_INVALID_ARG * 100 + 32;
 // item kItemUnits for its start and end, then one per key tile.  CTA c takes
 // the key tiles among units [c * per_cta, (c + 1) * per_cta), so that every
 // CTA has about the same work whatever the lengths.  A boundary that would
-// leave a CTA one tile of an item moves to the item's edge (snap_unit).
+// leave fewer than kMinPart tiles of an item on one side moves to that edge of
+// the item (snap_unit).
 constexpr int kAttnRows = 128;
 constexpr int kAttnKeys = 128;
 constexpr int kAttnMaxCtas = 256;
@@ -55,10 +56,14 @@ inline __host__ __device__ const QTile* schedule_tiles(const ScheduleHead* h)
     return reinterpret_cast<const QTile*>(h + 1);
 }
 
-// Boundary r (units from the item's start) of an item of `item` units.
+// Boundary r (units from the item's start) of an item of `item` units.  A part
+// costs its CTA about 5 us beside its tiles (about 2 us each), so short items
+// are not shared.
+constexpr int kMinPart = 5;
 inline __host__ __device__ int snap_unit(int r, int item)
 {
-    return item - r <= 1 ? item : r <= kItemUnits + 1 ? 0 : r;
+    const bool head = r < kItemUnits + kMinPart, tail = item - r < kMinPart;
+    return r >= item ? item : head && tail ? (2 * r < item ? 0 : item) : head ? 0 : tail ? item : r;
 }
 
 // Tokens of a row tile.

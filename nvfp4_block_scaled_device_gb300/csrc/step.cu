@@ -18,7 +18,6 @@ namespace {
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int64_t kMaxUnits = (int64_t)1 << 30;   // of a schedule (a call of seconds): the rest is not worked on
-constexpr int kMinTiles = 4;   // key tiles of a shared item's parts, at least: smaller ones cost more to join than they save
 
 struct PlanParams {
     nvfp4_step_t s;
@@ -142,7 +141,7 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, int32_t* 
     }
     __syncthreads();
     const int64_t share = (units + p.ctas - 1) / p.ctas;
-    const int64_t least = min((int64_t)(kItemUnits + kMinTiles), warp_sums[kPlanWarps]);
+    const int64_t least = min((int64_t)(kItemUnits + kMinPart), warp_sums[kPlanWarps]);
     const int64_t per_cta = share > least ? share : least;
     if (t == 0) {
         head->units = (int32_t)units;
