@@ -37,8 +37,11 @@
 // pages' unused rows or nothing at all.  Their scores are masked, and warp 11
 // zeroes the V rows before the tile is multiplied, so that NaN or infinities
 // there cannot reach a sum as 0 * NaN.
-#include <string.h>
-
+//
+// The softmax is one small loop over 64 keys at a time: the warps of a CTA run
+// four different programs, and code that is run only now and then (masks, a
+// risen maximum, an item's end) is fetched from far when it is; unrolled
+// copies of it cost thousands of cycles an item.
 #include "attn.h"
 #include "common.cuh"
 #include "internal.h"
@@ -49,10 +52,9 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kWarpMma = 8, kWarpKV = 10, kWarpQ = 11;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 0, kColS = 256;      // + 128 * warpgroup
-constexpr uint32_t kColP = 64;                  // P within S's columns: over the scores of the last 64 keys
+constexpr uint32_t kColO = 0, kColS = 256;      // + 128 * warpgroup; P of 64 keys over the first 32 columns of their S
 constexpr float kLazy = 8.0f;                   // log2 of the growth that P may carry
-constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+constexpr int kRegsSoftmax = 192, kRegsOther = 120;
 static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "the block's registers at launch");
 
 constexpr int kMaxStages = 10;
@@ -61,7 +63,7 @@ constexpr int kJoin = 8;                        // vectors of a shared item's pa
 struct Ctrl {
     uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], v_end[kMaxStages];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];
+    uint64_t s_full[2], p_half[2], p_full[2], o_half[2], o_full[2], o_free[2];
     uint64_t ml_full[4];
     uint64_t turn[2][4];
     uint64_t teardown;
@@ -141,14 +143,12 @@ __device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q_lo, uint32_t k_l
         "}\n" ::"r"(s), "r"(q_lo), "r"(k_lo), "r"(hi), "r"(idesc)
         : "memory");
 }
-// O += P V for half of a key tile's keys: P in tensor memory (8 columns for
-// 16 keys), V as stored (N-major; 16 keys are 2 KB).
-template <int kHalf>
+// O += P V over 64 keys: P in tensor memory (8 columns for 16 keys), V as
+// stored (N-major; 16 keys are 2 KB).
 __device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint32_t v_lo, uint32_t hi, uint32_t idesc,
                                          uint32_t acc)
 {
-    if (kHalf == 0)
-        asm volatile(
+    asm volatile(
         "{\n .reg .pred e, p, pt;\n .reg .b32 r, x, y;\n .reg .b64 db;\n"
         " elect.sync r|e, 0xffffffff;\n setp.eq.b32 pt, 0, 0;\n setp.ne.b32 p, %5, 0;\n"
         " add.u32 x, %2, 0; mov.b64 db, {x, %3}; add.u32 y, %1, 0;\n"
@@ -158,20 +158,6 @@ __device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint32_t v_lo, 
         " add.u32 x, %2, 256; mov.b64 db, {x, %3}; add.u32 y, %1, 16;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
         " add.u32 x, %2, 384; mov.b64 db, {x, %3}; add.u32 y, %1, 24;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
-        "}\n" ::"r"(o), "r"(p), "r"(v_lo), "r"(hi), "r"(idesc), "r"(acc)
-        : "memory");
-    else
-        asm volatile(
-        "{\n .reg .pred e, p, pt;\n .reg .b32 r, x, y;\n .reg .b64 db;\n"
-        " elect.sync r|e, 0xffffffff;\n setp.eq.b32 pt, 0, 0;\n setp.ne.b32 p, %5, 0;\n"
-        " add.u32 x, %2, 512; mov.b64 db, {x, %3}; add.u32 y, %1, 32;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, p;\n"
-        " add.u32 x, %2, 640; mov.b64 db, {x, %3}; add.u32 y, %1, 40;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
-        " add.u32 x, %2, 768; mov.b64 db, {x, %3}; add.u32 y, %1, 48;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
-        " add.u32 x, %2, 896; mov.b64 db, {x, %3}; add.u32 y, %1, 56;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
         "}\n" ::"r"(o), "r"(p), "r"(v_lo), "r"(hi), "r"(idesc), "r"(acc)
         : "memory");
@@ -245,6 +231,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r)
             taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -326,64 +323,54 @@ __device__ __forceinline__ bool wait_use(const volatile uint32_t* issued, uint32
     return wait_on(bar, parity, abort_flag, status, site);
 }
 
-// Scores of 64 keys from tensor memory, and what is done to them: the sign of
-// a negative scale, -inf at keys outside lw .. h - 1.
-__device__ __forceinline__ void load_half(float* s, uint32_t taddr)
-{
-    tmem_ld32(taddr, s);
-    tmem_ld32(taddr + 32, s + 32);
-    tmem_ld_wait();
-}
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
-__device__ __forceinline__ void finish_half(float* s, bool negate, bool masked, int h, int lw)
+
+// What is done to a row's 128 scores in tensor memory before the softmax reads
+// them: the sign of a negative scale, -inf at keys outside lw .. h - 1.
+__device__ __forceinline__ void edit_scores(uint32_t taddr, bool negate, int h, int lw)
 {
-    if (negate) {
+#pragma unroll 1
+    for (int x = 0; x < 128; x += 32) {
+        const uint32_t seen = low_bits(h - x) & ~low_bits(lw - x);
+        if (!negate && __all_sync(0xffffffffu, seen == ~0u)) continue;
+        float s[32];
+        tmem_ld32(taddr + x, s);
+        tmem_ld_wait();
+        uint32_t r[32];
 #pragma unroll
-        for (int k = 0; k < 64; k++) s[k] = -s[k];
+        for (int k = 0; k < 32; k++)
+            r[k] = (seen >> k) & 1u ? __float_as_uint(s[k]) ^ (negate ? 0x80000000u : 0u) : 0xff800000u;
+        tmem_st32(taddr + x, r);
     }
-    if (masked) {
-#pragma unroll
-        for (int x = 0; x < 64; x += 32) {
-            const uint32_t seen = low_bits(h - x) & ~low_bits(lw - x);
-            if (__all_sync(0xffffffffu, seen == ~0u)) continue;
-#pragma unroll
-            for (int k = 0; k < 32; k++) s[x + k] = (seen >> k) & 1u ? s[x + k] : -INFINITY;
-        }
-    }
+    tmem_st_wait();
 }
 
-// P of 64 keys into tensor memory: e = 2^(c s + mc) as bf16 pairs; returns
-// the two partial sums of e.
-__device__ __forceinline__ float2 exp_half(const float* s, float c, float mc, uint32_t taddr)
+// P of 64 keys: e = 2^(c s + mc) as bf16 pairs; returns the sum of e.
+__device__ __forceinline__ float exp_scores(const float* s, float c, float mc, uint32_t* r)
 {
     float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
-        uint32_t r[16];
-#pragma unroll
-        for (int y = 0; y < 16; y++) {
-            const int x = 32 * k + 2 * y;
-            float2 e = fma2(make_float2(s[x], s[x + 1]), make_float2(c, c), make_float2(mc, mc));
-            e.x = ex2(e.x);
-            e.y = ex2(e.y);
-            sum[y & 1] = add2(sum[y & 1], e);
-            r[y] = cvt_bf16x2(e.x, e.y);
-        }
-        tmem_st16(taddr + 16 * k, r);
+    for (int y = 0; y < 32; y++) {
+        float2 e = fma2(make_float2(s[2 * y], s[2 * y + 1]), make_float2(c, c), make_float2(mc, mc));
+        e.x = ex2(e.x);
+        e.y = ex2(e.y);
+        sum[y & 1] = add2(sum[y & 1], e);
+        r[y] = cvt_bf16x2(e.x, e.y);
     }
-    return add2(sum[0], sum[1]);
+    sum[0] = add2(sum[0], sum[1]);
+    return sum[0].x + sum[0].y;
 }
 
-__device__ __forceinline__ float max128(const float* s)
+__device__ __forceinline__ float max_scores(const float* s)
 {
     float x[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-    for (int k = 4; k < 124; k += 8) {
+    for (int k = 4; k < 60; k += 8) {
 #pragma unroll
         for (int y = 0; y < 4; y++) x[y] = max3(x[y], s[k + 2 * y], s[k + 2 * y + 1]);
     }
 #pragma unroll
-    for (int y = 0; y < 4; y++) x[y] = fmaxf(x[y], s[124 + y]);
+    for (int y = 0; y < 4; y++) x[y] = fmaxf(x[y], s[60 + y]);
     return fmaxf(max3(x[0], x[1], x[2]), x[3]);
 }
 
@@ -518,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             mbar_init(smem_u32(&ctrl->s_full[j]), 1);
             mbar_init(smem_u32(&ctrl->p_half[j]), 4);
             mbar_init(smem_u32(&ctrl->p_full[j]), 4);
+            mbar_init(smem_u32(&ctrl->o_half[j]), 1);
             mbar_init(smem_u32(&ctrl->o_full[j]), 1);
             mbar_init(smem_u32(&ctrl->o_free[j]), 4);
         }
@@ -681,6 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             const uint32_t ts = tmem + kColS + 128u * j, to = tmem + kColO + 128u * j;
             const uint32_t s_full = smem_u32(&ctrl->s_full[j]), o_full = smem_u32(&ctrl->o_full[j]);
             const uint32_t p_half = smem_u32(&ctrl->p_half[j]), p_full = smem_u32(&ctrl->p_full[j]);
+            const uint32_t o_half = smem_u32(&ctrl->o_half[j]);
             const uint32_t q_empty = smem_u32(&ctrl->q_empty);
             uint32_t use = 0;                      // stages used by the items before
             uint32_t qph = 0, pph = 0, oph = 1;    // phases: Q, P, O free (nothing to wait for at first)
@@ -724,14 +713,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                         break;
                     }
                     tc_fence_after();
-                    issue_pv<0>(to, ts + kColP, v_lo, v_hi, kIdescO, i != first);
+                    issue_pv(to, ts, v_lo, v_hi, kIdescO, i != first);
+                    mma_commit_warp(o_half);
                     if (!wait_on(p_full, pph, abort_flag, status, 49)) {
                         ok = false;
                         break;
                     }
                     pph ^= 1u;
                     tc_fence_after();
-                    issue_pv<1>(to, ts + kColP, v_lo, v_hi, kIdescO, 1u);
+                    issue_pv(to, ts + 64, v_lo + (64 * 128 >> 4), v_hi, kIdescO, 1u);
                     mma_commit_warp(o_full);
                     mma_commit_warp(empty0 + 8u * vs);
                     ks += 2 * by;
@@ -756,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         const int row_tokens = row_tile_tokens(a.group);
         const int tk = row / a.group, g = row - tk * a.group;    // this thread's token and head in a row tile
         const uint32_t lane_addr = tmem + ((uint32_t)(w * 32) << 16);
-        const uint32_t ts = lane_addr + kColS + 128 * j, tp = ts + kColP, to = lane_addr + kColO + 128 * j;
+        const uint32_t ts = lane_addr + kColS + 128 * j, to = lane_addr + kColO + 128 * j;
         const bool negate = a.scale < 0.0f;
         // a zero scale: any tiny factor gives equal probabilities, without 0 * inf at masked keys
         const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
@@ -797,66 +787,67 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 }
                 if (any) {
                     tc_fence_after();
-                    float s[128];
-                    load_half(s, ts);
-                    load_half(s + 64, ts + 64);
                     const int key0 = (p.tile0 + i) * kAttnKeys;
-                    const int h = hi - key0, lw = lo - key0;
-                    const bool masked = __any_sync(0xffffffffu, mine && (h < kAttnKeys || lw > 0));
-                    finish_half(s, negate, masked, h, lw);
-                    finish_half(s + 64, negate, masked, h - 64, lw - 64);
-                    // P of the first 64 keys with the m in use, the tile's
-                    // maximum beside it; where the maximum has outgrown m
-                    // (and at an item's first tile) that is done again
-                    float mc = m == -INFINITY ? 0.0f : -m * c;
-                    const float mx = max128(s);
-                    float2 sum = exp_half(s, c, mc, tp);
-                    const bool up = mine && (mx > m + lazy || (m == -INFINITY && mx > m));
-                    if (__any_sync(0xffffffffu, up)) {
-                        const float m1 = up ? mx : m;
-                        if (i > first) {
-                            // rescale what has been summed with the old maximum
-                            const float f = up ? ex2((m - m1) * c) : 1.0f;
-                            l *= f;
-                            if (!mbar_wait_warp(smem_u32(&ctrl->o_full[j]), (s_cnt - 2) & 1u, abort_flag, status, 51)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
+                    if (negate || __any_sync(0xffffffffu, mine && (hi < key0 + kAttnKeys || lo > key0)))
+                        edit_scores(ts, negate, hi - key0, lo - key0);
+                }
 #pragma unroll 1
-                            for (int k = 0; k < kDP / 16; k++) {
-                                float o[16];
-                                tmem_ld16(to + 16 * k, o);
-                                tmem_ld_wait();
-                                uint32_t q[16];
+                for (int half = 0; half < 2 && ok; half++) {     // 64 keys at a time
+                    if (any) {
+                        float s[64];
+                        uint32_t r[32];
+                        float mc, sum;
+                        for (;;) {
+                            tmem_ld32(ts + 64 * half, s);
+                            tmem_ld32(ts + 64 * half + 32, s + 32);
+                            tmem_ld_wait();
+                            // P with the m in use, their maximum beside it;
+                            // where that has outgrown m (and at an item's
+                            // first keys) m moves and P is formed again: S is
+                            // still there
+                            mc = m == -INFINITY ? 0.0f : -m * c;
+                            const float mx = max_scores(s);
+                            sum = exp_scores(s, c, mc, r);
+                            const bool up = mine && (mx > m + lazy || (m == -INFINITY && mx > m));
+                            if (!__any_sync(0xffffffffu, up)) break;
+                            const float m1 = up ? mx : m;
+                            if (i > first || half) {
+                                // rescale what has been summed with the old
+                                // maximum: the P V of the tiles before is
+                                // complete, as S is; that of the first half
+                                // has a signal
+                                const float f = up ? ex2((m - m1) * c) : 1.0f;
+                                l *= f;
+                                if (half && !mbar_wait_warp(smem_u32(&ctrl->o_half[j]), (s_cnt - 1) & 1u, abort_flag, status,
+                                                            51)) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int k = 0; k < kDP / 16; k++) {
+                                    float o[16];
+                                    tmem_ld16(to + 16 * k, o);
+                                    tmem_ld_wait();
+                                    uint32_t q[16];
 #pragma unroll
-                                for (int y = 0; y < 16; y++) q[y] = __float_as_uint(f == 0.0f ? 0.0f : o[y] * f);
-                                tmem_st16(to + 16 * k, q);
+                                    for (int y = 0; y < 16; y++) q[y] = __float_as_uint(f == 0.0f ? 0.0f : o[y] * f);
+                                    tmem_st16(to + 16 * k, q);
+                                }
                             }
+                            m = m1;
                         }
-                        m = m1;
-                        mc = m == -INFINITY ? 0.0f : -m * c;
-                        load_half(s, ts);        // P has not touched their columns
-                        finish_half(s, negate, masked, h, lw);
-                        sum = exp_half(s, c, mc, tp);
+                        tmem_st32(ts + 64 * half, r);
+                        l += sum;
+                        tmem_st_wait();
+                        tc_fence_before();
                     }
-                    tmem_st_wait();
-                    tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(smem_u32(&ctrl->p_half[j]));
-                        if (both) mbar_arrive(smem_u32(&ctrl->turn[1 - j][w]));
+                        mbar_arrive(smem_u32(half ? &ctrl->p_full[j] : &ctrl->p_half[j]));
+                        if (both && !half) mbar_arrive(smem_u32(&ctrl->turn[1 - j][w]));
                     }
-                    sum = add2(sum, exp_half(s + 64, c, mc, tp + 32));
-                    l += sum.x + sum.y;
-                    tmem_st_wait();
-                    tc_fence_before();
-                } else if (lane == 0) {
-                    mbar_arrive(smem_u32(&ctrl->p_half[j]));
-                    if (both) mbar_arrive(smem_u32(&ctrl->turn[1 - j][w]));
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctrl->p_full[j]));
             }
             if (!ok) break;
 
