@@ -53,19 +53,19 @@ constexpr int kThreads = 384;
 constexpr int kWarpMma = 8, kWarpKV = 10, kWarpQ = 11;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256;      // + 128 * warpgroup; P of 64 keys over the first 32 columns of their S
+constexpr int kStep = 64;                       // keys of a step
 constexpr float kLazy = 8.0f;                   // log2 of the growth that P may carry
 constexpr int kRegsSoftmax = 192, kRegsOther = 120;
 static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "the block's registers at launch");
 
 constexpr int kMaxStages = 10;
-constexpr int kJoin = 8;                        // vectors of a shared item's parts under way per lane
 
 struct Ctrl {
     uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], v_end[kMaxStages];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_half[2], p_full[2], o_half[2], o_full[2], o_free[2];
+    uint64_t s_full[2][2], p_full[2][2], o_full[2][2];   // of a warpgroup's even and odd steps
+    uint64_t o_free[2];
     uint64_t ml_full[4];
-    uint64_t turn[2][4];
     uint64_t teardown;
     uint32_t tmem_base;
     int abort_flag;
@@ -85,6 +85,11 @@ struct Cfg {
     static_assert(kStages <= kMaxStages, "barriers");
 };
 
+template <int kValue>
+struct Int {
+    static constexpr int value = kValue;
+};
+
 struct Params {
     CUtensorMap map_q, map_k, map_v;
     AttnArgs a;
@@ -100,11 +105,13 @@ __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_n_major)
 }
 
 // The tensor-core products of one step, each issued by one elected lane of the
-// converged warp from a single asm block (see stage_issue_1sm).
-// S = Q K^T: operands as 128-byte swizzled rows, K-major; K = 16 columns an
-// MMA, 64-column halves 16 KB apart.
+// converged warp from a single asm block (see stage_issue_1sm), and what its
+// completion signals.
+// S = Q K^T (N = 64 keys): operands as 128-byte swizzled rows, K-major; K = 16
+// columns an MMA, 64-column halves 16 KB apart.
 template <int kDP>
-__device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q_lo, uint32_t k_lo, uint32_t hi, uint32_t idesc)
+__device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q_lo, uint32_t k_lo, uint32_t hi, uint32_t idesc,
+                                         uint32_t bar)
 {
     if (kDP == 128)
         asm volatile(
@@ -126,7 +133,8 @@ __device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q_lo, uint32_t k_l
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
         " add.u32 x, %1, 1030; add.u32 y, %2, 1030; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
-        "}\n" ::"r"(s), "r"(q_lo), "r"(k_lo), "r"(hi), "r"(idesc)
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n"
+        "}\n" ::"r"(s), "r"(q_lo), "r"(k_lo), "r"(hi), "r"(idesc), "r"(bar)
         : "memory");
     else
         asm volatile(
@@ -140,13 +148,14 @@ __device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q_lo, uint32_t k_l
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
         " add.u32 x, %1, 6; add.u32 y, %2, 6; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
-        "}\n" ::"r"(s), "r"(q_lo), "r"(k_lo), "r"(hi), "r"(idesc)
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n"
+        "}\n" ::"r"(s), "r"(q_lo), "r"(k_lo), "r"(hi), "r"(idesc), "r"(bar)
         : "memory");
 }
 // O += P V over 64 keys: P in tensor memory (8 columns for 16 keys), V as
 // stored (N-major; 16 keys are 2 KB).
 __device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint32_t v_lo, uint32_t hi, uint32_t idesc,
-                                         uint32_t acc)
+                                         uint32_t acc, uint32_t bar)
 {
     asm volatile(
         "{\n .reg .pred e, p, pt;\n .reg .b32 r, x, y;\n .reg .b64 db;\n"
@@ -159,7 +168,16 @@ __device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint32_t v_lo, 
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
         " add.u32 x, %2, 384; mov.b64 db, {x, %3}; add.u32 y, %1, 24;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
-        "}\n" ::"r"(o), "r"(p), "r"(v_lo), "r"(hi), "r"(idesc), "r"(acc)
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n"
+        "}\n" ::"r"(o), "r"(p), "r"(v_lo), "r"(hi), "r"(idesc), "r"(acc), "r"(bar)
+        : "memory");
+}
+
+// Arrival of the warp (its lane 0), without a branch around it.
+__device__ __forceinline__ void mbar_arrive_warp(uint32_t bar, int lane)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"(lane)
         : "memory");
 }
 
@@ -323,14 +341,19 @@ __device__ __forceinline__ bool wait_use(const volatile uint32_t* issued, uint32
     return wait_on(bar, parity, abort_flag, status, site);
 }
 
+__device__ __forceinline__ bool test_use(const volatile uint32_t* issued, uint32_t use, uint32_t bar, uint32_t parity)
+{
+    return !__any_sync(0xffffffffu, (int32_t)(*issued - use) <= 0) && mbar_test_warp(bar, parity);
+}
+
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
-// What is done to a row's 128 scores in tensor memory before the softmax reads
+// What is done to a row's scores of a step in tensor memory before the softmax reads
 // them: the sign of a negative scale, -inf at keys outside lw .. h - 1.
 __device__ __forceinline__ void edit_scores(uint32_t taddr, bool negate, int h, int lw)
 {
 #pragma unroll 1
-    for (int x = 0; x < 128; x += 32) {
+    for (int x = 0; x < kStep; x += 32) {
         const uint32_t seen = low_bits(h - x) & ~low_bits(lw - x);
         if (!negate && __all_sync(0xffffffffu, seen == ~0u)) continue;
         float s[32];
@@ -467,8 +490,14 @@ struct Pieces {
     }
 };
 
-// A key tile's position in the ring: tile g of the CTA has its keys in stage
-// 2g % kStages, its values in the next.
+// The ring's order within an item of n key tiles: K0 K1 V0 K2 V1 ... K(n-1)
+// V(n-2) V(n-1).  Values are needed a softmax later than their keys; fetched
+// right behind them they would hold a stage for that time (with 5 stages of 32
+// KB that leaves too little under way for HBM's latency).
+__device__ __forceinline__ uint32_t use_of_k(int i) { return i == 0 ? 0u : 2u * i - 1u; }
+__device__ __forceinline__ uint32_t use_of_v(int i, int n) { return i == n - 1 ? 2u * n - 1u : 2u * i + 2u; }
+
+// Stage and phase parity of the ring's use `use`.
 template <int kStages>
 __device__ __forceinline__ uint32_t stage_of(uint32_t use, uint32_t* parity)
 {
@@ -502,18 +531,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         mbar_init(smem_u32(&ctrl->q_full), 1);
         mbar_init(smem_u32(&ctrl->q_empty), 2);
         for (int j = 0; j < 2; j++) {
-            mbar_init(smem_u32(&ctrl->s_full[j]), 1);
-            mbar_init(smem_u32(&ctrl->p_half[j]), 4);
-            mbar_init(smem_u32(&ctrl->p_full[j]), 4);
-            mbar_init(smem_u32(&ctrl->o_half[j]), 1);
-            mbar_init(smem_u32(&ctrl->o_full[j]), 1);
+            for (int x = 0; x < 2; x++) {
+                mbar_init(smem_u32(&ctrl->s_full[j][x]), 1);
+                mbar_init(smem_u32(&ctrl->p_full[j][x]), 4);
+                mbar_init(smem_u32(&ctrl->o_full[j][x]), 1);
+            }
             mbar_init(smem_u32(&ctrl->o_free[j]), 4);
         }
-        for (int w = 0; w < 4; w++) {
-            mbar_init(smem_u32(&ctrl->ml_full[w]), 1);
-            mbar_init(smem_u32(&ctrl->turn[0][w]), 1);
-            mbar_init(smem_u32(&ctrl->turn[1][w]), 1);
-        }
+        for (int w = 0; w < 4; w++) mbar_init(smem_u32(&ctrl->ml_full[w]), 1);
         mbar_init(smem_u32(&ctrl->teardown), 2);
         ctrl->abort_flag = 0;
         ctrl->issued = 0;
@@ -550,47 +575,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 const int* table = paged ? a.block_table + (int64_t)p.req * a.table_ld : nullptr;
                 int lo[2], hi[2];
                 for (int j = 0; j < 2; j++) p.range(j, row_tile_tokens(a.group), a.window, lo[j], hi[j]);
-                for (int i = 0; i < p.n && ok; i++) {
+                // the lane's page of tiles i, i + 1, i + 2 (lane l: the tile's l-th)
+                auto page_of = [&](int i) {
+                    const int at = (p.tile0 + i) * ppt + lane;
+                    return paged && i < p.n && lane < ppt && at * a.page_size < p.kv_end ? __ldg(table + at) : 0;
+                };
+                int page0 = page_of(0), page1 = page_of(1), page2 = page_of(2);
+                for (int x = 0; x < 2 * p.n; x++, use++) {
+                    const bool kv = x == 2 * p.n - 1 || (x > 0 && !(x & 1));   // values
+                    const int i = kv ? (x == 2 * p.n - 1 ? p.n - 1 : x / 2 - 1) : (x + 1) / 2;
                     const int key0 = (p.tile0 + i) * kAttnKeys;
                     const int valid = min(kAttnKeys, max(p.kv_end - key0, 0));
                     const int pages = paged ? (valid + a.page_size - 1) / a.page_size : 0;
-                    int page = 0;
-                    if (lane < pages) page = __ldg(table + (key0 / a.page_size) + lane);
-                    for (int kv = 0; kv < 2; kv++, use++) {
-                        uint32_t ph;
-                        const uint32_t s = stage_of<kStages>(use, &ph);
-                        if (!mbar_wait_warp(smem_u32(&ctrl->kv_empty[s]), ph ^ 1u, abort_flag, status, 41)) {
-                            ok = false;
-                            break;
-                        }
-                        if (lane == 0) *(volatile uint32_t*)&ctrl->issued = use + 1;
-                        const CUtensorMap* map = kv ? &prm.map_v : &prm.map_k;
-                        const uint32_t dst = base + C::kOffRing + s * C::kTileBytes;
-                        // an item's last values go through warp 11
-                        const uint32_t bar =
-                            smem_u32(kv && valid < kAttnKeys ? &ctrl->v_end[s] : &ctrl->kv_full[s]);
-                        const uint32_t bytes =
-                            paged ? (uint32_t)(pages * a.page_size * kDP * 2) : (uint32_t)C::kTileBytes;
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(bar, bytes);
-                            // only one MMA warp will use it
-                            if (!p.two || i < lo[0] || i >= hi[0] || i < lo[1] || i >= hi[1])
-                                mbar_arrive(smem_u32(&ctrl->kv_empty[s]));
-                        }
-                        __syncwarp();
-                        if (paged) {
-                            // box b: half b / ppt of page b % ppt (at most 16)
-                            const int b = lane, half = b / ppt, pg = b - half * ppt;
-                            const int id = __shfl_sync(0xffffffffu, page, pg);
-                            if (half < C::kHalves && pg < pages)
-                                tma_load_4d(dst + half * 16384 + pg * a.page_size * 128, map, bar, half * 64, 0, p.hk,
-                                            id);
-                        } else if (lane < C::kHalves) {
-                            tma_load_3d(dst + lane * 16384, map, bar, lane * 64, p.hk, p.kv_row + key0);
-                        }
-                        __syncwarp();
-                        issued |= 1u << s;
-                        issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
+                    const int page = kv || x == 0 ? page0 : page1;
+                    uint32_t ph;
+                    const uint32_t s = stage_of<kStages>(use, &ph);
+                    if (!mbar_wait_warp(smem_u32(&ctrl->kv_empty[s]), ph ^ 1u, abort_flag, status, 41)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) *(volatile uint32_t*)&ctrl->issued = use + 1;
+                    const CUtensorMap* map = kv ? &prm.map_v : &prm.map_k;
+                    const uint32_t dst = base + C::kOffRing + s * C::kTileBytes;
+                    // an item's last values go through warp 11
+                    const uint32_t bar = smem_u32(kv && valid < kAttnKeys ? &ctrl->v_end[s] : &ctrl->kv_full[s]);
+                    const uint32_t bytes = paged ? (uint32_t)(pages * a.page_size * kDP * 2) : (uint32_t)C::kTileBytes;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar, bytes);
+                        // only one MMA warp will use it
+                        if (!p.two || i < lo[0] || i >= hi[0] || i < lo[1] || i >= hi[1])
+                            mbar_arrive(smem_u32(&ctrl->kv_empty[s]));
+                    }
+                    __syncwarp();
+                    if (paged) {
+                        // box b: half b / ppt of page b % ppt (at most 16)
+                        const int b = lane, half = b / ppt, pg = b - half * ppt;
+                        const int id = __shfl_sync(0xffffffffu, page, pg);
+                        if (half < C::kHalves && pg < pages)
+                            tma_load_4d(dst + half * 16384 + pg * a.page_size * 128, map, bar, half * 64, 0, p.hk, id);
+                    } else if (lane < C::kHalves) {
+                        tma_load_3d(dst + lane * 16384, map, bar, lane * 64, p.hk, p.kv_row + key0);
+                    }
+                    __syncwarp();
+                    issued |= 1u << s;
+                    issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
+                    if (kv) {
+                        page0 = page1;
+                        page1 = page2;
+                        page2 = page_of(i + 3);
                     }
                 }
             }
@@ -652,86 +684,98 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             __syncwarp();
         } else {
             // ------------------------------------------------------- MMA
-            // Warp 8 + j issues warpgroup j's products: S of a key tile, then
-            // its O once P is there, then the next S into the same columns,
-            // across items too.  Two row tiles: both warps use every key
-            // tile; one row tile: warp j the tiles j, j + 2, ...  Either way
-            // a stage is free after two commits on it.
+            // Warp 8 + j issues warpgroup j's products: a step's S once the P V
+            // of the step two before has gone out (they share columns), across
+            // items too; a step's P V once P is there.  Two row tiles: both
+            // warps use every key tile; one row tile: warp j the tiles j,
+            // j + 2, ... (a stage is free after two arrivals: both warps', or
+            // the one warp's and the copying warp's own).
             const int j = warp - kWarpMma;
             const uint64_t kdesc0 = make_smem_desc(base, 16, 1024, 2);       // K-major: 8-row groups 1 KB apart
             const uint64_t vdesc0 = make_smem_desc(base, 16384, 1024, 2);    // N-major: 64-column halves 16 KB
                                                                              // apart, 8-key groups 1 KB apart
-            constexpr uint32_t kIdescS = idesc_of(128, false), kIdescO = idesc_of(kDP, true);
+            constexpr uint32_t kIdescS = idesc_of(kStep, false), kIdescO = idesc_of(kDP, true);
+            constexpr uint32_t kStepDesc = kStep * 128 >> 4;                 // 64 rows on
             const uint32_t k_hi = (uint32_t)(kdesc0 >> 32), v_hi = (uint32_t)(vdesc0 >> 32);
             const uint32_t q_lo = (uint32_t)kdesc0;
             const uint32_t ring_k = q_lo + (C::kOffRing >> 4), ring_v = (uint32_t)vdesc0 + (C::kOffRing >> 4);
             const uint32_t full0 = smem_u32(&ctrl->kv_full[0]), empty0 = smem_u32(&ctrl->kv_empty[0]);
             const uint32_t ts = tmem + kColS + 128u * j, to = tmem + kColO + 128u * j;
-            const uint32_t s_full = smem_u32(&ctrl->s_full[j]), o_full = smem_u32(&ctrl->o_full[j]);
-            const uint32_t p_half = smem_u32(&ctrl->p_half[j]), p_full = smem_u32(&ctrl->p_full[j]);
-            const uint32_t o_half = smem_u32(&ctrl->o_half[j]);
-            const uint32_t q_empty = smem_u32(&ctrl->q_empty);
+            const uint32_t s_full = smem_u32(&ctrl->s_full[j][0]), o_full = smem_u32(&ctrl->o_full[j][0]);
+            const uint32_t p_full = smem_u32(&ctrl->p_full[j][0]), o_free = smem_u32(&ctrl->o_free[j]);
+            const uint32_t q_full = smem_u32(&ctrl->q_full), q_empty = smem_u32(&ctrl->q_empty);
             uint32_t use = 0;                      // stages used by the items before
-            uint32_t qph = 0, pph = 0, oph = 1;    // phases: Q, P, O free (nothing to wait for at first)
+            uint32_t qph = 0, oph = 1;             // phases: Q, O free (nothing to wait for at first)
+            uint32_t s_cnt = 0, o_cnt = 0;         // steps whose S, whose P V have gone out
+            // the steps in between (at most two, the oldest first): the ring
+            // use of their V, and 4 bits each: second half of a tile, first
+            // of its item
+            uint32_t pend = 0, pend_use[2] = {0, 0};
             bool ok = true;
+            auto issue_o = [&]() {
+                const uint32_t d = pend & 15u, vu = pend_use[0], buf = o_cnt & 1u;
+                uint32_t vph;
+                const uint32_t vs = stage_of<kStages>(vu, &vph);
+                if ((d & 2u) && !wait_on(o_free, oph, abort_flag, status, 47)) return false;   // read by its last item
+                if (d & 2u) oph ^= 1u;
+                if (!(d & 1u) && !wait_use(&ctrl->issued, vu, full0 + 8u * vs, vph, abort_flag, status, 46)) return false;
+                if (!wait_on(p_full + 8u * buf, (o_cnt >> 1) & 1u, abort_flag, status, 48)) return false;
+                tc_fence_after();
+                issue_pv(to, ts + 64u * buf, ring_v + vs * (C::kTileBytes >> 4) + (d & 1u) * kStepDesc, v_hi, kIdescO,
+                         (d & 2u) ^ 2u, o_full + 8u * buf);
+                if (d & 1u) mma_commit_warp(empty0 + 8u * vs);
+                o_cnt++;
+                pend >>= 4;
+                pend_use[0] = pend_use[1];
+                return true;
+            };
             while (ok && pieces.next(p)) {
                 int first, end;
                 p.range(j, row_tile_tokens(a.group), a.window, first, end);
                 const int by = p.two ? 1 : 2;
                 if (!p.two) first = j;
-                uint32_t kph;                      // stage of the warp's next K, its phase; V is in the stage after
-                uint32_t ks = stage_of<kStages>(use + 2 * first, &kph);
                 const uint32_t qt = q_lo + (p.two && j ? C::kTileBytes >> 4 : 0);
-                if (!wait_on(smem_u32(&ctrl->q_full), qph, abort_flag, status, 44)) break;
+                while (ok && s_cnt != o_cnt && !mbar_test_warp(q_full, qph)) ok = issue_o();
+                if (!ok || !wait_on(q_full, qph, abort_flag, status, 44)) {
+                    ok = false;
+                    break;
+                }
                 qph ^= 1u;
-                if (first >= end && lane == 0) mbar_arrive(q_empty);     // no tile for this warp
-                for (int i = first; i < end; i += by) {
-                    const uint32_t ku = use + 2u * (uint32_t)i;
-                    if (!wait_use(&ctrl->issued, ku, full0 + 8u * ks, kph, abort_flag, status, 45)) {
+                if (first >= end) {                // no tile for this warp
+                    if (lane == 0) mbar_arrive(q_empty);
+                    __syncwarp();
+                }
+                for (int i = first; i < end && ok; i += by) {
+                    const uint32_t ku = use + use_of_k(i), vu = use + use_of_v(i, p.n);
+                    uint32_t kph;
+                    const uint32_t ks = stage_of<kStages>(ku, &kph), kb = full0 + 8u * ks;
+                    while (ok && s_cnt != o_cnt && !test_use(&ctrl->issued, ku, kb, kph)) ok = issue_o();
+                    if (!ok || !wait_use(&ctrl->issued, ku, kb, kph, abort_flag, status, 45)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-                    issue_qk<kDP>(ts, qt, ring_k + ks * (C::kTileBytes >> 4), k_hi, kIdescS);
-                    mma_commit_warp(s_full);
-                    mma_commit_warp(empty0 + 8u * ks);
-                    if (i + by >= end) mma_commit_warp(q_empty);
-                    const bool wrap = ks + 1 == kStages;
-                    const uint32_t vs = wrap ? 0 : ks + 1, vph = wrap ? kph ^ 1u : kph;
-                    // the accumulator's previous item has been read
-                    if (i == first) {
-                        if (!wait_on(smem_u32(&ctrl->o_free[j]), oph, abort_flag, status, 47)) {
-                            ok = false;
-                            break;
+                    for (int h = 0; h < 2; h++) {
+                        if (s_cnt - o_cnt == 2u && !(ok = issue_o())) break;
+                        const uint32_t buf = s_cnt & 1u;
+                        tc_fence_after();
+                        issue_qk<kDP>(ts + 64u * buf, qt, ring_k + ks * (C::kTileBytes >> 4) + h * kStepDesc, k_hi, kIdescS,
+                                      s_full + 8u * buf);
+                        
+                        if (h) {
+                            mma_commit_warp(empty0 + 8u * ks);
+                            if (i + by >= end) mma_commit_warp(q_empty);
                         }
-                        oph ^= 1u;
-                    }
-                    const uint32_t v_lo = ring_v + vs * (C::kTileBytes >> 4);
-                    if (!wait_use(&ctrl->issued, ku + 1, full0 + 8u * vs, vph, abort_flag, status, 46) ||
-                        !wait_on(p_half, pph, abort_flag, status, 48)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    issue_pv(to, ts, v_lo, v_hi, kIdescO, i != first);
-                    mma_commit_warp(o_half);
-                    if (!wait_on(p_full, pph, abort_flag, status, 49)) {
-                        ok = false;
-                        break;
-                    }
-                    pph ^= 1u;
-                    tc_fence_after();
-                    issue_pv(to, ts + 64, v_lo + (64 * 128 >> 4), v_hi, kIdescO, 1u);
-                    mma_commit_warp(o_full);
-                    mma_commit_warp(empty0 + 8u * vs);
-                    ks += 2 * by;
-                    if (ks >= kStages) {
-                        ks -= kStages;
-                        kph ^= 1u;
+                        const uint32_t d = (uint32_t)h | (i == first && h == 0 ? 2u : 0u);
+                        const bool one = s_cnt != o_cnt;       // one step is pending already
+                        pend |= d << (one ? 4 : 0);
+                        if (one) pend_use[1] = vu;
+                        else pend_use[0] = vu;
+                        s_cnt++;
                     }
                 }
                 use += 2u * (uint32_t)p.n;
             }
+            while (ok && s_cnt != o_cnt) ok = issue_o();
             // every MMA issued has completed before teardown
             mma_commit_warp(smem_u32(&ctrl->teardown));
             if (lane == 0) mbar_wait_teardown(smem_u32(&ctrl->teardown), 0);
@@ -747,16 +791,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         const int tk = row / a.group, g = row - tk * a.group;    // this thread's token and head in a row tile
         const uint32_t lane_addr = tmem + ((uint32_t)(w * 32) << 16);
         const uint32_t ts = lane_addr + kColS + 128 * j, to = lane_addr + kColO + 128 * j;
+        const uint32_t s_full = smem_u32(&ctrl->s_full[j][0]), p_full = smem_u32(&ctrl->p_full[j][0]);
+        const uint32_t o_full = smem_u32(&ctrl->o_full[j][0]);
         const bool negate = a.scale < 0.0f;
         // a zero scale: any tiny factor gives equal probabilities, without 0 * inf at masked keys
         const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
         const float lazy = kLazy / c;
-        uint32_t s_cnt = 0, ml_cnt = 0, t_cnt = 0;
+        uint32_t cnt = 0, ml_cnt = 0;      // steps done
         bool ok = true;
         while (ok && pieces.next(p)) {
-            int first, end, first_o, end_o;                      // tiles of this warpgroup, of the other
+            int first, end;                                      // tiles of this warpgroup
             p.range(j, row_tokens, a.window, first, end);
-            p.range(1 - j, row_tokens, a.window, first_o, end_o);
             const int by = p.two ? 1 : 2;
             if (!p.two) first = j;
             const int t = (p.two && j ? row_tokens : 0) + tk;    // token of the item
@@ -765,95 +810,76 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             const int pos = p.pos0 + t;
             const int hi = mine ? min(pos + 1, p.kv_end) : 0;      // keys lo .. hi - 1
             const int lo = mine && a.window ? max(pos + 1 - a.window, 0) : 0;
+            // keys that every row of the warp sees (edits are needed beyond)
+            const int hi_all = __reduce_min_sync(0xffffffffu, mine ? hi : 0x7fffffff);
+            const int lo_all = __reduce_max_sync(0xffffffffu, lo);
             float m = -INFINITY, l = 0.0f;
             if (first >= end) continue;      // the second warpgroup of a single key tile
-            for (int i = first; i < end; i += by) {
-                if (!mbar_wait_warp(smem_u32(&ctrl->s_full[j]), s_cnt & 1u, abort_flag, status, 50)) {
+#pragma unroll 1
+            for (int x = 0; x < 2 * (end - first); x += by == 1 || (x & 1) == 0 ? 1 : 3, cnt++) {
+                // step x: 64 keys; its barriers and columns alternate
+                const uint32_t buf = cnt & 1u, ph = (cnt >> 1) & 1u;
+                if (!mbar_wait_warp(s_full + 8u * buf, ph, abort_flag, status, 50)) {
                     ok = false;
                     break;
                 }
-                s_cnt++;
-                const bool both = p.two && i >= first_o && i < end_o;
-                if (both) {
-                    // the two warpgroups' exponentials in turn (per pair of
-                    // warps): together they would wait for the tensor pipe
-                    // together, and leave it idle together
-                    if (!mbar_wait_warp(smem_u32(&ctrl->turn[j][w]), (t_cnt & 1u) ^ (j ? 0u : 1u), abort_flag, status,
-                                        54)) {
-                        ok = false;
-                        break;
-                    }
-                    t_cnt++;
-                }
                 if (any) {
                     tc_fence_after();
-                    const int key0 = (p.tile0 + i) * kAttnKeys;
-                    if (negate || __any_sync(0xffffffffu, mine && (hi < key0 + kAttnKeys || lo > key0)))
-                        edit_scores(ts, negate, hi - key0, lo - key0);
-                }
-#pragma unroll 1
-                for (int half = 0; half < 2 && ok; half++) {     // 64 keys at a time
-                    if (any) {
-                        float s[64];
-                        uint32_t r[32];
-                        float mc, sum;
-                        for (;;) {
-                            tmem_ld32(ts + 64 * half, s);
-                            tmem_ld32(ts + 64 * half + 32, s + 32);
-                            tmem_ld_wait();
-                            // P with the m in use, their maximum beside it;
-                            // where that has outgrown m (and at an item's
-                            // first keys) m moves and P is formed again: S is
-                            // still there
-                            mc = m == -INFINITY ? 0.0f : -m * c;
-                            const float mx = max_scores(s);
-                            sum = exp_scores(s, c, mc, r);
-                            const bool up = mine && (mx > m + lazy || (m == -INFINITY && mx > m));
-                            if (!__any_sync(0xffffffffu, up)) break;
-                            const float m1 = up ? mx : m;
-                            if (i > first || half) {
-                                // rescale what has been summed with the old
-                                // maximum: the P V of the tiles before is
-                                // complete, as S is; that of the first half
-                                // has a signal
-                                const float f = up ? ex2((m - m1) * c) : 1.0f;
-                                l *= f;
-                                if (half && !mbar_wait_warp(smem_u32(&ctrl->o_half[j]), (s_cnt - 1) & 1u, abort_flag, status,
-                                                            51)) {
-                                    ok = false;
-                                    break;
-                                }
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int k = 0; k < kDP / 16; k++) {
-                                    float o[16];
-                                    tmem_ld16(to + 16 * k, o);
-                                    tmem_ld_wait();
-                                    uint32_t q[16];
-#pragma unroll
-                                    for (int y = 0; y < 16; y++) q[y] = __float_as_uint(f == 0.0f ? 0.0f : o[y] * f);
-                                    tmem_st16(to + 16 * k, q);
-                                }
+                    const int key0 = p.tile0 * kAttnKeys + 2 * first * kStep + x * kStep;
+                    if (negate || hi_all < key0 + kStep || lo_all > key0)
+                        edit_scores(ts + 64 * buf, negate, hi - key0, lo - key0);
+                    float s[kStep];
+                    uint32_t r[32];
+                    float mc, sum;
+                    for (;;) {
+                        tmem_ld32(ts + 64 * buf, s);
+                        tmem_ld32(ts + 64 * buf + 32, s + 32);
+                        tmem_ld_wait();
+                        // P with the m in use, the step's maximum beside it;
+                        // where that has outgrown m (and at an item's first
+                        // keys) m moves and P is formed again: S is still there
+                        mc = m == -INFINITY ? 0.0f : -m * c;
+                        const float mx = max_scores(s);
+                        sum = exp_scores(s, c, mc, r);
+                        const bool up = mine && (mx > m + lazy || (m == -INFINITY && mx > m));
+                        if (!__any_sync(0xffffffffu, up)) break;
+                        const float m1 = up ? mx : m;
+                        if (x > 0) {
+                            // rescale what has been summed with the old
+                            // maximum, once the last P V is complete
+                            const float f = up ? ex2((m - m1) * c) : 1.0f;
+                            l *= f;
+                            if (!mbar_wait_warp(o_full + 8u * (buf ^ 1u), ((cnt - 1) >> 1) & 1u, abort_flag, status, 51)) {
+                                ok = false;
+                                break;
                             }
-                            m = m1;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int k = 0; k < kDP / 16; k++) {
+                                float o[16];
+                                tmem_ld16(to + 16 * k, o);
+                                tmem_ld_wait();
+                                uint32_t q[16];
+#pragma unroll
+                                for (int y = 0; y < 16; y++) q[y] = __float_as_uint(f == 0.0f ? 0.0f : o[y] * f);
+                                tmem_st16(to + 16 * k, q);
+                            }
                         }
-                        tmem_st32(ts + 64 * half, r);
-                        l += sum;
-                        tmem_st_wait();
-                        tc_fence_before();
+                        m = m1;
                     }
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(smem_u32(half ? &ctrl->p_full[j] : &ctrl->p_half[j]));
-                        if (both && !half) mbar_arrive(smem_u32(&ctrl->turn[1 - j][w]));
-                    }
+                    tmem_st32(ts + 64 * buf, r);
+                    l += sum;
+                    tmem_st_wait();
+                    tc_fence_before();
                 }
+                __syncwarp();
+                mbar_arrive_warp(p_full + 8u * buf, lane);
             }
             if (!ok) break;
 
             // ---- the item's end: O in tensor memory, m and l here
             const bool merge = !p.two && p.n > 1;       // both warpgroups hold a share of the same rows
-            if (!mbar_wait_warp(smem_u32(&ctrl->o_full[j]), (s_cnt - 1) & 1u, abort_flag, status, 52)) break;
+            if (!mbar_wait_warp(o_full + 8u * ((cnt - 1) & 1u), ((cnt - 1) >> 1) & 1u, abort_flag, status, 52)) break;
             tc_fence_after();
             if (merge && j == 1) {
                 ctrl->m[row] = m;
@@ -884,54 +910,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 // contiguous bytes of 8 rows a store (a row a lane would be
                 // 16 bytes of 32 rows, four times the accesses)
                 const float inv = none ? 0.0f : 1.0f / l;
-                const uint32_t valid = __ballot_sync(0xffffffffu, mine);
+                const uint32_t valid = __ballot_sync(0xffffffffu, mine), zero = __ballot_sync(0xffffffffu, none);
                 const int64_t at = tok * a.ldo + head * a.ho;
 #pragma unroll 1
-                for (int h = 0; h < 2; h++) {                    // rows 16h .. 16h + 15 of the warp
-                    float fa[2], fb[2];
-                    __nv_bfloat16* out[2];
-                    bool live[2];
+                for (int x = 0; x < 2 * (kDP / 32); x++) {       // 16 rows, 32 columns at a time
+                    const int h = 16 * (x & 1), col = 32 * (x >> 1);
+                    if (valid >> h == 0) continue;               // (the rows of an item are its first)
+                    float o[16], o1[16];
+                    const uint32_t from = ((uint32_t)h << 16) + col;
+                    tmem_ld_rows(to + from, o);
+                    if (merge) tmem_ld_rows(to + 128 + from, o1);
+                    tmem_ld_wait();
 #pragma unroll
                     for (int b = 0; b < 2; b++) {
-                        const int r = 16 * h + 8 * b + (lane >> 2);
-                        fa[b] = __shfl_sync(0xffffffffu, f0 * inv, r);
-                        fb[b] = __shfl_sync(0xffffffffu, f1 * inv, r);
-                        out[b] = a.out + __shfl_sync(0xffffffffu, at, r) + 8 * (lane & 3);
-                        live[b] = (valid >> r) & 1u;
-                    }
-                    if ((valid >> (16 * h)) == 0) break;         // (the rows of an item are its first)
-#pragma unroll 1
-                    for (int k = 0; k < kDP; k += 64) {          // 64 columns at a time
-                        float o[32];
-                        const uint32_t at_h = ((uint32_t)(16 * h) << 16) + k;
-                        tmem_ld_rows(to + at_h, o);
-                        tmem_ld_rows(to + at_h + 32, o + 16);
-                        tmem_ld_wait();
+                        const int r = h + 8 * b + (lane >> 2);
+                        const float fa = __shfl_sync(0xffffffffu, f0 * inv, r), fb = __shfl_sync(0xffffffffu, f1 * inv, r);
+                        __nv_bfloat16* out = a.out + __shfl_sync(0xffffffffu, at, r) + col + 8 * (lane & 3);
+                        uint32_t w4[4];
 #pragma unroll
-                        for (int x = 0; x < 32; x++) o[x] = fa[(x >> 1) & 1] == 0.0f ? 0.0f : o[x] * fa[(x >> 1) & 1];
-                        if (merge) {
-                            float o1[32];
-                            tmem_ld_rows(to + 128 + at_h, o1);
-                            tmem_ld_rows(to + 128 + at_h + 32, o1 + 16);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int x = 0; x < 32; x++)
-                                o[x] += fb[(x >> 1) & 1] == 0.0f ? 0.0f : o1[x] * fb[(x >> 1) & 1];
-                        }
-#pragma unroll
-                        for (int y = 0; y < 2; y++) {
-#pragma unroll
-                            for (int b = 0; b < 2; b++) {
-                                uint32_t x[4];
-#pragma unroll
-                                for (int i = 0; i < 4; i++)
-                                    x[i] = cvt_bf16x2(o[16 * y + 4 * i + 2 * b], o[16 * y + 4 * i + 2 * b + 1]);
-                                quad_transpose(x, lane & 3);
-                                const int col = k + 32 * y;
-                                if (live[b] && col + 8 * (lane & 3) < a.head_dim)
-                                    *reinterpret_cast<uint4*>(out[b] + col) = make_uint4(x[0], x[1], x[2], x[3]);
+                        for (int i = 0; i < 4; i++) {
+                            float e0 = o[4 * i + 2 * b] * fa, e1 = o[4 * i + 2 * b + 1] * fa;
+                            if (merge) {
+                                e0 += o1[4 * i + 2 * b] * fb;
+                                e1 += o1[4 * i + 2 * b + 1] * fb;
                             }
+                            w4[i] = (zero >> r) & 1u ? 0u : cvt_bf16x2(e0, e1);
                         }
+                        quad_transpose(w4, lane & 3);
+                        if ((valid >> r) & 1u && col + 8 * (lane & 3) < a.head_dim)
+                            *reinterpret_cast<uint4*>(out) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
                     }
                 }
                 if (mine && a.lse)
@@ -940,21 +947,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 float* part = a.partials + (2 * cta + (p.cta0 == cta ? 1 : 0)) * kAttnSlotFloats;
                 const int srow = (p.two ? j * kAttnRows : 0) + row;
 #pragma unroll 1
-                for (int k = 0; k < kDP / 32; k++) {
-                    float o[32];
-                    tmem_ld32(to + 32 * k, o);
+                for (int k = 0; k < kDP; k += 16) {
+                    float o[16];
+                    tmem_ld16(to + k, o);
                     tmem_ld_wait();
                     if (merge) {
-                        float o1[32];
-                        tmem_ld32(to + 128 + 32 * k, o1);
+                        float o1[16];
+                        tmem_ld16(to + 128 + k, o1);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int y = 0; y < 32; y++) o[y] = (f0 == 0.0f ? 0.0f : o[y] * f0) + (f1 == 0.0f ? 0.0f : o1[y] * f1);
+                        for (int y = 0; y < 16; y++) o[y] = o[y] * f0 + o1[y] * f1;
                     }
                     if (!mine) continue;
 #pragma unroll
-                    for (int y = 0; y < 8; y++)
-                        __stcg(reinterpret_cast<float4*>(part) + (8 * k + y) * kAttnSlotRows + srow,
+                    for (int y = 0; y < 4; y++)
+                        __stcg(reinterpret_cast<float4*>(part) + (k / 4 + y) * kAttnSlotRows + srow,
                                make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]));
                 }
                 if (mine) {
@@ -979,69 +986,93 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             last = __shfl_sync(0xffffffffu, last, 0);
             if (!last) continue;
             if (lane == 0) *ticket = 0;
-            const int row0 = (p.two ? j * kAttnRows : 0) + w * 32;   // the warp's first row in a slot
+            // rows in turn over the lanes, `share` lanes to a row with every
+            // share-th 4-column vector each
             const int rows = __popc(__ballot_sync(0xffffffffu, mine));
+            const int share = rows <= 4 ? 8 : rows <= 8 ? 4 : rows <= 16 ? 2 : 1;
+            const int r = lane & (32 / share - 1), sub = lane / (32 / share);
+            const int srow = (p.two ? j * kAttnRows : 0) + w * 32 + r;
             // part i of the item is in slot 2 (cta0 + i), the first in 2 cta0 + 1
-            const float* const part0 = a.partials + (2 * p.cta0 + 1) * kAttnSlotFloats;
-            auto part_of = [&](int i) { return part0 + (i == 0 ? 0 : 2 * i - 1) * kAttnSlotFloats; };
-            const int my = row0 + min(lane, rows - 1);
+            const float* const stat = a.partials + kAttnSlotRows * kDP + srow;
+            auto slot_of = [&](int i) { return (2 * (p.cta0 + i) + (i == 0 ? 1 : 0)) * kAttnSlotFloats; };
+            // maximum and sum over the parts: each of a row's lanes takes
+            // every share-th part (a read of another CTA's words takes 1-2
+            // thousand cycles: few rounds of many)
             float mall = -INFINITY, lall = 0.0f;
-#pragma unroll 4
-            for (int i = 0; i < p.parts; i++) mall = fmaxf(mall, __ldcg(part_of(i) + kAttnSlotRows * kDP + my));
+#pragma unroll 1
+            for (int i0 = sub; i0 < p.parts; i0 += 4 * share) {
+                float mi[4], li[4], top = mall;
+#pragma unroll
+                for (int u = 0; u < 4; u++) {
+                    const int i = i0 + u * share;
+                    mi[u] = i < p.parts ? __ldcg(stat + slot_of(i)) : -INFINITY;
+                    li[u] = i < p.parts ? __ldcg(stat + slot_of(i) + kAttnSlotRows) : 0.0f;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; u++) top = fmaxf(top, mi[u]);
+                const float ref = top == -INFINITY ? 0.0f : top;
+                lall *= ex2(mall - ref);
+#pragma unroll
+                for (int u = 0; u < 4; u++) lall += li[u] * ex2(mi[u] - ref);
+                mall = top;
+            }
+#pragma unroll 1
+            for (int x = 32 / share; x < 32; x <<= 1) {
+                const float mo = __shfl_xor_sync(0xffffffffu, mall, x), lo = __shfl_xor_sync(0xffffffffu, lall, x);
+                const float top = fmaxf(mall, mo), ref = top == -INFINITY ? 0.0f : top;
+                lall = lall * ex2(mall - ref) + lo * ex2(mo - ref);
+                mall = top;
+            }
             const float ms = mall == -INFINITY ? 0.0f : mall;
-#pragma unroll 4
-            for (int i = 0; i < p.parts; i++) {
-                const float* part = part_of(i) + kAttnSlotRows * kDP + my;
-                lall += __ldcg(part + kAttnSlotRows) * ex2(__ldcg(part) - ms);
-            }
-            if (mine && a.lse)
-                a.lse[tok * a.heads + head] = lall == 0.0f ? -INFINITY : (mall + log2f(lall)) * 0.6931471805599453f;
             const float inv = lall == 0.0f ? 0.0f : 1.0f / lall;
-            const int64_t at = tok * a.ldo + head * a.ho;
-            // lane l takes the 4-column vectors l, l + 32, ... of the rows'
-            // vectors (row fastest), kJoin of them at a time
-            const int vecs = rows * (a.head_dim / 4);
-            const int dv = 32 / rows, dr = 32 - dv * rows;
-            int v = lane / rows, r = lane - v * rows;
-            for (int b = lane; b - lane < vecs; b += 32 * kJoin) {
-                float4 acc[kJoin];
-                int vv[kJoin], rr[kJoin];
+            const int64_t at = __shfl_sync(0xffffffffu, tok * a.ldo + head * a.ho, r);
+            const int64_t lse_at = __shfl_sync(0xffffffffu, tok * a.heads + head, r);
+            if (a.lse && r < rows && sub == 0)
+                a.lse[lse_at] = lall == 0.0f ? -INFINITY : (mall + log2f(lall)) * 0.6931471805599453f;
+            if (r >= rows) continue;
+            const int vecs = a.head_dim / 4;
+            auto join = [&](auto vecs_at_once, auto parts_at_once) {
+                constexpr int kV = decltype(vecs_at_once)::value, kP = decltype(parts_at_once)::value;
+#pragma unroll 1
+                for (int v0 = sub; v0 < vecs; v0 += kV * share) {
+                    float4 acc[kV];
 #pragma unroll
-                for (int y = 0; y < kJoin; y++) {
-                    const bool in = b + 32 * y < vecs;
-                    vv[y] = in ? v : 0;
-                    rr[y] = in ? r : 0;
-                    v += dv;
-                    r += dr;
-                    if (r >= rows) {
-                        r -= rows;
-                        v++;
+                    for (int y = 0; y < kV; y++) acc[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+                    for (int i0 = 0; i0 < p.parts; i0 += kP) {
+                        float f[kP];
+                        float4 e[kP][kV];
+#pragma unroll
+                        for (int u = 0; u < kP; u++) {
+                            const int i = min(i0 + u, p.parts - 1);
+                            f[u] = i0 + u < p.parts ? __ldcg(stat + slot_of(i)) : -INFINITY;
+                            const float4* o = reinterpret_cast<const float4*>(a.partials + slot_of(i)) + srow;
+#pragma unroll
+                            for (int y = 0; y < kV; y++)
+                                e[u][y] = __ldcg(o + min(v0 + y * share, vecs - 1) * kAttnSlotRows);
+                        }
+#pragma unroll
+                        for (int u = 0; u < kP; u++) {
+                            f[u] = ex2(f[u] - ms) * inv;
+#pragma unroll
+                            for (int y = 0; y < kV; y++) {
+                                acc[y].x += f[u] * e[u][y].x;
+                                acc[y].y += f[u] * e[u][y].y;
+                                acc[y].z += f[u] * e[u][y].z;
+                                acc[y].w += f[u] * e[u][y].w;
+                            }
+                        }
                     }
-                    acc[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                }
-#pragma unroll 2
-                for (int i = 0; i < p.parts; i++) {
-                    const float* part = part_of(i);
-                    const float f = ex2(__ldcg(part + kAttnSlotRows * kDP + my) - ms) * inv;
 #pragma unroll
-                    for (int y = 0; y < kJoin; y++) {
-                        const float4 o = __ldcg(reinterpret_cast<const float4*>(part) + vv[y] * kAttnSlotRows + row0 + rr[y]);
-                        const float fy = __shfl_sync(0xffffffffu, f, rr[y]);
-                        acc[y].x += fy * o.x;
-                        acc[y].y += fy * o.y;
-                        acc[y].z += fy * o.z;
-                        acc[y].w += fy * o.w;
-                    }
+                    for (int y = 0; y < kV; y++)
+                        if (v0 + y * share < vecs)
+                            *reinterpret_cast<uint2*>(a.out + at + 4 * (v0 + y * share)) =
+                                lall == 0.0f ? make_uint2(0u, 0u)
+                                             : make_uint2(cvt_bf16x2(acc[y].x, acc[y].y), cvt_bf16x2(acc[y].z, acc[y].w));
                 }
-#pragma unroll
-                for (int y = 0; y < kJoin; y++) {
-                    const int64_t ar = __shfl_sync(0xffffffffu, at, rr[y]);
-                    const bool none_r = __shfl_sync(0xffffffffu, inv, rr[y]) == 0.0f;
-                    const uint2 w2 = make_uint2(cvt_bf16x2(acc[y].x, acc[y].y), cvt_bf16x2(acc[y].z, acc[y].w));
-                    if (b + 32 * y < vecs)
-                        *reinterpret_cast<uint2*>(a.out + ar + 4 * vv[y]) = none_r ? make_uint2(0u, 0u) : w2;
-                }
-            }
+            };
+            if (share == 1) join(Int<8>(), Int<2>());
+            else join(Int<4>(), Int<4>());
         }
     }
     tc_fence_before();
