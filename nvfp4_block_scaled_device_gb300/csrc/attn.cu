@@ -400,7 +400,7 @@ __device__ __forceinline__ float max_scores(const float* s)
 // ------------------------------------------------------------------ pieces
 // A CTA's share of one item.
 struct Piece {
-    int tok0, n_tok, req, pos0, kv_end, kv_row;   // of its QTile
+    int tok0, n_tok, req, pos0, kv_end;   // of its QTile
     int hk;              // kv head
     int tile0, n;        // key tiles tile0 .. tile0 + n - 1
     bool two;            // two row tiles
@@ -426,7 +426,7 @@ template <bool kAhead>
 struct Pieces {
     const int4* table;
     int u, end, per_cta, qt, kv_heads, row_tokens;
-    int4 f0, f1, f2;     // QTile qt, or (kAhead) the one that comes next
+    int4 f0, f1;         // QTile qt, or (kAhead) the one that comes next
 
     __device__ __forceinline__ Pieces(const AttnArgs& a, int cta)
     {
@@ -437,7 +437,6 @@ struct Pieces {
         const int4* start = reinterpret_cast<const int4*>(&s->start[cta]);
         f0 = start[0];
         f1 = start[1];
-        f2 = start[2];
         qt = s->first[cta];
         const int units = s->units;
         per_cta = s->per_cta;
@@ -447,19 +446,18 @@ struct Pieces {
     __device__ __forceinline__ void fetch()
     {
         qt++;
-        f0 = table[3 * qt];
-        f1 = table[3 * qt + 1];
-        f2 = table[3 * qt + 2];
+        f0 = table[2 * qt];
+        f1 = table[2 * qt + 1];
     }
     __device__ __forceinline__ bool next(Piece& p)
     {
         while (u < end) {
-            int rel = u - f2.x;
-            if (!kAhead && rel == (kItemUnits + f1.w) * kv_heads) {
+            int rel = u - f1.w;
+            if (!kAhead && rel == (kItemUnits + f1.z) * kv_heads) {
                 fetch();
                 rel = 0;
             }
-            const int tiles = f1.w, item = kItemUnits + tiles;
+            const int tiles = f1.z, item = kItemUnits + tiles;
             p.hk = rel / item;
             const int r0 = rel - p.hk * item, r1 = min(end - u, item - r0) + r0;   // the CTA's units of the item
             const int k0 = max(snap_unit(r0, item) - kItemUnits, 0);
@@ -469,8 +467,7 @@ struct Pieces {
             p.req = f0.z;
             p.pos0 = f0.w;
             p.kv_end = f1.x;
-            p.kv_row = f1.y;
-            p.tile0 = f1.z + k0;
+            p.tile0 = f1.y + k0;
             p.two = f0.y > row_tokens;
             p.cta0 = 0;
             p.parts = 1;
@@ -614,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                         if (half < C::kHalves && pg < pages)
                             tma_load_4d(dst + half * 16384 + pg * a.page_size * 128, map, bar, half * 64, 0, p.hk, id);
                     } else if (lane < C::kHalves) {
-                        tma_load_3d(dst + lane * 16384, map, bar, lane * 64, p.hk, p.kv_row + key0);
+                        tma_load_3d(dst + lane * 16384, map, bar, lane * 64, p.hk, p.tok0 - p.pos0 + key0);   // (packed: the request's first row is its key 0)
                     }
                     __syncwarp();
                     issued |= 1u << s;

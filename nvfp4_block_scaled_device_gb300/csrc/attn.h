@@ -38,11 +38,11 @@ constexpr int kItemUnits = 2;
 struct QTile {
     int32_t tok0, n_tok;     // packed rows (tokens) tok0 .. tok0 + n_tok - 1
     int32_t req, pos0;       // the request, the position of token tok0
-    int32_t kv_end, kv_row;  // no row sees keys from kv_end on; packed row of the request's key 0
+    int32_t kv_end;          // no row sees keys from kv_end on
     int32_t tile0, tiles;    // key tiles tile0 .. tile0 + tiles - 1
-    int32_t unit0, pad[3];   // units before this QTile; it has (kItemUnits + tiles) * kv_heads
+    int32_t unit0;           // units before this QTile; it has (kItemUnits + tiles) * kv_heads
 };
-static_assert(sizeof(QTile) == 48, "QTile");
+static_assert(sizeof(QTile) == 32, "QTile");
 
 struct ScheduleHead {
     int32_t units, per_cta, qtiles, pad[13];

@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kMaxPosition = 1 << 30;
 constexpr int64_t kMaxUnits = (int64_t)1 << 30;   // of a schedule (a call of seconds): the rest is not worked on
 
 struct PlanParams {
@@ -24,6 +25,7 @@ struct PlanParams {
     int* status;
     int page_shift;
     int ctas;                // the attention kernel's grid
+    int schedulers;          // blocks that build the schedule
 };
 
 __device__ __forceinline__ void report(int* status, int code)
@@ -41,129 +43,139 @@ __device__ __forceinline__ int64_t warp_incl_sum(int64_t v, int lane)
     return v;
 }
 
-// A request's lengths, with negative ones taken as zero.
-struct Lens {
-    int64_t ctx, q;
-    bool bad;
-};
-
-__device__ __forceinline__ Lens lens_of(const nvfp4_step_t& s, int r)
-{
-    const int q = __ldg(s.q_len + r), c = s.ctx_len ? __ldg(s.ctx_len + r) : 0;
-    return {c < 0 ? 0 : c, q < 0 ? 0 : q, q < 0 || c < 0};
-}
-
-// Block-wide inclusive prefix sum over the threads (kPlanThreads of them);
-// total: the sum of all.  Every thread of the block calls it.
-__device__ __forceinline__ int64_t block_incl_sum(int64_t v, int64_t* warp_sums, int64_t* total)
+// Block-wide exclusive prefix sums over the threads of two values at once;
+// the totals in *ta, *tb.  Every thread of the block calls it.
+__device__ __forceinline__ void block_prefix(int64_t& a, int64_t& b, int64_t (*warp_sums)[2], int64_t* ta, int64_t* tb)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    v = warp_incl_sum(v, lane);
+    const int64_t ia = warp_incl_sum(a, lane), ib = warp_incl_sum(b, lane);
     __syncthreads();                // the sums of an earlier call have been read
-    if (lane == 31) warp_sums[warp] = v;
+    if (lane == 31) {
+        warp_sums[warp][0] = ia;
+        warp_sums[warp][1] = ib;
+    }
     __syncthreads();
-    int64_t before = 0, all = 0;
+    int64_t all_a = 0, all_b = 0;
+    a = ia - a;
+    b = ib - b;
 #pragma unroll
     for (int w = 0; w < kPlanWarps; w++) {
-        if (w < warp) before += warp_sums[w];
-        all += warp_sums[w];
+        if (w < warp) {
+            a += warp_sums[w][0];
+            b += warp_sums[w][1];
+        }
+        all_a += warp_sums[w][0];
+        all_b += warp_sums[w][1];
     }
-    *total = all;
-    return v + before;
+    *ta = all_a;
+    *tb = all_b;
 }
 
-// The attention's schedule, by one block: the QTiles of all requests in
+// The last of n ascending entries that is at or below v (entry 0 is).
+__device__ __forceinline__ int last_at_or_below(const int32_t* x, int n, int64_t v)
+{
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (x[mid] <= v) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// The attention's schedule, by the last blocks of the grid, each of which works
+// out all of it and writes its share (one SM would take 6 ns for each QTile's
+// store): the QTiles of all requests in
 // order, the prefix sum of their units, and the QTile of each CTA's first
-// unit.  cu: new tokens before each request (shared memory); tile0: room for
-// R + 1 int32 in shared memory.
-__device__ void build_schedule(const PlanParams& p, const int32_t* cu, int32_t* tile0, int64_t* warp_sums)
+// unit.  A thread takes consecutive QTiles, walking from request to request:
+// once for their units, once (the sums known) to write them.  cu: new tokens
+// before each request, ctx: cached tokens, tile0: room for R + 1 int32 (all
+// shared memory).
+__device__ void build_schedule(const PlanParams& p, const int32_t* cu, const int32_t* ctx, int32_t* tile0,
+                               int64_t (*warp_sums)[2], int* longest, int block, int blocks)
 {
     const nvfp4_step_t& s = p.s;
     const int R = (int)s.requests, t = threadIdx.x;
     const int per_tile = 2 * row_tile_tokens((int)(s.heads / s.kv_heads));
+    const int Hkv = (int)s.kv_heads;
     ScheduleHead* head = static_cast<ScheduleHead*>(s.schedule);
     QTile* tiles = const_cast<QTile*>(schedule_tiles(head));
     // QTiles before each request
-    const int per = (R + kPlanThreads - 1) / kPlanThreads;
-    int64_t mine = 0, total = 0;
-    for (int r = t * per; r < min(R, (t + 1) * per); r++) mine += (cu[r + 1] - cu[r] + per_tile - 1) / per_tile;
-    int64_t before = block_incl_sum(mine, warp_sums, &total) - mine;
+    const int per = ((R + kPlanThreads - 1) / kPlanThreads) | 1;     // (odd: no bank conflicts)
+    int64_t before = 0, unused = 0, total = 0, unused_total;
+    for (int r = t * per; r < min(R, (t + 1) * per); r++) before += (cu[r + 1] - cu[r] + per_tile - 1) / per_tile;
+    block_prefix(before, unused, warp_sums, &total, &unused_total);
     for (int r = t * per; r < min(R, (t + 1) * per); r++) {
         tile0[r] = (int32_t)before;
         before += (cu[r + 1] - cu[r] + per_tile - 1) / per_tile;
     }
     if (t == 0) {
         tile0[R] = (int32_t)total;
-        warp_sums[kPlanWarps] = 1;                  // units of the longest item
+        *longest = 1;
     }
     __syncthreads();
-    const int n = (int)total;
-    const int64_t cap = s.page_size ? s.table_cols * s.page_size : 0x7fffffff;
-    int64_t units = 0;
-    for (int base = 0; base < n; base += kPlanThreads) {
-        const int i = base + t;
+    const int n = (int)total, each = ((n + kPlanThreads - 1) / kPlanThreads) | 1;
+    const int i0 = min(n, t * each), i1 = min(n, i0 + each);
+    // (32-bit from here: positions up to 2^30)
+    const int cap = (int)min(s.page_size ? s.table_cols * s.page_size : (int64_t)kMaxPosition, (int64_t)kMaxPosition);
+    const int window = (int)s.window;
+    const int r0 = i0 < i1 ? last_at_or_below(tile0, R, i0) : 0;
+    auto tile_of = [&](int i, int& r) {
+        while (tile0[r + 1] <= i) r++;           // (requests without new tokens have no QTile)
+        const int off = (i - tile0[r]) * per_tile, q_len = cu[r + 1] - cu[r];
         QTile q = {};
-        int64_t u = 0;
-        if (i < n) {
-            int lo = 0, hi = R - 1;      // the last request whose first QTile is at or before i
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (tile0[mid] <= i) lo = mid; else hi = mid - 1;
-            }
-            const int off = (i - tile0[lo]) * per_tile, q_len = cu[lo + 1] - cu[lo];
-            const int64_t ctx = lens_of(s, lo).ctx;
-            q.tok0 = cu[lo] + off;
-            q.n_tok = min(per_tile, q_len - off);
-            q.req = lo;
-            q.kv_row = cu[lo];
-            const int64_t pos0 = min(ctx + off, (int64_t)0x7fffffff - q.n_tok);
-            q.pos0 = (int32_t)pos0;
-            const int64_t end = min(min(pos0 + q.n_tok, ctx + q_len), cap);
-            const int64_t begin = s.window ? max(pos0 + 1 - s.window, (int64_t)0) : 0;
-            q.kv_end = (int32_t)end;
-            q.tile0 = (int32_t)(begin / kAttnKeys);
-            // at least one tile, so that rows that see no key are written too
-            q.tiles = (int32_t)max((end + kAttnKeys - 1) / kAttnKeys - q.tile0, (int64_t)1);
-            u = (int64_t)(kItemUnits + q.tiles) * s.kv_heads;
-            atomicMax(reinterpret_cast<unsigned long long*>(warp_sums + kPlanWarps), (unsigned long long)(kItemUnits + q.tiles));
-        }
-        int64_t sum = 0;
-        const int64_t incl = block_incl_sum(u, warp_sums, &sum);
-        if (i < n) {
-            q.unit0 = (int32_t)min(units + incl - u, kMaxUnits);
-            tiles[i] = q;
-        }
-        units += sum;
+        q.tok0 = cu[r] + off;
+        q.n_tok = min(per_tile, q_len - off);
+        q.req = r;
+        q.pos0 = min(min(ctx[r], kMaxPosition) + off, kMaxPosition);
+        const int begin = window ? max(q.pos0 + 1 - window, 0) : 0;
+        q.kv_end = min(q.pos0 + q.n_tok, cap);
+        q.tile0 = begin / kAttnKeys;
+        // at least one tile, so that rows that see no key are written too
+        q.tiles = max((q.kv_end + kAttnKeys - 1) / kAttnKeys - q.tile0, 1);
+        return q;
+    };
+    int64_t unit = 0, units = 0;
+    int most = 1;
+    for (int i = i0, r = r0; i < i1; i++) {
+        const int item = kItemUnits + tile_of(i, r).tiles;
+        unit += (int64_t)item * Hkv;
+        most = max(most, item);
     }
+    atomicMax(longest, __reduce_max_sync(0xffffffffu, most));
+    block_prefix(unit, unused, warp_sums, &units, &unused_total);   // (its barriers order *longest too)
     if (units > kMaxUnits) {
         units = kMaxUnits;
         if (t == 0) report(p.status, kStatusPlan);
     }
-    __syncthreads();
-    const int64_t share = (units + p.ctas - 1) / p.ctas;
-    const int64_t least = min((int64_t)(kItemUnits + kMinPart), warp_sums[kPlanWarps]);
-    const int64_t per_cta = share > least ? share : least;
-    if (t == 0) {
+    const int share = (int)((units + p.ctas - 1) / p.ctas);
+    const int per_cta = max(share, min(kItemUnits + kMinPart, *longest));
+    if (t == 0 && block == 0) {
         head->units = (int32_t)units;
-        head->per_cta = (int32_t)per_cta;
+        head->per_cta = per_cta;
         head->qtiles = n;
     }
-    for (int i = t; i < n; i += kPlanThreads) {     // each thread reads the entries it wrote
-        const QTile q = tiles[i];
-        const int64_t u1 = min(q.unit0 + (int64_t)(kItemUnits + q.tiles) * s.kv_heads, units);
-        for (int64_t c = (q.unit0 + per_cta - 1) / per_cta; c * per_cta < u1; c++) {
+    if (t * blocks / kPlanThreads != block) return;
+    int c = (int)((min(unit, units) + per_cta - 1) / per_cta);       // the next CTA to start
+    for (int i = i0, r = r0; i < i1; i++) {
+        QTile q = tile_of(i, r);
+        q.unit0 = (int)min(unit, units);
+        unit += (int64_t)(kItemUnits + q.tiles) * Hkv;
+        tiles[i] = q;
+        for (const int next = (int)min(unit, units); c * per_cta < next; c++) {
             head->first[c] = i;
             head->start[c] = q;
         }
     }
 }
 
-// shared memory: cu [R+1] int32 (new tokens before each request, at most
-// `tokens`), first [R+1] int32 (pages taken before each request)
+// shared memory, int32: cu [R+1] (new tokens before each request, at most
+// `tokens`), first [R+1] (pages taken before each request), ctx [R] (cached
+// tokens)
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
 {
     extern __shared__ int32_t sh[];
-    __shared__ int64_t s_sums[kPlanWarps + 1];
+    __shared__ int64_t s_sums[kPlanWarps][2];
+    __shared__ int s_longest;
     griddep_launch_dependents();
     griddep_wait();                 // the lengths may come from the previous kernel
     const nvfp4_step_t& s = p.s;
@@ -171,95 +183,88 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
     const bool paged = s.page_size != 0;
     int32_t* cu = sh;
     int32_t* first = sh + R + 1;
+    int32_t* ctx = first + R + 1;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int64_t P = paged ? s.page_size : 1, round = P - 1;
     const int sft = p.page_shift;
-
-    // prefix sums over the requests: thread t takes the requests
-    // per*t .. per*t + per - 1
-    const int per = (R + kPlanThreads - 1) / kPlanThreads;
-    int64_t sq = 0, sn = 0;
-    bool bad = false;
-    for (int j = 0; j < per; j++) {
-        const int r = t * per + j;
-        if (r >= R) break;
-        const Lens l = lens_of(s, r);
-        bad |= l.bad;
-        sq += l.q;
-        if (paged) sn += ((l.ctx + l.q + round) >> sft) - ((l.ctx + round) >> sft);
-    }
-    int64_t total_q = 0, total_n = 0;
-    int64_t bq = block_incl_sum(sq, s_sums, &total_q) - sq;
-    int64_t bn = paged ? block_incl_sum(sn, s_sums, &total_n) - sn : 0;
-    const int64_t cap = s.tokens;
-    const int64_t cursor = paged && s.cursor ? __ldg(s.cursor) : 0;
     const int64_t kIntMax = 0x7fffffff;
-    for (int j = 0; j < per; j++) {
-        const int r = t * per + j;
-        if (r >= R) break;
-        const Lens l = lens_of(s, r);
+    const int64_t cursor = paged && s.cursor ? __ldg(s.cursor) : 0;
+
+    // the lengths, negative ones as zero
+    bool bad = false;
+    for (int r = t; r < R; r += kPlanThreads) {
+        const int q = __ldg(s.q_len + r), c = s.ctx_len ? __ldg(s.ctx_len + r) : 0;
+        bad |= q < 0 || c < 0;
+        cu[r] = max(q, 0);
+        ctx[r] = max(c, 0);
+    }
+    __syncthreads();
+    // prefix sums over the requests: thread t takes the requests per*t ..
+    const int per = ((R + kPlanThreads - 1) / kPlanThreads) | 1;     // (odd: no bank conflicts)
+    auto pages_of = [&](int64_t c, int64_t q) { return ((c + q + round) >> sft) - ((c + round) >> sft); };
+    int64_t bq = 0, bn = 0, total_q = 0, total_n = 0;
+    for (int r = t * per; r < min(R, (t + 1) * per); r++) {
+        bq += cu[r];
+        if (paged) bn += pages_of(ctx[r], cu[r]);
+    }
+    block_prefix(bq, bn, s_sums, &total_q, &total_n);
+    const int64_t cap = s.tokens;
+    for (int r = t * per; r < min(R, (t + 1) * per); r++) {
+        const int q = cu[r];
         cu[r] = (int32_t)min(bq, cap);
         first[r] = (int32_t)min(bn, kIntMax);
-        bq += l.q;
-        if (paged) bn += ((l.ctx + l.q + round) >> sft) - ((l.ctx + round) >> sft);
+        bq += q;
+        if (paged) bn += pages_of(ctx[r], q);
     }
     if (t == 0) {
         cu[R] = (int32_t)min(total_q, cap);
+        first[R] = (int32_t)min(total_n, kIntMax);
         if (total_q > cap) bad = true;
     }
-    const bool scheduler = s.heads != 0 && blockIdx.x == gridDim.x - 1;   // the last block builds the schedule
     if (bad && blockIdx.x == 0) report(p.status, kStatusPlan);
     __syncthreads();
-    if (scheduler) {
-        build_schedule(p, cu, first, s_sums);
+    const int blocks = gridDim.x - p.schedulers;
+    if ((int)blockIdx.x >= blocks) {
+        build_schedule(p, cu, ctx, first, s_sums, &s_longest, blockIdx.x - blocks, p.schedulers);
         return;
     }
-    const int blocks = s.heads ? gridDim.x - 1 : gridDim.x;
     const int32_t T = cu[R];
 
-    // per-request tables: a warp per request
-    for (int r = blockIdx.x * kPlanWarps + warp; r < R; r += blocks * kPlanWarps) {
-        const Lens l = lens_of(s, r);
-        const int q = cu[r + 1] - cu[r];
-        if (lane == 0) {
-            s.cu_q[r] = cu[r];
-            if (r == R - 1) s.cu_q[R] = T;
-            s.kv_len[r] = (int32_t)min(l.ctx + q, kIntMax);
-        }
-        if (paged && s.free_pages) {
-            const int64_t have = (l.ctx + round) >> sft, need = (l.ctx + l.q + round) >> sft;
-            for (int64_t j = have + lane; j < need; j += 32) {
-                const int64_t at = cursor + first[r] + (j - have);
+    // per-request tables
+    for (int r = blockIdx.x * kPlanThreads + t; r < R; r += blocks * kPlanThreads) {
+        s.cu_q[r] = cu[r];
+        s.kv_len[r] = (int32_t)min((int64_t)ctx[r] + (cu[r + 1] - cu[r]), kIntMax);
+    }
+    if (blockIdx.x == 0 && t == 0) s.cu_q[R] = T;
+    if (paged && s.free_pages) {
+        // the pages opened, a warp per request
+        for (int r = blockIdx.x * kPlanWarps + warp; r < R; r += blocks * kPlanWarps) {
+            const int64_t have = (ctx[r] + round) >> sft, taken = first[r + 1] - first[r];
+            for (int64_t x = lane; x < taken; x += 32) {
+                const int64_t at = cursor + first[r] + x, j = have + x;
                 const bool ok = at >= 0 && at < s.free_count && j < s.table_cols;
                 if (j < s.table_cols) s.block_table[r * s.table_ld + j] = ok ? __ldg(s.free_pages + at) : -1;
                 if (!ok) report(p.status, kStatusPlan);
             }
         }
+        if (blockIdx.x == 0 && t == 0 && s.cursor_out) *s.cursor_out = (int32_t)min(cursor + total_n, kIntMax);
     }
-    if (paged && blockIdx.x == 0 && t == 0 && s.cursor_out && s.free_pages)
-        *s.cursor_out = (int32_t)min(cursor + total_n, kIntMax);
 
     // per-token tables
     for (int64_t i = (int64_t)blockIdx.x * kPlanThreads + t; i < cap; i += (int64_t)blocks * kPlanThreads) {
         int pos = 0, slot = -1;
         if (i < T) {
-            // the last request that starts at or before row i and has rows
-            int lo = 0, hi = R - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (cu[mid] <= i) lo = mid; else hi = mid - 1;
-            }
-            const int64_t ctx = lens_of(s, lo).ctx;
-            const int64_t at = ctx + (i - cu[lo]);
+            const int r = last_at_or_below(cu, R, i);     // the request that row i is of
+            const int64_t at = (int64_t)ctx[r] + (i - cu[r]);
             pos = (int)min(at, kIntMax);
             if (paged) {
-                const int64_t j = at >> sft, have = (ctx + round) >> sft;
+                const int64_t j = at >> sft, have = (ctx[r] + round) >> sft;
                 int64_t page = -1;
                 if (j < s.table_cols) {
                     if (!s.free_pages || j < have) {
-                        page = s.block_table[lo * s.table_ld + j];
+                        page = s.block_table[r * s.table_ld + j];
                     } else {
-                        const int64_t f = cursor + first[lo] + (j - have);
+                        const int64_t f = cursor + first[r] + (j - have);
                         if (f >= 0 && f < s.free_count) page = __ldg(s.free_pages + f);
                     }
                 }
@@ -341,14 +346,14 @@ int log2_of(int64_t v)
 
 cudaError_t launch_attn_plan(const nvfp4_step_t& step, int* status, int num_sms, cudaStream_t stream)
 {
-    const size_t smem = (size_t)(step.requests + 1) * 8;
+    const size_t smem = (size_t)(step.requests + 1) * 12;
     static int attr_set_for_device[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 64 && !attr_set_for_device[dev]) {
         e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)((kStepMaxRequests + 1) * 8));
+                                 (int)((kStepMaxRequests + 1) * 12));
         if (e != cudaSuccess) return e;
         attr_set_for_device[dev] = 1;
     }
@@ -360,7 +365,12 @@ cudaError_t launch_attn_plan(const nvfp4_step_t& step, int* status, int num_sms,
     const int64_t by_requests = (step.requests + kPlanWarps - 1) / kPlanWarps;
     int64_t grid = by_tokens > by_requests ? by_tokens : by_requests;
     if (grid > num_sms) grid = num_sms;
-    if (step.heads) grid++;
+    p.schedulers = 0;
+    if (step.heads) {
+        const int64_t n = max_qtiles(step.requests, step.tokens, step.heads / step.kv_heads) / kPlanThreads;
+        p.schedulers = (int)(n < 1 ? 1 : n > 16 ? 16 : n);
+        grid += p.schedulers;
+    }
     p.ctas = num_sms < kAttnMaxCtas ? num_sms : kAttnMaxCtas;
     return launch_programmatic(plan_kernel, dim3((unsigned)grid), dim3(kPlanThreads), smem, stream, p);
 }
