@@ -163,8 +163,9 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:               # the current stream's handle, without a Stream object around it (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _bf16_2d(x: torch.Tensor, name: str):
@@ -363,19 +364,24 @@ def nvfp4_gemm_experts(A: NVFP4Tensor, W: NVFP4Tensor, num_experts: int, ids: to
 
 
 # ------------------------------------------------ attention over a KV cache
+# (The calls of a decode step cost the host more than the GPU: these functions
+# look at what they are given once and build nothing that they can do without.)
 def _i32(t, n, name):
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+    if t.dtype is not _I32 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of at least {n} elements")
     return t.data_ptr()
 
 
-def _heads_3d(x: torch.Tensor, name: str, tokens: int, heads: int, head_dim: int | None = None):
+_BF16, _I32 = torch.bfloat16, torch.int32
+
+
+def _heads_3d(x: torch.Tensor, name: str, tokens: int, heads: int, head_dim: int):
     """(address, row pitch, head pitch) of bf16 [tokens, heads, head_dim] with unit column stride."""
-    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.stride(2) != 1 or not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA bf16 [tokens, heads, head_dim] tensor with unit column stride")
-    if x.shape[0] != tokens or x.shape[1] != heads or (head_dim is not None and x.shape[2] != head_dim):
-        raise ValueError(f"{name} is {tuple(x.shape)}, not ({tokens}, {heads}, {head_dim})")
-    return x.data_ptr(), x.stride(0), x.stride(1)
+    st = x.stride()
+    if x.dtype is not _BF16 or x.shape != (tokens, heads, head_dim) or st[2] != 1 or not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA bf16 [{tokens}, {heads}, {head_dim}] tensor with unit column stride, "
+                         f"not {x.dtype} {tuple(x.shape)} on {x.device}")
+    return x.data_ptr(), st[0], st[1]
 
 
 def attn_schedule_bytes(requests: int, tokens: int, heads: int, kv_heads: int) -> int:
@@ -468,7 +474,7 @@ def nvfp4_attn_plan(plan: AttnPlan, q_len: torch.Tensor, ctx_len=None, free_page
     else:
         c.free_pages, c.free_count = None, 0
     c.cursor = None if cursor is None else _i32(cursor, 1, "cursor")
-    _check(lib().nvfp4_attn_plan(ctypes.byref(c), _stream(stream)), "nvfp4_attn_plan")
+    _check((_lib or lib()).nvfp4_attn_plan(ctypes.byref(c), _stream(stream)), "nvfp4_attn_plan")
 
 
 def nvfp4_kv_append(k: torch.Tensor, v: torch.Tensor, plan: AttnPlan, cache: KVCache, stream=None):
@@ -478,17 +484,20 @@ def nvfp4_kv_append(k: torch.Tensor, v: torch.Tensor, plan: AttnPlan, cache: KVC
         raise ValueError("the plan has no paged cache (page_size 0)")
     kp = _heads_3d(k, "k", plan.tokens, cache.kv_heads, cache.head_dim)
     vp = _heads_3d(v, "v", plan.tokens, cache.kv_heads, cache.head_dim)
-    _check(lib().nvfp4_kv_append(*kp, *vp, plan.slot.data_ptr(), plan.tokens, ctypes.byref(cache._c),
+    _check((_lib or lib()).nvfp4_kv_append(*kp, *vp, plan.slot.data_ptr(), plan.tokens, ctypes.byref(cache._c),
                                  _stream(stream)), "nvfp4_kv_append")
 
 
 def _attn_io(plan: AttnPlan, q: torch.Tensor, out: torch.Tensor, scale, lse) -> _AttnIOC:
-    d = q.shape[-1]
-    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or not lse.is_cuda or
-                            lse.numel() != plan.tokens * plan.heads):
+    d, tokens, heads = q.shape[-1], plan.tokens, plan.heads
+    if lse is None:
+        at = None
+    elif lse.dtype is torch.float32 and lse.is_contiguous() and lse.is_cuda and lse.numel() == tokens * heads:
+        at = lse.data_ptr()
+    else:
         raise ValueError("lse must be a contiguous CUDA float32 [tokens, heads] tensor")
-    return _AttnIOC(*_heads_3d(q, "q", plan.tokens, plan.heads, d), *_heads_3d(out, "out", plan.tokens, plan.heads, d),
-                    None if lse is None else lse.data_ptr(), d, d ** -0.5 if scale is None else scale)
+    return _AttnIOC(*_heads_3d(q, "q", tokens, heads, d), *_heads_3d(out, "out", tokens, heads, d), at, d,
+                    d ** -0.5 if scale is None else scale)
 
 
 def nvfp4_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: AttnPlan, out: torch.Tensor,
@@ -500,7 +509,7 @@ def nvfp4_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: A
     io = _attn_io(plan, q, out, scale, lse)
     kp = _heads_3d(k, "k", plan.tokens, plan.kv_heads, q.shape[2])
     vp = _heads_3d(v, "v", plan.tokens, plan.kv_heads, q.shape[2])
-    _check(lib().nvfp4_attn_prompt(ctypes.byref(plan._c), ctypes.byref(io), *kp, *vp, ws.data_ptr(),
+    _check((_lib or lib()).nvfp4_attn_prompt(ctypes.byref(plan._c), ctypes.byref(io), *kp, *vp, ws.data_ptr(),
                                    ws.numel() * ws.element_size(), _stream(stream)), "nvfp4_attn_prompt")
 
 
@@ -509,5 +518,5 @@ def nvfp4_attn_paged(q: torch.Tensor, cache: KVCache, plan: AttnPlan, out: torch
     """Attention of a step's new tokens over the paged cache, which holds
     their K and V already.  The rest as :func:`nvfp4_attn_prompt`."""
     io = _attn_io(plan, q, out, scale, lse)
-    _check(lib().nvfp4_attn_paged(ctypes.byref(plan._c), ctypes.byref(io), ctypes.byref(cache._c), ws.data_ptr(),
+    _check((_lib or lib()).nvfp4_attn_paged(ctypes.byref(plan._c), ctypes.byref(io), ctypes.byref(cache._c), ws.data_ptr(),
                                   ws.numel() * ws.element_size(), _stream(stream)), "nvfp4_attn_paged")

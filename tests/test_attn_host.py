@@ -128,6 +128,6 @@ def test_binding_checks_its_tensors(nv):
         nv.KVCache(torch.zeros(2, 2, 16, 64), torch.zeros(2, 2, 16, 64))
     x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
-        nv._heads_3d(x, "x", 4, 2)                  # not a CUDA tensor
+        nv._heads_3d(x, "x", 4, 2, 64)                  # not a CUDA tensor
     with pytest.raises(ValueError):
         nv._i32(torch.zeros(3, dtype=torch.int64), 3, "n")
