@@ -735,8 +735,8 @@ struct AttnKV {
 int make_rows_map(CUtensorMap* m, const void* base, int rank, const int64_t* dims, const int64_t* strides,
                   const int* box)
 {
-    cuuint64_t d[4], st[3];
-    cuuint32_t b[4], es[4] = {1, 1, 1, 1};
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], es[5] = {1, 1, 1, 1, 1};
     for (int i = 0; i < rank; i++) {
         d[i] = (cuuint64_t)dims[i];
         b[i] = (cuuint32_t)box[i];
@@ -765,7 +765,14 @@ int run_attn(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const AttnKV& 
         const int box[3] = {64, group, row_tile_tokens(group)};
         NVFP4_TRY(make_rows_map(&mq, io->q, 3, dims, st, box));
     }
-    if (kv.cache) {
+    const bool fold = kv.cache && kv.cache->page_size == 16 && D == 128;
+    if (fold) {
+        const nvfp4_kv_cache_t& c = *kv.cache;
+        const int64_t dims[5] = {64, 16, 2, c.kv_heads, c.pages}, st[4] = {D, 64, 16 * D, c.page_stride};
+        const int box[5] = {64, 16, 2, 1, 1};
+        NVFP4_TRY(make_rows_map(&mk, kv.k, 5, dims, st, box));
+        NVFP4_TRY(make_rows_map(&mv, kv.v, 5, dims, st, box));
+    } else if (kv.cache) {
         const nvfp4_kv_cache_t& c = *kv.cache;
         const int64_t dims[4] = {D, c.page_size, c.kv_heads, c.pages};
         const int64_t st[3] = {D, c.page_size * D, c.page_stride};
@@ -795,6 +802,7 @@ int run_attn(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const AttnKV& 
         a.block_table = step->block_table;
         a.table_ld = step->table_ld;
         a.page_size = (int)kv.cache->page_size;
+        a.fold = fold ? 1 : 0;
     }
     a.tickets = static_cast<int*>(workspace);
     a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttnTicketBytes);

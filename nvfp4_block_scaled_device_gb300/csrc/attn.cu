@@ -85,6 +85,23 @@ struct Cfg {
     static_assert(kStages <= kMaxStages, "barriers");
 };
 
+// How a tile of keys or values lies in its 128-row stage.  The usual layout:
+// 64-column halves 16 KB apart, rows in order; a step is 64 rows in a row.
+// kFold, for pages of 16 rows of 128 columns: a page's both halves in one copy,
+// [page][half][16 rows][64 columns], as a copy costs about 60 cycles beside 4
+// per 128 bytes and two copies of 2 KB a page keep HBM waiting.  Step h is then
+// the eight rows 8h .. 8h + 7 of each page: 8-row groups at one distance, which
+// is all that a descriptor can say.
+template <bool kFold>
+struct Layout {
+    static constexpr uint32_t kHalf = kFold ? 2048 : 16384;       // bytes between 64-column halves,
+    static constexpr uint32_t kGroup = kFold ? 4096 : 1024;       // a step's 8-row groups,
+    static constexpr uint32_t kStepAt = kFold ? 1024 : 8192;      // a tile's two steps
+    __device__ static uint32_t row(int r) { return kFold ? (uint32_t)(r >> 4) * 4096u + (r & 15) * 128u : r * 128u; }
+    // First key of 8-key group g of step h (from its tile's first key).
+    __device__ static int key(int h, int g) { return kFold ? 16 * g + 8 * h : kStep * h + 8 * g; }
+};
+
 template <int kValue>
 struct Int {
     static constexpr int value = kValue;
@@ -108,68 +125,72 @@ __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_n_major)
 // converged warp from a single asm block (see stage_issue_1sm), and what its
 // completion signals.
 // S = Q K^T (N = 64 keys): operands as 128-byte swizzled rows, K-major; K = 16
-// columns an MMA, 64-column halves 16 KB apart.
-template <int kDP>
-__device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q_lo, uint32_t k_lo, uint32_t hi, uint32_t idesc,
-                                         uint32_t bar)
+// columns an MMA, Q's 64-column halves 16 KB apart, K's kHalf bytes.
+template <int kDP, uint32_t kHalf>
+__device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q_lo, uint32_t q_hi, uint32_t k_lo, uint32_t k_hi,
+                                         uint32_t idesc, uint32_t bar)
 {
+    constexpr uint32_t kB = kHalf >> 4;
     if (kDP == 128)
         asm volatile(
         "{\n .reg .pred e, pf, pt;\n .reg .b32 r, x, y;\n .reg .b64 da, db;\n"
         " elect.sync r|e, 0xffffffff;\n setp.eq.b32 pt, 0, 0;\n setp.ne.b32 pf, 0, 0;\n"
-        " add.u32 x, %1, 0; add.u32 y, %2, 0; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " add.u32 x, %1, 0; add.u32 y, %2, 0; mov.b64 da, {x, %3}; mov.b64 db, {y, %6};\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pf;\n"
-        " add.u32 x, %1, 2; add.u32 y, %2, 2; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " add.u32 x, %1, 2; add.u32 y, %2, 2; mov.b64 da, {x, %3}; mov.b64 db, {y, %6};\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
-        " add.u32 x, %1, 4; add.u32 y, %2, 4; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " add.u32 x, %1, 4; add.u32 y, %2, 4; mov.b64 da, {x, %3}; mov.b64 db, {y, %6};\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
-        " add.u32 x, %1, 6; add.u32 y, %2, 6; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " add.u32 x, %1, 6; add.u32 y, %2, 6; mov.b64 da, {x, %3}; mov.b64 db, {y, %6};\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
-        " add.u32 x, %1, 1024; add.u32 y, %2, 1024; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " add.u32 x, %1, 1024; add.u32 y, %2, %7; mov.b64 da, {x, %3}; mov.b64 db, {y, %6};\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
-        " add.u32 x, %1, 1026; add.u32 y, %2, 1026; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " add.u32 x, %1, 1026; add.u32 y, %2, %8; mov.b64 da, {x, %3}; mov.b64 db, {y, %6};\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
-        " add.u32 x, %1, 1028; add.u32 y, %2, 1028; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " add.u32 x, %1, 1028; add.u32 y, %2, %9; mov.b64 da, {x, %3}; mov.b64 db, {y, %6};\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
-        " add.u32 x, %1, 1030; add.u32 y, %2, 1030; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " add.u32 x, %1, 1030; add.u32 y, %2, %10; mov.b64 da, {x, %3}; mov.b64 db, {y, %6};\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
         " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n"
-        "}\n" ::"r"(s), "r"(q_lo), "r"(k_lo), "r"(hi), "r"(idesc), "r"(bar)
+        "}\n" ::"r"(s), "r"(q_lo), "r"(k_lo), "r"(q_hi), "r"(idesc), "r"(bar), "r"(k_hi),
+        "n"(kB), "n"(kB + 2), "n"(kB + 4), "n"(kB + 6)
         : "memory");
     else
         asm volatile(
         "{\n .reg .pred e, pf, pt;\n .reg .b32 r, x, y;\n .reg .b64 da, db;\n"
         " elect.sync r|e, 0xffffffff;\n setp.eq.b32 pt, 0, 0;\n setp.ne.b32 pf, 0, 0;\n"
-        " add.u32 x, %1, 0; add.u32 y, %2, 0; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " add.u32 x, %1, 0; add.u32 y, %2, 0; mov.b64 da, {x, %3}; mov.b64 db, {y, %6};\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pf;\n"
-        " add.u32 x, %1, 2; add.u32 y, %2, 2; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " add.u32 x, %1, 2; add.u32 y, %2, 2; mov.b64 da, {x, %3}; mov.b64 db, {y, %6};\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
-        " add.u32 x, %1, 4; add.u32 y, %2, 4; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " add.u32 x, %1, 4; add.u32 y, %2, 4; mov.b64 da, {x, %3}; mov.b64 db, {y, %6};\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
-        " add.u32 x, %1, 6; add.u32 y, %2, 6; mov.b64 da, {x, %3}; mov.b64 db, {y, %3};\n"
+        " add.u32 x, %1, 6; add.u32 y, %2, 6; mov.b64 da, {x, %3}; mov.b64 db, {y, %6};\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, pt;\n"
         " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n"
-        "}\n" ::"r"(s), "r"(q_lo), "r"(k_lo), "r"(hi), "r"(idesc), "r"(bar)
+        "}\n" ::"r"(s), "r"(q_lo), "r"(k_lo), "r"(q_hi), "r"(idesc), "r"(bar), "r"(k_hi)
         : "memory");
 }
 // O += P V over 64 keys: P in tensor memory (8 columns for 16 keys), V as
 // stored (N-major; 16 keys are 2 KB).
+template <uint32_t kGroup>
 __device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint32_t v_lo, uint32_t hi, uint32_t idesc,
                                          uint32_t acc, uint32_t bar)
 {
+    constexpr uint32_t kMma = 2 * kGroup >> 4;       // 16 keys on
     asm volatile(
         "{\n .reg .pred e, p, pt;\n .reg .b32 r, x, y;\n .reg .b64 db;\n"
         " elect.sync r|e, 0xffffffff;\n setp.eq.b32 pt, 0, 0;\n setp.ne.b32 p, %5, 0;\n"
         " add.u32 x, %2, 0; mov.b64 db, {x, %3}; add.u32 y, %1, 0;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, p;\n"
-        " add.u32 x, %2, 128; mov.b64 db, {x, %3}; add.u32 y, %1, 8;\n"
+        " add.u32 x, %2, %7; mov.b64 db, {x, %3}; add.u32 y, %1, 8;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
-        " add.u32 x, %2, 256; mov.b64 db, {x, %3}; add.u32 y, %1, 16;\n"
+        " add.u32 x, %2, %8; mov.b64 db, {x, %3}; add.u32 y, %1, 16;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
-        " add.u32 x, %2, 384; mov.b64 db, {x, %3}; add.u32 y, %1, 24;\n"
+        " add.u32 x, %2, %9; mov.b64 db, {x, %3}; add.u32 y, %1, 24;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], db, %4, pt;\n"
         " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n"
-        "}\n" ::"r"(o), "r"(p), "r"(v_lo), "r"(hi), "r"(idesc), "r"(acc), "r"(bar)
+        "}\n" ::"r"(o), "r"(p), "r"(v_lo), "r"(hi), "r"(idesc), "r"(acc), "r"(bar), "n"(kMma), "n"(2 * kMma), "n"(3 * kMma)
         : "memory");
 }
 
@@ -202,6 +223,16 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
         "[%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                            int w, int v)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
         : "memory");
 }
 
@@ -348,13 +379,26 @@ __device__ __forceinline__ bool test_use(const volatile uint32_t* issued, uint32
 
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
-// What is done to a row's scores of a step in tensor memory before the softmax reads
-// them: the sign of a negative scale, -inf at keys outside lw .. h - 1.
-__device__ __forceinline__ void edit_scores(uint32_t taddr, bool negate, int h, int lw)
+// What is done to a row's scores of step h of a key tile in tensor memory before
+// the softmax reads them: the sign of a negative scale, -inf at keys outside
+// lo .. hi - 1 (from the tile's first key).
+template <bool kFold>
+__device__ __forceinline__ void edit_scores(uint32_t taddr, bool negate, int h, int lo, int hi)
 {
 #pragma unroll 1
     for (int x = 0; x < kStep; x += 32) {
-        const uint32_t seen = low_bits(h - x) & ~low_bits(lw - x);
+        uint32_t seen;
+        if (kFold) {
+            seen = 0;
+#pragma unroll 1
+            for (int g = 0; g < 4; g++) {
+                const int key = Layout<true>::key(h, x / 8 + g);
+                seen |= ((low_bits(hi - key) & ~low_bits(lo - key)) & 0xffu) << (8 * g);
+            }
+        } else {
+            const int key = kStep * h + x;
+            seen = low_bits(hi - key) & ~low_bits(lo - key);
+        }
         if (!negate && __all_sync(0xffffffffu, seen == ~0u)) continue;
         float s[32];
         tmem_ld32(taddr + x, s);
@@ -503,10 +547,11 @@ __device__ __forceinline__ uint32_t stage_of(uint32_t use, uint32_t* parity)
     return use - turn * kStages;
 }
 
-template <int kDP>
+template <int kDP, bool kFold>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ Params prm)
 {
     using C = Cfg<kDP>;
+    using L = Layout<kFold>;
     constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -604,7 +649,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                             mbar_arrive(smem_u32(&ctrl->kv_empty[s]));
                     }
                     __syncwarp();
-                    if (paged) {
+                    if (kFold) {
+                        const int id = __shfl_sync(0xffffffffu, page, lane & 7);
+                        if (lane < pages) tma_load_5d(dst + lane * 4096, map, bar, 0, 0, 0, p.hk, id);
+                    } else if (paged) {
                         // box b: half b / ppt of page b % ppt (at most 16)
                         const int b = lane, half = b / ppt, pg = b - half * ppt;
                         const int id = __shfl_sync(0xffffffffu, page, pg);
@@ -668,10 +716,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 }
                 ends ^= 1u << s;
                 uint8_t* v = smem + C::kOffRing + s * C::kTileBytes;
-                const int vec = (kAttnKeys - valid) * 8;          // 16-byte vectors of a half's rows
-                for (int x = lane; x < vec * C::kHalves; x += 32) {
-                    const int half = x / vec, y = x - half * vec;
-                    *reinterpret_cast<uint4*>(v + half * 16384 + valid * 128 + y * 16) = make_uint4(0, 0, 0, 0);
+                // four rows at a time, eight lanes to a row (the item's last
+                // product waits for this)
+                for (int r = valid + (lane >> 3); r < kAttnKeys; r += 4) {
+                    uint8_t* at = v + L::row(r) + (lane & 7) * 16;
+#pragma unroll
+                    for (int half = 0; half < C::kHalves; half++)
+                        *reinterpret_cast<uint4*>(at + half * L::kHalf) = make_uint4(0, 0, 0, 0);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -688,14 +739,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             // j + 2, ... (a stage is free after two arrivals: both warps', or
             // the one warp's and the copying warp's own).
             const int j = warp - kWarpMma;
-            const uint64_t kdesc0 = make_smem_desc(base, 16, 1024, 2);       // K-major: 8-row groups 1 KB apart
-            const uint64_t vdesc0 = make_smem_desc(base, 16384, 1024, 2);    // N-major: 64-column halves 16 KB
-                                                                             // apart, 8-key groups 1 KB apart
+            const uint64_t qdesc0 = make_smem_desc(base, 16, 1024, 2);                  // K-major
+            const uint64_t kdesc0 = make_smem_desc(base, 16, L::kGroup, 2);             // K-major
+            const uint64_t vdesc0 = make_smem_desc(base, L::kHalf, L::kGroup, 2);       // N-major
             constexpr uint32_t kIdescS = idesc_of(kStep, false), kIdescO = idesc_of(kDP, true);
-            constexpr uint32_t kStepDesc = kStep * 128 >> 4;                 // 64 rows on
-            const uint32_t k_hi = (uint32_t)(kdesc0 >> 32), v_hi = (uint32_t)(vdesc0 >> 32);
-            const uint32_t q_lo = (uint32_t)kdesc0;
-            const uint32_t ring_k = q_lo + (C::kOffRing >> 4), ring_v = (uint32_t)vdesc0 + (C::kOffRing >> 4);
+            constexpr uint32_t kStepDesc = L::kStepAt >> 4;
+            const uint32_t q_hi = (uint32_t)(qdesc0 >> 32), k_hi = (uint32_t)(kdesc0 >> 32), v_hi = (uint32_t)(vdesc0 >> 32);
+            const uint32_t q_lo = (uint32_t)qdesc0;
+            const uint32_t ring_k = (uint32_t)kdesc0 + (C::kOffRing >> 4), ring_v = (uint32_t)vdesc0 + (C::kOffRing >> 4);
             const uint32_t full0 = smem_u32(&ctrl->kv_full[0]), empty0 = smem_u32(&ctrl->kv_empty[0]);
             const uint32_t ts = tmem + kColS + 128u * j, to = tmem + kColO + 128u * j;
             const uint32_t s_full = smem_u32(&ctrl->s_full[j][0]), o_full = smem_u32(&ctrl->o_full[j][0]);
@@ -708,7 +759,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             // use of their V, and 4 bits each: second half of a tile, first
             // of its item
             uint32_t pend = 0, pend_use[2] = {0, 0};
-            bool ok = true;
             auto issue_o = [&]() {
                 const uint32_t d = pend & 15u, vu = pend_use[0], buf = o_cnt & 1u;
                 uint32_t vph;
@@ -718,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 if (!(d & 1u) && !wait_use(&ctrl->issued, vu, full0 + 8u * vs, vph, abort_flag, status, 46)) return false;
                 if (!wait_on(p_full + 8u * buf, (o_cnt >> 1) & 1u, abort_flag, status, 48)) return false;
                 tc_fence_after();
-                issue_pv(to, ts + 64u * buf, ring_v + vs * (C::kTileBytes >> 4) + (d & 1u) * kStepDesc, v_hi, kIdescO,
+                issue_pv<L::kGroup>(to, ts + 64u * buf, ring_v + vs * (C::kTileBytes >> 4) + (d & 1u) * kStepDesc, v_hi, kIdescO,
                          (d & 2u) ^ 2u, o_full + 8u * buf);
                 if (d & 1u) mma_commit_warp(empty0 + 8u * vs);
                 o_cnt++;
@@ -726,53 +776,78 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 pend_use[0] = pend_use[1];
                 return true;
             };
-            while (ok && pieces.next(p)) {
-                int first, end;
-                p.range(j, row_tile_tokens(a.group), a.window, first, end);
-                const int by = p.two ? 1 : 2;
-                if (!p.two) first = j;
-                const uint32_t qt = q_lo + (p.two && j ? C::kTileBytes >> 4 : 0);
-                while (ok && s_cnt != o_cnt && !mbar_test_warp(q_full, qph)) ok = issue_o();
-                if (!ok || !wait_on(q_full, qph, abort_flag, status, 44)) {
-                    ok = false;
-                    break;
+            // One loop with one copy of each product (what is issued next is
+            // data: with the loops written out the MMA warps' code was 44 KB).
+            bool have = false, last = false, fresh = false;   // a step to come, no more items, an item's first step
+            int i = 0, end = 0, by = 1, h = 0, n = 0;         // the step: half h of key tile i; the item's tiles
+            uint32_t qt = 0;
+            int64_t idle_from = 0;
+            for (;;) {
+                if (!have && !last) {                         // the next item
+                    use += 2u * (uint32_t)n;
+                    if (pieces.next(p)) {
+                        p.range(j, row_tile_tokens(a.group), a.window, i, end);
+                        by = p.two ? 1 : 2;
+                        if (!p.two) i = j;
+                        n = p.n;
+                        qt = q_lo + (p.two && j ? C::kTileBytes >> 4 : 0);
+                        have = fresh = true;
+                    } else {
+                        last = true;
+                    }
                 }
-                qph ^= 1u;
-                if (first >= end) {                // no tile for this warp
-                    if (lane == 0) mbar_arrive(q_empty);
-                    __syncwarp();
+                const uint32_t ku = use + use_of_k(i);
+                uint32_t kph;
+                const uint32_t ks = stage_of<kStages>(ku, &kph);
+                bool go = have && s_cnt - o_cnt < 2u;
+                if (go && fresh && h == 0) {
+                    go = mbar_test_warp(q_full, qph);
+                    if (go && i >= end) {                     // no tile for this warp
+                        mbar_arrive_warp(q_empty, lane);
+                        qph ^= 1u;
+                        have = false;
+                        continue;
+                    }
                 }
-                for (int i = first; i < end && ok; i += by) {
-                    const uint32_t ku = use + use_of_k(i), vu = use + use_of_v(i, p.n);
-                    uint32_t kph;
-                    const uint32_t ks = stage_of<kStages>(ku, &kph), kb = full0 + 8u * ks;
-                    while (ok && s_cnt != o_cnt && !test_use(&ctrl->issued, ku, kb, kph)) ok = issue_o();
-                    if (!ok || !wait_use(&ctrl->issued, ku, kb, kph, abort_flag, status, 45)) {
-                        ok = false;
+                if (go && h == 0) go = test_use(&ctrl->issued, ku, full0 + 8u * ks, kph);
+                if (go) {
+                    idle_from = 0;
+                    const uint32_t buf = s_cnt & 1u;
+                    tc_fence_after();
+                    issue_qk<kDP, L::kHalf>(ts + 64u * buf, qt, q_hi, ring_k + ks * (C::kTileBytes >> 4) + h * kStepDesc,
+                                            k_hi, kIdescS, s_full + 8u * buf);
+                    const uint32_t d = (uint32_t)h | (fresh ? 2u : 0u);
+                    const bool one = s_cnt != o_cnt;          // one step is pending already
+                    pend |= d << (one ? 4 : 0);
+                    if (one) pend_use[1] = use + use_of_v(i, n);
+                    else pend_use[0] = use + use_of_v(i, n);
+                    s_cnt++;
+                    if (fresh) qph ^= 1u;
+                    fresh = false;
+                    if (h) {
+                        mma_commit_warp(empty0 + 8u * ks);
+                        i += by;
+                        if (i >= end) {
+                            mma_commit_warp(q_empty);
+                            have = false;
+                        }
+                    }
+                    h ^= 1;
+                } else if (s_cnt != o_cnt) {
+                    if (!issue_o()) break;
+                } else {
+                    if (!have) break;                         // all done
+                    // nothing to do until keys arrive
+                    const int64_t now = clock64();
+                    if (idle_from == 0) idle_from = now;
+                    const bool late = now - idle_from > (int64_t)kWaitLimitCycles;
+                    if (__any_sync(0xffffffffu, late || *abort_flag)) {
+                        if (late && *abort_flag == 0) atomicCAS(status, 0, kErrTimeout * 100 + 45);
+                        *abort_flag = 1;
                         break;
                     }
-                    for (int h = 0; h < 2; h++) {
-                        if (s_cnt - o_cnt == 2u && !(ok = issue_o())) break;
-                        const uint32_t buf = s_cnt & 1u;
-                        tc_fence_after();
-                        issue_qk<kDP>(ts + 64u * buf, qt, ring_k + ks * (C::kTileBytes >> 4) + h * kStepDesc, k_hi, kIdescS,
-                                      s_full + 8u * buf);
-                        
-                        if (h) {
-                            mma_commit_warp(empty0 + 8u * ks);
-                            if (i + by >= end) mma_commit_warp(q_empty);
-                        }
-                        const uint32_t d = (uint32_t)h | (i == first && h == 0 ? 2u : 0u);
-                        const bool one = s_cnt != o_cnt;       // one step is pending already
-                        pend |= d << (one ? 4 : 0);
-                        if (one) pend_use[1] = vu;
-                        else pend_use[0] = vu;
-                        s_cnt++;
-                    }
                 }
-                use += 2u * (uint32_t)p.n;
             }
-            while (ok && s_cnt != o_cnt) ok = issue_o();
             // every MMA issued has completed before teardown
             mma_commit_warp(smem_u32(&ctrl->teardown));
             if (lane == 0) mbar_wait_teardown(smem_u32(&ctrl->teardown), 0);
@@ -822,9 +897,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 }
                 if (any) {
                     tc_fence_after();
-                    const int key0 = p.tile0 * kAttnKeys + 2 * first * kStep + x * kStep;
-                    if (negate || hi_all < key0 + kStep || lo_all > key0)
-                        edit_scores(ts + 64 * buf, negate, hi - key0, lo - key0);
+                    // the tile's first key; keys that the step reaches from there
+                    const int h = x & 1, key0 = p.tile0 * kAttnKeys + 2 * first * kStep + (x - h) * kStep;
+                    if (negate || hi_all < key0 + L::key(h, 7) + 8 || lo_all > key0 + L::key(h, 0))
+                        edit_scores<kFold>(ts + 64 * buf, negate, h, lo - key0, hi - key0);
                     float s[kStep];
                     uint32_t r[32];
                     float mc, sum;
@@ -1080,7 +1156,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
 }
 
-template <int kDP>
+template <int kDP, bool kFold>
 cudaError_t launch(const Params& p, int num_sms, cudaStream_t stream)
 {
     static int attr_set_for_device[64] = {0};
@@ -1088,11 +1164,11 @@ cudaError_t launch(const Params& p, int num_sms, cudaStream_t stream)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 64 && !attr_set_for_device[dev]) {
-        e = cudaFuncSetAttribute(attn_kernel<kDP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<kDP>::kSmemBytes);
+        e = cudaFuncSetAttribute(attn_kernel<kDP, kFold>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<kDP>::kSmemBytes);
         if (e != cudaSuccess) return e;
         attr_set_for_device[dev] = 1;
     }
-    return launch_programmatic(attn_kernel<kDP>, dim3((unsigned)num_sms), dim3(kThreads), Cfg<kDP>::kSmemBytes, stream,
+    return launch_programmatic(attn_kernel<kDP, kFold>, dim3((unsigned)num_sms), dim3(kThreads), Cfg<kDP>::kSmemBytes, stream,
                                p);
 }
 
@@ -1107,7 +1183,8 @@ cudaError_t launch_attn(const CUtensorMap& map_q, const CUtensorMap& map_k, cons
     p.map_v = map_v;
     p.a = args;
     const int ctas = num_sms < kAttnMaxCtas ? num_sms : kAttnMaxCtas;
-    return args.head_dim > 64 ? launch<128>(p, ctas, stream) : launch<64>(p, ctas, stream);
+    if (args.fold) return launch<128, true>(p, ctas, stream);
+    return args.head_dim > 64 ? launch<128, false>(p, ctas, stream) : launch<64, false>(p, ctas, stream);
 }
 
 }  // namespace nvfp4

@@ -104,6 +104,7 @@ struct AttnArgs {
     const int32_t* block_table;
     int64_t table_ld;
     int page_size;
+    int fold;            // pages of 16 rows of 128 columns: copied whole
     int* tickets;
     float* partials;
     int* status;
@@ -111,8 +112,9 @@ struct AttnArgs {
 
 // map_q: [head_dim, heads, tokens], boxes {64, group, tokens of a row tile};
 // map_k, map_v: packed [head_dim, kv_heads, tokens], boxes {64, 1, 128}, or
-// the cache [head_dim, page_size, kv_heads, pages], boxes {64, page_size, 1, 1};
-// all with 128-byte swizzle.
+// the cache [head_dim, page_size, kv_heads, pages], boxes {64, page_size, 1, 1}, or
+// (args.fold) [64, 16, 2 halves, kv_heads, pages], boxes {64, 16, 2, 1, 1}; all with
+// 128-byte swizzle.
 cudaError_t launch_attn(const CUtensorMap& map_q, const CUtensorMap& map_k, const CUtensorMap& map_v,
                         const AttnArgs& args, int num_sms, cudaStream_t stream);
 
