@@ -205,7 +205,14 @@ __device__ __forceinline__ void mbar_arrive_warp(uint32_t bar, int lane)
 // One poll, without waiting (warp-uniform).
 __device__ __forceinline__ bool mbar_test_warp(uint32_t bar, uint32_t parity)
 {
-    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n vote.sync.all.pred p, p, 0xffffffff;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z)
@@ -370,11 +377,6 @@ __device__ __forceinline__ bool wait_use(const volatile uint32_t* issued, uint32
         }
     }
     return wait_on(bar, parity, abort_flag, status, site);
-}
-
-__device__ __forceinline__ bool test_use(const volatile uint32_t* issued, uint32_t use, uint32_t bar, uint32_t parity)
-{
-    return !__any_sync(0xffffffffu, (int32_t)(*issued - use) <= 0) && mbar_test_warp(bar, parity);
 }
 
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
@@ -754,100 +756,106 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             const uint32_t q_full = smem_u32(&ctrl->q_full), q_empty = smem_u32(&ctrl->q_empty);
             uint32_t use = 0;                      // stages used by the items before
             uint32_t qph = 0, oph = 1;             // phases: Q, O free (nothing to wait for at first)
-            uint32_t s_cnt = 0, o_cnt = 0;         // steps whose S, whose P V have gone out
-            // the steps in between (at most two, the oldest first): the ring
-            // use of their V, and 4 bits each: second half of a tile, first
-            // of its item
-            uint32_t pend = 0, pend_use[2] = {0, 0};
-            auto issue_o = [&]() {
-                const uint32_t d = pend & 15u, vu = pend_use[0], buf = o_cnt & 1u;
-                uint32_t vph;
-                const uint32_t vs = stage_of<kStages>(vu, &vph);
-                if ((d & 2u) && !wait_on(o_free, oph, abort_flag, status, 47)) return false;   // read by its last item
-                if (d & 2u) oph ^= 1u;
-                if (!(d & 1u) && !wait_use(&ctrl->issued, vu, full0 + 8u * vs, vph, abort_flag, status, 46)) return false;
-                if (!wait_on(p_full + 8u * buf, (o_cnt >> 1) & 1u, abort_flag, status, 48)) return false;
+            // A key tile's two steps use the first and the second half of S (and
+            // of everything that alternates).  What lies between a tile's last
+            // product and the next tile's first is on the path that bounds
+            // long prompts (the tensor pipe is idle there): the keys' and
+            // values' barriers are looked at while the products before run.
+            bool pend = false;                     // the last tile's P V are still to be issued:
+            uint32_t v_use = 0, v_st = 0, v_ph = 0, v_first = 0;   // V's use, stage, phase; the item's first tile
+            bool v_ok = false;                     // V was there
+            uint32_t tph = 0, t_cnt = 0;           // the phase of the last tile's barriers; tiles
+            uint32_t safe = 0;                     // uses from here on follow one of their stage that this warp has waited for
+            auto there = [&](uint32_t u, uint32_t st, uint32_t ph) {
+                if ((int32_t)(u - safe) < 0 && __any_sync(0xffffffffu, (int32_t)(*(volatile uint32_t*)&ctrl->issued - u) <= 0))
+                    return false;
+                return mbar_test_warp(full0 + 8u * st, ph);
+            };
+            auto ready_v = [&]() {
+                if (v_ok) return true;
+                if (v_first) {                     // the accumulator's last item has been read
+                    if (!wait_on(o_free, oph, abort_flag, status, 47)) return false;
+                    oph ^= 1u;
+                }
+                return wait_use(&ctrl->issued, v_use, full0 + 8u * v_st, v_ph, abort_flag, status, 46);
+            };
+            auto issue_o = [&](uint32_t h) {
+                const uint32_t v = ring_v + v_st * (C::kTileBytes >> 4) + h * kStepDesc;
+                const uint32_t acc = h | (v_first ^ 1u);
+                if (!wait_on(p_full + 8u * h, tph, abort_flag, status, 48)) return false;
                 tc_fence_after();
-                issue_pv<L::kGroup>(to, ts + 64u * buf, ring_v + vs * (C::kTileBytes >> 4) + (d & 1u) * kStepDesc, v_hi, kIdescO,
-                         (d & 2u) ^ 2u, o_full + 8u * buf);
-                if (d & 1u) mma_commit_warp(empty0 + 8u * vs);
-                o_cnt++;
-                pend >>= 4;
-                pend_use[0] = pend_use[1];
+                issue_pv<L::kGroup>(to, ts + 64u * h, v, v_hi, kIdescO, acc, o_full + 8u * h);
+                if (h) mma_commit_warp(empty0 + 8u * v_st);
                 return true;
             };
-            // One loop with one copy of each product (what is issued next is
-            // data: with the loops written out the MMA warps' code was 44 KB).
-            bool have = false, last = false, fresh = false;   // a step to come, no more items, an item's first step
-            int i = 0, end = 0, by = 1, h = 0, n = 0;         // the step: half h of key tile i; the item's tiles
-            uint32_t qt = 0;
-            int64_t idle_from = 0;
-            for (;;) {
-                if (!have && !last) {                         // the next item
-                    use += 2u * (uint32_t)n;
-                    if (pieces.next(p)) {
-                        p.range(j, row_tile_tokens(a.group), a.window, i, end);
-                        by = p.two ? 1 : 2;
-                        if (!p.two) i = j;
-                        n = p.n;
-                        qt = q_lo + (p.two && j ? C::kTileBytes >> 4 : 0);
-                        have = fresh = true;
-                    } else {
-                        last = true;
-                    }
+            auto flush = [&]() {
+                if (!ready_v()) return false;
+#pragma unroll 1
+                for (uint32_t h = 0; h < 2; h++)
+                    if (!issue_o(h)) return false;
+                pend = false;
+                return true;
+            };
+            bool ok = true;
+            while (ok && pieces.next(p)) {
+                int i, end;
+                p.range(j, row_tile_tokens(a.group), a.window, i, end);
+                const int by = p.two ? 1 : 2;
+                if (!p.two) i = j;
+                if (!p.two || i > 0 || end < p.n) safe = use + 2u * (uint32_t)p.n + kStages;   // (it leaves some to the other)
+                const uint32_t qt = q_lo + (p.two && j ? C::kTileBytes >> 4 : 0);
+                bool fresh = true, k_ok = false;
+                if (i >= end) {                    // no tile for this warp
+                    if (!(ok = wait_on(q_full, qph, abort_flag, status, 44))) break;
+                    qph ^= 1u;
+                    mbar_arrive_warp(q_empty, lane);
                 }
-                const uint32_t ku = use + use_of_k(i);
-                uint32_t kph;
-                const uint32_t ks = stage_of<kStages>(ku, &kph);
-                bool go = have && s_cnt - o_cnt < 2u;
-                if (go && fresh && h == 0) {
-                    go = mbar_test_warp(q_full, qph);
-                    if (go && i >= end) {                     // no tile for this warp
-                        mbar_arrive_warp(q_empty, lane);
-                        qph ^= 1u;
-                        have = false;
-                        continue;
-                    }
-                }
-                if (go && h == 0) go = test_use(&ctrl->issued, ku, full0 + 8u * ks, kph);
-                if (go) {
-                    idle_from = 0;
-                    const uint32_t buf = s_cnt & 1u;
-                    tc_fence_after();
-                    issue_qk<kDP, L::kHalf>(ts + 64u * buf, qt, q_hi, ring_k + ks * (C::kTileBytes >> 4) + h * kStepDesc,
-                                            k_hi, kIdescS, s_full + 8u * buf);
-                    const uint32_t d = (uint32_t)h | (fresh ? 2u : 0u);
-                    const bool one = s_cnt != o_cnt;          // one step is pending already
-                    pend |= d << (one ? 4 : 0);
-                    if (one) pend_use[1] = use + use_of_v(i, n);
-                    else pend_use[0] = use + use_of_v(i, n);
-                    s_cnt++;
-                    if (fresh) qph ^= 1u;
-                    fresh = false;
-                    if (h) {
-                        mma_commit_warp(empty0 + 8u * ks);
-                        i += by;
-                        if (i >= end) {
-                            mma_commit_warp(q_empty);
-                            have = false;
+                uint32_t ku = use + use_of_k(i), kph, ks = stage_of<kStages>(ku, &kph);
+                while (i < end) {
+                    if (!k_ok && ((fresh && !mbar_test_warp(q_full, qph)) || !there(ku, ks, kph))) {
+                        // not there yet: what is pending first
+                        if ((pend && !flush()) || (fresh && !wait_on(q_full, qph, abort_flag, status, 44)) ||
+                            !wait_use(&ctrl->issued, ku, full0 + 8u * ks, kph, abort_flag, status, 45)) {
+                            ok = false;
+                            break;
                         }
                     }
-                    h ^= 1;
-                } else if (s_cnt != o_cnt) {
-                    if (!issue_o()) break;
-                } else {
-                    if (!have) break;                         // all done
-                    // nothing to do until keys arrive
-                    const int64_t now = clock64();
-                    if (idle_from == 0) idle_from = now;
-                    const bool late = now - idle_from > (int64_t)kWaitLimitCycles;
-                    if (__any_sync(0xffffffffu, late || *abort_flag)) {
-                        if (late && *abort_flag == 0) atomicCAS(status, 0, kErrTimeout * 100 + 45);
-                        *abort_flag = 1;
+                    const uint32_t k = ring_k + ks * (C::kTileBytes >> 4), empty = empty0 + 8u * ks;
+                    if (pend && (!ready_v() || !issue_o(0))) {
+                        ok = false;
                         break;
                     }
+                    if (!pend) tc_fence_after();
+                    issue_qk<kDP, L::kHalf>(ts, qt, q_hi, k, k_hi, kIdescS, s_full);
+                    const uint32_t vu = use + use_of_v(i, p.n);
+                    uint32_t vph;
+                    const uint32_t vst = stage_of<kStages>(vu, &vph);
+                    const bool v_there = !fresh && there(vu, vst, vph);
+                    i += by;
+                    ku = use + use_of_k(i);
+                    ks = stage_of<kStages>(ku, &kph);
+                    k_ok = i < end && there(ku, ks, kph);
+                    if (pend && !issue_o(1)) {
+                        ok = false;
+                        break;
+                    }
+                    issue_qk<kDP, L::kHalf>(ts + 64u, qt, q_hi, k + kStepDesc, k_hi, kIdescS, s_full + 8u);
+                    mma_commit_warp(empty);
+                    if (i >= end) mma_commit_warp(q_empty);
+                    v_use = vu;
+                    v_st = vst;
+                    v_ph = vph;
+                    v_ok = v_there;
+                    v_first = fresh ? 1u : 0u;
+                    if (fresh) qph ^= 1u;
+                    fresh = false;
+                    tph = t_cnt & 1u;
+                    t_cnt++;
+                    pend = true;
                 }
+                use += 2u * (uint32_t)p.n;
             }
+            if (ok && pend) flush();
             // every MMA issued has completed before teardown
             mma_commit_warp(smem_u32(&ctrl->teardown));
             if (lane == 0) mbar_wait_teardown(smem_u32(&ctrl->teardown), 0);
