@@ -17,11 +17,11 @@
 // m was set: P stays below 2^8, its bf16 rounding is relative, and O is
 // rescaled a few times per row instead of at every key tile.
 //
-// Two softmax warpgroups work on two tiles at a time, so that the tensor
-// pipe multiplies for one while the other is in its softmax.  An item with
-// more than 128 rows has two row tiles, one per warpgroup, on the same keys;
-// one with at most 128 rows (decoding) gives the even key tiles to the first
-// and the odd ones to the second, which the first merges at the end.
+// Two softmax warpgroups work on two row tiles at a time, 64 keys a step, each
+// with two halves of S (one is multiplied while the other is in its softmax).
+// An item with more than 128 rows has two row tiles, one per warpgroup, on the
+// same keys; one with at most 128 rows (decoding) gives the even key tiles to
+// the first and the odd ones to the second, which the first merges at the end.
 //
 // Items are cut at CTA boundaries (equal key tiles per CTA).  A CTA's part of
 // a shared item goes to the workspace as fp32 (O, m, l); the CTA whose warp
@@ -29,19 +29,32 @@
 // whatever the order of arrival).  No CTA waits for another.
 //
 // Warps: 0-3 and 4-7 softmax and epilogue; 8 and 9 the MMAs of the first and
-// the second warpgroup (one warp's instruction stream for both would take
-// longer than the MMAs themselves); 10 K/V copies; 11 Q copies and the keys'
-// end (below).
+// the second warpgroup; 10 K/V copies; 11 Q copies and the keys' end (next).
 //
 // Rows past the last key of an item's last tile hold other requests' rows,
 // pages' unused rows or nothing at all.  Their scores are masked, and warp 11
 // zeroes the V rows before the tile is multiplied, so that NaN or infinities
 // there cannot reach a sum as 0 * NaN.
 //
-// The softmax is one small loop over 64 keys at a time: the warps of a CTA run
-// four different programs, and code that is run only now and then (masks, a
-// risen maximum, an item's end) is fetched from far when it is; unrolled
-// copies of it cost thousands of cycles an item.
+// What bounds it (40 query heads on 8 kv heads of 128 columns, 2070 MHz):
+//   - Few rows, many keys: HBM.  Two requests of 65537 and more keys, 879 MB of
+//     cache: 140.8 us, 6.25 TB/s.  Many short ones add the start of each CTA
+//     (4-5 us until the first S) and an item's end: 64 requests of 200 to 8192
+//     keys 104 us, 5.3 TB/s.
+//   - Long prompts: the tensor pipe and what keeps it from running.  A prompt of
+//     8192: 524 us, 1.31 PFLOP/s.  128 keys against two row tiles take about
+//     3100 cycles.  The products take 2560 of them: Q K^T of 64 keys reads Q
+//     again (48 KB of shared memory for 384 cycles, where the arithmetic would
+//     take 256), P V 256.  S of 128 keys would not read Q twice, but fills
+//     tensor memory with one S a warpgroup: 587 us, as a warpgroup then waits
+//     for its own products.  The rest is latency from P's arrival to the next
+//     S, and 6000 cycles at an item's end.
+//   - Short prompts: those ends and the start.  17 tokens take 7.1 us.
+// The warps of a CTA run four different programs, which drive each other out of
+// the instruction cache: the softmax is one small loop, the MMA warps' path of a
+// key tile is short and straight (with a loop that chose each product by data
+// 604 us), and code that is run only now and then is kept compact (unrolled
+// copies of it cost thousands of cycles an item).
 #include "attn.h"
 #include "common.cuh"
 #include "internal.h"
@@ -89,7 +102,8 @@ struct Cfg {
 // 64-column halves 16 KB apart, rows in order; a step is 64 rows in a row.
 // kFold, for pages of 16 rows of 128 columns: a page's both halves in one copy,
 // [page][half][16 rows][64 columns], as a copy costs about 60 cycles beside 4
-// per 128 bytes and two copies of 2 KB a page keep HBM waiting.  Step h is then
+// per 128 bytes and two copies of 2 KB a page keep HBM waiting (64 requests of
+// 200 to 8192 keys: 144 us in two copies, 104 in one).  Step h is then
 // the eight rows 8h .. 8h + 7 of each page: 8-row groups at one distance, which
 // is all that a descriptor can say.
 template <bool kFold>
@@ -202,7 +216,7 @@ __device__ __forceinline__ void mbar_arrive_warp(uint32_t bar, int lane)
         : "memory");
 }
 
-// One poll, without waiting (warp-uniform).
+// One look (warp-uniform): test_wait, as try_wait may suspend the warp.
 __device__ __forceinline__ bool mbar_test_warp(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
@@ -342,7 +356,7 @@ __device__ __forceinline__ int atom_add_acq_rel(int* p, int v)
     return old;
 }
 
-// The MMA warp's waits: mbar_wait_warp with less code around the poll.
+// The MMA warps' waits: mbar_wait_warp with less code around the poll.
 __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status, int site)
 {
     if (mbar_test_warp(bar, parity)) return true;
@@ -734,9 +748,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             __syncwarp();
         } else {
             // ------------------------------------------------------- MMA
-            // Warp 8 + j issues warpgroup j's products: a step's S once the P V
-            // of the step two before has gone out (they share columns), across
-            // items too; a step's P V once P is there.  Two row tiles: both
+            // Warp 8 + j issues warpgroup j's products, across items too: for
+            // each half of a key tile the last tile's P V, once P is there,
+            // then this tile's S over it (they share columns).  Two row tiles: both
             // warps use every key tile; one row tile: warp j the tiles j,
             // j + 2, ... (a stage is free after two arrivals: both warps', or
             // the one warp's and the copying warp's own).
@@ -760,7 +774,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             // of everything that alternates).  What lies between a tile's last
             // product and the next tile's first is on the path that bounds
             // long prompts (the tensor pipe is idle there): the keys' and
-            // values' barriers are looked at while the products before run.
+            // values' barriers are looked at while the products before run
+            // (prompt of 8192: 527 -> 524 us; with try_wait, which suspends
+            // where a phase is not complete, 564).
             bool pend = false;                     // the last tile's P V are still to be issued:
             uint32_t v_use = 0, v_st = 0, v_ph = 0, v_first = 0;   // V's use, stage, phase; the item's first tile
             bool v_ok = false;                     // V was there
