@@ -32,9 +32,10 @@
 // the second warpgroup; 10 K/V copies; 11 Q copies and the keys' end (next).
 //
 // Rows past the last key of an item's last tile hold other requests' rows,
-// pages' unused rows or nothing at all.  Their scores are masked, and warp 11
-// zeroes the V rows before the tile is multiplied, so that NaN or infinities
-// there cannot reach a sum as 0 * NaN.
+// pages' unused rows or nothing at all, and so may rows before a window's
+// first key.  Their scores are masked, and warp 11 zeroes the V rows before
+// the tile is multiplied, so that NaN or infinities there cannot reach a sum
+// as 0 * NaN.
 //
 // What bounds it (40 query heads on 8 kv heads of 128 columns, 2070 MHz):
 //   - Few rows, many keys: HBM.  Two requests of 65537 and more keys, 879 MB of
@@ -478,6 +479,14 @@ struct Piece {
         lo = min(max(lo_key / kAttnKeys - tile0, 0), n - 1);
         hi = min(max((hi_key - 1) / kAttnKeys + 1 - tile0, lo + 1), n);
     }
+    // Keys live0 .. live1 - 1 of key tile i are live: the others precede every
+    // row's window, or follow the item's last key.
+    __device__ __forceinline__ void live(int i, int window, int& live0, int& live1) const
+    {
+        const int key0 = (tile0 + i) * kAttnKeys;
+        live0 = window ? min(max(pos0 + 1 - window - key0, 0), kAttnKeys) : 0;
+        live1 = min(kAttnKeys, max(kv_end - key0, 0));
+    }
 };
 
 // The pieces of CTA `cta` in order; every warp of the CTA walks them alike.
@@ -643,8 +652,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     const bool kv = x == 2 * p.n - 1 || (x > 0 && !(x & 1));   // values
                     const int i = kv ? (x == 2 * p.n - 1 ? p.n - 1 : x / 2 - 1) : (x + 1) / 2;
                     const int key0 = (p.tile0 + i) * kAttnKeys;
-                    const int valid = min(kAttnKeys, max(p.kv_end - key0, 0));
-                    const int pages = paged ? (valid + a.page_size - 1) / a.page_size : 0;
+                    int live0, live1;
+                    p.live(i, a.window, live0, live1);
+                    const int pages = paged ? (live1 + a.page_size - 1) / a.page_size : 0;
                     const int page = kv || x == 0 ? page0 : page1;
                     uint32_t ph;
                     const uint32_t s = stage_of<kStages>(use, &ph);
@@ -655,8 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     if (lane == 0) *(volatile uint32_t*)&ctrl->issued = use + 1;
                     const CUtensorMap* map = kv ? &prm.map_v : &prm.map_k;
                     const uint32_t dst = base + C::kOffRing + s * C::kTileBytes;
-                    // an item's last values go through warp 11
-                    const uint32_t bar = smem_u32(kv && valid < kAttnKeys ? &ctrl->v_end[s] : &ctrl->kv_full[s]);
+                    // an item's first and last values go through warp 11
+                    const bool edge = kv && (live0 > 0 || live1 < kAttnKeys);
+                    const uint32_t bar = smem_u32(edge ? &ctrl->v_end[s] : &ctrl->kv_full[s]);
                     const uint32_t bytes = paged ? (uint32_t)(pages * a.page_size * kDP * 2) : (uint32_t)C::kTileBytes;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar, bytes);
@@ -701,8 +712,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             }
             __syncwarp();
         } else if (warp == kWarpQ) {
-            // ------------------- Q copies, and values past the last key
-            uint32_t n = 0, tile = 0, ends = 0;    // items, key tiles; ends: bit s = phase of v_end[s]
+            // ------------------------ Q copies, and the ends of the values
+            uint32_t n = 0, use = 0, ends = 0;     // items, uses of the ring; ends: bit s = phase of v_end[s]
             bool ok = true;
             const int row_tokens = row_tile_tokens(a.group), rows = a.group * row_tokens;
             const uint32_t bar = smem_u32(&ctrl->q_full);
@@ -721,28 +732,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 }
                 __syncwarp();
                 n++;
-                tile += p.n;
-                const int valid = min(kAttnKeys, max(p.kv_end - (p.tile0 + p.n - 1) * kAttnKeys, 0));
-                if (valid == kAttnKeys) continue;
-                uint32_t ph;
-                const uint32_t s = stage_of<kStages>(2 * (tile - 1) + 1, &ph);
-                if (!mbar_wait_warp<true>(smem_u32(&ctrl->v_end[s]), (ends >> s) & 1u, abort_flag, status, 43)) {
-                    ok = false;
-                    break;
-                }
-                ends ^= 1u << s;
-                uint8_t* v = smem + C::kOffRing + s * C::kTileBytes;
-                // four rows at a time, eight lanes to a row (the item's last
-                // product waits for this)
-                for (int r = valid + (lane >> 3); r < kAttnKeys; r += 4) {
-                    uint8_t* at = v + L::row(r) + (lane & 7) * 16;
+                // the first tile's values before every row's window, the last's past the last key
+                for (int i = 0; i < p.n && ok; i = i < p.n - 1 ? p.n - 1 : p.n) {
+                    int live0, live1;
+                    p.live(i, a.window, live0, live1);
+                    if (live0 == 0 && live1 == kAttnKeys) continue;
+                    uint32_t ph;
+                    const uint32_t s = stage_of<kStages>(use + use_of_v(i, p.n), &ph);
+                    if (!mbar_wait_warp<true>(smem_u32(&ctrl->v_end[s]), (ends >> s) & 1u, abort_flag, status, 43)) {
+                        ok = false;
+                        break;
+                    }
+                    ends ^= 1u << s;
+                    uint8_t* v = smem + C::kOffRing + s * C::kTileBytes;
+                    // four rows at a time, eight lanes to a row (the item's last
+                    // product waits for this)
+                    for (int r = live0 > 0 ? lane >> 3 : live1 + (lane >> 3); r < kAttnKeys; r += 4) {
+                        if (r >= live0 && r < live1) continue;
+                        uint8_t* at = v + L::row(r) + (lane & 7) * 16;
 #pragma unroll
-                    for (int half = 0; half < C::kHalves; half++)
-                        *reinterpret_cast<uint4*>(at + half * L::kHalf) = make_uint4(0, 0, 0, 0);
+                        for (int half = 0; half < C::kHalves; half++)
+                            *reinterpret_cast<uint4*>(at + half * L::kHalf) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&ctrl->kv_full[s]));
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctrl->kv_full[s]));
+                if (!ok) break;
+                use += 2u * (uint32_t)p.n;
             }
             if (!ok && n > 0 && lane == 0) mbar_wait_teardown(bar, (n - 1) & 1u);
             __syncwarp();

@@ -350,6 +350,34 @@ def test_paged_window(nv, ws, window):
     run_paged(nv, ws, [1500, 90, 0], [1, 140, 33], 10, 2, 128, 16, window=window)
 
 
+@pytest.mark.parametrize("P,D", [(16, 128), (64, 128), (16, 64), (128, 80)])
+@pytest.mark.parametrize("window", [1, 40, 129, 700])
+def test_paged_rows_before_the_window(nv, ws, window, P, D):
+    """Cached rows that have left every row's window may hold anything (their
+    pages may be another request's by now)."""
+    gen, rng = torch.Generator("cuda").manual_seed(window + D), np.random.default_rng(P)
+    ctx, q, H, Hkv = [1500, 90, 2, 4111], [1, 33, 5, 1], 10, 2
+    cache, table, live = make_paged(nv, gen, rng, ctx, q, Hkv, D, P)
+    for r, c in enumerate(ctx):
+        for at in range(max(c + 1 - window, 0)):
+            for t in (cache.k, cache.v):
+                t[int(table[r, at // P]), :, at % P] = math.nan if at % 2 else math.inf
+    T = sum(q)
+    qq = rows(gen, T, H, D, "plain", 1.5)
+    out, lse = torch.empty_like(qq), torch.empty(T, H, device="cuda")
+    plan = nv.AttnPlan(len(q), T, H, Hkv, page_size=P, block_table=table, window=window)
+    nv.nvfp4_attn_plan(plan, i32(q), i32(ctx))
+    nv.nvfp4_attn_paged(qq, cache, plan, out, ws, lse=lse)
+    torch.cuda.synchronize()
+    assert nv.device_status() == 0
+    at = 0
+    for r, (c, n) in enumerate(zip(ctx, q)):
+        k, v = (x.double() for x in live[r])
+        ref = reference(qq[at:at + n].double(), k, v, c, D ** -0.5, window)
+        check(out[at:at + n], lse[at:at + n], *ref, f"rows before the window, ctx={c}")
+        at += n
+
+
 @pytest.mark.parametrize("layout,interleaved", [("heads_first", True), ("padded", False)])
 def test_paged_layouts(nv, ws, layout, interleaved):
     run_paged(nv, ws, [300, 12], [5, 64], 10, 2, 96, 64, layout=layout, interleaved=interleaved)
