@@ -498,6 +498,8 @@ int nvfp4_kv_append(const void* k, int64_t ldk, int64_t hk, const void* v, int64
  *   out = bf16( sum_j softmax_j(scale * q.k_j) v_j ),  lse = log sum_j exp(scale * q.k_j).
  * Scores, softmax statistics and sums are binary32; the probabilities are
  * rounded to bf16 for the product with V.  Rows past cu_q[R] are not written.
+ * A value that is not finite can make rows of its own request NaN that do not
+ * see its key (0 * NaN), never another request's.
  *   step     after nvfp4_attn_plan on the same stream order, with a schedule
  *            and ctx_len NULL.
  *   k, v     as nvfp4_kv_append.
@@ -513,8 +515,8 @@ int nvfp4_attn_prompt(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const
  * which holds their own K and V already (nvfp4_kv_append): row t of request r
  * is at position p = kv_len[r] - q_len[r] + t and sees cache positions
  * max(0, p - window + 1) .. p of its request, found through block_table.  The
- * rest as nvfp4_attn_prompt.  Cache rows that no row sees may hold anything,
- * NaN included.  A row that sees no key (its window lies past the table's last
+ * rest as nvfp4_attn_prompt.  Cache rows that no row of the request sees may
+ * hold anything, NaN included.  A row that sees no key (its window lies past the table's last
  * column) gives out 0 and lse -inf.  A page id outside the cache counts as a page of zeros.
  */
 int nvfp4_attn_paged(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const nvfp4_kv_cache_t* cache,
