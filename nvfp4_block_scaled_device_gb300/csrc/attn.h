@@ -57,9 +57,10 @@ inline __host__ __device__ const QTile* schedule_tiles(const ScheduleHead* h)
 }
 
 // Boundary r (units from the item's start) of an item of `item` units.  A part
-// costs its CTA about 5 us beside its tiles (about 2 us each), so short items
-// are not shared.
-constexpr int kMinPart = 5;
+// costs its CTA 3 to 5 us beside its tiles (1.1 to 1.7 us each), so short items
+// are not shared.  At least 3 tiles a part: prompts of 1 to 499 tokens 18.6 us,
+// one of 8192 523; 5: 21.8, 534; 2: 21.7, 529.
+constexpr int kMinPart = 3;
 inline __host__ __device__ int snap_unit(int r, int item)
 {
     const bool head = r < kItemUnits + kMinPart, tail = item - r < kMinPart;
