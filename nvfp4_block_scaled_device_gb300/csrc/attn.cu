@@ -926,6 +926,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             // keys that every row of the warp sees (edits are needed beyond)
             const int hi_all = __reduce_min_sync(0xffffffffu, mine ? hi : 0x7fffffff);
             const int lo_all = __reduce_max_sync(0xffffffffu, lo);
+            // keys that no row of the warp sees: below and from
+            const int lo_any = __reduce_min_sync(0xffffffffu, mine ? lo : 0x7fffffff);
+            const int hi_any = __reduce_max_sync(0xffffffffu, hi);
             float m = -INFINITY, l = 0.0f;
             if (first >= end) continue;      // the second warpgroup of a single key tile
 #pragma unroll 1
@@ -940,6 +943,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     tc_fence_after();
                     // the tile's first key; keys that the step reaches from there
                     const int h = x & 1, key0 = p.tile0 * kAttnKeys + 2 * first * kStep + (x - h) * kStep;
+                    if (key0 + L::key(h, 0) >= hi_any || key0 + L::key(h, 7) + 8 <= lo_any) {
+                        // none of the step's keys: P = 0
+                        uint32_t r[32];
+#pragma unroll
+                        for (int y = 0; y < 32; y++) r[y] = 0u;
+                        tmem_st32(ts + 64 * buf, r);
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        mbar_arrive_warp(p_full + 8u * buf, lane);
+                        continue;
+                    }
                     if (negate || hi_all < key0 + L::key(h, 7) + 8 || lo_all > key0 + L::key(h, 0))
                         edit_scores<kFold>(ts + 64 * buf, negate, h, lo - key0, hi - key0);
                     float s[kStep];
