@@ -795,6 +795,7 @@ int run_attn(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const AttnKV& 
     a.heads = (int)step->heads;
     a.kv_heads = (int)step->kv_heads;
     a.group = group;
+    a.row_tokens = row_tile_tokens(group);
     a.head_dim = (int)D;
     a.window = (int)step->window;
     a.scale = io->scale;

@@ -357,20 +357,41 @@ __device__ __forceinline__ int atom_add_acq_rel(int* p, int v)
     return old;
 }
 
-// The MMA warps' waits: mbar_wait_warp with less code around the poll.
-__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status, int site)
+// The waits of this kernel (converged, bounded by 2 to 4 seconds: %clock_hi
+// counts 2^32 cycles).  Less code than mbar_wait_warp at each of some twenty
+// places: a failure only notes where, and wait_failed reports it at the end.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, const volatile int* abort_flag, int& failed, int site)
 {
     if (mbar_test_warp(bar, parity)) return true;
-    const uint32_t t0 = (uint32_t)clock64();
-    while (!mbar_poll_warp<false>(bar, parity)) {
-        const bool late = (uint32_t)clock64() - t0 > 0xE0000000u;      // about 2 s
-        if (__any_sync(0xffffffffu, late || *abort_flag)) {
-            if (late && *abort_flag == 0) atomicCAS(status, 0, kErrTimeout * 100 + site);
-            *abort_flag = 1;
-            return false;
-        }
-    }
-    return true;
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p, q, f;\n .reg .u32 t0, t, a;\n mov.u32 t0, %%clock_hi;\n"
+        "POLL_%=:\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " vote.sync.all.pred p, p, 0xffffffff;\n"
+        " @p bra.uni DONE_%=;\n"
+        " ld.volatile.shared.u32 a, [%3];\n"
+        " mov.u32 t, %%clock_hi;\n"
+        " sub.u32 t, t, t0;\n"
+        " setp.lt.u32 q, t, 2;\n"
+        " setp.eq.and.u32 q, a, 0, q;\n"
+        " vote.sync.all.pred q, q, 0xffffffff;\n"
+        " @q bra.uni POLL_%=;\n"
+        "DONE_%=:\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(smem_u32((const void*)abort_flag))
+        : "memory");
+    if (!ok) failed = site;
+    return ok != 0;
+}
+
+// After a wait that failed: the CTA's other warps give up too; a wait that ran
+// out (not one that another's failure ended) is recorded.
+__device__ __forceinline__ void wait_failed(volatile int* abort_flag, int* status, int site)
+{
+    if (*abort_flag == 0) atomicCAS(status, 0, kErrTimeout * 100 + site);
+    *abort_flag = 1;
 }
 
 // Waits for the ring's stage use `use` to be full.  A warp that leaves uses to
@@ -378,20 +399,16 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile 
 // right from the phase before on: so first the copies of this use have begun,
 // which they do once the stage's use before has been consumed.
 __device__ __forceinline__ bool wait_use(const volatile uint32_t* issued, uint32_t use, uint32_t bar, uint32_t parity,
-                                         volatile int* abort_flag, int* status, int site)
+                                         const volatile int* abort_flag, int& failed, int site)
 {
-    if (__any_sync(0xffffffffu, (int32_t)(*issued - use) <= 0)) {
-        const uint32_t t0 = (uint32_t)clock64();
-        while (__any_sync(0xffffffffu, (int32_t)(*issued - use) <= 0)) {
-            const bool late = (uint32_t)clock64() - t0 > 0xE0000000u;
-            if (__any_sync(0xffffffffu, late || *abort_flag)) {
-                if (late && *abort_flag == 0) atomicCAS(status, 0, kErrTimeout * 100 + site);
-                *abort_flag = 1;
-                return false;
-            }
+    const uint32_t t0 = (uint32_t)(clock64() >> 32);
+    while (__any_sync(0xffffffffu, (int32_t)(*issued - use) <= 0)) {
+        if (__any_sync(0xffffffffu, (uint32_t)(clock64() >> 32) - t0 >= 2u || *abort_flag)) {
+            failed = site;
+            return false;
         }
     }
-    return wait_on(bar, parity, abort_flag, status, site);
+    return wait_on(bar, parity, abort_flag, failed, site);
 }
 
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
@@ -490,19 +507,19 @@ struct Piece {
 };
 
 // The pieces of CTA `cta` in order; every warp of the CTA walks them alike.
-// kAhead: the next QTile is fetched while the current one is worked on.
-template <bool kAhead>
+// The next QTile is fetched while the current one is worked on.
 struct Pieces {
     const int4* table;
     int u, end, per_cta, qt, kv_heads, row_tokens;
-    int4 f0, f1;         // QTile qt, or (kAhead) the one that comes next
+    int hk, r0;          // the next piece: its kv head, units of its item before it
+    int4 f0, f1;         // ... and QTile (number qt)
 
     __device__ __forceinline__ Pieces(const AttnArgs& a, int cta)
     {
         const ScheduleHead* s = a.sched;
         table = reinterpret_cast<const int4*>(schedule_tiles(s));
         kv_heads = a.kv_heads;
-        row_tokens = row_tile_tokens(a.group);
+        row_tokens = a.row_tokens;
         const int4* start = reinterpret_cast<const int4*>(&s->start[cta]);
         f0 = start[0];
         f1 = start[1];
@@ -511,26 +528,18 @@ struct Pieces {
         per_cta = s->per_cta;
         u = cta * per_cta < units ? cta * per_cta : units;
         end = units - u < per_cta ? units : u + per_cta;
-    }
-    __device__ __forceinline__ void fetch()
-    {
-        qt++;
-        f0 = table[2 * qt];
-        f1 = table[2 * qt + 1];
+        const uint32_t rel = (uint32_t)(u - f1.w), item = (uint32_t)(kItemUnits + f1.z);
+        hk = (int)(rel / item);
+        r0 = (int)(rel - hk * item);
     }
     __device__ __forceinline__ bool next(Piece& p)
     {
         while (u < end) {
-            int rel = u - f1.w;
-            if (!kAhead && rel == (kItemUnits + f1.z) * kv_heads) {
-                fetch();
-                rel = 0;
-            }
             const int tiles = f1.z, item = kItemUnits + tiles;
-            p.hk = rel / item;
-            const int r0 = rel - p.hk * item, r1 = min(end - u, item - r0) + r0;   // the CTA's units of the item
+            const int r1 = min(end - u + r0, item);      // the CTA's units of the item: r0 .. r1 - 1
             const int k0 = max(snap_unit(r0, item) - kItemUnits, 0);
             p.n = max(snap_unit(r1, item) - kItemUnits, 0) - k0;
+            p.hk = hk;
             p.tok0 = f0.x;
             p.n_tok = f0.y;
             p.req = f0.z;
@@ -549,7 +558,18 @@ struct Pieces {
                 p.parts = c1 - c0 + 1;
             }
             u += r1 - r0;
-            if (kAhead && rel + (r1 - r0) == item * kv_heads && u < end) fetch();
+            r0 = r1;
+            if (r1 == item) {
+                r0 = 0;
+                if (++hk == kv_heads) {
+                    hk = 0;
+                    if (u < end) {
+                        qt++;
+                        f0 = table[2 * qt];
+                        f1 = table[2 * qt + 1];
+                    }
+                }
+            }
             if (p.n > 0) return true;
         }
         return false;
@@ -627,9 +647,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     griddep_launch_dependents();
     griddep_wait();                  // schedule, Q, K, V, outputs, workspace: after the previous kernel
     Piece p;
+    int failed = 0;                  // the wait that failed
 
     if (warp >= 8) {
-        Pieces<true> pieces(a, cta);
+        Pieces pieces(a, cta);
         setmaxnreg_dec<kRegsOther>();
         if (warp == kWarpKV) {
             // ------------------------------------------------ K/V copies
@@ -641,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             while (ok && pieces.next(p)) {
                 const int* table = paged ? a.block_table + (int64_t)p.req * a.table_ld : nullptr;
                 int lo[2], hi[2];
-                for (int j = 0; j < 2; j++) p.range(j, row_tile_tokens(a.group), a.window, lo[j], hi[j]);
+                for (int j = 0; j < 2; j++) p.range(j, a.row_tokens, a.window, lo[j], hi[j]);
                 // the lane's page of tiles i, i + 1, i + 2 (lane l: the tile's l-th)
                 auto page_of = [&](int i) {
                     const int at = (p.tile0 + i) * ppt + lane;
@@ -658,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     const int page = kv || x == 0 ? page0 : page1;
                     uint32_t ph;
                     const uint32_t s = stage_of<kStages>(use, &ph);
-                    if (!mbar_wait_warp(smem_u32(&ctrl->kv_empty[s]), ph ^ 1u, abort_flag, status, 41)) {
+                    if (!wait_on(smem_u32(&ctrl->kv_empty[s]), ph ^ 1u, abort_flag, failed, 41)) {
                         ok = false;
                         break;
                     }
@@ -715,10 +736,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             // ------------------------ Q copies, and the ends of the values
             uint32_t n = 0, use = 0, ends = 0;     // items, uses of the ring; ends: bit s = phase of v_end[s]
             bool ok = true;
-            const int row_tokens = row_tile_tokens(a.group), rows = a.group * row_tokens;
+            const int row_tokens = a.row_tokens, rows = a.group * row_tokens;
             const uint32_t bar = smem_u32(&ctrl->q_full);
             while (pieces.next(p)) {
-                if (!mbar_wait_warp(smem_u32(&ctrl->q_empty), (n & 1u) ^ 1u, abort_flag, status, 42)) {
+                if (!wait_on(smem_u32(&ctrl->q_empty), (n & 1u) ^ 1u, abort_flag, failed, 42)) {
                     ok = false;
                     break;
                 }
@@ -739,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     if (live0 == 0 && live1 == kAttnKeys) continue;
                     uint32_t ph;
                     const uint32_t s = stage_of<kStages>(use + use_of_v(i, p.n), &ph);
-                    if (!mbar_wait_warp<true>(smem_u32(&ctrl->v_end[s]), (ends >> s) & 1u, abort_flag, status, 43)) {
+                    if (!wait_on(smem_u32(&ctrl->v_end[s]), (ends >> s) & 1u, abort_flag, failed, 43)) {
                         ok = false;
                         break;
                     }
@@ -807,88 +828,89 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             auto ready_v = [&]() {
                 if (v_ok) return true;
                 if (v_first) {                     // the accumulator's last item has been read
-                    if (!wait_on(o_free, oph, abort_flag, status, 47)) return false;
+                    if (!wait_on(o_free, oph, abort_flag, failed, 47)) return false;
                     oph ^= 1u;
                 }
-                return wait_use(&ctrl->issued, v_use, full0 + 8u * v_st, v_ph, abort_flag, status, 46);
+                return wait_use(&ctrl->issued, v_use, full0 + 8u * v_st, v_ph, abort_flag, failed, 46);
             };
-            auto issue_o = [&](uint32_t h) {
-                const uint32_t v = ring_v + v_st * (C::kTileBytes >> 4) + h * kStepDesc;
-                const uint32_t acc = h | (v_first ^ 1u);
-                if (!wait_on(p_full + 8u * h, tph, abort_flag, status, 48)) return false;
-                tc_fence_after();
-                issue_pv<L::kGroup>(to, ts + 64u * h, v, v_hi, kIdescO, acc, o_full + 8u * h);
-                if (h) mma_commit_warp(empty0 + 8u * v_st);
-                return true;
-            };
-            auto flush = [&]() {
-                if (!ready_v()) return false;
-#pragma unroll 1
-                for (uint32_t h = 0; h < 2; h++)
-                    if (!issue_o(h)) return false;
-                pend = false;
-                return true;
-            };
-            bool ok = true;
-            while (ok && pieces.next(p)) {
-                int i, end;
-                p.range(j, row_tile_tokens(a.group), a.window, i, end);
-                const int by = p.two ? 1 : 2;
-                if (!p.two) i = j;
-                if (!p.two || i > 0 || end < p.n) safe = use + 2u * (uint32_t)p.n + kStages;   // (it leaves some to the other)
-                const uint32_t qt = q_lo + (p.two && j ? C::kTileBytes >> 4 : 0);
-                bool fresh = true, k_ok = false;
-                if (i >= end) {                    // no tile for this warp
-                    if (!(ok = wait_on(q_full, qph, abort_flag, status, 44))) break;
-                    qph ^= 1u;
-                    mbar_arrive_warp(q_empty, lane);
-                }
-                uint32_t ku = use + use_of_k(i), kph, ks = stage_of<kStages>(ku, &kph);
-                while (i < end) {
-                    if (!k_ok && ((fresh && !mbar_test_warp(q_full, qph)) || !there(ku, ks, kph))) {
-                        // not there yet: what is pending first
-                        if ((pend && !flush()) || (fresh && !wait_on(q_full, qph, abort_flag, status, 44)) ||
-                            !wait_use(&ctrl->issued, ku, full0 + 8u * ks, kph, abort_flag, status, 45)) {
-                            ok = false;
-                            break;
+            bool fresh = false, k_ok = false, more = true;    // the item's first tile; its keys are there; items to come
+            int i = 0, end = 0, by = 1, n = 0;                // the next tile to multiply, the item's
+            uint32_t qt = 0, ku = 0, ks = 0, kph = 0;
+            for (;;) {
+                if (i >= end && more) {                       // the next item
+                    use += 2u * (uint32_t)n;
+                    more = pieces.next(p);
+                    if (more) {
+                        p.range(j, a.row_tokens, a.window, i, end);
+                        by = p.two ? 1 : 2;
+                        if (!p.two) i = j;
+                        n = p.n;
+                        if (!p.two || i > 0 || end < n) safe = use + 2u * (uint32_t)n + kStages;   // (it leaves some to the other)
+                        qt = q_lo + (p.two && j ? C::kTileBytes >> 4 : 0);
+                        ku = use + use_of_k(i);
+                        ks = stage_of<kStages>(ku, &kph);
+                        fresh = true;
+                        k_ok = false;
+                        if (i >= end) {                       // no tile for this warp
+                            if (!wait_on(q_full, qph, abort_flag, failed, 44)) break;
+                            qph ^= 1u;
+                            mbar_arrive_warp(q_empty, lane);
+                            continue;
                         }
                     }
-                    const uint32_t k = ring_k + ks * (C::kTileBytes >> 4), empty = empty0 + 8u * ks;
-                    if (pend && (!ready_v() || !issue_o(0))) {
-                        ok = false;
-                        break;
-                    }
-                    if (!pend) tc_fence_after();
-                    issue_qk<kDP, L::kHalf>(ts, qt, q_hi, k, k_hi, kIdescS, s_full);
-                    const uint32_t vu = use + use_of_v(i, p.n);
-                    uint32_t vph;
-                    const uint32_t vst = stage_of<kStages>(vu, &vph);
-                    const bool v_there = !fresh && there(vu, vst, vph);
-                    i += by;
-                    ku = use + use_of_k(i);
-                    ks = stage_of<kStages>(ku, &kph);
-                    k_ok = i < end && there(ku, ks, kph);
-                    if (pend && !issue_o(1)) {
-                        ok = false;
-                        break;
-                    }
-                    issue_qk<kDP, L::kHalf>(ts + 64u, qt, q_hi, k + kStepDesc, k_hi, kIdescS, s_full + 8u);
-                    mma_commit_warp(empty);
-                    if (i >= end) mma_commit_warp(q_empty);
-                    v_use = vu;
-                    v_st = vst;
-                    v_ph = vph;
-                    v_ok = v_there;
-                    v_first = fresh ? 1u : 0u;
-                    if (fresh) qph ^= 1u;
-                    fresh = false;
-                    tph = t_cnt & 1u;
-                    t_cnt++;
-                    pend = true;
                 }
-                use += 2u * (uint32_t)p.n;
+                // What goes out now: the last tile's P V, and the next tile's S
+                // over them if its operands are there (waited for only when
+                // nothing else is left).
+                bool s_too = i < end;
+                if (s_too && !k_ok) {
+                    s_too = (!fresh || mbar_test_warp(q_full, qph)) && there(ku, ks, kph);
+                    if (!s_too && !pend) {
+                        if ((fresh && !wait_on(q_full, qph, abort_flag, failed, 44)) ||
+                            !wait_use(&ctrl->issued, ku, full0 + 8u * ks, kph, abort_flag, failed, 45))
+                            break;
+                        s_too = true;
+                    }
+                }
+                if (!s_too && !pend) break;                   // all done
+                if (pend && !ready_v()) break;
+                const uint32_t k = ring_k + ks * (C::kTileBytes >> 4), k_empty = empty0 + 8u * ks;
+                const uint32_t v = ring_v + v_st * (C::kTileBytes >> 4), v_empty = empty0 + 8u * v_st;
+                const uint32_t first = v_first;
+                bool ok = true;
+#pragma unroll 1
+                for (uint32_t h = 0; h < 2; h++) {
+                    if (pend) {
+                        ok = wait_on(p_full + 8u * h, tph, abort_flag, failed, 48);
+                        if (!ok) break;
+                    }
+                    tc_fence_after();
+                    if (pend) {
+                        issue_pv<L::kGroup>(to, ts + 64u * h, v + h * kStepDesc, v_hi, kIdescO, h | (first ^ 1u), o_full + 8u * h);
+                        if (h) mma_commit_warp(v_empty);
+                    }
+                    if (!s_too) continue;
+                    issue_qk<kDP, L::kHalf>(ts + 64u * h, qt, q_hi, k + h * kStepDesc, k_hi, kIdescS, s_full + 8u * h);
+                    if (h) {
+                        mma_commit_warp(k_empty);
+                        if (i >= end) mma_commit_warp(q_empty);
+                    } else {
+                        v_use = use + use_of_v(i, n);
+                        v_st = stage_of<kStages>(v_use, &v_ph);
+                        v_first = fresh ? 1u : 0u;
+                        v_ok = !fresh && there(v_use, v_st, v_ph);
+                        if (fresh) qph ^= 1u;
+                        fresh = false;
+                        i += by;
+                        ku = use + use_of_k(i);
+                        ks = stage_of<kStages>(ku, &kph);
+                        k_ok = i < end && there(ku, ks, kph);
+                    }
+                }
+                if (!ok) break;
+                pend = s_too;
+                if (s_too) tph = t_cnt++ & 1u;
             }
-            if (ok && pend) flush();
             // every MMA issued has completed before teardown
             mma_commit_warp(smem_u32(&ctrl->teardown));
             if (lane == 0) mbar_wait_teardown(smem_u32(&ctrl->teardown), 0);
@@ -897,10 +919,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     } else {
         // ------------------------------------------- softmax and epilogue
         setmaxnreg_inc<kRegsSoftmax>();
-        Pieces<false> pieces(a, cta);
+        Pieces pieces(a, cta);
         const int j = warp >> 2, w = warp & 3;
         const int row = w * 32 + lane;
-        const int row_tokens = row_tile_tokens(a.group);
+        const int row_tokens = a.row_tokens;
         const int tk = row / a.group, g = row - tk * a.group;    // this thread's token and head in a row tile
         const uint32_t lane_addr = tmem + ((uint32_t)(w * 32) << 16);
         const uint32_t ts = lane_addr + kColS + 128 * j, to = lane_addr + kColO + 128 * j;
@@ -935,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             for (int x = 0; x < 2 * (end - first); x += by == 1 || (x & 1) == 0 ? 1 : 3, cnt++) {
                 // step x: 64 keys; its barriers and columns alternate
                 const uint32_t buf = cnt & 1u, ph = (cnt >> 1) & 1u;
-                if (!mbar_wait_warp(s_full + 8u * buf, ph, abort_flag, status, 50)) {
+                if (!wait_on(s_full + 8u * buf, ph, abort_flag, failed, 50)) {
                     ok = false;
                     break;
                 }
@@ -978,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                             // maximum, once the last P V is complete
                             const float f = up ? ex2((m - m1) * c) : 1.0f;
                             l *= f;
-                            if (!mbar_wait_warp(o_full + 8u * (buf ^ 1u), ((cnt - 1) >> 1) & 1u, abort_flag, status, 51)) {
+                            if (!wait_on(o_full + 8u * (buf ^ 1u), ((cnt - 1) >> 1) & 1u, abort_flag, failed, 51)) {
                                 ok = false;
                                 break;
                             }
@@ -1008,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
             // ---- the item's end: O in tensor memory, m and l here
             const bool merge = !p.two && p.n > 1;       // both warpgroups hold a share of the same rows
-            if (!mbar_wait_warp(o_full + 8u * ((cnt - 1) & 1u), ((cnt - 1) >> 1) & 1u, abort_flag, status, 52)) break;
+            if (!wait_on(o_full + 8u * ((cnt - 1) & 1u), ((cnt - 1) >> 1) & 1u, abort_flag, failed, 52)) break;
             tc_fence_after();
             if (merge && j == 1) {
                 ctrl->m[row] = m;
@@ -1019,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             }
             float f0 = 1.0f, f1 = 0.0f;
             if (merge) {
-                if (!mbar_wait_warp(smem_u32(&ctrl->ml_full[w]), ml_cnt & 1u, abort_flag, status, 53)) break;
+                if (!wait_on(smem_u32(&ctrl->ml_full[w]), ml_cnt & 1u, abort_flag, failed, 53)) break;
                 ml_cnt++;
                 tc_fence_after();
                 const float mb = ctrl->m[row], lb = ctrl->l[row];
@@ -1204,6 +1226,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             else join(Int<4>(), Int<4>());
         }
     }
+    if (failed) wait_failed(abort_flag, status, failed);
     tc_fence_before();
     __syncthreads();
     if (warp == kWarpMma) {

@@ -99,6 +99,7 @@ struct AttnArgs {
     int64_t ldo, ho;
     float* lse;
     int heads, kv_heads, group, head_dim;
+    int row_tokens;      // tokens of a row tile
     int window;
     float scale;
     // paged cache (block_table NULL: packed keys)
