@@ -656,66 +656,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             // ------------------------------------------------ K/V copies
             const bool paged = a.block_table != nullptr;
             const int ppt = paged ? kAttnKeys / a.page_size : 1;       // pages of a key tile
-            uint32_t use = 0;
-            uint32_t issued = 0, issued_ph = 0;   // stages with copies under way, and whose phase
+            const uint32_t page_bytes = paged ? (uint32_t)(a.page_size * kDP * 2) : (uint32_t)C::kTileBytes;
+            // a copy per lane: half `half` of the tile's page pg (at most 16 copies; kFold: whole pages)
+            const int half = kFold ? 0 : lane / ppt, pg = lane - half * ppt;
+            const uint32_t copy_at = base + C::kOffRing + (kFold ? lane * 4096u : half * 16384u + pg * a.page_size * 128u);
+            uint32_t use = 0, s = 0, ph = 1;      // the ring's next use, its stage, the phase of that stage's use before
             bool ok = true;
             while (ok && pieces.next(p)) {
                 const int* table = paged ? a.block_table + (int64_t)p.req * a.table_ld : nullptr;
-                int lo[2], hi[2];
+                int lo[2], hi[2], live0, live1, unused;
                 for (int j = 0; j < 2; j++) p.range(j, a.row_tokens, a.window, lo[j], hi[j]);
-                // the lane's page of tiles i, i + 1, i + 2 (lane l: the tile's l-th)
+                // tiles from .. to - 1 are both MMA warps', the others one's
+                const int from = p.two ? max(lo[0], lo[1]) : p.n, to = min(hi[0], hi[1]);
+                p.live(0, a.window, live0, unused);
+                p.live(p.n - 1, a.window, unused, live1);
+                const int last_pages = paged ? (live1 + a.page_size - 1) / a.page_size : 1;
+                // this lane's page of tiles i - 1, i, i + 1
                 auto page_of = [&](int i) {
-                    const int at = (p.tile0 + i) * ppt + lane;
-                    return paged && i < p.n && lane < ppt && at * a.page_size < p.kv_end ? __ldg(table + at) : 0;
+                    const int at = (p.tile0 + i) * ppt + pg;
+                    return paged && i < p.n && at * a.page_size < p.kv_end ? __ldg(table + at) : 0;
                 };
-                int page0 = page_of(0), page1 = page_of(1), page2 = page_of(2);
-                for (int x = 0; x < 2 * p.n; x++, use++) {
-                    const bool kv = x == 2 * p.n - 1 || (x > 0 && !(x & 1));   // values
-                    const int i = kv ? (x == 2 * p.n - 1 ? p.n - 1 : x / 2 - 1) : (x + 1) / 2;
-                    const int key0 = (p.tile0 + i) * kAttnKeys;
-                    int live0, live1;
-                    p.live(i, a.window, live0, live1);
-                    const int pages = paged ? (live1 + a.page_size - 1) / a.page_size : 0;
-                    const int page = kv || x == 0 ? page0 : page1;
-                    uint32_t ph;
-                    const uint32_t s = stage_of<kStages>(use, &ph);
-                    if (!wait_on(smem_u32(&ctrl->kv_empty[s]), ph ^ 1u, abort_flag, failed, 41)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) *(volatile uint32_t*)&ctrl->issued = use + 1;
-                    const CUtensorMap* map = kv ? &prm.map_v : &prm.map_k;
-                    const uint32_t dst = base + C::kOffRing + s * C::kTileBytes;
-                    // an item's first and last values go through warp 11
-                    const bool edge = kv && (live0 > 0 || live1 < kAttnKeys);
-                    const uint32_t bar = smem_u32(edge ? &ctrl->v_end[s] : &ctrl->kv_full[s]);
-                    const uint32_t bytes = paged ? (uint32_t)(pages * a.page_size * kDP * 2) : (uint32_t)C::kTileBytes;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(bar, bytes);
-                        // only one MMA warp will use it
-                        if (!p.two || i < lo[0] || i >= hi[0] || i < lo[1] || i >= hi[1])
-                            mbar_arrive(smem_u32(&ctrl->kv_empty[s]));
-                    }
-                    __syncwarp();
-                    if (kFold) {
-                        const int id = __shfl_sync(0xffffffffu, page, lane & 7);
-                        if (lane < pages) tma_load_5d(dst + lane * 4096, map, bar, 0, 0, 0, p.hk, id);
-                    } else if (paged) {
-                        // box b: half b / ppt of page b % ppt (at most 16)
-                        const int b = lane, half = b / ppt, pg = b - half * ppt;
-                        const int id = __shfl_sync(0xffffffffu, page, pg);
-                        if (half < C::kHalves && pg < pages)
-                            tma_load_4d(dst + half * 16384 + pg * a.page_size * 128, map, bar, half * 64, 0, p.hk, id);
-                    } else if (lane < C::kHalves) {
-                        tma_load_3d(dst + lane * 16384, map, bar, lane * 64, p.hk, p.tok0 - p.pos0 + key0);   // (packed: the request's first row is its key 0)
-                    }
-                    __syncwarp();
-                    issued |= 1u << s;
-                    issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
+                int page0 = 0, page1 = page_of(0), page2 = page_of(1);
+#pragma unroll 1
+                for (int x = 0; x < 2 * p.n + 2; x++) {
+                    // keys of tile i, then values of tile i - 1
+                    const int kv = x & 1, i = (x >> 1) - kv, id = kv ? page0 : page1;
                     if (kv) {
                         page0 = page1;
                         page1 = page2;
                         page2 = page_of(i + 3);
+                    }
+                    if (i < 0 || i == p.n) continue;
+                    if (!wait_on(smem_u32(&ctrl->kv_empty[s]), ph, abort_flag, failed, 41)) {
+                        ok = false;
+                        break;
+                    }
+                    const bool last = i == p.n - 1;
+                    const int pages = last ? last_pages : ppt;
+                    // an item's first and last values go through warp 11
+                    const bool edge = kv && ((i == 0 && live0 > 0) || (last && live1 < kAttnKeys));
+                    const uint32_t bar = smem_u32(edge ? &ctrl->v_end[s] : &ctrl->kv_full[s]);
+                    if (lane == 0) {
+                        *(volatile uint32_t*)&ctrl->issued = use + 1;
+                        mbar_arrive_expect_tx(bar, pages * page_bytes);
+                        if (i < from || i >= to) mbar_arrive(smem_u32(&ctrl->kv_empty[s]));   // only one MMA warp will use it
+                    }
+                    __syncwarp();
+                    const CUtensorMap* map = kv ? &prm.map_v : &prm.map_k;
+                    const uint32_t dst = copy_at + s * C::kTileBytes;
+                    if (half < C::kHalves && pg < pages) {
+                        if (kFold) tma_load_5d(dst, map, bar, 0, 0, 0, p.hk, id);
+                        else if (paged) tma_load_4d(dst, map, bar, half * 64, 0, p.hk, id);
+                        // (packed: the request's first row is its key 0)
+                        else tma_load_3d(dst, map, bar, half * 64, p.hk, p.tok0 - p.pos0 + (p.tile0 + i) * kAttnKeys);
+                    }
+                    __syncwarp();
+                    use++;
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1u;
                     }
                 }
             }
@@ -724,12 +723,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 // CTA's shared memory goes away (bounded).  Values that end
                 // an item complete on v_end, which has its own phases:
                 // waiting on both for either phase costs time only here
-                for (int s = 0; s < kStages; s++)
-                    if (issued & (1u << s)) {
-                        mbar_wait_teardown(smem_u32(&ctrl->kv_full[s]), (issued_ph >> s) & 1u);
-                        mbar_wait_teardown(smem_u32(&ctrl->v_end[s]), 0);
-                        mbar_wait_teardown(smem_u32(&ctrl->v_end[s]), 1);
-                    }
+                for (uint32_t u = use < kStages ? 0u : use - kStages; u < use; u++) {
+                    uint32_t uph;
+                    const uint32_t us = stage_of<kStages>(u, &uph);
+                    mbar_wait_teardown(smem_u32(&ctrl->kv_full[us]), uph);
+                    mbar_wait_teardown(smem_u32(&ctrl->v_end[us]), 0);
+                    mbar_wait_teardown(smem_u32(&ctrl->v_end[us]), 1);
+                }
             }
             __syncwarp();
         } else if (warp == kWarpQ) {
