@@ -39,23 +39,23 @@
 //
 // What bounds it (40 query heads on 8 kv heads of 128 columns, 2070 MHz):
 //   - Few rows, many keys: HBM.  Two requests of 65537 and more keys, 879 MB of
-//     cache: 140.8 us, 6.25 TB/s.  Many short ones add the start of each CTA
-//     (4-5 us until the first S) and an item's end: 64 requests of 200 to 8192
-//     keys 104 us, 5.3 TB/s.
+//     cache: 138 us, 6.35 TB/s.  Many short ones add the start of each CTA
+//     (4-5 us until the first S) and the items' ends: 64 requests of 200 to 8192
+//     keys 95 us, 5.8 TB/s.
 //   - Long prompts: the tensor pipe and what keeps it from running.  A prompt of
-//     8192: 524 us, 1.31 PFLOP/s.  128 keys against two row tiles take about
-//     3100 cycles.  The products take 2560 of them: Q K^T of 64 keys reads Q
+//     8192: 507 us, 1.35 PFLOP/s.  128 keys against two row tiles take about
+//     3000 cycles.  The products take 2560 of them: Q K^T of 64 keys reads Q
 //     again (48 KB of shared memory for 384 cycles, where the arithmetic would
 //     take 256), P V 256.  S of 128 keys would not read Q twice, but fills
-//     tensor memory with one S a warpgroup: 587 us, as a warpgroup then waits
-//     for its own products.  The rest is latency from P's arrival to the next
-//     S, and 6000 cycles at an item's end.
-//   - Short prompts: those ends and the start.  17 tokens take 7.1 us.
+//     tensor memory with one S a warpgroup: 587 us (where this took 524), as a
+//     warpgroup then waits for its own products.  The rest is latency from P's
+//     arrival to the next S, and 5000-6000 cycles at an item's end.
+//   - Short prompts: those ends and the start.  17 tokens take 6.6 us.
 // The warps of a CTA run four different programs, which drive each other out of
-// the instruction cache: the softmax is one small loop, the MMA warps' path of a
-// key tile is short and straight (with a loop that chose each product by data
-// 604 us), and code that is run only now and then is kept compact (unrolled
-// copies of it cost thousands of cycles an item).
+// the instruction cache; every program's repeated path is kept short.  With
+// loops written out, waits with their own time limits and divisions in the walk
+// over the items (110 KB of code instead of 81) the prompt of 8192 took 525 us,
+// the 64 requests 104.
 #include "attn.h"
 #include "common.cuh"
 #include "internal.h"
@@ -812,9 +812,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             // of everything that alternates).  What lies between a tile's last
             // product and the next tile's first is on the path that bounds
             // long prompts (the tensor pipe is idle there): the keys' and
-            // values' barriers are looked at while the products before run
-            // (prompt of 8192: 527 -> 524 us; with try_wait, which suspends
-            // where a phase is not complete, 564).
+            // values' barriers are looked at while the products before run,
+            // with test_wait (prompt of 8192 524 us; with try_wait, which
+            // suspends where a phase is not complete, 564).
             bool pend = false;                     // the last tile's P V are still to be issued:
             uint32_t v_use = 0, v_st = 0, v_ph = 0, v_first = 0;   // V's use, stage, phase; the item's first tile
             bool v_ok = false;                     // V was there
@@ -834,10 +834,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 return wait_use(&ctrl->issued, v_use, full0 + 8u * v_st, v_ph, abort_flag, failed, 46);
             };
             bool fresh = false, k_ok = false, more = true;    // the item's first tile; its keys are there; items to come
+            bool pass = false;                                // an item without a tile for this warp
             int i = 0, end = 0, by = 1, n = 0;                // the next tile to multiply, the item's
             uint32_t qt = 0, ku = 0, ks = 0, kph = 0;
             for (;;) {
-                if (i >= end && more) {                       // the next item
+                if (i >= end && more && !pass) {              // the next item
                     use += 2u * (uint32_t)n;
                     more = pieces.next(p);
                     if (more) {
@@ -851,12 +852,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                         ks = stage_of<kStages>(ku, &kph);
                         fresh = true;
                         k_ok = false;
-                        if (i >= end) {                       // no tile for this warp
-                            if (!wait_on(q_full, qph, abort_flag, failed, 44)) break;
-                            qph ^= 1u;
-                            mbar_arrive_warp(q_empty, lane);
-                            continue;
-                        }
+                        pass = i >= end;
+                    }
+                }
+                if (pass) {
+                    // No tile for this warp, it only passes Q on.  Not while it
+                    // holds values that the ring may need for the other's keys:
+                    // it waits with nothing pending.
+                    bool q_there = mbar_test_warp(q_full, qph);
+                    if (!q_there && !pend) {
+                        if (!wait_on(q_full, qph, abort_flag, failed, 44)) break;
+                        q_there = true;
+                    }
+                    if (q_there) {
+                        qph ^= 1u;
+                        mbar_arrive_warp(q_empty, lane);
+                        pass = false;
+                        continue;
                     }
                 }
                 // What goes out now: the last tile's P V, and the next tile's S

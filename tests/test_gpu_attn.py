@@ -350,6 +350,31 @@ def test_paged_window(nv, ws, window):
     run_paged(nv, ws, [1500, 90, 0], [1, 140, 33], 10, 2, 128, 16, window=window)
 
 
+@pytest.mark.parametrize("D", [128, 64])
+def test_many_short_items_after_a_longer_one(nv, ws, D):
+    """Items of a single key tile are one MMA warp's alone: the other passes
+    many of them in a row, whatever it still has to do for the item before."""
+    H, Hkv = 8, 4
+    lens = [200, 3, 1, 5, 2, 64, 7, 1, 1, 2] * 30
+    gen = torch.Generator("cuda").manual_seed(D)
+    T = sum(lens)
+    q, k, v = (rows(gen, T, h, D, "plain", 1.5) for h in (H, Hkv, Hkv))
+    out, lse = torch.empty_like(q), torch.empty(T, H, device="cuda")
+    plan = nv.AttnPlan(len(lens), T, H, Hkv)
+    nv.nvfp4_attn_plan(plan, i32(lens))
+    nv.nvfp4_attn_prompt(q, k, v, plan, out, ws, lse=lse)
+    torch.cuda.synchronize()
+    assert nv.device_status() == 0
+    at = 0
+    for n in lens:
+        sl = slice(at, at + n)
+        check(out[sl], lse[sl], *reference(q[sl].double(), k[sl].double(), v[sl].double(), 0, D ** -0.5), f"rows {sl}")
+        at += n
+    rng = np.random.default_rng(D)
+    ctx = [int(c) for c in rng.choice([3, 9, 40, 70, 100, 300, 700], 400, p=[.2, .2, .2, .1, .1, .1, .1])]
+    run_paged(nv, ws, ctx, [1] * len(ctx), H, Hkv, D, 16, seed=D)
+
+
 @pytest.mark.parametrize("P,D", [(16, 128), (64, 128), (16, 64), (128, 80)])
 @pytest.mark.parametrize("window", [1, 40, 129, 700])
 def test_paged_rows_before_the_window(nv, ws, window, P, D):
