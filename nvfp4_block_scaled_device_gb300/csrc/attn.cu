@@ -365,7 +365,7 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, const vol
     if (mbar_test_warp(bar, parity)) return true;
     uint32_t ok;
     asm volatile(
-        "{\n .reg .pred p, q, f;\n .reg .u32 t0, t, a;\n mov.u32 t0, %%clock_hi;\n"
+        "{\n .reg .pred p, q;\n .reg .u32 t0, t, a;\n mov.u32 t0, %%clock_hi;\n"
         "POLL_%=:\n"
         " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         " vote.sync.all.pred p, p, 0xffffffff;\n"
@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     if (lane == 0) {
                         *(volatile uint32_t*)&ctrl->issued = use + 1;
                         mbar_arrive_expect_tx(bar, pages * page_bytes);
-                        if (i < from || i >= to) mbar_arrive(smem_u32(&ctrl->kv_empty[s]));   // only one MMA warp will use it
+                        if (i < from || i >= to) mbar_arrive(smem_u32(&ctrl->kv_empty[s]));   // only one MMA warp's
                     }
                     __syncwarp();
                     const CUtensorMap* map = kv ? &prm.map_v : &prm.map_k;
@@ -819,9 +819,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             uint32_t v_use = 0, v_st = 0, v_ph = 0, v_first = 0;   // V's use, stage, phase; the item's first tile
             bool v_ok = false;                     // V was there
             uint32_t tph = 0, t_cnt = 0;           // the phase of the last tile's barriers; tiles
-            uint32_t safe = 0;                     // uses from here on follow one of their stage that this warp has waited for
+            uint32_t safe = 0;                     // this warp has waited for the stage's last use, from this use on
             auto there = [&](uint32_t u, uint32_t st, uint32_t ph) {
-                if ((int32_t)(u - safe) < 0 && __any_sync(0xffffffffu, (int32_t)(*(volatile uint32_t*)&ctrl->issued - u) <= 0))
+                const volatile uint32_t* issued = &ctrl->issued;
+                if ((int32_t)(u - safe) < 0 && __any_sync(0xffffffffu, (int32_t)(*issued - u) <= 0))
                     return false;
                 return mbar_test_warp(full0 + 8u * st, ph);
             };
@@ -846,7 +847,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                         by = p.two ? 1 : 2;
                         if (!p.two) i = j;
                         n = p.n;
-                        if (!p.two || i > 0 || end < n) safe = use + 2u * (uint32_t)n + kStages;   // (it leaves some to the other)
+                        // (it leaves some to the other)
+                        if (!p.two || i > 0 || end < n) safe = use + 2u * (uint32_t)n + kStages;
                         qt = q_lo + (p.two && j ? C::kTileBytes >> 4 : 0);
                         ku = use + use_of_k(i);
                         ks = stage_of<kStages>(ku, &kph);
@@ -898,7 +900,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     }
                     tc_fence_after();
                     if (pend) {
-                        issue_pv<L::kGroup>(to, ts + 64u * h, v + h * kStepDesc, v_hi, kIdescO, h | (first ^ 1u), o_full + 8u * h);
+                        issue_pv<L::kGroup>(to, ts + 64u * h, v + h * kStepDesc, v_hi, kIdescO, h | (first ^ 1u),
+                                            o_full + 8u * h);
                         if (h) mma_commit_warp(v_empty);
                     }
                     if (!s_too) continue;
@@ -1259,8 +1262,8 @@ cudaError_t launch(const Params& p, int num_sms, cudaStream_t stream)
         if (e != cudaSuccess) return e;
         attr_set_for_device[dev] = 1;
     }
-    return launch_programmatic(attn_kernel<kDP, kFold>, dim3((unsigned)num_sms), dim3(kThreads), Cfg<kDP>::kSmemBytes, stream,
-                               p);
+    return launch_programmatic(attn_kernel<kDP, kFold>, dim3((unsigned)num_sms), dim3(kThreads), Cfg<kDP>::kSmemBytes,
+                               stream, p);
 }
 
 }  // namespace
