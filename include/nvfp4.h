@@ -461,7 +461,7 @@ size_t nvfp4_attn_workspace_bytes(void);
 
 /*
  * nvfp4_attn_plan -- the tables of a step from its requests' lengths, in one
- * launch.  With need(x) = ceil(x / page_size) pages for x tokens:
+ * launch (two where cursor_out is cursor).  With need(x) = ceil(x / page_size) pages for x tokens:
  *   cu_q[r+1] = cu_q[r] + q_len[r],  kv_len[r] = ctx_len[r] + q_len[r];
  *   packed row cu_q[r] + t: pos = ctx_len[r] + t,
  *                           slot = block_table[r][pos / page_size] * page_size + pos % page_size;

@@ -8,7 +8,8 @@
 // tables; so the whole plan is one launch without a grid-wide wait.  The
 // tables are small (a few hundred KB at most): the launch and the dependent
 // reads set the time, not bandwidth (64 decoding requests 5.4 us; 4096 requests
-// of 1 to 13 new tokens 15.4 us).
+// of 1 to 13 new tokens 15.4 us).  Only a cursor that is advanced in place is
+// stored by a second launch (cursor_kernel).
 #include "attn.h"
 #include "common.cuh"
 #include "internal.h"
@@ -32,6 +33,13 @@ struct PlanParams {
 __device__ __forceinline__ void report(int* status, int code)
 {
     if (status) atomicCAS(status, 0, code);
+}
+
+// Pages that q new tokens behind c cached ones open (pages of 2^shift tokens).
+__device__ __forceinline__ int64_t pages_opened(int64_t c, int64_t q, int shift)
+{
+    const int64_t round = ((int64_t)1 << shift) - 1;
+    return ((c + q + round) >> shift) - ((c + round) >> shift);
 }
 
 __device__ __forceinline__ int64_t warp_incl_sum(int64_t v, int lane)
@@ -202,11 +210,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
     __syncthreads();
     // prefix sums over the requests: thread t takes the requests per*t ..
     const int per = ((R + kPlanThreads - 1) / kPlanThreads) | 1;     // (odd: no bank conflicts)
-    auto pages_of = [&](int64_t c, int64_t q) { return ((c + q + round) >> sft) - ((c + round) >> sft); };
     int64_t bq = 0, bn = 0, total_q = 0, total_n = 0;
     for (int r = t * per; r < min(R, (t + 1) * per); r++) {
         bq += cu[r];
-        if (paged) bn += pages_of(ctx[r], cu[r]);
+        if (paged) bn += pages_opened(ctx[r], cu[r], sft);
     }
     block_prefix(bq, bn, s_sums, &total_q, &total_n);
     const int64_t cap = s.tokens;
@@ -215,7 +222,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         cu[r] = (int32_t)min(bq, cap);
         first[r] = (int32_t)min(bn, kIntMax);
         bq += q;
-        if (paged) bn += pages_of(ctx[r], q);
+        if (paged) bn += pages_opened(ctx[r], q, sft);
     }
     if (t == 0) {
         cu[R] = (int32_t)min(total_q, cap);
@@ -248,7 +255,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
                 if (!ok) report(p.status, kStatusPlan);
             }
         }
-        if (blockIdx.x == 0 && t == 0 && s.cursor_out) *s.cursor_out = (int32_t)min(cursor + total_n, kIntMax);
+        if (blockIdx.x == 0 && t == 0 && s.cursor_out && s.cursor_out != s.cursor)
+            *s.cursor_out = (int32_t)min(cursor + total_n, kIntMax);
     }
 
     // per-token tables
@@ -278,6 +286,32 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         }
         if (s.pos) s.pos[i] = pos;
         if (paged) s.slot[i] = slot;
+    }
+}
+
+// *cursor_out where it is cursor itself.  The plan's blocks read the cursor
+// when they start, and nothing orders a block's start before another's end: a
+// store from within the plan could reach a block that has yet to read, and give
+// its requests pages that are others'.  So the word changes once the plan has
+// completed, by a block that counts the pages again (2 us more per step).
+constexpr int kCursorThreads = 512;
+
+__global__ void __launch_bounds__(kCursorThreads) cursor_kernel(const PlanParams p)
+{
+    __shared__ int64_t s_sums[kCursorThreads / 32];
+    griddep_launch_dependents();
+    griddep_wait();
+    const nvfp4_step_t& s = p.s;
+    int64_t n = 0;
+    for (int r = threadIdx.x; r < (int)s.requests; r += kCursorThreads)
+        n += pages_opened(max(s.ctx_len ? s.ctx_len[r] : 0, 0), max(s.q_len[r], 0), p.page_shift);
+    n = warp_incl_sum(n, threadIdx.x & 31);
+    if ((threadIdx.x & 31) == 31) s_sums[threadIdx.x >> 5] = n;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        n = *s.cursor;
+        for (int w = 0; w < kCursorThreads / 32; w++) n += s_sums[w];
+        *s.cursor_out = (int32_t)min(n, (int64_t)0x7fffffff);
     }
 }
 
@@ -375,7 +409,10 @@ cudaError_t launch_attn_plan(const nvfp4_step_t& step, int* status, int num_sms,
         grid += p.schedulers;
     }
     p.ctas = num_sms < kAttnMaxCtas ? num_sms : kAttnMaxCtas;
-    return launch_programmatic(plan_kernel, dim3((unsigned)grid), dim3(kPlanThreads), smem, stream, p);
+    e = launch_programmatic(plan_kernel, dim3((unsigned)grid), dim3(kPlanThreads), smem, stream, p);
+    if (e != cudaSuccess || !step.page_size || !step.free_pages || !step.cursor || step.cursor_out != step.cursor)
+        return e;
+    return launch_programmatic(cursor_kernel, dim3(1), dim3(kCursorThreads), 0, stream, p);
 }
 
 cudaError_t launch_kv_append(const __nv_bfloat16* k, int64_t ldk, int64_t hk, const __nv_bfloat16* v, int64_t ldv,
