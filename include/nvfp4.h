@@ -473,7 +473,8 @@ size_t nvfp4_attn_workspace_bytes(void);
  * free list ran out, the table has no such column) gets slot -1, its table
  * entry -1.  Each of these records NVFP4_ERR_INVALID_ARG * 100 + 31 in the
  * device status word.  *cursor_out counts the pages asked for, so that a value
- * above free_count tells how many were missing.
+ * above free_count tells how many were missing.  q_len and ctx_len are none of
+ * the outputs (a loop keeps its own ctx_len beside kv_len).
  */
 int nvfp4_attn_plan(const nvfp4_step_t* step, nvfp4_stream_t stream);
 

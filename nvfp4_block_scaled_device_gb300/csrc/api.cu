@@ -698,6 +698,13 @@ int check_step(const nvfp4_step_t* s, int what)
     return NVFP4_OK;
 }
 
+// Whether int32 arrays of na and nb elements share memory (NULL: no).
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + (uintptr_t)nb * 4 && y < x + (uintptr_t)na * 4;
+}
+
 // Rows [tokens][heads][head_dim] with pitches ld and h (elements).
 int check_rows(const void* p, int64_t tokens, int64_t heads, int64_t head_dim, int64_t ld, int64_t h)
 {
@@ -843,6 +850,13 @@ int nvfp4_attn_plan(const nvfp4_step_t* step, nvfp4_stream_t stream)
         if (!aligned(step->slot, 4) || !aligned(step->free_pages, 4) || !aligned(step->cursor, 4) ||
             !aligned(step->cursor_out, 4))
             return NVFP4_ERR_MISALIGNED;
+    }
+    // the blocks of the plan read the lengths while others fill the tables
+    for (const int32_t* in : {step->q_len, step->ctx_len}) {
+        const int64_t R = step->requests, T = step->tokens;
+        if (overlap(in, R, step->cu_q, R + 1) || overlap(in, R, step->kv_len, R) || overlap(in, R, step->pos, T) ||
+            (step->page_size && (overlap(in, R, step->slot, T) || overlap(in, R, step->cursor_out, 1))))
+            return NVFP4_ERR_INVALID_ARG;
     }
     DeviceInfo* d = nullptr;
     NVFP4_TRY(device_info(&d));
