@@ -1151,6 +1151,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             if (lane == 0) last = atom_add_acq_rel(ticket, 1) == p.parts - 1;   // (after the warp's stores: cumulative)
             last = __shfl_sync(0xffffffffu, last, 0);
             if (!last) continue;
+            __syncwarp();                    // the other CTAs' parts, acquired by lane 0, for every lane
             if (lane == 0) *ticket = 0;
             // rows in turn over the lanes, `share` lanes to a row with every
             // share-th 4-column vector each
