@@ -1033,6 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                         }
                         m = m1;
                     }
+                    if (!ok) break;
                     tmem_st32(ts + 64 * buf, r);
                     l += sum;
                     tmem_st_wait();
