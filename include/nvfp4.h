@@ -452,6 +452,7 @@ typedef struct {
     float* lse;                /* NULL, or fp32 [tokens x heads]: log of the row's sum of exp(score) */
     int64_t head_dim;          /* 16 .. 128, % 8 == 0 */
     float scale;               /* score = scale * q.k */
+    int32_t zero_padding;      /* rows of padding (cu_q[R] .. tokens - 1): 0 not written; else out 0, lse -inf */
 } nvfp4_attn_io_t;
 
 /* Bytes of a step's schedule for any lengths of R requests and tokens rows. */
@@ -498,7 +499,7 @@ int nvfp4_kv_append(const void* k, int64_t ldk, int64_t hk, const void* v, int64
  *   row t of a request sees keys max(0, t - window + 1) .. t of that request;
  *   out = bf16( sum_j softmax_j(scale * q.k_j) v_j ),  lse = log sum_j exp(scale * q.k_j).
  * Scores, softmax statistics and sums are binary32; the probabilities are
- * rounded to bf16 for the product with V.  Rows past cu_q[R] are not written.
+ * rounded to bf16 for the product with V.  Rows past cu_q[R] as io->zero_padding says.
  * A value that is not finite can make rows of its own request NaN that do not
  * see its key (0 * NaN), never another request's.
  *   step     after nvfp4_attn_plan on the same stream order, with a schedule

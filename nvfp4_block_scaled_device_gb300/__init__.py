@@ -62,7 +62,7 @@ class _CacheC(ctypes.Structure):
 class _AttnIOC(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("hq", ctypes.c_int64), ("out", ctypes.c_void_p),
                 ("ldo", ctypes.c_int64), ("ho", ctypes.c_int64), ("lse", ctypes.c_void_p),
-                ("head_dim", ctypes.c_int64), ("scale", ctypes.c_float)]
+                ("head_dim", ctypes.c_int64), ("scale", ctypes.c_float), ("zero_padding", ctypes.c_int32)]
 
 
 _SIGS = {
@@ -488,7 +488,7 @@ def nvfp4_kv_append(k: torch.Tensor, v: torch.Tensor, plan: AttnPlan, cache: KVC
                                  _stream(stream)), "nvfp4_kv_append")
 
 
-def _attn_io(plan: AttnPlan, q: torch.Tensor, out: torch.Tensor, scale, lse) -> _AttnIOC:
+def _attn_io(plan: AttnPlan, q: torch.Tensor, out: torch.Tensor, scale, lse, zero_padding) -> _AttnIOC:
     d, tokens, heads = q.shape[-1], plan.tokens, plan.heads
     if lse is None:
         at = None
@@ -497,16 +497,18 @@ def _attn_io(plan: AttnPlan, q: torch.Tensor, out: torch.Tensor, scale, lse) -> 
     else:
         raise ValueError("lse must be a contiguous CUDA float32 [tokens, heads] tensor")
     return _AttnIOC(*_heads_3d(q, "q", tokens, heads, d), *_heads_3d(out, "out", tokens, heads, d), at, d,
-                    d ** -0.5 if scale is None else scale)
+                    d ** -0.5 if scale is None else scale, 1 if zero_padding else 0)
 
 
 def nvfp4_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: AttnPlan, out: torch.Tensor,
-                      ws: torch.Tensor, scale=None, lse=None, stream=None):
+                      ws: torch.Tensor, scale=None, lse=None, stream=None, zero_padding=False):
     """Causal attention within packed prompts.  q, out: bf16 [tokens, heads,
     head_dim]; k, v: bf16 [tokens, kv_heads, head_dim] (any row and head
     pitch); scale: head_dim ** -0.5 if None; lse: None or float32 [tokens,
-    heads]; ws: a zero-filled workspace of attn_workspace_bytes()."""
-    io = _attn_io(plan, q, out, scale, lse)
+    heads]; ws: a zero-filled workspace of attn_workspace_bytes(); zero_padding:
+    rows past the step's last token become 0 in out and -inf in lse (else they
+    are not written)."""
+    io = _attn_io(plan, q, out, scale, lse, zero_padding)
     kp = _heads_3d(k, "k", plan.tokens, plan.kv_heads, q.shape[2])
     vp = _heads_3d(v, "v", plan.tokens, plan.kv_heads, q.shape[2])
     _check((_lib or lib()).nvfp4_attn_prompt(ctypes.byref(plan._c), ctypes.byref(io), *kp, *vp, ws.data_ptr(),
@@ -514,9 +516,9 @@ def nvfp4_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: A
 
 
 def nvfp4_attn_paged(q: torch.Tensor, cache: KVCache, plan: AttnPlan, out: torch.Tensor, ws: torch.Tensor, scale=None,
-                     lse=None, stream=None):
+                     lse=None, stream=None, zero_padding=False):
     """Attention of a step's new tokens over the paged cache, which holds
     their K and V already.  The rest as :func:`nvfp4_attn_prompt`."""
-    io = _attn_io(plan, q, out, scale, lse)
+    io = _attn_io(plan, q, out, scale, lse, zero_padding)
     _check((_lib or lib()).nvfp4_attn_paged(ctypes.byref(plan._c), ctypes.byref(io), ctypes.byref(cache._c), ws.data_ptr(),
                                   ws.numel() * ws.element_size(), _stream(stream)), "nvfp4_attn_paged")

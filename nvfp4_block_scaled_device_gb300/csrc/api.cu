@@ -799,6 +799,8 @@ int run_attn(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const AttnKV& 
     a.ldo = io->ldo;
     a.ho = io->ho;
     a.lse = io->lse;
+    a.cu_end = io->zero_padding ? step->cu_q + step->requests : nullptr;
+    a.tokens = step->tokens;
     a.heads = (int)step->heads;
     a.kv_heads = (int)step->kv_heads;
     a.group = group;

@@ -1244,6 +1244,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         }
     }
     if (failed) wait_failed(abort_flag, status, failed);
+    if (a.cu_end) {
+        // the rows past the step's last token, a warp to a row (by warps as
+        // they come to the end)
+        const int vecs = a.head_dim / 8, n = a.heads * vecs;
+        for (int64_t t = max(*a.cu_end, 0) + cta + (int)gridDim.x * warp; t < a.tokens; t += gridDim.x * (kThreads / 32)) {
+            for (int x = lane; x < n; x += 32) {
+                const int h = x / vecs;
+                *reinterpret_cast<uint4*>(a.out + t * a.ldo + h * a.ho + 8 * (x - h * vecs)) = make_uint4(0, 0, 0, 0);
+            }
+            if (a.lse)
+                for (int h = lane; h < a.heads; h += 32) a.lse[t * a.heads + h] = -INFINITY;
+        }
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == kWarpMma) {

@@ -98,6 +98,8 @@ struct AttnArgs {
     __nv_bfloat16* out;
     int64_t ldo, ho;
     float* lse;
+    const int32_t* cu_end;   // rows *cu_end .. tokens - 1 of out are zeroed, of lse -inf; NULL: not written
+    int64_t tokens;
     int heads, kv_heads, group, head_dim;
     int row_tokens;      // tokens of a row tile
     int window;

@@ -64,9 +64,7 @@ class ServingLayer:
             scratch = {
                 "h": NVFP4Tensor.empty(T, H, dev), "a": NVFP4Tensor.empty(T, heads * D, dev),
                 "qkv": torch.empty((T, N), dtype=torch.bfloat16, device=dev),
-                # rows past a step's last token are not written by the
-                # attention; they count in the next quantization's scale
-                "attn": torch.zeros((T, heads * D), dtype=torch.bfloat16, device=dev),
+                "attn": torch.empty((T, heads * D), dtype=torch.bfloat16, device=dev),
                 "x1": torch.empty((T, H), dtype=torch.bfloat16, device=dev),
                 "g_inter": torch.ones((1,), dtype=torch.float32, device=dev),
                 "ws_amax": workspace(256, dev), "ws_gemm": workspace(gemm_workspace_bytes(), dev),
@@ -87,11 +85,13 @@ class ServingLayer:
         rows = s["qkv"].view(T, heads + 2 * kv_heads, D)
         q, k, v = rows[:, :heads], rows[:, heads:heads + kv_heads], rows[:, heads + kv_heads:]
         a = s["attn"].view(T, heads, D)
+        # rows of padding count in the next quantization's scale: zero, so that
+        # nothing of an earlier step is left in them
         if self.cache is not None:
             nvfp4_kv_append(k, v, plan, self.cache, stream)
-            nvfp4_attn_paged(q, self.cache, plan, a, s["ws_attn"], stream=stream)
+            nvfp4_attn_paged(q, self.cache, plan, a, s["ws_attn"], stream=stream, zero_padding=True)
         else:
-            nvfp4_attn_prompt(q, k, v, plan, a, s["ws_attn"], stream=stream)
+            nvfp4_attn_prompt(q, k, v, plan, a, s["ws_attn"], stream=stream, zero_padding=True)
         nvfp4_scale_quantize(s["attn"], s["a"], s["ws_amax"], None, self.eps, stream)
         nvfp4_gemm(s["a"], w["o"], s["x1"], x, stream, s["ws_gemm"])
         nvfp4_mlp(s["x1"], self.mlp_norm, w["gate"], w["up"], w["down"], NVFP4_INTER_DYNAMIC, s["g_inter"], out,

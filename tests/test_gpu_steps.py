@@ -4,7 +4,10 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_attn import i32, plan_reference
+import synthetic
+from _gpu import dev
+from test_gpu_attn import i32, plan_reference, rows
+from test_gpu_serving import D, H, HEADS, KV, weights, x_of  # noqa: F401  (weights: the module's fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +60,66 @@ def test_cursor_advanced_in_place(nv, R, q_hi, P, captured):
         ctx += q
         # (the first 3 pages of the list are skipped: the last requests to open one may find none)
         assert nv.device_status() == (100 + 31 if cursor > len(free) else 0)
+
+
+# ------------------------------------------------------------------- padding
+@pytest.mark.parametrize("layout", ["plain", "heads_first", "padded"])
+@pytest.mark.parametrize("lens,pad", [([5, 0, 130], 1), ([1], 700), ([0, 0], 3), ([300, 2], 0)])
+def test_padding_rows_zeroed(nv, layout, lens, pad):
+    """Only where asked for: out 0 and lse -inf past the last token, every
+    other row (and what lies between the rows) bit for bit as without."""
+    H, Hkv, D = 10, 2, 72
+    gen = torch.Generator("cuda").manual_seed(pad)
+    T = sum(lens) + pad
+    q, k, v = (rows(gen, T, h, D, layout) for h in (H, Hkv, Hkv))
+    plan, ws = nv.AttnPlan(len(lens), T, H, Hkv), nv.workspace(nv.attn_workspace_bytes())
+    nv.nvfp4_attn_plan(plan, i32(lens))
+    got = []
+    for zero in (False, True):
+        out, lse = rows(gen, T, H, D, layout), torch.full((T, H), 7.0, device="cuda")
+        whole = out._base if out._base is not None else out
+        whole.fill_(7.0)
+        nv.nvfp4_attn_prompt(q, k, v, plan, out, ws, lse=lse, zero_padding=zero)
+        got.append((whole.clone(), out.clone(), lse))
+        if zero:
+            out[sum(lens):] = 7.0
+            assert torch.equal(whole, got[0][0])
+    n = sum(lens)
+    assert torch.equal(got[0][1][:n], got[1][1][:n]) and torch.equal(got[0][2][:n], got[1][2][:n])
+    assert (got[0][1][n:] == 7.0).all() and (got[0][2][n:] == 7.0).all()
+    assert (got[1][1][n:] == 0.0).all() and torch.isneginf(got[1][2][n:]).all()
+    assert nv.device_status() == 0
+
+
+@pytest.mark.parametrize("cached", [True, False])
+def test_a_step_does_not_depend_on_the_steps_before(nv, weights, cached):
+    """A step with few tokens after one with many (finite, then not) on the
+    same buffers gives what it gives on buffers of its own."""
+    T, R, page = 150, 3, 16
+    cos, sin = (torch.from_numpy(t).cuda() for t in synthetic.rope_tables(T, D))
+    norms = [dev(synthetic.norm_weight(80 + i, H)) for i in range(2)]
+    small, xs = i32([3, 0, 20]), x_of(T, 601)
+
+    def run(before):
+        plan = nv.AttnPlan(R, T, HEADS, KV, **(dict(page_size=page, block_table=10) if cached else {}))
+        cache = nv.KVCache(*(torch.zeros(64, KV, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+        layer = ServingLayer(plan, cache if cached else None, weights[0], *norms, cos, sin)
+        free = torch.arange(30, dtype=torch.int32, device="cuda")
+        out = torch.empty_like(xs)
+        for x in before:
+            nv.nvfp4_attn_plan(plan, i32([9, 140, 1]), None, free + 30 if cached else None)
+            layer.forward(x, out)
+        if cached:
+            plan.block_table.fill_(-1)
+        nv.nvfp4_attn_plan(plan, small, None, free if cached else None)
+        layer.forward(xs, out)
+        torch.cuda.synchronize()
+        return out
+
+    from nvfp4_block_scaled_device_gb300.serving import ServingLayer
+    large, broken = 50.0 * x_of(T, 602), x_of(T, 603)
+    broken[100] = float("inf")
+    alone = run([])
+    assert torch.isfinite(alone.float()).all()
+    assert torch.equal(run([large]), alone) and torch.equal(run([broken]), alone)
+    assert nv.device_status() == 0

@@ -25,3 +25,8 @@ def test_lengths_beside_the_outputs_are_not(nv, good):
     if torch.cuda.is_available():
         pytest.skip("the addresses are not memory")
     assert nv.lib().nvfp4_attn_plan(step(nv, **{**APART, **good}), None) != INVALID
+
+
+def test_zero_padding_fits_the_old_struct(nv):
+    """The flag lies in what was padding at the struct's end."""
+    assert ctypes.sizeof(nv._AttnIOC) == 72 and nv._AttnIOC.zero_padding.offset == 68
