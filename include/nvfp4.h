@@ -238,7 +238,7 @@ int nvfp4_gemm(const nvfp4_tensor_t* A, const nvfp4_tensor_t* W,
 
 /* Rotary embedding applied by nvfp4_gemm_rope (all pointers DEVICE). */
 typedef struct {
-    const int32_t* pos;   /* int32 [M]: position of each output row, in [0, positions) (not checked on the device) */
+    const int32_t* pos;   /* int32 [M]: position of each output row, in [0, positions) (below) */
     const float* cos_t;   /* fp32 [positions x table_ld]: cos of the angle of (position, pair i) at [p*table_ld + i] */
     const float* sin_t;   /* fp32, the same layout: sin of that angle */
     int64_t table_ld;     /* floats per table row, >= rope_dim / 2 */
@@ -262,7 +262,9 @@ typedef struct {
  * c = cos_t[pos[m]*table_ld + i], s = sin_t[...]:
  *   forward: e' = e*c - o*s,  o' = e*s + o*c;  inverse: e' = e*c + o*s,  o' = o*c - e*s
  * each product, sum and difference one binary32 operation, then rounded to
- * bf16; every other column is nvfp4_gemm's output.
+ * bf16; every other column is nvfp4_gemm's output.  A position outside the
+ * tables takes their first or last row, whichever is nearer, and records
+ * NVFP4_ERR_INVALID_ARG * 100 + 33 in the device status word.
  *   A, W, out, ldo, workspace  as nvfp4_gemm.
  *   rope     the embedding's tables and geometry (above).
  */

@@ -519,6 +519,7 @@ int run_linear(const nvfp4_tensor_t* A, const nvfp4_tensor_t* W, void* out, int6
         a.rope_hd = rope->head_dim;
         a.rope_rd = rope->rope_dim;
         a.rope_inverse = rope->inverse ? 1 : 0;
+        a.rope_positions = (int)(rope->positions < INT32_MAX ? rope->positions : INT32_MAX);
     }
     if (workspace) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);

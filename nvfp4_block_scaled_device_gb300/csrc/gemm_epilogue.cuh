@@ -38,9 +38,14 @@ __device__ __forceinline__ RopeCursor rope_begin(const GemmArgs& a, int64_t row,
     const int64_t head = rel >= 0 ? rel / a.rope_hd : -((-rel + a.rope_hd - 1) / a.rope_hd);
     k.head = (int32_t)head;
     k.within = (int32_t)(rel - head * a.rope_hd);
-    const int64_t p = a.rope_pos[row];
-    k.c = a.rope_cos + p * a.rope_ld;
-    k.s = a.rope_sin + p * a.rope_ld;
+    int32_t p = a.rope_pos[row];
+    if ((uint32_t)p >= (uint32_t)a.rope_positions) {
+        // outside the tables: the nearest row, and reported
+        if (a.status) atomicCAS(a.status, 0, kStatusRope);
+        p = p < 0 ? 0 : a.rope_positions - 1;
+    }
+    k.c = a.rope_cos + (int64_t)p * a.rope_ld;
+    k.s = a.rope_sin + (int64_t)p * a.rope_ld;
     return k;
 }
 

@@ -67,6 +67,10 @@ cudaError_t launch_scale_quantize(const __nv_bfloat16* x, int64_t rows, int64_t 
                                   int64_t ld_codes, uint8_t* sf, uint32_t* ws, int* status, int num_sms,
                                   cudaStream_t stream);
 
+// Device status of a rotary position outside the tables (NVFP4_ERR_INVALID_ARG
+// * 100 + site).
+constexpr int kStatusRope = NVFP4_ERR_INVALID_ARG * 100 + 33;
+
 enum EpilogueKind : int {
     kEpiBf16 = 0,        // out = bf16(alpha * acc) [+ residual]
     kEpiSwigluFp4 = 1,   // s = SwiGLU(gate, up) requantized to FP4 with a given scale
@@ -118,12 +122,14 @@ struct GemmArgs {
     // rope_pos NULL: none).  In each of the rope_heads heads of rope_hd
     // columns from column rope_col0, the last rope_rd columns form (even,
     // odd) pairs rotated by the angles of table row rope_pos[row] (rope_cos,
-    // rope_sin: rope_ld floats a row); rope_inverse: the inverse rotation
+    // rope_sin: rope_positions rows of rope_ld floats; a position outside
+    // them takes the nearest row and is reported); rope_inverse: the inverse
+    // rotation
     const int32_t* rope_pos;
     const float* rope_cos;
     const float* rope_sin;
     int64_t rope_ld, rope_col0, rope_heads, rope_hd, rope_rd;
-    int rope_inverse;
+    int rope_inverse, rope_positions;
     // grouped (expert-indexed) mode of the 1-SM kernel, from tables built on
     // the device (launch_gemm_grouped): A is the expert-sorted operand of
     // args.M rows (each expert's rows padded to 128); B the experts' weights

@@ -48,7 +48,8 @@ class ServingLayer:
         """weights: NVFP4Tensor values under 'qkv' [(heads + 2 kv_heads) D x H],
         'o' [H x heads D], 'gate', 'up' [I x H], 'down' [H x I]; cos_t, sin_t:
         the rotary tables of nvfp4_gemm_rope, as wide as half the rotated
-        columns."""
+        columns (a position past their last row is reported in the device
+        status and rotated as that row)."""
         self.plan, self.cache, self.w, self.eps = plan, cache, weights, eps
         self.attn_norm, self.mlp_norm, self.cos_t, self.sin_t = attn_norm, mlp_norm, cos_t, sin_t
         T, H, I = plan.tokens, weights["o"].rows, weights["gate"].rows
