@@ -247,13 +247,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
     if (paged && s.free_pages) {
         // the pages opened, a warp per request
         for (int r = blockIdx.x * kPlanWarps + warp; r < R; r += blocks * kPlanWarps) {
-            const int64_t have = (ctx[r] + round) >> sft, taken = first[r + 1] - first[r];
-            for (int64_t x = lane; x < taken; x += 32) {
-                const int64_t at = cursor + first[r] + x, j = have + x;
-                const bool ok = at >= 0 && at < s.free_count && j < s.table_cols;
-                if (j < s.table_cols) s.block_table[r * s.table_ld + j] = ok ? __ldg(s.free_pages + at) : -1;
-                if (!ok) report(p.status, kStatusPlan);
+            const int64_t have = (ctx[r] + round) >> sft;
+            // (first: exact below its limit)
+            const int64_t taken = first[r + 1] < kIntMax ? first[r + 1] - first[r]
+                                                         : pages_opened(ctx[r], max(__ldg(s.q_len + r), 0), sft);
+            // (no further than the table's last column, whatever the lengths ask for)
+            const int64_t room = max(s.table_cols - have, (int64_t)0), n = min(taken, room);
+            bool missing = taken > room;
+            for (int64_t x = lane; x < n; x += 32) {
+                const int64_t at = cursor + first[r] + x;
+                const bool ok = at >= 0 && at < s.free_count;
+                s.block_table[r * s.table_ld + have + x] = ok ? __ldg(s.free_pages + at) : -1;
+                missing |= !ok;
             }
+            if (missing) report(p.status, kStatusPlan);
         }
         if (blockIdx.x == 0 && t == 0 && s.cursor_out && s.cursor_out != s.cursor)
             *s.cursor_out = (int32_t)min(cursor + total_n, kIntMax);

@@ -62,6 +62,33 @@ def test_cursor_advanced_in_place(nv, R, q_hi, P, captured):
         assert nv.device_status() == (100 + 31 if cursor > len(free) else 0)
 
 
+@pytest.mark.parametrize("R", [1, 33, 8192])
+def test_lengths_far_beyond_the_tables(nv, R):
+    """Lengths that are not lengths (2^31 - 1 new tokens each) cost no more than
+    the tables have room for: pages for the columns there are, as long as the
+    list has some, and a report."""
+    cols, huge = 3, 2 ** 31 - 1
+    free = i32([7, 9])
+    plan = nv.AttnPlan(R, 40, 8, 2, page_size=16, block_table=cols)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    for ctx in (None, i32([16] * R), i32([huge] * R)):
+        plan.block_table.fill_(-5)
+        torch.cuda.synchronize()
+        start.record()
+        nv.nvfp4_attn_plan(plan, i32([huge] * R), ctx, free)
+        end.record()
+        torch.cuda.synchronize()
+        assert nv.device_status() == 100 + 31 and start.elapsed_time(end) < 50
+        have = 0 if ctx is None else min(cols, (int(ctx[0]) + 15) // 16)
+        want = np.full((R, cols), -5, np.int64)
+        want[:, have:] = -1
+        want[0, have:min(cols, have + 2)] = [7, 9][:cols - have]
+        assert np.array_equal(plan.block_table.cpu().numpy(), want)
+        taken = 2 ** 27 if ctx is None or int(ctx[0]) == huge else (16 + huge + 15) // 16 - 1
+        assert plan.cursor.item() == min(huge, R * taken)
+        assert plan.cu_q.tolist() == [0] + [40] * R
+
+
 # ------------------------------------------------------------------- padding
 @pytest.mark.parametrize("layout", ["plain", "heads_first", "padded"])
 @pytest.mark.parametrize("lens,pad", [([5, 0, 130], 1), ([1], 700), ([0, 0], 3), ([300, 2], 0)])
