@@ -474,8 +474,10 @@ size_t nvfp4_attn_workspace_bytes(void);
  * Rows past the last token get pos 0 and slot -1.  A negative length counts as
  * 0; tokens past `tokens` are dropped; a row whose page does not exist (the
  * free list ran out, the table has no such column) gets slot -1, its table
- * entry -1.  Each of these records NVFP4_ERR_INVALID_ARG * 100 + 31 in the
- * device status word.  *cursor_out counts the pages asked for, so that a value
+ * entry -1.  A schedule of more than 2^30 units (2 + ceil(keys / 128) for each
+ * kv head of each tile of rows) ends with the last whole item before that; the
+ * rows behind get no attention.  Each of these records
+ * NVFP4_ERR_INVALID_ARG * 100 + 31 in the device status word.  *cursor_out counts the pages asked for, so that a value
  * above free_count tells how many were missing.  q_len and ctx_len are none of
  * the outputs (a loop keeps its own ctx_len beside kv_len).
  */
@@ -508,7 +510,9 @@ int nvfp4_kv_append(const void* k, int64_t ldk, int64_t hk, const void* v, int64
  *            and ctx_len NULL.
  *   k, v     as nvfp4_kv_append.
  *   workspace nvfp4_attn_workspace_bytes() bytes, 256-B aligned, zero-filled
- *            once after allocation; calls sharing it must be stream-ordered.
+ *            once after allocation (calls leave its counters zeroed; after a
+ *            reported timeout zero it again); calls sharing it must be
+ *            stream-ordered.
  */
 int nvfp4_attn_prompt(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const void* k, int64_t ldk, int64_t hk,
                       const void* v, int64_t ldv, int64_t hv, void* workspace, size_t workspace_bytes,

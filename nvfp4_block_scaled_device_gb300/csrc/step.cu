@@ -153,7 +153,15 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, const int
     atomicMax(longest, __reduce_max_sync(0xffffffffu, most));
     block_prefix(unit, unused, warp_sums, &units, &unused_total);   // (its barriers order *longest too)
     if (units > kMaxUnits) {
-        units = kMaxUnits;
+        // ends with a whole item (one cut off would never collect its tickets)
+        int64_t at = unit;
+        for (int i = i0, r = r0; i < i1 && at <= kMaxUnits; i++) {
+            const int64_t item = kItemUnits + tile_of(i, r).tiles, next = at + item * Hkv;
+            if (next > kMaxUnits) *longest = (int)(at + (kMaxUnits - at) / item * item);
+            at = next;
+        }
+        __syncthreads();
+        units = *longest;
         if (t == 0) report(p.status, kStatusPlan);
     }
     const int share = (int)((units + p.ctas - 1) / p.ctas);

@@ -89,6 +89,18 @@ def test_lengths_far_beyond_the_tables(nv, R):
         assert plan.cu_q.tolist() == [0] + [40] * R
 
 
+@pytest.mark.parametrize("R,Hkv,ctx", [(64, 2, 2 ** 30 - 1), (300, 1, 2 ** 29 + 12345), (3, 80, 2 ** 30 - 1)])
+def test_a_schedule_too_long_ends_with_a_whole_item(nv, R, Hkv, ctx):
+    """Only the step's tables: no attention runs on them."""
+    plan = nv.AttnPlan(R, R, 4 * Hkv, Hkv)
+    nv.nvfp4_attn_plan(plan, i32([1] * R), i32([ctx] * R))
+    assert nv.device_status() == 100 + 31
+    units, per_cta, qtiles = plan.schedule.view(torch.int32)[:3].tolist()
+    item = 2 + (ctx + 1 + 127) // 128                    # units of one kv head of one request
+    assert R * Hkv * item > 2 ** 30
+    assert units == 2 ** 30 // item * item and qtiles == R
+
+
 # ------------------------------------------------------------------- padding
 @pytest.mark.parametrize("layout", ["plain", "heads_first", "padded"])
 @pytest.mark.parametrize("lens,pad", [([5, 0, 130], 1), ([1], 700), ([0, 0], 3), ([300, 2], 0)])
