@@ -476,7 +476,8 @@ size_t nvfp4_attn_workspace_bytes(void);
  * free list ran out, the table has no such column) gets slot -1, its table
  * entry -1.  A schedule of more than 2^30 units (2 + ceil(keys / 128) for each
  * kv head of each tile of rows) ends with the last whole item before that; the
- * rows behind get no attention.  Each of these records
+ * rows behind get no attention, nor do rows at positions from 2^30 on a right
+ * one.  Each of these records
  * NVFP4_ERR_INVALID_ARG * 100 + 31 in the device status word.  *cursor_out counts the pages asked for, so that a value
  * above free_count tells how many were missing.  q_len and ctx_len are none of
  * the outputs (a loop keeps its own ctx_len beside kv_len).

@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
             const int r = last_at_or_below(cu, R, i);     // the request that row i is of
             const int64_t at = (int64_t)ctx[r] + (i - cu[r]);
             pos = (int)min(at, kIntMax);
+            if (s.heads && at >= kMaxPosition) report(p.status, kStatusPlan);   // beyond the schedule's positions
             if (paged) {
                 const int64_t j = at >> sft, have = (ctx[r] + round) >> sft;
                 int64_t page = -1;

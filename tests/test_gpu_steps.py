@@ -101,6 +101,17 @@ def test_a_schedule_too_long_ends_with_a_whole_item(nv, R, Hkv, ctx):
     assert units == 2 ** 30 // item * item and qtiles == R
 
 
+def test_positions_beyond_the_schedule_are_reported(nv):
+    P = 128
+    table = torch.zeros((1, 2 ** 30 // P + 1), dtype=torch.int32, device="cuda")
+    for heads, ctx, n, status in ((8, 2 ** 30 - 2, 2, 0), (8, 2 ** 30 - 2, 3, 131), (8, 2 ** 30, 1, 131), (0, 2 ** 30, 1, 0)):
+        plan = nv.AttnPlan(1, n, 8, 2, page_size=P, block_table=table)
+        plan._c.heads = heads                            # (0: tables without a schedule)
+        nv.nvfp4_attn_plan(plan, i32([n]), i32([ctx]))
+        assert plan.pos.tolist() == [ctx + t for t in range(n)]
+        assert plan.slot.tolist() == [(ctx + t) % P for t in range(n)] and nv.device_status() == status
+
+
 # ------------------------------------------------------------------- padding
 @pytest.mark.parametrize("layout", ["plain", "heads_first", "padded"])
 @pytest.mark.parametrize("lens,pad", [([5, 0, 130], 1), ([1], 700), ([0, 0], 3), ([300, 2], 0)])
