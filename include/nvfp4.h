@@ -493,6 +493,8 @@ int nvfp4_attn_plan(const nvfp4_step_t* step, nvfp4_stream_t stream);
  *   slot     int32 [tokens]; -1 is skipped; any other value outside the cache
  *            is skipped and records NVFP4_ERR_INVALID_ARG * 100 + 32.  No slot
  *            appears twice.
+ *   cache    its page_size is the one of the step that made the slots (which a
+ *            slot does not tell).
  */
 int nvfp4_kv_append(const void* k, int64_t ldk, int64_t hk, const void* v, int64_t ldv, int64_t hv,
                     const int32_t* slot, int64_t tokens, const nvfp4_kv_cache_t* cache, nvfp4_stream_t stream);

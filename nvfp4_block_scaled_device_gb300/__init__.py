@@ -482,6 +482,8 @@ def nvfp4_kv_append(k: torch.Tensor, v: torch.Tensor, plan: AttnPlan, cache: KVC
     column slices of a QKV projection's output) into the cache's slots plan.slot."""
     if plan.slot is None:
         raise ValueError("the plan has no paged cache (page_size 0)")
+    if plan.page_size != cache.page_size:        # (a slot is page * page_size + row)
+        raise ValueError(f"the plan's pages of {plan.page_size} tokens are not the cache's of {cache.page_size}")
     kp = _heads_3d(k, "k", plan.tokens, cache.kv_heads, cache.head_dim)
     vp = _heads_3d(v, "v", plan.tokens, cache.kv_heads, cache.head_dim)
     _check((_lib or lib()).nvfp4_kv_append(*kp, *vp, plan.slot.data_ptr(), plan.tokens, ctypes.byref(cache._c),

@@ -60,6 +60,9 @@ class ServingLayer:
             raise ValueError("qkv and o do not fit the plan's heads")
         if bool(plan.page_size) != (cache is not None):
             raise ValueError("a plan with pages goes with a cache, one without goes without")
+        if cache is not None and (cache.page_size, cache.kv_heads, cache.head_dim) != (plan.page_size, kv_heads, D):
+            raise ValueError(f"a cache of pages of {cache.page_size} tokens, {cache.kv_heads} heads of {cache.head_dim} "
+                             f"columns does not fit a plan of {plan.page_size}, {kv_heads} and {D}")
         dev = attn_norm.device
         if scratch is None:
             scratch = {

@@ -30,3 +30,27 @@ def test_lengths_beside_the_outputs_are_not(nv, good):
 def test_zero_padding_fits_the_old_struct(nv):
     """The flag lies in what was padding at the struct's end."""
     assert ctypes.sizeof(nv._AttnIOC) == 72 and nv._AttnIOC.zero_padding.offset == 68
+
+
+class Shape:
+    """What the checks look at of a plan or a cache."""
+
+    def __init__(self, **f):
+        self.__dict__.update(f)
+
+
+def test_append_refuses_other_pages(nv):
+    """Before it looks at k and v: slots of pages of another size name other rows."""
+    for plan, cache in ((16, 32), (128, 64)):
+        with pytest.raises(ValueError, match="pages of"):
+            nv.nvfp4_kv_append(None, None, Shape(slot=1, page_size=plan, tokens=1), Shape(page_size=cache))
+
+
+@pytest.mark.parametrize("bad", [dict(page_size=64), dict(kv_heads=4), dict(head_dim=32)])
+def test_serving_layer_refuses_a_cache_that_does_not_fit(nv, bad):
+    from nvfp4_block_scaled_device_gb300.serving import ServingLayer
+    plan = Shape(tokens=4, heads=4, kv_heads=2, page_size=32)
+    weights = {k: Shape(rows=r, cols=c) for k, r, c in (("qkv", 512, 256), ("o", 256, 256), ("gate", 512, 256))}
+    cache = Shape(**{**dict(page_size=32, kv_heads=2, head_dim=64), **bad})
+    with pytest.raises(ValueError, match="does not fit"):
+        ServingLayer(plan, cache, weights, None, None, None, None)
