@@ -437,6 +437,8 @@ class AttnPlan:
         self.requests, self.tokens, self.heads, self.kv_heads = requests, tokens, heads, kv_heads
         self.page_size, self.window = page_size, window
         if isinstance(block_table, torch.Tensor):
+            if block_table.dim() == 2 and requests > 1 and block_table.stride(0) < block_table.shape[1]:
+                raise ValueError("block_table's rows overlap (an expanded tensor has to be made contiguous)")
             if block_table.dtype != torch.int32 or not block_table.is_cuda or block_table.dim() != 2 or \
                     block_table.shape[0] < requests or block_table.stride(1) != 1:
                 raise ValueError("block_table must be a CUDA int32 [requests, pages] tensor with unit column stride")

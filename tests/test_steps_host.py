@@ -54,3 +54,12 @@ def test_serving_layer_refuses_a_cache_that_does_not_fit(nv, bad):
     cache = Shape(**{**dict(page_size=32, kv_heads=2, head_dim=64), **bad})
     with pytest.raises(ValueError, match="does not fit"):
         ServingLayer(plan, cache, weights, None, None, None, None)
+
+
+def test_plan_refuses_a_table_with_overlapping_rows(nv):
+    """Its pitch was taken to be a row's width: rows past the first lay outside the tensor."""
+    import torch
+    row = torch.zeros((1, 8), dtype=torch.int32)
+    for table in (row.expand(4, 8), torch.zeros(14, dtype=torch.int32).as_strided((4, 8), (2, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            nv.AttnPlan(4, 4, 8, 2, page_size=16, block_table=table)
