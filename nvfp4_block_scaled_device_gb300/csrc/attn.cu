@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 // this lane's page of tiles i - 1, i, i + 1
                 auto page_of = [&](int i) {
                     const int at = (p.tile0 + i) * ppt + pg;
-                    return paged && i < p.n && at * a.page_size < p.kv_end ? __ldg(table + at) : 0;
+                    return paged && i < p.n && at * a.page_size < p.kv_end ? table[at] : 0;
                 };
                 int page0 = 0, page1 = page_of(0), page2 = page_of(1);
 #pragma unroll 1

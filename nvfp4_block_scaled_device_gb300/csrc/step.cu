@@ -194,7 +194,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
     __shared__ int64_t s_sums[kPlanWarps][2];
     __shared__ int s_longest;
     griddep_launch_dependents();
-    griddep_wait();                 // the lengths may come from the previous kernel
+    // (The lengths may come from the previous kernel, and what it writes while
+    // this one is already there is no constant: plain loads, not __ldg, here
+    // and in the other kernels of a step.)
+    griddep_wait();
     const nvfp4_step_t& s = p.s;
     const int R = (int)s.requests;
     const bool paged = s.page_size != 0;
@@ -205,12 +208,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
     const int64_t P = paged ? s.page_size : 1, round = P - 1;
     const int sft = p.page_shift;
     const int64_t kIntMax = 0x7fffffff;
-    const int64_t cursor = paged && s.cursor ? __ldg(s.cursor) : 0;
+    const int64_t cursor = paged && s.cursor ? *s.cursor : 0;
 
     // the lengths, negative ones as zero
     bool bad = false;
     for (int r = t; r < R; r += kPlanThreads) {
-        const int q = __ldg(s.q_len + r), c = s.ctx_len ? __ldg(s.ctx_len + r) : 0;
+        const int q = s.q_len[r], c = s.ctx_len ? s.ctx_len[r] : 0;
         bad |= q < 0 || c < 0;
         cu[r] = max(q, 0);
         ctx[r] = max(c, 0);
@@ -258,14 +261,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
             const int64_t have = (ctx[r] + round) >> sft;
             // (first: exact below its limit)
             const int64_t taken = first[r + 1] < kIntMax ? first[r + 1] - first[r]
-                                                         : pages_opened(ctx[r], max(__ldg(s.q_len + r), 0), sft);
+                                                         : pages_opened(ctx[r], max(s.q_len[r], 0), sft);
             // (no further than the table's last column, whatever the lengths ask for)
             const int64_t room = max(s.table_cols - have, (int64_t)0), n = min(taken, room);
             bool missing = taken > room;
             for (int64_t x = lane; x < n; x += 32) {
                 const int64_t at = cursor + first[r] + x;
                 const bool ok = at >= 0 && at < s.free_count;
-                s.block_table[r * s.table_ld + have + x] = ok ? __ldg(s.free_pages + at) : -1;
+                s.block_table[r * s.table_ld + have + x] = ok ? s.free_pages[at] : -1;
                 missing |= !ok;
             }
             if (missing) report(p.status, kStatusPlan);
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
                         page = s.block_table[r * s.table_ld + j];
                     } else {
                         const int64_t f = cursor + first[r] + (j - have);
-                        if (f >= 0 && f < s.free_count) page = __ldg(s.free_pages + f);
+                        if (f >= 0 && f < s.free_count) page = s.free_pages[f];
                     }
                 }
                 const int64_t sl = page * P + (at & round);
@@ -365,7 +368,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
         bool ok[kAppendRows];
 #pragma unroll
         for (int u = 0; u < kAppendRows; u++) {
-            const int64_t sl = t0 + u < p.tokens ? __ldg(p.slot + t0 + u) : -1;
+            const int64_t sl = t0 + u < p.tokens ? p.slot[t0 + u] : -1;
             ok[u] = sl >= 0 && sl < slots;
             if (!ok[u] && sl != -1 && threadIdx.x == 0) report(p.status, kStatusSlot);
             dst[u] = (sl >> p.page_shift) * p.c.page_stride + (sl & mask) * p.c.head_dim;
@@ -380,7 +383,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
             uint4 val[kAppendRows];
 #pragma unroll
             for (int u = 0; u < kAppendRows; u++)
-                if (ok[u]) val[u] = __ldg(reinterpret_cast<const uint4*>(src + (t0 + u) * ld));
+                if (ok[u]) val[u] = *reinterpret_cast<const uint4*>(src + (t0 + u) * ld);
 #pragma unroll
             for (int u = 0; u < kAppendRows; u++)
                 if (ok[u]) *reinterpret_cast<uint4*>(out + dst[u]) = val[u];
