@@ -453,7 +453,7 @@ typedef struct {
     int64_t ldo, ho;
     float* lse;                /* NULL, or fp32 [tokens x heads]: log of the row's sum of exp(score) */
     int64_t head_dim;          /* 16 .. 128, % 8 == 0 */
-    float scale;               /* score = scale * q.k */
+    float scale;               /* score = scale * q.k; finite, at most FLT_MAX / 1.5 */
     int32_t zero_padding;      /* rows of padding (cu_q[R] .. tokens - 1): 0 not written; else out 0, lse -inf */
 } nvfp4_attn_io_t;
 

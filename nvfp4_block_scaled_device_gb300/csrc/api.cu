@@ -3,6 +3,8 @@
 // Nothing here allocates device memory or synchronises the stream (except
 // nvfp4_device_status, a diagnostic).
 #include <cudaTypedefs.h>
+#include <float.h>
+#include <math.h>
 
 #include <mutex>
 
@@ -827,7 +829,9 @@ int check_io(const nvfp4_step_t* step, const nvfp4_attn_io_t* io)
     if (!io) return NVFP4_ERR_INVALID_ARG;
     NVFP4_TRY(check_head_dim(io->head_dim));
     NVFP4_TRY(check_rows(io->q, step->tokens, step->heads, io->head_dim, io->ldq, io->hq));
-    return check_rows(io->out, step->tokens, step->heads, io->head_dim, io->ldo, io->ho);
+    NVFP4_TRY(check_rows(io->out, step->tokens, step->heads, io->head_dim, io->ldo, io->ho));
+    // scores in units of log2 (scale * 1.44) are binary32 too
+    return fabsf(io->scale) <= FLT_MAX / 1.5f ? NVFP4_OK : NVFP4_ERR_INVALID_ARG;
 }
 
 }  // namespace

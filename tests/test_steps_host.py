@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from test_attn_host import INVALID, nv, step  # noqa: F401  (nv: the module's fixture)
+from test_attn_host import INVALID, cache, io, nv, step  # noqa: F401  (nv: the module's fixture)
 
 MB = 1 << 20
 APART = dict(requests=4, tokens=64, q_len=MB, ctx_len=2 * MB, cu_q=3 * MB, kv_len=4 * MB, pos=5 * MB, slot=6 * MB,
@@ -63,3 +63,19 @@ def test_plan_refuses_a_table_with_overlapping_rows(nv):
     for table in (row.expand(4, 8), torch.zeros(14, dtype=torch.int32).as_strided((4, 8), (2, 1))):
         with pytest.raises(ValueError, match="overlap"):
             nv.AttnPlan(4, 4, 8, 2, page_size=16, block_table=table)
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), float("-inf"), 3e38, -3e38])
+def test_attention_refuses_scales_that_are_not_finite(nv, scale):
+    """They ran as a scale of 0, or as an infinite one."""
+    L, ws = nv.lib(), (MB, 1 << 40, None)
+    assert L.nvfp4_attn_paged(step(nv), io(nv, scale=scale), cache(nv), *ws) == INVALID
+    assert L.nvfp4_attn_prompt(step(nv), io(nv, scale=scale), MB, 256, 128, MB, 256, 128, *ws) == INVALID
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, 1e-38, 2e38])
+def test_attention_takes_any_other_scale(nv, scale):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not memory")
+    assert nv.lib().nvfp4_attn_paged(step(nv), io(nv, scale=scale), cache(nv), MB, 1 << 40, None) != INVALID
