@@ -510,7 +510,10 @@ int nvfp4_kv_append(const void* k, int64_t ldk, int64_t hk, const void* v, int64
  * A value that is not finite can make rows of its own request NaN that do not
  * see its key (0 * NaN), never another request's.
  *   step     after nvfp4_attn_plan on the same stream order, with a schedule
- *            and ctx_len NULL.
+ *            and ctx_len NULL.  A step with pages serves too (its slots take the
+ *            same prompts into the cache), as far as its block table reaches:
+ *            a request's keys from table_cols * page_size on, which the plan
+ *            reports, are seen by no row.
  *   k, v     as nvfp4_kv_append.
  *   workspace nvfp4_attn_workspace_bytes() bytes, 256-B aligned, zero-filled
  *            once after allocation (calls leave its counters zeroed; after a

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import synthetic
+from _attn import check
 from _gpu import dev
 from test_gpu_attn import i32, plan_reference, rows
 from test_gpu_serving import D, H, HEADS, KV, weights, x_of  # noqa: F401  (weights: the module's fixture)
@@ -173,3 +174,33 @@ def test_a_step_does_not_depend_on_the_steps_before(nv, weights, cached):
     assert torch.isfinite(alone.float()).all()
     assert torch.equal(run([large]), alone) and torch.equal(run([broken]), alone)
     assert nv.device_status() == 0
+
+
+@pytest.mark.parametrize("window", [0, 40])
+def test_packed_prompts_of_a_step_with_pages(nv, window):
+    """Bit for bit as without pages where the block table reaches, and no keys
+    past it (reported by the plan)."""
+    lens, heads, kv, d, page = [150, 0, 33, 96], 10, 2, 64, 16
+    gen = torch.Generator("cuda").manual_seed(window)
+    T = sum(lens)
+    q, k, v = (rows(gen, T, h, d, "plain", 1.5) for h in (heads, kv, kv))
+    got = []
+    for cols in (None, 10, 6):                      # none, enough for 150 tokens, for 96
+        plan = nv.AttnPlan(len(lens), T, heads, kv, window=window, **({"page_size": page, "block_table": cols} if cols else {}))
+        out, lse = torch.empty_like(q), torch.empty(T, heads, device="cuda")
+        nv.nvfp4_attn_plan(plan, i32(lens), None, torch.arange(99, dtype=torch.int32, device="cuda") if cols else None)
+        assert nv.device_status() == (131 if cols == 6 else 0)
+        nv.nvfp4_attn_prompt(q, k, v, plan, out, nv.workspace(nv.attn_workspace_bytes()), lse=lse)
+        got.append((out, lse))
+    for a, b, c in zip(*got):
+        assert torch.equal(a, b) and torch.equal(c[:96], a[:96]) and torch.equal(c[150:], a[150:])
+    # the rows past the table: keys up to its end, within their window
+    p = torch.arange(150, device="cuda")[:, None]
+    j = torch.arange(96, device="cuda")
+    seen = (j <= p) & (j > p - window if window else j >= 0)
+    for h in range(heads):
+        s = (q[:150, h].double() @ k[:96, h // 5].double().T / d ** 0.5).masked_fill(~seen, -float("inf"))
+        ref = torch.logsumexp(s, 1)
+        w = torch.where(seen, torch.exp(s - ref.clamp(min=-1e300)[:, None]), 0.0)
+        check(got[2][0][:150, h], got[2][1][:150, h], w @ v[:96, h // 5].double(), w @ v[:96, h // 5].double().abs(), ref,
+              f"head {h}")
