@@ -75,6 +75,10 @@ class ServingLayer:
                 "ws_attn": workspace(attn_workspace_bytes(), dev),
                 "ws_mlp": workspace(mlp_workspace_bytes(T, H, I, NVFP4_INTER_DYNAMIC), dev),
             }
+        elif not (scratch["h"].rows == scratch["a"].rows == T and scratch["h"].cols == H and
+                  scratch["a"].cols == heads * D and tuple(scratch["qkv"].shape) == (T, N) and
+                  scratch["ws_mlp"].numel() >= mlp_workspace_bytes(T, H, I, NVFP4_INTER_DYNAMIC)):
+            raise ValueError("scratch is a layer's of other sizes")
         self.scratch = scratch
 
     def forward(self, x: torch.Tensor, out: torch.Tensor, stream=None):
@@ -83,6 +87,8 @@ class ServingLayer:
         last token hold what their x gives."""
         s, plan, w = self.scratch, self.plan, self.w
         T, heads, kv_heads, D = plan.tokens, plan.heads, plan.kv_heads, self.head_dim
+        if x.shape != s["x1"].shape or out.shape != x.shape:
+            raise ValueError(f"x and out must be {tuple(s['x1'].shape)}, not {tuple(x.shape)} and {tuple(out.shape)}")
         nvfp4_scale_quantize(x, s["h"], s["ws_amax"], self.attn_norm, self.eps, stream)
         nvfp4_gemm_rope(s["h"], w["qkv"], s["qkv"], plan.pos, self.cos_t, self.sin_t, 0, heads + kv_heads, D,
                         2 * self.cos_t.shape[1], False, stream, s["ws_gemm"])

@@ -79,3 +79,36 @@ def test_attention_takes_any_other_scale(nv, scale):
     if torch.cuda.is_available():
         pytest.skip("the addresses are not memory")
     assert nv.lib().nvfp4_attn_paged(step(nv), io(nv, scale=scale), cache(nv), MB, 1 << 40, None) != INVALID
+
+
+def layer_scratch(T, heads, N, H):
+    import torch
+    return {"h": Shape(rows=T, cols=H), "a": Shape(rows=T, cols=heads * 64), "qkv": torch.empty(T, N),
+            "x1": torch.empty(T, H), "ws_mlp": torch.empty(1 << 24, dtype=torch.uint8)}
+
+
+def serving_layer(T, scratch, heads=4):
+    from nvfp4_block_scaled_device_gb300.serving import ServingLayer
+    plan = Shape(tokens=T, heads=heads, kv_heads=2, page_size=0)
+    N = (heads + 4) * 64
+    weights = {k: Shape(rows=r, cols=c) for k, r, c in (("qkv", N, 256), ("o", 256, heads * 64), ("gate", 512, 256))}
+    return ServingLayer(plan, None, weights, Shape(device="cpu"), None, None, None, scratch=scratch)
+
+
+def test_serving_layer_refuses_scratch_of_other_sizes(nv):
+    """A larger step's rows were written past a smaller one's buffers."""
+    serving_layer(8, layer_scratch(8, 4, 512, 256))
+    for bad in (layer_scratch(7, 4, 512, 256), layer_scratch(8, 2, 512, 256), layer_scratch(8, 4, 448, 256),
+                layer_scratch(8, 4, 512, 192), {**layer_scratch(8, 4, 512, 256), "ws_mlp": layer_scratch(1, 1, 1, 1)["x1"]}):
+        with pytest.raises(ValueError, match="other sizes"):
+            serving_layer(8, bad)
+
+
+def test_serving_layer_refuses_rows_that_are_not_the_plan_s(nv):
+    """Before anything is launched."""
+    import torch
+    layer = serving_layer(8, layer_scratch(8, 4, 512, 256))
+    x = torch.empty(8, 256)
+    for a, b in ((torch.empty(9, 256), torch.empty(9, 256)), (x, torch.empty(7, 256)), (torch.empty(8, 320), x)):
+        with pytest.raises(ValueError, match="must be"):
+            layer.forward(a, b)
