@@ -43,19 +43,19 @@
 //     (4-5 us until the first S) and the items' ends: 64 requests of 200 to 8192
 //     keys 95 us, 5.8 TB/s.
 //   - Long prompts: the tensor pipe and what keeps it from running.  A prompt of
-//     8192: 507 us, 1.35 PFLOP/s.  128 keys against two row tiles take about
+//     8192: 505 to 530 us from run to run, 1.3 PFLOP/s.  128 keys against two row tiles take about
 //     3000 cycles.  The products take 2560 of them: Q K^T of 64 keys reads Q
 //     again (48 KB of shared memory for 384 cycles, where the arithmetic would
 //     take 256), P V 256.  S of 128 keys would not read Q twice, but fills
 //     tensor memory with one S a warpgroup: 587 us (where this took 524), as a
 //     warpgroup then waits for its own products.  The rest is latency from P's
 //     arrival to the next S, and 5000-6000 cycles at an item's end.
-//   - Short prompts: those ends and the start.  17 tokens take 6.6 us.
+//   - Short prompts: those ends and the start.  17 tokens take 6.8 us.
 // The warps of a CTA run four different programs, which drive each other out of
 // the instruction cache; every program's repeated path is kept short.  With
 // loops written out, waits with their own time limits and divisions in the walk
-// over the items (110 KB of code instead of 81) the prompt of 8192 took 525 us,
-// the 64 requests 104.
+// over the items (110 KB of code instead of 81) the prompt of 8192 took 525 us
+// where it then took 508, the 64 requests 104 and 98.
 #include "attn.h"
 #include "common.cuh"
 #include "internal.h"

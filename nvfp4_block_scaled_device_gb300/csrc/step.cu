@@ -7,8 +7,8 @@
 // waiting for a first kernel to do it, then fills its own slice of the
 // tables; so the whole plan is one launch without a grid-wide wait.  The
 // tables are small (a few hundred KB at most): the launch and the dependent
-// reads set the time, not bandwidth (64 decoding requests 5.4 us; 4096 requests
-// of 1 to 13 new tokens 15.4 us).  Only a cursor that is advanced in place is
+// reads set the time, not bandwidth (64 decoding requests 5.6 us; 4096 requests
+// of 1 to 13 new tokens 15.9 us).  Only a cursor that is advanced in place is
 // stored by a second launch (cursor_kernel).
 #include "attn.h"
 #include "common.cuh"
@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
 // when they start, and nothing orders a block's start before another's end: a
 // store from within the plan could reach a block that has yet to read, and give
 // its requests pages that are others'.  So the word changes once the plan has
-// completed, by a block that counts the pages again (2 us more per step).
+// completed, by a block that counts the pages again (64 requests 5.6 us with
+// the cursor apart, 7.0 with it in place; 4096 requests 15.7 and 17.6).
 constexpr int kCursorThreads = 512;
 
 __global__ void __launch_bounds__(kCursorThreads) cursor_kernel(const PlanParams p)
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(kCursorThreads) cursor_kernel(const PlanParams
 // One 16-byte vector of a head's row per thread: a block copies whole packed
 // rows (both K and V, every kv head), kAppendRows of them at a time, all
 // their loads in flight before the first store.  Bound by HBM: 16272 tokens of
-// 8 heads of 128 columns (133 MB read and written) 22.6 us, 5.9 TB/s; a decode
+// 8 heads of 128 columns (133 MB read and written) 22.9 us, 5.8 TB/s; a decode
 // step's 17 tokens 2.0 us.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendRows = 4;

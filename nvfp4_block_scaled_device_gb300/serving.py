@@ -25,7 +25,9 @@ be captured in a CUDA graph and replayed as the contexts grow (plan.cursor count
         ctx_len.add_(q_len)
 
 Plans of different sizes (prompts, decoding) that share the block table, and
-layers that share the cache, serve the same requests.
+layers that share the cache, serve the same requests.  Each plan has a cursor of
+its own: where the next step is another plan's, its cursor is copied first
+(decode.cursor.copy_(prompts.cursor)), or pages are given out twice.
 
 A plan without a cache (page_size 0) runs packed prompts by themselves
 (nvfp4_attn_prompt), e.g. for embeddings or scores.
@@ -41,7 +43,8 @@ from . import (NVFP4_INTER_DYNAMIC, AttnPlan, KVCache, NVFP4Tensor, attn_workspa
 
 class ServingLayer:
     """One layer's buffers, all allocated at construction (layers that run one
-    after the other may share ``scratch`` of an earlier one)."""
+    after the other may share ``scratch`` of an earlier one of the same sizes; the
+    attention's workspace alone is 40 MB)."""
 
     def __init__(self, plan: AttnPlan, cache: KVCache | None, weights: dict, attn_norm: torch.Tensor,
                  mlp_norm: torch.Tensor, cos_t: torch.Tensor, sin_t: torch.Tensor, eps=1e-6, scratch=None):
