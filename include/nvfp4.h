@@ -536,6 +536,178 @@ int nvfp4_attn_prompt(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const
 int nvfp4_attn_paged(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const nvfp4_kv_cache_t* cache,
                      void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
 
+/* -------------------------------------------- norms and rotation of heads
+ *
+ * What lies between a QKV projection and the attention where the model
+ * normalises its query and key heads.
+ */
+
+typedef struct nvfp4_kv4_cache nvfp4_kv4_cache_t;   /* below */
+
+/* Heads of one call: the row of token t, head h of a matrix x starts at
+ * x + t*ldx + h*hx (elements), 16-byte aligned, pitches % 8 == 0. */
+typedef struct {
+    int64_t tokens;            /* >= 1 */
+    int64_t heads, kv_heads;   /* of q and of k and v; one of them may be 0 */
+    int64_t head_dim;          /* 16 .. 128, % 8 == 0 */
+    const void* q;             /* bf16 [tokens][heads][head_dim] */
+    int64_t ldq, hq;
+    void* q_out;               /* likewise; may be q with its pitches */
+    int64_t ldqo, hqo;
+    const void* k;             /* bf16 [tokens][kv_heads][head_dim] */
+    int64_t ldk, hk;
+    void* k_out;               /* likewise; may be k with its pitches; NULL where a cache takes the rows */
+    int64_t ldko, hko;
+    const void* q_norm;        /* bf16 [head_dim]: the norms' weights; NULL: no norm */
+    const void* k_norm;
+    float eps;                 /* >= 0 */
+    const int32_t* pos;        /* [tokens]: position of each token; NULL: no rotation, and the rest is ignored */
+    const float* cos_t;        /* as in nvfp4_rope_t */
+    const float* sin_t;
+    int64_t table_ld, positions;
+    int64_t rope_dim;          /* the LAST rope_dim columns of a head are rotated; even, <= head_dim */
+    int32_t halves;            /* pairs: 0 (2i, 2i+1); else (i, i + rope_dim/2), rope_dim % 16 == 0, of those columns */
+    /* a cache that takes the k rows and those of v (slot NULL: none) */
+    const int32_t* slot;       /* [tokens], as in nvfp4_kv_append */
+    const void* v;             /* bf16 [tokens][kv_heads][head_dim] */
+    int64_t ldv, hv;
+    const nvfp4_kv_cache_t* cache;     /* one of the two */
+    const nvfp4_kv4_cache_t* cache4;
+} nvfp4_heads_t;
+
+/*
+ * nvfp4_qk_norm_rope -- RMSNorm of each query and key head and their rotary
+ * embedding in one pass, for a token's heads x of q or k:
+ *   y = x * (1 / sqrt(mean(x^2) + eps)) * norm           (or x without a norm)
+ *   each pair (a, b) of the rotated columns:  a' = a*c - b*s,  b' = a*s + b*c
+ * in binary32, each product, sum and difference one operation, rounded to bf16 once at the end.  c and s are
+ * those of the pair in row pos[t] of the tables; a position outside them takes
+ * the nearest row and records NVFP4_ERR_INVALID_ARG * 100 + 33.
+ * With a cache the rows of k, rounded to bf16, and those of v go where
+ * nvfp4_kv_append (or nvfp4_kv4_append) would put them, bit for bit; k_out may
+ * then be NULL.
+ */
+int nvfp4_qk_norm_rope(const nvfp4_heads_t* heads, nvfp4_stream_t stream);
+
+/* ------------------------------------------------- a KV cache in 4 bits
+ *
+ * Rows of the paged cache as NVFP4: 9/32 of the bf16 cache's bytes, which is
+ * what a decode step reads.
+ */
+
+/* Page p, kv head h, row i of K: codes (two columns to a byte, the even one in
+ * the low nibble) at k + p*page_stride + (h*page_size + i)*head_dim/2, one E4M3
+ * scale per 16 columns at k_sf + p*sf_stride + (h*page_size + i)*head_dim/16;
+ * column value = E2M1(code) * E4M3(scale) * *k_g.  V likewise. */
+struct nvfp4_kv4_cache {
+    uint8_t* k;                /* 16-byte aligned */
+    uint8_t* v;
+    uint8_t* k_sf;
+    uint8_t* v_sf;
+    const float* k_g;          /* [1], device: > 0, normal; e.g. a power of two near max |k| / 2688 */
+    const float* v_g;
+    int64_t pages, page_size, kv_heads;
+    int64_t head_dim;          /* 16 .. 128, % 16 == 0 */
+    int64_t page_stride;       /* bytes, >= kv_heads*page_size*head_dim/2, % 16 == 0 */
+    int64_t sf_stride;         /* bytes, >= kv_heads*page_size*head_dim/16, % 16 == 0 */
+};
+
+/*
+ * nvfp4_kv4_append -- nvfp4_kv_append into a 4-bit cache: each 16 columns
+ * quantized as nvfp4_quantize does with the global scale *k_g (*v_g):
+ *   s = E4M3(amax16 / (6*g)),  code = s == 0 ? +0 : E2M1(x / (E4M3(s) * g)).
+ * Infinities count as the largest bf16 number; a block with a NaN gets the
+ * scale NaN and the codes 0.  Slots as in nvfp4_kv_append.
+ */
+int nvfp4_kv4_append(const void* k, int64_t ldk, int64_t hk, const void* v, int64_t ldv, int64_t hv,
+                     const int32_t* slot, int64_t tokens, const nvfp4_kv4_cache_t* cache, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_kv4_expand -- the rows of a 4-bit cache that a step's new tokens see
+ * (request r: positions max(0, kv_len - q_len - window + 1) .. kv_len - 1; none
+ * where q_len is 0), as bf16 into the same pages and rows of `out`; its other rows stay as they are.  The
+ * value is rounded to bf16 once (exact where *k_g is a power of two).
+ *   step     after nvfp4_attn_plan on the same stream order; its window counts
+ *            if it has heads.
+ *   out      pages, page_size, kv_heads and head_dim of `cache`.
+ * Entries of the block table outside the cache are skipped.
+ */
+int nvfp4_kv4_expand(const nvfp4_kv4_cache_t* cache, const nvfp4_step_t* step, const nvfp4_kv_cache_t* out,
+                     nvfp4_stream_t stream);
+
+/* ------------------------------------------------------ pages of a cache
+ *
+ * Requests that fork, pages that come free, pages moved together.  A page is in
+ * use while a request holds it: request r holds the first
+ * ceil(ctx_len[r] / page_size) entries of its row of the block table.  Requests
+ * may share pages; one has ended when its ctx_len is 0.  No counts are kept.
+ */
+
+typedef struct {
+    int32_t* block_table;      /* [R x table_cols], row pitch table_ld */
+    int64_t requests;          /* R, 1 .. 8192 */
+    int64_t table_cols, table_ld;
+    int32_t* ctx_len;          /* [R] tokens in the cache */
+    int64_t page_size;         /* 16, 32, 64 or 128 */
+    int64_t pages;             /* of the caches, 1 .. 2^20 */
+} nvfp4_pages_t;
+
+/*
+ * nvfp4_pages_fork -- request dst[i] becomes a copy of request src[i], i < n:
+ * it gets its length and shares its full pages.  A last page that is not full,
+ * which both will write, becomes one of free_pages[*cursor ..] (pair after
+ * pair), and (its source, itself) are (copy_src[i], copy_dst[i]) for
+ * nvfp4_pages_copy, -1 where nothing is to be copied.  The rest of dst's row
+ * becomes -1.
+ *   src, dst   int32 [n], device; n <= requests.  A pair with a request that
+ *              does not exist, a dst that is some pair's src or an earlier
+ *              pair's dst, or a src whose length its row cannot hold, is
+ *              left out.
+ *   cursor     [1] entries of free_pages already taken, or NULL: 0; cursor_out
+ *              [1] or NULL: that plus the pages taken, may alias cursor.
+ *   copy_src, copy_dst   int32 [n], device, out.
+ * A pair left out, and a page that the free list did not have (the entry is
+ * -1), record NVFP4_ERR_INVALID_ARG * 100 + 34.
+ */
+int nvfp4_pages_fork(const nvfp4_pages_t* pages, const int32_t* src, const int32_t* dst, int64_t n,
+                     const int32_t* free_pages, int64_t free_count, const int32_t* cursor, int32_t* cursor_out,
+                     int32_t* copy_src, int32_t* copy_dst, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_pages_free -- the free list from what the requests hold: the pages that
+ * none of them holds, ascending, then -1, into free_pages (int32 [pages]; the
+ * next step's list, its cursor at 0), their number into *free_count.  With
+ * table_out the pages in use are moved together as well: those at or past their
+ * number take the lowest free ids, in order.  (move_src[i], move_dst[i]), int32
+ * [pages / 2] each, -1 past the last, are the moves for nvfp4_pages_copy;
+ * table_out (row pitch table_out_ld; may be the table itself) gets the rows with
+ * the new ids, -1 past what a request holds; and the free list is that after the
+ * moves.  Lengths and block_table are not changed.
+ * A held entry that is no page is left as it is and recorded
+ * (NVFP4_ERR_INVALID_ARG * 100 + 34), as is a length that its row cannot hold.
+ */
+int nvfp4_pages_free(const nvfp4_pages_t* pages, int32_t* free_pages, int32_t* free_count, int32_t* table_out,
+                     int64_t table_out_ld, int32_t* move_src, int32_t* move_dst, nvfp4_stream_t stream);
+
+/* One matrix of pages: page p is page_bytes bytes at base + p*page_stride
+ * (16-byte aligned, both % 16 == 0): K or V of a cache, codes or scales. */
+typedef struct {
+    void* base;
+    int64_t page_bytes, page_stride;
+} nvfp4_plane_t;
+
+/*
+ * nvfp4_pages_copy -- page src[i] to page dst[i], i < n, in every plane (the
+ * caches of all layers in one call).  A pair of -1 is skipped; any other id
+ * outside [0, pages) skips its pair and records NVFP4_ERR_INVALID_ARG * 100 + 34.
+ * No page is the destination of two pairs, or source and destination
+ * of different ones.
+ *   planes   HOST array; up to 64 to a launch.
+ *   src, dst int32 [n], device.
+ */
+int nvfp4_pages_copy(const nvfp4_plane_t* planes, int64_t n_planes, int64_t pages, const int32_t* src,
+                     const int32_t* dst, int64_t n, nvfp4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -65,6 +65,36 @@ class _AttnIOC(ctypes.Structure):
                 ("head_dim", ctypes.c_int64), ("scale", ctypes.c_float), ("zero_padding", ctypes.c_int32)]
 
 
+class _Cache4C(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_sf", ctypes.c_void_p), ("v_sf", ctypes.c_void_p),
+                ("k_g", ctypes.c_void_p), ("v_g", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("sf_stride", ctypes.c_int64)]
+
+
+class _HeadsC(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("heads", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("hq", ctypes.c_int64),
+                ("q_out", ctypes.c_void_p), ("ldqo", ctypes.c_int64), ("hqo", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("ldk", ctypes.c_int64), ("hk", ctypes.c_int64), ("k_out", ctypes.c_void_p), ("ldko", ctypes.c_int64),
+                ("hko", ctypes.c_int64), ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("pos", ctypes.c_void_p), ("cos_t", ctypes.c_void_p),
+                ("sin_t", ctypes.c_void_p), ("table_ld", ctypes.c_int64), ("positions", ctypes.c_int64),
+                ("rope_dim", ctypes.c_int64), ("halves", ctypes.c_int32), ("slot", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("ldv", ctypes.c_int64), ("hv", ctypes.c_int64),
+                ("cache", ctypes.POINTER(_CacheC)), ("cache4", ctypes.POINTER(_Cache4C))]
+
+
+class _PagesC(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("requests", ctypes.c_int64), ("table_cols", ctypes.c_int64),
+                ("table_ld", ctypes.c_int64), ("ctx_len", ctypes.c_void_p), ("page_size", ctypes.c_int64),
+                ("pages", ctypes.c_int64)]
+
+
+class _PlaneC(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("page_stride", ctypes.c_int64)]
+
+
 _SIGS = {
     "nvfp4_codes_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
     "nvfp4_sf_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
@@ -122,6 +152,19 @@ _SIGS = {
                                          ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "nvfp4_attn_paged": (ctypes.c_int, [ctypes.POINTER(_StepC), ctypes.POINTER(_AttnIOC), ctypes.POINTER(_CacheC),
                                         ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "nvfp4_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(_HeadsC), ctypes.c_void_p]),
+    "nvfp4_kv4_append": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                        ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                        ctypes.POINTER(_Cache4C), ctypes.c_void_p]),
+    "nvfp4_kv4_expand": (ctypes.c_int, [ctypes.POINTER(_Cache4C), ctypes.POINTER(_StepC), ctypes.POINTER(_CacheC),
+                                        ctypes.c_void_p]),
+    "nvfp4_pages_fork": (ctypes.c_int, [ctypes.POINTER(_PagesC), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "nvfp4_pages_free": (ctypes.c_int, [ctypes.POINTER(_PagesC), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "nvfp4_pages_copy": (ctypes.c_int, [ctypes.POINTER(_PlaneC), ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
 }
 
 EXPORTED_FUNCTIONS = tuple(_SIGS)
@@ -526,3 +569,218 @@ def nvfp4_attn_paged(q: torch.Tensor, cache: KVCache, plan: AttnPlan, out: torch
     io = _attn_io(plan, q, out, scale, lse, zero_padding)
     _check((_lib or lib()).nvfp4_attn_paged(ctypes.byref(plan._c), ctypes.byref(io), ctypes.byref(cache._c), ws.data_ptr(),
                                   ws.numel() * ws.element_size(), _stream(stream)), "nvfp4_attn_paged")
+
+
+# ------------------------------- heads, the 4-bit cache, pages of a cache
+# (These calls refuse tensors that are not on the current device, whose stream
+# and library state they would use.)
+def _on_device(name: str, *tensors):
+    here = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != here):
+            raise ValueError(f"{name}: every tensor must be on the current CUDA device, not {t.device}")
+
+
+class KVCache4:
+    """A paged KV cache in 4 bits (nvfp4_kv4_cache_t): ``k`` and ``v`` uint8
+    [pages, kv_heads, page_size, head_dim // 2] (two E2M1 codes to a byte),
+    ``k_sf`` and ``v_sf`` uint8 [pages, kv_heads, page_size, head_dim // 16]
+    (E4M3), ``k_g`` and ``v_g`` float32 [1], the scales of all keys and of all
+    values.  Pages may be apart (stride(0)); within a page they are contiguous."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_sf: torch.Tensor, v_sf: torch.Tensor, k_g: torch.Tensor,
+                 v_g: torch.Tensor):
+        for name, t in (("k", k), ("v", v), ("k_sf", k_sf), ("v_sf", v_sf)):
+            if t.dtype != torch.uint8 or t.dim() != 4 or not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA uint8 [pages, kv_heads, page_size, bytes of a row] tensor")
+            if t.stride()[1:] != (t.shape[2] * t.shape[3], t.shape[3], 1):
+                raise ValueError(f"{name}'s pages must be contiguous")
+        for a, b in ((k, v), (k_sf, v_sf)):
+            if a.shape != b.shape or (a.stride(0) != b.stride(0) and a.shape[0] > 1):
+                raise ValueError("k and v must have one shape and one page stride")
+        if k_sf.shape[:3] != k.shape[:3] or k_sf.shape[3] * 8 != k.shape[3]:
+            raise ValueError("a scale for each 16 columns (8 bytes of codes)")
+        for name, g in (("k_g", k_g), ("v_g", v_g)):
+            if g.dtype != torch.float32 or g.numel() != 1 or not g.is_cuda:
+                raise ValueError(f"{name} must be a CUDA float32 tensor of one element")
+        self.k, self.v, self.k_sf, self.v_sf, self.k_g, self.v_g = k, v, k_sf, v_sf, k_g, v_g
+        self.pages, self.kv_heads, self.page_size = k.shape[:3]
+        self.head_dim = 2 * k.shape[3]
+        stride = lambda t: t.stride(0) if self.pages > 1 else t.shape[1] * t.shape[2] * t.shape[3]
+        self._c = _Cache4C(k.data_ptr(), v.data_ptr(), k_sf.data_ptr(), v_sf.data_ptr(), k_g.data_ptr(),
+                           v_g.data_ptr(), self.pages, self.page_size, self.kv_heads, self.head_dim, stride(k),
+                           stride(k_sf))
+
+    @staticmethod
+    def empty(pages: int, kv_heads: int, page_size: int, head_dim: int, k_g=2.0 ** -6, v_g=2.0 ** -6,
+              device=None) -> "KVCache4":
+        """k_g, v_g: the scales (a power of two near the largest magnitude / 2688
+        loses nothing by them); 2^-6 reaches to 42, with full precision down to
+        blocks whose largest magnitude is 0.0015."""
+        make = lambda n: torch.empty((pages, kv_heads, page_size, n), dtype=torch.uint8, device=device or "cuda")
+        scale = lambda g: torch.full((1,), g, dtype=torch.float32, device=device or "cuda")
+        return KVCache4(make(head_dim // 2), make(head_dim // 2), make(head_dim // 16), make(head_dim // 16), scale(k_g),
+                        scale(v_g))
+
+
+def _cache_fits(plan: AttnPlan, cache, name="cache"):
+    if plan.slot is None:
+        raise ValueError("the plan has no paged cache (page_size 0)")
+    if plan.page_size != cache.page_size:        # (a slot is page * page_size + row)
+        raise ValueError(f"the plan's pages of {plan.page_size} tokens are not the {name}'s of {cache.page_size}")
+
+
+def nvfp4_qk_norm_rope(q, k, q_norm=None, k_norm=None, pos=None, cos_t=None, sin_t=None, q_out=None, k_out=None,
+                       halves=False, eps=1e-6, rope_dim=None, v=None, plan=None, cache=None, stream=None):
+    """RMSNorm of each head of q [tokens, heads, head_dim] and k [tokens,
+    kv_heads, head_dim] (bf16, any row and head pitch; either may be None) and
+    their rotation, in one pass.  q_norm, k_norm: bf16 [head_dim], None for no
+    norm.  pos int32 [tokens], cos_t and sin_t float32 [positions, >= rope_dim /
+    2]; None for no rotation.  rope_dim: the last columns of a head that are
+    rotated (None: twice the tables' width); halves: pairs (i, i + rope_dim / 2)
+    instead of (2i, 2i + 1).  q_out, k_out: where the rows go (None: in place).
+
+    With v, plan and cache (KVCache or KVCache4) the rows of k, and those of v,
+    go into the cache's slots plan.slot instead (and to k_out where it is given)."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k")
+    tokens, D = ref.shape[0], ref.shape[2]
+    if (cache is None) != (v is None) or (cache is None) != (plan is None):
+        raise ValueError("v, plan and cache go together")
+    h = _HeadsC(tokens=tokens, head_dim=D, eps=eps)
+    if q is not None:
+        h.heads = q.shape[1]
+        h.q, h.ldq, h.hq = _heads_3d(q, "q", tokens, h.heads, D)
+        h.q_out, h.ldqo, h.hqo = (h.q, h.ldq, h.hq) if q_out is None else _heads_3d(q_out, "q_out", tokens, h.heads, D)
+    if k is not None:
+        h.kv_heads = k.shape[1]
+        h.k, h.ldk, h.hk = _heads_3d(k, "k", tokens, h.kv_heads, D)
+        if k_out is not None:
+            h.k_out, h.ldko, h.hko = _heads_3d(k_out, "k_out", tokens, h.kv_heads, D)
+        elif cache is None:
+            h.k_out, h.ldko, h.hko = h.k, h.ldk, h.hk
+    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if w is not None:
+            if w.dtype is not _BF16 or w.numel() != D or not w.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous bf16 [{D}] tensor")
+            setattr(h, name, w.data_ptr())
+    if pos is not None:
+        if cos_t is None or sin_t is None or cos_t.dtype is not torch.float32 or sin_t.dtype is not torch.float32 or \
+                cos_t.dim() != 2 or cos_t.shape != sin_t.shape or cos_t.stride(1) != 1 or sin_t.stride() != cos_t.stride():
+            raise ValueError("cos_t and sin_t must be row-major float32 2-D tensors of one shape")
+        h.pos, h.cos_t, h.sin_t = _i32(pos, tokens, "pos"), cos_t.data_ptr(), sin_t.data_ptr()
+        h.positions, h.table_ld = cos_t.shape[0], max(cos_t.stride(0), cos_t.shape[1])
+        h.rope_dim, h.halves = 2 * cos_t.shape[1] if rope_dim is None else rope_dim, 1 if halves else 0
+        if h.rope_dim > 2 * cos_t.shape[1]:
+            raise ValueError("the tables are narrower than half of rope_dim")
+    if cache is not None:
+        _cache_fits(plan, cache)
+        if k is None or plan.tokens != tokens:
+            raise ValueError("a cache takes the rows of k and v of all of the plan's tokens")
+        h.slot = plan.slot.data_ptr()
+        h.v, h.ldv, h.hv = _heads_3d(v, "v", tokens, h.kv_heads, D)
+        if isinstance(cache, KVCache4):
+            h.cache4 = ctypes.pointer(cache._c)
+        else:
+            h.cache = ctypes.pointer(cache._c)
+        _on_device("nvfp4_qk_norm_rope", cache.k, plan.slot)
+    _on_device("nvfp4_qk_norm_rope", q, k, v, q_out, k_out, q_norm, k_norm, pos, cos_t, sin_t)
+    _check((_lib or lib()).nvfp4_qk_norm_rope(ctypes.byref(h), _stream(stream)), "nvfp4_qk_norm_rope")
+
+
+def nvfp4_kv4_append(k: torch.Tensor, v: torch.Tensor, plan: AttnPlan, cache: KVCache4, stream=None):
+    """k, v: bf16 [tokens, kv_heads, head_dim] (any row and head pitch) into the
+    4-bit cache's slots plan.slot."""
+    _cache_fits(plan, cache)
+    kp = _heads_3d(k, "k", plan.tokens, cache.kv_heads, cache.head_dim)
+    vp = _heads_3d(v, "v", plan.tokens, cache.kv_heads, cache.head_dim)
+    _on_device("nvfp4_kv4_append", k, v, plan.slot, cache.k)
+    _check((_lib or lib()).nvfp4_kv4_append(*kp, *vp, plan.slot.data_ptr(), plan.tokens, ctypes.byref(cache._c),
+                                            _stream(stream)), "nvfp4_kv4_append")
+
+
+def nvfp4_kv4_expand(cache: KVCache4, plan: AttnPlan, out: KVCache, stream=None):
+    """The rows of the cache that the step's new tokens see, as bf16 in the same
+    pages of out (a KVCache of the same sizes)."""
+    _cache_fits(plan, cache)
+    _on_device("nvfp4_kv4_expand", cache.k, plan.kv_len, out.k)
+    _check((_lib or lib()).nvfp4_kv4_expand(ctypes.byref(cache._c), ctypes.byref(plan._c), ctypes.byref(out._c),
+                                            _stream(stream)), "nvfp4_kv4_expand")
+
+
+class PageTable:
+    """What the requests of a server hold (nvfp4_pages_t): block_table int32
+    [requests, pages per request], ctx_len int32 [requests], in pages of
+    page_size rows of caches of so many pages.  ctx_len 0: the request has ended."""
+
+    def __init__(self, block_table: torch.Tensor, ctx_len: torch.Tensor, page_size: int, pages: int):
+        _table(block_table, "block_table", block_table.shape)
+        self.block_table, self.ctx_len, self.page_size, self.pages = block_table, ctx_len, page_size, pages
+        self.requests, self.cols = block_table.shape
+        self._c = _PagesC(block_table.data_ptr(), self.requests, self.cols, max(block_table.stride(0), self.cols),
+                          _i32(ctx_len, self.requests, "ctx_len"), page_size, pages)
+
+
+def _table(t: torch.Tensor, name: str, shape):
+    if t.dtype is not _I32 or not t.is_cuda or t.dim() != 2 or t.stride(1) != 1 or t.shape != shape:
+        raise ValueError(f"{name} must be a CUDA int32 [requests, pages] tensor with unit column stride")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}'s rows overlap (an expanded tensor has to be made contiguous)")
+
+
+def nvfp4_pages_fork(table: PageTable, src: torch.Tensor, dst: torch.Tensor, free_pages: torch.Tensor, cursor, cursor_out,
+                     copy_src: torch.Tensor, copy_dst: torch.Tensor, stream=None):
+    """Requests dst become copies of requests src (int32 [n]), sharing their full
+    pages; last pages that are not full become pages of free_pages (int32) from
+    cursor (int32 [1] or None: 0) on.  (copy_src, copy_dst), int32 [n]: the pages
+    for :func:`nvfp4_pages_copy`.  cursor_out: int32 [1] or None, may be cursor."""
+    n = src.numel()
+    args = [_i32(src, n, "src"), _i32(dst, n, "dst"), n, _i32(free_pages, 0, "free_pages"), free_pages.numel(),
+            None if cursor is None else _i32(cursor, 1, "cursor"),
+            None if cursor_out is None else _i32(cursor_out, 1, "cursor_out"), _i32(copy_src, n, "copy_src"),
+            _i32(copy_dst, n, "copy_dst")]
+    if dst.numel() != n:
+        raise ValueError("as many dst as src")
+    _on_device("nvfp4_pages_fork", table.block_table, table.ctx_len, src, dst, free_pages, cursor, cursor_out, copy_src,
+               copy_dst)
+    _check((_lib or lib()).nvfp4_pages_fork(ctypes.byref(table._c), *args, _stream(stream)), "nvfp4_pages_fork")
+
+
+def nvfp4_pages_free(table: PageTable, free_pages: torch.Tensor, free_count: torch.Tensor, table_out=None, move_src=None,
+                     move_dst=None, stream=None):
+    """The pages that no request holds, ascending, then -1, into free_pages (int32
+    [pages]), their number into free_count (int32 [1]).  With table_out (int32,
+    block_table's shape; may be block_table) the pages in use are moved to the
+    lowest ids: move_src and move_dst (int32 [pages // 2], -1 past the last) are
+    the moves for :func:`nvfp4_pages_copy`."""
+    if (table_out is None) != (move_src is None) or (table_out is None) != (move_dst is None):
+        raise ValueError("table_out, move_src and move_dst go together")
+    args = [_i32(free_pages, table.pages, "free_pages"), _i32(free_count, 1, "free_count"), None, 0, None, None]
+    if table_out is not None:
+        _table(table_out, "table_out", table.block_table.shape)
+        args[2:] = [table_out.data_ptr(), max(table_out.stride(0), table.cols),
+                    _i32(move_src, table.pages // 2, "move_src"), _i32(move_dst, table.pages // 2, "move_dst")]
+    _on_device("nvfp4_pages_free", table.block_table, table.ctx_len, free_pages, free_count, table_out, move_src, move_dst)
+    _check((_lib or lib()).nvfp4_pages_free(ctypes.byref(table._c), *args, _stream(stream)), "nvfp4_pages_free")
+
+
+def nvfp4_pages_copy(caches, src: torch.Tensor, dst: torch.Tensor, stream=None):
+    """Page src[i] to page dst[i] (int32 [n]; pairs of -1 are skipped) in every
+    one of caches (KVCache, KVCache4; one or a list, all of as many pages)."""
+    caches = list(caches) if isinstance(caches, (list, tuple)) else [caches]
+    n = src.numel()
+    if not caches or any(c.pages != caches[0].pages for c in caches):
+        raise ValueError("caches of one number of pages")
+    if dst.numel() != n:
+        raise ValueError("as many dst as src")
+    planes = []
+    for c in caches:
+        _on_device("nvfp4_pages_copy", c.k, src, dst)
+        for t in ((c.k, c.v, c.k_sf, c.v_sf) if isinstance(c, KVCache4) else (c.k, c.v)):
+            size = t.element_size()
+            page = t.shape[1] * t.shape[2] * t.shape[3] * size
+            planes.append(_PlaneC(t.data_ptr(), page, t.stride(0) * size if c.pages > 1 else page))
+    _check((_lib or lib()).nvfp4_pages_copy((_PlaneC * len(planes))(*planes), len(planes), caches[0].pages,
+                                            _i32(src, n, "src"), _i32(dst, n, "dst"), n, _stream(stream)),
+           "nvfp4_pages_copy")

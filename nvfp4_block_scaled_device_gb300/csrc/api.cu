@@ -11,6 +11,7 @@
 #include "attn.h"
 #include "gemv.h"
 #include "internal.h"
+#include "kv4.h"
 #include "nvfp4.h"
 
 using namespace nvfp4;
@@ -918,6 +919,226 @@ int nvfp4_attn_paged(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const 
     kv.v = static_cast<const __nv_bfloat16*>(cache->v);
     kv.cache = cache;
     return run_attn(step, io, kv, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------- heads, the 4-bit cache, pages of a cache
+namespace {
+
+bool page_size_ok(int64_t P) { return P == 16 || P == 32 || P == 64 || P == 128; }
+
+int check_cache4(const nvfp4_kv4_cache_t* c)
+{
+    if (!c || !c->k || !c->v || !c->k_sf || !c->v_sf || !c->k_g || !c->v_g || c->pages < 1 || c->kv_heads < 1)
+        return NVFP4_ERR_INVALID_ARG;
+    const int64_t P = c->page_size, D = c->head_dim;
+    if (!page_size_ok(P)) return NVFP4_ERR_INVALID_ARG;
+    NVFP4_TRY(check_head_dim(D));
+    if (D % 16 != 0 || c->pages > INT32_MAX / P || c->kv_heads > 65535 || c->page_stride < c->kv_heads * P * D / 2 ||
+        c->sf_stride < c->kv_heads * P * D / 16)
+        return NVFP4_ERR_INVALID_ARG;
+    for (const void* x : {(const void*)c->k, (const void*)c->v, (const void*)c->k_sf, (const void*)c->v_sf})
+        if (!aligned(x, 16)) return NVFP4_ERR_MISALIGNED;
+    if (!aligned(c->k_g, 4) || !aligned(c->v_g, 4) || c->page_stride % 16 != 0 || c->sf_stride % 16 != 0)
+        return NVFP4_ERR_MISALIGNED;
+    return NVFP4_OK;
+}
+
+// A bf16 cache of the same pages as a 4-bit one.
+int check_same_pages(const nvfp4_kv4_cache_t* c, const nvfp4_kv_cache_t* x)
+{
+    NVFP4_TRY(check_cache(x));
+    return x->pages == c->pages && x->page_size == c->page_size && x->kv_heads == c->kv_heads &&
+                   x->head_dim == c->head_dim
+               ? NVFP4_OK
+               : NVFP4_ERR_INVALID_ARG;
+}
+
+int check_pages(const nvfp4_pages_t* t)
+{
+    if (!t || !t->block_table || !t->ctx_len || t->requests < 1 || t->requests > kStepMaxRequests || t->table_cols < 1 ||
+        t->table_ld < t->table_cols || t->pages < 1 || t->pages > kMaxPages || !page_size_ok(t->page_size) ||
+        t->table_cols * t->page_size > INT32_MAX)
+        return NVFP4_ERR_INVALID_ARG;
+    if (!aligned(t->block_table, 4) || !aligned(t->ctx_len, 4)) return NVFP4_ERR_MISALIGNED;
+    return NVFP4_OK;
+}
+
+// int32 words from a table's first entry to its last.
+int64_t table_words(const nvfp4_pages_t* t, int64_t ld) { return (t->requests - 1) * ld + t->table_cols; }
+
+}  // namespace
+
+extern "C" {
+
+int nvfp4_qk_norm_rope(const nvfp4_heads_t* h, nvfp4_stream_t stream)
+{
+    if (!h || h->tokens < 1 || h->tokens > INT32_MAX || h->heads < 0 || h->kv_heads < 0 || h->heads > 65535 ||
+        h->kv_heads > 65535 || h->heads + h->kv_heads < 1 || !(h->eps >= 0.0f) || h->eps > FLT_MAX)
+        return NVFP4_ERR_INVALID_ARG;
+    const int64_t T = h->tokens, D = h->head_dim;
+    NVFP4_TRY(check_head_dim(D));
+    if (h->heads) {
+        NVFP4_TRY(check_rows(h->q, T, h->heads, D, h->ldq, h->hq));
+        NVFP4_TRY(check_rows(h->q_out, T, h->heads, D, h->ldqo, h->hqo));
+        if (h->q_out == h->q && (h->ldqo != h->ldq || h->hqo != h->hq)) return NVFP4_ERR_INVALID_ARG;
+    }
+    if (h->kv_heads) {
+        NVFP4_TRY(check_rows(h->k, T, h->kv_heads, D, h->ldk, h->hk));
+        if (h->k_out || !h->slot) NVFP4_TRY(check_rows(h->k_out, T, h->kv_heads, D, h->ldko, h->hko));
+        if (h->k_out == h->k && (h->ldko != h->ldk || h->hko != h->hk)) return NVFP4_ERR_INVALID_ARG;
+    }
+    if (!aligned(h->q_norm, 16) || !aligned(h->k_norm, 16)) return NVFP4_ERR_MISALIGNED;
+    if (h->pos) {
+        const int64_t rd = h->rope_dim;
+        if (!h->cos_t || !h->sin_t || rd < 2 || rd > D || rd % (h->halves ? 16 : 2) != 0 || h->table_ld < rd / 2 ||
+            h->positions < 1 || h->positions > INT32_MAX)
+            return NVFP4_ERR_INVALID_ARG;
+        if (!aligned(h->pos, 4) || !aligned(h->cos_t, 4) || !aligned(h->sin_t, 4)) return NVFP4_ERR_MISALIGNED;
+    }
+    if (h->slot) {
+        if (!h->kv_heads || (h->cache != nullptr) == (h->cache4 != nullptr)) return NVFP4_ERR_INVALID_ARG;
+        NVFP4_TRY(check_rows(h->v, T, h->kv_heads, D, h->ldv, h->hv));
+        int64_t heads, dim;
+        if (h->cache) {
+            NVFP4_TRY(check_cache(h->cache));
+            heads = h->cache->kv_heads, dim = h->cache->head_dim;
+        } else {
+            NVFP4_TRY(check_cache4(h->cache4));
+            heads = h->cache4->kv_heads, dim = h->cache4->head_dim;
+        }
+        if (heads != h->kv_heads || dim != D) return NVFP4_ERR_INVALID_ARG;
+        if (!aligned(h->slot, 4)) return NVFP4_ERR_MISALIGNED;
+    }
+    DeviceInfo* d = nullptr;
+    NVFP4_TRY(device_info(&d));
+    NVFP4_CUDA(launch_heads(*h, d->status, d->num_sms, (cudaStream_t)stream));
+    return NVFP4_OK;
+}
+
+int nvfp4_kv4_append(const void* k, int64_t ldk, int64_t hk, const void* v, int64_t ldv, int64_t hv,
+                     const int32_t* slot, int64_t tokens, const nvfp4_kv4_cache_t* cache, nvfp4_stream_t stream)
+{
+    NVFP4_TRY(check_cache4(cache));
+    if (tokens < 1 || tokens > INT32_MAX || !slot) return NVFP4_ERR_INVALID_ARG;
+    NVFP4_TRY(check_rows(k, tokens, cache->kv_heads, cache->head_dim, ldk, hk));
+    NVFP4_TRY(check_rows(v, tokens, cache->kv_heads, cache->head_dim, ldv, hv));
+    if (!aligned(slot, 4)) return NVFP4_ERR_MISALIGNED;
+    DeviceInfo* d = nullptr;
+    NVFP4_TRY(device_info(&d));
+    nvfp4_heads_t h = {};
+    h.tokens = tokens;
+    h.kv_heads = cache->kv_heads;
+    h.head_dim = cache->head_dim;
+    h.k = k;
+    h.ldk = ldk;
+    h.hk = hk;
+    h.v = v;
+    h.ldv = ldv;
+    h.hv = hv;
+    h.slot = slot;
+    h.cache4 = cache;
+    NVFP4_CUDA(launch_heads(h, d->status, d->num_sms, (cudaStream_t)stream));
+    return NVFP4_OK;
+}
+
+int nvfp4_kv4_expand(const nvfp4_kv4_cache_t* cache, const nvfp4_step_t* step, const nvfp4_kv_cache_t* out,
+                     nvfp4_stream_t stream)
+{
+    NVFP4_TRY(check_cache4(cache));
+    NVFP4_TRY(check_same_pages(cache, out));
+    NVFP4_TRY(check_step(step, 1));
+    if (step->page_size != cache->page_size) return NVFP4_ERR_INVALID_ARG;
+    if (step->heads && (step->window < 0 || step->window > INT32_MAX)) return NVFP4_ERR_INVALID_ARG;
+    DeviceInfo* d = nullptr;
+    NVFP4_TRY(device_info(&d));
+    NVFP4_CUDA(launch_kv4_expand(*cache, *step, *out, true, d->num_sms, (cudaStream_t)stream));
+    return NVFP4_OK;
+}
+
+int nvfp4_pages_fork(const nvfp4_pages_t* pages, const int32_t* src, const int32_t* dst, int64_t n,
+                     const int32_t* free_pages, int64_t free_count, const int32_t* cursor, int32_t* cursor_out,
+                     int32_t* copy_src, int32_t* copy_dst, nvfp4_stream_t stream)
+{
+    NVFP4_TRY(check_pages(pages));
+    if (n < 0 || n > pages->requests || free_count < 0 || (n && (!src || !dst || !copy_src || !copy_dst)))
+        return NVFP4_ERR_INVALID_ARG;
+    for (const int32_t* x : {src, dst, free_pages, cursor, (const int32_t*)cursor_out, (const int32_t*)copy_src,
+                             (const int32_t*)copy_dst})
+        if (!aligned(x, 4)) return NVFP4_ERR_MISALIGNED;
+    // what some blocks write while others read
+    const int64_t words = table_words(pages, pages->table_ld), R = pages->requests;
+    for (const int32_t* in : {src, dst})
+        if (overlap(in, n, copy_src, n) || overlap(in, n, copy_dst, n) || overlap(in, n, cursor_out, 1) ||
+            overlap(in, n, pages->ctx_len, R) || overlap(in, n, pages->block_table, words))
+            return NVFP4_ERR_INVALID_ARG;
+    if (overlap(pages->ctx_len, R, copy_src, n) || overlap(pages->ctx_len, R, copy_dst, n) ||
+        overlap(pages->ctx_len, R, cursor_out, 1) || overlap(free_pages, free_count, pages->block_table, words) ||
+        overlap(pages->ctx_len, R, pages->block_table, words))
+        return NVFP4_ERR_INVALID_ARG;
+    DeviceInfo* d = nullptr;
+    NVFP4_TRY(device_info(&d));
+    NVFP4_CUDA(launch_pages_fork(*pages, src, dst, n, free_pages, free_count, cursor, cursor_out, copy_src, copy_dst,
+                                 d->status, (cudaStream_t)stream));
+    return NVFP4_OK;
+}
+
+int nvfp4_pages_free(const nvfp4_pages_t* pages, int32_t* free_pages, int32_t* free_count, int32_t* table_out,
+                     int64_t table_out_ld, int32_t* move_src, int32_t* move_dst, nvfp4_stream_t stream)
+{
+    NVFP4_TRY(check_pages(pages));
+    if (!free_pages || !free_count) return NVFP4_ERR_INVALID_ARG;
+    if (table_out && (table_out_ld < pages->table_cols || (pages->pages > 1 && (!move_src || !move_dst))))
+        return NVFP4_ERR_INVALID_ARG;
+    for (const int32_t* x : {free_pages, free_count, table_out, move_src, move_dst})
+        if (!aligned(x, 4)) return NVFP4_ERR_MISALIGNED;
+    const int64_t words = table_words(pages, pages->table_ld), R = pages->requests, N = pages->pages;
+    struct { const int32_t* at; int64_t n; } out[5] = {{free_pages, N}, {free_count, 1},
+                                                       {table_out, table_words(pages, table_out_ld)},
+                                                       {table_out ? move_src : nullptr, N / 2},
+                                                       {table_out ? move_dst : nullptr, N / 2}};
+    const bool in_place = table_out == pages->block_table && table_out_ld == pages->table_ld;
+    for (int i = 0; i < 5; i++) {
+        if (overlap(out[i].at, out[i].n, pages->ctx_len, R) ||
+            (overlap(out[i].at, out[i].n, pages->block_table, words) && !(i == 2 && in_place)))
+            return NVFP4_ERR_INVALID_ARG;
+        for (int j = 0; j < i; j++)
+            if (overlap(out[i].at, out[i].n, out[j].at, out[j].n)) return NVFP4_ERR_INVALID_ARG;
+    }
+    DeviceInfo* d = nullptr;
+    NVFP4_TRY(device_info(&d));
+    NVFP4_CUDA(launch_pages_free(*pages, free_pages, free_count, table_out, table_out_ld, move_src, move_dst, d->status,
+                                 (cudaStream_t)stream));
+    return NVFP4_OK;
+}
+
+int nvfp4_pages_copy(const nvfp4_plane_t* planes, int64_t n_planes, int64_t pages, const int32_t* src,
+                     const int32_t* dst, int64_t n, nvfp4_stream_t stream)
+{
+    if (!planes || n_planes < 1 || pages < 1 || pages > INT32_MAX || n < 0 || n > INT32_MAX || (n && (!src || !dst)))
+        return NVFP4_ERR_INVALID_ARG;
+    int64_t most = 16;
+    for (int64_t i = 0; i < n_planes; i++) {
+        const nvfp4_plane_t& x = planes[i];
+        if (!x.base || x.page_bytes < 16 || x.page_bytes > 65535 * kPageCopyChunk || x.page_stride < x.page_bytes)
+            return NVFP4_ERR_INVALID_ARG;
+        if (!aligned(x.base, 16) || x.page_bytes % 16 != 0 || x.page_stride % 16 != 0) return NVFP4_ERR_MISALIGNED;
+        most = x.page_bytes > most ? x.page_bytes : most;
+    }
+    if (!aligned(src, 4) || !aligned(dst, 4)) return NVFP4_ERR_MISALIGNED;
+    DeviceInfo* d = nullptr;
+    NVFP4_TRY(device_info(&d));
+    if (n == 0) return NVFP4_OK;
+    const int64_t chunks = (most + kPageCopyChunk - 1) / kPageCopyChunk;
+    const int64_t fit = 65535 / chunks, at_once = fit < kMaxPlanes ? fit : kMaxPlanes;       // (the grid's second axis)
+    for (int64_t i = 0; i < n_planes; i += at_once) {
+        PageCopyPlanes p = {};
+        const int k = (int)(n_planes - i < at_once ? n_planes - i : at_once);
+        for (int j = 0; j < k; j++) p.p[j] = planes[i + j];
+        NVFP4_CUDA(launch_pages_copy(p, k, most, pages, src, dst, n, d->status, d->num_sms, (cudaStream_t)stream));
+    }
+    return NVFP4_OK;
 }
 
 }  // extern "C"
