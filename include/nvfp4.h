@@ -635,6 +635,27 @@ int nvfp4_kv4_append(const void* k, int64_t ldk, int64_t hk, const void* v, int6
 int nvfp4_kv4_expand(const nvfp4_kv4_cache_t* cache, const nvfp4_step_t* step, const nvfp4_kv_cache_t* out,
                      nvfp4_stream_t stream);
 
+/*
+ * nvfp4_attn_paged4 -- nvfp4_attn_paged over a 4-bit cache, whose values it
+ * takes as they are stored (in half precision, which holds code times scale
+ * exactly; *k_g and *v_g multiply the scores and the outputs).  q counts with
+ * at least 11 bits beside the largest of its row, the probabilities are rounded
+ * to half precision (2^-11).
+ *   expanded  NULL, or a bf16 cache of the same pages, page_size, kv_heads and
+ *            head_dim as scratch: a step with many rows per request then takes
+ *            its keys' rows out of the 4 bits once (into their pages there, bf16
+ *            that holds code times scale exactly) and runs nvfp4_attn_paged's
+ *            kernel on them, with probabilities rounded to bf16 as there.  One
+ *            serves all layers that run one after the other.
+ *   workspace as nvfp4_attn_paged.
+ * head_dim % 16 == 0.  The rest as nvfp4_attn_paged: cache rows that no row of
+ * a request sees may hold anything, a page id outside the cache counts as a
+ * page of zeros.
+ */
+int nvfp4_attn_paged4(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const nvfp4_kv4_cache_t* cache,
+                      const nvfp4_kv_cache_t* expanded, void* workspace, size_t workspace_bytes,
+                      nvfp4_stream_t stream);
+
 /* ------------------------------------------------------ pages of a cache
  *
  * Requests that fork, pages that come free, pages moved together.  A page is in

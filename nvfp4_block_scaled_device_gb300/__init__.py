@@ -158,6 +158,8 @@ _SIGS = {
                                         ctypes.POINTER(_Cache4C), ctypes.c_void_p]),
     "nvfp4_kv4_expand": (ctypes.c_int, [ctypes.POINTER(_Cache4C), ctypes.POINTER(_StepC), ctypes.POINTER(_CacheC),
                                         ctypes.c_void_p]),
+    "nvfp4_attn_paged4": (ctypes.c_int, [ctypes.POINTER(_StepC), ctypes.POINTER(_AttnIOC), ctypes.POINTER(_Cache4C),
+                                         ctypes.POINTER(_CacheC), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "nvfp4_pages_fork": (ctypes.c_int, [ctypes.POINTER(_PagesC), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
                                         ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
@@ -707,6 +709,18 @@ def nvfp4_kv4_expand(cache: KVCache4, plan: AttnPlan, out: KVCache, stream=None)
     _on_device("nvfp4_kv4_expand", cache.k, plan.kv_len, out.k)
     _check((_lib or lib()).nvfp4_kv4_expand(ctypes.byref(cache._c), ctypes.byref(plan._c), ctypes.byref(out._c),
                                             _stream(stream)), "nvfp4_kv4_expand")
+
+
+def nvfp4_attn_paged4(q: torch.Tensor, cache: KVCache4, plan: AttnPlan, out: torch.Tensor, ws: torch.Tensor, scale=None,
+                      lse=None, stream=None, zero_padding=False, expanded: KVCache | None = None):
+    """:func:`nvfp4_attn_paged` over a 4-bit cache.  expanded: a KVCache of the
+    same sizes as scratch, which steps with many rows per request (prompts) are
+    faster with; one serves all layers that run one after the other."""
+    io = _attn_io(plan, q, out, scale, lse, zero_padding)
+    _on_device("nvfp4_attn_paged4", q, out, lse, ws, cache.k, plan.kv_len, None if expanded is None else expanded.k)
+    _check((_lib or lib()).nvfp4_attn_paged4(ctypes.byref(plan._c), ctypes.byref(io), ctypes.byref(cache._c),
+                                             None if expanded is None else ctypes.byref(expanded._c), ws.data_ptr(),
+                                             ws.numel() * ws.element_size(), _stream(stream)), "nvfp4_attn_paged4")
 
 
 class PageTable:

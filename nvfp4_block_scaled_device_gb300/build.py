@@ -20,8 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnvfp4.so")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "gemm2.cu", "gemv.cu", "gemm_decode.cu", "noalloc.cu", "probe.cu", "experts.cu",
-           "step.cu", "attn.cu", "kv4.cu", "pages.cu"]
-HEADERS = ["common.cuh", "internal.h", "gemm_epilogue.cuh", "decode_epilogue.cuh", "gemv.h", "attn.h", "kv4.h"]
+           "step.cu", "attn.cu", "kv4.cu", "attn4.cu", "pages.cu"]
+HEADERS = ["common.cuh", "internal.h", "gemm_epilogue.cuh", "decode_epilogue.cuh", "gemv.h", "attn.h", "attn_walk.cuh", "kv4.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -738,6 +738,8 @@ struct AttnKV {
     const void* v;
     int64_t ldk, hk, ldv, hv;
     const nvfp4_kv_cache_t* cache;
+    const float* k_g;              // as AttnArgs'
+    const float* v_g;
 };
 
 // bf16 tensor map of `rank` dimensions (innermost first, strides in elements
@@ -757,6 +759,30 @@ int make_rows_map(CUtensorMap* m, const void* base, int rank, const int64_t* dim
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
+// The arguments of an attention call that do not depend on where its keys are.
+AttnArgs attn_args(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, void* workspace, int* status)
+{
+    AttnArgs a = {};
+    a.sched = static_cast<const ScheduleHead*>(step->schedule);
+    a.out = static_cast<__nv_bfloat16*>(io->out);
+    a.ldo = io->ldo;
+    a.ho = io->ho;
+    a.lse = io->lse;
+    a.cu_end = io->zero_padding ? step->cu_q + step->requests : nullptr;
+    a.tokens = step->tokens;
+    a.heads = (int)step->heads;
+    a.kv_heads = (int)step->kv_heads;
+    a.group = a.heads / a.kv_heads;
+    a.row_tokens = row_tile_tokens(a.group);
+    a.head_dim = (int)io->head_dim;
+    a.window = (int)step->window;
+    a.scale = io->scale;
+    a.tickets = static_cast<int*>(workspace);
+    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttnTicketBytes);
+    a.status = status;
+    return a;
 }
 
 int run_attn(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const AttnKV& kv, void* workspace,
@@ -797,30 +823,15 @@ int run_attn(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const AttnKV& 
         NVFP4_TRY(make_rows_map(&mk, kv.k, 3, dims, sk, box));
         NVFP4_TRY(make_rows_map(&mv, kv.v, 3, dims, sv, box));
     }
-    AttnArgs a = {};
-    a.sched = static_cast<const ScheduleHead*>(step->schedule);
-    a.out = static_cast<__nv_bfloat16*>(io->out);
-    a.ldo = io->ldo;
-    a.ho = io->ho;
-    a.lse = io->lse;
-    a.cu_end = io->zero_padding ? step->cu_q + step->requests : nullptr;
-    a.tokens = step->tokens;
-    a.heads = (int)step->heads;
-    a.kv_heads = (int)step->kv_heads;
-    a.group = group;
-    a.row_tokens = row_tile_tokens(group);
-    a.head_dim = (int)D;
-    a.window = (int)step->window;
-    a.scale = io->scale;
+    AttnArgs a = attn_args(step, io, workspace, d->status);
+    a.k_g = kv.k_g;
+    a.v_g = kv.v_g;
     if (kv.cache) {
         a.block_table = step->block_table;
         a.table_ld = step->table_ld;
         a.page_size = (int)kv.cache->page_size;
         a.fold = fold ? 1 : 0;
     }
-    a.tickets = static_cast<int*>(workspace);
-    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttnTicketBytes);
-    a.status = d->status;
     NVFP4_CUDA(launch_attn(mq, mk, mv, a, d->num_sms, (cudaStream_t)stream));
     return NVFP4_OK;
 }
@@ -1054,6 +1065,43 @@ int nvfp4_kv4_expand(const nvfp4_kv4_cache_t* cache, const nvfp4_step_t* step, c
     DeviceInfo* d = nullptr;
     NVFP4_TRY(device_info(&d));
     NVFP4_CUDA(launch_kv4_expand(*cache, *step, *out, true, d->num_sms, (cudaStream_t)stream));
+    return NVFP4_OK;
+}
+
+int nvfp4_attn_paged4(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const nvfp4_kv4_cache_t* cache,
+                      const nvfp4_kv_cache_t* expanded, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream)
+{
+    NVFP4_TRY(check_step(step, 3));
+    NVFP4_TRY(check_io(step, io));
+    NVFP4_TRY(check_cache4(cache));
+    if (cache->page_size != step->page_size || cache->kv_heads != step->kv_heads || cache->head_dim != io->head_dim)
+        return NVFP4_ERR_INVALID_ARG;
+    if (expanded) NVFP4_TRY(check_same_pages(cache, expanded));
+    if (io->lse && !aligned(io->lse, 4)) return NVFP4_ERR_MISALIGNED;
+    if (!workspace || workspace_bytes < nvfp4_attn_workspace_bytes()) return NVFP4_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return NVFP4_ERR_MISALIGNED;
+    DeviceInfo* d = nullptr;
+    NVFP4_TRY(device_info(&d));
+    cudaStream_t st = (cudaStream_t)stream;
+    const int64_t rows = (step->tokens + step->requests - 1) / step->requests * (step->heads / step->kv_heads);
+    if (expanded && rows >= kExpandRows) {
+        NVFP4_CUDA(launch_kv4_expand(*cache, *step, *expanded, false, d->num_sms, st));
+        AttnKV kv = {};
+        kv.k = expanded->k;
+        kv.v = expanded->v;
+        kv.cache = expanded;
+        kv.k_g = cache->k_g;
+        kv.v_g = cache->v_g;
+        return run_attn(step, io, kv, workspace, workspace_bytes, stream);
+    }
+    AttnArgs a = attn_args(step, io, workspace, d->status);
+    a.k_g = cache->k_g;
+    a.v_g = cache->v_g;
+    a.block_table = step->block_table;
+    a.table_ld = step->table_ld;
+    a.page_size = (int)cache->page_size;
+    NVFP4_CUDA(launch_attn4(a, *cache, static_cast<const __nv_bfloat16*>(io->q), io->ldq, io->hq, step->requests,
+                            d->num_sms, st));
     return NVFP4_OK;
 }
 

@@ -104,6 +104,8 @@ struct AttnArgs {
     int row_tokens;      // tokens of a row tile
     int window;
     float scale;
+    const float* k_g;    // device scalars that multiply every score and every output, or NULL: 1
+    const float* v_g;
     // paged cache (block_table NULL: packed keys)
     const int32_t* block_table;
     int64_t table_ld;

@@ -9,6 +9,9 @@ namespace nvfp4 {
 // Device status of the page operators (NVFP4_ERR_INVALID_ARG * 100 + site).
 constexpr int kStatusPages = NVFP4_ERR_INVALID_ARG * 100 + 34;
 
+// Rows of a request, on average, from which a step's keys are expanded once.
+constexpr int64_t kExpandRows = 64;
+
 constexpr int64_t kMaxPages = 1 << 20;      // of the page operators (a bit each in shared memory)
 constexpr int kMaxPlanes = 64;              // of one copying launch
 constexpr int64_t kPageCopyChunk = 16384;   // bytes of a page that a block copies
@@ -25,6 +28,10 @@ cudaError_t launch_heads(const nvfp4_heads_t& heads, int* status, int num_sms, c
 // times the cache's global scales (else code times E4M3 scale, exact in bf16).
 cudaError_t launch_kv4_expand(const nvfp4_kv4_cache_t& cache, const nvfp4_step_t& step, const nvfp4_kv_cache_t& out,
                               bool scaled, int num_sms, cudaStream_t stream);
+
+// Attention over a 4-bit cache (args.k_g, v_g and the paged fields set).
+cudaError_t launch_attn4(const AttnArgs& args, const nvfp4_kv4_cache_t& cache, const __nv_bfloat16* q, int64_t ldq,
+                         int64_t hq, int64_t requests, int num_sms, cudaStream_t stream);
 
 cudaError_t launch_pages_fork(const nvfp4_pages_t& t, const int32_t* src, const int32_t* dst, int64_t n,
                               const int32_t* free_pages, int64_t free_count, const int32_t* cursor,

@@ -168,3 +168,20 @@ def test_binding_checks_its_tensors(nv):
         nv.nvfp4_qk_norm_rope(None, None)
     with pytest.raises(ValueError):
         nv.nvfp4_pages_copy([], torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+def test_attention_refusals(nv):
+    from test_attn_host import IO_BAD, WORKSPACE, io
+    L, c = nv.lib(), ctypes.byref(cache4(nv))
+    for bad, status in CACHE4_BAD:
+        assert L.nvfp4_attn_paged4(step(nv), io(nv), ctypes.byref(cache4(nv, **bad)), None, A, 1 << 40, None) == status, bad
+    for bad, status in IO_BAD:
+        assert L.nvfp4_attn_paged4(step(nv), io(nv, **bad), c, None, A, 1 << 40, None) == status, bad
+    for bad in (dict(pages=11), dict(kv_heads=1), dict(head_dim=64), dict(k=None)):
+        assert L.nvfp4_attn_paged4(step(nv), io(nv), c, cache(nv, **bad), A, 1 << 40, None) == INVALID, bad
+    for s in (step(nv, page_size=0), step(nv, page_size=32), step(nv, heads=0), step(nv, kv_heads=1), None):
+        assert L.nvfp4_attn_paged4(s, io(nv), c, None, A, 1 << 40, None) == INVALID
+    assert L.nvfp4_attn_paged4(step(nv), None, c, None, A, 1 << 40, None) == INVALID
+    assert L.nvfp4_attn_paged4(step(nv), io(nv), None, None, A, 1 << 40, None) == INVALID
+    for ws, n, status in ((None, 1 << 40, WORKSPACE), (A, 16, WORKSPACE), (A + 128, 1 << 40, MISALIGNED)):
+        assert L.nvfp4_attn_paged4(step(nv), io(nv), c, None, ws, n, None) == status
