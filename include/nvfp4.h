@@ -608,8 +608,8 @@ struct nvfp4_kv4_cache {
     const float* v_g;
     int64_t pages, page_size, kv_heads;
     int64_t head_dim;          /* 16 .. 128, % 16 == 0 */
-    int64_t page_stride;       /* bytes, >= kv_heads*page_size*head_dim/2, % 16 == 0 */
-    int64_t sf_stride;         /* bytes, >= kv_heads*page_size*head_dim/16, % 16 == 0 */
+    int64_t page_stride;       /* bytes, >= kv_heads*page_size*head_dim/2, % 16 == 0, below 2^32 */
+    int64_t sf_stride;         /* bytes, >= kv_heads*page_size*head_dim/16, % 16 == 0, below 2^32 */
 };
 
 /*

@@ -947,7 +947,7 @@ int check_cache4(const nvfp4_kv4_cache_t* c)
     if (!page_size_ok(P)) return NVFP4_ERR_INVALID_ARG;
     NVFP4_TRY(check_head_dim(D));
     if (D % 16 != 0 || c->pages > INT32_MAX / P || c->kv_heads > 65535 || c->page_stride < c->kv_heads * P * D / 2 ||
-        c->sf_stride < c->kv_heads * P * D / 16)
+        c->sf_stride < c->kv_heads * P * D / 16 || c->page_stride > UINT32_MAX || c->sf_stride > UINT32_MAX)
         return NVFP4_ERR_INVALID_ARG;
     for (const void* x : {(const void*)c->k, (const void*)c->v, (const void*)c->k_sf, (const void*)c->v_sf})
         if (!aligned(x, 16)) return NVFP4_ERR_MISALIGNED;
