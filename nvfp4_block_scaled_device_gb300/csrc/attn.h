@@ -34,6 +34,7 @@ constexpr int kAttnRows = 128;
 constexpr int kAttnKeys = 128;
 constexpr int kAttnMaxCtas = 256;
 constexpr int kItemUnits = 2;
+constexpr int kItemUnits4 = 2, kChunksOfTile = 4;
 
 struct QTile {
     int32_t tok0, n_tok;     // packed rows (tokens) tok0 .. tok0 + n_tok - 1
@@ -45,15 +46,30 @@ struct QTile {
 static_assert(sizeof(QTile) == 32, "QTile");
 
 struct ScheduleHead {
-    int32_t units, per_cta, qtiles, pad[13];
+    int32_t units, per_cta, qtiles;
+    // The second axis, for the attention that gives each warp its own share
+    // (attn4.cu): an item is kItemUnits4 units, then one per 32 keys of its tiles,
+    // kChunksOfTile for each; QTile i begins at 4 unit0 - (4 kItemUnits -
+    // kItemUnits4) kv_heads i.  CTA c takes units c * per_cta4 .. as above.
+    int32_t units4, per_cta4;      // 0: too long for it
+    int32_t most_tokens;           // of a QTile
+    int32_t pad[10];
     int32_t first[kAttnMaxCtas];   // QTile of the first unit of CTA c ...
     QTile start[kAttnMaxCtas];     // ... and a copy of it, next to what a CTA reads first
+    int32_t first4[kAttnMaxCtas];  // the same of the second axis
+    QTile start4[kAttnMaxCtas];
 };
 static_assert(sizeof(ScheduleHead) % 16 == 0, "QTiles follow the head, 16-byte aligned");
 
 inline __host__ __device__ const QTile* schedule_tiles(const ScheduleHead* h)
 {
     return reinterpret_cast<const QTile*>(h + 1);
+}
+
+// Units of the second axis before QTile i.
+inline __host__ __device__ int64_t units4_before(int64_t unit0, int64_t kv_heads, int64_t i)
+{
+    return kChunksOfTile * unit0 - (kChunksOfTile * kItemUnits - kItemUnits4) * kv_heads * i;
 }
 
 // Boundary r (units from the item's start) of an item of `item` units.  A part
@@ -64,6 +80,14 @@ constexpr int kMinPart = 3;
 inline __host__ __device__ int snap_unit(int r, int item)
 {
     const bool head = r < kItemUnits + kMinPart, tail = item - r < kMinPart;
+    return r >= item ? item : head && tail ? (2 * r < item ? 0 : item) : head ? 0 : tail ? item : r;
+}
+
+// The same on the second axis, in chunks of 32 keys.
+constexpr int kMinPart4 = 8;
+inline __host__ __device__ int snap_unit4(int r, int item)
+{
+    const bool head = r < kItemUnits4 + kMinPart4, tail = item - r < kMinPart4;
     return r >= item ? item : head && tail ? (2 * r < item ? 0 : item) : head ? 0 : tail ? item : r;
 }
 

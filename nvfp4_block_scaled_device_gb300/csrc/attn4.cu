@@ -42,6 +42,7 @@ namespace {
 
 constexpr int kHalf = 16;              // keys of a page's smallest run, and of an MMA
 constexpr int kChunk = 2 * kHalf;      // keys of a ring's stage
+static_assert(kChunk * kChunksOfTile == kAttnKeys, "chunks of the schedule");
 constexpr float kLazy = 8.0f;          // log2 of the growth that P may carry
 constexpr float kLift = 6.0f;          // log2 of P at m
 constexpr float kLog2e = 1.4426950408889634f;
@@ -52,6 +53,7 @@ struct Cfg4 {
     static constexpr int kStages = kNT == 1 ? 2 : 3;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRows = 8 * kNT;
+    static constexpr bool kOwnShares = kNT <= 2;                 // shares of warps (see above)
     static constexpr int kAtOnce = kNT == 1 ? 2 : 1;             // halves of a chunk worked on together
     static constexpr int kRowBytes = kDP / 2;
     static constexpr int kCodes = kHalf * kRowBytes;             // of K or V of half a chunk
@@ -59,31 +61,19 @@ struct Cfg4 {
     static constexpr int kHalfBytes = 2 * (kCodes + kScales);    // K, V, scales of K, scales of V
     static constexpr int kStageBytes = 2 * kHalfBytes;
     static constexpr int kRing = kWarps * kStages * kStageBytes;
-    // O of all warps for kJoin tiles of 8 rows: two rows and 4 words of padding a line
+    // O of all warps for kJoin tiles of 8 rows: two rows and 4 words of padding a
+    // line (or a warp's own lanes, one vector after the other)
     static constexpr int kJoin = 16 / kWarps;
     static constexpr int kLine = 2 * kDP + 4;
     static constexpr int kWarpO = kJoin * 4 * kLine;             // floats
+    static_assert(!kOwnShares || kWarpO >= kRows * kDP, "a warp's O");
     static constexpr int kOffO = kRing;
     static constexpr int kOffQ = kOffO + kWarps * kWarpO * 4;    // Q's rows (bf16), then (kNT > 1) its fragments
     static constexpr int kOffFrag = kOffQ + kRows * kDP * 2;
     static constexpr int kOffM = kOffFrag + (kNT > 1 ? kNT * (kDP / 16) * 32 * 8 : 0);
     static constexpr int kSmem = kOffM + kWarps * kRows * 2 * 4;
     static constexpr int kQVecs = kRows * kDP / 8 / kThreads > 0 ? kRows * kDP / 8 / kThreads : 1;
-    static_assert(kSmem <= 232448 - 1024, "shared memory per block");
-};
-
-// One pass of a CTA over the keys of a piece, for up to kRows of its rows.  The
-// first warp writes them down two ahead, in shared memory, for all to read.
-struct Pass {
-    int valid;
-    int rows, r0;            // rows of the piece's item; the pass is for rows r0 ..
-    int tok0, pos0, hk;
-    int kv_end, key_end;     // no row sees keys from kv_end on; the piece ends at key_end
-    int lo, lo_all, hi_all;  // some row sees key lo; all see lo_all .. hi_all - 1
-    int kb, ke;              // keys of the pass (kb a multiple of kChunk)
-    int cta0, parts;
-    int last;                // of the piece
-    const int32_t* table;    // the request's pages
+    static_assert(kSmem <= 232448 - 4096, "shared memory per block");
 };
 
 struct Params4 {
@@ -158,6 +148,414 @@ __device__ __forceinline__ void copies_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
+// Log of a row's sum of 2^(score - m + kLift), to base e.
+__device__ __forceinline__ float log_sum(float m, float l)
+{
+    return l == 0.0f ? -INFINITY : (m - kLift + log2f(l)) * 0.6931471805599453f;
+}
+
+// What a warp has of up to 8 kNT rows: a lane has, of rows 2j and 2j + 1 of each
+// tile (j = lane % 4), kDP / 8 columns of O, and their statistics.
+template <int kDP, int kNT>
+struct Rows {
+    float o[kNT][kDP / 16][4];                 // two columns: one of rows 2j, 2j + 1, then the next of them
+    float m[kNT][2], nm[kNT][2];               // maximum (log2); kLift - maximum
+    float limit[kNT][2];                       // the score from which the maximum moves
+    float l[kNT][2];                           // sum over this lane's keys
+    float cf[kNT][2];                          // the row's factor of the scores
+
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int n = 0; n < kNT; n++) {
+#pragma unroll
+            for (int s = 0; s < kDP / 16; s++) o[n][s][0] = o[n][s][1] = o[n][s][2] = o[n][s][3] = 0.0f;
+#pragma unroll
+            for (int y = 0; y < 2; y++) m[n][y] = limit[n][y] = -INFINITY, nm[n][y] = l[n][y] = 0.0f;
+        }
+    }
+    // The sums of a row's lanes.
+    __device__ __forceinline__ void join_sums()
+    {
+#pragma unroll
+        for (int n = 0; n < kNT; n++) {
+#pragma unroll
+            for (int y = 0; y < 2; y++) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[n][y] += __shfl_xor_sync(0xffffffffu, l[n][y], x);
+            }
+        }
+    }
+};
+
+// One tile's Q in fragments: raw holds this lane's kDP / 4 columns (from kDP / 4
+// * j) of row g as bf16 and becomes f16 for the MMAs.  Scaled by 2^(141 - e), e
+// the row's largest biased exponent, which brings that to 2^14 .. 2^15; the
+// factor of the row's scores (for the rows of this lane's accumulators) takes it
+// back.  A negative scale's sign goes into Q; a zero scale is any tiny factor (no
+// 0 * inf where masked).
+template <int kDP>
+__device__ __forceinline__ void make_q(uint32_t* raw, float scale, float k_g, float* cf, int j)
+{
+    float amax = 0.0f;
+#pragma unroll
+    for (int x = 0; x < kDP / 8; x++) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(raw[x])), fabsf(bf16_hi(raw[x]))));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const int e = max((int)(__float_as_uint(amax) >> 23), 15);
+    const float up = __uint_as_float((uint32_t)(268 - e) << 23 | (__float_as_uint(scale) & 0x80000000u));
+    const float down = __uint_as_float((uint32_t)(e - 14) << 23);
+#pragma unroll
+    for (int x = 0; x < kDP / 8; x++) raw[x] = cvt_f16x2(bf16_lo(raw[x]) * up, bf16_hi(raw[x]) * up);
+    const float c = fmaxf(fabsf(scale) * kLog2e * k_g * down, 1.17549435e-38f);
+    cf[0] = __shfl_sync(0xffffffffu, c, 8 * j);
+    cf[1] = __shfl_sync(0xffffffffu, c, 8 * j + 4);
+}
+
+// Which keys rows see.
+struct Seen {
+    int pos0, r0, group;         // position of row r of the tiles: pos0 + (r0 + r) / group
+    int lo, ke, window;          // some row sees keys lo .. ke - 1, none one past
+};
+
+// kH halves of a chunk at `st`, keys k0 ..: scores, softmax, products.  edge:
+// some row does not see all of them.  q(n, x): fragment x of tile n's Q.
+template <int kDP, int kNT, bool kFull, int kH, typename Q>
+__device__ __forceinline__ void work_halves(const uint8_t* st, int k0, bool edge, const Seen& seen, int nb,
+                                            Rows<kDP, kNT>& w, Q&& q, int g, int j)
+{
+    using C = Cfg4<kDP, kNT>;
+    constexpr int kSteps = kDP / 16;
+    const int key_row = (g >> 1) + 4 * (g & 1);            // key of a half that is row g of its S^T (and 8 + it)
+    // ---- S^T = K Q^T
+    float s[kH][kNT][4];
+#pragma unroll
+    for (int h = 0; h < kH; h++) {
+        const uint8_t* sk = st + h * C::kHalfBytes;
+        uint32_t code[2][kDP / 32];                        // of keys key_row and 8 + key_row
+        __half2 sc[2];                                     // their scales (128 columns: of two blocks)
+#pragma unroll
+        for (int y = 0; y < 2; y++) {
+            const int key = key_row + 8 * y;
+            const uint8_t* sf = sk + 2 * C::kCodes + key * nb;
+            if (kDP == 128) {
+                const uint4 x = *reinterpret_cast<const uint4*>(sk + key * C::kRowBytes + j * 16);
+                code[y][0] = x.x, code[y][1] = x.y, code[y][kDP / 32 - 2] = x.z, code[y][kDP / 32 - 1] = x.w;
+                uint32_t b;
+                if (kFull) {
+                    b = *reinterpret_cast<const uint16_t*>(sf + 2 * j);
+                } else {
+                    b = 2 * j < nb ? sf[2 * j] : 0u;
+                    b |= 2 * j + 1 < nb ? (uint32_t)sf[2 * j + 1] << 8 : 0u;
+                }
+                sc[y] = as_half2(e4m3x2_to_f16x2(b));
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(sk + key * C::kRowBytes + j * 8);
+                code[y][0] = x.x, code[y][1] = x.y;
+                sc[y] = as_half2(e4m3x2_to_f16x2(j < nb ? sf[j] : 0u));
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < kNT; n++) s[h][n][0] = s[h][n][1] = s[h][n][2] = s[h][n][3] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kDP / 32; x++) {               // a word of codes: two MMAs
+            uint32_t f[2][4];
+#pragma unroll
+            for (int y = 0; y < 2; y++) {
+                e2m1x8_to_f16x2(code[y][x], f[y]);
+                const __half2 z = kDP == 128 && x >= 2 ? __high2half2(sc[y]) : __low2half2(sc[y]);
+#pragma unroll
+                for (int u = 0; u < 4; u++) f[y][u] = as_u32(__hmul2(as_half2(f[y][u]), z));
+            }
+#pragma unroll
+            for (int u = 0; u < 2; u++) {
+                const uint32_t fa[4] = {f[0][2 * u], f[1][2 * u], f[0][2 * u + 1], f[1][2 * u + 1]};
+#pragma unroll
+                for (int n = 0; n < kNT; n++) {
+                    const uint2 b = q(n, 2 * x + u);
+                    mma16816(s[h][n], fa, b.x, b.y);
+                }
+            }
+        }
+    }
+    // ---- softmax
+    if (edge) {
+#pragma unroll
+        for (int h = 0; h < kH; h++) {
+#pragma unroll
+            for (int n = 0; n < kNT; n++) {
+#pragma unroll
+                for (int y = 0; y < 4; y++) {
+                    const int pos = seen.pos0 + (seen.r0 + 8 * n + 2 * j + (y & 1)) / seen.group;
+                    const int key = k0 + h * kHalf + key_row + 8 * (y >> 1);
+                    if (key > pos || key >= seen.ke || (seen.window && key <= pos - seen.window)) s[h][n][y] = -INFINITY;
+                }
+            }
+        }
+    }
+    bool up = false;
+#pragma unroll
+    for (int n = 0; n < kNT; n++) {
+#pragma unroll
+        for (int y = 0; y < 2; y++) {
+            float top = fmaxf(s[0][n][y], s[0][n][y + 2]);
+            if (kH == 2) top = fmaxf(top, fmaxf(s[kH - 1][n][y], s[kH - 1][n][y + 2]));
+            up |= top > w.limit[n][y];
+        }
+    }
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int n = 0; n < kNT; n++) {
+#pragma unroll
+            for (int y = 0; y < 2; y++) {
+                float top = fmaxf(s[0][n][y], s[0][n][y + 2]);
+                if (kH == 2) top = fmaxf(top, fmaxf(s[kH - 1][n][y], s[kH - 1][n][y + 2]));
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                top = fmaxf(top * w.cf[n][y], w.m[n][y]);
+                const float f = w.m[n][y] == -INFINITY ? 0.0f : ex2(w.m[n][y] - top);
+                w.m[n][y] = top;
+                w.nm[n][y] = top == -INFINITY ? 0.0f : kLift - top;
+                w.limit[n][y] = (top + kLazy) / w.cf[n][y];
+                w.l[n][y] *= f;
+#pragma unroll
+                for (int x = 0; x < kSteps; x++) {
+                    w.o[n][x][y] *= f;
+                    w.o[n][x][y + 2] *= f;
+                }
+            }
+        }
+    }
+    uint32_t pt[kH][kNT][2];
+#pragma unroll
+    for (int h = 0; h < kH; h++) {
+#pragma unroll
+        for (int n = 0; n < kNT; n++) {
+            float e[4];
+#pragma unroll
+            for (int y = 0; y < 4; y++) {
+                e[y] = ex2(fmaf(s[h][n][y], w.cf[n][y & 1], w.nm[n][y & 1]));
+                w.l[n][y & 1] += e[y];
+            }
+            pt[h][n][0] = transpose8x8(cvt_f16x2(e[0], e[1]));
+            pt[h][n][1] = transpose8x8(cvt_f16x2(e[2], e[3]));
+        }
+    }
+    // ---- O^T += V^T P^T: keys j, j + 4 and j + 8, j + 12 of a half, columns kDP / 8 * g ..
+    constexpr int kVW = kDP / 64;                          // words of a key's codes
+#pragma unroll
+    for (int h = 0; h < kH; h++) {
+        const uint8_t* sv = st + h * C::kHalfBytes + C::kCodes;
+        const uint8_t* sf = sv + C::kCodes + C::kScales;
+        uint32_t v[4][kVW], b[4];
+        const int blk = kDP == 128 ? g : g >> 1;
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            const int key = j + 4 * u;
+            if (kVW == 2) {
+                const uint2 x = *reinterpret_cast<const uint2*>(sv + key * C::kRowBytes + g * 8);
+                v[u][0] = x.x, v[u][kVW - 1] = x.y;
+            } else {
+                v[u][0] = *reinterpret_cast<const uint32_t*>(sv + key * C::kRowBytes + g * 4);
+            }
+            b[u] = kFull || blk < nb ? sf[key * nb + blk] : 0u;
+        }
+        if (edge) {                                        // a value that no row sees may be anything
+            const int lo = seen.lo - k0 - h * kHalf, ke = seen.ke - k0 - h * kHalf;
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+                if (j + 4 * u < lo || j + 4 * u >= ke) b[u] = 0u;
+        }
+        const __half2 vs[2] = {as_half2(e4m3x2_to_f16x2(__byte_perm(b[0], b[1], 0x3340))),
+                               as_half2(e4m3x2_to_f16x2(__byte_perm(b[2], b[3], 0x3340)))};
+#pragma unroll
+        for (int y = 0; y < kVW; y++) {
+            uint32_t even[2][4], odd[2][4];                // two keys side by side, of even and odd columns
+#pragma unroll
+            for (int u = 0; u < 2; u++) {
+                const uint32_t x0 = v[2 * u][y], x1 = v[2 * u + 1][y];
+                e2m1x8_to_f16x2((x0 & 0x0f0f0f0fu) | (x1 << 4 & 0xf0f0f0f0u), even[u]);
+                e2m1x8_to_f16x2((x0 >> 4 & 0x0f0f0f0fu) | (x1 & 0xf0f0f0f0u), odd[u]);
+            }
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+                uint32_t f[4];
+#pragma unroll
+                for (int u = 0; u < 2; u++) {
+                    f[2 * u] = as_u32(__hmul2(as_half2(even[u][x]), vs[u]));
+                    f[2 * u + 1] = as_u32(__hmul2(as_half2(odd[u][x]), vs[u]));
+                }
+#pragma unroll
+                for (int n = 0; n < kNT; n++) mma16816(w.o[n][4 * y + x], f, pt[h][n][0], pt[h][n][1]);
+            }
+        }
+    }
+}
+
+// A warp's ring of chunks, and the copies into it.  kRowChunks: lanes' shares.
+template <int kDP, int kNT, bool kFull>
+struct Ring {
+    using C = Cfg4<kDP, kNT>;
+    const Params4& prm;
+    uint8_t* base;
+    uint32_t addr;
+    int lane, D, nb, chunk, chunks;            // bytes of a copy, copies of a half's codes
+    int to[kFull ? 1 : 4];
+    uint32_t sf_to;
+    const uint8_t* sf_base;
+    int in = 0, out = 0, ahead = 0;            // stages to fill and to read next; filled ones
+
+    __device__ __forceinline__ Ring(const Params4& prm, uint8_t* base, int lane, int D) : prm(prm), base(base), lane(lane), D(D)
+    {
+        addr = smem_u32(base);
+        nb = D / 16;
+        // 16 bytes of codes (or, where a row is not whole sixteens, 8) and of
+        // scales (16 keys' are D bytes)
+        chunk = kFull || D % 32 == 0 ? 16 : 8;
+        const int per_row = D / 2 / chunk;
+        chunks = kHalf * per_row;
+#pragma unroll
+        for (int i = 0; i < (kFull ? 1 : 4); i++) {
+            const int c = lane + 32 * i;
+            to[i] = (c / per_row) * C::kRowBytes + (c % per_row) * chunk;
+        }
+        const bool of_v = lane >> 3 & 1;
+        sf_to = (lane >> 4) * C::kHalfBytes + 2 * C::kCodes + (of_v ? C::kScales : 0) + (lane & 7) * 16;
+        sf_base = (of_v ? prm.v_sf : prm.k_sf) + (lane & 7) * 16;
+    }
+    // Page ids of the halves of 16 chunks, `stride` keys apart, from key k on:
+    // a lane each; none from ke on.
+    __device__ __forceinline__ int load_ids(const int32_t* table, int k, int stride, int ke) const
+    {
+        k += (lane >> 1) * stride + (lane & 1) * kHalf;
+        return k < ke ? table[k >> prm.page_shift] : -1;
+    }
+    // Copies of the chunk of keys k0 .., kv head hk, into the next stage; the ids
+    // of its pages are in lanes 2i and 2i + 1.  A page that the cache does not have
+    // is zeros; a half past the keys' end is masked as a whole.
+    __device__ __forceinline__ void copy(int k0, int hk, int ids, int i)
+    {
+        const uint32_t st = addr + in * C::kStageBytes;
+        const int page_mask = (1 << prm.page_shift) - 1;
+        const int row0 = (hk << prm.page_shift) + (k0 & page_mask);
+        const int row1 = (hk << prm.page_shift) + ((k0 + kHalf) & page_mask);
+        const uint32_t id0 = __shfl_sync(0xffffffffu, ids, 2 * i), id1 = __shfl_sync(0xffffffffu, ids, 2 * i + 1);
+        const bool real0 = id0 < (uint32_t)prm.pages, real1 = id1 < (uint32_t)prm.pages;
+        const uint32_t page0 = real0 ? id0 : 0u, page1 = real1 ? id1 : 0u;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const uint64_t at = (uint64_t)(h ? page1 : page0) * prm.page_stride + (uint32_t)((h ? row1 : row0) * (D / 2));
+            const bool real = h ? real1 : real0;
+            const uint32_t sh = st + h * C::kHalfBytes + to[0];
+            const uint8_t* ck = prm.k + lane * chunk + at;
+            const uint8_t* cv = prm.v + lane * chunk + at;
+            if (kFull) {
+                const int n = real ? 16 : 0;
+                copy16<0>(sh, ck, n);
+                if (kDP == 128) copy16<512>(sh, ck, n);
+                copy16<0>(sh + C::kCodes, cv, n);
+                if (kDP == 128) copy16<512>(sh + C::kCodes, cv, n);
+            } else if (chunk == 16) {
+#pragma unroll
+                for (int y = 0; y < (kDP == 128 ? 2 : 1); y++)
+                    if (lane + 32 * y < chunks) {
+                        copy16<0>(sh + to[kFull ? 0 : y] - to[0], ck + 512 * y, real ? 16 : 0);
+                        copy16<0>(sh + C::kCodes + to[kFull ? 0 : y] - to[0], cv + 512 * y, real ? 16 : 0);
+                    }
+            } else {
+#pragma unroll
+                for (int y = 0; y < (kDP == 128 ? 4 : 2); y++)
+                    if (lane + 32 * y < chunks) {
+                        copy8(sh + to[kFull ? 0 : y] - to[0], ck + 256 * y, real ? 8 : 0);
+                        copy8(sh + C::kCodes + to[kFull ? 0 : y] - to[0], cv + 256 * y, real ? 8 : 0);
+                    }
+            }
+        }
+        const bool second = lane >> 4;
+        if ((lane & 7) * 16 < D)
+            copy16<0>(st + sf_to, sf_base + (uint64_t)(second ? page1 : page0) * prm.sf_stride + (uint32_t)((second ? row1 : row0) * nb),
+                      (second ? real1 : real0) ? 16 : 0);
+        copies_end();
+        in = in + 1 == C::kStages ? 0 : in + 1;
+        ahead++;
+    }
+    // The oldest chunk, once it is there.
+    __device__ __forceinline__ const uint8_t* wait()
+    {
+        if (C::kStages == 3 && ahead == 3) copies_wait<2>();
+        else if (ahead >= 2) copies_wait<1>();
+        else copies_wait<0>();
+        __syncwarp();
+        return base + out * C::kStageBytes;
+    }
+    __device__ __forceinline__ void release()
+    {
+        __syncwarp();
+        out = out + 1 == C::kStages ? 0 : out + 1;
+        ahead--;
+    }
+};
+
+// The parts of an item that CTAs share, added up by all threads of the last of
+// them: part i is in slot 2 (cta0 + i), the first in 2 cta0 + 1.
+template <int kDP, int kThreads>
+__device__ __forceinline__ void join_parts(const AttnArgs& a, int cta0, int parts, int rows, int tok0, int hk, float v_g)
+{
+    auto slot_of = [&](int i) { return a.partials + (2 * (cta0 + i) + (i == 0 ? 1 : 0)) * kAttnSlotFloats; };
+    for (int x = threadIdx.x; x < rows * (kDP / 2); x += kThreads) {
+        const int r = x / (kDP / 2), col = 2 * (x % (kDP / 2));
+        if (col >= a.head_dim) continue;
+        const int t = r / a.group, head = hk * a.group + r - t * a.group;
+        float top = -INFINITY, sum = 0.0f;
+        float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+        for (int i0 = 0; i0 < parts; i0 += 8) {
+            float2 ml[8], e[8];
+#pragma unroll
+            for (int u = 0; u < 8; u++) {
+                const float* from = slot_of(min(i0 + u, parts - 1));
+                ml[u] = __ldcg(reinterpret_cast<const float2*>(from + kAttnSlotRows * kDP + 2 * r));
+                e[u] = __ldcg(reinterpret_cast<const float2*>(from + r * kDP + col));
+                if (i0 + u >= parts) ml[u] = make_float2(-INFINITY, 0.0f);
+            }
+            float most = top;
+#pragma unroll
+            for (int u = 0; u < 8; u++) most = fmaxf(most, ml[u].x);
+            const float f0 = top == -INFINITY ? 0.0f : ex2(top - most);
+            acc.x *= f0;
+            acc.y *= f0;
+            sum *= f0;
+            top = most;
+#pragma unroll
+            for (int u = 0; u < 8; u++) {
+                if (ml[u].y == 0.0f) continue;             // no key of this part
+                const float f = ml[u].x == -INFINITY ? 0.0f : ex2(ml[u].x - top);
+                acc.x += f * e[u].x;
+                acc.y += f * e[u].y;
+                sum += f * ml[u].y;
+            }
+        }
+        const float inv = sum == 0.0f ? 0.0f : v_g / sum;
+        *reinterpret_cast<uint32_t*>(a.out + (int64_t)(tok0 + t) * a.ldo + (int64_t)head * a.ho + col) =
+            sum == 0.0f ? 0u : cvt_bf16x2(acc.x * inv, acc.y * inv);
+        if (col == 0 && a.lse)
+            a.lse[(int64_t)(tok0 + t) * a.heads + head] = log_sum(top, sum);
+    }
+}
+
+// One pass of a CTA over the keys of a piece, for up to kRows of its rows.  The
+// first warp writes them down two ahead, in shared memory, for all to read.
+struct Pass {
+    int valid;
+    int rows, r0;            // rows of the piece's item; the pass is for rows r0 ..
+    int tok0, pos0, hk;
+    int kv_end, key_end;     // no row sees keys from kv_end on; the piece ends at key_end
+    int lo, lo_all, hi_all;  // some row sees key lo; all see lo_all .. hi_all - 1
+    int kb, ke;              // keys of the pass (kb a multiple of kChunk)
+    int cta0, parts;
+    int last;                // of the piece
+    const int32_t* table;    // the request's pages
+};
 
 // The passes of CTA `cta` in order.
 template <int kRows>
@@ -200,29 +598,22 @@ struct Passes {
     }
 };
 
+// ------------------------------------------------ passes of all warps together
 template <int kDP, int kNT, bool kFull>
-__global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(const __grid_constant__ Params4 prm)
+__device__ __forceinline__ void passes_together(const Params4& prm, uint8_t* smem, int cta)
 {
     using C = Cfg4<kDP, kNT>;
     constexpr int kSteps = kDP / 16;           // MMAs over a key's columns; of 16 columns of O
-    constexpr int kH = C::kAtOnce;
-    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_last;
     __shared__ Pass s_pass[3];
     const AttnArgs& a = prm.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
-    const int cta = blockIdx.x, D = kFull ? kDP : a.head_dim, nb = D / 16;
-    uint8_t* ring = smem + warp * (C::kStages * C::kStageBytes);
-    const uint32_t ring_addr = smem_u32(ring);
+    const int D = kFull ? kDP : a.head_dim, nb = D / 16;
     float* o_all = reinterpret_cast<float*>(smem + C::kOffO);
     float2* m_all = reinterpret_cast<float2*>(smem + C::kOffM);            // [warp][row] m, l
     uint4* q_rows = reinterpret_cast<uint4*>(smem + C::kOffQ);             // [row][kDP / 8]
     uint2* q_frag = reinterpret_cast<uint2*>(smem + C::kOffFrag);          // [tile][step][lane]
 
-    griddep_launch_dependents();
-    if (!kFull)                                 // the columns that no copy writes are zeros
-        for (int i = tid; i < C::kRing / 16; i += C::kThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
-    griddep_wait();
     Passes<C::kRows> passes(a, cta);            // (the first warp's)
     if (warp == 0) {
         passes.next(a, &s_pass[0], lane);
@@ -230,76 +621,14 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
     }
     __syncthreads();
 
-    // this lane's share of a half's copies: 16 bytes of codes (or, where a row is
-    // not whole sixteens, 8) and of scales (16 keys' are D bytes)
-    const int chunk = kFull || D % 32 == 0 ? 16 : 8, per_row = D / 2 / chunk, chunks = kHalf * per_row;
-    int to[kFull ? 1 : 4];
-#pragma unroll
-    for (int i = 0; i < (kFull ? 1 : 4); i++) {
-        const int c = lane + 32 * i;
-        to[i] = (c / per_row) * C::kRowBytes + (c % per_row) * chunk;
-    }
-    const int sf_half = lane >> 4, sf_at = (lane & 7) * 16;
-    const uint32_t sf_to = sf_half * C::kHalfBytes + 2 * C::kCodes + (lane >> 3 & 1 ? C::kScales : 0) + sf_at;
-    const uint8_t* const sf_base = (lane >> 3 & 1 ? prm.v_sf : prm.k_sf) + sf_at;
     const float k_g = *a.k_g, v_g = *a.v_g;
-    const int key_row = (g >> 1) + 4 * (g & 1);            // key of a half that is row g of its S^T (and 8 + it)
-    const int page_mask = (1 << prm.page_shift) - 1;
-
     // chunks of this warp in a pass
     auto chunks_of = [&](const Pass& x) {
         const int n = x.valid && x.ke > x.kb ? (x.ke - x.kb + kChunk - 1) / kChunk : 0;
         return n > warp ? (n - warp + C::kWarps - 1) / C::kWarps : 0;
     };
-    // page ids of the halves of 16 chunks of this warp from chunk i on, a lane each
-    auto load_ids = [&](const Pass& x, int i, int n) {
-        const int c = i + (lane >> 1), k = x.kb + (warp + c * C::kWarps) * kChunk + (lane & 1) * kHalf;
-        return c < n && k < x.ke ? x.table[k >> prm.page_shift] : -1;
-    };
-    // Copies of chunk i of a pass into a stage.  A page that the cache does not
-    // have is zeros; a half past the pass's end is masked as a whole.
-    auto copy = [&](const Pass& x, int i, int ids, int stage) {
-        const int k0 = x.kb + (warp + i * C::kWarps) * kChunk;
-        const uint32_t st = ring_addr + stage * C::kStageBytes;
-        const int row0 = (x.hk << prm.page_shift) + (k0 & page_mask);      // (of the page; the second half's: 16 on, or 0)
-        const int row1 = (x.hk << prm.page_shift) + ((k0 + kHalf) & page_mask);
-        const uint32_t id0 = __shfl_sync(0xffffffffu, ids, 2 * (i & 15)), id1 = __shfl_sync(0xffffffffu, ids, 2 * (i & 15) + 1);
-        const bool real0 = id0 < (uint32_t)prm.pages, real1 = id1 < (uint32_t)prm.pages;
-        const uint32_t page0 = real0 ? id0 : 0u, page1 = real1 ? id1 : 0u;
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const uint64_t at = (uint64_t)(h ? page1 : page0) * prm.page_stride + (uint32_t)((h ? row1 : row0) * (D / 2));
-            const bool real = h ? real1 : real0;
-            const uint32_t sh = st + h * C::kHalfBytes + to[0];
-            const uint8_t* ck = prm.k + lane * chunk + at;
-            const uint8_t* cv = prm.v + lane * chunk + at;
-            if (kFull) {
-                const int n = real ? 16 : 0;
-                copy16<0>(sh, ck, n);
-                if (kDP == 128) copy16<512>(sh, ck, n);
-                copy16<0>(sh + C::kCodes, cv, n);
-                if (kDP == 128) copy16<512>(sh + C::kCodes, cv, n);
-            } else if (chunk == 16) {
-#pragma unroll
-                for (int y = 0; y < (kDP == 128 ? 2 : 1); y++)
-                    if (lane + 32 * y < chunks) {
-                        copy16<0>(sh + to[kFull ? 0 : y] - to[0], ck + 512 * y, real ? 16 : 0);
-                        copy16<0>(sh + C::kCodes + to[kFull ? 0 : y] - to[0], cv + 512 * y, real ? 16 : 0);
-                    }
-            } else {
-#pragma unroll
-                for (int y = 0; y < (kDP == 128 ? 4 : 2); y++)
-                    if (lane + 32 * y < chunks) {
-                        copy8(sh + to[kFull ? 0 : y] - to[0], ck + 256 * y, real ? 8 : 0);
-                        copy8(sh + C::kCodes + to[kFull ? 0 : y] - to[0], cv + 256 * y, real ? 8 : 0);
-                    }
-            }
-        }
-        if (sf_at < D)
-            copy16<0>(st + sf_to, sf_base + (uint64_t)(sf_half ? page1 : page0) * prm.sf_stride + (uint32_t)((sf_half ? row1 : row0) * nb),
-                      (sf_half ? real1 : real0) ? 16 : 0);
-        copies_end();
-    };
+    constexpr int kStride = C::kWarps * kChunk;            // a warp's chunks are this many keys apart
+    Ring<kDP, kNT, kFull> ring(prm, smem + warp * (C::kStages * C::kStageBytes), lane, D);
     // Q's rows of a pass, a share of each thread
     auto load_q = [&](const Pass& x, uint4* v) {
 #pragma unroll
@@ -321,11 +650,10 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
 
     // The ring runs through the passes: while a pass's last chunks are worked on
     // and joined, the first ones of the next are on their way.
-    int stage_in = 0, stage_out = 0, ahead = 0;            // next stage to fill, to read; stages filled
-    int issue_i = 0, issue_n, ids, ids_next;
+    int issue_i = 0, issue_n = chunks_of(s_pass[0]), ids, ids_next;
     bool in_next = false;                                  // what is issued is of the next pass
-    issue_n = chunks_of(s_pass[0]);
-    ids = load_ids(s_pass[0], 0, issue_n);
+    auto ids_of = [&](const Pass& x, int i) { return ring.load_ids(x.table, x.kb + (warp + i * C::kWarps) * kChunk, kStride, x.ke); };
+    ids = issue_n ? ids_of(s_pass[0], 0) : 0;
     {
         uint4 v[C::kQVecs];
         load_q(s_pass[0], v);
@@ -340,7 +668,7 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
         if (!cur.valid) break;
         const int mine = chunks_of(cur), next_n = chunks_of(nxt);
         if (in_next) in_next = false;                      // (issue_i, issue_n and ids are this pass's)
-        ids_next = load_ids(nxt, 0, next_n);
+        ids_next = next_n ? ids_of(nxt, 0) : 0;
         auto issue = [&]() {
             if (issue_i == issue_n && !in_next) {
                 in_next = true;
@@ -350,38 +678,25 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
             }
             if (issue_i == issue_n) return;
             const Pass& from = in_next ? nxt : cur;
-            if (issue_i && (issue_i & 15) == 0) ids = load_ids(from, issue_i, issue_n);
-            copy(from, issue_i++, ids, stage_in);
-            stage_in = stage_in + 1 == C::kStages ? 0 : stage_in + 1;
-            ahead++;
+            if (issue_i && (issue_i & 15) == 0) ids = ids_of(from, issue_i);
+            ring.copy(from.kb + (warp + issue_i * C::kWarps) * kChunk, from.hk, ids, issue_i & 15);
+            issue_i++;
         };
 #pragma unroll 1
-        for (int y = ahead; y < C::kStages; y++) issue();
+        for (int y = ring.ahead; y < C::kStages; y++) issue();
 
         // Q of the pass: row g of tile n, columns kDP / 4 * j .. of this lane
-        uint32_t q[kNT == 1 ? 2 * kSteps : 1];
-        float cf[kNT][2];
+        Rows<kDP, kNT> w;
+        uint32_t q[kNT == 1 ? kDP / 8 : 1];
 #pragma unroll
         for (int n = 0; n < kNT; n++) {
-            uint32_t raw[kDP / 8];                         // this lane's kDP / 4 columns
-            float amax = 0.0f;
+            uint32_t raw[kDP / 8];
 #pragma unroll
             for (int x = 0; x < kDP / 32; x++) {
                 const uint4 y = q_rows[(8 * n + g) * (kDP / 8) + j * (kDP / 32) + x];
                 raw[4 * x] = y.x, raw[4 * x + 1] = y.y, raw[4 * x + 2] = y.z, raw[4 * x + 3] = y.w;
             }
-#pragma unroll
-            for (int x = 0; x < kDP / 8; x++) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(raw[x])), fabsf(bf16_hi(raw[x]))));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // times 2^(141 - e), e the largest's biased exponent: it is then
-            // 2^14 .. 2^15; and back in the row's factor.  A negative scale's sign
-            // goes into Q; a zero scale is any tiny factor (no 0 * inf where masked).
-            const int e = max((int)(__float_as_uint(amax) >> 23), 15);
-            const float up = __uint_as_float((uint32_t)(268 - e) << 23 | (__float_as_uint(a.scale) & 0x80000000u));
-            const float down = __uint_as_float((uint32_t)(e - 14) << 23);
-#pragma unroll
-            for (int x = 0; x < kDP / 8; x++) raw[x] = cvt_f16x2(bf16_lo(raw[x]) * up, bf16_hi(raw[x]) * up);
+            make_q<kDP>(raw, a.scale, k_g, w.cf[n], j);
             if (kNT == 1) {
 #pragma unroll
                 for (int x = 0; x < kDP / 8; x++) q[kNT == 1 ? x : 0] = raw[x];
@@ -389,208 +704,25 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
 #pragma unroll
                 for (int s = 0; s < kSteps; s++) q_frag[(n * kSteps + s) * 32 + lane] = make_uint2(raw[2 * s], raw[2 * s + 1]);
             }
-            const float c = fmaxf(fabsf(a.scale) * kLog2e * k_g * down, 1.17549435e-38f);
-            cf[n][0] = __shfl_sync(0xffffffffu, c, 8 * j);
-            cf[n][1] = __shfl_sync(0xffffffffu, c, 8 * j + 4);
         }
         if (kNT > 1) __syncthreads();
-
-        // nm: kLift - m; top: the score from which m moves
-        float o[kNT][kSteps][4], m[kNT][2], nm[kNT][2], limit[kNT][2], l[kNT][2];
-#pragma unroll
-        for (int n = 0; n < kNT; n++) {
-#pragma unroll
-            for (int s = 0; s < kSteps; s++) o[n][s][0] = o[n][s][1] = o[n][s][2] = o[n][s][3] = 0.0f;
-#pragma unroll
-            for (int y = 0; y < 2; y++) m[n][y] = limit[n][y] = -INFINITY, nm[n][y] = l[n][y] = 0.0f;
-        }
+        w.clear();
+        const Seen seen = {cur.pos0, cur.r0, a.group, cur.lo, cur.ke, a.window};
         const int lo_all = cur.lo_all, hi_all = cur.hi_all;
         int kc = cur.kb + warp * kChunk;                   // first key of the chunk
 #pragma unroll 1
-        for (int i = 0; i < mine; i++, kc += C::kWarps * kChunk) {
-            if (C::kStages == 3 && ahead == 3) copies_wait<2>();
-            else if (ahead >= 2) copies_wait<1>();
-            else copies_wait<0>();
-            __syncwarp();
+        for (int i = 0; i < mine; i++, kc += kStride) {
+            const uint8_t* st = ring.wait();
+            auto frag = [&](int n, int x) {
+                return kNT == 1 ? make_uint2(q[kNT == 1 ? 2 * x : 0], q[kNT == 1 ? 2 * x + 1 : 0]) : q_frag[(n * kSteps + x) * 32 + lane];
+            };
 #pragma unroll 1
-            for (int h0 = 0; h0 < 2; h0 += kH) {
-                const uint8_t* st = ring + stage_out * C::kStageBytes + h0 * C::kHalfBytes;
-                const int k0 = kc + h0 * kHalf;
-                const bool edge = k0 < lo_all || k0 + kH * kHalf > hi_all;
-                // ---- S^T = K Q^T
-                float s[kH][kNT][4];
-#pragma unroll
-                for (int h = 0; h < kH; h++) {
-                    const uint8_t* sk = st + h * C::kHalfBytes;
-                    uint32_t w[2][kDP / 32];               // codes of keys key_row and 8 + key_row
-                    __half2 sc[2];                         // their scales (128 columns: of two blocks)
-#pragma unroll
-                    for (int y = 0; y < 2; y++) {
-                        const int key = key_row + 8 * y;
-                        const uint8_t* sf = sk + 2 * C::kCodes + key * nb;
-                        if (kDP == 128) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(sk + key * C::kRowBytes + j * 16);
-                            w[y][0] = x.x, w[y][1] = x.y, w[y][kDP / 32 - 2] = x.z, w[y][kDP / 32 - 1] = x.w;
-                            uint32_t b;
-                            if (kFull) {
-                                b = *reinterpret_cast<const uint16_t*>(sf + 2 * j);
-                            } else {
-                                b = 2 * j < nb ? sf[2 * j] : 0u;
-                                b |= 2 * j + 1 < nb ? (uint32_t)sf[2 * j + 1] << 8 : 0u;
-                            }
-                            sc[y] = as_half2(e4m3x2_to_f16x2(b));
-                        } else {
-                            const uint2 x = *reinterpret_cast<const uint2*>(sk + key * C::kRowBytes + j * 8);
-                            w[y][0] = x.x, w[y][1] = x.y;
-                            sc[y] = as_half2(e4m3x2_to_f16x2(j < nb ? sf[j] : 0u));
-                        }
-                    }
-#pragma unroll
-                    for (int n = 0; n < kNT; n++) s[h][n][0] = s[h][n][1] = s[h][n][2] = s[h][n][3] = 0.0f;
-#pragma unroll
-                    for (int x = 0; x < kDP / 32; x++) {   // a word of codes: two MMAs
-                        uint32_t f[2][4];
-#pragma unroll
-                        for (int y = 0; y < 2; y++) {
-                            e2m1x8_to_f16x2(w[y][x], f[y]);
-                            const __half2 z = kDP == 128 && x >= 2 ? __high2half2(sc[y]) : __low2half2(sc[y]);
-#pragma unroll
-                            for (int u = 0; u < 4; u++) f[y][u] = as_u32(__hmul2(as_half2(f[y][u]), z));
-                        }
-#pragma unroll
-                        for (int u = 0; u < 2; u++) {
-                            const uint32_t fa[4] = {f[0][2 * u], f[1][2 * u], f[0][2 * u + 1], f[1][2 * u + 1]};
-#pragma unroll
-                            for (int n = 0; n < kNT; n++) {
-                                if (kNT == 1) {
-                                    mma16816(s[h][n], fa, q[kNT == 1 ? 4 * x + 2 * u : 0], q[kNT == 1 ? 4 * x + 2 * u + 1 : 0]);
-                                } else {
-                                    const uint2 b = q_frag[(n * kSteps + 2 * x + u) * 32 + lane];
-                                    mma16816(s[h][n], fa, b.x, b.y);
-                                }
-                            }
-                        }
-                    }
-                }
-                // ---- softmax
-                if (edge) {
-#pragma unroll
-                    for (int h = 0; h < kH; h++) {
-#pragma unroll
-                        for (int n = 0; n < kNT; n++) {
-#pragma unroll
-                            for (int y = 0; y < 4; y++) {
-                                const int pos = cur.pos0 + (cur.r0 + 8 * n + 2 * j + (y & 1)) / a.group;
-                                const int key = k0 + h * kHalf + key_row + 8 * (y >> 1);
-                                const bool seen = key <= pos && key < cur.key_end && (!a.window || key > pos - a.window);
-                                if (!seen) s[h][n][y] = -INFINITY;
-                            }
-                        }
-                    }
-                }
-                bool up = false;
-#pragma unroll
-                for (int n = 0; n < kNT; n++) {
-#pragma unroll
-                    for (int y = 0; y < 2; y++) {
-                        float top = fmaxf(s[0][n][y], s[0][n][y + 2]);
-                        if (kH == 2) top = fmaxf(top, fmaxf(s[kH - 1][n][y], s[kH - 1][n][y + 2]));
-                        up |= top > limit[n][y];
-                    }
-                }
-                if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-                    for (int n = 0; n < kNT; n++) {
-#pragma unroll
-                        for (int y = 0; y < 2; y++) {
-                            float top = fmaxf(s[0][n][y], s[0][n][y + 2]);
-                            if (kH == 2) top = fmaxf(top, fmaxf(s[kH - 1][n][y], s[kH - 1][n][y + 2]));
-#pragma unroll
-                            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                            top = fmaxf(top * cf[n][y], m[n][y]);
-                            const float f = m[n][y] == -INFINITY ? 0.0f : ex2(m[n][y] - top);
-                            m[n][y] = top;
-                            nm[n][y] = top == -INFINITY ? 0.0f : kLift - top;
-                            limit[n][y] = (top + kLazy) / cf[n][y];
-                            l[n][y] *= f;
-#pragma unroll
-                            for (int x = 0; x < kSteps; x++) {
-                                o[n][x][y] *= f;
-                                o[n][x][y + 2] *= f;
-                            }
-                        }
-                    }
-                }
-                uint32_t pt[kH][kNT][2];
-#pragma unroll
-                for (int h = 0; h < kH; h++) {
-#pragma unroll
-                    for (int n = 0; n < kNT; n++) {
-                        float e[4];
-#pragma unroll
-                        for (int y = 0; y < 4; y++) {
-                            e[y] = ex2(fmaf(s[h][n][y], cf[n][y & 1], nm[n][y & 1]));
-                            l[n][y & 1] += e[y];
-                        }
-                        pt[h][n][0] = transpose8x8(cvt_f16x2(e[0], e[1]));
-                        pt[h][n][1] = transpose8x8(cvt_f16x2(e[2], e[3]));
-                    }
-                }
-                // ---- O^T += V^T P^T: keys j, j + 4 and j + 8, j + 12 of a half, columns kDP / 8 * g ..
-                constexpr int kVW = kDP / 64;              // words of a key's codes
-#pragma unroll
-                for (int h = 0; h < kH; h++) {
-                    const uint8_t* sv = st + h * C::kHalfBytes + C::kCodes;
-                    const uint8_t* sf = sv + C::kCodes + C::kScales;
-                    uint32_t v[4][kVW];
-                    __half2 vs[2];
-                    const int blk = kDP == 128 ? g : g >> 1;
-                    uint32_t b[4];
-#pragma unroll
-                    for (int u = 0; u < 4; u++) {
-                        const int key = j + 4 * u;
-                        if (kVW == 2) {
-                            const uint2 x = *reinterpret_cast<const uint2*>(sv + key * C::kRowBytes + g * 8);
-                            v[u][0] = x.x, v[u][kVW - 1] = x.y;
-                        } else {
-                            v[u][0] = *reinterpret_cast<const uint32_t*>(sv + key * C::kRowBytes + g * 4);
-                        }
-                        b[u] = kFull || blk < nb ? sf[key * nb + blk] : 0u;
-                    }
-                    if (edge) {                            // a value that no row sees may be anything
-                        const int lo = cur.lo - k0 - h * kHalf, ke = cur.ke - k0 - h * kHalf;
-#pragma unroll
-                        for (int u = 0; u < 4; u++)
-                            if (j + 4 * u < lo || j + 4 * u >= ke) b[u] = 0u;
-                    }
-                    vs[0] = as_half2(e4m3x2_to_f16x2(__byte_perm(b[0], b[1], 0x3340)));
-                    vs[1] = as_half2(e4m3x2_to_f16x2(__byte_perm(b[2], b[3], 0x3340)));
-#pragma unroll
-                    for (int y = 0; y < kVW; y++) {
-                        uint32_t even[2][4], odd[2][4];    // two keys side by side, of even and odd columns
-#pragma unroll
-                        for (int u = 0; u < 2; u++) {
-                            const uint32_t x0 = v[2 * u][y], x1 = v[2 * u + 1][y];
-                            e2m1x8_to_f16x2((x0 & 0x0f0f0f0fu) | (x1 << 4 & 0xf0f0f0f0u), even[u]);
-                            e2m1x8_to_f16x2((x0 >> 4 & 0x0f0f0f0fu) | (x1 & 0xf0f0f0f0u), odd[u]);
-                        }
-#pragma unroll
-                        for (int x = 0; x < 4; x++) {
-                            uint32_t f[4];
-#pragma unroll
-                            for (int u = 0; u < 2; u++) {
-                                f[2 * u] = as_u32(__hmul2(as_half2(even[u][x]), vs[u]));
-                                f[2 * u + 1] = as_u32(__hmul2(as_half2(odd[u][x]), vs[u]));
-                            }
-#pragma unroll
-                            for (int n = 0; n < kNT; n++) mma16816(o[n][4 * y + x], f, pt[h][n][0], pt[h][n][1]);
-                        }
-                    }
-                }
+            for (int h = 0; h < 2; h += C::kAtOnce) {
+                const int k = kc + h * kHalf;
+                const bool edge = k < lo_all || k + C::kAtOnce * kHalf > hi_all;
+                work_halves<kDP, kNT, kFull, C::kAtOnce>(st + h * C::kHalfBytes, k, edge, seen, nb, w, frag, g, j);
             }
-            __syncwarp();                                  // the stage has been read
-            stage_out = stage_out + 1 == C::kStages ? 0 : stage_out + 1;
-            ahead--;
+            ring.release();
             issue();
         }
 
@@ -601,13 +733,13 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
         uint4 q_next[C::kQVecs];
         load_q(nxt, q_next);
         if (warp == 0) passes.next(a, &s_pass[x_pass == 0 ? 2 : x_pass - 1], lane);
+        w.join_sums();
+        if (g == 0) {
 #pragma unroll
-        for (int n = 0; n < kNT; n++) {
+            for (int n = 0; n < kNT; n++) {
 #pragma unroll
-            for (int y = 0; y < 2; y++) {
-#pragma unroll
-                for (int x = 4; x < 32; x <<= 1) l[n][y] += __shfl_xor_sync(0xffffffffu, l[n][y], x);
-                if (g == 0) m_all[warp * C::kRows + 8 * n + 2 * j + y] = make_float2(m[n][y], l[n][y]);
+                for (int y = 0; y < 2; y++)
+                    m_all[warp * C::kRows + 8 * n + 2 * j + y] = make_float2(w.m[n][y], w.l[n][y]);
             }
         }
 #pragma unroll
@@ -621,7 +753,7 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
                                                             g * (kDP / 8));
 #pragma unroll
                     for (int x = 0; x < kSteps; x += 2)
-                        to4[x / 2] = make_float4(o[n][x][y], o[n][x][y + 2], o[n][x + 1][y], o[n][x + 1][y + 2]);
+                        to4[x / 2] = make_float4(w.o[n][x][y], w.o[n][x][y + 2], w.o[n][x + 1][y], w.o[n][x + 1][y + 2]);
                 }
             }
             __syncthreads();
@@ -652,8 +784,7 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
                     *reinterpret_cast<uint32_t*>(a.out + (int64_t)(tok0 + t) * a.ldo + (int64_t)head * a.ho + col) =
                         sum == 0.0f ? 0u : cvt_bf16x2(acc.x * inv, acc.y * inv);
                     if (col == 0 && a.lse)
-                        a.lse[(int64_t)(tok0 + t) * a.heads + head] =
-                            sum == 0.0f ? -INFINITY : (top - kLift + log2f(sum)) * 0.6931471805599453f;
+                        a.lse[(int64_t)(tok0 + t) * a.heads + head] = log_sum(top, sum);
                 } else {
                     __stcg(reinterpret_cast<float2*>(part + r * kDP + col), acc);
                     if (col == 0) __stcg(reinterpret_cast<float2*>(part + kAttnSlotRows * kDP + 2 * r), make_float2(top, sum));
@@ -676,53 +807,334 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
         const bool mine_to_join = s_last;
         __syncthreads();
         if (!mine_to_join) continue;
-        // part i of the item is in slot 2 (cta0 + i), the first in 2 cta0 + 1
-        auto slot_of = [&](int i) { return a.partials + (2 * (cta0 + i) + (i == 0 ? 1 : 0)) * kAttnSlotFloats; };
-        for (int x = tid; x < rows * (kDP / 2); x += C::kThreads) {
-            const int r = x / (kDP / 2), col = 2 * (x % (kDP / 2));
-            if (col >= D) continue;
-            const int t = r / a.group, head = hk * a.group + r - t * a.group;
-            float top = -INFINITY, sum = 0.0f;
-            float2 acc = make_float2(0.0f, 0.0f);
-#pragma unroll 1
-            for (int i0 = 0; i0 < parts; i0 += 8) {
-                float2 ml[8], e[8];
+        join_parts<kDP, C::kThreads>(a, cta0, parts, rows, tok0, hk, v_g);
+    }
+}
+
+// ------------------------------------------------------- shares of warps
+// The part of an item that a warp works on, in its shared memory (this and the
+// next one).
+struct Work {
+    int valid;
+    int tok0, rows, pos0, hk;
+    int s, item;             // the item's first unit, its units
+    int a, b, chunks;        // chunks a .. b - 1 of the item's are this CTA's
+    int x0, x1;              // x0 .. x1 - 1 are this warp's
+    int lo, lo_all, hi_all;  // as Pass's
+    int kb, ke, n;           // keys of its chunks that rows see, chunks
+    const int32_t* table;
+};
+
+// A warp's walk over the items of its CTA's share of the schedule's second axis.
+struct Walk {
+    QTile t;
+    int qt, hk, s;           // the next item: its QTile's number, kv head, first unit
+};
+
+// An item that this CTA shares with others: [0] with the CTAs before it, [1] one
+// that begins here.
+struct Share {
+    int valid, cta0, parts, rows, tok0, hk, last;
+};
+
+template <int kDP, int kNT, bool kFull>
+__device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, int cta)
+{
+    using C = Cfg4<kDP, kNT>;
+    constexpr int kSteps = kDP / 16;
+    __shared__ Work s_work[C::kWarps][2];
+    __shared__ Walk s_walk[C::kWarps];
+    __shared__ Share s_share[2];
+    const AttnArgs& a = prm.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
+    const int D = kFull ? kDP : a.head_dim, Hkv = a.kv_heads, nb = D / 16;
+    float* const deposits = reinterpret_cast<float*>(smem + C::kOffO);     // [warp][tile, vector][lane][4]
+    float2* const deposit_ml = reinterpret_cast<float2*>(smem + C::kOffM); // [warp][row]
+    const ScheduleHead* head = a.sched;
+    const QTile* tiles = schedule_tiles(head);
+
+    // the CTA's units u0 .. u1 - 1, this warp's v0 .. v1 - 1
+    const int per = head->per_cta4, units = head->units4, n_tiles = head->qtiles, begin = head->first4[cta];
+    const QTile start = head->start4[cta];
+    const int u0 = min(cta * per, units), u1 = min(u0 + per, units), len = u1 - u0;
+    auto bound = [&](int w) { return u0 + len * w / C::kWarps; };
+    const int v0 = bound(warp), v1 = bound(warp + 1);
+    const bool final_warp = warp == C::kWarps - 1;
+    const float k_g = *a.k_g, v_g = *a.v_g;
+    if (tid < 2) s_share[tid].valid = 0;
+
+    Walk& walk = s_walk[warp];
+    const bool any = len > 0;
+    if (any) {
+        int qt = begin, s = (int)units4_before(start.unit0, Hkv, begin);
+        QTile t = start;
+        if (v0 >= s + (kItemUnits4 + kChunksOfTile * t.tiles) * Hkv) {
+            // a later QTile of the CTA's: the last that begins at or below v0
+            for (int base = begin + 1;; base += 32) {
+                const int i = base + lane;
+                const int64_t at = i < n_tiles ? units4_before(tiles[i].unit0, Hkv, i) : 0x7fffffff;
+                const int k = __popc(__ballot_sync(0xffffffffu, at <= v0));
+                qt = base + k - 1;
+                if (k < 32) break;
+            }
+            t = tiles[qt];
+            s = (int)units4_before(t.unit0, Hkv, qt);
+        }
+        const int item = kItemUnits4 + kChunksOfTile * t.tiles, hk = (v0 - s) / item;
+        if (lane == 0) walk = Walk{t, qt, hk, s + hk * item};
+        __syncwarp();
+    }
+    // The warp's next part into *out.
+    auto next = [&](Work* out) {
+        Work x;
+        x.valid = 0;
+        const int end = final_warp ? u1 : v1;
+        QTile t = walk.t;
+        int qt = walk.qt, hk = walk.hk, s = walk.s;
+        while (any && s < end) {
+            const int chunks = kChunksOfTile * t.tiles, item = kItemUnits4 + chunks;
+            x.a = u0 <= s ? 0 : max(snap_unit4(u0 - s, item) - kItemUnits4, 0);
+            x.b = max(snap_unit4(min(u1 - s, item), item) - kItemUnits4, 0);
+            x.x0 = warp == 0 ? x.a : min(max(v0 - s - kItemUnits4, x.a), x.b);
+            x.x1 = final_warp ? x.b : min(max(v1 - s - kItemUnits4, x.a), x.b);
+            if (x.x1 > x.x0) {
+                x.valid = 1;
+                x.tok0 = t.tok0;
+                x.rows = t.n_tok * a.group;
+                x.pos0 = t.pos0;
+                x.hk = hk;
+                x.s = s;
+                x.item = item;
+                x.chunks = chunks;
+                x.lo = a.window ? max(t.pos0 + 1 - a.window, 0) : 0;
+                x.lo_all = a.window ? max(t.pos0 + t.n_tok - a.window, 0) : 0;
+                const int key0 = t.tile0 * kAttnKeys;
+                x.kb = max(key0 + x.x0 * kChunk, x.lo & ~(kChunk - 1));
+                x.ke = min(key0 + x.x1 * kChunk, t.kv_end);
+                x.hi_all = min(t.pos0 + 1, x.ke);
+                x.n = x.ke > x.kb ? (x.ke - x.kb + kChunk - 1) / kChunk : 0;
+                x.table = a.block_table + t.req * a.table_ld;
+            }
+            s += item;
+            if (++hk == Hkv) {
+                hk = 0;
+                qt++;
+                if (s < end) t = tiles[qt];
+            }
+            if (x.valid) break;
+        }
+        __syncwarp();                                      // (every lane has read what this replaces)
+        if (lane == 0) {
+            *out = x;
+            walk = Walk{t, qt, hk, s};
+        }
+        __syncwarp();
+    };
+
+    Ring<kDP, kNT, kFull> ring(prm, smem + warp * (C::kStages * C::kStageBytes), lane, D);
+    Rows<kDP, kNT> w;
+    next(&s_work[warp][0]);
+    int issue_k, issue_ke, issue_i = 0, ids;               // the next chunk to copy: of this part or (in_next) the next
+    bool in_next = false;
+    {
+        const Work& x = s_work[warp][0];
+        issue_k = x.valid ? x.kb : 0;
+        issue_ke = x.valid ? x.ke : 0;
+        ids = issue_k < issue_ke ? ring.load_ids(x.table, issue_k, kChunk, issue_ke) : 0;
+    }
+    int at = 0;
+    bool pending = false;
+    // The rows of *this warp* are the CTA's part of the item: out, or to the CTA's slot.
+    auto finish = [&](const Work& x) {
+        const bool whole = x.a == 0 && x.b == x.chunks;
+        float* part = a.partials + (2 * cta + (x.a == 0 ? 1 : 0)) * kAttnSlotFloats;
 #pragma unroll
-                for (int u = 0; u < 8; u++) {
-                    const float* from = slot_of(min(i0 + u, parts - 1));
-                    ml[u] = __ldcg(reinterpret_cast<const float2*>(from + kAttnSlotRows * kDP + 2 * r));
-                    e[u] = __ldcg(reinterpret_cast<const float2*>(from + r * kDP + col));
-                    if (i0 + u >= parts) ml[u] = make_float2(-INFINITY, 0.0f);
-                }
-                float most = top;
+        for (int n = 0; n < kNT; n++) {
 #pragma unroll
-                for (int u = 0; u < 8; u++) most = fmaxf(most, ml[u].x);
-                const float f0 = top == -INFINITY ? 0.0f : ex2(top - most);
-                acc.x *= f0;
-                acc.y *= f0;
-                sum *= f0;
-                top = most;
+            for (int y = 0; y < 2; y++) {
+                const int r = 8 * n + 2 * j + y, col = g * (kDP / 8);
+                if (r >= x.rows) continue;
+                if (whole) {
+                    const int t = r / a.group, hd = x.hk * a.group + r - t * a.group;
+                    const bool none = w.l[n][y] == 0.0f;
+                    const float inv = none ? 0.0f : v_g / w.l[n][y];
+                    uint32_t v[kSteps];
 #pragma unroll
-                for (int u = 0; u < 8; u++) {
-                    if (ml[u].y == 0.0f) continue;         // no key of this part
-                    const float f = ml[u].x == -INFINITY ? 0.0f : ex2(ml[u].x - top);
-                    acc.x += f * e[u].x;
-                    acc.y += f * e[u].y;
-                    sum += f * ml[u].y;
+                    for (int i = 0; i < kSteps; i++) v[i] = none ? 0u : cvt_bf16x2(w.o[n][i][y] * inv, w.o[n][i][y + 2] * inv);
+                    uint4* out = reinterpret_cast<uint4*>(a.out + (int64_t)(x.tok0 + t) * a.ldo + (int64_t)hd * a.ho + col);
+#pragma unroll
+                    for (int i = 0; i < kSteps / 4; i++)
+                        if (kFull || col + 8 * i < D) out[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    if (g == 0 && a.lse) a.lse[(int64_t)(x.tok0 + t) * a.heads + hd] = log_sum(w.m[n][y], w.l[n][y]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kSteps; i += 2)
+                        __stcg(reinterpret_cast<float4*>(part + r * kDP + col) + i / 2,
+                               make_float4(w.o[n][i][y], w.o[n][i][y + 2], w.o[n][i + 1][y], w.o[n][i + 1][y + 2]));
+                    if (g == 0)
+                        __stcg(reinterpret_cast<float2*>(part + kAttnSlotRows * kDP + 2 * r), make_float2(w.m[n][y], w.l[n][y]));
                 }
             }
-            const float inv = sum == 0.0f ? 0.0f : v_g / sum;
-            *reinterpret_cast<uint32_t*>(a.out + (int64_t)(tok0 + t) * a.ldo + (int64_t)head * a.ho + col) =
-                sum == 0.0f ? 0u : cvt_bf16x2(acc.x * inv, acc.y * inv);
-            if (col == 0 && a.lse)
-                a.lse[(int64_t)(tok0 + t) * a.heads + head] =
-                    sum == 0.0f ? -INFINITY : (top - kLift + log2f(sum)) * 0.6931471805599453f;
+        }
+        if (!whole && lane == 0) {
+            int c0 = x.s / per, c1 = (x.s + x.item - 1) / per;
+            if (snap_unit4((c0 + 1) * per - x.s, x.item) == 0) c0++;
+            if (c1 > c0 && snap_unit4(c1 * per - x.s, x.item) == x.item) c1--;
+            s_share[x.a == 0 ? 1 : 0] = Share{1, c0, c1 - c0 + 1, x.rows, x.tok0, x.hk, 0};
+        }
+    };
+    if (s_work[warp][0].valid) {
+#pragma unroll 1
+        for (;; at ^= 1) {
+            const Work& cur = s_work[warp][at];
+            const Work& nxt = s_work[warp][at ^ 1];
+            // Q of the item: row g of tile n, columns kDP / 4 * j .. of this lane
+            uint32_t q[kNT][kDP / 8];
+#pragma unroll
+            for (int n = 0; n < kNT; n++) {
+                const int r = 8 * n + g, t = r / a.group;
+                const __nv_bfloat16* src = prm.q + (int64_t)(cur.tok0 + t) * prm.ldq +
+                                           (int64_t)(cur.hk * a.group + r - t * a.group) * prm.hq + j * (kDP / 4);
+#pragma unroll
+                for (int x = 0; x < kDP / 32; x++) {
+                    uint4 y = make_uint4(0, 0, 0, 0);
+                    if (r < cur.rows && (kFull || j * (kDP / 4) + 8 * x < D)) y = *reinterpret_cast<const uint4*>(src + 8 * x);
+                    q[n][4 * x] = y.x, q[n][4 * x + 1] = y.y, q[n][4 * x + 2] = y.z, q[n][4 * x + 3] = y.w;
+                }
+            }
+            next(&s_work[warp][at ^ 1]);
+            const int next_ids = nxt.valid && nxt.n ? ring.load_ids(nxt.table, nxt.kb, kChunk, nxt.ke) : 0;
+            in_next = false;                               // (what has been issued of the next part is now this one's)
+            auto issue = [&]() {
+                if (issue_k >= issue_ke && !in_next && nxt.valid) {
+                    in_next = true;
+                    issue_k = nxt.kb;
+                    issue_ke = nxt.ke;
+                    issue_i = 0;
+                    ids = next_ids;
+                }
+                if (issue_k >= issue_ke) return;
+                const Work& from = in_next ? nxt : cur;
+                if (issue_i == 16) {
+                    issue_i = 0;
+                    ids = ring.load_ids(from.table, issue_k, kChunk, issue_ke);
+                }
+                ring.copy(issue_k, from.hk, ids, issue_i++);
+                issue_k += kChunk;
+            };
+#pragma unroll 1
+            for (int y = ring.ahead; y < C::kStages; y++) issue();
+#pragma unroll
+            for (int n = 0; n < kNT; n++) make_q<kDP>(q[n], a.scale, k_g, w.cf[n], j);
+            w.clear();
+            const Seen seen = {cur.pos0, 0, a.group, cur.lo, cur.ke, a.window};
+            const int lo_all = cur.lo_all, hi_all = cur.hi_all;
+            int k0 = cur.kb;
+#pragma unroll 1
+            for (int i = cur.n; i > 0; i--, k0 += kChunk) {
+                const uint8_t* st = ring.wait();
+                auto frag = [&](int n, int x) { return make_uint2(q[n][2 * x], q[n][2 * x + 1]); };
+#pragma unroll
+                for (int h = 0; h < 2; h += C::kAtOnce) {
+                    const int k = k0 + h * kHalf;
+                    const bool edge = k < lo_all || k + C::kAtOnce * kHalf > hi_all;
+                    work_halves<kDP, kNT, kFull, C::kAtOnce>(st + h * C::kHalfBytes, k, edge, seen, nb, w, frag, g, j);
+                }
+                ring.release();
+                issue();
+            }
+            w.join_sums();
+            if (cur.x0 > cur.a) {                          // the part began in an earlier warp, which will add this
+                float4* to4 = reinterpret_cast<float4*>(deposits + warp * C::kWarpO) + lane;
+#pragma unroll
+                for (int n = 0; n < kNT; n++) {
+#pragma unroll
+                    for (int i = 0; i < kSteps; i++)
+                        to4[32 * (n * kSteps + i)] = make_float4(w.o[n][i][0], w.o[n][i][1], w.o[n][i][2], w.o[n][i][3]);
+#pragma unroll
+                    for (int y = 0; y < 2; y++)
+                        if (g == 0) deposit_ml[warp * C::kRows + 8 * n + 2 * j + y] = make_float2(w.m[n][y], w.l[n][y]);
+                }
+            } else if (cur.x1 == cur.b) {
+                finish(cur);
+            } else {
+                pending = true;                            // goes on in the warps behind
+                break;
+            }
+            if (!nxt.valid) break;
         }
     }
+    __syncthreads();
+    if (pending) {
+        const Work& x = s_work[warp][at];
+        int reached = x.x1;
+#pragma unroll 1
+        for (int o = warp + 1; reached < x.b; o++) {
+            const int to = o == C::kWarps - 1 ? x.b : min(max(bound(o + 1) - x.s - kItemUnits4, x.a), x.b);
+            if (to == reached) continue;
+            reached = to;
+            const float4* from = reinterpret_cast<const float4*>(deposits + o * C::kWarpO) + lane;
+#pragma unroll
+            for (int n = 0; n < kNT; n++) {
+                float f0[2], f1[2];
+#pragma unroll
+                for (int y = 0; y < 2; y++) {
+                    const float2 ml = deposit_ml[o * C::kRows + 8 * n + 2 * j + y];
+                    const float top = fmaxf(w.m[n][y], ml.x), ref = top == -INFINITY ? 0.0f : top;
+                    f0[y] = ex2(w.m[n][y] - ref);
+                    f1[y] = ex2(ml.x - ref);
+                    w.m[n][y] = top;
+                    w.l[n][y] = w.l[n][y] * f0[y] + ml.y * f1[y];
+                }
+#pragma unroll
+                for (int i = 0; i < kSteps; i++) {
+                    const float4 e = from[32 * (n * kSteps + i)];
+                    w.o[n][i][0] = w.o[n][i][0] * f0[0] + e.x * f1[0];
+                    w.o[n][i][1] = w.o[n][i][1] * f0[1] + e.y * f1[1];
+                    w.o[n][i][2] = w.o[n][i][2] * f0[0] + e.z * f1[0];
+                    w.o[n][i][3] = w.o[n][i][3] * f0[1] + e.w * f1[1];
+                }
+            }
+        }
+        finish(x);
+    }
+    __syncthreads();
+    if (!s_share[0].valid && !s_share[1].valid) return;
+    if (tid < 2 && s_share[tid].valid) {
+        Share& x = s_share[tid];
+        int* ticket = a.tickets + x.cta0 * 8;
+        x.last = atom_add_acq_rel(ticket, 1) == x.parts - 1;
+        if (x.last) *ticket = 0;
+    }
+    __syncthreads();
+    for (int i = 0; i < 2; i++) {
+        const Share& x = s_share[i];
+        if (x.valid && x.last) join_parts<kDP, C::kThreads>(a, x.cta0, x.parts, x.rows, x.tok0, x.hk, v_g);
+    }
+}
+
+template <int kDP, int kNT, bool kFull>
+__global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(const __grid_constant__ Params4 prm)
+{
+    using C = Cfg4<kDP, kNT>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const AttnArgs& a = prm.a;
+    const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    griddep_launch_dependents();
+    if (!kFull)                                 // the columns that no copy writes are zeros
+        for (int i = threadIdx.x; i < C::kRing / 16; i += C::kThreads)
+            reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    griddep_wait();
+    __syncthreads();
+    if (C::kOwnShares && a.sched->per_cta4 > 0 && a.sched->most_tokens * a.group <= C::kRows)
+        own_shares<kDP, kNT, kFull>(prm, smem, cta);
+    else
+        passes_together<kDP, kNT, kFull>(prm, smem, cta);
     copies_wait<0>();
     if (a.cu_end) {
         // the rows past the step's last token, a warp to a row
-        const int vecs = D / 8, n = a.heads * vecs;
+        const int vecs = a.head_dim / 8, n = a.heads * vecs;
         for (int64_t t = max(*a.cu_end, 0) + cta + (int)gridDim.x * warp; t < a.tokens; t += gridDim.x * C::kWarps) {
             for (int x = lane; x < n; x += 32) {
                 const int h = x / vecs;

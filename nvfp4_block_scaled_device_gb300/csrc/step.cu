@@ -100,7 +100,7 @@ __device__ __forceinline__ int last_at_or_below(const int32_t* x, int n, int64_t
 // before each request, ctx: cached tokens, tile0: room for R + 1 int32 (all
 // shared memory).
 __device__ void build_schedule(const PlanParams& p, const int32_t* cu, const int32_t* ctx, int32_t* tile0,
-                               int64_t (*warp_sums)[2], int* longest, int block, int blocks)
+                               int64_t (*warp_sums)[2], int* longest, int* most_tokens, int block, int blocks)
 {
     const nvfp4_step_t& s = p.s;
     const int R = (int)s.requests, t = threadIdx.x;
@@ -120,6 +120,7 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, const int
     if (t == 0) {
         tile0[R] = (int32_t)total;
         *longest = 1;
+        *most_tokens = 0;
     }
     __syncthreads();
     const int n = (int)total, each = ((n + kPlanThreads - 1) / kPlanThreads) | 1;
@@ -144,13 +145,16 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, const int
         return q;
     };
     int64_t unit = 0, units = 0;
-    int most = 1;
+    int most = 1, tokens = 0;
     for (int i = i0, r = r0; i < i1; i++) {
-        const int item = kItemUnits + tile_of(i, r).tiles;
+        const QTile q = tile_of(i, r);
+        const int item = kItemUnits + q.tiles;
         unit += (int64_t)item * Hkv;
         most = max(most, item);
+        tokens = max(tokens, q.n_tok);
     }
     atomicMax(longest, __reduce_max_sync(0xffffffffu, most));
+    atomicMax(most_tokens, __reduce_max_sync(0xffffffffu, tokens));
     block_prefix(unit, unused, warp_sums, &units, &unused_total);   // (its barriers order *longest too)
     if (units > kMaxUnits) {
         // ends with a whole item (one cut off would never collect its tickets)
@@ -166,13 +170,23 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, const int
     }
     const int share = (int)((units + p.ctas - 1) / p.ctas);
     const int per_cta = max(share, min(kItemUnits + kMinPart, *longest));
+    // the second axis (at least a chunk for each warp of a CTA, where items have
+    // as many)
+    const int64_t units4 = units4_before(units, Hkv, n);
+    const bool has4 = units < kMaxUnits / 8;
+    const int longest4 = has4 ? kChunksOfTile * (*longest - kItemUnits) + kItemUnits4 : 1;
+    const int per_cta4 = has4 ? max(max((int)((units4 + p.ctas - 1) / p.ctas), min(kItemUnits4 + 16, longest4)), 1) : 0;
     if (t == 0 && block == 0) {
         head->units = (int32_t)units;
         head->per_cta = per_cta;
         head->qtiles = n;
+        head->units4 = has4 ? (int32_t)units4 : 0;
+        head->per_cta4 = per_cta4;
+        head->most_tokens = *most_tokens;
     }
     if (t * blocks / kPlanThreads != block) return;
     int c = (int)((min(unit, units) + per_cta - 1) / per_cta);       // the next CTA to start
+    int c4 = has4 ? (int)((units4_before(unit, Hkv, i0) + per_cta4 - 1) / per_cta4) : 0;
     for (int i = i0, r = r0; i < i1; i++) {
         QTile q = tile_of(i, r);
         q.unit0 = (int)min(unit, units);
@@ -181,6 +195,11 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, const int
         for (const int next = (int)min(unit, units); c * per_cta < next; c++) {
             head->first[c] = i;
             head->start[c] = q;
+        }
+        if (!has4) continue;
+        for (const int next = (int)units4_before(unit, Hkv, i + 1); c4 * per_cta4 < next; c4++) {
+            head->first4[c4] = i;
+            head->start4[c4] = q;
         }
     }
 }
@@ -192,7 +211,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
 {
     extern __shared__ int32_t sh[];
     __shared__ int64_t s_sums[kPlanWarps][2];
-    __shared__ int s_longest;
+    __shared__ int s_longest, s_most_tokens;
     griddep_launch_dependents();
     // (The lengths may come from the previous kernel, and what it writes while
     // this one is already there is no constant: plain loads, not __ldg, here
@@ -244,7 +263,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
     __syncthreads();
     const int blocks = gridDim.x - p.schedulers;
     if ((int)blockIdx.x >= blocks) {
-        build_schedule(p, cu, ctx, first, s_sums, &s_longest, blockIdx.x - blocks, p.schedulers);
+        build_schedule(p, cu, ctx, first, s_sums, &s_longest, &s_most_tokens, blockIdx.x - blocks, p.schedulers);
         return;
     }
     const int32_t T = cu[R];
