@@ -131,14 +131,15 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t b)
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"((uint16_t)b));
     return y;
 }
-// 16 (8) bytes of global memory into shared memory, kAt bytes on from both
+// 16 (8) bytes of global memory into shared memory, kDst and kSrc on from the
 // addresses; `real` 0: zeros instead.
-template <int kAt>
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t real)
+template <int kDst = 0, int kSrc = 0>
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, uint32_t real)
 {
-    asm volatile("cp.async.cg.shared.global [%0 + %3], [%1 + %3], 16, %2;" ::"r"(dst), "l"(src), "r"(real), "n"(kAt) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0 + %3], [%1 + %4], 16, %2;" ::"r"(dst), "l"(src), "r"(real), "n"(kDst), "n"(kSrc)
+                 : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src, uint32_t real)
+__device__ __forceinline__ void copy8(uint32_t dst, const uint8_t* src, uint32_t real)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
 }
@@ -218,11 +219,12 @@ struct Seen {
     int lo, ke, window;          // some row sees keys lo .. ke - 1, none one past
 };
 
-// kH halves of a chunk at `st`, keys k0 ..: scores, softmax, products.  edge:
-// some row does not see all of them.  q(n, x): fragment x of tile n's Q.
-template <int kDP, int kNT, bool kFull, int kH, typename Q>
-__device__ __forceinline__ void work_halves(const uint8_t* st, int k0, bool edge, const Seen& seen, int nb,
-                                            Rows<kDP, kNT>& w, Q&& q, int g, int j)
+// kH halves of a chunk at `st`, keys k0 ..: scores, softmax, products.  kEdge:
+// some row does not see all of them (code of its own: the branches around each
+// mask cost more than the masks).  q(n, x): fragment x of tile n's Q.
+template <int kDP, int kNT, bool kFull, int kH, bool kEdge, typename Q>
+__device__ __forceinline__ void work_halves(const uint8_t* st, int k0, const Seen& seen, int nb, Rows<kDP, kNT>& w, Q&& q,
+                                            int g, int j)
 {
     using C = Cfg4<kDP, kNT>;
     constexpr int kSteps = kDP / 16;
@@ -279,7 +281,7 @@ __device__ __forceinline__ void work_halves(const uint8_t* st, int k0, bool edge
         }
     }
     // ---- softmax
-    if (edge) {
+    if (kEdge) {
 #pragma unroll
         for (int h = 0; h < kH; h++) {
 #pragma unroll
@@ -316,7 +318,7 @@ __device__ __forceinline__ void work_halves(const uint8_t* st, int k0, bool edge
                 const float f = w.m[n][y] == -INFINITY ? 0.0f : ex2(w.m[n][y] - top);
                 w.m[n][y] = top;
                 w.nm[n][y] = top == -INFINITY ? 0.0f : kLift - top;
-                w.limit[n][y] = (top + kLazy) / w.cf[n][y];
+                w.limit[n][y] = __fdividef(top + kLazy, w.cf[n][y]);
                 w.l[n][y] *= f;
 #pragma unroll
                 for (int x = 0; x < kSteps; x++) {
@@ -360,7 +362,7 @@ __device__ __forceinline__ void work_halves(const uint8_t* st, int k0, bool edge
             }
             b[u] = kFull || blk < nb ? sf[key * nb + blk] : 0u;
         }
-        if (edge) {                                        // a value that no row sees may be anything
+        if (kEdge) {                                       // a value that no row sees may be anything
             const int lo = seen.lo - k0 - h * kHalf, ke = seen.ke - k0 - h * kHalf;
 #pragma unroll
             for (int u = 0; u < 4; u++)
@@ -392,37 +394,45 @@ __device__ __forceinline__ void work_halves(const uint8_t* st, int k0, bool edge
     }
 }
 
-// A warp's ring of chunks, and the copies into it.  kRowChunks: lanes' shares.
+// A warp's ring of chunks, and the copies into it.  Every copy() is followed by
+// a release() or, at a part's start, by as many copies as stages are free: with a
+// commit for each of them, real or not, the oldest chunk is there when all but
+// kStages - 1 commits are complete.
 template <int kDP, int kNT, bool kFull>
 struct Ring {
     using C = Cfg4<kDP, kNT>;
     const Params4& prm;
     uint8_t* base;
     uint32_t addr;
-    int lane, D, nb, chunk, chunks;            // bytes of a copy, copies of a half's codes
+    int lane, D, chunks;                       // copies of a half's codes
+    bool whole16;                              // ... of 16 bytes (8 where a row is not whole sixteens)
     int to[kFull ? 1 : 4];
     uint32_t sf_to;
-    const uint8_t* sf_base;
-    int in = 0, out = 0, ahead = 0;            // stages to fill and to read next; filled ones
+    const uint8_t* k_at;                       // this lane's first bytes of page 0: codes of K and V, scales
+    const uint8_t* v_at;
+    const uint8_t* sf_at;
+    int in = 0, out = 0;                       // stages to fill and to read next, in bytes
+    int ahead = 0;                             // filled ones
 
     __device__ __forceinline__ Ring(const Params4& prm, uint8_t* base, int lane, int D) : prm(prm), base(base), lane(lane), D(D)
     {
         addr = smem_u32(base);
-        nb = D / 16;
-        // 16 bytes of codes (or, where a row is not whole sixteens, 8) and of
-        // scales (16 keys' are D bytes)
-        chunk = kFull || D % 32 == 0 ? 16 : 8;
-        const int per_row = D / 2 / chunk;
+        whole16 = kFull || D % 32 == 0;
+        const int chunk = whole16 ? 16 : 8, per_row = D / 2 / chunk;
         chunks = kHalf * per_row;
 #pragma unroll
         for (int i = 0; i < (kFull ? 1 : 4); i++) {
             const int c = lane + 32 * i;
             to[i] = (c / per_row) * C::kRowBytes + (c % per_row) * chunk;
         }
+        k_at = prm.k + lane * chunk;
+        v_at = prm.v + lane * chunk;
+        // 16 keys' scales are D bytes: lanes 0-7 and 8-15 K's and V's of the first half, then the second's
         const bool of_v = lane >> 3 & 1;
         sf_to = (lane >> 4) * C::kHalfBytes + 2 * C::kCodes + (of_v ? C::kScales : 0) + (lane & 7) * 16;
-        sf_base = (of_v ? prm.v_sf : prm.k_sf) + (lane & 7) * 16;
+        sf_at = (of_v ? prm.v_sf : prm.k_sf) + (lane & 7) * 16;
     }
+    __device__ __forceinline__ static int next(int at) { return C::kStages == 2 ? C::kStageBytes - at : at == (C::kStages - 1) * C::kStageBytes ? 0 : at + C::kStageBytes; }
     // Page ids of the halves of 16 chunks, `stride` keys apart, from key k on:
     // a lane each; none from ke on.
     __device__ __forceinline__ int load_ids(const int32_t* table, int k, int stride, int ke) const
@@ -435,63 +445,59 @@ struct Ring {
     // is zeros; a half past the keys' end is masked as a whole.
     __device__ __forceinline__ void copy(int k0, int hk, int ids, int i)
     {
-        const uint32_t st = addr + in * C::kStageBytes;
-        const int page_mask = (1 << prm.page_shift) - 1;
-        const int row0 = (hk << prm.page_shift) + (k0 & page_mask);
-        const int row1 = (hk << prm.page_shift) + ((k0 + kHalf) & page_mask);
-        const uint32_t id0 = __shfl_sync(0xffffffffu, ids, 2 * i), id1 = __shfl_sync(0xffffffffu, ids, 2 * i + 1);
-        const bool real0 = id0 < (uint32_t)prm.pages, real1 = id1 < (uint32_t)prm.pages;
-        const uint32_t page0 = real0 ? id0 : 0u, page1 = real1 ? id1 : 0u;
+        const uint32_t st = addr + in;
+        const int page_mask = (1 << prm.page_shift) - 1, head = hk << prm.page_shift;
+        uint32_t page[2], row[2], size[2];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const uint64_t at = (uint64_t)(h ? page1 : page0) * prm.page_stride + (uint32_t)((h ? row1 : row0) * (D / 2));
-            const bool real = h ? real1 : real0;
+            const uint32_t id = __shfl_sync(0xffffffffu, ids, 2 * i + h);
+            size[h] = id < (uint32_t)prm.pages ? 16 : 0;
+            page[h] = size[h] ? id : 0u;
+            row[h] = head + ((k0 + kHalf * h) & page_mask);
+            const uint64_t at = (uint64_t)page[h] * prm.page_stride + row[h] * (uint32_t)(D / 2);
+            const uint8_t* ck = k_at + at;
+            const uint8_t* cv = v_at + at;
             const uint32_t sh = st + h * C::kHalfBytes + to[0];
-            const uint8_t* ck = prm.k + lane * chunk + at;
-            const uint8_t* cv = prm.v + lane * chunk + at;
             if (kFull) {
-                const int n = real ? 16 : 0;
-                copy16<0>(sh, ck, n);
-                if (kDP == 128) copy16<512>(sh, ck, n);
-                copy16<0>(sh + C::kCodes, cv, n);
-                if (kDP == 128) copy16<512>(sh + C::kCodes, cv, n);
-            } else if (chunk == 16) {
+                copy16(sh, ck, size[h]);
+                if (kDP == 128) copy16<512, 512>(sh, ck, size[h]);
+                copy16<C::kCodes>(sh, cv, size[h]);
+                if (kDP == 128) copy16<C::kCodes + 512, 512>(sh, cv, size[h]);
+            } else if (whole16) {
 #pragma unroll
                 for (int y = 0; y < (kDP == 128 ? 2 : 1); y++)
                     if (lane + 32 * y < chunks) {
-                        copy16<0>(sh + to[kFull ? 0 : y] - to[0], ck + 512 * y, real ? 16 : 0);
-                        copy16<0>(sh + C::kCodes + to[kFull ? 0 : y] - to[0], cv + 512 * y, real ? 16 : 0);
+                        copy16(sh - to[0] + to[kFull ? 0 : y], ck + 512 * y, size[h]);
+                        copy16<C::kCodes>(sh - to[0] + to[kFull ? 0 : y], cv + 512 * y, size[h]);
                     }
             } else {
 #pragma unroll
                 for (int y = 0; y < (kDP == 128 ? 4 : 2); y++)
                     if (lane + 32 * y < chunks) {
-                        copy8(sh + to[kFull ? 0 : y] - to[0], ck + 256 * y, real ? 8 : 0);
-                        copy8(sh + C::kCodes + to[kFull ? 0 : y] - to[0], cv + 256 * y, real ? 8 : 0);
+                        copy8(sh - to[0] + to[kFull ? 0 : y], ck + 256 * y, size[h] / 2);
+                        copy8(sh - to[0] + C::kCodes + to[kFull ? 0 : y], cv + 256 * y, size[h] / 2);
                     }
             }
         }
         const bool second = lane >> 4;
-        if ((lane & 7) * 16 < D)
-            copy16<0>(st + sf_to, sf_base + (uint64_t)(second ? page1 : page0) * prm.sf_stride + (uint32_t)((second ? row1 : row0) * nb),
-                      (second ? real1 : real0) ? 16 : 0);
-        copies_end();
-        in = in + 1 == C::kStages ? 0 : in + 1;
+        if ((kFull && kDP == 128) || (lane & 7) * 16 < D)
+            copy16(st + sf_to,
+                   sf_at + (uint64_t)(second ? page[1] : page[0]) * prm.sf_stride + (second ? row[1] : row[0]) * (uint32_t)(D / 16),
+                   second ? size[1] : size[0]);
+        in = next(in);
         ahead++;
     }
     // The oldest chunk, once it is there.
     __device__ __forceinline__ const uint8_t* wait()
     {
-        if (C::kStages == 3 && ahead == 3) copies_wait<2>();
-        else if (ahead >= 2) copies_wait<1>();
-        else copies_wait<0>();
+        copies_wait<C::kStages - 1>();
         __syncwarp();
-        return base + out * C::kStageBytes;
+        return base + out;
     }
     __device__ __forceinline__ void release()
     {
         __syncwarp();
-        out = out + 1 == C::kStages ? 0 : out + 1;
+        out = next(out);
         ahead--;
     }
 };
@@ -676,11 +682,13 @@ __device__ __forceinline__ void passes_together(const Params4& prm, uint8_t* sme
                 issue_n = next_n;
                 ids = ids_next;
             }
-            if (issue_i == issue_n) return;
-            const Pass& from = in_next ? nxt : cur;
-            if (issue_i && (issue_i & 15) == 0) ids = ids_of(from, issue_i);
-            ring.copy(from.kb + (warp + issue_i * C::kWarps) * kChunk, from.hk, ids, issue_i & 15);
-            issue_i++;
+            if (issue_i < issue_n) {
+                const Pass& from = in_next ? nxt : cur;
+                if (issue_i && (issue_i & 15) == 0) ids = ids_of(from, issue_i);
+                ring.copy(from.kb + (warp + issue_i * C::kWarps) * kChunk, from.hk, ids, issue_i & 15);
+                issue_i++;
+            }
+            copies_end();
         };
 #pragma unroll 1
         for (int y = ring.ahead; y < C::kStages; y++) issue();
@@ -720,7 +728,10 @@ __device__ __forceinline__ void passes_together(const Params4& prm, uint8_t* sme
             for (int h = 0; h < 2; h += C::kAtOnce) {
                 const int k = kc + h * kHalf;
                 const bool edge = k < lo_all || k + C::kAtOnce * kHalf > hi_all;
-                work_halves<kDP, kNT, kFull, C::kAtOnce>(st + h * C::kHalfBytes, k, edge, seen, nb, w, frag, g, j);
+                if (edge)
+                    work_halves<kDP, kNT, kFull, C::kAtOnce, true>(st + h * C::kHalfBytes, k, seen, nb, w, frag, g, j);
+                else
+                    work_halves<kDP, kNT, kFull, C::kAtOnce, false>(st + h * C::kHalfBytes, k, seen, nb, w, frag, g, j);
             }
             ring.release();
             issue();
@@ -934,13 +945,17 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
     Ring<kDP, kNT, kFull> ring(prm, smem + warp * (C::kStages * C::kStageBytes), lane, D);
     Rows<kDP, kNT> w;
     next(&s_work[warp][0]);
-    int issue_k, issue_ke, issue_i = 0, ids;               // the next chunk to copy: of this part or (in_next) the next
+    // the next chunk to copy, of this part or (in_next) the next; chunks whose
+    // pages' ids are in `ids`, from the issue_i-th on
+    int issue_k = 0, issue_ke = 0, issue_hk = 0, issue_i = 0, issue_left = 0, ids = 0;
     bool in_next = false;
-    {
+    if (s_work[warp][0].valid) {
         const Work& x = s_work[warp][0];
-        issue_k = x.valid ? x.kb : 0;
-        issue_ke = x.valid ? x.ke : 0;
-        ids = issue_k < issue_ke ? ring.load_ids(x.table, issue_k, kChunk, issue_ke) : 0;
+        issue_k = x.kb;
+        issue_ke = x.ke;
+        issue_hk = x.hk;
+        if (x.n) ids = ring.load_ids(x.table, x.kb, kChunk, x.ke);
+        issue_left = min(x.n, 16);
     }
     int at = 0;
     bool pending = false;
@@ -1006,21 +1021,25 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
             const int next_ids = nxt.valid && nxt.n ? ring.load_ids(nxt.table, nxt.kb, kChunk, nxt.ke) : 0;
             in_next = false;                               // (what has been issued of the next part is now this one's)
             auto issue = [&]() {
-                if (issue_k >= issue_ke && !in_next && nxt.valid) {
-                    in_next = true;
-                    issue_k = nxt.kb;
-                    issue_ke = nxt.ke;
+                if (issue_left == 0) {                     // the next ids: of this part, or of the next
+                    if (issue_k >= issue_ke && !in_next && nxt.valid) {
+                        in_next = true;
+                        issue_k = nxt.kb;
+                        issue_ke = nxt.ke;
+                        issue_hk = nxt.hk;
+                        ids = next_ids;
+                    } else if (issue_k < issue_ke) {
+                        ids = ring.load_ids((in_next ? nxt : cur).table, issue_k, kChunk, issue_ke);
+                    }
+                    issue_left = min(max((issue_ke - issue_k + kChunk - 1) / kChunk, 0), 16);
                     issue_i = 0;
-                    ids = next_ids;
                 }
-                if (issue_k >= issue_ke) return;
-                const Work& from = in_next ? nxt : cur;
-                if (issue_i == 16) {
-                    issue_i = 0;
-                    ids = ring.load_ids(from.table, issue_k, kChunk, issue_ke);
+                if (issue_left) {
+                    ring.copy(issue_k, issue_hk, ids, issue_i++);
+                    issue_k += kChunk;
+                    issue_left--;
                 }
-                ring.copy(issue_k, from.hk, ids, issue_i++);
-                issue_k += kChunk;
+                copies_end();
             };
 #pragma unroll 1
             for (int y = ring.ahead; y < C::kStages; y++) issue();
@@ -1034,11 +1053,14 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
             for (int i = cur.n; i > 0; i--, k0 += kChunk) {
                 const uint8_t* st = ring.wait();
                 auto frag = [&](int n, int x) { return make_uint2(q[n][2 * x], q[n][2 * x + 1]); };
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < 2; h += C::kAtOnce) {
                     const int k = k0 + h * kHalf;
                     const bool edge = k < lo_all || k + C::kAtOnce * kHalf > hi_all;
-                    work_halves<kDP, kNT, kFull, C::kAtOnce>(st + h * C::kHalfBytes, k, edge, seen, nb, w, frag, g, j);
+                    if (edge)
+                        work_halves<kDP, kNT, kFull, C::kAtOnce, true>(st + h * C::kHalfBytes, k, seen, nb, w, frag, g, j);
+                    else
+                        work_halves<kDP, kNT, kFull, C::kAtOnce, false>(st + h * C::kHalfBytes, k, seen, nb, w, frag, g, j);
                 }
                 ring.release();
                 issue();
