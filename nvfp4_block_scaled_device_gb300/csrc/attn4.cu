@@ -515,10 +515,10 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int cta0, int part
         float top = -INFINITY, sum = 0.0f;
         float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll 1
-        for (int i0 = 0; i0 < parts; i0 += 8) {
-            float2 ml[8], e[8];
+        for (int i0 = 0; i0 < parts; i0 += 16) {
+            float2 ml[16], e[16];
 #pragma unroll
-            for (int u = 0; u < 8; u++) {
+            for (int u = 0; u < 16; u++) {
                 const float* from = slot_of(min(i0 + u, parts - 1));
                 ml[u] = __ldcg(reinterpret_cast<const float2*>(from + kAttnSlotRows * kDP + 2 * r));
                 e[u] = __ldcg(reinterpret_cast<const float2*>(from + r * kDP + col));
@@ -526,14 +526,14 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int cta0, int part
             }
             float most = top;
 #pragma unroll
-            for (int u = 0; u < 8; u++) most = fmaxf(most, ml[u].x);
+            for (int u = 0; u < 16; u++) most = fmaxf(most, ml[u].x);
             const float f0 = top == -INFINITY ? 0.0f : ex2(top - most);
             acc.x *= f0;
             acc.y *= f0;
             sum *= f0;
             top = most;
 #pragma unroll
-            for (int u = 0; u < 8; u++) {
+            for (int u = 0; u < 16; u++) {
                 if (ml[u].y == 0.0f) continue;             // no key of this part
                 const float f = ml[u].x == -INFINITY ? 0.0f : ex2(ml[u].x - top);
                 acc.x += f * e[u].x;
@@ -1149,10 +1149,19 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
             reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     griddep_wait();
     __syncthreads();
-    if (C::kOwnShares && a.sched->per_cta4 > 0 && a.sched->most_tokens * a.group <= C::kRows)
-        own_shares<kDP, kNT, kFull>(prm, smem, cta);
-    else
-        passes_together<kDP, kNT, kFull>(prm, smem, cta);
+    // Shares of warps where there are several items for each CTA, or long ones: one
+    // join at the end, whatever the items' lengths (64 requests of 200 to 8192 keys
+    // 43 us, 70 with all warps on one item at a time; a request of 131071 with one of
+    // 65537 53 and 56).  Else all warps at once on a CTA's one part, which is
+    // joined faster (a request of 333 keys 6.9 us, 8.8; 8 of 2000 13.3, 19.1).
+    bool own = false;
+    if constexpr (C::kOwnShares) {
+        const int64_t items = (int64_t)a.sched->qtiles * a.kv_heads;
+        const int per = a.sched->per_cta4;
+        own = per > 0 && a.sched->most_tokens * a.group <= C::kRows && (2 * items >= 3 * (int)gridDim.x || per >= 256);
+        if (own) own_shares<kDP, kNT, kFull>(prm, smem, cta);
+    }
+    if (!own) passes_together<kDP, kNT, kFull>(prm, smem, cta);
     copies_wait<0>();
     if (a.cu_end) {
         // the rows past the step's last token, a warp to a row

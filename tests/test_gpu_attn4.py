@@ -127,6 +127,33 @@ def test_long_contexts_shared_by_ctas(nv, ws, ctx, H, Hkv, D, page):
     run(nv, ws, ctx, [3] * len(ctx), H, Hkv, D, page, window=4000, seed=1)
 
 
+@pytest.mark.parametrize("H,Hkv,D,page,tokens", [(40, 8, 128, 16, 1), (12, 12, 64, 32, 1), (16, 8, 96, 64, 3), (24, 8, 128, 128, 4),
+                                                 (16, 4, 32, 16, 2), (128, 8, 128, 16, 1)])
+@pytest.mark.parametrize("kind", ["mixed", "tiny", "empty", "window"])
+def test_more_items_than_ctas(nv, ws, H, Hkv, D, page, tokens, kind):
+    """Several items to a CTA, cut anywhere between its warps."""
+    rng = np.random.default_rng(H + D)
+    n = 96 if kind == "tiny" else 72
+    ctx = {"mixed": rng.integers(0, 2500, n), "tiny": rng.integers(0, 40, n), "empty": rng.integers(0, 900, n),
+           "window": rng.integers(0, 3000, n)}[kind].tolist()
+    q = [tokens] * n
+    if kind == "empty":                                       # requests without new tokens in between
+        q = [0 if rng.random() < 0.2 else int(rng.integers(1, tokens + 1)) for _ in ctx]
+    run(nv, ws, ctx, q, H, Hkv, D, page, window=300 if kind == "window" else 0, pad=1)
+
+
+def test_one_request_of_many_tokens_among_single_ones(nv, ws):
+    """Rows of one request that need several passes, where the step's average is a few."""
+    ctx = [int(c) for c in np.random.default_rng(3).integers(0, 700, 64)]
+    run(nv, ws, ctx, [1] * 20 + [70] + [1] * 43, 10, 2, 128, 16)
+    run(nv, ws, ctx, [1] * 63 + [200], 4, 4, 64, 32, expanded=True)
+
+
+def test_a_share_of_very_long_items(nv, ws):
+    run(nv, ws, [170000], [1], 8, 8, 64, 128)
+    run(nv, ws, [120000, 90000], [1, 2], 8, 8, 32, 64)
+
+
 @pytest.mark.parametrize("layout", ["heads_first", "padded"])
 @pytest.mark.parametrize("D", [128, 80])
 def test_layouts(nv, ws, layout, D):
