@@ -24,10 +24,13 @@ int log2_of(int64_t v)
 // y = x / sqrt(mean(x^2) + eps) * w, then the rotation, in binary32, rounded
 // once.  A head's row is D / 8 lanes of one 16-byte vector each, so that the
 // mean is a few shuffles, interleaved pairs lie in one lane and those of halves
-// in two; a warp takes 32 / (D / 8) rows of one token at a time and keeps the
-// token's cosines and sines over its rows.  K rows go to k_out or, with those
-// of V, into the cache, in 4 bits from the bf16 value (so that the pass gives
-// what the two calls give); a block of 16 columns is two lanes.
+// in two; a warp takes 32 / (D / 8) rows of one token and kind (q, k, v) at a
+// time and keeps the token's cosines and sines over its rows.  Arithmetic on
+// pairs of columns (two binary32 operations an instruction: without it, and with
+// the kinds mixed in a warp, the pass was bound by its instructions, 195 us where
+// it now takes HEADS_US).  K rows go to k_out or, with those of V, into the cache,
+// in 4 bits from the bf16 value (so that the pass gives what the two calls give);
+// a block of 16 columns is two lanes.
 //
 // Bound by HBM with many tokens (2 B in, 2 B out a column); with few by the
 // launch and one dependent chain of loads, so the rows of a token are spread
@@ -37,28 +40,44 @@ constexpr int kHeadWarps = kHeadThreads / 32;
 constexpr int kHeadBatch = 4;          // rows of a lane loaded before the first is worked on
 
 enum { kToRows = 0, kToCache = 1, kToCache4 = 2 };
+enum { kNoRope = 0, kPairs = 1, kHalves = 2 };
 
 struct HeadsParams {
     nvfp4_heads_t h;
     nvfp4_kv_cache_t c;                // kToCache
     nvfp4_kv4_cache_t c4;              // kToCache4
     int lanes;                         // of a row: a power of two >= head_dim / 8
-    int rows;                          // of a token: q, k and (into a cache) v heads
-    int per;                           // batches of kHeadBatch rows a lane of a warp's unit
-    int units;                         // of a token
+    int per;                           // batches of a warp's unit
+    int units_q, units_k, units;       // units of a token: of q, of k, of all kinds
     int page_shift;
     int wide_tables;                   // the tables can be read in 16-byte vectors
     int* status;
 };
 
-__device__ __forceinline__ uint4 pack8(const float* v)
+// Two binary32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
 {
-    return make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
+    float2 d;
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
-__device__ __forceinline__ void unpack8(uint4 x, float* v)
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
-    v[0] = bf16_lo(x.x), v[1] = bf16_hi(x.x), v[2] = bf16_lo(x.y), v[3] = bf16_hi(x.y);
-    v[4] = bf16_lo(x.z), v[5] = bf16_hi(x.z), v[6] = bf16_lo(x.w), v[7] = bf16_hi(x.w);
+    float2 d;
+    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+        " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ void unpack4(uint4 x, float2* v)
+{
+    v[0] = make_float2(bf16_lo(x.x), bf16_hi(x.x));
+    v[1] = make_float2(bf16_lo(x.y), bf16_hi(x.y));
+    v[2] = make_float2(bf16_lo(x.z), bf16_hi(x.z));
+    v[3] = make_float2(bf16_lo(x.w), bf16_hi(x.w));
 }
 
 // Largest magnitude of two bf16x2, NaN if one is.
@@ -85,8 +104,116 @@ __device__ __forceinline__ void load_table(const float* t, int64_t at, bool wide
     }
 }
 
-template <int kTo>
-__global__ void __launch_bounds__(kHeadThreads) heads_kernel(const __grid_constant__ HeadsParams p)
+// A lane's place in a warp's rows, and where these come from and go.
+struct HeadRows {
+    const __nv_bfloat16* src;          // this lane's columns of row 0, and of a row kHeadBatch * at_once on ...
+    int64_t step;                      // ... elements from one of its rows to the next
+    __nv_bfloat16* out;                // NULL: none
+    int64_t step_out;
+    uint8_t* codes;                    // kToCache4: of the slot's row 0 (NULL: none), its scale, bytes from one to the next
+    uint8_t* sf;
+    uint32_t step_codes, step_sf;
+    float g;
+    __nv_bfloat16* also;               // k_out beside a cache
+    int64_t step_also;
+    int left;                          // rows from this lane's first on (in steps)
+};
+
+// The rows of a warp's unit.  norm: times w / rms; kRope: rotated by c, s; kTo:
+// bf16 to out, or codes and scales.
+template <int kTo, int kRope, bool kNorm>
+__device__ __forceinline__ void work_rows(HeadRows& q, int batches, int L, const float2* w, float inv_d, float eps, const float* c,
+                                          const float* s, bool rotate, int skip, float sign, int partner, bool scale_lane)
+{
+    constexpr int kAngles = kRope == kHalves ? 8 : 4;
+#pragma unroll 1
+    for (;;) {
+        uint4 x[kHeadBatch];
+#pragma unroll
+        for (int i = 0; i < kHeadBatch; i++)
+            x[i] = i < q.left ? *reinterpret_cast<const uint4*>(q.src + i * q.step) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kHeadBatch; i++) {
+            uint4 y = x[i];
+            if (kNorm || kRope != kNoRope) {
+                float2 v[4];
+                unpack4(x[i], v);
+                if (kNorm) {
+                    float2 sq = mul2(v[0], v[0]);
+#pragma unroll
+                    for (int z = 1; z < 4; z++) sq = fma2(v[z], v[z], sq);
+                    float sum = sq.x + sq.y;
+#pragma unroll
+                    for (int o = 8; o; o >>= 1) {
+                        const float other = __shfl_xor_sync(0xffffffffu, sum, o);
+                        if (o < L) sum += other;
+                    }
+                    const float inv = rsqrtf(sum * inv_d + eps);
+#pragma unroll
+                    for (int z = 0; z < 4; z++) v[z] = mul2(mul2(v[z], make_float2(inv, inv)), w[z]);
+                }
+                if (kRope == kHalves) {
+#pragma unroll
+                    for (int z = 0; z < 4; z++) {
+                        const float2 other = make_float2(__shfl_sync(0xffffffffu, v[z].x, partner), __shfl_sync(0xffffffffu, v[z].y, partner));
+                        // (products rounded first: the sum with a factor of 1 or -1 is one operation)
+                        const float2 r = fma2(mul2(other, make_float2(s[(2 * z) % kAngles], s[(2 * z + 1) % kAngles])), make_float2(sign, sign),
+                                              mul2(v[z], make_float2(c[(2 * z) % kAngles], c[(2 * z + 1) % kAngles])));
+                        if (rotate) v[z] = r;
+                    }
+                } else if (kRope == kPairs) {
+#pragma unroll
+                    for (int z = 0; z < 4; z++) {
+                        const float2 r = fma2(mul2(make_float2(v[z].y, v[z].x), make_float2(s[z], s[z])), make_float2(-1.0f, 1.0f),
+                                              mul2(v[z], make_float2(c[z], c[z])));
+                        // (columns before the rotated ones are not touched: 1 and 0 would lose a -0 or a NaN's partner)
+                        if (z >= skip) v[z] = r;
+                    }
+                }
+                y = make_uint4(cvt_bf16x2(v[0].x, v[0].y), cvt_bf16x2(v[1].x, v[1].y), cvt_bf16x2(v[2].x, v[2].y), cvt_bf16x2(v[3].x, v[3].y));
+            }
+            const bool here = i < q.left;
+            if (q.out && here) *reinterpret_cast<uint4*>(q.out + i * q.step_out) = y;
+            if (kTo != kToRows && q.also && here) *reinterpret_cast<uint4*>(q.also + i * q.step_also) = y;
+            if (kTo == kToCache4 && q.codes) {
+                uint32_t m = amax_bf16x2(amax_bf16x2(y.x, y.y), amax_bf16x2(y.z, y.w));
+                m = amax_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = amax_bf16x2(m, m >> 16 | m << 16);
+                float2 v[4];
+                float z[8];
+                unpack4(y, v);
+#pragma unroll
+                for (int k = 0; k < 4; k++) z[2 * k] = v[k].x, z[2 * k + 1] = v[k].y;
+                float amax = bf16_lo(m);
+                const bool nan = amax != amax;
+                constexpr float kMost = 3.3895313892515355e38f;          // of bf16
+                if (!(amax <= kMost)) {
+                    amax = kMost;
+#pragma unroll
+                    for (int k = 0; k < 8; k++) z[k] = fminf(fmaxf(z[k], -kMost), kMost);
+                }
+                uint32_t sc, codes = quant_half_block(z, q.g, amax, &sc);
+                if (nan) sc = 0x7f, codes = 0;
+                if (here) {
+                    *reinterpret_cast<uint32_t*>(q.codes + (uint64_t)i * q.step_codes) = codes;
+                    if (scale_lane) q.sf[(uint64_t)i * q.step_sf] = (uint8_t)sc;
+                }
+            }
+        }
+        q.left -= kHeadBatch;
+        if (--batches == 0 || !__any_sync(0xffffffffu, q.left > 0)) break;
+        q.src += kHeadBatch * q.step;
+        if (q.out) q.out += kHeadBatch * q.step_out;
+        if (kTo != kToRows && q.also) q.also += kHeadBatch * q.step_also;
+        if (kTo == kToCache4 && q.codes) {
+            q.codes += (uint64_t)kHeadBatch * q.step_codes;
+            q.sf += (uint64_t)kHeadBatch * q.step_sf;
+        }
+    }
+}
+
+template <int kTo, int kRope>
+__global__ void __launch_bounds__(kHeadThreads, kTo == kToCache4 ? 2 : 3) heads_kernel(const __grid_constant__ HeadsParams p)
 {
     griddep_launch_dependents();
     griddep_wait();
@@ -94,17 +221,56 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(const __grid_consta
     const int lane = threadIdx.x & 31, L = p.lanes, D = (int)h.head_dim;
     const int sub = lane / L, col = 8 * (lane & (L - 1)), at_once = 32 / L;
     const bool in_row = col < D;
-    const int64_t unit = (int64_t)blockIdx.x * kHeadWarps + (threadIdx.x >> 5);
-    const int64_t t = unit / p.units;
+    const uint32_t unit = blockIdx.x * kHeadWarps + (threadIdx.x >> 5), t = unit / (uint32_t)p.units;
     if (t >= h.tokens) return;
-    const int row0 = (int)(unit - t * p.units) * p.per * kHeadBatch * at_once;
-    const int Hq = (int)h.heads, Hk = Hq + (int)h.kv_heads;
+    // the warp's rows: of one kind
+    int u = (int)(unit - t * p.units);
+    const bool is_q = u < p.units_q, is_v = kTo != kToRows && u >= p.units_q + p.units_k;
+    u -= is_q ? 0 : is_v ? p.units_q + p.units_k : p.units_q;
+    const int rows = (int)(is_q ? h.heads : h.kv_heads), r0 = u * p.per * kHeadBatch * at_once + sub;
+    const int64_t pitch = is_q ? h.hq : is_v ? h.hv : h.hk, ld = is_q ? h.ldq : is_v ? h.ldv : h.ldk;
+    HeadRows q = {};
+    q.src = static_cast<const __nv_bfloat16*>(is_q ? h.q : is_v ? h.v : h.k) + t * ld + r0 * pitch + col;
+    q.step = at_once * pitch;
+    q.left = in_row && r0 < rows ? (rows - r0 + at_once - 1) / at_once : 0;
+    const int64_t pitch_out = is_q ? h.hqo : h.hko;
+    __nv_bfloat16* rows_out = static_cast<__nv_bfloat16*>(is_q ? h.q_out : is_v ? nullptr : h.k_out);
+    if (rows_out) rows_out += t * (is_q ? h.ldqo : h.ldko) + r0 * pitch_out + col;
+    q.out = rows_out;
+    q.step_out = at_once * pitch_out;
+    if (kTo != kToRows && !is_q) {
+        const int64_t slots = (kTo == kToCache ? p.c.pages : p.c4.pages) << p.page_shift;
+        const int64_t slot = h.slot[t];
+        const bool ok = slot >= 0 && slot < slots;
+        if (!ok && slot != -1 && lane == 0 && u == 0) report(p.status, kStatusSlot);
+        const int64_t page = slot >> p.page_shift, at = ((int64_t)r0 << p.page_shift) + (slot & (((int64_t)1 << p.page_shift) - 1));
+        if (kTo == kToCache) {
+            q.also = rows_out;
+            q.step_also = q.step_out;
+            q.out = ok ? static_cast<__nv_bfloat16*>(is_v ? p.c.v : p.c.k) + page * p.c.page_stride + at * D + col : nullptr;
+            q.step_out = (int64_t)(at_once << p.page_shift) * D;
+        } else {
+            q.codes = ok ? (is_v ? p.c4.v : p.c4.k) + page * p.c4.page_stride + at * (D / 2) + col / 2 : nullptr;
+            q.sf = (is_v ? p.c4.v_sf : p.c4.k_sf) + page * p.c4.sf_stride + at * (D / 16) + col / 16;
+            q.step_codes = (at_once << p.page_shift) * (D / 2);
+            q.step_sf = (at_once << p.page_shift) * (D / 16);
+            q.g = *(is_v ? p.c4.v_g : p.c4.k_g);
+        }
+    }
+    const bool scale_lane = (col & 8) == 0;
+    const float inv_d = 1.0f / (float)D;
+    const __nv_bfloat16* weight = static_cast<const __nv_bfloat16*>(is_q ? h.q_norm : is_v ? nullptr : h.k_norm);
+    if (kTo != kToRows && is_v) {
+        work_rows<kTo, kNoRope, false>(q, p.per, L, nullptr, inv_d, h.eps, nullptr, nullptr, false, 0, 0.0f, lane, scale_lane);
+        return;
+    }
 
     // the angles of this lane's columns: of 4 pairs, or of 8 columns and their other halves
     const int rd = (int)h.rope_dim, rot0 = D - rd, half = rd / 2;
-    float c[8], s[8];
+    constexpr int kAngles = kRope == kHalves ? 8 : 4;
+    float c[kAngles], s[kAngles];
     bool rotate = false;
-    if (h.pos && in_row && col + 8 > rot0) {
+    if (kRope != kNoRope && in_row && col + 8 > rot0) {
         int64_t at = h.pos[t];
         if (at < 0 || at >= h.positions) {
             if (col + 8 >= D && sub == 0) report(p.status, kStatusRope);
@@ -112,141 +278,56 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(const __grid_consta
         }
         at *= h.table_ld;
         rotate = true;
-        if (h.halves) {
+        if (kRope == kHalves) {
             const int i = col - rot0 < half ? col - rot0 : col - rot0 - half;
-            load_table<8>(h.cos_t, at + i, p.wide_tables, c);
-            load_table<8>(h.sin_t, at + i, p.wide_tables, s);
+            load_table<kAngles>(h.cos_t, at + i, p.wide_tables, c);
+            load_table<kAngles>(h.sin_t, at + i, p.wide_tables, s);
         } else if (col >= rot0 && (col - rot0) % 8 == 0) {
-            load_table<4>(h.cos_t, at + (col - rot0) / 2, p.wide_tables, c);
-            load_table<4>(h.sin_t, at + (col - rot0) / 2, p.wide_tables, s);
+            load_table<kAngles>(h.cos_t, at + (col - rot0) / 2, p.wide_tables, c);
+            load_table<kAngles>(h.sin_t, at + (col - rot0) / 2, p.wide_tables, s);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const int x = col + 2 * i - rot0;
-                c[i] = x >= 0 ? h.cos_t[at + x / 2] : 1.0f;
-                s[i] = x >= 0 ? h.sin_t[at + x / 2] : 0.0f;
+                const int y = col + 2 * i - rot0;
+                c[i] = y >= 0 ? h.cos_t[at + y / 2] : 1.0f;
+                s[i] = y >= 0 ? h.sin_t[at + y / 2] : 0.0f;
             }
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kAngles; i++) c[i] = s[i] = 0.0f;
     }
-    const int partner = lane + (col - rot0 < half ? rd / 16 : -rd / 16);
-    float wq[8], wk[8];
-    if (h.q_norm && in_row) unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(h.q_norm) + col), wq);
-    if (h.k_norm && in_row) unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(h.k_norm) + col), wk);
-    int64_t slot = -1;
-    float g_k = 0.0f, g_v = 0.0f;
-    if (kTo != kToRows) {
-        const int64_t slots = (kTo == kToCache ? p.c.pages : p.c4.pages) << p.page_shift;
-        slot = h.slot[t];
-        if (slot != -1 && (slot < 0 || slot >= slots)) {
-            if (lane == 0 && row0 == 0) report(p.status, kStatusSlot);
-            slot = -1;
-        }
-        if (kTo == kToCache4) g_k = *p.c4.k_g, g_v = *p.c4.v_g;
-    }
-    const int64_t page = slot >> p.page_shift, in_page = slot & (((int64_t)1 << p.page_shift) - 1);
-
-    for (int b = 0; b < p.per; b++) {
-        uint4 x[kHeadBatch];
-        const int r0 = row0 + b * kHeadBatch * at_once + sub;
-        if (r0 - sub >= p.rows) return;
-#pragma unroll
-        for (int u = 0; u < kHeadBatch; u++) {
-            const int r = r0 + u * at_once;
-            const void* base = r < Hq ? h.q : r < Hk ? h.k : h.v;
-            const int64_t ld = r < Hq ? h.ldq : r < Hk ? h.ldk : h.ldv, hd = r < Hq ? h.hq : r < Hk ? h.hk : h.hv;
-            const int i = r < Hq ? r : r < Hk ? r - Hq : r - Hk;
-            x[u] = make_uint4(0, 0, 0, 0);
-            if (in_row && r < p.rows)
-                x[u] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + t * ld + i * hd + col);
-        }
-#pragma unroll
-        for (int u = 0; u < kHeadBatch; u++) {
-            const int r = r0 + u * at_once;
-            const bool is_q = r < Hq, is_v = r >= Hk;
-            const int i = is_q ? r : is_v ? r - Hk : r - Hq;
-            const bool norm = !is_v && (is_q ? h.q_norm : h.k_norm) != nullptr;
-            float v[8];
-            unpack8(x[u], v);
-            if (h.q_norm || h.k_norm) {                    // (all lanes: the sum goes over lanes of other rows' kinds)
-                float sum = 0.0f;
-#pragma unroll
-                for (int y = 0; y < 8; y++) sum += v[y] * v[y];
-                for (int o = L / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (norm) {
-                    const float inv = rsqrtf(sum / (float)D + h.eps);
-#pragma unroll
-                    for (int y = 0; y < 8; y++) v[y] = v[y] * inv * (is_q ? wq[y] : wk[y]);
-                }
-            }
-            if (h.pos) {
-                if (h.halves) {
-#pragma unroll
-                    for (int y = 0; y < 8; y++) {
-                        const float other = __shfl_sync(0xffffffffu, v[y], rotate ? partner : lane);
-                        if (rotate && !is_v)
-                            v[y] = col - rot0 < half ? __fsub_rn(__fmul_rn(v[y], c[y]), __fmul_rn(other, s[y]))
-                                                     : __fadd_rn(__fmul_rn(other, s[y]), __fmul_rn(v[y], c[y]));
-                    }
-                } else if (rotate && !is_v) {
-#pragma unroll
-                    for (int y = 0; y < 4; y++) {
-                        // (columns before the rotated ones are not touched: 1 and 0 would lose a -0 or a NaN's partner)
-                        if (col + 2 * y < rot0) continue;
-                        const float a = v[2 * y], d = v[2 * y + 1];
-                        v[2 * y] = __fsub_rn(__fmul_rn(a, c[y]), __fmul_rn(d, s[y]));
-                        v[2 * y + 1] = __fadd_rn(__fmul_rn(a, s[y]), __fmul_rn(d, c[y]));
-                    }
-                }
-            }
-            const uint4 y = norm || (h.pos && !is_v) ? pack8(v) : x[u];
-            const bool here = in_row && r < p.rows;
-            if (is_q || (!is_v && h.k_out)) {
-                if (here)
-                    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_q ? h.q_out : h.k_out) +
-                                              t * (is_q ? h.ldqo : h.ldko) + i * (is_q ? h.hqo : h.hko) + col) = y;
-            }
-            if (kTo == kToCache && !is_q && here && slot >= 0) {
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(is_v ? p.c.v : p.c.k);
-                *reinterpret_cast<uint4*>(out + page * p.c.page_stride + (((int64_t)i << p.page_shift) + in_page) * D + col) = y;
-            }
-            if (kTo == kToCache4) {
-                unpack8(y, v);
-                uint32_t m = amax_bf16x2(amax_bf16x2(y.x, y.y), amax_bf16x2(y.z, y.w));
-                m = amax_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = amax_bf16x2(m, m >> 16 | m << 16);
-                if (!is_q && here && slot >= 0) {
-                    float amax = bf16_lo(m);
-                    const bool nan = amax != amax;
-                    constexpr float kMost = 3.3895313892515355e38f;      // of bf16
-                    if (!(amax <= kMost)) {
-                        amax = kMost;
-#pragma unroll
-                        for (int z = 0; z < 8; z++) v[z] = fminf(fmaxf(v[z], -kMost), kMost);
-                    }
-                    uint32_t sc, codes = quant_half_block(v, is_v ? g_v : g_k, amax, &sc);
-                    if (nan) sc = 0x7f, codes = 0;
-                    const int64_t at = ((int64_t)i << p.page_shift) + in_page;
-                    *reinterpret_cast<uint32_t*>((is_v ? p.c4.v : p.c4.k) + page * p.c4.page_stride + at * (D / 2) + col / 2) =
-                        codes;
-                    if ((col & 8) == 0)
-                        (is_v ? p.c4.v_sf : p.c4.k_sf)[page * p.c4.sf_stride + at * (D / 16) + col / 16] = (uint8_t)sc;
-                }
-            }
-        }
+    const bool low = col - rot0 < half;
+    const int partner = !rotate ? lane : low ? lane + rd / 16 : lane - rd / 16;
+    const int skip = rotate ? max(rot0 - col, 0) / 2 : 4;      // pairs of the lane before the rotated ones
+    const float sign = low ? -1.0f : 1.0f;
+    if (weight) {
+        float2 w[4];
+        if (in_row) unpack4(*reinterpret_cast<const uint4*>(weight + col), w);
+        work_rows<kTo, kRope, true>(q, p.per, L, w, inv_d, h.eps, c, s, rotate, skip, sign, partner, scale_lane);
+    } else {
+        work_rows<kTo, kRope, false>(q, p.per, L, nullptr, inv_d, h.eps, c, s, rotate, skip, sign, partner, scale_lane);
     }
 }
 
 template <int kTo>
 cudaError_t run_heads(HeadsParams& p, int num_sms, cudaStream_t stream)
 {
-    const int batch = kHeadBatch * (32 / p.lanes), most = (p.rows + batch - 1) / batch;
+    const int batch = kHeadBatch * (32 / p.lanes);
+    const int64_t q = (p.h.heads + batch - 1) / batch, kv = (p.h.kv_heads + batch - 1) / batch;
     // as many warps as fill the GPU, each with as many rows of its token as that leaves
-    const int64_t per = p.h.tokens * most / ((int64_t)num_sms * 64);
+    // (no more than the smaller kind has, so that a block's warps end together)
+    const int64_t most = q && (!kv || q < kv) ? q : kv, per = p.h.tokens * (q + (kTo != kToRows ? 2 : 1) * kv) / ((int64_t)num_sms * 64);
     p.per = (int)(per < 1 ? 1 : per > most ? most : per);
-    p.units = (most + p.per - 1) / p.per;
+    p.units_q = (int)((q + p.per - 1) / p.per);
+    p.units_k = (int)((kv + p.per - 1) / p.per);
+    p.units = p.units_q + p.units_k * (kTo != kToRows ? 2 : 1);
     const int64_t blocks = (p.h.tokens * p.units + kHeadWarps - 1) / kHeadWarps;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    return launch_programmatic(heads_kernel<kTo>, dim3((unsigned)blocks), dim3(kHeadThreads), 0, stream, p);
+    if (blocks * kHeadWarps > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)blocks), block(kHeadThreads);
+    if (!p.h.pos) return launch_programmatic(heads_kernel<kTo, kNoRope>, grid, block, 0, stream, p);
+    return p.h.halves ? launch_programmatic(heads_kernel<kTo, kHalves>, grid, block, 0, stream, p)
+                      : launch_programmatic(heads_kernel<kTo, kPairs>, grid, block, 0, stream, p);
 }
 
 // ----------------------------------------------------------------- expand
@@ -372,7 +453,6 @@ cudaError_t launch_heads(const nvfp4_heads_t& heads, int* status, int num_sms, c
     p.status = status;
     p.lanes = 1 << log2_of((heads.head_dim + 7) / 8);
     const bool to_cache = heads.slot != nullptr;
-    p.rows = (int)(heads.heads + heads.kv_heads * (to_cache ? 2 : 1));
     p.wide_tables = heads.pos && heads.table_ld % 4 == 0 && ((uintptr_t)heads.cos_t | (uintptr_t)heads.sin_t) % 16 == 0;
     if (!to_cache) return run_heads<kToRows>(p, num_sms, stream);
     if (heads.cache) {
