@@ -38,6 +38,7 @@ int log2_of(int64_t v)
 constexpr int kHeadThreads = 256;
 constexpr int kHeadWarps = kHeadThreads / 32;
 constexpr int kHeadBatch = 4;          // rows of a lane loaded before the first is worked on
+constexpr int kHeadBlocks = 4;
 
 enum { kToRows = 0, kToCache = 1, kToCache4 = 2 };
 enum { kNoRope = 0, kPairs = 1, kHalves = 2 };
@@ -119,13 +120,28 @@ struct HeadRows {
     int left;                          // rows from this lane's first on (in steps)
 };
 
-// The rows of a warp's unit.  norm: times w / rms; kRope: rotated by c, s; kTo:
-// bf16 to out, or codes and scales.
-template <int kTo, int kRope, bool kNorm>
-__device__ __forceinline__ void work_rows(HeadRows& q, int batches, int L, const float2* w, float inv_d, float eps, const float* c,
-                                          const float* s, bool rotate, int skip, float sign, int partner, bool scale_lane)
+// What a lane does to its 8 columns of a row.
+struct HeadMath {
+    int L;                             // lanes of a row
+    float inv_d, eps;
+    // with a norm: column pair y becomes (v[y] * p[y] + other * q[y]) / rms, where
+    // `other` is the partner lane's pair (halves) or the pair's columns exchanged:
+    // weight times cosine, the other one's weight times sine with its sign
+    float2 p[4], q[4];
+    // without: the rotation in single operations
+    float c[8], s[8];
+    bool rotate;
+    int skip;                          // pairs of the lane before the rotated ones
+    float sign;
+    int partner;
+    bool scale_lane;
+};
+
+// The rows of a warp's unit.  kNorm: times w / rms; kRope: rotated; kTo: bf16 to
+// out, or codes and scales; kWhole: a row is 16 whole lanes, all of them rotated.
+template <int kTo, int kRope, bool kNorm, bool kWhole>
+__device__ __forceinline__ void work_rows(HeadRows& q, int batches, const HeadMath& h)
 {
-    constexpr int kAngles = kRope == kHalves ? 8 : 4;
 #pragma unroll 1
     for (;;) {
         uint4 x[kHeadBatch];
@@ -135,39 +151,49 @@ __device__ __forceinline__ void work_rows(HeadRows& q, int batches, int L, const
 #pragma unroll
         for (int i = 0; i < kHeadBatch; i++) {
             uint4 y = x[i];
-            if (kNorm || kRope != kNoRope) {
+            if (kNorm) {
+                float2 v[4], r[4];
+                unpack4(x[i], v);
+                float2 sq = mul2(v[0], v[0]);
+#pragma unroll
+                for (int z = 1; z < 4; z++) sq = fma2(v[z], v[z], sq);
+                float sum = sq.x + sq.y;
+#pragma unroll
+                for (int o = 8; o; o >>= 1) {
+                    const float other = __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (kWhole || o < h.L) sum += other;
+                }
+                const float inv = rsqrtf(sum * h.inv_d + h.eps);
+#pragma unroll
+                for (int z = 0; z < 4; z++) r[z] = mul2(v[z], h.p[z]);
+                if (kRope == kHalves) {
+                    // (the bf16 row itself goes between the lanes)
+                    const uint4 ox = make_uint4(__shfl_sync(0xffffffffu, x[i].x, h.partner), __shfl_sync(0xffffffffu, x[i].y, h.partner),
+                                                __shfl_sync(0xffffffffu, x[i].z, h.partner), __shfl_sync(0xffffffffu, x[i].w, h.partner));
+                    unpack4(ox, v);
+                }
+#pragma unroll
+                for (int z = 0; z < 4; z++) {
+                    if (kRope != kNoRope) r[z] = fma2(kRope == kPairs ? make_float2(v[z].y, v[z].x) : v[z], h.q[z], r[z]);
+                    r[z] = mul2(r[z], make_float2(inv, inv));
+                }
+                y = make_uint4(cvt_bf16x2(r[0].x, r[0].y), cvt_bf16x2(r[1].x, r[1].y), cvt_bf16x2(r[2].x, r[2].y), cvt_bf16x2(r[3].x, r[3].y));
+            } else if (kRope != kNoRope) {
+                // (products rounded first: the sum with a factor of 1 or -1 is one operation)
                 float2 v[4];
                 unpack4(x[i], v);
-                if (kNorm) {
-                    float2 sq = mul2(v[0], v[0]);
 #pragma unroll
-                    for (int z = 1; z < 4; z++) sq = fma2(v[z], v[z], sq);
-                    float sum = sq.x + sq.y;
-#pragma unroll
-                    for (int o = 8; o; o >>= 1) {
-                        const float other = __shfl_xor_sync(0xffffffffu, sum, o);
-                        if (o < L) sum += other;
-                    }
-                    const float inv = rsqrtf(sum * inv_d + eps);
-#pragma unroll
-                    for (int z = 0; z < 4; z++) v[z] = mul2(mul2(v[z], make_float2(inv, inv)), w[z]);
-                }
-                if (kRope == kHalves) {
-#pragma unroll
-                    for (int z = 0; z < 4; z++) {
-                        const float2 other = make_float2(__shfl_sync(0xffffffffu, v[z].x, partner), __shfl_sync(0xffffffffu, v[z].y, partner));
-                        // (products rounded first: the sum with a factor of 1 or -1 is one operation)
-                        const float2 r = fma2(mul2(other, make_float2(s[(2 * z) % kAngles], s[(2 * z + 1) % kAngles])), make_float2(sign, sign),
-                                              mul2(v[z], make_float2(c[(2 * z) % kAngles], c[(2 * z + 1) % kAngles])));
-                        if (rotate) v[z] = r;
-                    }
-                } else if (kRope == kPairs) {
-#pragma unroll
-                    for (int z = 0; z < 4; z++) {
-                        const float2 r = fma2(mul2(make_float2(v[z].y, v[z].x), make_float2(s[z], s[z])), make_float2(-1.0f, 1.0f),
-                                              mul2(v[z], make_float2(c[z], c[z])));
+                for (int z = 0; z < 4; z++) {
+                    if (kRope == kHalves) {
+                        const float2 other = make_float2(__shfl_sync(0xffffffffu, v[z].x, h.partner), __shfl_sync(0xffffffffu, v[z].y, h.partner));
+                        const float2 r = fma2(mul2(other, make_float2(h.s[2 * z], h.s[2 * z + 1])), make_float2(h.sign, h.sign),
+                                              mul2(v[z], make_float2(h.c[2 * z], h.c[2 * z + 1])));
+                        if (h.rotate) v[z] = r;
+                    } else {
+                        const float2 r = fma2(mul2(make_float2(v[z].y, v[z].x), make_float2(h.s[z], h.s[z])), make_float2(-1.0f, 1.0f),
+                                              mul2(v[z], make_float2(h.c[z], h.c[z])));
                         // (columns before the rotated ones are not touched: 1 and 0 would lose a -0 or a NaN's partner)
-                        if (z >= skip) v[z] = r;
+                        if (z >= h.skip) v[z] = r;
                     }
                 }
                 y = make_uint4(cvt_bf16x2(v[0].x, v[0].y), cvt_bf16x2(v[1].x, v[1].y), cvt_bf16x2(v[2].x, v[2].y), cvt_bf16x2(v[3].x, v[3].y));
@@ -196,7 +222,7 @@ __device__ __forceinline__ void work_rows(HeadRows& q, int batches, int L, const
                 if (nan) sc = 0x7f, codes = 0;
                 if (here) {
                     *reinterpret_cast<uint32_t*>(q.codes + (uint64_t)i * q.step_codes) = codes;
-                    if (scale_lane) q.sf[(uint64_t)i * q.step_sf] = (uint8_t)sc;
+                    if (h.scale_lane) q.sf[(uint64_t)i * q.step_sf] = (uint8_t)sc;
                 }
             }
         }
@@ -212,15 +238,15 @@ __device__ __forceinline__ void work_rows(HeadRows& q, int batches, int L, const
     }
 }
 
-template <int kTo, int kRope>
-__global__ void __launch_bounds__(kHeadThreads, kTo == kToCache4 ? 2 : 3) heads_kernel(const __grid_constant__ HeadsParams p)
+template <int kTo, int kRope, bool kWhole>
+__global__ void __launch_bounds__(kHeadThreads, kTo == kToCache4 ? 2 : kHeadBlocks) heads_kernel(const __grid_constant__ HeadsParams p)
 {
     griddep_launch_dependents();
     griddep_wait();
     const nvfp4_heads_t& h = p.h;
-    const int lane = threadIdx.x & 31, L = p.lanes, D = (int)h.head_dim;
+    const int lane = threadIdx.x & 31, L = kWhole ? 16 : p.lanes, D = kWhole ? 128 : (int)h.head_dim;
     const int sub = lane / L, col = 8 * (lane & (L - 1)), at_once = 32 / L;
-    const bool in_row = col < D;
+    const bool in_row = kWhole || col < D;
     const uint32_t unit = blockIdx.x * kHeadWarps + (threadIdx.x >> 5), t = unit / (uint32_t)p.units;
     if (t >= h.tokens) return;
     // the warp's rows: of one kind
@@ -257,57 +283,73 @@ __global__ void __launch_bounds__(kHeadThreads, kTo == kToCache4 ? 2 : 3) heads_
             q.g = *(is_v ? p.c4.v_g : p.c4.k_g);
         }
     }
-    const bool scale_lane = (col & 8) == 0;
-    const float inv_d = 1.0f / (float)D;
+    HeadMath m;
+    m.L = L;
+    m.inv_d = 1.0f / (float)D;
+    m.eps = h.eps;
+    m.scale_lane = (col & 8) == 0;
     const __nv_bfloat16* weight = static_cast<const __nv_bfloat16*>(is_q ? h.q_norm : is_v ? nullptr : h.k_norm);
     if (kTo != kToRows && is_v) {
-        work_rows<kTo, kNoRope, false>(q, p.per, L, nullptr, inv_d, h.eps, nullptr, nullptr, false, 0, 0.0f, lane, scale_lane);
+        work_rows<kTo, kNoRope, false, kWhole>(q, p.per, m);
         return;
     }
 
     // the angles of this lane's columns: of 4 pairs, or of 8 columns and their other halves
-    const int rd = (int)h.rope_dim, rot0 = D - rd, half = rd / 2;
+    const int rd = kWhole ? D : (int)h.rope_dim, rot0 = D - rd, half = rd / 2;
     constexpr int kAngles = kRope == kHalves ? 8 : 4;
-    float c[kAngles], s[kAngles];
-    bool rotate = false;
-    if (kRope != kNoRope && in_row && col + 8 > rot0) {
+    m.rotate = kRope != kNoRope && in_row && (kWhole || col + 8 > rot0);
+    const bool low = col - rot0 < half;
+    m.partner = !m.rotate ? lane : low ? lane + rd / 16 : lane - rd / 16;
+    m.skip = m.rotate ? max(rot0 - col, 0) / 2 : 4;
+    m.sign = low ? -1.0f : 1.0f;
+#pragma unroll
+    for (int i = 0; i < kAngles; i++) m.c[i] = 1.0f, m.s[i] = 0.0f;
+    if (kRope != kNoRope && m.rotate) {
         int64_t at = h.pos[t];
         if (at < 0 || at >= h.positions) {
             if (col + 8 >= D && sub == 0) report(p.status, kStatusRope);
             at = at < 0 ? 0 : h.positions - 1;
         }
         at *= h.table_ld;
-        rotate = true;
         if (kRope == kHalves) {
-            const int i = col - rot0 < half ? col - rot0 : col - rot0 - half;
-            load_table<kAngles>(h.cos_t, at + i, p.wide_tables, c);
-            load_table<kAngles>(h.sin_t, at + i, p.wide_tables, s);
-        } else if (col >= rot0 && (col - rot0) % 8 == 0) {
-            load_table<kAngles>(h.cos_t, at + (col - rot0) / 2, p.wide_tables, c);
-            load_table<kAngles>(h.sin_t, at + (col - rot0) / 2, p.wide_tables, s);
+            const int i = low ? col - rot0 : col - rot0 - half;
+            load_table<kAngles>(h.cos_t, at + i, p.wide_tables, m.c);
+            load_table<kAngles>(h.sin_t, at + i, p.wide_tables, m.s);
+        } else if (kWhole || (col >= rot0 && (col - rot0) % 8 == 0)) {
+            load_table<kAngles>(h.cos_t, at + (col - rot0) / 2, p.wide_tables, m.c);
+            load_table<kAngles>(h.sin_t, at + (col - rot0) / 2, p.wide_tables, m.s);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const int y = col + 2 * i - rot0;
-                c[i] = y >= 0 ? h.cos_t[at + y / 2] : 1.0f;
-                s[i] = y >= 0 ? h.sin_t[at + y / 2] : 0.0f;
+                if (y < 0) continue;
+                m.c[i] = h.cos_t[at + y / 2];
+                m.s[i] = h.sin_t[at + y / 2];
             }
         }
-    } else {
+    }
+    if (!weight) {
+        work_rows<kTo, kRope, false, kWhole>(q, p.per, m);
+        return;
+    }
+    float2 w[4] = {}, o[4] = {};
+    if (in_row) {
+        unpack4(*reinterpret_cast<const uint4*>(weight + col), w);
+        if (kRope == kHalves && m.rotate) unpack4(*reinterpret_cast<const uint4*>(weight + (low ? col + half : col - half)), o);
+    }
 #pragma unroll
-        for (int i = 0; i < kAngles; i++) c[i] = s[i] = 0.0f;
+    for (int y = 0; y < 4; y++) {
+        if (kRope == kHalves) {
+            m.p[y] = mul2(w[y], make_float2(m.c[2 * y], m.c[2 * y + 1]));
+            m.q[y] = mul2(o[y], make_float2(m.sign * m.s[2 * y], m.sign * m.s[2 * y + 1]));
+        } else if (kRope == kPairs) {
+            m.p[y] = mul2(w[y], make_float2(m.c[y], m.c[y]));
+            m.q[y] = mul2(make_float2(w[y].y, w[y].x), make_float2(-m.s[y], m.s[y]));
+        } else {
+            m.p[y] = w[y];
+        }
     }
-    const bool low = col - rot0 < half;
-    const int partner = !rotate ? lane : low ? lane + rd / 16 : lane - rd / 16;
-    const int skip = rotate ? max(rot0 - col, 0) / 2 : 4;      // pairs of the lane before the rotated ones
-    const float sign = low ? -1.0f : 1.0f;
-    if (weight) {
-        float2 w[4];
-        if (in_row) unpack4(*reinterpret_cast<const uint4*>(weight + col), w);
-        work_rows<kTo, kRope, true>(q, p.per, L, w, inv_d, h.eps, c, s, rotate, skip, sign, partner, scale_lane);
-    } else {
-        work_rows<kTo, kRope, false>(q, p.per, L, nullptr, inv_d, h.eps, c, s, rotate, skip, sign, partner, scale_lane);
-    }
+    work_rows<kTo, kRope, true, kWhole>(q, p.per, m);
 }
 
 template <int kTo>
@@ -325,9 +367,11 @@ cudaError_t run_heads(HeadsParams& p, int num_sms, cudaStream_t stream)
     const int64_t blocks = (p.h.tokens * p.units + kHeadWarps - 1) / kHeadWarps;
     if (blocks * kHeadWarps > 0x7fffffff) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)blocks), block(kHeadThreads);
-    if (!p.h.pos) return launch_programmatic(heads_kernel<kTo, kNoRope>, grid, block, 0, stream, p);
-    return p.h.halves ? launch_programmatic(heads_kernel<kTo, kHalves>, grid, block, 0, stream, p)
-                      : launch_programmatic(heads_kernel<kTo, kPairs>, grid, block, 0, stream, p);
+    const bool rope = p.h.pos, whole = p.h.head_dim == 128 && (!rope || p.h.rope_dim == 128);
+    auto go = [&](void (*kernel)(HeadsParams)) { return launch_programmatic(kernel, grid, block, 0, stream, p); };
+    if (!rope) return whole ? go(heads_kernel<kTo, kNoRope, true>) : go(heads_kernel<kTo, kNoRope, false>);
+    if (p.h.halves) return whole ? go(heads_kernel<kTo, kHalves, true>) : go(heads_kernel<kTo, kHalves, false>);
+    return whole ? go(heads_kernel<kTo, kPairs, true>) : go(heads_kernel<kTo, kPairs, false>);
 }
 
 // ----------------------------------------------------------------- expand
