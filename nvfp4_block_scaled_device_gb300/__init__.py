@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from dataclasses import dataclass
 
@@ -82,7 +83,11 @@ class _HeadsC(ctypes.Structure):
                 ("sin_t", ctypes.c_void_p), ("table_ld", ctypes.c_int64), ("positions", ctypes.c_int64),
                 ("rope_dim", ctypes.c_int64), ("halves", ctypes.c_int32), ("slot", ctypes.c_void_p),
                 ("v", ctypes.c_void_p), ("ldv", ctypes.c_int64), ("hv", ctypes.c_int64),
-                ("cache", ctypes.POINTER(_CacheC)), ("cache4", ctypes.POINTER(_Cache4C))]
+                ("cache", ctypes.c_void_p), ("cache4", ctypes.c_void_p)]
+
+
+# The same bytes for less than making the structure (0.3 us, 1.5).
+_pack_heads = struct.Struct("@4q" + 4 * "Pqq" + "PPfPPPqqqiPPqqPP").pack
 
 
 class _PagesC(ctypes.Structure):
@@ -152,7 +157,7 @@ _SIGS = {
                                          ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "nvfp4_attn_paged": (ctypes.c_int, [ctypes.POINTER(_StepC), ctypes.POINTER(_AttnIOC), ctypes.POINTER(_CacheC),
                                         ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
-    "nvfp4_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(_HeadsC), ctypes.c_void_p]),
+    "nvfp4_qk_norm_rope": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "nvfp4_kv4_append": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                         ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
                                         ctypes.POINTER(_Cache4C), ctypes.c_void_p]),
@@ -455,6 +460,7 @@ class KVCache:
         page = self.kv_heads * self.page_size * self.head_dim
         self._c = _CacheC(k.data_ptr(), v.data_ptr(), self.pages, self.page_size, self.kv_heads, self.head_dim,
                           k.stride(0) if self.pages > 1 else page)
+        self._planes = [_PlaneC(t.data_ptr(), 2 * page, 2 * self._c.page_stride) for t in (k, v)]
 
     @staticmethod
     def empty(pages: int, kv_heads: int, page_size: int, head_dim: int, device=None) -> "KVCache":
@@ -575,12 +581,32 @@ def nvfp4_attn_paged(q: torch.Tensor, cache: KVCache, plan: AttnPlan, out: torch
 
 # ------------------------------- heads, the 4-bit cache, pages of a cache
 # (These calls refuse tensors that are not on the current device, whose stream
-# and library state they would use.)
-def _on_device(name: str, *tensors):
-    here = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != here):
-            raise ValueError(f"{name}: every tensor must be on the current CUDA device, not {t.device}")
+# and library state they would use: get_device() is -1 on the CPU.)
+_here, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_F32 = torch.float32
+
+
+def _elsewhere(name: str, t: torch.Tensor):
+    raise ValueError(f"{name} must be on the current CUDA device, not on {t.device}")
+
+
+def _stream_of(stream, here: int):
+    return _raw_stream(here) if stream is None else stream.cuda_stream
+
+
+def _rows_of(x: torch.Tensor, name: str, shape, here: int):
+    """(address, row pitch, head pitch) of bf16 rows [tokens, heads, head_dim]."""
+    st = x.stride()
+    if x.dtype is not _BF16 or x.shape != shape or st[2] != 1 or x.get_device() != here:
+        raise ValueError(f"{name} must be a bf16 {list(shape)} tensor on the current CUDA device with unit column stride, "
+                         f"not {x.dtype} {tuple(x.shape)} on {x.device}")
+    return x.data_ptr(), st[0], st[1]
+
+
+def _ints_of(t, n: int, name: str, here: int):
+    if t.dtype is not _I32 or t.get_device() != here or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of at least {n} elements on the current CUDA device")
+    return t.data_ptr()
 
 
 class KVCache4:
@@ -612,6 +638,7 @@ class KVCache4:
         self._c = _Cache4C(k.data_ptr(), v.data_ptr(), k_sf.data_ptr(), v_sf.data_ptr(), k_g.data_ptr(),
                            v_g.data_ptr(), self.pages, self.page_size, self.kv_heads, self.head_dim, stride(k),
                            stride(k_sf))
+        self._planes = [_PlaneC(t.data_ptr(), t.shape[1] * t.shape[2] * t.shape[3], stride(t)) for t in (k, v, k_sf, v_sf)]
 
     @staticmethod
     def empty(pages: int, kv_heads: int, page_size: int, head_dim: int, k_g=2.0 ** -6, v_g=2.0 ** -6,
@@ -644,71 +671,89 @@ def nvfp4_qk_norm_rope(q, k, q_norm=None, k_norm=None, pos=None, cos_t=None, sin
 
     With v, plan and cache (KVCache or KVCache4) the rows of k, and those of v,
     go into the cache's slots plan.slot instead (and to k_out where it is given)."""
-    ref = q if q is not None else k
+    ref = k if q is None else q
     if ref is None:
         raise ValueError("q or k")
-    tokens, D = ref.shape[0], ref.shape[2]
+    if ref.dim() != 3:
+        raise ValueError("q and k must be [tokens, heads, head_dim]")
+    tokens, _, D = ref.shape
+    here = ref.get_device()
+    if here < 0 or here != _here():
+        _elsewhere("q and k", ref)
     if (cache is None) != (v is None) or (cache is None) != (plan is None):
         raise ValueError("v, plan and cache go together")
-    h = _HeadsC(tokens=tokens, head_dim=D, eps=eps)
+    heads = kv_heads = slot = at = at4 = 0
+    qp = qo = kp = ko = vp = (0, 0, 0)
     if q is not None:
-        h.heads = q.shape[1]
-        h.q, h.ldq, h.hq = _heads_3d(q, "q", tokens, h.heads, D)
-        h.q_out, h.ldqo, h.hqo = (h.q, h.ldq, h.hq) if q_out is None else _heads_3d(q_out, "q_out", tokens, h.heads, D)
+        heads = q.shape[1]
+        shape = (tokens, heads, D)
+        qp = qo = _rows_of(q, "q", shape, here)
+        if q_out is not None:
+            qo = _rows_of(q_out, "q_out", shape, here)
     if k is not None:
-        h.kv_heads = k.shape[1]
-        h.k, h.ldk, h.hk = _heads_3d(k, "k", tokens, h.kv_heads, D)
+        kv_heads = k.shape[1]
+        shape = (tokens, kv_heads, D)
+        kp = _rows_of(k, "k", shape, here)
         if k_out is not None:
-            h.k_out, h.ldko, h.hko = _heads_3d(k_out, "k_out", tokens, h.kv_heads, D)
+            ko = _rows_of(k_out, "k_out", shape, here)
         elif cache is None:
-            h.k_out, h.ldko, h.hko = h.k, h.ldk, h.hk
+            ko = kp
     for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if w is not None:
-            if w.dtype is not _BF16 or w.numel() != D or not w.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous bf16 [{D}] tensor")
-            setattr(h, name, w.data_ptr())
+        if w is not None and (w.dtype is not _BF16 or w.numel() != D or not w.is_contiguous() or w.get_device() != here):
+            raise ValueError(f"{name} must be a contiguous bf16 [{D}] tensor on the current CUDA device")
+    ld = rows = 0
+    p = c = s = 0
     if pos is not None:
-        if cos_t is None or sin_t is None or cos_t.dtype is not torch.float32 or sin_t.dtype is not torch.float32 or \
-                cos_t.dim() != 2 or cos_t.shape != sin_t.shape or cos_t.stride(1) != 1 or sin_t.stride() != cos_t.stride():
-            raise ValueError("cos_t and sin_t must be row-major float32 2-D tensors of one shape")
-        h.pos, h.cos_t, h.sin_t = _i32(pos, tokens, "pos"), cos_t.data_ptr(), sin_t.data_ptr()
-        h.positions, h.table_ld = cos_t.shape[0], max(cos_t.stride(0), cos_t.shape[1])
-        h.rope_dim, h.halves = 2 * cos_t.shape[1] if rope_dim is None else rope_dim, 1 if halves else 0
-        if h.rope_dim > 2 * cos_t.shape[1]:
+        if cos_t is None or sin_t is None or cos_t.dtype is not _F32 or sin_t.dtype is not _F32 or cos_t.dim() != 2 or \
+                cos_t.shape != sin_t.shape or cos_t.stride() != sin_t.stride() or cos_t.stride(1) != 1 or \
+                cos_t.get_device() != here or sin_t.get_device() != here:
+            raise ValueError("cos_t and sin_t must be row-major float32 2-D tensors of one shape on the current CUDA device")
+        rows, width = cos_t.shape
+        p, c, s, ld = _ints_of(pos, tokens, "pos", here), cos_t.data_ptr(), sin_t.data_ptr(), max(cos_t.stride(0), width)
+        if rope_dim is None:
+            rope_dim = 2 * width
+        elif rope_dim > 2 * width:
             raise ValueError("the tables are narrower than half of rope_dim")
     if cache is not None:
         _cache_fits(plan, cache)
         if k is None or plan.tokens != tokens:
             raise ValueError("a cache takes the rows of k and v of all of the plan's tokens")
-        h.slot = plan.slot.data_ptr()
-        h.v, h.ldv, h.hv = _heads_3d(v, "v", tokens, h.kv_heads, D)
+        if cache.k.get_device() != here or plan.slot.get_device() != here:
+            _elsewhere("cache and plan", cache.k)
+        slot = plan.slot.data_ptr()
+        vp = _rows_of(v, "v", shape, here)
         if isinstance(cache, KVCache4):
-            h.cache4 = ctypes.pointer(cache._c)
+            at4 = ctypes.addressof(cache._c)
         else:
-            h.cache = ctypes.pointer(cache._c)
-        _on_device("nvfp4_qk_norm_rope", cache.k, plan.slot)
-    _on_device("nvfp4_qk_norm_rope", q, k, v, q_out, k_out, q_norm, k_norm, pos, cos_t, sin_t)
-    _check((_lib or lib()).nvfp4_qk_norm_rope(ctypes.byref(h), _stream(stream)), "nvfp4_qk_norm_rope")
+            at = ctypes.addressof(cache._c)
+    h = _pack_heads(tokens, heads, kv_heads, D, *qp, *qo, *kp, *ko, 0 if q_norm is None else q_norm.data_ptr(),
+                    0 if k_norm is None else k_norm.data_ptr(), eps, p, c, s, ld, rows, rope_dim or 0, 1 if halves else 0,
+                    slot, *vp, at, at4)
+    _check((_lib or lib()).nvfp4_qk_norm_rope(h, _stream_of(stream, here)), "nvfp4_qk_norm_rope")
 
 
 def nvfp4_kv4_append(k: torch.Tensor, v: torch.Tensor, plan: AttnPlan, cache: KVCache4, stream=None):
     """k, v: bf16 [tokens, kv_heads, head_dim] (any row and head pitch) into the
     4-bit cache's slots plan.slot."""
     _cache_fits(plan, cache)
-    kp = _heads_3d(k, "k", plan.tokens, cache.kv_heads, cache.head_dim)
-    vp = _heads_3d(v, "v", plan.tokens, cache.kv_heads, cache.head_dim)
-    _on_device("nvfp4_kv4_append", k, v, plan.slot, cache.k)
-    _check((_lib or lib()).nvfp4_kv4_append(*kp, *vp, plan.slot.data_ptr(), plan.tokens, ctypes.byref(cache._c),
-                                            _stream(stream)), "nvfp4_kv4_append")
+    here = cache.k.get_device()
+    if here != _here() or plan.slot.get_device() != here:
+        _elsewhere("cache and plan", cache.k)
+    shape = (plan.tokens, cache.kv_heads, cache.head_dim)
+    _check((_lib or lib()).nvfp4_kv4_append(*_rows_of(k, "k", shape, here), *_rows_of(v, "v", shape, here),
+                                            plan.slot.data_ptr(), plan.tokens, ctypes.byref(cache._c),
+                                            _stream_of(stream, here)), "nvfp4_kv4_append")
 
 
 def nvfp4_kv4_expand(cache: KVCache4, plan: AttnPlan, out: KVCache, stream=None):
     """The rows of the cache that the step's new tokens see, as bf16 in the same
     pages of out (a KVCache of the same sizes)."""
     _cache_fits(plan, cache)
-    _on_device("nvfp4_kv4_expand", cache.k, plan.kv_len, out.k)
+    here = cache.k.get_device()
+    if here != _here() or plan.slot.get_device() != here or out.k.get_device() != here:
+        _elsewhere("cache, plan and out", cache.k)
     _check((_lib or lib()).nvfp4_kv4_expand(ctypes.byref(cache._c), ctypes.byref(plan._c), ctypes.byref(out._c),
-                                            _stream(stream)), "nvfp4_kv4_expand")
+                                            _stream_of(stream, here)), "nvfp4_kv4_expand")
 
 
 def nvfp4_attn_paged4(q: torch.Tensor, cache: KVCache4, plan: AttnPlan, out: torch.Tensor, ws: torch.Tensor, scale=None,
@@ -716,11 +761,22 @@ def nvfp4_attn_paged4(q: torch.Tensor, cache: KVCache4, plan: AttnPlan, out: tor
     """:func:`nvfp4_attn_paged` over a 4-bit cache.  expanded: a KVCache of the
     same sizes as scratch, which steps with many rows per request (prompts) are
     faster with; one serves all layers that run one after the other."""
-    io = _attn_io(plan, q, out, scale, lse, zero_padding)
-    _on_device("nvfp4_attn_paged4", q, out, lse, ws, cache.k, plan.kv_len, None if expanded is None else expanded.k)
+    here = cache.k.get_device()
+    if here != _here() or plan.kv_len.get_device() != here or ws.get_device() != here or \
+            (expanded is not None and expanded.k.get_device() != here):
+        _elsewhere("cache, plan, ws and expanded", cache.k)
+    tokens, heads, d = plan.tokens, plan.heads, cache.head_dim
+    shape, at = (tokens, heads, d), None
+    if lse is not None:
+        if lse.dtype is not _F32 or lse.get_device() != here or not lse.is_contiguous() or lse.numel() != tokens * heads:
+            raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor on the current CUDA device")
+        at = lse.data_ptr()
+    io = _AttnIOC(*_rows_of(q, "q", shape, here), *_rows_of(out, "out", shape, here), at, d,
+                  d ** -0.5 if scale is None else scale, 1 if zero_padding else 0)
     _check((_lib or lib()).nvfp4_attn_paged4(ctypes.byref(plan._c), ctypes.byref(io), ctypes.byref(cache._c),
                                              None if expanded is None else ctypes.byref(expanded._c), ws.data_ptr(),
-                                             ws.numel() * ws.element_size(), _stream(stream)), "nvfp4_attn_paged4")
+                                             ws.numel() * ws.element_size(), _stream_of(stream, here)),
+           "nvfp4_attn_paged4")
 
 
 class PageTable:
@@ -750,15 +806,18 @@ def nvfp4_pages_fork(table: PageTable, src: torch.Tensor, dst: torch.Tensor, fre
     cursor (int32 [1] or None: 0) on.  (copy_src, copy_dst), int32 [n]: the pages
     for :func:`nvfp4_pages_copy`.  cursor_out: int32 [1] or None, may be cursor."""
     n = src.numel()
-    args = [_i32(src, n, "src"), _i32(dst, n, "dst"), n, _i32(free_pages, 0, "free_pages"), free_pages.numel(),
-            None if cursor is None else _i32(cursor, 1, "cursor"),
-            None if cursor_out is None else _i32(cursor_out, 1, "cursor_out"), _i32(copy_src, n, "copy_src"),
-            _i32(copy_dst, n, "copy_dst")]
+    here = table.block_table.get_device()
+    if here != _here() or table.ctx_len.get_device() != here:
+        _elsewhere("table", table.block_table)
     if dst.numel() != n:
         raise ValueError("as many dst as src")
-    _on_device("nvfp4_pages_fork", table.block_table, table.ctx_len, src, dst, free_pages, cursor, cursor_out, copy_src,
-               copy_dst)
-    _check((_lib or lib()).nvfp4_pages_fork(ctypes.byref(table._c), *args, _stream(stream)), "nvfp4_pages_fork")
+    _check((_lib or lib()).nvfp4_pages_fork(
+        ctypes.byref(table._c), _ints_of(src, n, "src", here), _ints_of(dst, n, "dst", here), n,
+        _ints_of(free_pages, 0, "free_pages", here), free_pages.numel(),
+        None if cursor is None else _ints_of(cursor, 1, "cursor", here),
+        None if cursor_out is None else _ints_of(cursor_out, 1, "cursor_out", here),
+        _ints_of(copy_src, n, "copy_src", here), _ints_of(copy_dst, n, "copy_dst", here), _stream_of(stream, here)),
+        "nvfp4_pages_fork")
 
 
 def nvfp4_pages_free(table: PageTable, free_pages: torch.Tensor, free_count: torch.Tensor, table_out=None, move_src=None,
@@ -770,31 +829,41 @@ def nvfp4_pages_free(table: PageTable, free_pages: torch.Tensor, free_count: tor
     the moves for :func:`nvfp4_pages_copy`."""
     if (table_out is None) != (move_src is None) or (table_out is None) != (move_dst is None):
         raise ValueError("table_out, move_src and move_dst go together")
-    args = [_i32(free_pages, table.pages, "free_pages"), _i32(free_count, 1, "free_count"), None, 0, None, None]
+    here = table.block_table.get_device()
+    if here != _here() or table.ctx_len.get_device() != here:
+        _elsewhere("table", table.block_table)
+    out, ld, ms, md = None, 0, None, None
     if table_out is not None:
         _table(table_out, "table_out", table.block_table.shape)
-        args[2:] = [table_out.data_ptr(), max(table_out.stride(0), table.cols),
-                    _i32(move_src, table.pages // 2, "move_src"), _i32(move_dst, table.pages // 2, "move_dst")]
-    _on_device("nvfp4_pages_free", table.block_table, table.ctx_len, free_pages, free_count, table_out, move_src, move_dst)
-    _check((_lib or lib()).nvfp4_pages_free(ctypes.byref(table._c), *args, _stream(stream)), "nvfp4_pages_free")
+        if table_out.get_device() != here:
+            _elsewhere("table_out", table_out)
+        out, ld = table_out.data_ptr(), max(table_out.stride(0), table.cols)
+        ms, md = _ints_of(move_src, table.pages // 2, "move_src", here), _ints_of(move_dst, table.pages // 2, "move_dst", here)
+    _check((_lib or lib()).nvfp4_pages_free(ctypes.byref(table._c), _ints_of(free_pages, table.pages, "free_pages", here),
+                                            _ints_of(free_count, 1, "free_count", here), out, ld, ms, md,
+                                            _stream_of(stream, here)), "nvfp4_pages_free")
 
 
 def nvfp4_pages_copy(caches, src: torch.Tensor, dst: torch.Tensor, stream=None):
     """Page src[i] to page dst[i] (int32 [n]; pairs of -1 are skipped) in every
     one of caches (KVCache, KVCache4; one or a list, all of as many pages)."""
-    caches = list(caches) if isinstance(caches, (list, tuple)) else [caches]
-    n = src.numel()
-    if not caches or any(c.pages != caches[0].pages for c in caches):
-        raise ValueError("caches of one number of pages")
-    if dst.numel() != n:
-        raise ValueError("as many dst as src")
+    if not isinstance(caches, (list, tuple)):
+        caches = (caches,)
+    if not caches:
+        raise ValueError("no caches")
+    n, pages = src.numel(), caches[0].pages
+    here = caches[0].k.get_device()
     planes = []
     for c in caches:
-        _on_device("nvfp4_pages_copy", c.k, src, dst)
-        for t in ((c.k, c.v, c.k_sf, c.v_sf) if isinstance(c, KVCache4) else (c.k, c.v)):
-            size = t.element_size()
-            page = t.shape[1] * t.shape[2] * t.shape[3] * size
-            planes.append(_PlaneC(t.data_ptr(), page, t.stride(0) * size if c.pages > 1 else page))
-    _check((_lib or lib()).nvfp4_pages_copy((_PlaneC * len(planes))(*planes), len(planes), caches[0].pages,
-                                            _i32(src, n, "src"), _i32(dst, n, "dst"), n, _stream(stream)),
-           "nvfp4_pages_copy")
+        if c.pages != pages:
+            raise ValueError("caches of one number of pages")
+        if c.k.get_device() != here:
+            _elsewhere("every cache", c.k)
+        planes += c._planes
+    if here != _here():
+        _elsewhere("every cache", caches[0].k)
+    if dst.numel() != n:
+        raise ValueError("as many dst as src")
+    _check((_lib or lib()).nvfp4_pages_copy((_PlaneC * len(planes))(*planes), len(planes), pages,
+                                            _ints_of(src, n, "src", here), _ints_of(dst, n, "dst", here), n,
+                                            _stream_of(stream, here)), "nvfp4_pages_copy")

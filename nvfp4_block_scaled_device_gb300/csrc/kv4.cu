@@ -35,10 +35,10 @@ int log2_of(int64_t v)
 // Bound by HBM with many tokens (2 B in, 2 B out a column); with few by the
 // launch and one dependent chain of loads, so the rows of a token are spread
 // over as many warps as there is room for.
-constexpr int kHeadThreads = 256;
+constexpr int kHeadThreads = 128;
 constexpr int kHeadWarps = kHeadThreads / 32;
 constexpr int kHeadBatch = 4;          // rows of a lane loaded before the first is worked on
-constexpr int kHeadBlocks = 4;
+constexpr int kHeadBlocks = 8;             // of an SM
 
 enum { kToRows = 0, kToCache = 1, kToCache4 = 2 };
 enum { kNoRope = 0, kPairs = 1, kHalves = 2 };
@@ -239,7 +239,7 @@ __device__ __forceinline__ void work_rows(HeadRows& q, int batches, const HeadMa
 }
 
 template <int kTo, int kRope, bool kWhole>
-__global__ void __launch_bounds__(kHeadThreads, kTo == kToCache4 ? 2 : kHeadBlocks) heads_kernel(const __grid_constant__ HeadsParams p)
+__global__ void __launch_bounds__(kHeadThreads, kHeadBlocks) heads_kernel(const __grid_constant__ HeadsParams p)
 {
     griddep_launch_dependents();
     griddep_wait();

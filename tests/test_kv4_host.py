@@ -39,7 +39,7 @@ def test_cache4_refusals(nv, bad, status):
     L, c = nv.lib(), cache4(nv, **bad)
     assert L.nvfp4_kv4_append(A, 256, 128, A, 256, 128, A, 64, ctypes.byref(c), None) == status
     assert L.nvfp4_kv4_expand(ctypes.byref(c), step(nv), cache(nv), None) == status
-    assert L.nvfp4_qk_norm_rope(heads(nv, slot=A, v=A, ldv=256, hv=128, cache4=ctypes.pointer(c)), None) == status
+    assert L.nvfp4_qk_norm_rope(heads(nv, slot=A, v=A, ldv=256, hv=128, cache4=ctypes.addressof(c)), None) == status
 
 
 def test_append4_and_expand_refusals(nv):
@@ -78,16 +78,16 @@ def test_heads_refusals(nv, bad, status):
 
 def test_heads_refuse_caches_that_do_not_fit(nv):
     L = nv.lib()
-    c, c4 = cache(nv)._obj, cache4(nv)
+    c, c4, none = cache(nv)._obj, cache4(nv), cache(nv, pages=0)._obj
     ok = dict(slot=A, v=A, ldv=256, hv=128)
     assert L.nvfp4_qk_norm_rope(None, None) == INVALID
-    for bad in (dict(), dict(cache=ctypes.pointer(c), cache4=ctypes.pointer(c4)),
-                dict(cache=ctypes.pointer(c), v=None), dict(cache=ctypes.pointer(c), kv_heads=1),
-                dict(cache=ctypes.pointer(c), kv_heads=0), dict(cache4=ctypes.pointer(c4), head_dim=64, rope_dim=64),
-                dict(cache=ctypes.pointer(cache(nv, pages=0)._obj))):
+    for bad in (dict(), dict(cache=ctypes.addressof(c), cache4=ctypes.addressof(c4)),
+                dict(cache=ctypes.addressof(c), v=None), dict(cache=ctypes.addressof(c), kv_heads=1),
+                dict(cache=ctypes.addressof(c), kv_heads=0), dict(cache4=ctypes.addressof(c4), head_dim=64, rope_dim=64),
+                dict(cache=ctypes.addressof(none))):
         assert L.nvfp4_qk_norm_rope(heads(nv, **{**ok, **bad}), None) == INVALID, bad
     for bad in (dict(slot=A + 2), dict(v=A + 8), dict(ldv=260)):
-        assert L.nvfp4_qk_norm_rope(heads(nv, **{**ok, "cache": ctypes.pointer(c), **bad}), None) == MISALIGNED, bad
+        assert L.nvfp4_qk_norm_rope(heads(nv, **{**ok, "cache": ctypes.addressof(c), **bad}), None) == MISALIGNED, bad
 
 
 # ------------------------------------------------------------------- pages
@@ -185,3 +185,8 @@ def test_attention_refusals(nv):
     assert L.nvfp4_attn_paged4(step(nv), io(nv), None, None, A, 1 << 40, None) == INVALID
     for ws, n, status in ((None, 1 << 40, WORKSPACE), (A, 16, WORKSPACE), (A + 128, 1 << 40, MISALIGNED)):
         assert L.nvfp4_attn_paged4(step(nv), io(nv), c, None, ws, n, None) == status
+
+
+def test_heads_as_bytes_are_the_structure(nv):
+    values = (1, 2, 3, 4, *range(5, 17), 17, 18, 1e-6, 19, 20, 21, 22, 23, 24, 1, 25, 26, 27, 28, 29, 30)
+    assert nv._pack_heads(*values) == bytes(nv._HeadsC(*values))
