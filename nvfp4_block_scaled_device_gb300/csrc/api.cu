@@ -1128,7 +1128,7 @@ int nvfp4_pages_fork(const nvfp4_pages_t* pages, const int32_t* src, const int32
     DeviceInfo* d = nullptr;
     NVFP4_TRY(device_info(&d));
     NVFP4_CUDA(launch_pages_fork(*pages, src, dst, n, free_pages, free_count, cursor, cursor_out, copy_src, copy_dst,
-                                 d->status, (cudaStream_t)stream));
+                                 d->status, d->num_sms, (cudaStream_t)stream));
     return NVFP4_OK;
 }
 

@@ -9,8 +9,10 @@ namespace nvfp4 {
 // Device status of the page operators (NVFP4_ERR_INVALID_ARG * 100 + site).
 constexpr int kStatusPages = NVFP4_ERR_INVALID_ARG * 100 + 34;
 
-// Rows of a request, on average, from which a step's keys are expanded once.
-constexpr int64_t kExpandRows = 64;
+// Rows of a request, on average, from which a step's keys are expanded once (40
+// rows: 8 requests of 2000 keys 43.7 us that way and 52.0 straight from the codes, 1
+// of 8000 45.1 and 45.0; 20 rows: 44.8 and 28.2, 52.6 and 24.3).
+constexpr int64_t kExpandRows = 40;
 
 constexpr int64_t kMaxPages = 1 << 20;      // of the page operators (a bit each in shared memory)
 constexpr int kMaxPlanes = 64;              // of one copying launch
@@ -35,7 +37,7 @@ cudaError_t launch_attn4(const AttnArgs& args, const nvfp4_kv4_cache_t& cache, c
 
 cudaError_t launch_pages_fork(const nvfp4_pages_t& t, const int32_t* src, const int32_t* dst, int64_t n,
                               const int32_t* free_pages, int64_t free_count, const int32_t* cursor,
-                              int32_t* cursor_out, int32_t* copy_src, int32_t* copy_dst, int* status,
+                              int32_t* cursor_out, int32_t* copy_src, int32_t* copy_dst, int* status, int num_sms,
                               cudaStream_t stream);
 
 cudaError_t launch_pages_free(const nvfp4_pages_t& t, int32_t* free_pages, int32_t* free_count, int32_t* table_out,

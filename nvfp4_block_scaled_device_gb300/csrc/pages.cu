@@ -8,11 +8,12 @@
 // a sweep, whose result does not depend on what was freed when, or twice.
 //
 // The tables are small next to the cache (4096 requests of 512 pages: 8 MB):
-// the launch and the dependent reads set the time.  Each call is one launch of
-// one cluster of 8 CTAs, so that the steps between which everyone has to wait
-// (all pages marked, all moves known, the cursor read) are cluster barriers
-// instead of launches, and the marks are bits in the CTAs' shared memory
-// instead of a workspace to be kept at zero.
+// the launch and the dependent reads set the time.  The sweep is one launch of one
+// cluster of 16 CTAs, so that the steps between which everyone has to wait (all
+// pages marked, all moves known) are cluster barriers instead of launches, and
+// the marks are bits in the CTAs' shared memory instead of a workspace to be kept
+// at zero.  (400 requests of 255 pages at most, 19569 pages moved together: 8 CTAs
+// 23.0 us, FREE_US with 16.)
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.h"
@@ -22,8 +23,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCluster = 8;
-constexpr int kSegment = 1024;         // entries of a table's row that a warp takes at a time
+constexpr int kCluster = 16;
+constexpr int kSegment = 256;          // entries of a table's row that a warp takes at a time
 constexpr int kGroup = 8;              // words of the bit map per entry of its prefix sum
 
 __device__ __forceinline__ void report(int* status, int code)
@@ -77,14 +78,17 @@ struct ForkParams {
     int32_t* copy_dst;
     int* status;
     int shift;
+    int cursor_only;
 };
 
 // Every CTA looks at all pairs (which of them count, and how many free pages
 // the earlier ones take) in its shared memory: first [R] the first pair with
 // this destination, at [n] the pair's free page (-1: none, -2: the pair does
 // not count), src_bits [R / 32] the requests that are sources.  Then the warps
-// of the cluster write the rows, a segment at a time.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) fork_kernel(const ForkParams p)
+// write the rows, a segment at a time.  No row or length that is read is
+// written.  A cursor that is advanced in place is stored by a launch of its own
+// (cursor_only), as in the plan: the CTAs read it when they start.
+__global__ void __launch_bounds__(kThreads) fork_kernel(const ForkParams p)
 {
     extern __shared__ int32_t sh[];
     __shared__ int s_sums[kWarps];
@@ -134,11 +138,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) for
     }
     __syncthreads();
 
-    const int rank = (int)cluster_ctarank();
-    if (bad && rank == 0) report(p.status, kStatusPages);
+    if (p.cursor_only || (blockIdx.x == 0 && p.cursor_out && p.cursor_out != p.cursor)) {
+        if (t == 0) *p.cursor_out = (int32_t)min(cursor + all, (int64_t)0x7fffffff);
+        if (p.cursor_only) return;
+    }
+    if (bad && blockIdx.x == 0) report(p.status, kStatusPages);
     const int segments = (int)((cols + kSegment - 1) / kSegment);
     const int64_t units = (int64_t)n * segments;
-    for (int64_t u = rank * kWarps + (t >> 5); u < units; u += kCluster * kWarps) {
+    for (int64_t u = (int64_t)blockIdx.x * kWarps + (t >> 5); u < units; u += (int64_t)gridDim.x * kWarps) {
         const int i = (int)(u / segments), seg = (int)(u - (int64_t)i * segments);
         const int page = at[i];
         if (page == -2) {
@@ -151,7 +158,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) for
         const int32_t* from = p.t.block_table + s * ld;
         int32_t* to = p.t.block_table + d * ld;
         const int j1 = (int)min(cols, (int64_t)(seg + 1) * kSegment);
-#pragma unroll 4
+#pragma unroll 8
         for (int j = seg * kSegment + lane; j < j1; j += 32) {
             const int32_t e = j < need ? from[j] : -1;
             to[j] = j == last ? max(page, -1) : e;
@@ -162,8 +169,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) for
             p.t.ctx_len[d] = ctx;
         }
     }
-    cluster_sync_all();                // every CTA has read the cursor: it may be advanced in place
-    if (rank == 0 && t == 0 && p.cursor_out) *p.cursor_out = (int32_t)min(cursor + all, (int64_t)0x7fffffff);
 }
 
 // ------------------------------------------------------------------- free
@@ -211,11 +216,21 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) fre
     for (int w = t; w < W; w += kThreads) bits[w] = 0;
     __syncthreads();
     bool bad = false;
-    for (int64_t u = unit0; u < units; u += kCluster * kWarps) {
+    // (a warp's next units' lengths are read 32 at a time)
+    constexpr int kStep = kCluster * kWarps;
+    int held = 0;
+    auto held_of = [&](int64_t u, int i) {
+        if ((i & 31) == 0) {
+            const int64_t mine = u + (int64_t)lane * kStep;
+            held = mine < units ? held_entries(p.t.ctx_len[mine / segments], p.shift, cols, &bad) : 0;
+        }
+        return __shfl_sync(0xffffffffu, held, i & 31);
+    };
+    for (int64_t u = unit0, i = 0; u < units; u += kStep, i++) {
         const int r = (int)(u / segments), seg = (int)(u - (int64_t)r * segments);
-        const int j1 = min(held_entries(p.t.ctx_len[r], p.shift, cols, &bad), (seg + 1) * kSegment);
+        const int j1 = min(held_of(u, (int)i), (seg + 1) * kSegment);
         const int32_t* row = p.t.block_table + r * ld;
-#pragma unroll 4
+#pragma unroll 8
         for (int j = seg * kSegment + lane; j < j1; j += 32) {
             const int32_t e = row[j];
             if (e >= 0 && e < pages) atomicOr(&bits[e >> 5], 1u << (e & 31));
@@ -278,13 +293,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) fre
     for (int i = moves + rank * kThreads + t; i < pages / 2; i += kCluster * kThreads) p.move_src[i] = p.move_dst[i] = -1;
     __threadfence();
     cluster_sync_all();                // the moves are known (and every entry has been read)
-    for (int64_t u = unit0; u < units; u += kCluster * kWarps) {
+    for (int64_t u = unit0, i = 0; u < units; u += kStep, i++) {
         const int r = (int)(u / segments), seg = (int)(u - (int64_t)r * segments);
-        const int need = held_entries(p.t.ctx_len[r], p.shift, cols, &bad);
+        const int need = held_of(u, (int)i);
         const int32_t* row = p.t.block_table + r * ld;
         int32_t* out = p.table_out + r * p.table_out_ld;
         const int j1 = (int)min(cols, (int64_t)(seg + 1) * kSegment);
-#pragma unroll 4
+#pragma unroll 8
         for (int j = seg * kSegment + lane; j < j1; j += 32) {
             int32_t e = -1;
             if (j < need) {
@@ -367,26 +382,37 @@ cudaError_t allow_smem(K kernel, int bytes, int (&done)[64])
 
 cudaError_t launch_pages_fork(const nvfp4_pages_t& t, const int32_t* src, const int32_t* dst, int64_t n,
                               const int32_t* free_pages, int64_t free_count, const int32_t* cursor,
-                              int32_t* cursor_out, int32_t* copy_src, int32_t* copy_dst, int* status,
+                              int32_t* cursor_out, int32_t* copy_src, int32_t* copy_dst, int* status, int num_sms,
                               cudaStream_t stream)
 {
     static int done[64] = {0};
     constexpr int kMost = (int)(2 * kStepMaxRequests + kStepMaxRequests / 32) * 4;
     cudaError_t e = allow_smem(fork_kernel, kMost, done);
     if (e != cudaSuccess) return e;
-    const ForkParams p = {t, src, dst, (int)n, free_pages, free_pages ? free_count : 0, cursor, cursor_out,
-                          copy_src, copy_dst, status, log2_of(t.page_size)};
-    return launch_programmatic(fork_kernel, dim3(kCluster), dim3(kThreads),
-                               (size_t)(t.requests + n + (t.requests + 31) / 32) * 4, stream, p);
+    ForkParams p = {t, src, dst, (int)n, free_pages, free_pages ? free_count : 0, cursor, cursor_out,
+                    copy_src, copy_dst, status, log2_of(t.page_size), 0};
+    const size_t smem = (size_t)(t.requests + n + (t.requests + 31) / 32) * 4;
+    const int64_t units = n * ((t.table_cols + kSegment - 1) / kSegment), want = (units + kWarps - 1) / kWarps;
+    const unsigned grid = (unsigned)(want < 1 ? 1 : want < num_sms ? want : num_sms);
+    e = launch_programmatic(fork_kernel, dim3(grid), dim3(kThreads), smem, stream, p);
+    if (e != cudaSuccess || !cursor_out || cursor_out != cursor) return e;
+    p.cursor_only = 1;
+    return launch_programmatic(fork_kernel, dim3(1), dim3(kThreads), smem, stream, p);
 }
 
 cudaError_t launch_pages_free(const nvfp4_pages_t& t, int32_t* free_pages, int32_t* free_count, int32_t* table_out,
                               int64_t table_out_ld, int32_t* move_src, int32_t* move_dst, int* status,
                               cudaStream_t stream)
 {
-    static int done[64] = {0};
+    static int done[64] = {0}, wide[64] = {0};
     constexpr int kMost = (int)(kMaxPages / 32 + kMaxPages / 32 / kGroup) * 4;
     cudaError_t e = allow_smem(free_kernel, kMost, done);
+    int dev = 0;
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= 64 || !wide[dev])) {
+        e = cudaFuncSetAttribute(free_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);    // more than 8 CTAs
+        if (e == cudaSuccess && dev < 64) wide[dev] = 1;
+    }
     if (e != cudaSuccess) return e;
     FreeParams p = {t, free_pages, free_count, table_out, table_out_ld, move_src, move_dst, status,
                     log2_of(t.page_size), 0, 0};

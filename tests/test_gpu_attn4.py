@@ -105,7 +105,7 @@ def test_heads(nv, ws, H, Hkv, D):
                                        ([1000], [64]), ([333, 0, 10], [1, 90, 1]), ([0], [1])])
 @pytest.mark.parametrize("H,Hkv,D,page", [(10, 2, 128, 16), (3, 3, 64, 128), (24, 2, 96, 64)])
 def test_several_tokens(nv, ws, ctx, q_len, H, Hkv, D, page, expanded):
-    few = sum(q_len) / len(q_len) * (H // Hkv) < 64           # (few rows do not go through the bf16 pages)
+    few = sum(q_len) / len(q_len) * (H // Hkv) < 40           # (few rows do not go through the bf16 pages)
     if expanded and few:
         pytest.skip("the same call")
     run(nv, ws, ctx, q_len, H, Hkv, D, page, expanded=expanded)
