@@ -640,7 +640,7 @@ int nvfp4_kv4_expand(const nvfp4_kv4_cache_t* cache, const nvfp4_step_t* step, c
  * takes as they are stored (in half precision, which holds code times scale
  * exactly; *k_g and *v_g multiply the scores and the outputs).  q counts with
  * at least 11 bits beside the largest of its row, the probabilities are rounded
- * to half precision (2^-11).
+ * to half precision (2^-11; one below 2^-20 of its row's largest by 2^-31 of that).
  *   expanded  NULL, or a bf16 cache of the same pages, page_size, kv_heads and
  *            head_dim as scratch: a step with many rows per request then takes
  *            its keys' rows out of the 4 bits once (into their pages there, bf16

@@ -25,18 +25,22 @@ def ws(nv):
     return nv.workspace(nv.attn_workspace_bytes())
 
 
-# |out - ref| <= 2^-8 |ref| (the output's rounding to bf16, half a step) + p sum_j p_j |v_j|
-# with p = 2^-11 + 2^-11: a probability's rounding to half precision (half a step; those
-# below 2^-20 of the largest are off by 2^-31 of it at most, 1e4 of them by less than
-# 2^-17), and the binary32 scores, whose errors stay below 2^-15 as in _attn.py (code
-# times scale is exact; q's bits too, down to 2^-28 of its row's largest).  Through the
+# |out - ref| <= 2^-8 |ref| (the output's rounding to bf16, half a step)
+#             + p sum_j p_j |v_j| + 2^-31 sum_j |v_j|
+# with p = 2^-11 + 2^-11: a probability's rounding to half precision (half a step),
+# and the binary32 scores, whose errors stay below 2^-15 as in _attn.py (code times
+# scale is exact; q's bits too, down to 2^-28 of its row's largest).  Probabilities
+# are carried 2^6 above the largest, so one below 2^-20 of it lies among half
+# precision's subnormals, 2^-24 apart: off by 2^-25 / 2^6 = 2^-31 of the largest at
+# most, and the sum that they are divided by is no smaller than that.  Through the
 # bf16 pages p is OUT_P, that kernel's.
 P_HALF = 2.0 ** -11 + 2.0 ** -11
 
 
-def check(out, lse, ref, mag, ref_lse, p, what=""):
+def check(out, lse, ref, mag, ref_lse, p, vals, what=""):
     err = (out.double() - ref).abs()
-    bad = ~(err <= 2.0 ** -8 * ref.abs() + p * mag + 1e-30)
+    tiny = 2.0 ** -31 * vals.abs().sum(0).max() if len(vals) else 0.0
+    bad = ~(err <= 2.0 ** -8 * ref.abs() + p * mag + tiny + 1e-30)
     assert not bad.any(), (what, int(bad.sum()), bad.nonzero()[0].tolist(), out[tuple(bad.nonzero()[0])].item(),
                            ref[tuple(bad.nonzero()[0])].item())
     if lse is not None:
@@ -82,7 +86,8 @@ def run(nv, ws, ctx, q_len, H, Hkv, D, page, window=0, layout="plain", pad=0, sc
             pg, row = plan.block_table[r].long()[pos // page], pos % page
             keys, vals = (x[pg, :, row].nan_to_num() for x in (k, v))     # (the rows that are NaN are not seen)
             ref = reference(q[at:at + n].double(), keys, vals, c, D ** -0.5 if scale is None else scale, window)
-            check(out[at:at + n], lse[at:at + n], *ref, OUT_P if expanded else P_HALF, f"request {r}: {n} behind {c}")
+            check(out[at:at + n], lse[at:at + n], *ref, OUT_P if expanded else P_HALF, vals,
+                  f"request {r}: {n} behind {c}")
         at += n
     assert (out[at:] == 7.0).all() and (lse[at:] == 7.0).all()
     return out, lse
@@ -184,7 +189,7 @@ def test_rising_scores(nv, ws):
         nv.nvfp4_attn_paged4(q, cache, plan, out, ws, lse=lse)
         k, v = values(cache)
         pg, row = plan.block_table[0].long()[at // 16], at % 16
-        check(out, lse, *reference(q.double(), k[pg, :, row], v[pg, :, row], L - 1, D ** -0.5), P_HALF)
+        check(out, lse, *reference(q.double(), k[pg, :, row], v[pg, :, row], L - 1, D ** -0.5), P_HALF, v[pg, :, row])
 
 
 def test_page_ids_outside_the_cache_are_pages_of_zeros(nv, ws):
@@ -202,7 +207,7 @@ def test_page_ids_outside_the_cache_are_pages_of_zeros(nv, ws):
     ok = ((ids >= 0) & (ids < 10))[:, None, None]
     keys, vals = (torch.where(ok, x[ids.clamp(0, 9), :, at % page], 0.0) for x in (k, v))
     ref = reference(q.double(), keys, vals, ctx, D ** -0.5)
-    check(out, None, *ref, P_HALF)
+    check(out, None, *ref, P_HALF, vals)
 
 
 @pytest.mark.parametrize("window", [0, 20])
@@ -223,7 +228,7 @@ def test_rows_past_the_tables_columns(nv, ws, window):
         at = torch.arange(64, device="cuda")
         keys, vals = (x[at // page, :, at % page] for x in (k, v))
         ref = reference(q.double(), keys, vals, ctx, D ** -0.5, window)
-        check(out, lse, *ref, P_HALF)
+        check(out, lse, *ref, P_HALF, vals)
         if window and ctx == 200:
             assert (out == 0).all() and (lse == -float("inf")).all()
 
