@@ -86,7 +86,9 @@ class _HeadsC(ctypes.Structure):
                 ("cache", ctypes.c_void_p), ("cache4", ctypes.c_void_p)]
 
 
-# The same bytes for less than making the structure (0.3 us, 1.5).
+# The bytes of a structure for less than making it (nvfp4_heads_t 0.3 us, 1.5).
+_pack_io = struct.Struct("@PqqPqqPqfi").pack
+_pack_plane = struct.Struct("@Pqq").pack
 _pack_heads = struct.Struct("@4q" + 4 * "Pqq" + "PPfPPPqqqiPPqqPP").pack
 
 
@@ -163,14 +165,14 @@ _SIGS = {
                                         ctypes.POINTER(_Cache4C), ctypes.c_void_p]),
     "nvfp4_kv4_expand": (ctypes.c_int, [ctypes.POINTER(_Cache4C), ctypes.POINTER(_StepC), ctypes.POINTER(_CacheC),
                                         ctypes.c_void_p]),
-    "nvfp4_attn_paged4": (ctypes.c_int, [ctypes.POINTER(_StepC), ctypes.POINTER(_AttnIOC), ctypes.POINTER(_Cache4C),
+    "nvfp4_attn_paged4": (ctypes.c_int, [ctypes.POINTER(_StepC), ctypes.c_void_p, ctypes.POINTER(_Cache4C),
                                          ctypes.POINTER(_CacheC), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "nvfp4_pages_fork": (ctypes.c_int, [ctypes.POINTER(_PagesC), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
                                         ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "nvfp4_pages_free": (ctypes.c_int, [ctypes.POINTER(_PagesC), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                         ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
-    "nvfp4_pages_copy": (ctypes.c_int, [ctypes.POINTER(_PlaneC), ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+    "nvfp4_pages_copy": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                         ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
 }
 
@@ -460,7 +462,8 @@ class KVCache:
         page = self.kv_heads * self.page_size * self.head_dim
         self._c = _CacheC(k.data_ptr(), v.data_ptr(), self.pages, self.page_size, self.kv_heads, self.head_dim,
                           k.stride(0) if self.pages > 1 else page)
-        self._planes = [_PlaneC(t.data_ptr(), 2 * page, 2 * self._c.page_stride) for t in (k, v)]
+        self._planes = b"".join(_pack_plane(t.data_ptr(), 2 * page, 2 * self._c.page_stride) for t in (k, v))
+        self._device = k.get_device()
 
     @staticmethod
     def empty(pages: int, kv_heads: int, page_size: int, head_dim: int, device=None) -> "KVCache":
@@ -638,7 +641,11 @@ class KVCache4:
         self._c = _Cache4C(k.data_ptr(), v.data_ptr(), k_sf.data_ptr(), v_sf.data_ptr(), k_g.data_ptr(),
                            v_g.data_ptr(), self.pages, self.page_size, self.kv_heads, self.head_dim, stride(k),
                            stride(k_sf))
-        self._planes = [_PlaneC(t.data_ptr(), t.shape[1] * t.shape[2] * t.shape[3], stride(t)) for t in (k, v, k_sf, v_sf)]
+        self._planes = b"".join(_pack_plane(t.data_ptr(), t.shape[1] * t.shape[2] * t.shape[3], stride(t))
+                                for t in (k, v, k_sf, v_sf))
+        self._device = k.get_device()
+        if any(t.get_device() != self._device for t in (v, k_sf, v_sf, k_g, v_g)):
+            raise ValueError("k, v, their scales and k_g, v_g must be on one device")
 
     @staticmethod
     def empty(pages: int, kv_heads: int, page_size: int, head_dim: int, k_g=2.0 ** -6, v_g=2.0 ** -6,
@@ -704,12 +711,14 @@ def nvfp4_qk_norm_rope(q, k, q_norm=None, k_norm=None, pos=None, cos_t=None, sin
     ld = rows = 0
     p = c = s = 0
     if pos is not None:
-        if cos_t is None or sin_t is None or cos_t.dtype is not _F32 or sin_t.dtype is not _F32 or cos_t.dim() != 2 or \
-                cos_t.shape != sin_t.shape or cos_t.stride() != sin_t.stride() or cos_t.stride(1) != 1 or \
-                cos_t.get_device() != here or sin_t.get_device() != here:
+        if cos_t is None or sin_t is None:
+            raise ValueError("a rotation takes cos_t and sin_t")
+        shape, st = cos_t.shape, cos_t.stride()
+        if cos_t.dtype is not _F32 or sin_t.dtype is not _F32 or len(shape) != 2 or shape != sin_t.shape or \
+                st != sin_t.stride() or st[1] != 1 or cos_t.get_device() != here or sin_t.get_device() != here:
             raise ValueError("cos_t and sin_t must be row-major float32 2-D tensors of one shape on the current CUDA device")
-        rows, width = cos_t.shape
-        p, c, s, ld = _ints_of(pos, tokens, "pos", here), cos_t.data_ptr(), sin_t.data_ptr(), max(cos_t.stride(0), width)
+        rows, width = shape
+        p, c, s, ld = _ints_of(pos, tokens, "pos", here), cos_t.data_ptr(), sin_t.data_ptr(), max(st[0], width)
         if rope_dim is None:
             rope_dim = 2 * width
         elif rope_dim > 2 * width:
@@ -718,10 +727,10 @@ def nvfp4_qk_norm_rope(q, k, q_norm=None, k_norm=None, pos=None, cos_t=None, sin
         _cache_fits(plan, cache)
         if k is None or plan.tokens != tokens:
             raise ValueError("a cache takes the rows of k and v of all of the plan's tokens")
-        if cache.k.get_device() != here or plan.slot.get_device() != here:
+        if cache._device != here or plan.slot.get_device() != here:
             _elsewhere("cache and plan", cache.k)
         slot = plan.slot.data_ptr()
-        vp = _rows_of(v, "v", shape, here)
+        vp = _rows_of(v, "v", (tokens, kv_heads, D), here)
         if isinstance(cache, KVCache4):
             at4 = ctypes.addressof(cache._c)
         else:
@@ -736,7 +745,7 @@ def nvfp4_kv4_append(k: torch.Tensor, v: torch.Tensor, plan: AttnPlan, cache: KV
     """k, v: bf16 [tokens, kv_heads, head_dim] (any row and head pitch) into the
     4-bit cache's slots plan.slot."""
     _cache_fits(plan, cache)
-    here = cache.k.get_device()
+    here = cache._device
     if here != _here() or plan.slot.get_device() != here:
         _elsewhere("cache and plan", cache.k)
     shape = (plan.tokens, cache.kv_heads, cache.head_dim)
@@ -749,8 +758,8 @@ def nvfp4_kv4_expand(cache: KVCache4, plan: AttnPlan, out: KVCache, stream=None)
     """The rows of the cache that the step's new tokens see, as bf16 in the same
     pages of out (a KVCache of the same sizes)."""
     _cache_fits(plan, cache)
-    here = cache.k.get_device()
-    if here != _here() or plan.slot.get_device() != here or out.k.get_device() != here:
+    here = cache._device
+    if here != _here() or plan.slot.get_device() != here or out._device != here:
         _elsewhere("cache, plan and out", cache.k)
     _check((_lib or lib()).nvfp4_kv4_expand(ctypes.byref(cache._c), ctypes.byref(plan._c), ctypes.byref(out._c),
                                             _stream_of(stream, here)), "nvfp4_kv4_expand")
@@ -761,19 +770,19 @@ def nvfp4_attn_paged4(q: torch.Tensor, cache: KVCache4, plan: AttnPlan, out: tor
     """:func:`nvfp4_attn_paged` over a 4-bit cache.  expanded: a KVCache of the
     same sizes as scratch, which steps with many rows per request (prompts) are
     faster with; one serves all layers that run one after the other."""
-    here = cache.k.get_device()
+    here = cache._device
     if here != _here() or plan.kv_len.get_device() != here or ws.get_device() != here or \
-            (expanded is not None and expanded.k.get_device() != here):
+            (expanded is not None and expanded._device != here):
         _elsewhere("cache, plan, ws and expanded", cache.k)
     tokens, heads, d = plan.tokens, plan.heads, cache.head_dim
-    shape, at = (tokens, heads, d), None
+    shape, at = (tokens, heads, d), 0
     if lse is not None:
         if lse.dtype is not _F32 or lse.get_device() != here or not lse.is_contiguous() or lse.numel() != tokens * heads:
             raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor on the current CUDA device")
         at = lse.data_ptr()
-    io = _AttnIOC(*_rows_of(q, "q", shape, here), *_rows_of(out, "out", shape, here), at, d,
+    io = _pack_io(*_rows_of(q, "q", shape, here), *_rows_of(out, "out", shape, here), at, d,
                   d ** -0.5 if scale is None else scale, 1 if zero_padding else 0)
-    _check((_lib or lib()).nvfp4_attn_paged4(ctypes.byref(plan._c), ctypes.byref(io), ctypes.byref(cache._c),
+    _check((_lib or lib()).nvfp4_attn_paged4(ctypes.byref(plan._c), io, ctypes.byref(cache._c),
                                              None if expanded is None else ctypes.byref(expanded._c), ws.data_ptr(),
                                              ws.numel() * ws.element_size(), _stream_of(stream, here)),
            "nvfp4_attn_paged4")
@@ -851,19 +860,16 @@ def nvfp4_pages_copy(caches, src: torch.Tensor, dst: torch.Tensor, stream=None):
         caches = (caches,)
     if not caches:
         raise ValueError("no caches")
-    n, pages = src.numel(), caches[0].pages
-    here = caches[0].k.get_device()
+    n, pages, here = src.numel(), caches[0].pages, _here()
     planes = []
     for c in caches:
         if c.pages != pages:
             raise ValueError("caches of one number of pages")
-        if c.k.get_device() != here:
+        if c._device != here:
             _elsewhere("every cache", c.k)
-        planes += c._planes
-    if here != _here():
-        _elsewhere("every cache", caches[0].k)
+        planes.append(c._planes)
     if dst.numel() != n:
         raise ValueError("as many dst as src")
-    _check((_lib or lib()).nvfp4_pages_copy((_PlaneC * len(planes))(*planes), len(planes), pages,
-                                            _ints_of(src, n, "src", here), _ints_of(dst, n, "dst", here), n,
-                                            _stream_of(stream, here)), "nvfp4_pages_copy")
+    planes = b"".join(planes)
+    _check((_lib or lib()).nvfp4_pages_copy(planes, len(planes) // 24, pages, _ints_of(src, n, "src", here),
+                                            _ints_of(dst, n, "dst", here), n, _stream_of(stream, here)), "nvfp4_pages_copy")

@@ -187,6 +187,9 @@ def test_attention_refusals(nv):
         assert L.nvfp4_attn_paged4(step(nv), io(nv), c, None, ws, n, None) == status
 
 
-def test_heads_as_bytes_are_the_structure(nv):
+def test_packed_bytes_are_the_structures(nv):
     values = (1, 2, 3, 4, *range(5, 17), 17, 18, 1e-6, 19, 20, 21, 22, 23, 24, 1, 25, 26, 27, 28, 29, 30)
     assert nv._pack_heads(*values) == bytes(nv._HeadsC(*values))
+    io = (1, 2, 3, 4, 5, 6, 7, 64, 0.25, 1)
+    assert nv._pack_io(*io) == bytes(nv._AttnIOC(*io))
+    assert nv._pack_plane(1, 2, 3) == bytes(nv._PlaneC(1, 2, 3))
