@@ -28,7 +28,7 @@ int log2_of(int64_t v)
 // time and keeps the token's cosines and sines over its rows.  Arithmetic on
 // pairs of columns (two binary32 operations an instruction: without it, and with
 // the kinds mixed in a warp, the pass was bound by its instructions, 195 us where
-// it now takes HEADS_US).  K rows go to k_out or, with those of V, into the cache,
+// it now takes 91).  K rows go to k_out or, with those of V, into the cache,
 // in 4 bits from the bf16 value (so that the pass gives what the two calls give);
 // a block of 16 columns is two lanes.
 //

@@ -12,8 +12,8 @@
 // cluster of 16 CTAs, so that the steps between which everyone has to wait (all
 // pages marked, all moves known) are cluster barriers instead of launches, and
 // the marks are bits in the CTAs' shared memory instead of a workspace to be kept
-// at zero.  (400 requests of 255 pages at most, 19569 pages moved together: 8 CTAs
-// 23.0 us, FREE_US with 16.)
+// at zero.  (64 requests of up to 246 pages 5.0 us; 400 of up to 255, 19569 pages
+// moved together, 17.9; 23.0 with 8 CTAs and longer segments.)
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.h"
@@ -24,7 +24,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 16;
-constexpr int kSegment = 256;          // entries of a table's row that a warp takes at a time
+constexpr int kSegment = 64;           // entries of a table's row that a warp takes at a time (256: 20.2 us below)
 constexpr int kGroup = 8;              // words of the bit map per entry of its prefix sum
 
 __device__ __forceinline__ void report(int* status, int code)
