@@ -740,6 +740,7 @@ struct AttnKV {
     const nvfp4_kv_cache_t* cache;
     const float* k_g;              // as AttnArgs'
     const float* v_g;
+    int skip_few;
 };
 
 // bf16 tensor map of `rank` dimensions (innermost first, strides in elements
@@ -826,6 +827,7 @@ int run_attn(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const AttnKV& 
     AttnArgs a = attn_args(step, io, workspace, d->status);
     a.k_g = kv.k_g;
     a.v_g = kv.v_g;
+    a.skip_few = kv.skip_few;
     if (kv.cache) {
         a.block_table = step->block_table;
         a.table_ld = step->table_ld;
@@ -1064,7 +1066,7 @@ int nvfp4_kv4_expand(const nvfp4_kv4_cache_t* cache, const nvfp4_step_t* step, c
     if (step->heads && (step->window < 0 || step->window > INT32_MAX)) return NVFP4_ERR_INVALID_ARG;
     DeviceInfo* d = nullptr;
     NVFP4_TRY(device_info(&d));
-    NVFP4_CUDA(launch_kv4_expand(*cache, *step, *out, true, d->num_sms, (cudaStream_t)stream));
+    NVFP4_CUDA(launch_kv4_expand(*cache, *step, *out, true, false, d->num_sms, (cudaStream_t)stream));
     return NVFP4_OK;
 }
 
@@ -1084,15 +1086,21 @@ int nvfp4_attn_paged4(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const
     NVFP4_TRY(device_info(&d));
     cudaStream_t st = (cudaStream_t)stream;
     const int64_t rows = (step->tokens + step->requests - 1) / step->requests * (step->heads / step->kv_heads);
-    if (expanded && rows >= kExpandRows) {
-        NVFP4_CUDA(launch_kv4_expand(*cache, *step, *expanded, false, d->num_sms, st));
+    // Many rows on average: through the bf16 pages.  As many tokens as requests:
+    // straight from the codes.  In between the lengths decide, which are on the
+    // device: both are launched, and one returns at once.
+    const bool many = expanded && rows >= kExpandRows, either = expanded && !many && step->tokens > step->requests;
+    if (many || either) {
+        NVFP4_CUDA(launch_kv4_expand(*cache, *step, *expanded, false, either, d->num_sms, st));
         AttnKV kv = {};
         kv.k = expanded->k;
         kv.v = expanded->v;
         kv.cache = expanded;
         kv.k_g = cache->k_g;
         kv.v_g = cache->v_g;
-        return run_attn(step, io, kv, workspace, workspace_bytes, stream);
+        kv.skip_few = either;
+        NVFP4_TRY(run_attn(step, io, kv, workspace, workspace_bytes, stream));
+        if (many) return NVFP4_OK;
     }
     AttnArgs a = attn_args(step, io, workspace, d->status);
     a.k_g = cache->k_g;
@@ -1100,6 +1108,7 @@ int nvfp4_attn_paged4(const nvfp4_step_t* step, const nvfp4_attn_io_t* io, const
     a.block_table = step->block_table;
     a.table_ld = step->table_ld;
     a.page_size = (int)cache->page_size;
+    a.skip_few = either;
     NVFP4_CUDA(launch_attn4(a, *cache, static_cast<const __nv_bfloat16*>(io->q), io->ldq, io->hq, step->requests,
                             d->num_sms, st));
     return NVFP4_OK;

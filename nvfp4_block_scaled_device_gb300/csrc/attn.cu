@@ -502,6 +502,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const int cta = blockIdx.x;
     int* status = a.status;
 
+    if (a.skip_few) {                // (one of two calls of which the schedule decides)
+        griddep_wait();
+        if (a.sched->few_passes) return;
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; s++) {
             mbar_init(smem_u32(&ctrl->kv_full[s]), 1);

@@ -35,6 +35,7 @@ constexpr int kAttnKeys = 128;
 constexpr int kAttnMaxCtas = 256;
 constexpr int kItemUnits = 2;
 constexpr int kItemUnits4 = 2, kChunksOfTile = 4;
+constexpr int kPassRows = 32;
 
 struct QTile {
     int32_t tok0, n_tok;     // packed rows (tokens) tok0 .. tok0 + n_tok - 1
@@ -53,7 +54,9 @@ struct ScheduleHead {
     // kItemUnits4) kv_heads i.  CTA c takes units c * per_cta4 .. as above.
     int32_t units4, per_cta4;      // 0: too long for it
     int32_t most_tokens;           // of a QTile
-    int32_t pad[10];
+    // few passes of kPassRows rows over the keys suffice, on average over them
+    int32_t few_passes;
+    int32_t pad[9];
     int32_t first[kAttnMaxCtas];   // QTile of the first unit of CTA c ...
     QTile start[kAttnMaxCtas];     // ... and a copy of it, next to what a CTA reads first
     int32_t first4[kAttnMaxCtas];  // the same of the second axis
@@ -130,6 +133,7 @@ struct AttnArgs {
     float scale;
     const float* k_g;    // device scalars that multiply every score and every output, or NULL: 1
     const float* v_g;
+    int skip_few;        // attention over bf16 returns at once where the schedule has few_passes, over 4 bits where not
     // paged cache (block_table NULL: packed keys)
     const int32_t* block_table;
     int64_t table_ld;

@@ -1148,6 +1148,7 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
         for (int i = threadIdx.x; i < C::kRing / 16; i += C::kThreads)
             reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     griddep_wait();
+    if (a.skip_few && !a.sched->few_passes) return;
     __syncthreads();
     // Shares of warps where there are several items for each CTA, or long ones: one
     // join at the end, whatever the items' lengths (64 requests of 200 to 8192 keys

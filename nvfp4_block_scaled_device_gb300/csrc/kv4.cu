@@ -394,6 +394,7 @@ struct ExpandParams {
     int requests, table_cols, window, page_shift, scaled;
     int halves;                                     // half blocks of a page of K
     int chunks;                                     // of kExpandChunk
+    const ScheduleHead* unless_few;                 // nothing to do where its few_passes is set; NULL: there is
 };
 
 // First position that a new token of request r sees, and the end.
@@ -411,6 +412,7 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
     __shared__ int s_sums[kExpandThreads / 32];
     griddep_launch_dependents();
     griddep_wait();
+    if (p.unless_few && p.unless_few->few_passes) return;
     const int R = p.requests, t = threadIdx.x, lane = t & 31, warp = t >> 5, P = 1 << p.page_shift;
     const int per = (R + kExpandThreads - 1) / kExpandThreads;
     auto pages_of = [&](int r) {
@@ -510,9 +512,10 @@ cudaError_t launch_heads(const nvfp4_heads_t& heads, int* status, int num_sms, c
 }
 
 cudaError_t launch_kv4_expand(const nvfp4_kv4_cache_t& cache, const nvfp4_step_t& step, const nvfp4_kv_cache_t& out,
-                              bool scaled, int num_sms, cudaStream_t stream)
+                              bool scaled, bool unless_few, int num_sms, cudaStream_t stream)
 {
     ExpandParams p = {};
+    p.unless_few = unless_few ? static_cast<const ScheduleHead*>(step.schedule) : nullptr;
     p.c = cache;
     p.out = out;
     p.cu_q = step.cu_q;

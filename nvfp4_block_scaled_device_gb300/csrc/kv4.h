@@ -27,9 +27,10 @@ struct PageCopyPlanes {
 cudaError_t launch_heads(const nvfp4_heads_t& heads, int* status, int num_sms, cudaStream_t stream);
 
 // The rows of a 4-bit cache that a step sees, into a bf16 cache's pages; scaled:
-// times the cache's global scales (else code times E4M3 scale, exact in bf16).
+// times the cache's global scales (else code times E4M3 scale, exact in bf16);
+// unless_few: only where the step's schedule does not have few_passes.
 cudaError_t launch_kv4_expand(const nvfp4_kv4_cache_t& cache, const nvfp4_step_t& step, const nvfp4_kv_cache_t& out,
-                              bool scaled, int num_sms, cudaStream_t stream);
+                              bool scaled, bool unless_few, int num_sms, cudaStream_t stream);
 
 // Attention over a 4-bit cache (args.k_g, v_g and the paged fields set).
 cudaError_t launch_attn4(const AttnArgs& args, const nvfp4_kv4_cache_t& cache, const __nv_bfloat16* q, int64_t ldq,

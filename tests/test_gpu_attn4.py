@@ -151,7 +151,22 @@ def test_one_request_of_many_tokens_among_single_ones(nv, ws):
     """Rows of one request that need several passes, where the step's average is a few."""
     ctx = [int(c) for c in np.random.default_rng(3).integers(0, 700, 64)]
     run(nv, ws, ctx, [1] * 20 + [70] + [1] * 43, 10, 2, 128, 16)
-    run(nv, ws, ctx, [1] * 63 + [200], 4, 4, 64, 32, expanded=True)
+    run(nv, ws, ctx, [1] * 63 + [200], 4, 4, 64, 32)
+
+
+def _through_the_pages(nv, ws, ctx, q_len, H, Hkv, D):
+    """Whether a step went through its bf16 pages: bit for bit what the call without them gives, or not."""
+    a, b = (run(nv, ws, ctx, q_len, H, Hkv, D, 16, expanded=x) for x in (False, True))
+    return not (torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]))
+
+
+@pytest.mark.parametrize("H,Hkv,D", [(10, 2, 128), (8, 1, 64)])
+def test_the_lengths_decide_about_the_bf16_pages(nv, ws, H, Hkv, D):
+    ctx = [int(c) for c in np.random.default_rng(4).integers(100, 700, 30)]
+    assert not _through_the_pages(nv, ws, ctx, [2] * 29 + [3], H, Hkv, D)          # a few rows each
+    assert not _through_the_pages(nv, ws, ctx, [1] * 29 + [9], H, Hkv, D)          # one of two passes among many of one
+    assert _through_the_pages(nv, ws, [2000] + ctx[1:], [90] + [1] * 29, H, Hkv, D)    # one of many rows and keys
+    assert not _through_the_pages(nv, ws, ctx, [1] * 29 + [0], H, Hkv, D)          # (no more tokens than requests)
 
 
 def test_a_share_of_very_long_items(nv, ws):
