@@ -4,11 +4,11 @@
 //
 // A decode step is few rows against many keys: 72 bytes of keys and as many of
 // values a key of 128 columns, each read once, and what has to be done for them
-// is to turn codes into numbers.  So nothing is written back to shared memory:
-// every warp has its own ring of groups of 16 keys (cp.async), turns a group's
-// codes into the fragments of mma.m16n8k16 in registers (cvt of two codes to two
-// halves, times the scale: six bits of significand, exact in half precision)
-// and multiplies
+// is to turn codes into numbers.  So nothing goes back to shared memory (as the
+// operands of tcgen05.mma would have to): every warp has its own ring of chunks of
+// 32 keys (cp.async), turns a chunk's codes into the fragments of mma.m16n8k16 in
+// registers (cvt of two codes to two halves, times the scale: six bits of
+// significand, exact in half precision) and multiplies, for each half of the chunk,
 //   S^T = K Q^T      16 keys x 8 rows at a time, over 16 columns
 //   O^T += V^T P^T   16 columns x 8 rows at a time, over the 16 keys
 // so that 8 rows, not 16, fill an instruction.  The order of a product's inner
@@ -17,18 +17,34 @@
 // P^T comes out of S^T by transposing its 8 x 8 blocks (movmatrix).
 //   Softmax: 2^(c s - m), c = scale * log2(e) * *k_g, statistics and sums in
 // binary32; m only moves when a score has outgrown it by 2^8, which one vote per
-// group finds out.  P is rounded to half precision, 2^-11 relative, and carried
+// chunk finds out.  P is rounded to half precision, 2^-11 relative, and carried
 // 2^6 above 1 so that what is below 2^-20 of the largest loses bits only.  Q is
 // scaled by a power of two to the top of half precision's range (its bf16 bits
 // fit down to 2^-28 of the row's largest).
 //
-// Work is cut as in attn.cu (the plan's schedule: equal key tiles per CTA).  The
-// warps of a CTA take the groups of its piece of an item in turn, with rows,
-// maxima and sums of their own, and are joined in shared memory at its end; the
-// pieces of an item that several CTAs share are joined by the last of them, in
-// CTA order.  No CTA waits for another.
+// The work is cut for CTAs and warps in one of two ways:
+//   shares of warps  each warp a contiguous share of its CTA's items on the
+//                    schedule's second axis (attn.h), whatever the items' lengths; what
+//                    several warps have of an item is added up at the CTA's end;
+//   passes together  all warps of a CTA take the chunks of its part of an item in
+//                    turn, on the first axis, and are joined at the part's end; an item
+//                    of more rows than a warp holds takes several passes.
+// Parts of an item that several CTAs have are joined by the last of them, in CTA
+// order.  No CTA waits for another, and the results do not depend on who is first.
 //
-// More than 8 kNT rows of an item take several passes over its keys.
+// What bounds it (40 query heads on 8 kv heads of 128 columns): HBM in the steady
+// state -- twice the keys of one request of 131071 and one of 65537 take 37.5 us
+// more for 248 MB, 6.6 TB/s -- where 32 keys are 430 instructions of a warp, 1.3 us for
+// the 16 of an SM, against 1.66 us for their bytes (with the bytes of the codes taken
+// apart by shifts, 550 instructions and the binding limit).  Beside that some 17 us
+// pass from the launch to the end: 4 to 7 until the first keys are there (the
+// schedule, the block table, Q, the keys, one after the other, and every warp's
+// ring at once), 3 for the spread of the warps' ends, 2 to add up their shares, 4 to 5 for
+// the parts of other CTAs.  These two requests 54 us; 64 requests of 200 to 8192
+// keys 44 (bf16: 95); one of 333 keys 7.0.  With 9 to 16 rows a request 52 (64
+// requests of 200 to 4000 keys, 3 tokens each), with 17 to 32, where the softmax and
+// Q's fragments out of shared memory weigh as much as the codes, 104 (64 of 200 to
+// 8192, 1 to 4 tokens each).
 #include <cuda_fp16.h>
 
 #include "attn.h"
@@ -53,7 +69,6 @@ struct Cfg4 {
     static constexpr int kStages = kNT == 1 ? 2 : 3;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRows = 8 * kNT;
-    static constexpr bool kOwnShares = kNT <= 2;                 // shares of warps (see above)
     static constexpr int kAtOnce = kNT == 1 ? 2 : 1;             // halves of a chunk worked on together
     static constexpr int kRowBytes = kDP / 2;
     static constexpr int kCodes = kHalf * kRowBytes;             // of K or V of half a chunk
@@ -66,12 +81,25 @@ struct Cfg4 {
     static constexpr int kJoin = 16 / kWarps;
     static constexpr int kLine = 2 * kDP + 4;
     static constexpr int kWarpO = kJoin * 4 * kLine;             // floats
-    static_assert(!kOwnShares || kWarpO >= kRows * kDP, "a warp's O");
+    static_assert(kNT == 4 || kWarpO >= kRows * kDP, "a warp's O");
     static constexpr int kOffO = kRing;
     static constexpr int kOffQ = kOffO + kWarps * kWarpO * 4;    // Q's rows (bf16), then (kNT > 1) its fragments
     static constexpr int kOffFrag = kOffQ + kRows * kDP * 2;
     static constexpr int kOffM = kOffFrag + (kNT > 1 ? kNT * (kDP / 16) * 32 * 8 : 0);
-    static constexpr int kSmem = kOffM + kWarps * kRows * 2 * 4;
+    static constexpr int kSmemTogether = kOffM + kWarps * kRows * 2 * 4;
+    // Shares of warps.  kNT <= 2: Q in registers, and what a warp leaves for
+    // another (its O) where O is above.  4: Q's fragments of each warp in shared
+    // memory, and what a warp leaves in its ring, which has to be as large, or (with
+    // another part to come) in a part of the CTA's slots that rows do not reach.
+    static constexpr bool kLeaveInRing = kNT == 4;
+    static constexpr int kOwnStages = kLeaveInRing ? 4 : kStages;
+    static constexpr int kOwnRing = kWarps * kOwnStages * kStageBytes;
+    static constexpr int kFrags = kNT * (kDP / 16) * 32;         // uint2
+    static constexpr int kOffOwnM = kLeaveInRing ? kOwnRing + kWarps * kFrags * 8 : kOffM;
+    static constexpr int kSmemOwn = kOffOwnM + kWarps * kRows * 2 * 4;
+    static_assert(!kLeaveInRing || kOwnStages * kStageBytes >= kRows * kDP * 4, "a warp's O");
+    static constexpr int kSmem = kSmemOwn > kSmemTogether ? kSmemOwn : kSmemTogether;
+    static constexpr int kMostRing = kOwnRing > kRing ? kOwnRing : kRing;
     static constexpr int kQVecs = kRows * kDP / 8 / kThreads > 0 ? kRows * kDP / 8 / kThreads : 1;
     static_assert(kSmem <= 232448 - 4096, "shared memory per block");
 };
@@ -398,7 +426,7 @@ __device__ __forceinline__ void work_halves(const uint8_t* st, int k0, const See
 // a release() or, at a part's start, by as many copies as stages are free: with a
 // commit for each of them, real or not, the oldest chunk is there when all but
 // kStages - 1 commits are complete.
-template <int kDP, int kNT, bool kFull>
+template <int kDP, int kNT, bool kFull, int kStages>
 struct Ring {
     using C = Cfg4<kDP, kNT>;
     const Params4& prm;
@@ -432,7 +460,7 @@ struct Ring {
         sf_to = (lane >> 4) * C::kHalfBytes + 2 * C::kCodes + (of_v ? C::kScales : 0) + (lane & 7) * 16;
         sf_at = (of_v ? prm.v_sf : prm.k_sf) + (lane & 7) * 16;
     }
-    __device__ __forceinline__ static int next(int at) { return C::kStages == 2 ? C::kStageBytes - at : at == (C::kStages - 1) * C::kStageBytes ? 0 : at + C::kStageBytes; }
+    __device__ __forceinline__ static int next(int at) { return kStages == 2 ? C::kStageBytes - at : at == (kStages - 1) * C::kStageBytes ? 0 : at + C::kStageBytes; }
     // Page ids of the halves of 16 chunks, `stride` keys apart, from key k on:
     // a lane each; none from ke on.
     __device__ __forceinline__ int load_ids(const int32_t* table, int k, int stride, int ke) const
@@ -490,7 +518,7 @@ struct Ring {
     // The oldest chunk, once it is there.
     __device__ __forceinline__ const uint8_t* wait()
     {
-        copies_wait<C::kStages - 1>();
+        copies_wait<kStages - 1>();
         __syncwarp();
         return base + out;
     }
@@ -634,7 +662,7 @@ __device__ __forceinline__ void passes_together(const Params4& prm, uint8_t* sme
         return n > warp ? (n - warp + C::kWarps - 1) / C::kWarps : 0;
     };
     constexpr int kStride = C::kWarps * kChunk;            // a warp's chunks are this many keys apart
-    Ring<kDP, kNT, kFull> ring(prm, smem + warp * (C::kStages * C::kStageBytes), lane, D);
+    Ring<kDP, kNT, kFull, C::kStages> ring(prm, smem + warp * (C::kStages * C::kStageBytes), lane, D);
     // Q's rows of a pass, a share of each thread
     auto load_q = [&](const Pass& x, uint4* v) {
 #pragma unroll
@@ -859,8 +887,11 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
     const AttnArgs& a = prm.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
     const int D = kFull ? kDP : a.head_dim, Hkv = a.kv_heads, nb = D / 16;
-    float* const deposits = reinterpret_cast<float*>(smem + C::kOffO);     // [warp][tile, vector][lane][4]
-    float2* const deposit_ml = reinterpret_cast<float2*>(smem + C::kOffM); // [warp][row]
+    // what a warp leaves for an earlier one: O in its lanes' order, [tile, vector]
+    // [lane][4] floats; its maxima and sums [warp][row]
+    __shared__ float4* s_left[C::kWarps];
+    float2* const left_ml = reinterpret_cast<float2*>(smem + C::kOffOwnM);
+    uint2* const frags = reinterpret_cast<uint2*>(smem + C::kOwnRing) + warp * C::kFrags + lane;   // (kNT 4)
     const ScheduleHead* head = a.sched;
     const QTile* tiles = schedule_tiles(head);
 
@@ -942,7 +973,7 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
         __syncwarp();
     };
 
-    Ring<kDP, kNT, kFull> ring(prm, smem + warp * (C::kStages * C::kStageBytes), lane, D);
+    Ring<kDP, kNT, kFull, C::kOwnStages> ring(prm, smem + warp * (C::kOwnStages * C::kStageBytes), lane, D);
     Rows<kDP, kNT> w;
     next(&s_work[warp][0]);
     // the next chunk to copy, of this part or (in_next) the next; chunks whose
@@ -1004,9 +1035,8 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
             const Work& cur = s_work[warp][at];
             const Work& nxt = s_work[warp][at ^ 1];
             // Q of the item: row g of tile n, columns kDP / 4 * j .. of this lane
-            uint32_t q[kNT][kDP / 8];
-#pragma unroll
-            for (int n = 0; n < kNT; n++) {
+            uint32_t q[C::kLeaveInRing ? 1 : kNT][kDP / 8];
+            auto load_q = [&](int n, uint32_t* raw) {
                 const int r = 8 * n + g, t = r / a.group;
                 const __nv_bfloat16* src = prm.q + (int64_t)(cur.tok0 + t) * prm.ldq +
                                            (int64_t)(cur.hk * a.group + r - t * a.group) * prm.hq + j * (kDP / 4);
@@ -1014,8 +1044,12 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
                 for (int x = 0; x < kDP / 32; x++) {
                     uint4 y = make_uint4(0, 0, 0, 0);
                     if (r < cur.rows && (kFull || j * (kDP / 4) + 8 * x < D)) y = *reinterpret_cast<const uint4*>(src + 8 * x);
-                    q[n][4 * x] = y.x, q[n][4 * x + 1] = y.y, q[n][4 * x + 2] = y.z, q[n][4 * x + 3] = y.w;
+                    raw[4 * x] = y.x, raw[4 * x + 1] = y.y, raw[4 * x + 2] = y.z, raw[4 * x + 3] = y.w;
                 }
+            };
+            if (!C::kLeaveInRing) {
+#pragma unroll
+                for (int n = 0; n < kNT; n++) load_q(n, q[C::kLeaveInRing ? 0 : n]);
             }
             next(&s_work[warp][at ^ 1]);
             const int next_ids = nxt.valid && nxt.n ? ring.load_ids(nxt.table, nxt.kb, kChunk, nxt.ke) : 0;
@@ -1042,9 +1076,17 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
                 copies_end();
             };
 #pragma unroll 1
-            for (int y = ring.ahead; y < C::kStages; y++) issue();
+            for (int y = ring.ahead; y < C::kOwnStages; y++) issue();
 #pragma unroll
-            for (int n = 0; n < kNT; n++) make_q<kDP>(q[n], a.scale, k_g, w.cf[n], j);
+            for (int n = 0; n < kNT; n++) {
+                uint32_t* raw = q[C::kLeaveInRing ? 0 : n];
+                if (C::kLeaveInRing) load_q(n, raw);
+                make_q<kDP>(raw, a.scale, k_g, w.cf[n], j);
+                if (C::kLeaveInRing) {
+#pragma unroll
+                    for (int x = 0; x < kSteps; x++) frags[32 * (n * kSteps + x)] = make_uint2(raw[2 * x], raw[2 * x + 1]);
+                }
+            }
             w.clear();
             const Seen seen = {cur.pos0, 0, a.group, cur.lo, cur.ke, a.window};
             const int lo_all = cur.lo_all, hi_all = cur.hi_all;
@@ -1052,7 +1094,10 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
 #pragma unroll 1
             for (int i = cur.n; i > 0; i--, k0 += kChunk) {
                 const uint8_t* st = ring.wait();
-                auto frag = [&](int n, int x) { return make_uint2(q[n][2 * x], q[n][2 * x + 1]); };
+                auto frag = [&](int n, int x) {
+                    const uint32_t* raw = q[C::kLeaveInRing ? 0 : n];
+                    return C::kLeaveInRing ? frags[32 * (n * kSteps + x)] : make_uint2(raw[2 * x], raw[2 * x + 1]);
+                };
 #pragma unroll 1
                 for (int h = 0; h < 2; h += C::kAtOnce) {
                     const int k = k0 + h * kHalf;
@@ -1067,7 +1112,15 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
             }
             w.join_sums();
             if (cur.x0 > cur.a) {                          // the part began in an earlier warp, which will add this
-                float4* to4 = reinterpret_cast<float4*>(deposits + warp * C::kWarpO) + lane;
+                float* left = reinterpret_cast<float*>(smem + C::kOffO) + warp * C::kWarpO;
+                if (C::kLeaveInRing) {
+                    constexpr int kSpare = (kAttnSlotRows - C::kRows) / C::kRows;      // warps to a slot, behind its rows
+                    static_assert(!C::kLeaveInRing || 2 * kSpare >= C::kWarps, "room in the CTA's slots");
+                    left = nxt.valid ? a.partials + (2 * cta + warp / kSpare) * kAttnSlotFloats + (1 + warp % kSpare) * C::kRows * kDP
+                                     : reinterpret_cast<float*>(smem + warp * (C::kOwnStages * C::kStageBytes));
+                }
+                float4* to4 = reinterpret_cast<float4*>(left) + lane;
+                if (lane == 0) s_left[warp] = reinterpret_cast<float4*>(left);
 #pragma unroll
                 for (int n = 0; n < kNT; n++) {
 #pragma unroll
@@ -1075,7 +1128,7 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
                         to4[32 * (n * kSteps + i)] = make_float4(w.o[n][i][0], w.o[n][i][1], w.o[n][i][2], w.o[n][i][3]);
 #pragma unroll
                     for (int y = 0; y < 2; y++)
-                        if (g == 0) deposit_ml[warp * C::kRows + 8 * n + 2 * j + y] = make_float2(w.m[n][y], w.l[n][y]);
+                        if (g == 0) left_ml[warp * C::kRows + 8 * n + 2 * j + y] = make_float2(w.m[n][y], w.l[n][y]);
                 }
             } else if (cur.x1 == cur.b) {
                 finish(cur);
@@ -1095,13 +1148,13 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
             const int to = o == C::kWarps - 1 ? x.b : min(max(bound(o + 1) - x.s - kItemUnits4, x.a), x.b);
             if (to == reached) continue;
             reached = to;
-            const float4* from = reinterpret_cast<const float4*>(deposits + o * C::kWarpO) + lane;
+            const float4* from = s_left[o] + lane;
 #pragma unroll
             for (int n = 0; n < kNT; n++) {
                 float f0[2], f1[2];
 #pragma unroll
                 for (int y = 0; y < 2; y++) {
-                    const float2 ml = deposit_ml[o * C::kRows + 8 * n + 2 * j + y];
+                    const float2 ml = left_ml[o * C::kRows + 8 * n + 2 * j + y];
                     const float top = fmaxf(w.m[n][y], ml.x), ref = top == -INFINITY ? 0.0f : top;
                     f0[y] = ex2(w.m[n][y] - ref);
                     f1[y] = ex2(ml.x - ref);
@@ -1145,7 +1198,7 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
 
     griddep_launch_dependents();
     if (!kFull)                                 // the columns that no copy writes are zeros
-        for (int i = threadIdx.x; i < C::kRing / 16; i += C::kThreads)
+        for (int i = threadIdx.x; i < C::kMostRing / 16; i += C::kThreads)
             reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     griddep_wait();
     if (a.skip_few && !a.sched->few_passes) return;
@@ -1155,14 +1208,12 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
     // 43 us, 70 with all warps on one item at a time; a request of 131071 with one of
     // 65537 53 and 56).  Else all warps at once on a CTA's one part, which is
     // joined faster (a request of 333 keys 6.9 us, 8.8; 8 of 2000 13.3, 19.1).
-    bool own = false;
-    if constexpr (C::kOwnShares) {
-        const int64_t items = (int64_t)a.sched->qtiles * a.kv_heads;
-        const int per = a.sched->per_cta4;
-        own = per > 0 && a.sched->most_tokens * a.group <= C::kRows && (2 * items >= 3 * (int)gridDim.x || per >= 256);
-        if (own) own_shares<kDP, kNT, kFull>(prm, smem, cta);
-    }
-    if (!own) passes_together<kDP, kNT, kFull>(prm, smem, cta);
+    const int64_t items = (int64_t)a.sched->qtiles * a.kv_heads;
+    const int per = a.sched->per_cta4;
+    if (per > 0 && a.sched->most_tokens * a.group <= C::kRows && (2 * items >= 3 * (int)gridDim.x || per >= 256))
+        own_shares<kDP, kNT, kFull>(prm, smem, cta);
+    else
+        passes_together<kDP, kNT, kFull>(prm, smem, cta);
     copies_wait<0>();
     if (a.cu_end) {
         // the rows past the step's last token, a warp to a row
@@ -1194,7 +1245,7 @@ cudaError_t launch4(const Params4& p, int ctas, cudaStream_t stream)
     return launch_programmatic(attn4_kernel<kDP, kNT, kFull>, dim3((unsigned)ctas), dim3(C::kThreads), C::kSmem, stream, p);
 }
 
-// Rows of a request, on average: one tile of 8, two, or passes of four.
+// By the rows of a request: one tile of 8, two, or passes of four.
 template <int kDP, bool kFull>
 cudaError_t launch_rows(const Params4& p, int64_t rows, int ctas, cudaStream_t stream)
 {
@@ -1222,7 +1273,10 @@ cudaError_t launch_attn4(const AttnArgs& args, const nvfp4_kv4_cache_t& cache, c
     p.pages = (int)cache.pages;
     while ((1 << p.page_shift) < cache.page_size) p.page_shift++;
     const int ctas = num_sms < kAttnMaxCtas ? num_sms : kAttnMaxCtas;
-    const int64_t rows = (args.tokens + requests - 1) / requests * args.group;
+    // the same number of tokens for each request where that is possible; else some
+    // have more than the average
+    const bool even = args.tokens % requests == 0;
+    const int64_t rows = (args.tokens + requests - 1) / requests * args.group * (even ? 1 : 2);
     const int d = args.head_dim;
     return d == 128  ? launch_rows<128, true>(p, rows, ctas, stream)
            : d > 64  ? launch_rows<128, false>(p, rows, ctas, stream)
