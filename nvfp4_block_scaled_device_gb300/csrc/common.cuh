@@ -750,21 +750,6 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t b)
     return __half2float(__ushort_as_half((uint16_t)(h2 & 0xFFFFu)));
 }
 
-// Two E2M1 codes (a byte, the first in the low nibble) -> f16x2 (exact).
-__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t b)
-{
-    uint32_t out;
-    asm("{\n .reg .b8 x, a, b, c;\n mov.b32 {x, a, b, c}, %1;\n cvt.rn.f16x2.e2m1x2 %0, x;\n}" : "=r"(out) : "r"(b));
-    return out;
-}
-
-// The same -> binary32.
-__device__ __forceinline__ float2 e2m1x2_to_f32(uint32_t b)
-{
-    const uint32_t h = e2m1x2_to_f16x2(b);
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 

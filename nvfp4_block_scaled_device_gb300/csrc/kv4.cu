@@ -1,6 +1,8 @@
 // Rows on their way into and out of a layer's cache: norms and rotation of the
 // query and key heads (nvfp4_qk_norm_rope), the write of rows into a cache in 4
 // bits (nvfp4_kv4_append), and the rows of a step out of it (nvfp4_kv4_expand).
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.h"
@@ -375,6 +377,14 @@ cudaError_t run_heads(HeadsParams& p, int num_sms, cudaStream_t stream)
 }
 
 // ----------------------------------------------------------------- expand
+// Two E2M1 codes (a byte, the first in the low nibble) -> binary32 (exact).
+__device__ __forceinline__ float2 e2m1x2_to_f32(uint32_t b)
+{
+    uint32_t h;
+    asm("{\n .reg .b8 x, a, b, c;\n mov.b32 {x, a, b, c}, %1;\n cvt.rn.f16x2.e2m1x2 %0, x;\n}" : "=r"(h) : "r"(b));
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
 // A page's rows of all heads are one run of half blocks (8 columns: 4 bytes of
 // codes, a scale that two share, 16 bytes out), so nothing but the pages at a
 // request's ends has to know which row it is at.  Every block sums up the
