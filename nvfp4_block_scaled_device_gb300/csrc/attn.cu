@@ -485,7 +485,10 @@ __device__ __forceinline__ uint32_t stage_of(uint32_t use, uint32_t* parity)
     return use - turn * kStages;
 }
 
-template <int kDP, bool kFold>
+// kScaled: the rows are those of a 4-bit cache without its global scales, which
+// multiply the scores and the outputs here (a variant of its own: three more loads
+// cost a prompt of 8192 rows 4 %).
+template <int kDP, bool kFold, bool kScaled>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ Params prm)
 {
     using C = Cfg<kDP>;
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const int cta = blockIdx.x;
     int* status = a.status;
 
-    if (a.skip_few) {                // (one of two calls of which the schedule decides)
+    if (kScaled && a.skip_few) {     // (one of two calls of which the schedule decides)
         griddep_wait();
         if (a.sched->few_passes) return;
     }
@@ -842,8 +845,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         const uint32_t o_full = smem_u32(&ctrl->o_full[j][0]);
         const bool negate = a.scale < 0.0f;
         // a zero scale: any tiny factor gives equal probabilities, without 0 * inf at masked keys
-        const float c = fmaxf(fabsf(a.scale) * (a.k_g ? *a.k_g : 1.0f) * 1.4426950408889634f, 1.17549435e-38f);
-        const float v_g = a.v_g ? *a.v_g : 1.0f;
+        const float c = fmaxf(fabsf(a.scale) * (kScaled ? *a.k_g : 1.0f) * 1.4426950408889634f, 1.17549435e-38f);
+        const float v_g = kScaled ? *a.v_g : 1.0f;
         const float lazy = kLazy / c;
         uint32_t cnt = 0, ml_cnt = 0;      // steps done
         bool ok = true;
@@ -1163,7 +1166,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
 }
 
-template <int kDP, bool kFold>
+template <int kDP, bool kFold, bool kScaled>
 cudaError_t launch(const Params& p, int num_sms, cudaStream_t stream)
 {
     static int attr_set_for_device[64] = {0};
@@ -1171,11 +1174,11 @@ cudaError_t launch(const Params& p, int num_sms, cudaStream_t stream)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 64 && !attr_set_for_device[dev]) {
-        e = cudaFuncSetAttribute(attn_kernel<kDP, kFold>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<kDP>::kSmemBytes);
+        e = cudaFuncSetAttribute(attn_kernel<kDP, kFold, kScaled>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<kDP>::kSmemBytes);
         if (e != cudaSuccess) return e;
         attr_set_for_device[dev] = 1;
     }
-    return launch_programmatic(attn_kernel<kDP, kFold>, dim3((unsigned)num_sms), dim3(kThreads), Cfg<kDP>::kSmemBytes,
+    return launch_programmatic(attn_kernel<kDP, kFold, kScaled>, dim3((unsigned)num_sms), dim3(kThreads), Cfg<kDP>::kSmemBytes,
                                stream, p);
 }
 
@@ -1190,8 +1193,12 @@ cudaError_t launch_attn(const CUtensorMap& map_q, const CUtensorMap& map_k, cons
     p.map_v = map_v;
     p.a = args;
     const int ctas = num_sms < kAttnMaxCtas ? num_sms : kAttnMaxCtas;
-    if (args.fold) return launch<128, true>(p, ctas, stream);
-    return args.head_dim > 64 ? launch<128, false>(p, ctas, stream) : launch<64, false>(p, ctas, stream);
+    if (args.k_g) {
+        if (args.fold) return launch<128, true, true>(p, ctas, stream);
+        return args.head_dim > 64 ? launch<128, false, true>(p, ctas, stream) : launch<64, false, true>(p, ctas, stream);
+    }
+    if (args.fold) return launch<128, true, false>(p, ctas, stream);
+    return args.head_dim > 64 ? launch<128, false, false>(p, ctas, stream) : launch<64, false, false>(p, ctas, stream);
 }
 
 }  // namespace nvfp4

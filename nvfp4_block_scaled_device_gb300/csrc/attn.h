@@ -70,7 +70,7 @@ inline __host__ __device__ const QTile* schedule_tiles(const ScheduleHead* h)
 }
 
 // Units of the second axis before QTile i.
-inline __host__ __device__ int64_t units4_before(int64_t unit0, int64_t kv_heads, int64_t i)
+inline __host__ __device__ int units4_before(int unit0, int kv_heads, int i)
 {
     return kChunksOfTile * unit0 - (kChunksOfTile * kItemUnits - kItemUnits4) * kv_heads * i;
 }
@@ -131,9 +131,10 @@ struct AttnArgs {
     int row_tokens;      // tokens of a row tile
     int window;
     float scale;
-    const float* k_g;    // device scalars that multiply every score and every output, or NULL: 1
+    // attention over a 4-bit cache, or over rows taken out of one (k_g NULL: neither)
+    const float* k_g;    // device scalars that multiply every score and every output
     const float* v_g;
-    int skip_few;        // attention over bf16 returns at once where the schedule has few_passes, over 4 bits where not
+    int skip_few;        // over bf16 rows it returns at once where the schedule has few_passes, over 4 bits where not
     // paged cache (block_table NULL: packed keys)
     const int32_t* block_table;
     int64_t table_ld;

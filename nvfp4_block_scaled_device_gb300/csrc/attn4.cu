@@ -908,19 +908,19 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
     Walk& walk = s_walk[warp];
     const bool any = len > 0;
     if (any) {
-        int qt = begin, s = (int)units4_before(start.unit0, Hkv, begin);
+        int qt = begin, s = units4_before(start.unit0, Hkv, begin);
         QTile t = start;
         if (v0 >= s + (kItemUnits4 + kChunksOfTile * t.tiles) * Hkv) {
             // a later QTile of the CTA's: the last that begins at or below v0
             for (int base = begin + 1;; base += 32) {
                 const int i = base + lane;
-                const int64_t at = i < n_tiles ? units4_before(tiles[i].unit0, Hkv, i) : 0x7fffffff;
+                const int at = i < n_tiles ? units4_before(tiles[i].unit0, Hkv, i) : 0x7fffffff;
                 const int k = __popc(__ballot_sync(0xffffffffu, at <= v0));
                 qt = base + k - 1;
                 if (k < 32) break;
             }
             t = tiles[qt];
-            s = (int)units4_before(t.unit0, Hkv, qt);
+            s = units4_before(t.unit0, Hkv, qt);
         }
         const int item = kItemUnits4 + kChunksOfTile * t.tiles, hk = (v0 - s) / item;
         if (lane == 0) walk = Walk{t, qt, hk, s + hk * item};

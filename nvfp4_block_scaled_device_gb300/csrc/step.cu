@@ -99,6 +99,10 @@ __device__ __forceinline__ int last_at_or_below(const int32_t* x, int n, int64_t
 // once for their units, once (the sums known) to write them.  cu: new tokens
 // before each request, ctx: cached tokens, tile0: room for R + 1 int32 (all
 // shared memory).
+// kSecond: the second axis (attn.h), by a block of its own, so that the first is
+// there no later (64 requests 5.8 us; 6.9 in the same blocks).  It is without the
+// lengths' limits: has no units where the first has many.
+template <bool kSecond>
 __device__ void build_schedule(const PlanParams& p, const int32_t* cu, const int32_t* ctx, int32_t* tile0,
                                int64_t (*warp_sums)[2], int* longest, int* most_tokens, int block, int blocks)
 {
@@ -120,7 +124,7 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, const int
     if (t == 0) {
         tile0[R] = (int32_t)total;
         *longest = 1;
-        *most_tokens = 0;
+        if (kSecond) *most_tokens = 0;
     }
     __syncthreads();
     const int n = (int)total, each = ((n + kPlanThreads - 1) / kPlanThreads) | 1;
@@ -145,23 +149,49 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, const int
         return q;
     };
     int64_t unit = 0, units = 0;
+    int64_t pass_tiles = 0, all_pass_tiles;         // (kSecond) key tiles times the passes of kPassRows rows over them
     int most = 1, tokens = 0;
-    int64_t pass_tiles = 0, all_pass_tiles;         // key tiles times the passes of kPassRows rows over them
     const int group = (int)(s.heads / s.kv_heads);
     for (int i = i0, r = r0; i < i1; i++) {
         const QTile q = tile_of(i, r);
         const int item = kItemUnits + q.tiles;
         unit += (int64_t)item * Hkv;
         most = max(most, item);
-        tokens = max(tokens, q.n_tok);
-        pass_tiles += (int64_t)q.tiles * ((q.n_tok * group + kPassRows - 1) / kPassRows);
+        if (kSecond) {
+            tokens = max(tokens, q.n_tok);
+            pass_tiles += (int64_t)q.tiles * ((q.n_tok * group + kPassRows - 1) / kPassRows);
+        }
     }
     atomicMax(longest, __reduce_max_sync(0xffffffffu, most));
-    atomicMax(most_tokens, __reduce_max_sync(0xffffffffu, tokens));
-    block_prefix(unit, pass_tiles, warp_sums, &units, &all_pass_tiles);   // (its barriers order *longest too)
-    // (measured: 8 requests of 2000 keys 28 us straight from 4 bits in one pass, 52 in
-    // two; 44 in bf16 after taking them out, up to 32 rows and beyond)
-    const bool few_passes = 10 * all_pass_tiles <= 17 * (units / Hkv - (int64_t)kItemUnits * n);
+    if (kSecond) atomicMax(most_tokens, __reduce_max_sync(0xffffffffu, tokens));
+    block_prefix(unit, kSecond ? pass_tiles : unused, warp_sums, &units, kSecond ? &all_pass_tiles : &unused_total);   // (its barriers order *longest too)
+    if (kSecond) {
+        const bool has4 = units < kMaxUnits / 8;
+        const int units4 = has4 ? units4_before((int)units, Hkv, n) : 0;
+        // (at least a chunk for each warp of a CTA, where items have as many)
+        const int longest4 = has4 ? kChunksOfTile * (*longest - kItemUnits) + kItemUnits4 : 1;
+        const int per = has4 ? max(max((units4 + p.ctas - 1) / p.ctas, min(kItemUnits4 + 16, longest4)), 1) : 0;
+        if (t == 0) {
+            head->units4 = units4;
+            head->per_cta4 = per;
+            head->most_tokens = *most_tokens;
+            // (measured: 8 requests of 2000 keys 28 us straight from 4 bits in one pass,
+            // 52 in two; 44 in bf16 after taking them out, up to 32 rows and beyond)
+            head->few_passes = 10 * all_pass_tiles * Hkv <= 17 * (units - (int64_t)kItemUnits * n * Hkv);
+        }
+        if (!has4) return;
+        int c = (units4_before((int)unit, Hkv, i0) + per - 1) / per;
+        for (int i = i0, r = r0; i < i1; i++) {
+            QTile q = tile_of(i, r);
+            q.unit0 = (int)unit;
+            unit += (int64_t)(kItemUnits + q.tiles) * Hkv;
+            for (const int next = units4_before((int)unit, Hkv, i + 1); c * per < next; c++) {
+                head->first4[c] = i;
+                head->start4[c] = q;
+            }
+        }
+        return;
+    }
     if (units > kMaxUnits) {
         // ends with a whole item (one cut off would never collect its tickets)
         int64_t at = unit;
@@ -176,24 +206,13 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, const int
     }
     const int share = (int)((units + p.ctas - 1) / p.ctas);
     const int per_cta = max(share, min(kItemUnits + kMinPart, *longest));
-    // the second axis (at least a chunk for each warp of a CTA, where items have
-    // as many)
-    const int64_t units4 = units4_before(units, Hkv, n);
-    const bool has4 = units < kMaxUnits / 8;
-    const int longest4 = has4 ? kChunksOfTile * (*longest - kItemUnits) + kItemUnits4 : 1;
-    const int per_cta4 = has4 ? max(max((int)((units4 + p.ctas - 1) / p.ctas), min(kItemUnits4 + 16, longest4)), 1) : 0;
     if (t == 0 && block == 0) {
         head->units = (int32_t)units;
         head->per_cta = per_cta;
         head->qtiles = n;
-        head->units4 = has4 ? (int32_t)units4 : 0;
-        head->per_cta4 = per_cta4;
-        head->most_tokens = *most_tokens;
-        head->few_passes = few_passes;
     }
     if (t * blocks / kPlanThreads != block) return;
     int c = (int)((min(unit, units) + per_cta - 1) / per_cta);       // the next CTA to start
-    int c4 = has4 ? (int)((units4_before(unit, Hkv, i0) + per_cta4 - 1) / per_cta4) : 0;
     for (int i = i0, r = r0; i < i1; i++) {
         QTile q = tile_of(i, r);
         q.unit0 = (int)min(unit, units);
@@ -202,11 +221,6 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, const int
         for (const int next = (int)min(unit, units); c * per_cta < next; c++) {
             head->first[c] = i;
             head->start[c] = q;
-        }
-        if (!has4) continue;
-        for (const int next = (int)units4_before(unit, Hkv, i + 1); c4 * per_cta4 < next; c4++) {
-            head->first4[c4] = i;
-            head->start4[c4] = q;
         }
     }
 }
@@ -268,9 +282,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
     }
     if (bad && blockIdx.x == 0) report(p.status, kStatusPlan);
     __syncthreads();
-    const int blocks = gridDim.x - p.schedulers;
+    const int blocks = gridDim.x - p.schedulers - (p.schedulers ? 1 : 0);
     if ((int)blockIdx.x >= blocks) {
-        build_schedule(p, cu, ctx, first, s_sums, &s_longest, &s_most_tokens, blockIdx.x - blocks, p.schedulers);
+        const int block = blockIdx.x - blocks;
+        if (block < p.schedulers)
+            build_schedule<false>(p, cu, ctx, first, s_sums, &s_longest, nullptr, block, p.schedulers);
+        else
+            build_schedule<true>(p, cu, ctx, first, s_sums, &s_longest, &s_most_tokens, 0, 1);
         return;
     }
     const int32_t T = cu[R];
@@ -452,7 +470,7 @@ cudaError_t launch_attn_plan(const nvfp4_step_t& step, int* status, int num_sms,
     if (step.heads) {
         const int64_t n = max_qtiles(step.requests, step.tokens, step.heads / step.kv_heads) / kPlanThreads;
         p.schedulers = (int)(n < 1 ? 1 : n > 16 ? 16 : n);
-        grid += p.schedulers;
+        grid += p.schedulers + 1;
     }
     p.ctas = num_sms < kAttnMaxCtas ? num_sms : kAttnMaxCtas;
     e = launch_programmatic(plan_kernel, dim3((unsigned)grid), dim3(kPlanThreads), smem, stream, p);
