@@ -691,8 +691,8 @@ typedef struct {
  *   cursor     [1] entries of free_pages already taken, or NULL: 0; cursor_out
  *              [1] or NULL: that plus the pages taken, may alias cursor.
  *   copy_src, copy_dst   int32 [n], device, out.
- * A pair left out, and a page that the free list did not have (the entry is
- * -1), record NVFP4_ERR_INVALID_ARG * 100 + 34.
+ * A pair left out, and a page that the free list did not have or that is no page
+ * (the entry is -1), record NVFP4_ERR_INVALID_ARG * 100 + 34.
  */
 int nvfp4_pages_fork(const nvfp4_pages_t* pages, const int32_t* src, const int32_t* dst, int64_t n,
                      const int32_t* free_pages, int64_t free_count, const int32_t* cursor, int32_t* cursor_out,

@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkParams p)
     for (int i = t * per; i < min(n, (t + 1) * per); i++) {
         if (at[i] < 0) continue;
         const int64_t f = cursor + before + at[i];
-        const int32_t page = f >= 0 && f < p.free_count ? p.free_pages[f] : -1;
+        int32_t page = f >= 0 && f < p.free_count ? p.free_pages[f] : -1;
+        if (page >= p.t.pages) page = -1;
         bad |= page < 0;
         at[i] = page < 0 ? -3 : page;  // -3: a page that the list did not have
     }

@@ -36,7 +36,7 @@ def on_gpu(nv, table, ctx, page, pages, cols):
 
 
 # -------------------------------------------------------------------- fork
-def fork_reference(table, ctx, page, cols, src, dst, free, cursor):
+def fork_reference(table, ctx, page, cols, src, dst, free, cursor, pages):
     table, ctx, copies, bad = table.copy(), list(ctx), [], False
     R = len(ctx)
     for i, (a, b) in enumerate(zip(src, dst)):
@@ -49,7 +49,7 @@ def fork_reference(table, ctx, page, cols, src, dst, free, cursor):
         new[:full] = table[a, :full]
         pair = (-1, -1)
         if rest:
-            if cursor < len(free):
+            if cursor < len(free) and 0 <= free[cursor] < pages:
                 pair = (int(table[a, full]), int(free[cursor]))
                 new[full] = free[cursor]
             else:
@@ -78,7 +78,7 @@ def check_fork(nv, table, ctx, page, cols, pages, src, dst, free, cursor=0, in_p
     else:
         call()
     torch.cuda.synchronize()
-    new, lens, copies, at, bad = fork_reference(table, ctx, page, cols, list(src), list(dst), free, cursor)
+    new, lens, copies, at, bad = fork_reference(table, ctx, page, cols, list(src), list(dst), free, cursor, pages)
     assert out.item() == at and t.ctx_len.tolist() == lens
     whole = t.block_table._base if t.block_table._base is not None else t.block_table
     assert np.array_equal(whole.cpu().numpy(), new)
@@ -127,6 +127,7 @@ def test_fork_leaves_out_what_it_cannot_do(nv):
         check_fork(nv, table, ctx, 16, 4, 40, src, dst, free)
     for count in (0, 1, 2):                                   # pages run out
         check_fork(nv, table, ctx, 16, 4, 40, [0, 1, 2], [5, 6, 7], free[:count])
+    check_fork(nv, table, ctx, 16, 4, 40, [0, 1, 2], [5, 6, 7], [int(free[0]), 40, -5])    # ids that are no pages
     check_fork(nv, table, ctx, 16, 4, 40, [], [], free, 3)
     with pytest.raises(ValueError):
         nv.nvfp4_pages_fork(on_gpu(nv, table, ctx, 16, 40, 4), i32([0]), i32([5, 6]), i32([1]), None, None, i32([0]), i32([0]))
