@@ -846,7 +846,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         const bool negate = a.scale < 0.0f;
         // a zero scale: any tiny factor gives equal probabilities, without 0 * inf at masked keys
         const float c = fmaxf(fabsf(a.scale) * (kScaled ? *a.k_g : 1.0f) * 1.4426950408889634f, 1.17549435e-38f);
-        const float v_g = kScaled ? *a.v_g : 1.0f;
         const float lazy = kLazy / c;
         uint32_t cnt = 0, ml_cnt = 0;      // steps done
         bool ok = true;
@@ -977,7 +976,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 // rows in the accumulator layout, four lanes to a row: 64
                 // contiguous bytes of 8 rows a store (a row a lane would be
                 // 16 bytes of 32 rows, four times the accesses)
-                const float inv = none ? 0.0f : 1.0f / l * v_g;
+                const float inv = none ? 0.0f : kScaled ? *a.v_g / l : 1.0f / l;
                 const uint32_t valid = __ballot_sync(0xffffffffu, mine), zero = __ballot_sync(0xffffffffu, none);
                 const int64_t at = tok * a.ldo + head * a.ho;
 #pragma unroll 1
@@ -1093,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 mall = top;
             }
             const float ms = mall == -INFINITY ? 0.0f : mall;
-            const float inv = lall == 0.0f ? 0.0f : 1.0f / lall * v_g;
+            const float inv = lall == 0.0f ? 0.0f : kScaled ? *a.v_g / lall : 1.0f / lall;
             const int64_t at = __shfl_sync(0xffffffffu, tok * a.ldo + head * a.ho, r);
             const int64_t lse_at = __shfl_sync(0xffffffffu, tok * a.heads + head, r);
             if (a.lse && r < rows && sub == 0)
