@@ -41,10 +41,10 @@
 // schedule, the block table, Q, the keys, one after the other, and every warp's
 // ring at once), 3 for the spread of the warps' ends, 2 to add up their shares, 4 to 5 for
 // the parts of other CTAs.  These two requests 54 us; 64 requests of 200 to 8192
-// keys 44 (bf16: 95); one of 333 keys 7.0.  With 9 to 16 rows a request 52 (64
+// keys 43 (bf16: 95); one of 333 keys 7.0.  With 9 to 16 rows a request 52 (64
 // requests of 200 to 4000 keys, 3 tokens each), with 17 to 32, where the softmax and
-// Q's fragments out of shared memory weigh as much as the codes, 104 (64 of 200 to
-// 8192, 1 to 4 tokens each).
+// Q's fragments out of shared memory weigh as much as the codes, 102 (64 of 200 to
+// 8192, 1 to 4 tokens each, and the launches that decide about bf16 pages).
 #include <cuda_fp16.h>
 
 #include "attn.h"
@@ -895,10 +895,20 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
     const ScheduleHead* head = a.sched;
     const QTile* tiles = schedule_tiles(head);
 
-    // the CTA's units u0 .. u1 - 1, this warp's v0 .. v1 - 1
+    // The CTA's units u0 .. u1 - 1 (its bounds moved to the edge of an item that they
+    // would cut too near it: the warps share what that leaves, or the last one would
+    // have up to eight chunks more than the others), this warp's v0 .. v1 - 1.
     const int per = head->per_cta4, units = head->units4, n_tiles = head->qtiles, begin = head->first4[cta];
     const QTile start = head->start4[cta];
-    const int u0 = min(cta * per, units), u1 = min(u0 + per, units), len = u1 - u0;
+    auto snapped = [&](int u, const QTile& t, int i) {
+        const int item = kItemUnits4 + kChunksOfTile * t.tiles, s = units4_before(t.unit0, Hkv, i);
+        const int at = s + (u - s) / item * item;          // the item that it cuts
+        return at + snap_unit4(u - at, item);
+    };
+    const int raw0 = min(cta * per, units), raw1 = min(raw0 + per, units);
+    const int u0 = raw0 < units ? snapped(raw0, start, begin) : units;
+    const int u1 = raw1 < units ? snapped(raw1, head->start4[cta + 1], head->first4[cta + 1]) : units;
+    const int len = u1 - u0;
     auto bound = [&](int w) { return u0 + len * w / C::kWarps; };
     const int v0 = bound(warp), v1 = bound(warp + 1);
     const bool final_warp = warp == C::kWarps - 1;
@@ -935,8 +945,8 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
         int qt = walk.qt, hk = walk.hk, s = walk.s;
         while (any && s < end) {
             const int chunks = kChunksOfTile * t.tiles, item = kItemUnits4 + chunks;
-            x.a = u0 <= s ? 0 : max(snap_unit4(u0 - s, item) - kItemUnits4, 0);
-            x.b = max(snap_unit4(min(u1 - s, item), item) - kItemUnits4, 0);
+            x.a = min(max(u0 - s - kItemUnits4, 0), chunks);
+            x.b = min(max(u1 - s - kItemUnits4, 0), chunks);
             x.x0 = warp == 0 ? x.a : min(max(v0 - s - kItemUnits4, x.a), x.b);
             x.x1 = final_warp ? x.b : min(max(v1 - s - kItemUnits4, x.a), x.b);
             if (x.x1 > x.x0) {
