@@ -41,7 +41,7 @@
 // schedule, the block table, Q, the keys, one after the other, and every warp's
 // ring at once), 3 for the spread of the warps' ends, 2 to add up their shares, 4 to 5 for
 // the parts of other CTAs.  These two requests 54 us; 64 requests of 200 to 8192
-// keys 43 (bf16: 95); one of 333 keys 7.0.  With 9 to 16 rows a request 52 (64
+// keys 42 (bf16: 95); one of 333 keys 7.0.  With 9 to 16 rows a request 52 (64
 // requests of 200 to 4000 keys, 3 tokens each), with 17 to 32, where the softmax and
 // Q's fragments out of shared memory weigh as much as the codes, 102 (64 of 200 to
 // 8192, 1 to 4 tokens each, and the launches that decide about bf16 pages).
@@ -177,6 +177,16 @@ __device__ __forceinline__ void copies_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
+// (x - m) * f + kLift of two rows, two operations in one instruction.
+__device__ __forceinline__ float2 exponent2(float x0, float x1, const float* minus_m, const float* f)
+{
+    float2 d;
+    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
+        " mov.b64 a, {%6, %7};\n mov.b64 c, {%8, %8};\n fma.rn.f32x2 d, d, a, c;\n mov.b64 {%0, %1}, d;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(x0), "f"(x1), "f"(minus_m[0]), "f"(minus_m[1]), "f"(f[0]), "f"(f[1]), "f"(kLift));
+    return d;
+}
 // Log of a row's sum of 2^(score - m + kLift), to base e.
 __device__ __forceinline__ float log_sum(float m, float l)
 {
@@ -188,7 +198,9 @@ __device__ __forceinline__ float log_sum(float m, float l)
 template <int kDP, int kNT>
 struct Rows {
     float o[kNT][kDP / 16][4];                 // two columns: one of rows 2j, 2j + 1, then the next of them
-    float m[kNT][2], nm[kNT][2];               // maximum (log2); kLift - maximum
+    // maximum (of the scores without their factor: the difference to it is right
+    // for scores of any size; from join_sums() on with it), minus that (0 where there is none)
+    float m[kNT][2], nm[kNT][2];
     float limit[kNT][2];                       // the score from which the maximum moves
     float l[kNT][2];                           // sum over this lane's keys
     float cf[kNT][2];                          // the row's factor of the scores
@@ -203,7 +215,7 @@ struct Rows {
             for (int y = 0; y < 2; y++) m[n][y] = limit[n][y] = -INFINITY, nm[n][y] = l[n][y] = 0.0f;
         }
     }
-    // The sums of a row's lanes.
+    // The sums of a row's lanes, and the maxima as log2.
     __device__ __forceinline__ void join_sums()
     {
 #pragma unroll
@@ -212,6 +224,7 @@ struct Rows {
             for (int y = 0; y < 2; y++) {
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l[n][y] += __shfl_xor_sync(0xffffffffu, l[n][y], x);
+                m[n][y] *= cf[n][y];
             }
         }
     }
@@ -342,11 +355,12 @@ __device__ __forceinline__ void work_halves(const uint8_t* st, int k0, const See
                 if (kH == 2) top = fmaxf(top, fmaxf(s[kH - 1][n][y], s[kH - 1][n][y + 2]));
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                top = fmaxf(top * w.cf[n][y], w.m[n][y]);
-                const float f = w.m[n][y] == -INFINITY ? 0.0f : ex2(w.m[n][y] - top);
+                top = fmaxf(top, w.m[n][y]);
+                const bool none = top == -INFINITY;
+                const float f = w.m[n][y] == -INFINITY ? 0.0f : ex2((w.m[n][y] - top) * w.cf[n][y]);
                 w.m[n][y] = top;
-                w.nm[n][y] = top == -INFINITY ? 0.0f : kLift - top;
-                w.limit[n][y] = __fdividef(top + kLazy, w.cf[n][y]);
+                w.nm[n][y] = none ? 0.0f : -top;
+                w.limit[n][y] = none ? -INFINITY : __fadd_rd(top, __fdividef(kLazy, w.cf[n][y]));
                 w.l[n][y] *= f;
 #pragma unroll
                 for (int x = 0; x < kSteps; x++) {
@@ -363,9 +377,12 @@ __device__ __forceinline__ void work_halves(const uint8_t* st, int k0, const See
         for (int n = 0; n < kNT; n++) {
             float e[4];
 #pragma unroll
-            for (int y = 0; y < 4; y++) {
-                e[y] = ex2(fmaf(s[h][n][y], w.cf[n][y & 1], w.nm[n][y & 1]));
-                w.l[n][y & 1] += e[y];
+            for (int y = 0; y < 4; y += 2) {
+                const float2 x = exponent2(s[h][n][y], s[h][n][y + 1], w.nm[n], w.cf[n]);
+                e[y] = ex2(x.x);
+                e[y + 1] = ex2(x.y);
+                w.l[n][0] += e[y];
+                w.l[n][1] += e[y + 1];
             }
             pt[h][n][0] = transpose8x8(cvt_f16x2(e[0], e[1]));
             pt[h][n][1] = transpose8x8(cvt_f16x2(e[2], e[3]));
@@ -1215,7 +1232,7 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
     __syncthreads();
     // Shares of warps where there are several items for each CTA, or long ones: one
     // join at the end, whatever the items' lengths (64 requests of 200 to 8192 keys
-    // 43 us, 70 with all warps on one item at a time; a request of 131071 with one of
+    // 42 us, 70 with all warps on one item at a time; a request of 131071 with one of
     // 65537 53 and 56).  Else all warps at once on a CTA's one part, which is
     // joined faster (a request of 333 keys 6.9 us, 8.8; 8 of 2000 13.3, 19.1).
     const int64_t items = (int64_t)a.sched->qtiles * a.kv_heads;

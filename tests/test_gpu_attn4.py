@@ -189,6 +189,42 @@ def test_scores_of_all_sizes(nv, ws, std, scale, k_g):
         run(nv, ws, [150, 61], [n, n], 10, 2, 64, 16, std=std, scale=scale, k_g=k_g, expanded=expanded)
 
 
+@pytest.mark.parametrize("q_len", [1, 2, 5])
+@pytest.mark.parametrize("L", [300, 9000])
+def test_scores_beyond_binary32s_whole_numbers(nv, ws, L, q_len):
+    """Scores of 10^9 and more, where neighbours in binary32 are 64 apart: a row whose
+    largest score is alone gives that key's value.  The products' sums are off by less
+    than D 2^-24 of sum |q_i k_i|; two scores that far apart and 200 more leave e^-200."""
+    H, Hkv, D = 8, 4, 64
+    gen = torch.Generator("cuda").manual_seed(L)
+    pages = -(-(L + q_len) // 16)
+    cache = random_cache4(nv, gen, pages, Hkv, 16, D, 2.0 ** 2)
+    plan = plan_of(nv, [q_len], [L], H, Hkv, 16, pages)
+    q = (torch.randn(q_len, H, D, device="cuda", generator=gen) * 2e7).bfloat16()
+    out, lse = torch.empty_like(q), torch.empty(q_len, H, device="cuda")
+    nv.nvfp4_attn_paged4(q, cache, plan, out, ws, lse=lse)
+    k, v = values(cache)
+    at = torch.arange(L + q_len, device="cuda")
+    pg, row = plan.block_table[0].long()[at // 16], at % 16
+    keys, vals = k[pg, :, row], v[pg, :, row]
+    alone = 0
+    for t in range(q_len):
+        for h in range(H):
+            n, x = L + t + 1, q[t, h].double()
+            products = keys[:n, h // 2] * x * D ** -0.5
+            s = products.sum(1)
+            top = s.topk(2)
+            gap = 2 * D * 2.0 ** -24 * products.abs().sum(1).max() + 200
+            if top.values[0] - top.values[1] < gap:
+                continue
+            alone += 1
+            want = vals[top.indices[0], h // 2]
+            assert top.values[0] > 1e9
+            assert ((out[t, h].double() - want).abs() <= 2.0 ** -8 * want.abs()).all(), (t, h)
+            assert abs(lse[t, h].double() - top.values[0]) <= gap / 2 + 2.0 ** -22 * top.values[0]
+    assert alone >= H * q_len // 2
+
+
 def test_rising_scores(nv, ws):
     """Scores that rise (or fall) along the keys: the running maximum moves at every group."""
     L, D = 1500, 64
