@@ -1124,16 +1124,19 @@ int nvfp4_pages_fork(const nvfp4_pages_t* pages, const int32_t* src, const int32
     for (const int32_t* x : {src, dst, free_pages, cursor, (const int32_t*)cursor_out, (const int32_t*)copy_src,
                              (const int32_t*)copy_dst})
         if (!aligned(x, 4)) return NVFP4_ERR_MISALIGNED;
-    // what some blocks write while others read
-    const int64_t words = table_words(pages, pages->table_ld), R = pages->requests;
-    for (const int32_t* in : {src, dst})
-        if (overlap(in, n, copy_src, n) || overlap(in, n, copy_dst, n) || overlap(in, n, cursor_out, 1) ||
-            overlap(in, n, pages->ctx_len, R) || overlap(in, n, pages->block_table, words))
-            return NVFP4_ERR_INVALID_ARG;
-    if (overlap(pages->ctx_len, R, copy_src, n) || overlap(pages->ctx_len, R, copy_dst, n) ||
-        overlap(pages->ctx_len, R, cursor_out, 1) || overlap(free_pages, free_count, pages->block_table, words) ||
-        overlap(pages->ctx_len, R, pages->block_table, words))
-        return NVFP4_ERR_INVALID_ARG;
+    // what some blocks write while others read, or two write
+    const int64_t R = pages->requests;
+    struct Words { const int32_t* at; int64_t n; };
+    const Words out[5] = {{pages->block_table, table_words(pages, pages->table_ld)}, {pages->ctx_len, R},
+                          {copy_src, n}, {copy_dst, n}, {cursor_out, 1}};
+    const Words in[4] = {{src, n}, {dst, n}, {free_pages, free_count}, {cursor, 1}};
+    for (int i = 0; i < 5; i++) {
+        for (int j = 0; j < i; j++)
+            if (overlap(out[i].at, out[i].n, out[j].at, out[j].n)) return NVFP4_ERR_INVALID_ARG;
+        for (const Words& x : in)
+            if (overlap(out[i].at, out[i].n, x.at, x.n) && !(out[i].at == cursor_out && cursor_out == cursor && x.at == cursor))
+                return NVFP4_ERR_INVALID_ARG;
+    }
     DeviceInfo* d = nullptr;
     NVFP4_TRY(device_info(&d));
     NVFP4_CUDA(launch_pages_fork(*pages, src, dst, n, free_pages, free_count, cursor, cursor_out, copy_src, copy_dst,

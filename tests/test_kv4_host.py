@@ -120,7 +120,9 @@ def test_fork_refusals(nv):
         L.nvfp4_pages_fork(pages(nv), src, dst, n, free, count, cursor, out, cs, cd, None)
     for bad in (dict(src=None), dict(dst=None), dict(n=-1), dict(n=5), dict(count=-1), dict(cs=None), dict(cd=None),
                 dict(cs=B[1]), dict(cd=B[1] + 4), dict(cs=B[2]), dict(out=B[1]), dict(src=B[0]), dict(dst=A + 8),
-                dict(cs=B[0] + 12), dict(out=B[0]), dict(free=A)):
+                dict(cs=B[0] + 12), dict(out=B[0]), dict(free=A), dict(free=B[4]), dict(free=B[5] - 8),
+                dict(cs=B[5] + 4), dict(out=B[4]), dict(out=B[3] + 36), dict(cursor=B[5]), dict(cursor=B[0] + 4),
+                dict(cs=A + 8), dict(out=A)):
         assert call(**bad) == INVALID, bad
     for bad in (dict(src=B[1] + 2), dict(dst=B[2] + 1), dict(free=B[3] + 2), dict(cursor=B[6] + 2), dict(out=B[6] + 2),
                 dict(cs=B[4] + 2), dict(cd=B[5] + 2)):
