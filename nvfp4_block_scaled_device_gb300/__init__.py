@@ -718,7 +718,7 @@ def nvfp4_qk_norm_rope(q, k, q_norm=None, k_norm=None, pos=None, cos_t=None, sin
                 st != sin_t.stride() or st[1] != 1 or cos_t.get_device() != here or sin_t.get_device() != here:
             raise ValueError("cos_t and sin_t must be row-major float32 2-D tensors of one shape on the current CUDA device")
         rows, width = shape
-        p, c, s, ld = _ints_of(pos, tokens, "pos", here), cos_t.data_ptr(), sin_t.data_ptr(), max(st[0], width)
+        p, c, s, ld = _ints_of(pos, tokens, "pos", here), cos_t.data_ptr(), sin_t.data_ptr(), st[0] if rows > 1 else width
         if rope_dim is None:
             rope_dim = 2 * width
         elif rope_dim > 2 * width:

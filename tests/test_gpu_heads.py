@@ -330,6 +330,9 @@ def test_refusals(nv):
             nv.nvfp4_qk_norm_rope(**args)
     with pytest.raises(nv.NVFP4Error):
         nv.nvfp4_qk_norm_rope(x, x, w, w, pos, cos, cos, rope_dim=24, halves=True)
+    one = cos[:1].expand(8, 32)                               # rows that are one: no table of 8
+    with pytest.raises(nv.NVFP4Error):
+        nv.nvfp4_qk_norm_rope(x, x, w, w, pos, one, one)
     with pytest.raises(ValueError):
         nv.nvfp4_kv4_append(x, x[:3], plan, cache)
     with pytest.raises(nv.NVFP4Error):
