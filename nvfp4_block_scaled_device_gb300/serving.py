@@ -92,7 +92,7 @@ class ServingLayer:
         dev = attn_norm.device
         # prompts over a 4-bit cache: bf16 pages, taken out once per layer and step
         self.four = isinstance(cache, KVCache4)
-        expands = self.four and -(-T // plan.requests) * (heads // kv_heads) >= _EXPAND_ROWS
+        self.expands = expands = self.four and -(-T // plan.requests) * (heads // kv_heads) >= _EXPAND_ROWS
         if scratch is None:
             scratch = {
                 "h": NVFP4Tensor.empty(T, H, dev), "a": NVFP4Tensor.empty(T, heads * D, dev),
@@ -141,7 +141,7 @@ class ServingLayer:
         # nothing of an earlier step is left in them
         if self.four:
             nvfp4_attn_paged4(q, cache, plan, a, s["ws_attn"], stream=stream, zero_padding=True,
-                              expanded=s.get("expanded"))
+                              expanded=s["expanded"] if self.expands else None)
         elif cache is not None:
             nvfp4_attn_paged(q, cache, plan, a, s["ws_attn"], stream=stream, zero_padding=True)
         else:
