@@ -91,6 +91,52 @@ __device__ __forceinline__ uint32_t amax_bf16x2(uint32_t a, uint32_t b)
     return r;
 }
 
+// Scales of a cache's blocks: 6 g and its correctly rounded reciprocal.
+struct BlockScale {
+    float g, d, rd;
+};
+__device__ __forceinline__ BlockScale block_scale(float g)
+{
+    const float d = __fmul_rn(6.0f, g);
+    return BlockScale{g, d, __frcp_rn(d)};
+}
+
+// One block's scale and codes, nvfp4_quantize's bit for bit: each lane has kVecs
+// vectors of it (8 columns), amax is the block's, *sc its scale.  The quotients v /
+// den are those of div_by_recip in pairs of columns, negated (q = -v y, q + (v + q
+// den) (-y): the remainder's sign needs no operation, and a zero keeps the sign
+// that the codes' XOR then turns around).
+template <int kVecs>
+__device__ __forceinline__ void quant_block(const uint4* x, uint32_t amax_bits, const BlockScale& b, uint32_t* codes, uint32_t* sc)
+{
+    float amax = bf16_lo(amax_bits);
+    constexpr float kMost = 3.3895313892515355e38f;                  // of bf16
+    const bool odd = !(amax <= kMost), nan = amax != amax;           // an infinity or NaN in it
+    if (odd) amax = kMost;
+    const uint32_t s = cvt_e4m3(div_by_recip(amax, b.d, b.rd));
+    const float den = __fmul_rn(e4m3_to_f32(s), b.g);
+    const float ny = -__frcp_rn(s ? den : 1.0f);
+    const float2 ny2 = make_float2(ny, ny), den2 = make_float2(den, den);
+#pragma unroll
+    for (int i = 0; i < kVecs; i++) {
+        float2 v[4];
+        unpack4(x[i], v);
+        if (odd) {
+#pragma unroll
+            for (int y = 0; y < 4; y++)
+                v[y] = make_float2(fminf(fmaxf(v[y].x, -kMost), kMost), fminf(fmaxf(v[y].y, -kMost), kMost));
+        }
+        float q[8];
+#pragma unroll
+        for (int y = 0; y < 4; y++) {
+            const float2 z = mul2(v[y], ny2), r = fma2(fma2(z, den2, v[y]), ny2, z);
+            q[2 * y] = r.x, q[2 * y + 1] = r.y;
+        }
+        codes[i] = s == 0 || nan ? 0u : cvt_e2m1x8(q) ^ 0x88888888u;
+    }
+    *sc = nan ? 0x7fu : s;
+}
+
 // n table entries from `at` on (n 4 or 8).
 template <int kN>
 __device__ __forceinline__ void load_table(const float* t, int64_t at, bool wide, float* out)
@@ -144,6 +190,7 @@ struct HeadMath {
 template <int kTo, int kRope, bool kNorm, bool kWhole>
 __device__ __forceinline__ void work_rows(HeadRows& q, int batches, const HeadMath& h)
 {
+    const BlockScale scale = block_scale(kTo == kToCache4 ? q.g : 1.0f);
 #pragma unroll 1
     for (;;) {
         uint4 x[kHeadBatch];
@@ -207,21 +254,8 @@ __device__ __forceinline__ void work_rows(HeadRows& q, int batches, const HeadMa
                 uint32_t m = amax_bf16x2(amax_bf16x2(y.x, y.y), amax_bf16x2(y.z, y.w));
                 m = amax_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = amax_bf16x2(m, m >> 16 | m << 16);
-                float2 v[4];
-                float z[8];
-                unpack4(y, v);
-#pragma unroll
-                for (int k = 0; k < 4; k++) z[2 * k] = v[k].x, z[2 * k + 1] = v[k].y;
-                float amax = bf16_lo(m);
-                const bool nan = amax != amax;
-                constexpr float kMost = 3.3895313892515355e38f;          // of bf16
-                if (!(amax <= kMost)) {
-                    amax = kMost;
-#pragma unroll
-                    for (int k = 0; k < 8; k++) z[k] = fminf(fmaxf(z[k], -kMost), kMost);
-                }
-                uint32_t sc, codes = quant_half_block(z, q.g, amax, &sc);
-                if (nan) sc = 0x7f, codes = 0;
+                uint32_t sc, codes;
+                quant_block<1>(&y, m, scale, &codes, &sc);
                 if (here) {
                     *reinterpret_cast<uint32_t*>(q.codes + (uint64_t)i * q.step_codes) = codes;
                     if (h.scale_lane) q.sf[(uint64_t)i * q.step_sf] = (uint8_t)sc;
@@ -240,6 +274,64 @@ __device__ __forceinline__ void work_rows(HeadRows& q, int batches, const HeadMa
     }
 }
 
+// Rows as they are into the 4-bit cache: unit u of token t's rows of k or v, `per`
+// times kHeadBatch rows for each that L lanes of 8 columns would have.  A lane has a
+// whole block of 16 columns (so that what is done once per block is done once) of
+// two rows at a time.
+__device__ __forceinline__ void append_rows(const HeadsParams& p, uint32_t t, bool is_v, int u, int lane, int L, int D)
+{
+    const nvfp4_heads_t& h = p.h;
+    const int lanes = L / 2, at_once = 32 / lanes, col = 16 * (lane & (lanes - 1));
+    const int first = u * p.per * (kHeadBatch / 2) * at_once, end = min((int)h.kv_heads, first + p.per * (kHeadBatch / 2) * at_once);
+    const int64_t slots = p.c4.pages << p.page_shift, slot = h.slot[t];
+    if (slot < 0 || slot >= slots) {
+        if (slot != -1 && lane == 0 && u == 0) report(p.status, kStatusSlot);
+        return;
+    }
+    if (col >= D) return;
+    const int64_t page = slot >> p.page_shift, pitch = is_v ? h.hv : h.hk;
+    const uint32_t in_page = (uint32_t)slot & ((1u << p.page_shift) - 1);
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? h.v : h.k) + t * (is_v ? h.ldv : h.ldk) + col;
+    uint8_t* codes = (is_v ? p.c4.v : p.c4.k) + page * p.c4.page_stride + col / 2;
+    uint8_t* sf = (is_v ? p.c4.v_sf : p.c4.k_sf) + page * p.c4.sf_stride + col / 16;
+    const BlockScale scale = block_scale(*(is_v ? p.c4.v_g : p.c4.k_g));
+#pragma unroll 1
+    for (int r = first + lane / lanes; r < end; r += 2 * at_once) {
+        uint4 x[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const uint4* from = reinterpret_cast<const uint4*>(src + (r + i * at_once) * pitch);
+#pragma unroll
+            for (int y = 0; y < 2; y++) x[i][y] = i == 0 || r + at_once < end ? from[y] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            if (i && r + at_once >= end) break;
+            uint32_t m = amax_bf16x2(amax_bf16x2(amax_bf16x2(x[i][0].x, x[i][0].y), amax_bf16x2(x[i][0].z, x[i][0].w)),
+                                     amax_bf16x2(amax_bf16x2(x[i][1].x, x[i][1].y), amax_bf16x2(x[i][1].z, x[i][1].w)));
+            m = amax_bf16x2(m, m >> 16 | m << 16);
+            uint32_t w[2], sc;
+            quant_block<2>(x[i], m, scale, w, &sc);
+            const uint32_t at = ((uint32_t)(r + i * at_once) << p.page_shift) + in_page;
+            *reinterpret_cast<uint2*>(codes + (uint64_t)at * (D / 2)) = make_uint2(w[0], w[1]);
+            sf[(uint64_t)at * (D / 16)] = (uint8_t)sc;
+        }
+    }
+}
+
+// nvfp4_kv4_append.
+template <bool kWhole>
+__global__ void __launch_bounds__(kHeadThreads, kHeadBlocks) append_kernel(const __grid_constant__ HeadsParams p)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const uint32_t unit = blockIdx.x * kHeadWarps + (threadIdx.x >> 5), t = unit / (uint32_t)p.units;
+    if (t >= p.h.tokens) return;
+    const int u = (int)(unit - t * p.units);
+    const bool is_v = u >= p.units_k;
+    append_rows(p, t, is_v, is_v ? u - p.units_k : u, threadIdx.x & 31, kWhole ? 16 : p.lanes, kWhole ? 128 : (int)p.h.head_dim);
+}
+
 template <int kTo, int kRope, bool kWhole>
 __global__ void __launch_bounds__(kHeadThreads, kHeadBlocks) heads_kernel(const __grid_constant__ HeadsParams p)
 {
@@ -255,6 +347,10 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadBlocks) heads_kernel(const 
     int u = (int)(unit - t * p.units);
     const bool is_q = u < p.units_q, is_v = kTo != kToRows && u >= p.units_q + p.units_k;
     u -= is_q ? 0 : is_v ? p.units_q + p.units_k : p.units_q;
+    if (kTo == kToCache4 && is_v) {
+        append_rows(p, t, true, u, lane, L, D);
+        return;
+    }
     const int rows = (int)(is_q ? h.heads : h.kv_heads), r0 = u * p.per * kHeadBatch * at_once + sub;
     const int64_t pitch = is_q ? h.hq : is_v ? h.hv : h.hk, ld = is_q ? h.ldq : is_v ? h.ldv : h.ldk;
     HeadRows q = {};
@@ -278,11 +374,14 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadBlocks) heads_kernel(const 
             q.out = ok ? static_cast<__nv_bfloat16*>(is_v ? p.c.v : p.c.k) + page * p.c.page_stride + at * D + col : nullptr;
             q.step_out = (int64_t)(at_once << p.page_shift) * D;
         } else {
-            q.codes = ok ? (is_v ? p.c4.v : p.c4.k) + page * p.c4.page_stride + at * (D / 2) + col / 2 : nullptr;
-            q.sf = (is_v ? p.c4.v_sf : p.c4.k_sf) + page * p.c4.sf_stride + at * (D / 16) + col / 16;
+            q.also = rows_out;
+            q.step_also = q.step_out;
+            q.out = nullptr;
+            q.codes = ok ? p.c4.k + page * p.c4.page_stride + at * (D / 2) + col / 2 : nullptr;
+            q.sf = p.c4.k_sf + page * p.c4.sf_stride + at * (D / 16) + col / 16;
             q.step_codes = (at_once << p.page_shift) * (D / 2);
             q.step_sf = (at_once << p.page_shift) * (D / 16);
-            q.g = *(is_v ? p.c4.v_g : p.c4.k_g);
+            q.g = *p.c4.k_g;
         }
     }
     HeadMath m;
@@ -291,7 +390,7 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadBlocks) heads_kernel(const 
     m.eps = h.eps;
     m.scale_lane = (col & 8) == 0;
     const __nv_bfloat16* weight = static_cast<const __nv_bfloat16*>(is_q ? h.q_norm : is_v ? nullptr : h.k_norm);
-    if (kTo != kToRows && is_v) {
+    if (kTo == kToCache && is_v) {
         work_rows<kTo, kNoRope, false, kWhole>(q, p.per, m);
         return;
     }
@@ -371,6 +470,8 @@ cudaError_t run_heads(HeadsParams& p, int num_sms, cudaStream_t stream)
     const dim3 grid((unsigned)blocks), block(kHeadThreads);
     const bool rope = p.h.pos, whole = p.h.head_dim == 128 && (!rope || p.h.rope_dim == 128);
     auto go = [&](void (*kernel)(HeadsParams)) { return launch_programmatic(kernel, grid, block, 0, stream, p); };
+    if (kTo == kToCache4 && !p.h.heads && !rope && !p.h.k_norm && !p.h.k_out)
+        return p.h.head_dim == 128 ? go(append_kernel<true>) : go(append_kernel<false>);
     if (!rope) return whole ? go(heads_kernel<kTo, kNoRope, true>) : go(heads_kernel<kTo, kNoRope, false>);
     if (p.h.halves) return whole ? go(heads_kernel<kTo, kHalves, true>) : go(heads_kernel<kTo, kHalves, false>);
     return whole ? go(heads_kernel<kTo, kPairs, true>) : go(heads_kernel<kTo, kPairs, false>);
