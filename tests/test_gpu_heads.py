@@ -337,3 +337,34 @@ def test_refusals(nv):
         nv.nvfp4_kv4_append(x, x[:3], plan, cache)
     with pytest.raises(nv.NVFP4Error):
         nv.nvfp4_kv4_expand(cache, plan, nv.KVCache.empty(5, 2, 16, 64))
+
+
+def test_cache_whose_offsets_pass_32_bits(nv):
+    """Pages 1 GB apart: rows behind 4 GB are written, expanded, attended and copied as others."""
+    Hkv, page, D, T, pages = 2, 16, 64, 75, 7
+    gen = torch.Generator("cuda").manual_seed(9)
+    far, stride = [], 10 ** 9
+    for n in (D // 2, D // 2, D // 16, D // 16):
+        flat = torch.empty((pages - 1) * stride + Hkv * page * n, dtype=torch.uint8, device="cuda")
+        far.append(flat.as_strided((pages, Hkv, page, n), (stride, page * n, n, 1)))
+    assert (pages - 2) * stride > 2 ** 32
+    near = nv.KVCache4.empty(pages, Hkv, page, D)
+    far = nv.KVCache4(*far, near.k_g, near.v_g)
+    plan = plan_of(nv, [T], [0], 4, Hkv, page, pages)
+    plan.block_table[0, :5] = i32([6, 1, 5, 0, 4])
+    nv.nvfp4_attn_plan(plan, i32([T]), i32([0]))
+    q = torch.randn(T, 4, D, device="cuda", generator=gen).bfloat16()
+    k, v = (torch.randn(T, Hkv, D, device="cuda", generator=gen).bfloat16() for _ in range(2))
+    ws, got = nv.workspace(nv.attn_workspace_bytes()), []
+    for cache in (near, far):
+        nv.nvfp4_kv4_append(k, v, plan, cache)
+        nv.nvfp4_qk_norm_rope(None, k[:, :, :].clone(), v=v, plan=plan, cache=cache)
+        nv.nvfp4_pages_copy(cache, i32([6, 5]), i32([3, 2]))
+        out, rows = torch.empty_like(q), nv.KVCache(*(torch.zeros(pages, Hkv, page, D, device="cuda").bfloat16() for _ in range(2)))
+        nv.nvfp4_attn_paged4(q, cache, plan, out, ws)
+        nv.nvfp4_kv4_expand(cache, plan, rows)
+        got.append((out, rows.k, rows.v, *(x[[6, 1, 5, 0, 3, 2]] for x in (cache.k, cache.v, cache.k_sf, cache.v_sf))))
+    assert nv.device_status() == 0
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert (got[0][0].float().abs().sum() > 0) and torch.equal(far.k[3], far.k[6])
