@@ -41,7 +41,7 @@
 // schedule, the block table, Q, the keys, one after the other, and every warp's
 // ring at once), 3 for the spread of the warps' ends, 2 to add up their shares, 4 to 5 for
 // the parts of other CTAs.  These two requests 54 us; 64 requests of 200 to 8192
-// keys 42 (bf16: 95); one of 333 keys 7.0.  With 9 to 16 rows a request 52 (64
+// keys 42 (bf16: 95); one of 333 keys 7.0.  With 9 to 16 rows a request 50 (64
 // requests of 200 to 4000 keys, 3 tokens each), with 17 to 32, where the softmax and
 // Q's fragments out of shared memory weigh as much as the codes, 102 (64 of 200 to
 // 8192, 1 to 4 tokens each, and the launches that decide about bf16 pages).
@@ -69,7 +69,9 @@ struct Cfg4 {
     static constexpr int kStages = kNT == 1 ? 2 : 3;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRows = 8 * kNT;
-    static constexpr int kAtOnce = kNT == 1 ? 2 : 1;             // halves of a chunk worked on together
+    // halves of a chunk worked on together (two tiles: 64 requests of 2 tokens 60.5 us,
+    // 63.5 with one after the other; four do not have the registers for it)
+    static constexpr int kAtOnce = kNT <= 2 ? 2 : 1;
     static constexpr int kRowBytes = kDP / 2;
     static constexpr int kCodes = kHalf * kRowBytes;             // of K or V of half a chunk
     static constexpr int kScales = kHalf * kDP / 16;
@@ -1227,6 +1229,11 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
     if (!kFull)                                 // the columns that no copy writes are zeros
         for (int i = threadIdx.x; i < C::kMostRing / 16; i += C::kThreads)
             reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x < 3) {                      // what every warp reads first, on its way into L2 meanwhile
+        const ScheduleHead* h = a.sched;
+        const void* at = threadIdx.x == 0 ? (const void*)h : threadIdx.x == 1 ? (const void*)&h->first4[cta] : (const void*)&h->start4[cta];
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+    }
     griddep_wait();
     if (a.skip_few && !a.sched->few_passes) return;
     __syncthreads();
@@ -1234,7 +1241,7 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
     // join at the end, whatever the items' lengths (64 requests of 200 to 8192 keys
     // 42 us, 70 with all warps on one item at a time; a request of 131071 with one of
     // 65537 53 and 56).  Else all warps at once on a CTA's one part, which is
-    // joined faster (a request of 333 keys 6.9 us, 8.8; 8 of 2000 13.3, 19.1).
+    // joined faster (a request of 333 keys 7.0 us, 8.8; 8 of 2000 13.3, 19.1).
     const int64_t items = (int64_t)a.sched->qtiles * a.kv_heads;
     const int per = a.sched->per_cta4;
     if (per > 0 && a.sched->most_tokens * a.group <= C::kRows && (2 * items >= 3 * (int)gridDim.x || per >= 256))
