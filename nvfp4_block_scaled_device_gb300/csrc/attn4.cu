@@ -549,48 +549,58 @@ struct Ring {
     }
 };
 
-// The parts of an item that CTAs share, added up by all threads of the last of
-// them: part i is in slot 2 (cta0 + i), the first in 2 cta0 + 1.
-template <int kDP, int kThreads>
-__device__ __forceinline__ void join_parts(const AttnArgs& a, int cta0, int parts, int rows, int tok0, int hk, float v_g)
+// The parts of an item that CTAs share, added up by threads [thread0, thread0 +
+// threads) of the last of them: part i is in slot 2 (cta0 + i), the first in 2 cta0 + 1.
+// A thread adds four columns of a row; the parts' reads are on their way together.
+constexpr int kJoinBatch = 12;
+
+template <int kDP>
+__device__ __forceinline__ void join_parts(const AttnArgs& a, int thread0, int threads, int cta0, int parts, int rows, int tok0,
+                                           int hk, float v_g)
 {
     auto slot_of = [&](int i) { return a.partials + (2 * (cta0 + i) + (i == 0 ? 1 : 0)) * kAttnSlotFloats; };
-    for (int x = threadIdx.x; x < rows * (kDP / 2); x += kThreads) {
-        const int r = x / (kDP / 2), col = 2 * (x % (kDP / 2));
+    for (int x = (int)threadIdx.x - thread0; x < rows * (kDP / 4); x += threads) {
+        const int r = x / (kDP / 4), col = 4 * (x % (kDP / 4));
         if (col >= a.head_dim) continue;
         const int t = r / a.group, head = hk * a.group + r - t * a.group;
         float top = -INFINITY, sum = 0.0f;
-        float2 acc = make_float2(0.0f, 0.0f);
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-        for (int i0 = 0; i0 < parts; i0 += 16) {
-            float2 ml[16], e[16];
+        for (int i0 = 0; i0 < parts; i0 += kJoinBatch) {
+            float2 ml[kJoinBatch];
+            float4 e[kJoinBatch];
 #pragma unroll
-            for (int u = 0; u < 16; u++) {
-                const float* from = slot_of(min(i0 + u, parts - 1));
-                ml[u] = __ldcg(reinterpret_cast<const float2*>(from + kAttnSlotRows * kDP + 2 * r));
-                e[u] = __ldcg(reinterpret_cast<const float2*>(from + r * kDP + col));
-                if (i0 + u >= parts) ml[u] = make_float2(-INFINITY, 0.0f);
+            for (int u = 0; u < kJoinBatch; u++) {
+                ml[u] = make_float2(-INFINITY, 0.0f);
+                e[u] = acc;
+                if (i0 + u < parts) {
+                    const float* from = slot_of(i0 + u);
+                    ml[u] = __ldcg(reinterpret_cast<const float2*>(from + kAttnSlotRows * kDP + 2 * r));
+                    e[u] = __ldcg(reinterpret_cast<const float4*>(from + r * kDP + col));
+                }
             }
             float most = top;
 #pragma unroll
-            for (int u = 0; u < 16; u++) most = fmaxf(most, ml[u].x);
+            for (int u = 0; u < kJoinBatch; u++) most = fmaxf(most, ml[u].x);
             const float f0 = top == -INFINITY ? 0.0f : ex2(top - most);
-            acc.x *= f0;
-            acc.y *= f0;
+            acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
             sum *= f0;
             top = most;
 #pragma unroll
-            for (int u = 0; u < 16; u++) {
+            for (int u = 0; u < kJoinBatch; u++) {
                 if (ml[u].y == 0.0f) continue;             // no key of this part
                 const float f = ml[u].x == -INFINITY ? 0.0f : ex2(ml[u].x - top);
                 acc.x += f * e[u].x;
                 acc.y += f * e[u].y;
+                acc.z += f * e[u].z;
+                acc.w += f * e[u].w;
                 sum += f * ml[u].y;
             }
         }
         const float inv = sum == 0.0f ? 0.0f : v_g / sum;
-        *reinterpret_cast<uint32_t*>(a.out + (int64_t)(tok0 + t) * a.ldo + (int64_t)head * a.ho + col) =
-            sum == 0.0f ? 0u : cvt_bf16x2(acc.x * inv, acc.y * inv);
+        *reinterpret_cast<uint2*>(a.out + (int64_t)(tok0 + t) * a.ldo + (int64_t)head * a.ho + col) =
+            sum == 0.0f ? make_uint2(0u, 0u)
+                        : make_uint2(cvt_bf16x2(acc.x * inv, acc.y * inv), cvt_bf16x2(acc.z * inv, acc.w * inv));
         if (col == 0 && a.lse)
             a.lse[(int64_t)(tok0 + t) * a.heads + head] = log_sum(top, sum);
     }
@@ -865,7 +875,7 @@ __device__ __forceinline__ void passes_together(const Params4& prm, uint8_t* sme
         const bool mine_to_join = s_last;
         __syncthreads();
         if (!mine_to_join) continue;
-        join_parts<kDP, C::kThreads>(a, cta0, parts, rows, tok0, hk, v_g);
+        join_parts<kDP>(a, 0, C::kThreads, cta0, parts, rows, tok0, hk, v_g);
     }
 }
 
@@ -1211,10 +1221,13 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
         if (x.last) *ticket = 0;
     }
     __syncthreads();
-    for (int i = 0; i < 2; i++) {
-        const Share& x = s_share[i];
-        if (x.valid && x.last) join_parts<kDP, C::kThreads>(a, x.cta0, x.parts, x.rows, x.tok0, x.hk, v_g);
-    }
+    // (the CTA that ends last often has both to join: half of its threads each)
+    const bool join0 = s_share[0].valid && s_share[0].last, join1 = s_share[1].valid && s_share[1].last;
+    if (!join0 && !join1) return;
+    const int half = C::kThreads / 2, second = join0 && join1 ? tid >= half : join1;
+    const Share& x = s_share[second];
+    join_parts<kDP>(a, join0 && join1 && second ? half : 0, join0 && join1 ? half : C::kThreads, x.cta0, x.parts, x.rows, x.tok0,
+                    x.hk, v_g);
 }
 
 template <int kDP, int kNT, bool kFull>
