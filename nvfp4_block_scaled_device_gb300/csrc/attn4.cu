@@ -551,59 +551,85 @@ struct Ring {
 
 // The parts of an item that CTAs share, added up by threads [thread0, thread0 +
 // threads) of the last of them: part i is in slot 2 (cta0 + i), the first in 2 cta0 + 1.
-// A thread adds four columns of a row; the parts' reads are on their way together.
-constexpr int kJoinBatch = 12;
-
+// A thread adds four columns of a row, of kX rows at a time, kB parts of each at a
+// time: their reads are on their way together.
+template <int kDP, int kX, int kB>
+__device__ __forceinline__ void join_some(const AttnArgs& a, int thread0, int threads, int cta0, int parts, int rows, int tok0,
+                                          int hk, float v_g)
+{
+    auto slot_of = [&](int i) { return a.partials + (2 * (cta0 + i) + (i == 0 ? 1 : 0)) * kAttnSlotFloats; };
+    const int n = rows * (kDP / 4);
+#pragma unroll 1
+    for (int x0 = (int)threadIdx.x - thread0; x0 < n; x0 += kX * threads) {
+        float top[kX], sum[kX];
+        float4 acc[kX];
+#pragma unroll
+        for (int y = 0; y < kX; y++) {
+            top[y] = -INFINITY;
+            sum[y] = 0.0f;
+            acc[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll 1
+        for (int i0 = 0; i0 < parts; i0 += kB) {
+            float2 ml[kX][kB];
+            float4 e[kX][kB];
+#pragma unroll
+            for (int y = 0; y < kX; y++) {
+                const int x = x0 + y * threads, r = x / (kDP / 4), col = 4 * (x % (kDP / 4));
+#pragma unroll
+                for (int u = 0; u < kB; u++) {
+                    ml[y][u] = make_float2(-INFINITY, 0.0f);
+                    e[y][u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (i0 + u < parts && x < n) {
+                        const float* from = slot_of(i0 + u);
+                        ml[y][u] = __ldcg(reinterpret_cast<const float2*>(from + kAttnSlotRows * kDP + 2 * r));
+                        e[y][u] = __ldcg(reinterpret_cast<const float4*>(from + r * kDP + col));
+                    }
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < kX; y++) {
+                float most = top[y];
+#pragma unroll
+                for (int u = 0; u < kB; u++) most = fmaxf(most, ml[y][u].x);
+                const float f0 = top[y] == -INFINITY ? 0.0f : ex2(top[y] - most);
+                acc[y].x *= f0, acc[y].y *= f0, acc[y].z *= f0, acc[y].w *= f0;
+                sum[y] *= f0;
+                top[y] = most;
+#pragma unroll
+                for (int u = 0; u < kB; u++) {
+                    if (ml[y][u].y == 0.0f) continue;      // no key of this part
+                    const float f = ml[y][u].x == -INFINITY ? 0.0f : ex2(ml[y][u].x - top[y]);
+                    acc[y].x += f * e[y][u].x;
+                    acc[y].y += f * e[y][u].y;
+                    acc[y].z += f * e[y][u].z;
+                    acc[y].w += f * e[y][u].w;
+                    sum[y] += f * ml[y][u].y;
+                }
+            }
+        }
+#pragma unroll
+        for (int y = 0; y < kX; y++) {
+            const int x = x0 + y * threads, r = x / (kDP / 4), col = 4 * (x % (kDP / 4));
+            if (x >= n || col >= a.head_dim) continue;
+            const int t = r / a.group, head = hk * a.group + r - t * a.group;
+            const float inv = sum[y] == 0.0f ? 0.0f : v_g / sum[y];
+            *reinterpret_cast<uint2*>(a.out + (int64_t)(tok0 + t) * a.ldo + (int64_t)head * a.ho + col) =
+                sum[y] == 0.0f ? make_uint2(0u, 0u)
+                               : make_uint2(cvt_bf16x2(acc[y].x * inv, acc[y].y * inv), cvt_bf16x2(acc[y].z * inv, acc[y].w * inv));
+            if (col == 0 && a.lse)
+                a.lse[(int64_t)(tok0 + t) * a.heads + head] = log_sum(top[y], sum[y]);
+        }
+    }
+}
 template <int kDP>
 __device__ __forceinline__ void join_parts(const AttnArgs& a, int thread0, int threads, int cta0, int parts, int rows, int tok0,
                                            int hk, float v_g)
 {
-    auto slot_of = [&](int i) { return a.partials + (2 * (cta0 + i) + (i == 0 ? 1 : 0)) * kAttnSlotFloats; };
-    for (int x = (int)threadIdx.x - thread0; x < rows * (kDP / 4); x += threads) {
-        const int r = x / (kDP / 4), col = 4 * (x % (kDP / 4));
-        if (col >= a.head_dim) continue;
-        const int t = r / a.group, head = hk * a.group + r - t * a.group;
-        float top = -INFINITY, sum = 0.0f;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-        for (int i0 = 0; i0 < parts; i0 += kJoinBatch) {
-            float2 ml[kJoinBatch];
-            float4 e[kJoinBatch];
-#pragma unroll
-            for (int u = 0; u < kJoinBatch; u++) {
-                ml[u] = make_float2(-INFINITY, 0.0f);
-                e[u] = acc;
-                if (i0 + u < parts) {
-                    const float* from = slot_of(i0 + u);
-                    ml[u] = __ldcg(reinterpret_cast<const float2*>(from + kAttnSlotRows * kDP + 2 * r));
-                    e[u] = __ldcg(reinterpret_cast<const float4*>(from + r * kDP + col));
-                }
-            }
-            float most = top;
-#pragma unroll
-            for (int u = 0; u < kJoinBatch; u++) most = fmaxf(most, ml[u].x);
-            const float f0 = top == -INFINITY ? 0.0f : ex2(top - most);
-            acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
-            sum *= f0;
-            top = most;
-#pragma unroll
-            for (int u = 0; u < kJoinBatch; u++) {
-                if (ml[u].y == 0.0f) continue;             // no key of this part
-                const float f = ml[u].x == -INFINITY ? 0.0f : ex2(ml[u].x - top);
-                acc.x += f * e[u].x;
-                acc.y += f * e[u].y;
-                acc.z += f * e[u].z;
-                acc.w += f * e[u].w;
-                sum += f * ml[u].y;
-            }
-        }
-        const float inv = sum == 0.0f ? 0.0f : v_g / sum;
-        *reinterpret_cast<uint2*>(a.out + (int64_t)(tok0 + t) * a.ldo + (int64_t)head * a.ho + col) =
-            sum == 0.0f ? make_uint2(0u, 0u)
-                        : make_uint2(cvt_bf16x2(acc.x * inv, acc.y * inv), cvt_bf16x2(acc.z * inv, acc.w * inv));
-        if (col == 0 && a.lse)
-            a.lse[(int64_t)(tok0 + t) * a.heads + head] = log_sum(top, sum);
-    }
+    if (parts <= 3)
+        join_some<kDP, 4, 3>(a, thread0, threads, cta0, parts, rows, tok0, hk, v_g);
+    else
+        join_some<kDP, 1, 12>(a, thread0, threads, cta0, parts, rows, tok0, hk, v_g);
 }
 
 // One pass of a CTA over the keys of a piece, for up to kRows of its rows.  The
