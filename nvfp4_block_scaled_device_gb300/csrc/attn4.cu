@@ -932,13 +932,12 @@ struct Share {
 };
 
 template <int kDP, int kNT, bool kFull>
-__device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, int cta)
+__device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, int cta, Share* s_share)
 {
     using C = Cfg4<kDP, kNT>;
     constexpr int kSteps = kDP / 16;
     __shared__ Work s_work[C::kWarps][2];
     __shared__ Walk s_walk[C::kWarps];
-    __shared__ Share s_share[2];
     const AttnArgs& a = prm.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
     const int D = kFull ? kDP : a.head_dim, Hkv = a.kv_heads, nb = D / 16;
@@ -955,6 +954,8 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
     // have up to eight chunks more than the others), this warp's v0 .. v1 - 1.
     const int per = head->per_cta4, units = head->units4, n_tiles = head->qtiles, begin = head->first4[cta];
     const QTile start = head->start4[cta];
+    const int after = min(cta + 1, kAttnMaxCtas - 1), begin1 = head->first4[after];      // (read at once with the rest)
+    const QTile start1 = head->start4[after];
     auto snapped = [&](int u, const QTile& t, int i) {
         const int item = kItemUnits4 + kChunksOfTile * t.tiles, s = units4_before(t.unit0, Hkv, i);
         const int at = s + (u - s) / item * item;          // the item that it cuts
@@ -962,13 +963,12 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
     };
     const int raw0 = min(cta * per, units), raw1 = min(raw0 + per, units);
     const int u0 = raw0 < units ? snapped(raw0, start, begin) : units;
-    const int u1 = raw1 < units ? snapped(raw1, head->start4[cta + 1], head->first4[cta + 1]) : units;
+    const int u1 = raw1 < units ? snapped(raw1, start1, begin1) : units;
     const int len = u1 - u0;
     auto bound = [&](int w) { return u0 + len * w / C::kWarps; };
     const int v0 = bound(warp), v1 = bound(warp + 1);
     const bool final_warp = warp == C::kWarps - 1;
     const float k_g = *a.k_g, v_g = *a.v_g;
-    if (tid < 2) s_share[tid].valid = 0;
 
     Walk& walk = s_walk[warp];
     const bool any = len > 0;
@@ -1093,7 +1093,20 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
             if (c1 > c0 && snap_unit4(c1 * per - x.s, x.item) == x.item) c1--;
             s_share[x.a == 0 ? 1 : 0] = Share{1, c0, c1 - c0 + 1, x.rows, x.tok0, x.hk, 0};
         }
+        return whole ? 0 : x.a == 0 ? 2 : 1;
     };
+    // Tickets for the CTA's parts (bits 0 and 1 of `which`) that this warp has written:
+    // as soon as it has nothing else to do, not when all are ready.
+    auto tickets = [&](int which) {
+        __syncwarp();
+        if (lane < 2 && (which >> lane & 1)) {
+            Share& x = s_share[lane];
+            int* ticket = a.tickets + x.cta0 * 8;
+            x.last = atom_add_acq_rel(ticket, 1) == x.parts - 1;
+            if (x.last) *ticket = 0;
+        }
+    };
+    int written = 0;
     if (s_work[warp][0].valid) {
 #pragma unroll 1
         for (;; at ^= 1) {
@@ -1185,7 +1198,7 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
                                      : reinterpret_cast<float*>(smem + warp * (C::kOwnStages * C::kStageBytes));
                 }
                 float4* to4 = reinterpret_cast<float4*>(left) + lane;
-                if (lane == 0) s_left[warp] = reinterpret_cast<float4*>(left);
+                if (C::kLeaveInRing && lane == 0) s_left[warp] = reinterpret_cast<float4*>(left);
 #pragma unroll
                 for (int n = 0; n < kNT; n++) {
 #pragma unroll
@@ -1196,7 +1209,7 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
                         if (g == 0) left_ml[warp * C::kRows + 8 * n + 2 * j + y] = make_float2(w.m[n][y], w.l[n][y]);
                 }
             } else if (cur.x1 == cur.b) {
-                finish(cur);
+                written |= finish(cur);
             } else {
                 pending = true;                            // goes on in the warps behind
                 break;
@@ -1204,6 +1217,7 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
             if (!nxt.valid) break;
         }
     }
+    if (written) tickets(written);
     __syncthreads();
     if (pending) {
         const Work& x = s_work[warp][at];
@@ -1213,7 +1227,7 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
             const int to = o == C::kWarps - 1 ? x.b : min(max(bound(o + 1) - x.s - kItemUnits4, x.a), x.b);
             if (to == reached) continue;
             reached = to;
-            const float4* from = s_left[o] + lane;
+            const float4* from = (C::kLeaveInRing ? s_left[o] : reinterpret_cast<const float4*>(smem + C::kOffO + o * C::kWarpO * 4)) + lane;
 #pragma unroll
             for (int n = 0; n < kNT; n++) {
                 float f0[2], f1[2];
@@ -1236,15 +1250,8 @@ __device__ __forceinline__ void own_shares(const Params4& prm, uint8_t* smem, in
                 }
             }
         }
-        finish(x);
-    }
-    __syncthreads();
-    if (!s_share[0].valid && !s_share[1].valid) return;
-    if (tid < 2 && s_share[tid].valid) {
-        Share& x = s_share[tid];
-        int* ticket = a.tickets + x.cta0 * 8;
-        x.last = atom_add_acq_rel(ticket, 1) == x.parts - 1;
-        if (x.last) *ticket = 0;
+        written = finish(x);
+        if (written) tickets(written);
     }
     __syncthreads();
     // (the CTA that ends last often has both to join: half of its threads each)
@@ -1275,6 +1282,8 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
     }
     griddep_wait();
     if (a.skip_few && !a.sched->few_passes) return;
+    __shared__ Share s_share[2];
+    if (threadIdx.x < 2) s_share[threadIdx.x].valid = 0;
     __syncthreads();
     // Shares of warps where there are several items for each CTA, or long ones: one
     // join at the end, whatever the items' lengths (64 requests of 200 to 8192 keys
@@ -1284,7 +1293,7 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
     const int64_t items = (int64_t)a.sched->qtiles * a.kv_heads;
     const int per = a.sched->per_cta4;
     if (per > 0 && a.sched->most_tokens * a.group <= C::kRows && (2 * items >= 3 * (int)gridDim.x || per >= 256))
-        own_shares<kDP, kNT, kFull>(prm, smem, cta);
+        own_shares<kDP, kNT, kFull>(prm, smem, cta, s_share);
     else
         passes_together<kDP, kNT, kFull>(prm, smem, cta);
     copies_wait<0>();
