@@ -36,15 +36,16 @@
 // state -- twice the keys of one request of 131071 and one of 65537 take 37.5 us
 // more for 248 MB, 6.6 TB/s -- where 32 keys are 430 instructions of a warp, 1.3 us for
 // the 16 of an SM, against 1.66 us for their bytes (with the bytes of the codes taken
-// apart by shifts, 550 instructions and the binding limit).  Beside that some 17 us
+// apart by shifts, 550 instructions and the binding limit).  Beside that some 15 us
 // pass from the launch to the end: 4 to 7 until the first keys are there (the
 // schedule, the block table, Q, the keys, one after the other, and every warp's
-// ring at once), 3 for the spread of the warps' ends, 2 to add up their shares, 4 to 5 for
-// the parts of other CTAs.  These two requests 54 us; 64 requests of 200 to 8192
-// keys 42 (bf16: 95); one of 333 keys 7.0.  With 9 to 16 rows a request 50 (64
-// requests of 200 to 4000 keys, 3 tokens each), with 17 to 32, where the softmax and
-// Q's fragments out of shared memory weigh as much as the codes, 102 (64 of 200 to
-// 8192, 1 to 4 tokens each, and the launches that decide about bf16 pages).
+// ring at once), 4 for the spread of the warps' ends, 2 to add up their shares, 3 for
+// the parts of other CTAs.  These two requests 53 us; 64 requests of 200 to 8192
+// keys 39 (bf16: 95); one of 333 keys 6.9.  With 9 to 16 rows a request 40 (64
+// requests of 200 to 4000 keys, 3 tokens each), with 17 to 32, where two warps of a
+// scheduler wait for one another's results (255 registers: 8 warps an SM; code for the
+// tiles that are there alone gave nothing), 95 (64 of 200 to 8192, 1 to 4 tokens
+// each, and the launches that decide about bf16 pages).
 #include <cuda_fp16.h>
 
 #include "attn.h"
@@ -1285,14 +1286,15 @@ __global__ void __launch_bounds__(Cfg4<kDP, kNT>::kThreads, 1) attn4_kernel(cons
     __shared__ Share s_share[2];
     if (threadIdx.x < 2) s_share[threadIdx.x].valid = 0;
     __syncthreads();
-    // Shares of warps where there are several items for each CTA, or long ones: one
-    // join at the end, whatever the items' lengths (64 requests of 200 to 8192 keys
-    // 42 us, 70 with all warps on one item at a time; a request of 131071 with one of
-    // 65537 53 and 56).  Else all warps at once on a CTA's one part, which is
-    // joined faster (a request of 333 keys 7.0 us, 8.8; 8 of 2000 13.3, 19.1).
+    // Shares of warps where there is an item for each CTA, or a long one: one join at
+    // the end, whatever the items' lengths (us, with the shares and with all warps on
+    // one item at a time: 40 requests of 200 to 8000 keys 31 and 48, 28 of 200 to 4000
+    // 21.7 and 25.7, 20 of 100 to 4000 16.4 and 18.7, 16 of 1000 to 3000 -- 128 items on
+    // 152 CTAs -- 19.2 and 19.2).  Else all warps at once on a CTA's one part, which is
+    // joined faster (a request of 333 keys 9.3 and 6.6, 8 of 2000 15.5 and 12.2).
     const int64_t items = (int64_t)a.sched->qtiles * a.kv_heads;
     const int per = a.sched->per_cta4;
-    if (per > 0 && a.sched->most_tokens * a.group <= C::kRows && (2 * items >= 3 * (int)gridDim.x || per >= 256))
+    if (per > 0 && a.sched->most_tokens * a.group <= C::kRows && (items >= (int)gridDim.x || per >= 256))
         own_shares<kDP, kNT, kFull>(prm, smem, cta, s_share);
     else
         passes_together<kDP, kNT, kFull>(prm, smem, cta);
