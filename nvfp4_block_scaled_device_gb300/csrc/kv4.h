@@ -9,9 +9,10 @@ namespace nvfp4 {
 // Device status of the page operators (NVFP4_ERR_INVALID_ARG * 100 + site).
 constexpr int kStatusPages = NVFP4_ERR_INVALID_ARG * 100 + 34;
 
-// Rows of a request, on average, from which a step's keys are expanded once (40
-// rows: 8 requests of 2000 keys 43.7 us that way and 52.0 straight from the codes, 1
-// of 8000 45.1 and 45.0; 20 rows: 44.8 and 28.2, 52.6 and 24.3).
+// Rows of a request, on average, from which a step's keys are expanded once (us that way
+// and straight from the codes, 40 rows: 32 requests of 200 to 4000 keys 91 and 113, 8 of
+// 2000 43 and 42, 1 of 8000 47 and 41; 60 rows: 64 of 100 to 2000 93 and 160; 20 rows: 8 of
+// 2000 45 and 24, 1 of 8000 55 and 24).
 constexpr int64_t kExpandRows = 40;
 
 constexpr int64_t kMaxPages = 1 << 20;      // of the page operators (a bit each in shared memory)
