@@ -30,14 +30,14 @@ int log2_of(int64_t v)
 // time and keeps the token's cosines and sines over its rows.  Arithmetic on
 // pairs of columns (two binary32 operations an instruction: without it, and with
 // the kinds mixed in a warp, the pass was bound by its instructions, 195 us where
-// it now takes 91).  K rows go to k_out or, with those of V, into the cache,
+// it now takes 87).  K rows go to k_out or, with those of V, into the cache,
 // in 4 bits from the bf16 value (so that the pass gives what the two calls give);
 // a block of 16 columns is two lanes.
 //
 // Bound by HBM with many tokens (2 B in, 2 B out a column): 16272 tokens of 40 query and
-// 8 key heads, with the values into the 4-bit cache, 91 us for 475 MB (5.2 TB/s; blocks
-// of 64 registers, 8 to an SM: 9 blocks 92, 6 blocks 115, 10 and fewer rows at once
-// 104); with few by the launch and one dependent chain of loads, so the rows of a token
+// 8 key heads, with the values into the 4-bit cache, 87 us for 475 MB (5.5 TB/s; blocks
+// of 64 registers, 8 to an SM, 91 then: 9 blocks 92, 6 blocks 115, 10 and fewer rows at
+// once 104); with few by the launch and one dependent chain of loads, so the rows of a token
 // are spread over as many warps as there is room for (8 tokens 2.6 us).
 constexpr int kHeadThreads = 128;
 constexpr int kHeadWarps = kHeadThreads / 32;
@@ -250,7 +250,8 @@ __device__ __forceinline__ void work_rows(HeadRows& q, int batches, const HeadMa
                 y = make_uint4(cvt_bf16x2(v[0].x, v[0].y), cvt_bf16x2(v[1].x, v[1].y), cvt_bf16x2(v[2].x, v[2].y), cvt_bf16x2(v[3].x, v[3].y));
             }
             const bool here = i < q.left;
-            if (q.out && here) *reinterpret_cast<uint4*>(q.out + i * q.step_out) = y;
+            // (leaves L2 first: rows to come are read through it; 16272 tokens 87 us, 91 without)
+            if (q.out && here) __stcs(reinterpret_cast<uint4*>(q.out + i * q.step_out), y);
             if (kTo != kToRows && q.also && here) *reinterpret_cast<uint4*>(q.also + i * q.step_also) = y;
             if (kTo == kToCache4 && q.codes) {
                 uint32_t m = amax_bf16x2(amax_bf16x2(y.x, y.y), amax_bf16x2(y.z, y.w));
