@@ -280,9 +280,9 @@ __device__ __forceinline__ void work_rows(HeadRows& q, int batches, const HeadMa
 // Rows as they are into the 4-bit cache: unit u of token t's rows of k or v, `per`
 // times kHeadBatch rows for each that L lanes of 8 columns would have.  A lane has a
 // whole block of 16 columns (so that what is done once per block is done once) of
-// two rows at a time.  16272 tokens of 8 heads: 19.7 us for 85 MB (4.3 TB/s; with half
-// a block to a lane 25, bound by its instructions; a warp that loops over tokens with
-// the next one's rows on their way 19.8).
+// two rows at a time.  16272 tokens of 8 heads: 18.0 us for 85 MB (4.7 TB/s; with half
+// a block to a lane 25, bound by its instructions; then, without the loads' hint, 19.7, and
+// with warps that loop over tokens, the next one's rows on their way, 19.8).
 __device__ __forceinline__ void append_rows(const HeadsParams& p, uint32_t t, bool is_v, int u, int lane, int L, int D)
 {
     const nvfp4_heads_t& h = p.h;
@@ -306,8 +306,9 @@ __device__ __forceinline__ void append_rows(const HeadsParams& p, uint32_t t, bo
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             const uint4* from = reinterpret_cast<const uint4*>(src + (r + i * at_once) * pitch);
+            // (nothing reads the bf16 rows of a cached token again: they leave L2 first)
 #pragma unroll
-            for (int y = 0; y < 2; y++) x[i][y] = i == 0 || r + at_once < end ? from[y] : make_uint4(0, 0, 0, 0);
+            for (int y = 0; y < 2; y++) x[i][y] = i == 0 || r + at_once < end ? __ldcs(from + y) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int i = 0; i < 2; i++) {
