@@ -604,7 +604,7 @@ struct nvfp4_kv4_cache {
     uint8_t* v;
     uint8_t* k_sf;
     uint8_t* v_sf;
-    const float* k_g;          /* [1], device: > 0, normal; e.g. a power of two near max |k| / 2688 */
+    const float* k_g;          /* [1], device: 2^-80 .. 2^120; e.g. a power of two near max |k| / 2688 */
     const float* v_g;
     int64_t pages, page_size, kv_heads;
     int64_t head_dim;          /* 16 .. 128, % 16 == 0 */
@@ -616,8 +616,9 @@ struct nvfp4_kv4_cache {
  * nvfp4_kv4_append -- nvfp4_kv_append into a 4-bit cache: each 16 columns
  * quantized as nvfp4_quantize does with the global scale *k_g (*v_g):
  *   s = E4M3(amax16 / (6*g)),  code = s == 0 ? +0 : E2M1(x / (E4M3(s) * g)).
- * Infinities count as the largest bf16 number; a block with a NaN gets the
- * scale NaN and the codes 0.  Slots as in nvfp4_kv_append.
+ * Infinities count as the largest bf16 number (beyond 448*6*g a block's scale
+ * is 448, and a value beyond 6 times that scale is 6 times it); a block with a
+ * NaN gets the scale NaN and the codes 0.  Slots as in nvfp4_kv_append.
  */
 int nvfp4_kv4_append(const void* k, int64_t ldk, int64_t hk, const void* v, int64_t ldv, int64_t hv,
                      const int32_t* slot, int64_t tokens, const nvfp4_kv4_cache_t* cache, nvfp4_stream_t stream);

@@ -93,14 +93,18 @@ __device__ __forceinline__ uint32_t amax_bf16x2(uint32_t a, uint32_t b)
     return r;
 }
 
-// Scales of a cache's blocks: 6 g and its correctly rounded reciprocal.
+constexpr float kMostBf16 = 3.3895313892515355e38f;
+
+// Scales of a cache's blocks: 6 g, its correctly rounded reciprocal, and the
+// largest magnitude that counts in a block's scale (beyond 448 * 6 g it is 448,
+// as it is there; an infinity is the largest bf16 number).
 struct BlockScale {
-    float g, d, rd;
+    float g, d, rd, most;
 };
 __device__ __forceinline__ BlockScale block_scale(float g)
 {
     const float d = __fmul_rn(6.0f, g);
-    return BlockScale{g, d, __frcp_rn(d)};
+    return BlockScale{g, d, __frcp_rn(d), fminf(__fmul_rn(448.0f, d), kMostBf16)};
 }
 
 // One block's scale and codes, nvfp4_quantize's bit for bit: each lane has kVecs
@@ -112,9 +116,8 @@ template <int kVecs>
 __device__ __forceinline__ void quant_block(const uint4* x, uint32_t amax_bits, const BlockScale& b, uint32_t* codes, uint32_t* sc)
 {
     float amax = bf16_lo(amax_bits);
-    constexpr float kMost = 3.3895313892515355e38f;                  // of bf16
-    const bool odd = !(amax <= kMost), nan = amax != amax;           // an infinity or NaN in it
-    if (odd) amax = kMost;
+    const bool odd = !(amax <= b.most), nan = amax != amax;          // too large, an infinity or NaN in it
+    if (odd) amax = b.most;
     const uint32_t s = cvt_e4m3(div_by_recip(amax, b.d, b.rd));
     const float den = __fmul_rn(e4m3_to_f32(s), b.g);
     const float ny = -__frcp_rn(s ? den : 1.0f);
@@ -124,9 +127,10 @@ __device__ __forceinline__ void quant_block(const uint4* x, uint32_t amax_bits, 
         float2 v[4];
         unpack4(x[i], v);
         if (odd) {
+            const float most = fminf(__fmul_rn(8.0f, den), kMostBf16);
 #pragma unroll
             for (int y = 0; y < 4; y++)
-                v[y] = make_float2(fminf(fmaxf(v[y].x, -kMost), kMost), fminf(fmaxf(v[y].y, -kMost), kMost));
+                v[y] = make_float2(fminf(fmaxf(v[y].x, -most), most), fminf(fmaxf(v[y].y, -most), most));
         }
         float q[8];
 #pragma unroll

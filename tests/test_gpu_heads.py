@@ -223,6 +223,40 @@ def test_append4_of_values_that_are_not_finite(nv):
     assert row(2)[40] == -2688
 
 
+@pytest.mark.parametrize("with_heads", [False, True])
+@pytest.mark.parametrize("D", [128, 80])
+@pytest.mark.parametrize("g", [1.0, 2.0 ** -6, 2.0 ** -11, 0.0123, 2.0 ** -80, 2.0 ** 90, 2.0 ** 115])
+def test_append4_of_infinities_and_the_largest_numbers(nv, g, D, with_heads):
+    """Whatever the global scale, infinities are the largest bf16 number and what the
+    scales do not reach saturates, bit for bit the oracle's; NaN stays in its block."""
+    T, Hkv, page, inf = 9, 3, 16, float("inf")
+    gen = torch.Generator("cuda").manual_seed(D)
+    cache = random_cache4(nv, gen, 4, Hkv, page, D, g, g)
+    plan = plan_of(nv, [T], [2], Hkv, Hkv, page, 4)
+    x = torch.randn(T, Hkv, D, device="cuda", generator=gen).bfloat16() * min(g, 2.0 ** 100) * 3
+    most = torch.finfo(torch.bfloat16).max
+    x[0, 0, 5], x[1, 1, 20], x[2, 2, 63] = inf, -inf, most
+    x[3, 0, 16:32] = torch.tensor([inf, -inf, most, -most, 1e38, -1e37, 1e36, -1e30, 1e20, 1.0, -1.0, 0.0, -0.0, 1e-3, 1e-30, -1e35])
+    x[4, :, ::16], x[5, :, 3::16], x[6] = 1e36, -inf, inf
+    x[7, 1, 33], x[7, 1, 34], x[8, 0, 0] = float("nan"), inf, 1e38
+    y = x.flip(0).neg().contiguous()                          # (the values: other blocks)
+    if with_heads:
+        out = torch.empty_like(x)
+        nv.nvfp4_qk_norm_rope(None, x, k_out=out, v=y, plan=plan, cache=cache)
+        assert torch.equal(out.view(torch.int16), x.view(torch.int16))
+    else:
+        nv.nvfp4_kv4_append(x, y, plan, cache)
+    at = plan.slot.long()
+    for rows_in, codes, sf in ((x, cache.k, cache.k_sf), (y, cache.v, cache.v_sf)):
+        nan = rows_in.view(T, Hkv, D // 16, 16).isnan().any(-1).cpu()
+        c, s = oracle.quantize(host(rows_in.clamp(-most, most).nan_to_num().reshape(T * Hkv, D)), np.float32(g))
+        c, s = (torch.from_numpy(z).view(T, Hkv, D // 16, -1).clone() for z in (c, s))
+        c[nan], s[nan] = 0, 0x7f
+        assert int(nan.sum()) == 1
+        assert torch.equal(codes[at // page, :, at % page].cpu().view(T, Hkv, D // 16, 8), c)
+        assert torch.equal(sf[at // page, :, at % page].cpu().view(T, Hkv, D // 16, 1), s)
+
+
 def test_slots_outside_the_cache_are_reported(nv):
     cache = random_cache4(nv, torch.Generator("cuda").manual_seed(2), 2, 2, 16, 64)
     plan = nv.AttnPlan(1, 4, 2, 2, page_size=16, block_table=1)
