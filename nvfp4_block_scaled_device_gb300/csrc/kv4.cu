@@ -229,7 +229,11 @@ __device__ __forceinline__ void work_rows(HeadRows& q, int batches, const HeadMa
                 }
 #pragma unroll
                 for (int z = 0; z < 4; z++) {
-                    if (kRope != kNoRope) r[z] = fma2(kRope == kPairs ? make_float2(v[z].y, v[z].x) : v[z], h.q[z], r[z]);
+                    if (kRope != kNoRope) {
+                        const float2 turned = fma2(kRope == kPairs ? make_float2(v[z].y, v[z].x) : v[z], h.q[z], r[z]);
+                        // (a column that is not rotated takes nothing of its neighbour, which may be infinite)
+                        if (kWhole || (kRope == kPairs ? z >= h.skip : h.rotate)) r[z] = turned;
+                    }
                     r[z] = mul2(r[z], make_float2(inv, inv));
                 }
                 y = make_uint4(cvt_bf16x2(r[0].x, r[0].y), cvt_bf16x2(r[1].x, r[1].y), cvt_bf16x2(r[2].x, r[2].y), cvt_bf16x2(r[3].x, r[3].y));

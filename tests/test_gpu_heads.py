@@ -126,6 +126,32 @@ def test_values_that_are_not_finite_stay_in_their_row(nv):
     assert torch.equal(got[same], clean[same]) and got[4, 3].isnan().all() and got[9, 0].isnan().any()
 
 
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("D,rd", [(128, 64), (96, 32), (64, 48), (128, 128)])
+def test_an_infinity_in_a_normed_row(nv, D, rd, halves):
+    """Its row's mean is infinite: the row becomes 0, NaN at the infinity and, among the
+    rotated columns, at its partner; columns that are not rotated keep their zeros' signs."""
+    gen = torch.Generator("cuda").manual_seed(D + rd)
+    q = rows(gen, 2 * D, 3, D, "plain")
+    w = (1 + torch.rand(D, device="cuda", generator=gen)).bfloat16()
+    cos, sin = tables(2 * D, rd // 2, gen)
+    pos, at = torch.arange(2 * D, device="cuda").int(), torch.arange(D, device="cuda")
+    q[at, 1, at], q[D + at, 2, at] = float("inf"), -float("inf")
+    q[:, 0, :D - rd] = -0.0
+    rot0, half = D - rd, rd // 2
+    mate = torch.where(at < rot0, at, torch.where(at < rot0 + half, at + half, at - half) if halves else at ^ 1)
+    nan = torch.zeros(q.shape, dtype=torch.bool, device="cuda")
+    for first, head in ((0, 1), (D, 2)):
+        nan[first + at, head, at] = nan[first + at, head, mate] = True
+    gone = torch.zeros(2 * D, 3, dtype=torch.bool, device="cuda")
+    gone[:D, 1] = gone[D:, 2] = True
+    out = torch.empty_like(q)
+    nv.nvfp4_qk_norm_rope(q, None, w, None, pos, cos, sin, q_out=out, halves=halves)
+    assert torch.equal(out.isnan(), nan)
+    assert ((out == 0) | nan)[gone].all()
+    assert (out[:, 0, :rot0].view(torch.int16) == -2 ** 15).all()
+
+
 def test_rotation_is_that_of_the_projection(nv):
     """Without norms: nvfp4_gemm then this, bit for bit nvfp4_gemm_rope."""
     ws = nv.workspace(256)
