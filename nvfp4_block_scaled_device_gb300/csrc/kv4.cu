@@ -174,13 +174,18 @@ struct HeadRows {
     int left;                          // rows from this lane's first on (in steps)
 };
 
+// The weights count a power of two less and 1 / rms as much more, which no result
+// of ordinary size notices: a row whose squares are beyond binary32 is 0 (1 / rms
+// is), not 0 times an infinite product (of weights up to 2^15).
+constexpr float kLess = 1.0f / 65536.0f;
+
 // What a lane does to its 8 columns of a row.
 struct HeadMath {
     int L;                             // lanes of a row
     float inv_d, eps;
-    // with a norm: column pair y becomes (v[y] * p[y] + other * q[y]) / rms, where
+    // with a norm: column pair y becomes (v[y] * p[y] + other * q[y]) / (kLess rms), where
     // `other` is the partner lane's pair (halves) or the pair's columns exchanged:
-    // weight times cosine, the other one's weight times sine with its sign
+    // kLess times weight times cosine, the other one's weight times sine with its sign
     float2 p[4], q[4];
     // without: the rotation in single operations
     float c[8], s[8];
@@ -218,7 +223,7 @@ __device__ __forceinline__ void work_rows(HeadRows& q, int batches, const HeadMa
                     const float other = __shfl_xor_sync(0xffffffffu, sum, o);
                     if (kWhole || o < h.L) sum += other;
                 }
-                const float inv = rsqrtf(sum * h.inv_d + h.eps);
+                const float inv = rsqrtf(sum * h.inv_d + h.eps) * (1.0f / kLess);
 #pragma unroll
                 for (int z = 0; z < 4; z++) r[z] = mul2(v[z], h.p[z]);
                 if (kRope == kHalves) {
@@ -452,6 +457,8 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadBlocks) heads_kernel(const 
         unpack4(*reinterpret_cast<const uint4*>(weight + col), w);
         if (kRope == kHalves && m.rotate) unpack4(*reinterpret_cast<const uint4*>(weight + (low ? col + half : col - half)), o);
     }
+#pragma unroll
+    for (int y = 0; y < 4; y++) w[y] = mul2(w[y], make_float2(kLess, kLess)), o[y] = mul2(o[y], make_float2(kLess, kLess));
 #pragma unroll
     for (int y = 0; y < 4; y++) {
         if (kRope == kHalves) {

@@ -152,6 +152,27 @@ def test_an_infinity_in_a_normed_row(nv, D, rd, halves):
     assert (out[:, 0, :rot0].view(torch.int16) == -2 ** 15).all()
 
 
+@pytest.mark.parametrize("halves", [None, False, True])
+@pytest.mark.parametrize("D,rd", [(128, 128), (128, 64), (80, 48)])
+def test_rows_whose_squares_are_beyond_binary32(nv, D, rd, halves):
+    """Their mean is infinite in binary32, 1 / rms is 0 and so are they, whatever the weights."""
+    gen = torch.Generator("cuda").manual_seed(D + rd)
+    q = rows(gen, 9, 4, D, "plain")
+    w = (1 + 99 * torch.rand(D, device="cuda", generator=gen)).bfloat16()
+    big = (1 + torch.rand(5, D, device="cuda", generator=gen)) * torch.tensor([1e19, 1e25, 1e37, 1.2e38, 1.6e38], device="cuda")[:, None]
+    q[2:7, 1], q[2:7, 3] = big.bfloat16(), -big.bfloat16()
+    cos, sin = tables(9, rd // 2, gen)
+    pos = torch.arange(9, device="cuda").int()
+    out = torch.empty_like(q)
+    rope = {} if halves is None else dict(pos=pos, cos_t=cos, sin_t=sin, halves=halves)
+    nv.nvfp4_qk_norm_rope(q, None, w, None, q_out=out, **rope)
+    assert (out[2:7, 1] == 0).all() and (out[2:7, 3] == 0).all()
+    q[2:7, 1], q[2:7, 3] = 1, 1
+    other = torch.empty_like(q)
+    nv.nvfp4_qk_norm_rope(q, None, w, None, q_out=other, **rope)
+    assert torch.equal(out[:, ::2], other[:, ::2]) and torch.equal(out[:2], other[:2]) and torch.equal(out[7:], other[7:])
+
+
 def test_rotation_is_that_of_the_projection(nv):
     """Without norms: nvfp4_gemm then this, bit for bit nvfp4_gemm_rope."""
     ws = nv.workspace(256)
