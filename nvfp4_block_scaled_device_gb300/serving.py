@@ -52,7 +52,7 @@ from . import (NVFP4_INTER_DYNAMIC, AttnPlan, KVCache, KVCache4, NVFP4Tensor, at
                nvfp4_gemm, nvfp4_gemm_rope, nvfp4_kv4_append, nvfp4_kv_append, nvfp4_mlp, nvfp4_qk_norm_rope,
                nvfp4_scale_quantize, workspace)
 
-_EXPAND_ROWS = 40    # rows of a request, on average, from which nvfp4_attn_paged4 uses its bf16 pages
+_PASS_ROWS = 32      # rows of a request that nvfp4_attn_paged4 takes in one pass over its keys' codes
 
 
 class ServingLayer:
@@ -62,14 +62,19 @@ class ServingLayer:
 
     def __init__(self, plan: AttnPlan, cache: KVCache | KVCache4 | None, weights: dict, attn_norm: torch.Tensor,
                  mlp_norm: torch.Tensor, cos_t: torch.Tensor, sin_t: torch.Tensor, eps=1e-6, scratch=None,
-                 q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None, halves=False):
+                 q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None, halves=False, expand=True):
         """weights: NVFP4Tensor values under 'qkv' [(heads + 2 kv_heads) D x H],
         'o' [H x heads D], 'gate', 'up' [I x H], 'down' [H x I]; cos_t, sin_t:
         the rotary tables of nvfp4_gemm_rope, as wide as half the rotated
         columns (a position past their last row is reported in the device
         status and rotated as that row).  q_norm, k_norm: bf16 [D], the norms of
         the query and key heads, or None; halves: the rotation pairs column i with
-        column i + half of the rotated ones instead of 2i with 2i + 1."""
+        column i + half of the rotated ones instead of 2i with 2i + 1.  expand: over
+        a KVCache4, scratch["expanded"] are bf16 pages (3.6 times one layer's cache) where
+        a request of the plan may have more rows than one pass over the codes takes:
+        prompts, chunks, also one among decoding requests.  False: none, for plans whose
+        requests have a few tokens each (a step of them is 5 us a layer faster then, and
+        one with a chunk in it several times slower)."""
         self.plan, self.cache, self.w, self.eps = plan, cache, weights, eps
         self.attn_norm, self.mlp_norm, self.cos_t, self.sin_t = attn_norm, mlp_norm, cos_t, sin_t
         self.q_norm, self.k_norm, self.halves = q_norm, k_norm, halves
@@ -91,8 +96,9 @@ class ServingLayer:
             raise ValueError("halves: tables of a multiple of 8 columns")
         dev = attn_norm.device
         # prompts over a 4-bit cache: bf16 pages, taken out once per layer and step
+        # (whether they are is nvfp4_attn_paged4's decision, from each step's lengths)
         self.four = isinstance(cache, KVCache4)
-        self.expands = expands = self.four and -(-T // plan.requests) * (heads // kv_heads) >= _EXPAND_ROWS
+        self.expands = expands = self.four and expand and (T > plan.requests or heads // kv_heads > _PASS_ROWS)
         if scratch is None:
             scratch = {
                 "h": NVFP4Tensor.empty(T, H, dev), "a": NVFP4Tensor.empty(T, heads * D, dev),

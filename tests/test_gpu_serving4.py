@@ -96,6 +96,56 @@ def test_steps(nv, weights, four, norms, halves, page, window):
         s.step([1, 1, 1], x_of(3, 610 + i), stack=1)
 
 
+@pytest.mark.parametrize("window", [0, 70])
+def test_a_chunk_among_decoding_requests(nv, weights, window):
+    """A few rows per request on average, one request with many: through the bf16 pages,
+    bit for bit as nvfp4_attn_paged4 does that; not without them, nor in a step of single tokens."""
+    R, page, lens = 12, 16, [300] + [20] * 11
+    s = Server(nv, weights, R, [sum(lens), 105], page, 30, 80, True, True, True, window)
+    s.step(lens, x_of(sum(lens), 630))
+    plan, layers = s.stacks[1]
+    assert 105 / R * (HEADS // KV) < 40 and all(layer.expands for layer in layers)
+    for i, q in enumerate(([90] + [1] * 11, [1] * 12, [0] + [1] * 11)):
+        s.step(q, x_of(105, 631 + i), stack=1)                # (3 rows of padding and more)
+        for at, layer in enumerate(layers):
+            rows, n = layer.scratch["qkv"].view(-1, HEADS + 2 * KV, D), sum(q)
+            if at + 1 < len(layers):
+                continue                                      # (the scratch is the last layer's)
+            out = [torch.empty(105, HEADS, D, device="cuda").bfloat16() for _ in range(2)]
+            pages = nv.KVCache.empty(80, KV, page, D)
+            for o, e in zip(out, (pages, None)):
+                nv.nvfp4_attn_paged4(rows[:, :HEADS], s.caches[at], plan, o, layer.scratch["ws_attn"], zero_padding=True, expanded=e)
+            assert torch.equal(layer.scratch["attn"].view(-1, HEADS, D), out[0])
+            assert torch.equal(out[0][:n], out[1][:n]) == (q[0] < 2) and (out[0][n:] == 0).all()
+
+
+def test_a_layer_without_bf16_pages(nv, weights):
+    from nvfp4_block_scaled_device_gb300.serving import ServingLayer
+    cos, sin = (torch.from_numpy(t).cuda() for t in synthetic.rope_tables(64, D))
+    norm = dev(synthetic.norm_weight(80, H))
+    make = lambda R, T, four=True, **f: ServingLayer(
+        nv.AttnPlan(R, T, HEADS, KV, page_size=16, block_table=4),
+        nv.KVCache4.empty(20, KV, 16, D) if four else nv.KVCache.empty(20, KV, 16, D), weights[0], norm, norm, cos, sin, **f)
+    for layer, has in ((make(4, 5), True), (make(4, 4), False), (make(4, 300), True), (make(4, 300, expand=False), False),
+                       (make(4, 300, four=False), False)):
+        assert layer.expands == has and (layer.scratch["expanded"] is not None) == has
+    outs = []                                                 # a prompt straight from the codes
+    for expand in (True, False):
+        layer = make(1, 50, expand=expand)
+        layer.plan.block_table.copy_(i32([[3, 0, 7, 5]]))
+        nv.nvfp4_attn_plan(layer.plan, i32([50]), i32([0]))
+        x = x_of(50, 640)
+        layer.forward(x, torch.empty_like(x))
+        rows, got = layer.scratch["qkv"].view(50, -1, D), layer.scratch["attn"].view(50, HEADS, D)
+        k, v = values(layer.cache)
+        pos = torch.arange(50, device="cuda")
+        ids = layer.plan.block_table[0].long()[pos // 16]
+        check(got, None, *reference(rows[:, :HEADS].double(), k[ids, :, pos % 16], v[ids, :, pos % 16], 0, D ** -0.5),
+              OUT_P if expand else P_HALF, v[ids, :, pos % 16])
+        outs.append(got.clone())
+    assert not torch.equal(*outs)
+
+
 @pytest.mark.parametrize("four", [False, True])
 def test_what_the_cache_holds(nv, weights, four):
     """Norm, rotation and the write in one pass: what the calls one by one give."""
