@@ -648,9 +648,10 @@ int nvfp4_kv4_expand(const nvfp4_kv4_cache_t* cache, const nvfp4_step_t* step, c
  *            that holds code times scale exactly) and runs nvfp4_attn_paged's
  *            kernel on them, with probabilities rounded to bf16 as there.  That is
  *            so with 40 rows (tokens times heads / kv_heads) per request or more on
- *            average, never with as many tokens as requests, and in between where the
- *            lengths want more than a few passes over the keys (the plan's schedule
- *            has that; two of the three launches then return at once or one does).
+ *            average, else never with as many tokens as requests, and in between where
+ *            the lengths want more than a few passes over the keys, of all requests or
+ *            of one (the plan's schedule has that; two of the three launches then
+ *            return at once or one does).
  *            One serves all layers that run one after the other.
  *   workspace as nvfp4_attn_paged.
  * head_dim % 16 == 0.  The rest as nvfp4_attn_paged: cache rows that no row of

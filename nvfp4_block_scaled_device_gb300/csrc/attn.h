@@ -54,7 +54,7 @@ struct ScheduleHead {
     // kItemUnits4) kv_heads i.  CTA c takes units c * per_cta4 .. as above.
     int32_t units4, per_cta4;      // 0: too long for it
     int32_t most_tokens;           // of a QTile
-    // few passes of kPassRows rows over the keys suffice, on average over them
+    // few passes of kPassRows rows over the keys suffice, on average and for each CTA
     int32_t few_passes;
     int32_t pad[9];
     int32_t first[kAttnMaxCtas];   // QTile of the first unit of CTA c ...

@@ -171,13 +171,21 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, const int
         // (at least a chunk for each warp of a CTA, where items have as many)
         const int longest4 = has4 ? kChunksOfTile * (*longest - kItemUnits) + kItemUnits4 : 1;
         const int per = has4 ? max(max((units4 + p.ctas - 1) / p.ctas, min(kItemUnits4 + 16, longest4)), 1) : 0;
-        if (t == 0) {
+        if (t == kPlanThreads - 1) {                   // (which has no QTiles where there are few)
             head->units4 = units4;
             head->per_cta4 = per;
             head->most_tokens = *most_tokens;
-            // (measured: 8 requests of 2000 keys 28 us straight from 4 bits in one pass,
-            // 52 in two; 44 in bf16 after taking them out, up to 32 rows and beyond)
-            head->few_passes = 10 * all_pass_tiles * Hkv <= 17 * (units - (int64_t)kItemUnits * n * Hkv);
+            // Few on average, and for the CTAs that have the QTile with most of them (their
+            // shares are cut by tiles, and no warp has one of its own then) one or no more
+            // than 15 tiles times passes.  Measured, us straight from 4 bits and in bf16 after
+            // taking them out: 8 requests of 2000 keys 28 in one pass, 52 in two, and 44; 64 of 100
+            // to 1000, one of them with 200 tokens of 5 rows, 375 and 78; 32 of 50 to 500
+            // with 40 tokens there 130 and 28, with 9 there (7 tiles twice) 39 and 26 with the
+            // two launches that return at once; 64 of 200 to 8192 with 9 of 8 rows there 53 and 105.
+            const int passes = (*most_tokens * group + kPassRows - 1) / kPassRows;
+            const int share = max(((int)min(units, kMaxUnits) + p.ctas - 1) / p.ctas, min(kItemUnits + kMinPart, *longest));
+            head->few_passes = 10 * all_pass_tiles * Hkv <= 17 * (units - (int64_t)kItemUnits * n * Hkv) &&
+                               (passes == 1 || passes * share <= 15);
         }
         if (!has4) return;
         int c = (units4_before((int)unit, Hkv, i0) + per - 1) / per;

@@ -169,6 +169,59 @@ def test_the_lengths_decide_about_the_bf16_pages(nv, ws, H, Hkv, D):
     assert not _through_the_pages(nv, ws, ctx, [1] * 29 + [0], H, Hkv, D)          # (no more tokens than requests)
 
 
+@pytest.mark.parametrize("H,Hkv,n", [(40, 8, 200), (28, 4, 40), (32, 32, 400)])
+def test_one_request_of_many_passes_decides(nv, ws, H, Hkv, n):
+    """Few passes on average, but many for the CTAs that have the one request."""
+    ctx = [int(c) for c in np.random.default_rng(6).integers(100, 1000, 64)]
+    assert _through_the_pages(nv, ws, ctx, [1] * 20 + [n] + [1] * 43, H, Hkv, 128)
+    assert not _through_the_pages(nv, ws, ctx, [1] * 20 + [2] + [1] * 43, H, Hkv, 128)
+
+
+@pytest.mark.parametrize("window", [0, 1, 60, 1000])
+@pytest.mark.parametrize("H,Hkv,D,page", [(10, 2, 128, 16), (8, 8, 64, 64), (9, 3, 96, 32)])
+def test_steps_whose_lengths_decide(nv, ws, H, Hkv, D, page, window):
+    """With bf16 pages at hand and a few rows per request on average."""
+    ctx = [int(c) for c in np.random.default_rng(D).integers(0, 900, 40)]
+    for q in ([1] * 39 + [90], [0, 2] * 20, [3] * 39 + [1], [100, 0, 0, 1] + [1] * 36):
+        q = [max(n, 1) for n in q] if window else q           # (run()'s rows that nobody sees need a token then)
+        run(nv, ws, ctx, q, H, Hkv, D, page, window, pad=3, expanded=True, layout="padded")
+
+
+def test_a_captured_step_whose_lengths_decide(nv, ws):
+    """One graph: replays with many rows for a request and with few, bit for bit the plain
+    calls; rows of padding are zeros whichever way was taken."""
+    H, Hkv, D, page, R, T = 10, 2, 128, 16, 12, 84
+    gen = torch.Generator("cuda").manual_seed(12)
+    ctx = [int(c) for c in np.random.default_rng(9).integers(50, 400, R)]
+    cache = random_cache4(nv, gen, 400, Hkv, page, D)
+    table = plan_of(nv, [T] * R, ctx, H, Hkv, page, 400).block_table
+    plan = nv.AttnPlan(R, T, H, Hkv, page_size=page, block_table=table)
+    assert T > R and -(-T // R) * (H // Hkv) < 40
+    q = torch.randn(T, H, D, device="cuda", generator=gen).bfloat16()
+    lens, at, scratch = i32([1] * R), i32(ctx), nv.KVCache.empty(400, Hkv, page, D)
+    out, lse = torch.empty_like(q), torch.empty(T, H, device="cuda")
+
+    def step(o, l, e):
+        nv.nvfp4_attn_plan(plan, lens, at)
+        nv.nvfp4_attn_paged4(q, cache, plan, o, ws, lse=l, zero_padding=True, expanded=e)
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    step(out, lse, scratch)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        step(out, lse, scratch)
+    for n in ([70] + [1] * 11, [1] * 12, [1] * 11 + [73], [2] * 12, [0] * 12, [84] + [0] * 11):
+        lens.copy_(i32(n))
+        out.fill_(7.0), lse.fill_(7.0)
+        graph.replay()
+        plain, codes = ((torch.empty_like(out), torch.empty_like(lse)) for _ in range(2))
+        step(*plain, scratch)
+        step(*codes, None)
+        assert torch.equal(out, plain[0]) and torch.equal(lse, plain[1])
+        assert torch.equal(out, codes[0]) == (max(n) < 10)
+        assert (out[sum(n):] == 0).all() and (lse[sum(n):] == -float("inf")).all()
+    assert nv.device_status() == 0 and not ws[:8192].any()
+
+
 def test_a_share_of_very_long_items(nv, ws):
     run(nv, ws, [170000], [1], 8, 8, 64, 128)
     run(nv, ws, [120000, 90000], [1, 2], 8, 8, 32, 64)
