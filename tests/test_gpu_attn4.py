@@ -222,6 +222,21 @@ def test_a_captured_step_whose_lengths_decide(nv, ws):
     assert nv.device_status() == 0 and not ws[:8192].any()
 
 
+def test_a_plan_without_pages_has_no_second_axis(nv):
+    """Only the attention over a paged 4-bit cache reads it; the first axis is that of the step with pages."""
+    lens = [300, 1, 40, 7, 0, 129]
+    plans = [nv.AttnPlan(6, sum(lens), 8, 2), nv.AttnPlan(6, sum(lens), 8, 2, page_size=16, block_table=20)]
+    for p in plans:
+        nv.nvfp4_attn_plan(p, i32(lens))
+    plain, paged = (p.schedule.view(torch.int32) for p in plans)
+    n, first4 = int(plain[2]), 16 + 256 * 9                   # QTiles; where the second axis' CTAs begin
+    assert n == int(paged[2]) > 0
+    assert torch.equal(plain[:3], paged[:3]) and torch.equal(plain[16:first4], paged[16:first4])
+    at = first4 + 256 * 9
+    assert torch.equal(plain[at:at + 8 * n], paged[at:at + 8 * n])
+    assert not plain[3:16].any() and not plain[first4:at].any() and paged[3:6].all()
+
+
 def test_a_share_of_very_long_items(nv, ws):
     run(nv, ws, [170000], [1], 8, 8, 64, 128)
     run(nv, ws, [120000, 90000], [1, 2], 8, 8, 32, 64)
