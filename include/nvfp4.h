@@ -580,9 +580,13 @@ typedef struct {
  * embedding in one pass, for a token's heads x of q or k:
  *   y = x * (1 / sqrt(mean(x^2) + eps)) * norm           (or x without a norm)
  *   each pair (a, b) of the rotated columns:  a' = a*c - b*s,  b' = a*s + b*c
- * in binary32, each product, sum and difference one operation, rounded to bf16 once at the end.  c and s are
- * those of the pair in row pos[t] of the tables; a position outside them takes
- * the nearest row and records NVFP4_ERR_INVALID_ARG * 100 + 33.
+ * in binary32, rounded to bf16 once at the end.  Without a norm each product, sum
+ * and difference is one operation (nvfp4_gemm_rope's bits).  With one the weights
+ * are folded into c and s, the sums fused and 1 / rms applied last: before the last
+ * rounding within 2^-18 of the sum of the products' magnitudes.  A row whose squares
+ * are beyond binary32 becomes 0, an infinity in it (and, rotated, its partner) NaN.
+ * c and s are those of the pair in row pos[t] of the tables; a position outside
+ * them takes the nearest row and records NVFP4_ERR_INVALID_ARG * 100 + 33.
  * With a cache the rows of k, rounded to bf16, and those of v go where
  * nvfp4_kv_append (or nvfp4_kv4_append) would put them, bit for bit; k_out may
  * then be NULL.
@@ -647,8 +651,8 @@ int nvfp4_kv4_expand(const nvfp4_kv4_cache_t* cache, const nvfp4_step_t* step, c
  *            its keys' rows out of the 4 bits once (into their pages there, bf16
  *            that holds code times scale exactly) and runs nvfp4_attn_paged's
  *            kernel on them, with probabilities rounded to bf16 as there.  That is
- *            so with 40 rows (tokens times heads / kv_heads) per request or more on
- *            average, else never with as many tokens as requests, and in between where
+ *            so with 40 rows (tokens, padding included, times heads / kv_heads) per
+ *            request or more on average, else never with as many tokens as requests, and in between where
  *            the lengths want more than a few passes over the keys, of all requests or
  *            of one (the plan's schedule has that; two of the three launches then
  *            return at once or one does).

@@ -4,8 +4,8 @@
 //
 // A decode step is few rows against many keys: 72 bytes of keys and as many of
 // values a key of 128 columns, each read once, and what has to be done for them
-// is to turn codes into numbers.  So nothing goes back to shared memory (as the
-// operands of tcgen05.mma would have to): every warp has its own ring of chunks of
+// is to turn codes into numbers.  So nothing of them goes back to shared or tensor
+// memory, where tcgen05.mma would take them from: every warp has its own ring of chunks of
 // 32 keys (cp.async), turns a chunk's codes into the fragments of mma.m16n8k16 in
 // registers (cvt of two codes to two halves, times the scale: six bits of
 // significand, exact in half precision) and multiplies, for each half of the chunk,

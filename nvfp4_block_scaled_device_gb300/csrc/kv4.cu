@@ -34,10 +34,13 @@ int log2_of(int64_t v)
 // in 4 bits from the bf16 value (so that the pass gives what the two calls give);
 // a block of 16 columns is two lanes.
 //
-// Bound by HBM with many tokens (2 B in, 2 B out a column): 16272 tokens of 40 query and
-// 8 key heads, with the values into the 4-bit cache, 87 us for 475 MB (5.5 TB/s; blocks
+// Bound by HBM's latency with many tokens (2 B in, 2 B out a column): 16272 tokens of 40
+// query and 8 key heads, with the values into the bf16 cache, 87 us for 475 MB (5.5 TB/s; blocks
 // of 64 registers, 8 to an SM, 91 then: 9 blocks 92, 6 blocks 115, 10 and fewer rows at
-// once 104); with few by the launch and one dependent chain of loads, so the rows of a token
+// once 104).  Into the 4-bit cache 106 us for 427 MB (4.0 TB/s; 94 with interleaved
+// pairs): 79 M instructions of a warp instead of 59 M, as a lane quantizes half a block
+// of K.  Part of a head rotated 91 to 120, heads of 96 columns 94 and (4 bits) 120,
+// of 64 columns 65 and 83.  With few tokens by the launch and one dependent chain of loads, so the rows of a token
 // are spread over as many warps as there is room for (8 tokens 2.6 us).
 constexpr int kHeadThreads = 128;
 constexpr int kHeadWarps = kHeadThreads / 32;
@@ -511,9 +514,12 @@ __device__ __forceinline__ float2 e2m1x2_to_f32(uint32_t b)
 // codes, a scale that two share, 16 bytes out), so nothing but the pages at a
 // request's ends has to know which row it is at.  Every block sums up the
 // pages of all requests in shared memory and takes its share of them.
-// Bound by HBM: 0.56 B in, 2 B out a column; 16272 rows of 8 heads 17.9 us (4.8 TB/s,
-// some 3 us of it until the first codes are there: lengths, table, codes one after
-// the other; 4 half blocks to a thread 18.1, 2 23.3).
+// 0.56 B in, 2 B out a column; 16272 rows of 8 heads 17.9 us (4.8 TB/s; the
+// bytes alone would take 12.7).  Bound by its instructions, 12.2 M of a warp (issue active 71 %,
+// beside 29 MB of HBM traffic: the rest stays in L2), after some 3 us until the first
+// codes are there: lengths, table, codes one after the other; 4 half blocks to a
+// thread 18.1, 2 23.3.  Pages of less than a chunk (one head of 16 rows of 128
+// columns: 256 half blocks) leave threads idle.
 constexpr int kExpandThreads = 256;
 constexpr int kExpandVecs = 8;                      // half blocks of a thread
 constexpr int kExpandChunk = kExpandThreads * kExpandVecs;
