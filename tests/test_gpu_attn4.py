@@ -225,9 +225,11 @@ def test_a_captured_step_whose_lengths_decide(nv, ws):
 def test_a_plan_without_pages_has_no_second_axis(nv):
     """Only the attention over a paged 4-bit cache reads it; the first axis is that of the step with pages."""
     lens = [300, 1, 40, 7, 0, 129]
-    plans = [nv.AttnPlan(6, sum(lens), 8, 2), nv.AttnPlan(6, sum(lens), 8, 2, page_size=16, block_table=20)]
+    table = torch.arange(120, dtype=torch.int32, device="cuda").view(6, 20)
+    plans = [nv.AttnPlan(6, sum(lens), 8, 2), nv.AttnPlan(6, sum(lens), 8, 2, page_size=16, block_table=table)]
     for p in plans:
         nv.nvfp4_attn_plan(p, i32(lens))
+    assert nv.device_status() == 0
     plain, paged = (p.schedule.view(torch.int32) for p in plans)
     n, first4 = int(plain[2]), 16 + 256 * 9                   # QTiles; where the second axis' CTAs begin
     assert n == int(paged[2]) > 0
