@@ -8,7 +8,8 @@
 //   S = Q K^T      tcgen05.mma kind::f16 (bf16, fp32 accumulation), operands
 //                  in shared memory (TMA, 128-byte swizzle), S in tensor memory
 //   P = 2^(c s - c m), c = scale * log2(e), m a running row maximum: one row
-//                  per thread, S read from and P (bf16) written to tensor
+//                  per thread, S read from and P (bf16; halves over rows taken out
+//                  of a 4-bit cache) written to tensor
 //                  memory, the row's sum of P kept in fp32
 //   O += P V       tcgen05.mma with P from tensor memory, V in shared memory
 //                  (as stored, keys by columns: the MMA's N-major form), O in
@@ -70,6 +71,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256;      // + 128 * warpgroup; P of 64 keys over the first 32 columns of their S
 constexpr int kStep = 64;                       // keys of a step
 constexpr float kLazy = 8.0f;                   // log2 of the growth that P may carry
+constexpr float kLift = 6.0f;                   // log2 of P at m in half precision
 constexpr int kRegsSoftmax = 192, kRegsOther = 120;
 static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "the block's registers at launch");
 
@@ -129,11 +131,11 @@ struct Params {
 };
 
 // ------------------------------------------------------------ instructions
-// Instruction descriptor, kind::f16: fp32 D, bf16 A and B, M = 128; B of the
-// second product is N-major (bit 16).
-__host__ __device__ constexpr uint32_t idesc_of(int n, bool b_n_major)
+// Instruction descriptor, kind::f16: fp32 D, bf16 (or half precision) A and B, M =
+// 128; B of the second product is N-major (bit 16).
+__host__ __device__ constexpr uint32_t idesc_of(int n, bool b_n_major, bool half = false)
 {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+    return (1u << 4) | (half ? 0u : 1u << 7 | 1u << 10) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
            ((128u >> 4) << 24);
 }
 
@@ -440,7 +442,9 @@ __device__ __forceinline__ void edit_scores(uint32_t taddr, bool negate, int h, 
     tmem_st_wait();
 }
 
-// P of 64 keys: e = 2^(c s + mc) as bf16 pairs; returns the sum of e.
+// P of 64 keys: e = 2^(c s + mc) as bf16 pairs or (kHalf) as pairs of halves;
+// returns the sum of e.
+template <bool kHalf>
 __device__ __forceinline__ float exp_scores(const float* s, float c, float mc, uint32_t* r)
 {
     float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
@@ -450,7 +454,10 @@ __device__ __forceinline__ float exp_scores(const float* s, float c, float mc, u
         e.x = ex2(e.x);
         e.y = ex2(e.y);
         sum[y & 1] = add2(sum[y & 1], e);
-        r[y] = cvt_bf16x2(e.x, e.y);
+        if (kHalf)
+            asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r[y]) : "f"(e.y), "f"(e.x));
+        else
+            r[y] = cvt_bf16x2(e.x, e.y);
     }
     sum[0] = add2(sum[0], sum[1]);
     return sum[0].x + sum[0].y;
@@ -487,7 +494,12 @@ __device__ __forceinline__ uint32_t stage_of(uint32_t use, uint32_t* parity)
 
 // kScaled: the rows are those of a 4-bit cache without its global scales, which
 // multiply the scores and the outputs here (a variant of its own: three more loads
-// cost a prompt of 8192 rows 4 %).
+// cost a prompt of 8192 rows 4 %).  Its values are halves, which hold code times
+// scale exactly, and so is P: rounded by 2^-11, carried 2^6 above 1 so that only
+// what is below 2^-20 of the largest loses bits (2^14 at most, with kLazy; scores
+// beyond 2^25, whose product with c rounds by more than that leaves, saturate).  A
+// chunk of 1024 rows at 15360 takes 269 us with its expansion; 270 with P in bf16 (2^-9),
+// 280 with differences of scores formed before their factor, as straight from the codes.
 template <int kDP, bool kFold, bool kScaled>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ Params prm)
 {
@@ -696,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             const uint64_t qdesc0 = make_smem_desc(base, 16, 1024, 2);                  // K-major
             const uint64_t kdesc0 = make_smem_desc(base, 16, L::kGroup, 2);             // K-major
             const uint64_t vdesc0 = make_smem_desc(base, L::kHalf, L::kGroup, 2);       // N-major
-            constexpr uint32_t kIdescS = idesc_of(kStep, false), kIdescO = idesc_of(kDP, true);
+            constexpr uint32_t kIdescS = idesc_of(kStep, false), kIdescO = idesc_of(kDP, true, kScaled);
             constexpr uint32_t kStepDesc = L::kStepAt >> 4;
             const uint32_t q_hi = (uint32_t)(qdesc0 >> 32), k_hi = (uint32_t)(kdesc0 >> 32), v_hi = (uint32_t)(vdesc0 >> 32);
             const uint32_t q_lo = (uint32_t)qdesc0;
@@ -904,9 +916,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                         // P with the m in use, the step's maximum beside it;
                         // where that has outgrown m (and at an item's first
                         // keys) m moves and P is formed again: S is still there
-                        mc = m == -INFINITY ? 0.0f : -m * c;
+                        mc = m == -INFINITY ? 0.0f : kScaled ? __fmaf_rn(-m, c, kLift) : -m * c;
                         const float mx = max_scores(s);
-                        sum = exp_scores(s, c, mc, r);
+                        sum = exp_scores<kScaled>(s, c, mc, r);
                         const bool up = mine && (mx > m + lazy || (m == -INFINITY && mx > m));
                         if (!__any_sync(0xffffffffu, up)) break;
                         const float m1 = up ? mx : m;
@@ -967,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 l = l * f0 + lb * f1;
                 m = mm;
             }
-            const float m2 = m * c;                              // log2 of e^(largest score)
+            const float m2 = m * c - (kScaled ? kLift : 0.0f);   // log2 of what O and l are multiples of
             const bool whole = p.parts == 1;
             const bool none = l == 0.0f;                         // the row sees no key
             const int head = p.hk * a.group + g;

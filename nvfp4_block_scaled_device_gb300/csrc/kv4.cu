@@ -502,12 +502,12 @@ cudaError_t run_heads(HeadsParams& p, int num_sms, cudaStream_t stream)
 }
 
 // ----------------------------------------------------------------- expand
-// Two E2M1 codes (a byte, the first in the low nibble) -> binary32 (exact).
-__device__ __forceinline__ float2 e2m1x2_to_f32(uint32_t b)
+// Two E2M1 codes (a byte, the first in the low nibble) -> two halves (exact).
+__device__ __forceinline__ __half2 e2m1x2_to_f16x2(uint32_t b)
 {
     uint32_t h;
     asm("{\n .reg .b8 x, a, b, c;\n mov.b32 {x, a, b, c}, %1;\n cvt.rn.f16x2.e2m1x2 %0, x;\n}" : "=r"(h) : "r"(b));
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return *reinterpret_cast<const __half2*>(&h);
 }
 
 // A page's rows of all heads are one run of half blocks (8 columns: 4 bytes of
@@ -531,7 +531,7 @@ struct ExpandParams {
     const int32_t* kv_len;
     const int32_t* block_table;
     int64_t table_ld;
-    int requests, table_cols, window, page_shift, scaled;
+    int requests, table_cols, window, page_shift;
     int halves;                                     // half blocks of a page of K
     int chunks;                                     // of kExpandChunk
     const ScheduleHead* unless_few;                 // nothing to do where its few_passes is set; NULL: there is
@@ -546,6 +546,8 @@ __device__ __forceinline__ int2 seen_rows(const ExpandParams& p, int r)
     return make_int2(p.window ? max(kv - q + 1 - p.window, 0) : 0, (int)min((int64_t)kv, cap));
 }
 
+// kScaled: times the global scales, bf16; else without them, K as bf16 and V as halves.
+template <bool kScaled>
 __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_constant__ ExpandParams p)
 {
     extern __shared__ int32_t pre[];                // [requests + 1] pages before each request
@@ -579,10 +581,10 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
     __syncthreads();
     const int64_t units = (int64_t)pre[R] * 2 * p.chunks;
     const int per_row = (int)p.c.head_dim / 8;
-    const float g[2] = {p.scaled ? *p.c.k_g : 1.0f, p.scaled ? *p.c.v_g : 1.0f};
+    const float g[2] = {kScaled ? *p.c.k_g : 1.0f, kScaled ? *p.c.v_g : 1.0f};
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int i = (int)(u / (2 * p.chunks)), part = (int)(u - (int64_t)i * 2 * p.chunks);
-        const bool is_v = part >= p.chunks;
+        const bool is_v = part >= p.chunks, halves = is_v && !kScaled;
         const int h0 = (is_v ? part - p.chunks : part) * kExpandChunk + t;
         int lo = 0, hi = R - 1;                     // the request that page i is of
         while (lo < hi) {
@@ -621,9 +623,15 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
             uint32_t o[4];
 #pragma unroll
             for (int y = 0; y < 4; y++) {
-                const float2 v = e2m1x2_to_f32(w[x] >> (8 * y));
-                // (code times scale is exact)
-                o[y] = cvt_bf16x2(v.x * f * gg, v.y * f * gg);
+                const __half2 h = e2m1x2_to_f16x2(w[x] >> (8 * y));
+                // (code times scale is exact, in bf16 and as halves)
+                if (halves) {
+                    const __half2 z = __hmul2(h, __float2half2_rn(f));
+                    o[y] = *reinterpret_cast<const uint32_t*>(&z);
+                } else {
+                    const float2 v = __half22float2(h);
+                    o[y] = kScaled ? cvt_bf16x2(v.x * f * gg, v.y * f * gg) : cvt_bf16x2(v.x * f, v.y * f);
+                }
             }
             out[hb] = make_uint4(o[0], o[1], o[2], o[3]);
         }
@@ -666,10 +674,9 @@ cudaError_t launch_kv4_expand(const nvfp4_kv4_cache_t& cache, const nvfp4_step_t
     p.table_cols = (int)step.table_cols;
     p.window = step.heads ? (int)step.window : 0;
     p.page_shift = log2_of(cache.page_size);
-    p.scaled = scaled;
     p.halves = (int)(cache.kv_heads * cache.page_size * cache.head_dim / 8);
     p.chunks = (p.halves + kExpandChunk - 1) / kExpandChunk;
-    return launch_programmatic(expand_kernel, dim3((unsigned)num_sms * 8), dim3(kExpandThreads),
+    return launch_programmatic(scaled ? expand_kernel<true> : expand_kernel<false>, dim3((unsigned)num_sms * 8), dim3(kExpandThreads),
                                (size_t)(step.requests + 1) * 4, stream, p);
 }
 

@@ -28,7 +28,8 @@ struct PageCopyPlanes {
 cudaError_t launch_heads(const nvfp4_heads_t& heads, int* status, int num_sms, cudaStream_t stream);
 
 // The rows of a 4-bit cache that a step sees, into a bf16 cache's pages; scaled:
-// times the cache's global scales (else code times E4M3 scale, exact in bf16);
+// times the cache's global scales (else code times E4M3 scale, exact: K in bf16, V as
+// halves in the bf16 cache's place, what nvfp4_attn_paged4's own variant reads);
 // unless_few: only where the step's schedule does not have few_passes.
 cudaError_t launch_kv4_expand(const nvfp4_kv4_cache_t& cache, const nvfp4_step_t& step, const nvfp4_kv_cache_t& out,
                               bool scaled, bool unless_few, int num_sms, cudaStream_t stream);

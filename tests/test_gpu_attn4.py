@@ -177,6 +177,57 @@ def test_one_request_of_many_passes_decides(nv, ws, H, Hkv, n):
     assert not _through_the_pages(nv, ws, ctx, [1] * 20 + [2] + [1] * 43, H, Hkv, 128)
 
 
+@pytest.mark.parametrize("H,Hkv,D,page", [(10, 2, 128, 16), (8, 8, 64, 64), (9, 3, 96, 32), (4, 1, 128, 128), (6, 2, 16, 16)])
+@pytest.mark.parametrize("ctx,q_len,std", [([0], [70], 1.0), ([3, 1, 0], [60, 50, 90], 4.0), ([3000], [100], 1.0), ([900, 20], [130, 300], 0.1)])
+def test_probabilities_through_the_pages(nv, ws, H, Hkv, D, page, ctx, q_len, std):
+    """They are rounded to half precision there too: the tolerance of the codes."""
+    gen = torch.Generator("cuda").manual_seed(D + sum(ctx))
+    pages = sum(-(-(c + n) // page) for c, n in zip(ctx, q_len)) + 3
+    cache = random_cache4(nv, gen, pages, Hkv, page, D)
+    plan = plan_of(nv, q_len, ctx, H, Hkv, page, pages)
+    q = rows(gen, plan.tokens, H, D, "plain", std)
+    out, lse = torch.empty_like(q), torch.empty(plan.tokens, H, device="cuda")
+    nv.nvfp4_attn_paged4(q, cache, plan, out, ws, lse=lse, expanded=nv.KVCache.empty(pages, Hkv, page, D))
+    k, v = values(cache)
+    at = 0
+    for r, (c, n) in enumerate(zip(ctx, q_len)):
+        pos = torch.arange(c + n, device="cuda")
+        ids, row = plan.block_table[r].long()[pos // page], pos % page
+        ref = reference(q[at:at + n].double(), k[ids, :, row], v[ids, :, row], c, D ** -0.5)
+        check(out[at:at + n], lse[at:at + n], *ref, P_HALF, v[ids, :, row], f"request {r}")
+        at += n
+    assert nv.device_status() == 0
+
+
+@pytest.mark.parametrize("L,std", [(300, 2e4), (2000, 2e4)])
+def test_large_scores_through_the_pages(nv, ws, L, std):
+    """Scores of 10^6 to 10^7: a row whose largest is alone gives that key's value (bounds as above)."""
+    H, Hkv, D, T = 8, 4, 64, 64
+    gen = torch.Generator("cuda").manual_seed(L)
+    pages = -(-(L + T) // 16)
+    cache = random_cache4(nv, gen, pages, Hkv, 16, D, 2.0 ** 2)
+    plan = plan_of(nv, [T], [L], H, Hkv, 16, pages)
+    q = (torch.randn(T, H, D, device="cuda", generator=gen) * std).bfloat16()
+    out = torch.empty_like(q)
+    nv.nvfp4_attn_paged4(q, cache, plan, out, ws, expanded=nv.KVCache.empty(pages, Hkv, 16, D))
+    k, v = values(cache)
+    at = torch.arange(L + T, device="cuda")
+    keys, vals = (x[plan.block_table[0].long()[at // 16], :, at % 16] for x in (k, v))
+    alone = 0
+    for h in range(H):
+        x = q[:, h].double() * D ** -0.5
+        seen = at[None] <= L + torch.arange(T, device="cuda")[:, None]
+        s = torch.where(seen, x @ keys[:, h // 2].T, -float("inf"))
+        top = s.topk(2)
+        gap = 2 * D * 2.0 ** -24 * (x.abs() @ keys[:, h // 2].abs().T).max(1).values + 200
+        sure = top.values[:, 0] - top.values[:, 1] > gap
+        alone += int(sure.sum())
+        assert (top.values[sure, 0] > 1e5).all() and top.values.max() < 2 ** 24
+        want = vals[top.indices[:, 0], h // 2]
+        assert ((out[:, h].double() - want).abs() <= 2.0 ** -8 * want.abs())[sure].all()
+    assert alone >= H * T // 2
+
+
 @pytest.mark.parametrize("window", [0, 1, 60, 1000])
 @pytest.mark.parametrize("H,Hkv,D,page", [(10, 2, 128, 16), (8, 8, 64, 64), (9, 3, 96, 32)])
 def test_steps_whose_lengths_decide(nv, ws, H, Hkv, D, page, window):
