@@ -653,10 +653,10 @@ int nvfp4_kv4_expand(const nvfp4_kv4_cache_t* cache, const nvfp4_step_t* step, c
  *            kernel on them, q as it is and probabilities in half precision too (scores
  *            below 2^24 keep their largest there, straight from the codes those of any
  *            size).  That is so with 40 rows (tokens, padding included, times heads /
- *            kv_heads) per request or more on average, else never with as many tokens as requests, and in
- *            between where the lengths want more than a few passes over the keys, of
- *            all requests or of one (the plan's schedule has that; two of the three
- *            launches then return at once or one does).
+ *            kv_heads) per request or more on average, else never with as many tokens as
+ *            requests, and in between where the lengths want more than a few passes over
+ *            the keys, of all requests or of one (the plan's schedule has that; two of
+ *            the three launches then return at once or one does).
  *            One serves all layers that run one after the other.
  *   workspace as nvfp4_attn_paged.
  * head_dim % 16 == 0.  The rest as nvfp4_attn_paged: cache rows that no row of

@@ -8,9 +8,9 @@
 //   S = Q K^T      tcgen05.mma kind::f16 (bf16, fp32 accumulation), operands
 //                  in shared memory (TMA, 128-byte swizzle), S in tensor memory
 //   P = 2^(c s - c m), c = scale * log2(e), m a running row maximum: one row
-//                  per thread, S read from and P (bf16; halves over rows taken out
-//                  of a 4-bit cache) written to tensor
-//                  memory, the row's sum of P kept in fp32
+//                  per thread, S read from and P (bf16; halves over rows taken
+//                  out of a 4-bit cache) written to tensor memory, the row's
+//                  sum of P kept in fp32
 //   O += P V       tcgen05.mma with P from tensor memory, V in shared memory
 //                  (as stored, keys by columns: the MMA's N-major form), O in
 //                  tensor memory

@@ -37,10 +37,11 @@ int log2_of(int64_t v)
 // Bound by HBM's latency with many tokens (2 B in, 2 B out a column): 16272 tokens of 40
 // query and 8 key heads, with the values into the bf16 cache, 87 us for 475 MB (5.5 TB/s; blocks
 // of 64 registers, 8 to an SM, 91 then: 9 blocks 92, 6 blocks 115, 10 and fewer rows at
-// once 104).  Into the 4-bit cache 106 us for 427 MB (4.0 TB/s; 94 with interleaved
-// pairs): 79 M instructions of a warp instead of 59 M, as a lane quantizes half a block
-// of K.  Part of a head rotated 91 to 120, heads of 96 columns 94 and (4 bits) 120,
-// of 64 columns 65 and 83.  With few tokens by the launch and one dependent chain of loads, so the rows of a token
+// once 104).  Into the 4-bit cache 102 us for 427 MB (4.2 TB/s; 94 with interleaved
+// pairs): 78 M instructions of a warp instead of 59 M, as a lane quantizes half a block
+// of K.  Part of a head rotated 91 to 117, heads of 96 columns 94 and (4 bits) 116,
+// of 64 columns 65 and 81.  With few tokens by the launch and one dependent chain of
+// loads, so the rows of a token
 // are spread over as many warps as there is room for (8 tokens 2.6 us).
 constexpr int kHeadThreads = 128;
 constexpr int kHeadWarps = kHeadThreads / 32;
@@ -96,49 +97,57 @@ __device__ __forceinline__ uint32_t amax_bf16x2(uint32_t a, uint32_t b)
     return r;
 }
 
+// Two bf16, no more than `far` from 0.
+__device__ __forceinline__ uint32_t clamp_bf16x2(uint32_t x, uint32_t far)
+{
+    asm("min.bf16x2 %0, %0, %1;\n max.bf16x2 %0, %0, %2;" : "+r"(x) : "r"(far), "r"(far | 0x80008000u));
+    return x;
+}
+
 constexpr float kMostBf16 = 3.3895313892515355e38f;
 
-// Scales of a cache's blocks: 6 g, its correctly rounded reciprocal, and the
-// largest magnitude that counts in a block's scale (beyond 448 * 6 g it is 448,
-// as it is there; an infinity is the largest bf16 number).
+// Scales of a cache's blocks: 6 g and its correctly rounded reciprocal.
 struct BlockScale {
-    float g, d, rd, most;
+    float g, d, rd;
 };
 __device__ __forceinline__ BlockScale block_scale(float g)
 {
     const float d = __fmul_rn(6.0f, g);
-    return BlockScale{g, d, __frcp_rn(d), fminf(__fmul_rn(448.0f, d), kMostBf16)};
+    return BlockScale{g, d, __frcp_rn(d)};
 }
 
 // One block's scale and codes, nvfp4_quantize's bit for bit: each lane has kVecs
 // vectors of it (8 columns), amax is the block's, *sc its scale.  The quotients v /
 // den are those of div_by_recip in pairs of columns, negated (q = -v y, q + (v + q
 // den) (-y): the remainder's sign needs no operation, and a zero keeps the sign
-// that the codes' XOR then turns around).
+// that the codes' XOR then turns around).  They are right for dividends whose quotients
+// are far from overflow: amax no more than 448 d (the scale is 448 from there on; an
+// infinity is the largest bf16 number), then v no more than 8 den (the code is 6).
 template <int kVecs>
 __device__ __forceinline__ void quant_block(const uint4* x, uint32_t amax_bits, const BlockScale& b, uint32_t* codes, uint32_t* sc)
 {
     float amax = bf16_lo(amax_bits);
-    const bool odd = !(amax <= b.most), nan = amax != amax;          // too large, an infinity or NaN in it
-    if (odd) amax = b.most;
+    const float most = __fmul_rn(448.0f, b.d);
+    const bool odd = !(amax < most), nan = amax != amax;             // too large, an infinity or NaN in it
+    if (odd) amax = fminf(most, kMostBf16);
     const uint32_t s = cvt_e4m3(div_by_recip(amax, b.d, b.rd));
     const float den = __fmul_rn(e4m3_to_f32(s), b.g);
     const float ny = -__frcp_rn(s ? den : 1.0f);
     const float2 ny2 = make_float2(ny, ny), den2 = make_float2(den, den);
 #pragma unroll
     for (int i = 0; i < kVecs; i++) {
-        float2 v[4];
-        unpack4(x[i], v);
+        uint4 z = x[i];
         if (odd) {
-            const float most = fminf(__fmul_rn(8.0f, den), kMostBf16);
-#pragma unroll
-            for (int y = 0; y < 4; y++)
-                v[y] = make_float2(fminf(fmaxf(v[y].x, -most), most), fminf(fmaxf(v[y].y, -most), most));
+            const float far = fminf(__fmul_rn(8.0f, den), kMostBf16);
+            const uint32_t far2 = cvt_bf16x2(far, far);
+            z = make_uint4(clamp_bf16x2(z.x, far2), clamp_bf16x2(z.y, far2), clamp_bf16x2(z.z, far2), clamp_bf16x2(z.w, far2));
         }
+        float2 v[4];
+        unpack4(z, v);
         float q[8];
 #pragma unroll
         for (int y = 0; y < 4; y++) {
-            const float2 z = mul2(v[y], ny2), r = fma2(fma2(z, den2, v[y]), ny2, z);
+            const float2 q0 = mul2(v[y], ny2), r = fma2(fma2(q0, den2, v[y]), ny2, q0);
             q[2 * y] = r.x, q[2 * y + 1] = r.y;
         }
         codes[i] = s == 0 || nan ? 0u : cvt_e2m1x8(q) ^ 0x88888888u;

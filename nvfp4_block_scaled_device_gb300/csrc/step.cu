@@ -175,13 +175,13 @@ __device__ void build_schedule(const PlanParams& p, const int32_t* cu, const int
             head->units4 = units4;
             head->per_cta4 = per;
             head->most_tokens = *most_tokens;
-            // Few on average, and for the CTAs that have the QTile with most of them (their
-            // shares are cut by tiles, and no warp has one of its own then) one or no more
-            // than 15 tiles times passes.  Measured, us straight from 4 bits and in bf16 after
-            // taking them out: 8 requests of 2000 keys 28 in one pass, 52 in two, and 44; 64 of 100
-            // to 1000, one of them with 200 tokens of 5 rows, 375 and 78; 32 of 50 to 500
-            // with 40 tokens there 130 and 28, with 9 there (7 tiles twice) 39 and 26 with the
-            // two launches that return at once; 64 of 200 to 8192 with 9 of 8 rows there 53 and 105.
+            // Few on average, and for the CTAs that have the QTile with most of them, as their
+            // shares are cut by tiles, and no warp has one of its own then.  Measured, us
+            // straight from 4 bits and after taking them out: 8 requests of 2000 keys 28 in one
+            // pass, 52 in two, and 44; 64 of 100 to 1000, one of them with 200 tokens of 5 rows,
+            // 375 and 78; 32 of 50 to 500 with 40 tokens there 130 and 28.  With 9 tokens there
+            // it is 39 and 26: up to 15 tiles times passes a step keeps to the codes, which
+            // costs it 7 to 20 us and spares it the traffic of the pages.
             const int passes = (*most_tokens * group + kPassRows - 1) / kPassRows;
             const int share = max(((int)min(units, kMaxUnits) + p.ctas - 1) / p.ctas, min(kItemUnits + kMinPart, *longest));
             head->few_passes = 10 * all_pass_tiles * Hkv <= 17 * (units - (int64_t)kItemUnits * n * Hkv) &&
